@@ -349,6 +349,147 @@ cp_status cp_measure_stream_read(const void* buf, uint64_t bytes, void* stream);
 cp_status cp_measure_record_read(const void* table, uint64_t table_bytes, uint32_t record_bytes,
                                  const int64_t* rows, uint64_t n, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The memory layer's other operators: training a table's rows before they are
+ * encoded (cp_embed, cp_embed_grad), bringing rows into the residual stream
+ * (cp_rms_norm, cp_rms_norm_grad) and projecting them in 8 bits
+ * (cp_rms_norm_fp8, cp_quantize_fp8, cp_matmul_fp8).
+ *
+ * Conventions beyond those above:
+ *   - Every call queues kernels only: no allocation, no synchronisation, so all
+ *     of them can be captured into a CUDA graph.  What needs scratch takes a
+ *     workspace from the caller (its size from the *_workspace_bytes call; 16-byte
+ *     aligned device memory, used until the queued work completes, its contents
+ *     of no meaning before and after, calls sharing it ordered on one stream).
+ *   - Arrays are device memory, aligned to their element, rows of unit stride;
+ *     a row stride is counted in elements and may exceed the row's length (a
+ *     view into a wider array).  Outputs do not overlap inputs, except where a
+ *     call says so.  Any length is accepted; whole octets (rows whose every
+ *     eight elements lie on a boundary of eight elements) run on wide loads.
+ *   - Sums and statistics are fp32, in an order fixed by the shapes (and, for
+ *     cp_embed_grad, the ids): the same call gives the same bits.
+ * ---------------------------------------------------------------------- */
+
+/* Element types. */
+enum { CP_F32 = 0, CP_F16 = 1, CP_BF16 = 2 };
+
+/*
+ * cp_embed -- scaled lookup in a table of plain rows (a memory table in
+ * training, or a token embedding):
+ *   out[j][q] = rn(scale * weight[ids[j]][q]),  one fp32 product rounded once.
+ *   weight   [n_rows][d] of dtype (CP_F32, CP_F16, CP_BF16), row stride
+ *            weight_stride >= d.
+ *   ids      n int64.  An id outside [0, n_rows) gives a row of zeros.
+ *   out      [n][d] of the same type, row stride out_stride >= d.
+ *   status   device uint32 or NULL: bit 0 is OR-ed in for an id out of range.
+ * n < 2^31, d <= 2^20.
+ */
+cp_status cp_embed(const void* weight, int dtype, uint64_t n_rows, uint32_t d,
+                   uint64_t weight_stride, const int64_t* ids, uint64_t n, float scale, void* out,
+                   uint64_t out_stride, uint32_t* status, void* stream);
+
+/*
+ * cp_embed_grad -- the gradient of cp_embed by its table:
+ *   sum[r][q] = sum of dy[j][q] over the j with ids[j] = r       (fp32)
+ *   accumulate = 0: grad[r] = rn(scale * sum[r]) for every row, zeros for the
+ *                   rows that no id names;
+ *   accumulate = 1: grad[r] = rn(grad[r] + scale * sum[r]) for the rows that ids
+ *                   name; the others are not touched.  (With scale = -rate this
+ *                   is a step of gradient descent on the table itself.)
+ * The ids are sorted (stably, so each row sums its lookups in an order fixed by
+ * the ids), and rows and lookups are dealt evenly to the warps, so neither a hot
+ * row nor a table of untouched rows holds one of them up.
+ *   dy       [n][d] of dy_dtype, row stride dy_stride >= d.
+ *   ids      n int64; ids outside [0, n_rows) are left out (bit 0 of status).
+ *   grad     [n_rows][d] of grad_dtype, row stride grad_stride >= d.
+ *   workspace  cp_embed_grad_workspace_bytes(n, n_rows, d) bytes, 16-byte aligned.
+ * n < 2^31, n_rows < 2^31, d <= 2^20.  n = 0 with accumulate = 0 clears grad.
+ */
+uint64_t cp_embed_grad_workspace_bytes(uint64_t n, uint64_t n_rows, uint32_t d);
+cp_status cp_embed_grad(const void* dy, int dy_dtype, uint64_t dy_stride, const int64_t* ids,
+                        uint64_t n, uint64_t n_rows, uint32_t d, float scale, int accumulate,
+                        void* grad, int grad_dtype, uint64_t grad_stride, uint32_t* status,
+                        void* workspace, uint64_t workspace_bytes, void* stream);
+
+/*
+ * cp_rms_norm -- root-mean-square norm with the residual's addition:
+ *   s = x + residual (fp32);  h = rn(s);  r = 1 / sqrt(mean(s^2) + eps)
+ *   y = rn(s * r * weight)
+ * Without a residual s = x, and h is not written.
+ *   x, residual, h, y   [rows][d] of dtype; x and residual with their own row
+ *            strides (0 repeats one row), h and y contiguous.  h may be the
+ *            residual itself (stride d), or x; y may be x.  Otherwise no overlap.
+ *   residual, h  both NULL, or neither.
+ *   weight   [d] of weight_dtype.
+ * d <= 49152, rows < 2^31, eps >= 0.
+ */
+cp_status cp_rms_norm(const void* x, uint64_t x_stride, const void* residual,
+                      uint64_t residual_stride, int dtype, const void* weight, int weight_dtype,
+                      uint64_t rows, uint32_t d, float eps, void* y, void* h, void* stream);
+
+/*
+ * cp_rms_norm_fp8 -- the same norm, y left in 8 bits with scales: for each group
+ * g of 128 columns of a row (the last one may be shorter)
+ *   scales[i][g] = max(amax |y|, 1e-30) / 448
+ *   q = e4m3(y * (1 / scales[i][g])),  to nearest even, y in fp32 before it.
+ *   q        [rows][d] e4m3 bytes, contiguous; no overlap with any input.
+ *   scales   [rows][ceil(d / 128)] fp32, contiguous.
+ * A NaN in a group makes the group's scale and values NaN; an infinity makes the
+ * scale infinite, itself NaN and the group's finite values zero.
+ */
+cp_status cp_rms_norm_fp8(const void* x, uint64_t x_stride, const void* residual,
+                          uint64_t residual_stride, int dtype, const void* weight,
+                          int weight_dtype, uint64_t rows, uint32_t d, float eps, uint8_t* q,
+                          float* scales, void* h, void* stream);
+
+/*
+ * cp_rms_norm_grad -- the gradients of y = s * r * weight by s and by weight, at
+ * s = h (the norm's input after the residual's addition):
+ *   n = h * r,  t = dy * weight
+ *   dx = rn(dres + r * (t - n * mean(t * n)))     dw = sum over rows of dy * n
+ *   dy, h    [rows][d] of dtype, with row strides.
+ *   dres     the gradient that reaches the stream past the norm, [rows][d] with
+ *            its row stride, or NULL (zero).
+ *   dx       [rows][d] of dtype, contiguous; the gradient by x and by the residual
+ *            alike.  It may be dres (stride d) or dy (stride d).
+ *   dw       [d] of weight_dtype, written whole (zeros for rows = 0).
+ *   workspace  cp_rms_norm_grad_workspace_bytes(rows, d) bytes, 16-byte aligned.
+ */
+uint64_t cp_rms_norm_grad_workspace_bytes(uint64_t rows, uint32_t d);
+cp_status cp_rms_norm_grad(const void* dy, uint64_t dy_stride, const void* h, uint64_t h_stride,
+                           const void* dres, uint64_t dres_stride, int dtype, const void* weight,
+                           int weight_dtype, uint64_t rows, uint32_t d, float eps, void* dx,
+                           void* dw, void* workspace, uint64_t workspace_bytes, void* stream);
+
+/*
+ * cp_quantize_fp8 -- x to e4m3 with a scale for each block of block_rows x 128
+ * (1: activations, one row's groups; 128: weights), by cp_rms_norm_fp8's rule.
+ *   x        [rows][d] of dtype, row stride x_stride.
+ *   q        [rows][d] e4m3 bytes, contiguous.
+ *   scales   [ceil(rows / block_rows)][ceil(d / 128)] fp32, contiguous.
+ * ceil(rows / block_rows) * ceil(d / 128) < 2^31.
+ */
+cp_status cp_quantize_fp8(const void* x, uint64_t x_stride, int dtype, uint64_t rows, uint32_t d,
+                          uint32_t block_rows, uint8_t* q, float* scales, void* stream);
+
+/*
+ * cp_matmul_fp8 -- product of e4m3 matrices with a scale for each block of 128:
+ *   out[i][j] = rn( sum over g of a_scales[i][g] * w_scales[j / 128][g]
+ *                   * sum over k in group g of a[i][k] * w[j][k] )
+ * products exact, sums fp32.
+ *   a        [m][k] e4m3 bytes, row stride a_stride (one token to a prompt).
+ *   a_scales [m][ceil(k / 128)] fp32, contiguous.
+ *   w        [n][k] e4m3 bytes, row stride w_stride (a projection's weights).
+ *   w_scales [ceil(n / 128)][ceil(k / 128)] fp32, contiguous.
+ *   out      [m][n] of out_dtype, row stride out_stride.
+ * k = 0 gives zeros.  m, n, k < 2^31.  Rows on 16-byte boundaries (k of any
+ * length, pointers and strides multiples of 16) take the tensor-memory kernels.
+ */
+cp_status cp_matmul_fp8(const uint8_t* a, uint64_t a_stride, const float* a_scales,
+                        const uint8_t* w, uint64_t w_stride, const float* w_scales, uint64_t m,
+                        uint64_t n, uint64_t k, void* out, int out_dtype, uint64_t out_stride,
+                        void* stream);
+
 /* Release what the handle owns (LUT copy, status word, host registration made
  * by cp_table_load).  Borrowed buffers are untouched.  NULL is a no-op. */
 void cp_table_free(cp_table* t);

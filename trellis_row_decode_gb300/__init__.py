@@ -25,6 +25,8 @@ __all__ = [
     "lookup_decode_reduce", "set_cache", "load_mixed_table", "encode_rows",
     "measure_stream_read", "measure_record_read", "encode_workspace", "encode_rows_ws",
     "CP_LAYOUT_AOS", "CP_LAYOUT_SOA", "CP_RESIDENT_DEVICE", "CP_RESIDENT_HOST",
+    "CP_F32", "CP_F16", "CP_BF16", "embed", "embed_grad", "embed_grad_workspace", "rms_norm",
+    "rms_norm_fp8", "rms_norm_grad", "rms_norm_grad_workspace", "quantize_fp8", "matmul_fp8",
 ]
 
 _PKG = Path(__file__).resolve().parent
@@ -381,3 +383,9 @@ def lookup_decode_host_noalloc(records: torch.Tensor, n_rows: int, d: int, k: in
                                              status.data_ptr(), _stream_ptr(stream))
     _check(st, "cp_lookup_decode_host_noalloc")
     return out
+
+
+# The memory layer's operators around the lookup-decode (their module uses the names above).
+from .layer import (  # noqa: E402
+    CP_BF16, CP_F16, CP_F32, embed, embed_grad, embed_grad_workspace, matmul_fp8, quantize_fp8,
+    rms_norm, rms_norm_fp8, rms_norm_grad, rms_norm_grad_workspace)

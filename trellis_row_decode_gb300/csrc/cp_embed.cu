@@ -1,0 +1,109 @@
+// cp_embed.cu -- scaled lookup in a table of plain rows (include/cp.h, cp_embed).
+//
+//   out[j] = scale * weight[ids[j]],  zeros for an id outside the table.
+//
+// One fp32 product per element: the kernel is bound by its memory stream (the
+// distinct rows read, the output written).  A lane moves octets (16 or 32 bytes);
+// `1 << lanes_log2` lanes share a row, so short rows fill a warp, and a lane keeps
+// up to four octets of its row in flight before it stores the first.
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "cp.h"
+#include "cp_internal.h"
+#include "cp_layer.cuh"
+
+namespace {
+
+using namespace cpl;
+
+constexpr int kThreads = 256;
+constexpr uint32_t kOctets = 4;   // octets of a row that a lane holds at once
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+    embed_kernel(const T* __restrict__ weight, uint64_t n_rows, uint32_t d, uint64_t weight_stride,
+                 const int64_t* __restrict__ ids, uint64_t n, float scale, T* __restrict__ out,
+                 uint64_t out_stride, uint32_t* status, uint32_t lanes_log2, uint32_t slabs) {
+  const uint32_t lanes = 1u << lanes_log2;
+  const uint64_t team = (static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x) >> lanes_log2;
+  const uint64_t j = slabs == 1 ? team : team / slabs;
+  if (j >= n) return;
+  const uint32_t slab = slabs == 1 ? 0 : static_cast<uint32_t>(team - j * slabs);
+  const uint32_t octets = (d + 7) / 8;
+  const uint32_t o0 = slab * lanes * kOctets + (threadIdx.x & (lanes - 1));
+  const int64_t id = __ldg(ids + j);
+  const bool valid = static_cast<uint64_t>(id) < n_rows;
+  const T* src = weight + (valid ? static_cast<uint64_t>(id) : 0) * weight_stride;
+  T* dst = out + j * out_stride;
+  Packed<T> r[kOctets];
+#pragma unroll
+  for (uint32_t i = 0; i < kOctets; ++i) {
+    const uint32_t o = o0 + i * lanes;
+    r[i] = valid && o < octets ? load_row_octet<T, VEC>(src, o, d) : zero_octet<T>();
+  }
+  if (!valid && status != nullptr && o0 == 0) atomicOr(status, 1u);
+#pragma unroll
+  for (uint32_t i = 0; i < kOctets; ++i) {
+    const uint32_t o = o0 + i * lanes;
+    if (o < octets) {
+      float v[8];
+      unpack<T>(r[i], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = valid ? scale * v[e] : 0.0f;
+      store_row_octet<T, VEC>(dst, o, d, pack<T>(v));
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch(const void* weight, uint64_t n_rows, uint32_t d, uint64_t weight_stride,
+                   const int64_t* ids, uint64_t n, float scale, void* out, uint64_t out_stride,
+                   uint32_t* status, cudaStream_t s) {
+  const uint32_t octets = (d + 7) / 8;
+  uint32_t lanes_log2 = 0;
+  while (lanes_log2 < 5 && (1u << lanes_log2) < octets) ++lanes_log2;
+  const uint32_t per_slab = (1u << lanes_log2) * kOctets;
+  const uint32_t slabs = (octets + per_slab - 1) / per_slab;
+  const uint64_t blocks = (((n * slabs) << lanes_log2) + kThreads - 1) / kThreads;
+  if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
+  const bool vec = octets_ok(weight, weight_stride, d, sizeof(T)) &&
+                   octets_ok(out, out_stride, d, sizeof(T));
+  auto* fn = vec ? &embed_kernel<T, true> : &embed_kernel<T, false>;
+  fn<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(
+      static_cast<const T*>(weight), n_rows, d, weight_stride, ids, n, scale,
+      static_cast<T*>(out), out_stride, status, lanes_log2, slabs);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+extern "C" cp_status cp_embed(const void* weight, int dtype, uint64_t n_rows, uint32_t d,
+                              uint64_t weight_stride, const int64_t* ids, uint64_t n, float scale,
+                              void* out, uint64_t out_stride, uint32_t* status, void* stream) {
+  if (!dtype_ok(dtype) || d == 0 || d > (1u << 20) || n >= (1ull << 31) || weight_stride < d ||
+      out_stride < d) {
+    cpx::set_error("bad dtype, d, n or row stride");
+    return CP_ERR_INVALID_ARG;
+  }
+  if (n == 0) return CP_OK;
+  const uint64_t elt = dtype_size(dtype);
+  if ((weight == nullptr && n_rows != 0) || ids == nullptr || out == nullptr ||
+      !cpx::aligned(weight, elt) || !cpx::aligned(out, elt) || !cpx::aligned(ids, 8) ||
+      !cpx::aligned(status, 4)) {
+    cpx::set_error("null or misaligned weight, ids, out or status");
+    return CP_ERR_INVALID_ARG;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (dtype == CP_F32)
+    e = launch<float>(weight, n_rows, d, weight_stride, ids, n, scale, out, out_stride, status, s);
+  else if (dtype == CP_F16)
+    e = launch<__half>(weight, n_rows, d, weight_stride, ids, n, scale, out, out_stride, status, s);
+  else
+    e = launch<__nv_bfloat16>(weight, n_rows, d, weight_stride, ids, n, scale, out, out_stride,
+                              status, s);
+  if (e != cudaSuccess) return cpx::cuda_fail(e, "embed launch");
+  return CP_OK;
+}

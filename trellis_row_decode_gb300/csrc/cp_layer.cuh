@@ -1,0 +1,242 @@
+// cp_layer.cuh -- helpers shared by the memory layer's kernels (embed, RMS norm,
+// 8-bit quantiser, 8-bit product): element types, octets of eight elements (the
+// unit that one lane loads and stores), reductions, e4m3 groups.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "cp.h"
+
+namespace cpl {
+
+// ---------------------------------------------------------------- element types
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+
+// One value of an array whose type is known at run time (CP_F32, CP_F16, CP_BF16);
+// the branch is the same for every thread.
+__device__ __forceinline__ float load_as_f32(const void* p, uint64_t i, int dtype) {
+  if (dtype == CP_F32) return __ldg(static_cast<const float*>(p) + i);
+  if (dtype == CP_F16) return to_f32(static_cast<const __half*>(p)[i]);
+  return to_f32(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+__device__ __forceinline__ void store_from_f32(void* p, uint64_t i, int dtype, float x) {
+  if (dtype == CP_F32) static_cast<float*>(p)[i] = x;
+  else if (dtype == CP_F16) static_cast<__half*>(p)[i] = from_f32<__half>(x);
+  else static_cast<__nv_bfloat16*>(p)[i] = from_f32<__nv_bfloat16>(x);
+}
+
+// ---------------------------------------------------------------------- octets
+//
+// An octet is eight consecutive elements.  Packed<T> holds one as loaded, 16 bytes
+// (16-bit types: one 128-bit access) or 32 bytes (fp32: one 256-bit access), so a
+// kernel can keep several in flight before it converts them.
+
+template <typename T>
+struct Packed {
+  static constexpr int kWords = sizeof(T) * 2;
+  uint32_t w[kWords];
+};
+
+template <typename T>
+__device__ __forceinline__ Packed<T> load_octet(const T* p) {
+  Packed<T> r;
+  if constexpr (sizeof(T) == 2) {
+    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
+                 : "l"(p));
+  } else {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]),
+                   "=r"(r.w[5]), "=r"(r.w[6]), "=r"(r.w[7])
+                 : "l"(p));
+  }
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_octet(T* p, const Packed<T>& r) {
+  if constexpr (sizeof(T) == 2) {
+    asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(r.w[0]), "r"(r.w[1]),
+                 "r"(r.w[2]), "r"(r.w[3])
+                 : "memory");
+  } else {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r.w[0]),
+                 "r"(r.w[1]), "r"(r.w[2]), "r"(r.w[3]), "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]),
+                 "r"(r.w[7])
+                 : "memory");
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack(const Packed<T>& r, float (&v)[8]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint16_t lo = static_cast<uint16_t>(r.w[i]), hi = static_cast<uint16_t>(r.w[i] >> 16);
+      if constexpr (sizeof(T) == 2) {
+        T a, b;
+        memcpy(&a, &lo, 2);
+        memcpy(&b, &hi, 2);
+        v[2 * i] = to_f32(a);
+        v[2 * i + 1] = to_f32(b);
+      }
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ Packed<T> pack(const float (&v)[8]) {
+  Packed<T> r;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.w[i] = __float_as_uint(v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const T a = from_f32<T>(v[2 * i]), b = from_f32<T>(v[2 * i + 1]);
+      uint16_t lo, hi;
+      memcpy(&lo, &a, 2);
+      memcpy(&hi, &b, 2);
+      r.w[i] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+    }
+  }
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ Packed<T> zero_octet() {
+  Packed<T> r;
+#pragma unroll
+  for (int i = 0; i < Packed<T>::kWords; ++i) r.w[i] = 0;
+  return r;
+}
+
+// Octet `o` of a row of d elements at p.  VEC: rows whose every octet is whole and
+// aligned to its own size; otherwise single elements, and the last octet may be
+// part full (the rest reads as zero and is not written).
+template <typename T, bool VEC>
+__device__ __forceinline__ Packed<T> load_row_octet(const T* row, uint32_t o, uint32_t d) {
+  if constexpr (VEC) {
+    return load_octet(row + 8ull * o);
+  } else {
+    Packed<T> r = zero_octet<T>();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t c = 8 * o + i;
+      if (c < d) {
+        if constexpr (sizeof(T) == 4) {
+          r.w[i] = reinterpret_cast<const uint32_t*>(row)[c];
+        } else {
+          const uint32_t u = reinterpret_cast<const uint16_t*>(row)[c];
+          r.w[i / 2] |= u << (16 * (i & 1));
+        }
+      }
+    }
+    return r;
+  }
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_row_octet(T* row, uint32_t o, uint32_t d,
+                                                const Packed<T>& r) {
+  if constexpr (VEC) {
+    store_octet(row + 8ull * o, r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t c = 8 * o + i;
+      if (c < d) {
+        if constexpr (sizeof(T) == 4) {
+          reinterpret_cast<uint32_t*>(row)[c] = r.w[i];
+        } else {
+          reinterpret_cast<uint16_t*>(row)[c] = static_cast<uint16_t>(r.w[i / 2] >> (16 * (i & 1)));
+        }
+      }
+    }
+  }
+}
+
+// Whether rows at p, `stride` elements apart and d long, may be read by whole octets.
+inline bool octets_ok(const void* p, uint64_t stride, uint32_t d, uint64_t elt) {
+  return reinterpret_cast<uintptr_t>(p) % (8 * elt) == 0 && stride % 8 == 0 && d % 8 == 0;
+}
+
+inline uint64_t dtype_size(int dtype) { return dtype == CP_F32 ? 4 : 2; }
+inline bool dtype_ok(int dtype) { return dtype == CP_F32 || dtype == CP_F16 || dtype == CP_BF16; }
+
+// ------------------------------------------------------------------- reductions
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+  return x;
+}
+
+// Largest magnitude as the bits of |x|: ordered like the magnitudes themselves, with
+// infinity above every number and NaN above infinity, so a NaN is never lost.
+__device__ __forceinline__ uint32_t mag_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// ---------------------------------------------------------------- e4m3 and scales
+//
+// A group's scale is amax / 448, 448 the largest e4m3 value; amax below 1e-30 counts
+// as 1e-30, so the scale and its reciprocal stay normal numbers and a group of zeros
+// gives zeros.  Values are multiplied by the reciprocal of the rounded scale, at most
+// 448 (1 + 2^-22), and the conversion saturates: no finite value of a finite group
+// becomes NaN.  A NaN or an infinity in the group makes its scale NaN or infinite,
+// and the values that carry it NaN: y / scale, as the formula says.
+__device__ __forceinline__ float scale_of(uint32_t amax_bits) {
+  float amax = __uint_as_float(amax_bits);
+  if (amax < 1e-30f) amax = 1e-30f;
+  return __fdiv_rn(amax, 448.0f);
+}
+
+__device__ __forceinline__ uint2 quantize_octet(const float (&v)[8], float inv) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+        make_float2(v[4 * i] * inv, v[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+        make_float2(v[4 * i + 2] * inv, v[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+    w[i] = lo | (hi << 16);
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// VEC: q rows 8-byte aligned with whole octets.
+template <bool VEC>
+__device__ __forceinline__ void store_q_octet(uint8_t* row, uint32_t o, uint32_t d, uint2 q) {
+  if constexpr (VEC) {
+    *reinterpret_cast<uint2*>(row + 8ull * o) = q;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t c = 8 * o + i;
+      if (c < d) row[c] = static_cast<uint8_t>((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+    }
+  }
+}
+
+}  // namespace cpl

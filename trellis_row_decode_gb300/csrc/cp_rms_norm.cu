@@ -1,0 +1,573 @@
+// cp_rms_norm.cu -- root-mean-square norm with the residual's addition, in the
+// input's type or in 8 bits with scales, and its gradients (include/cp.h).
+//
+//   s = x + residual,  r = 1 / sqrt(mean(s^2) + eps),  y = s r w
+//   scales = amax |y| / 448 over 128 columns,  q = e4m3(y / scales)
+//   dx = dres + r (t - n mean(t n)),  dw = sum over rows of dy n,  n = s r, t = dy w
+//
+// One pass: a row's octets stay in registers between the sum of squares and the
+// scaling, so every array is read and written once and the kernels are bound by
+// memory.  A team of threads holds a row (kOct octets a thread); 16 neighbouring lanes
+// hold one group of 128 columns, whose largest magnitude takes four shuffles.  Rows too
+// wide for the registers of one team (d > 16384) are read twice, the second time from
+// the cache.
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "cp.h"
+#include "cp_internal.h"
+#include "cp_layer.cuh"
+
+namespace {
+
+using namespace cpl;
+
+constexpr uint32_t kMaxD = 49152;      // the weight gradient's sums of one CTA: 192 KB
+
+struct NormParams {
+  const void* x;
+  const void* residual;        // or null
+  const void* weight;
+  void* y;                     // null: the 8-bit output
+  void* h;                     // with the residual
+  uint8_t* q;
+  float* scales;
+  uint64_t x_stride, residual_stride;
+  uint32_t rows, d;
+  int weight_dtype;
+  float eps;
+};
+
+// Sums `a` and `b` over the CTA's threads, in the same order on every thread.
+// (One barrier each way: `red` is written again only behind the next call's.)
+template <int THREADS>
+__device__ __forceinline__ void team_sum(float& a, float& b, float2* red) {
+  a = warp_sum(a);
+  b = warp_sum(b);
+  if constexpr (THREADS > 32) {
+    constexpr int W = THREADS / 32;
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    a = b = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float2 v = red[w];
+      a += v.x;
+      b += v.y;
+    }
+  }
+}
+
+// Eight weights of octet o (zeros past d).
+template <bool VEC>
+__device__ __forceinline__ void load_weight(const void* w, int dtype, uint32_t o, uint32_t d,
+                                            float (&v)[8]) {
+  if constexpr (VEC) {
+    if (dtype == CP_F32)
+      unpack<float>(load_octet(static_cast<const float*>(w) + 8ull * o), v);
+    else if (dtype == CP_F16)
+      unpack<__half>(load_octet(static_cast<const __half*>(w) + 8ull * o), v);
+    else
+      unpack<__nv_bfloat16>(load_octet(static_cast<const __nv_bfloat16*>(w) + 8ull * o), v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 8 * o + e < d ? load_as_f32(w, 8 * o + e, dtype) : 0.0f;
+  }
+}
+
+// One octet of s = x + residual.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_sum(const NormParams& p, const T* x, const T* res, uint32_t o,
+                                         float (&v)[8]) {
+  unpack<T>(load_row_octet<T, VEC>(x, o, p.d), v);
+  if (res != nullptr) {
+    float u[8];
+    unpack<T>(load_row_octet<T, VEC>(res, o, p.d), u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += u[e];
+  }
+}
+
+// The octet's part of the output.  All lanes of the warp take part (the group's
+// largest magnitude is shuffled); `live`: the octet lies in the row.
+template <typename T, bool VEC, bool Q>
+__device__ __forceinline__ void emit(const NormParams& p, uint64_t row, uint32_t o, bool live,
+                                     float r, const float (&s)[8]) {
+  float y[8];
+  if (live) {
+    if (p.residual != nullptr)
+      store_row_octet<T, VEC>(static_cast<T*>(p.h) + row * p.d, o, p.d, pack<T>(s));
+    load_weight<VEC>(p.weight, p.weight_dtype, o, p.d, y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = s[e] * r * y[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = 0.0f;
+  }
+  if constexpr (!Q) {
+    if (live) store_row_octet<T, VEC>(static_cast<T*>(p.y) + row * p.d, o, p.d, pack<T>(y));
+  } else {
+    uint32_t amax = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (VEC || 8 * o + e < p.d) amax = max(amax, mag_bits(y[e]));
+#pragma unroll
+    for (int m = 8; m > 0; m >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, m));
+    const float scale = scale_of(amax);
+    if (live) {
+      store_q_octet<VEC>(p.q + row * p.d, o, p.d, quantize_octet(y, __frcp_rn(scale)));
+      if ((o & 15) == 0) p.scales[row * ((p.d + 127) / 128) + o / 16] = scale;
+    }
+  }
+}
+
+// A row per team of THREADS threads; one warp: several rows per CTA.
+template <typename T, bool VEC, bool Q, int THREADS, int kOct>
+__global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS) norm_kernel(NormParams p) {
+  constexpr int kTeams = THREADS == 32 ? 4 : 1;
+  __shared__ float2 red[THREADS / 32];
+  const uint32_t tid = threadIdx.x % THREADS;
+  const uint64_t row = static_cast<uint64_t>(blockIdx.x) * kTeams + threadIdx.x / THREADS;
+  if (row >= p.rows) return;
+  const uint32_t octets = (p.d + 7) / 8;
+  const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
+  const T* res = p.residual != nullptr
+                     ? static_cast<const T*>(p.residual) + row * p.residual_stride
+                     : nullptr;
+  float s[kOct][8];
+  float sq = 0.0f, unused = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kOct; ++i) {
+    const uint32_t o = tid + i * THREADS;
+    if (o < octets) {
+      load_sum<T, VEC>(p, x, res, o, s[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[i][e] = 0.0f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kOct; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sq = fmaf(s[i][e], s[i][e], sq);
+  team_sum<THREADS>(sq, unused, red);
+  const float r = 1.0f / sqrtf(sq / static_cast<float>(p.d) + p.eps);
+#pragma unroll
+  for (int i = 0; i < kOct; ++i) {
+    const uint32_t o = tid + i * THREADS;
+    emit<T, VEC, Q>(p, row, o, o < octets, r, s[i]);
+  }
+}
+
+// Rows of any width: the second reading comes from the cache.
+template <typename T, bool VEC, bool Q>
+__global__ void __launch_bounds__(1024) norm_wide_kernel(NormParams p) {
+  __shared__ float2 red[32];
+  const uint64_t row = blockIdx.x;
+  const uint32_t octets = (p.d + 7) / 8;
+  const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
+  const T* res = p.residual != nullptr
+                     ? static_cast<const T*>(p.residual) + row * p.residual_stride
+                     : nullptr;
+  float sq = 0.0f, unused = 0.0f;
+  for (uint32_t o = threadIdx.x; o < octets; o += 1024) {
+    float s[8];
+    load_sum<T, VEC>(p, x, res, o, s);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sq = fmaf(s[e], s[e], sq);
+  }
+  team_sum<1024>(sq, unused, red);
+  const float r = 1.0f / sqrtf(sq / static_cast<float>(p.d) + p.eps);
+  for (uint32_t o0 = 0; o0 < octets; o0 += 1024) {
+    const uint32_t o = o0 + threadIdx.x;
+    float s[8] = {};
+    if (o < octets) load_sum<T, VEC>(p, x, res, o, s);
+    emit<T, VEC, Q>(p, row, o, o < octets, r, s);
+  }
+}
+
+// ------------------------------------------------------------------------ gradient
+
+struct GradParams {
+  const void* dy;
+  const void* h;
+  const void* dres;            // or null
+  const void* weight;
+  void* dx;
+  void* dw;
+  float* parts;                // [gridDim.x][d]: each CTA's sums for dw
+  uint64_t dy_stride, h_stride, dres_stride;
+  uint32_t rows, d, ctas;
+  int weight_dtype;
+  float eps;
+};
+
+// dx = dres + r t - h r^3 mean(t h), the formula with n = h r written out.
+template <typename T, bool VEC>
+__device__ __forceinline__ void emit_dx(const GradParams& p, uint64_t row, uint32_t o, float r,
+                                        float c, const float (&t)[8], const float (&h)[8]) {
+  float dx[8];
+  if (p.dres != nullptr) {
+    unpack<T>(load_row_octet<T, VEC>(static_cast<const T*>(p.dres) + row * p.dres_stride, o, p.d),
+              dx);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dx[e] = 0.0f;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) dx[e] += r * (t[e] - h[e] * c);
+  store_row_octet<T, VEC>(static_cast<T*>(p.dx) + row * p.d, o, p.d, pack<T>(dx));
+}
+
+// CTAs walk over the rows; a thread's columns are the same in every row, so it sums
+// its part of dw in registers and leaves it behind the last row.
+template <typename T, bool VEC, int THREADS, int kOct>
+__global__ void __launch_bounds__(THREADS) norm_grad_kernel(GradParams p) {
+  __shared__ float2 red[THREADS / 32];
+  const uint32_t octets = (p.d + 7) / 8;
+  float dw[kOct][8];
+#pragma unroll
+  for (int i = 0; i < kOct; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
+  for (uint64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const T* dyr = static_cast<const T*>(p.dy) + row * p.dy_stride;
+    const T* hr = static_cast<const T*>(p.h) + row * p.h_stride;
+    Packed<T> g[kOct], hp[kOct];
+#pragma unroll
+    for (int i = 0; i < kOct; ++i) {
+      const uint32_t o = threadIdx.x + i * THREADS;
+      hp[i] = o < octets ? load_row_octet<T, VEC>(hr, o, p.d) : zero_octet<T>();
+      g[i] = o < octets ? load_row_octet<T, VEC>(dyr, o, p.d) : zero_octet<T>();
+    }
+    float sq = 0.0f, th = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kOct; ++i) {
+      const uint32_t o = threadIdx.x + i * THREADS;
+      float h[8], t[8], w[8];
+      unpack<T>(hp[i], h);
+      unpack<T>(g[i], t);
+      if (o < octets) {
+        load_weight<VEC>(p.weight, p.weight_dtype, o, p.d, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          sq = fmaf(h[e], h[e], sq);
+          th = fmaf(t[e] * w[e], h[e], th);
+        }
+      }
+    }
+    team_sum<THREADS>(sq, th, red);
+    const float inv_d = 1.0f / static_cast<float>(p.d);
+    const float r = 1.0f / sqrtf(sq * inv_d + p.eps);
+    const float c = r * r * (th * inv_d);
+#pragma unroll
+    for (int i = 0; i < kOct; ++i) {
+      const uint32_t o = threadIdx.x + i * THREADS;
+      if (o < octets) {
+        float h[8], t[8], w[8];
+        unpack<T>(hp[i], h);
+        unpack<T>(g[i], t);
+        load_weight<VEC>(p.weight, p.weight_dtype, o, p.d, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          dw[i][e] = fmaf(t[e], h[e] * r, dw[i][e]);
+          t[e] *= w[e];
+        }
+        emit_dx<T, VEC>(p, row, o, r, c, t, h);
+      }
+    }
+  }
+  float* part = p.parts + static_cast<uint64_t>(blockIdx.x) * p.d;
+#pragma unroll
+  for (int i = 0; i < kOct; ++i) {
+    const uint32_t o = threadIdx.x + i * THREADS;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (8 * o + e < p.d) part[8 * o + e] = dw[i][e];
+  }
+}
+
+// Rows wider than the registers: read twice, dw summed in shared memory (each thread
+// its own columns).
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(1024) norm_grad_wide_kernel(GradParams p) {
+  __shared__ float2 red[32];
+  extern __shared__ float dw[];
+  const uint32_t octets = (p.d + 7) / 8;
+  for (uint32_t o = threadIdx.x; o < octets; o += 1024)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[e * octets + o] = 0.0f;
+  for (uint64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const T* dyr = static_cast<const T*>(p.dy) + row * p.dy_stride;
+    const T* hr = static_cast<const T*>(p.h) + row * p.h_stride;
+    float sq = 0.0f, th = 0.0f;
+    for (uint32_t o = threadIdx.x; o < octets; o += 1024) {
+      float h[8], t[8], w[8];
+      unpack<T>(load_row_octet<T, VEC>(hr, o, p.d), h);
+      unpack<T>(load_row_octet<T, VEC>(dyr, o, p.d), t);
+      load_weight<VEC>(p.weight, p.weight_dtype, o, p.d, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sq = fmaf(h[e], h[e], sq);
+        th = fmaf(t[e] * w[e], h[e], th);
+      }
+    }
+    team_sum<1024>(sq, th, red);
+    const float inv_d = 1.0f / static_cast<float>(p.d);
+    const float r = 1.0f / sqrtf(sq * inv_d + p.eps);
+    const float c = r * r * (th * inv_d);
+    for (uint32_t o = threadIdx.x; o < octets; o += 1024) {
+      float h[8], t[8], w[8];
+      unpack<T>(load_row_octet<T, VEC>(hr, o, p.d), h);
+      unpack<T>(load_row_octet<T, VEC>(dyr, o, p.d), t);
+      load_weight<VEC>(p.weight, p.weight_dtype, o, p.d, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        dw[e * octets + o] = fmaf(t[e], h[e] * r, dw[e * octets + o]);
+        t[e] *= w[e];
+      }
+      emit_dx<T, VEC>(p, row, o, r, c, t, h);
+    }
+  }
+  float* part = p.parts + static_cast<uint64_t>(blockIdx.x) * p.d;
+  for (uint32_t o = threadIdx.x; o < octets; o += 1024)
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (8 * o + e < p.d) part[8 * o + e] = dw[e * octets + o];
+}
+
+constexpr int kDwThreads = 1024;
+
+// dw[c] = sum of the CTAs' parts in order: 32 columns a CTA, 32 warps a contiguous share
+// of the parts each.
+__global__ void __launch_bounds__(kDwThreads) norm_dw_kernel(GradParams p) {
+  __shared__ float sums[32][33];
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t col = blockIdx.x * 32 + lane;
+  const uint32_t share = (p.ctas + 31) / 32;
+  const uint32_t lo = warp * share, hi = min(lo + share, p.ctas);
+  float s = 0.0f;
+  if (col < p.d) {
+#pragma unroll 8
+    for (uint32_t k = lo; k < hi; ++k) s += p.parts[static_cast<uint64_t>(k) * p.d + col];
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && col < p.d) {
+    for (int w = 1; w < 32; ++w) s += sums[w][lane];
+    store_from_f32(p.dw, col, p.weight_dtype, s);
+  }
+}
+
+// -------------------------------------------------------------------------- host
+
+template <typename T, bool VEC, bool Q>
+cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
+  const uint32_t octets = (p.d + 7) / 8;
+  if (octets <= 128) {
+    norm_kernel<T, VEC, Q, 32, 4><<<(p.rows + 3) / 4, 128, 0, s>>>(p);
+  } else if (octets <= 256) {
+    norm_kernel<T, VEC, Q, 128, 2><<<p.rows, 128, 0, s>>>(p);
+  } else if (octets <= 512) {
+    norm_kernel<T, VEC, Q, 256, 2><<<p.rows, 256, 0, s>>>(p);
+  } else if (octets <= 1024) {
+    norm_kernel<T, VEC, Q, 512, 2><<<p.rows, 512, 0, s>>>(p);
+  } else if (octets <= 2048) {
+    norm_kernel<T, VEC, Q, 1024, 2><<<p.rows, 1024, 0, s>>>(p);
+  } else {
+    norm_wide_kernel<T, VEC, Q><<<p.rows, 1024, 0, s>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_norm(const NormParams& p, bool vec, cudaStream_t s) {
+  if (p.y == nullptr)
+    return vec ? launch_norm<T, true, true>(p, s) : launch_norm<T, false, true>(p, s);
+  return vec ? launch_norm<T, true, false>(p, s) : launch_norm<T, false, false>(p, s);
+}
+
+template <typename T, bool VEC>
+cudaError_t launch_grad(const GradParams& p, cudaStream_t s) {
+  const uint32_t octets = (p.d + 7) / 8;
+  if (octets <= 128) {
+    norm_grad_kernel<T, VEC, 128, 1><<<p.ctas, 128, 0, s>>>(p);
+  } else if (octets <= 256) {
+    norm_grad_kernel<T, VEC, 128, 2><<<p.ctas, 128, 0, s>>>(p);
+  } else if (octets <= 512) {
+    norm_grad_kernel<T, VEC, 256, 2><<<p.ctas, 256, 0, s>>>(p);
+  } else if (octets <= 1024) {
+    norm_grad_kernel<T, VEC, 512, 2><<<p.ctas, 512, 0, s>>>(p);
+  } else {
+    const int smem = static_cast<int>(octets * 32);
+    auto* fn = &norm_grad_wide_kernel<T, VEC>;
+    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    fn<<<p.ctas, 1024, smem, s>>>(p);
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  norm_dw_kernel<<<(p.d + 31) / 32, kDwThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+// CTAs of a gradient call: enough to fill the card, each with its own sums for dw.
+uint32_t grad_ctas(uint64_t rows, uint32_t d) {
+  const uint32_t octets = (d + 7) / 8;
+  const uint64_t per_sm = octets <= 256 ? 8 : octets <= 512 ? 4 : octets <= 1024 ? 2 : 1;
+  const uint64_t most = per_sm * 152;
+  return static_cast<uint32_t>(rows < most ? rows : most);
+}
+
+// Checks shared by the norms; writes whether whole octets can be moved.
+cp_status norm_args(NormParams* p, const void* x, uint64_t x_stride, const void* residual,
+                    uint64_t residual_stride, int dtype, const void* weight, int weight_dtype,
+                    uint64_t rows, uint32_t d, float eps, const void* out, uint64_t out_align,
+                    uint64_t out_vec, void* h, bool* vec) {
+  if (!dtype_ok(dtype) || !dtype_ok(weight_dtype) || d == 0 || d > kMaxD || rows >= (1ull << 31) ||
+      (x_stride < d && x_stride != 0) || !(eps >= 0.0f) ||
+      (residual != nullptr && residual_stride < d && residual_stride != 0)) {
+    cpx::set_error("bad dtype, rows, d, row stride or eps");
+    return CP_ERR_INVALID_ARG;
+  }
+  if ((residual == nullptr) != (h == nullptr)) {
+    cpx::set_error("residual and h go together");
+    return CP_ERR_INVALID_ARG;
+  }
+  const uint64_t elt = dtype_size(dtype), welt = dtype_size(weight_dtype);
+  if (rows != 0 && (x == nullptr || weight == nullptr || out == nullptr || !cpx::aligned(x, elt) ||
+                    !cpx::aligned(residual, elt) || !cpx::aligned(h, elt) ||
+                    !cpx::aligned(weight, welt) || !cpx::aligned(out, out_align))) {
+    cpx::set_error("null or misaligned x, residual, weight or output");
+    return CP_ERR_INVALID_ARG;
+  }
+  p->x = x;
+  p->residual = residual;
+  p->weight = weight;
+  p->h = h;
+  p->x_stride = x_stride;
+  p->residual_stride = residual_stride;
+  p->rows = static_cast<uint32_t>(rows);
+  p->d = d;
+  p->weight_dtype = weight_dtype;
+  p->eps = eps;
+  *vec = octets_ok(x, x_stride, d, elt) && octets_ok(weight, 0, d, welt) &&
+         cpx::aligned(out, out_vec) &&
+         (residual == nullptr ||
+          (octets_ok(residual, residual_stride, d, elt) && octets_ok(h, d, d, elt)));
+  return CP_OK;
+}
+
+cp_status run_norm(const NormParams& p, int dtype, bool vec, cudaStream_t s) {
+  if (p.rows == 0) return CP_OK;
+  cudaError_t e;
+  if (dtype == CP_F32) e = launch_norm<float>(p, vec, s);
+  else if (dtype == CP_F16) e = launch_norm<__half>(p, vec, s);
+  else e = launch_norm<__nv_bfloat16>(p, vec, s);
+  if (e != cudaSuccess) return cpx::cuda_fail(e, "rms norm launch");
+  return CP_OK;
+}
+
+}  // namespace
+
+extern "C" cp_status cp_rms_norm(const void* x, uint64_t x_stride, const void* residual,
+                                 uint64_t residual_stride, int dtype, const void* weight,
+                                 int weight_dtype, uint64_t rows, uint32_t d, float eps, void* y,
+                                 void* h, void* stream) {
+  NormParams p{};
+  bool vec = false;
+  const uint64_t elt = dtype_ok(dtype) ? dtype_size(dtype) : 4;
+  const cp_status st = norm_args(&p, x, x_stride, residual, residual_stride, dtype, weight,
+                                 weight_dtype, rows, d, eps, y, elt, 8 * elt, h, &vec);
+  if (st != CP_OK) return st;
+  p.y = y;
+  return run_norm(p, dtype, vec, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" cp_status cp_rms_norm_fp8(const void* x, uint64_t x_stride, const void* residual,
+                                     uint64_t residual_stride, int dtype, const void* weight,
+                                     int weight_dtype, uint64_t rows, uint32_t d, float eps,
+                                     uint8_t* q, float* scales, void* h, void* stream) {
+  NormParams p{};
+  bool vec = false;
+  const cp_status st = norm_args(&p, x, x_stride, residual, residual_stride, dtype, weight,
+                                 weight_dtype, rows, d, eps, q, 1, 8, h, &vec);
+  if (st != CP_OK) return st;
+  if (rows != 0 && (scales == nullptr || !cpx::aligned(scales, 4))) {
+    cpx::set_error("null or misaligned scales");
+    return CP_ERR_INVALID_ARG;
+  }
+  p.q = q;
+  p.scales = scales;
+  return run_norm(p, dtype, vec, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" uint64_t cp_rms_norm_grad_workspace_bytes(uint64_t rows, uint32_t d) {
+  if (d == 0 || d > kMaxD || rows >= (1ull << 31)) return 0;
+  const uint64_t bytes = 4ull * grad_ctas(rows, d) * d;
+  return bytes == 0 ? 16 : bytes;
+}
+
+extern "C" cp_status cp_rms_norm_grad(const void* dy, uint64_t dy_stride, const void* h,
+                                      uint64_t h_stride, const void* dres, uint64_t dres_stride,
+                                      int dtype, const void* weight, int weight_dtype,
+                                      uint64_t rows, uint32_t d, float eps, void* dx, void* dw,
+                                      void* workspace, uint64_t workspace_bytes, void* stream) {
+  if (!dtype_ok(dtype) || !dtype_ok(weight_dtype) || d == 0 || d > kMaxD || rows >= (1ull << 31) ||
+      (dy_stride < d && dy_stride != 0) || (h_stride < d && h_stride != 0) ||
+      (dres != nullptr && dres_stride < d && dres_stride != 0) || !(eps >= 0.0f)) {
+    cpx::set_error("bad dtype, rows, d, row stride or eps");
+    return CP_ERR_INVALID_ARG;
+  }
+  const uint64_t elt = dtype_size(dtype), welt = dtype_size(weight_dtype);
+  if (dw == nullptr || !cpx::aligned(dw, welt) ||
+      (rows != 0 && (dy == nullptr || h == nullptr || weight == nullptr || dx == nullptr ||
+                     !cpx::aligned(dy, elt) || !cpx::aligned(h, elt) || !cpx::aligned(dres, elt) ||
+                     !cpx::aligned(dx, elt) || !cpx::aligned(weight, welt)))) {
+    cpx::set_error("null or misaligned dy, h, dres, weight, dx or dw");
+    return CP_ERR_INVALID_ARG;
+  }
+  if (workspace == nullptr || !cpx::aligned(workspace, 16) ||
+      workspace_bytes < cp_rms_norm_grad_workspace_bytes(rows, d)) {
+    cpx::set_error(
+        "workspace must be 16-byte aligned and hold cp_rms_norm_grad_workspace_bytes bytes");
+    return CP_ERR_INVALID_ARG;
+  }
+  GradParams p{};
+  p.dy = dy;
+  p.h = h;
+  p.dres = dres;
+  p.weight = weight;
+  p.dx = dx;
+  p.dw = dw;
+  p.parts = static_cast<float*>(workspace);
+  p.dy_stride = dy_stride;
+  p.h_stride = h_stride;
+  p.dres_stride = dres_stride;
+  p.rows = static_cast<uint32_t>(rows);
+  p.d = d;
+  p.ctas = grad_ctas(rows, d);
+  p.weight_dtype = weight_dtype;
+  p.eps = eps;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (rows == 0) {
+    norm_dw_kernel<<<(d + 31) / 32, kDwThreads, 0, s>>>(p);      // no parts: zeros
+    e = cudaGetLastError();
+  } else {
+    const bool vec = octets_ok(dy, dy_stride, d, elt) && octets_ok(h, h_stride, d, elt) &&
+                     octets_ok(dx, d, d, elt) && octets_ok(weight, 0, d, welt) &&
+                     (dres == nullptr || octets_ok(dres, dres_stride, d, elt));
+    if (dtype == CP_F32)
+      e = vec ? launch_grad<float, true>(p, s) : launch_grad<float, false>(p, s);
+    else if (dtype == CP_F16)
+      e = vec ? launch_grad<__half, true>(p, s) : launch_grad<__half, false>(p, s);
+    else
+      e = vec ? launch_grad<__nv_bfloat16, true>(p, s) : launch_grad<__nv_bfloat16, false>(p, s);
+  }
+  if (e != cudaSuccess) return cpx::cuda_fail(e, "rms norm gradient launch");
+  return CP_OK;
+}
