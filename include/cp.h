@@ -490,6 +490,13 @@ cp_status cp_matmul_fp8(const uint8_t* a, uint64_t a_stride, const float* a_scal
                         uint64_t n, uint64_t k, void* out, int out_dtype, uint64_t out_stride,
                         void* stream);
 
+/*
+ * cp_matmul_fp8_status -- synchronise `stream`, then report and clear the current
+ * device's record of waits that ran out inside cp_matmul_fp8 (two seconds each; the
+ * kernel then returns and its output is not valid): CP_ERR_CUDA if there was one.
+ */
+cp_status cp_matmul_fp8_status(void* stream);
+
 /* Release what the handle owns (LUT copy, status word, host registration made
  * by cp_table_load).  Borrowed buffers are untouched.  NULL is a no-op. */
 void cp_table_free(cp_table* t);

@@ -158,6 +158,10 @@ def test_matmul_on_another_stream_and_in_a_graph():
         assert torch.equal(ref, out)
 
 
+def test_matmul_status_is_clear():
+    assert cp.matmul_fp8_status() == cp.CP_OK
+
+
 def test_matmul_refusals():
     g = gen(1)
     a, sa, w, sw = _operands(g, 4, 200, 256)

@@ -5,13 +5,16 @@
 //
 // The products of a group are exact in the tensor core's fp32 sums; a group's sum is
 // scaled and added to the running fp32 sum before the next group begins.
+#include <atomic>
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "cp.h"
 #include "cp_internal.h"
 #include "cp_layer.cuh"
+#include "cp_tcgen05.cuh"
 
 namespace {
 
@@ -159,7 +162,484 @@ __global__ void __launch_bounds__(kAnyThreads) matmul_any_kernel(MatmulParams p)
       }
 }
 
+// ------------------------------------------------- rows on 16-byte boundaries: tcgen05
+//
+// A pair of CTAs (two SMs) makes 256 x bn outputs, bn a multiple of 32 up to 256.  Each
+// CTA stages its 128 rows of a and its half of the bn rows of w (128 bytes of k a stage,
+// 128-byte swizzle), so a byte that enters an SM feeds both tensor cores.  Roles: one
+// thread per CTA issues the TMA loads; one thread of the first CTA issues four
+// tcgen05.mma (k = 32 each) per group of 128 into one of two tensor-memory buffers; eight
+// warps per CTA read the other buffer, scale it and add it to their registers (a lane has
+// a row, a warp half of the columns).  The scales differ from group to group, so the
+// running sum cannot stay in tensor memory; the two buffers let the tensor core work on
+// the next group meanwhile.  With few tiles, `splits` pairs of one cluster share a tile's
+// groups and add their sums, in the order of the pairs, through distributed shared memory.
+
+constexpr int kSumWarps = 8;
+constexpr int kTcThreads = (kSumWarps + 4) * 32;       // + the TMA warp, the MMA warp and two idle
+// Registers: launched with 168 a thread (65,536 over 12 warps); the eight summing warps (128
+// sums and 32 values in flight a thread) take what the other four give up.
+constexpr int kLaunchRegs = 168, kSumRegs = 224, kOtherRegs = 56;
+static_assert(2 * kSumRegs + kOtherRegs <= 3 * kLaunchRegs, "a warpgroup's share of the launch");
+constexpr uint32_t kMaxStages = 8;
+constexpr uint32_t kTileA = 128 * 128;                 // bytes of a's rows per stage and CTA
+constexpr uint32_t kSmemMost = 224 * 1024;             // dynamic shared memory of a CTA
+
+// A wait that ran out sets this word; cp_matmul_fp8_status reads and clears it.
+__device__ uint32_t g_matmul_gave_up;
+
+struct TcParams {
+  const float* sa;
+  const float* sw;
+  void* out;
+  uint64_t ldo;
+  uint32_t m, n, groups;
+  int out_dtype;
+  uint32_t bn, tiles_m, tiles, stages, splits, tmem_columns;
+  uint32_t a_rows;          // rows of a's TMA box
+  bool vec;                 // out rows on 16-byte boundaries
+};
+
+// Sixteen consecutive outputs of a row.
+__device__ __forceinline__ void store16(const TcParams& p, uint32_t row, uint32_t col,
+                                        const float (&v)[16]) {
+  const uint64_t at = static_cast<uint64_t>(row) * p.ldo + col;
+  if (p.vec && col + 16 <= p.n) {
+    if (p.out_dtype == CP_F32) {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+      uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float u[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = v[8 * i + e];
+        uint4 w;
+        if (p.out_dtype == CP_F16) {
+          const Packed<__half> r = pack<__half>(u);
+          w = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+        } else {
+          const Packed<__nv_bfloat16> r = pack<__nv_bfloat16>(u);
+          w = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+        }
+        o[i] = w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (col + e < p.n) store_from_f32(p.out, at + e, p.out_dtype, v[e]);
+  }
+}
+
+__global__ void __launch_bounds__(kTcThreads, 1)
+    matmul_tc_kernel(const __grid_constant__ CUtensorMap map_a,
+                     const __grid_constant__ CUtensorMap map_w, const TcParams p) {
+  extern __shared__ uint8_t dyn[];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 4];
+  __shared__ uint32_t tmem_base;
+  __shared__ int gave_up;
+  uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cpt::cluster_rank();
+  const uint32_t half = rank & 1, split = rank >> 1, first = rank & ~1u;
+  const uint32_t stage_bytes = kTileA + p.bn * 64;
+  const uint32_t full = cpt::smem_addr(bars), empty = full + 8 * kMaxStages;
+  const uint32_t acc_full = empty + 8 * kMaxStages, acc_empty = acc_full + 16;
+  // the first CTA's barriers hold the pair's loads and reads
+  const uint32_t pair_full = cpt::map_rank(full, first);
+  const uint32_t pair_acc_empty = cpt::map_rank(acc_empty, first);
+
+  if (threadIdx.x == 0) {
+    for (uint32_t s = 0; s < p.stages; ++s) {
+      cpt::mbar_init(full + 8 * s, 1);
+      cpt::mbar_init(empty + 8 * s, 1);
+    }
+    for (uint32_t b = 0; b < 2; ++b) {
+      cpt::mbar_init(acc_full + 8 * b, 1);
+      cpt::mbar_init(acc_empty + 8 * b, 2 * kSumWarps);
+    }
+    cpt::mbar_init_fence();
+    gave_up = 0;
+  }
+  if (warp == kSumWarps + 1) cpt::tmem_alloc_pair(cpt::smem_addr(&tmem_base), p.tmem_columns);
+  cpt::tc_fence_before();
+  __syncthreads();
+  cpt::cluster_sync();
+  cpt::tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  const uint32_t kb0 = static_cast<uint32_t>(static_cast<uint64_t>(p.groups) * split / p.splits);
+  const uint32_t kb1 =
+      static_cast<uint32_t>(static_cast<uint64_t>(p.groups) * (split + 1) / p.splits);
+  const uint32_t step = gridDim.x / (2 * p.splits), tile0 = blockIdx.x / (2 * p.splits);
+
+  if (warp >= kSumWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kSumWarps && lane == 0) {
+      // -------------------------------------------------------------- loads
+      cpt::tma_prefetch_map(&map_a);
+      cpt::tma_prefetch_map(&map_w);
+      const uint32_t w_bytes = p.bn * 64;
+      uint32_t it = 0;
+      bool ok = true;
+      for (uint32_t tile = tile0; tile < p.tiles && ok; tile += step) {
+        const uint32_t row0 = tile % p.tiles_m * 256, col0 = tile / p.tiles_m * p.bn;
+        const bool a0 = row0 < p.m, a1 = row0 + 128 < p.m;      // a's halves with any row
+        const bool mine = half ? a1 : a0;
+        const uint32_t bytes =
+            2 * w_bytes + ((a0 ? 1 : 0) + (a1 ? 1 : 0)) * p.a_rows * 128;
+        for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
+          const uint32_t s = it % p.stages, round = it / p.stages;
+          if (round > 0 && !cpt::mbar_wait(empty + 8 * s, (round - 1) & 1, &gave_up)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = cpt::smem_addr(tiles + s * stage_bytes);
+          if (half == 0) cpt::mbar_expect(full + 8 * s, bytes);
+          if (mine)
+            cpt::tma_load_pair(dst, &map_a, kb * 128, row0 + half * 128, pair_full + 8 * s);
+          cpt::tma_load_pair(dst + kTileA, &map_w, kb * 128, col0 + half * (p.bn / 2),
+                             pair_full + 8 * s);
+        }
+      }
+      if (!ok) {      // the loads in flight land before the CTA leaves
+        int unused = 0;
+        for (uint32_t k = it > p.stages ? it - p.stages : 0; half == 0 && k < it; ++k)
+          cpt::mbar_wait(full + 8 * (k % p.stages), (k / p.stages) & 1, &unused);
+      }
+    }
+    if (warp == kSumWarps + 1 && half == 0 && lane == 0) {
+      // ----------------------------------------------------------- products
+      const uint32_t instr = cpt::e4m3_instr_desc(256, p.bn);
+      const uint16_t pair = static_cast<uint16_t>(3u << first);
+      uint32_t it = 0;
+      bool ok = true;
+      for (uint32_t tile = tile0; tile < p.tiles && ok; tile += step) {
+        for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
+          const uint32_t s = it % p.stages, round = it / p.stages, b = it & 1;
+          if ((it >= 2 && !cpt::mbar_wait(acc_empty + 8 * b, ((it >> 1) - 1) & 1, &gave_up)) ||
+              !cpt::mbar_wait(full + 8 * s, round & 1, &gave_up)) {
+            ok = false;
+            break;
+          }
+          cpt::tc_fence_after();
+          const uint32_t at = cpt::smem_addr(tiles + s * stage_bytes);
+          const uint64_t da = cpt::operand_desc(at), dw = cpt::operand_desc(at + kTileA);
+#pragma unroll
+          for (uint32_t k = 0; k < 4; ++k)
+            cpt::mma_pair(tmem + b * p.bn, da + 2 * k, dw + 2 * k, instr, k != 0);
+          cpt::mma_commit_pair(empty + 8 * s, pair);
+          cpt::mma_commit_pair(acc_full + 8 * b, pair);
+        }
+      }
+    }
+  } else {
+    // ----------------------------------------------------------------- sums
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+    const uint32_t side = warp >> 2;                     // which half of the columns
+    const uint32_t chunks = p.bn / 32;                   // of 16 columns
+    const uint32_t lanes = (warp & 3) * 32;              // tensor-memory lanes of this warp
+    uint32_t it = 0;
+    bool ok = true;
+    for (uint32_t tile = tile0; tile < p.tiles && ok; tile += step) {
+      const uint32_t row0 = tile % p.tiles_m * 256 + half * 128 + lanes;
+      const uint32_t row = row0 + lane;
+      const uint32_t col = tile / p.tiles_m * p.bn + side * (p.bn / 2);
+      const bool any = row0 < p.m && col < p.n;          // the warp has outputs
+      const uint32_t blocks = (p.n + 127) / 128;
+      const uint32_t block0 = min(col / 128, blocks - 1), block1 = min(col / 128 + 1, blocks - 1);
+      const uint32_t turn = (128 - col % 128) / 16;      // chunks from here on are in block1
+      const float* sa = p.sa + static_cast<uint64_t>(min(row, p.m - 1)) * p.groups;
+      const float* sw0 = p.sw + static_cast<uint64_t>(block0) * p.groups;
+      const float* sw1 = p.sw + static_cast<uint64_t>(block1) * p.groups;
+      uint64_t acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      float fa = 0.0f, f0 = 0.0f, f1 = 0.0f;
+      if (any && kb0 < kb1) {
+        fa = __ldg(sa + kb0);
+        f0 = __ldg(sw0 + kb0);
+        f1 = __ldg(sw1 + kb0);
+      }
+      for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
+        const uint32_t b = it & 1;
+        const uint32_t s0 = __float_as_uint(fa * f0), s1 = __float_as_uint(fa * f1);
+        const uint64_t scale0 = cpt::pair_of(s0, s0), scale1 = cpt::pair_of(s1, s1);
+        if (any && kb + 1 < kb1) {
+          fa = __ldg(sa + kb + 1);
+          f0 = __ldg(sw0 + kb + 1);
+          f1 = __ldg(sw1 + kb + 1);
+        }
+        if (!__all_sync(0xFFFFFFFFu, cpt::mbar_wait(acc_full + 8 * b, (it >> 1) & 1, &gave_up))) {
+          ok = false;
+          break;
+        }
+        cpt::tc_fence_after();
+        if (any) {
+          const uint32_t at = tmem + (lanes << 16) + b * p.bn + side * (p.bn / 2);
+          uint32_t v[2][16];
+          cpt::tmem_load16(v[0], at);
+#pragma unroll
+          for (uint32_t c = 0; c < 8; ++c) {
+            if (c < chunks) {
+              cpt::tmem_load_wait(v[c & 1]);
+              if (c + 1 < chunks) cpt::tmem_load16(v[(c + 1) & 1], at + 16 * (c + 1));
+              const uint64_t f = c < turn ? scale0 : scale1;
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                cpt::fma2(acc[8 * c + i], cpt::pair_of(v[c & 1][2 * i], v[c & 1][2 * i + 1]), f);
+            }
+          }
+        }
+        cpt::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) cpt::mbar_arrive_cluster(pair_acc_empty + 8 * b);
+      }
+      if (!ok) break;
+      if (p.splits == 1) {
+        if (any && row < p.m) {
+#pragma unroll
+          for (uint32_t c = 0; c < 8; ++c) {
+            if (c < chunks && col + 16 * c < p.n) {
+              float v[16];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                v[2 * i] = __uint_as_float(static_cast<uint32_t>(acc[8 * c + i]));
+                v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(acc[8 * c + i] >> 32));
+              }
+              store16(p, row, col + 16 * c, v);
+            }
+          }
+        }
+      } else if (any) {
+        // this pair's sums, [row][bn + 4] floats over the stages (all loads are used up)
+        float* part = reinterpret_cast<float*>(tiles) + (lanes + lane) * (p.bn + 4) +
+                      side * (p.bn / 2);
+#pragma unroll
+        for (uint32_t c = 0; c < 8; ++c) {
+          if (c < chunks) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint64_t x = acc[8 * c + 2 * i], y = acc[8 * c + 2 * i + 1];
+              *reinterpret_cast<uint4*>(part + 16 * c + 4 * i) =
+                  make_uint4(static_cast<uint32_t>(x), static_cast<uint32_t>(x >> 32),
+                             static_cast<uint32_t>(y), static_cast<uint32_t>(y >> 32));
+            }
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) atomicOr(&g_matmul_gave_up, 1u);
+  }
+  __syncwarp();
+  cpt::tc_fence_before();
+  __syncthreads();
+  cpt::cluster_sync();
+  if (p.splits > 1 && gave_up == 0 && warp < kSumWarps) {
+    // the pairs' sums, added in order: each pair takes a share of the tile's columns
+    const uint32_t row0 = tile0 % p.tiles_m * 256 + half * 128, col0 = tile0 / p.tiles_m * p.bn;
+    const uint32_t rows = row0 < p.m ? min(128u, p.m - row0) : 0;
+    const uint32_t c0 = p.bn * split / p.splits, c1 = p.bn * (split + 1) / p.splits;
+    const uint32_t wide = c1 - c0, base = cpt::smem_addr(tiles);
+    for (uint32_t i = threadIdx.x; i < rows * wide; i += kSumWarps * 32) {
+      const uint32_t r = i / wide, c = c0 + i - r * wide;
+      if (col0 + c < p.n) {
+        const uint32_t off = base + (r * (p.bn + 4) + c) * 4;
+        float sum = 0.0f;
+        for (uint32_t q = 0; q < p.splits; ++q) {
+          float v;
+          asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                       : "=f"(v)
+                       : "r"(cpt::map_rank(off, 2 * q + half)));
+          sum = q == 0 ? v : sum + v;
+        }
+        store_from_f32(p.out, static_cast<uint64_t>(row0 + r) * p.ldo + col0 + c, p.out_dtype, sum);
+      }
+    }
+  }
+  __syncwarp();
+  cpt::cluster_sync();                 // no CTA leaves while another may read its shared memory
+  if (warp == kSumWarps + 1) cpt::tmem_free_pair(tmem, p.tmem_columns);
+}
+
+// What a launch needs to know of the device, found once.
+struct TcDevice {
+  std::atomic<int> state{0};           // 0: not asked, 1: usable, 2: not
+  int clusters[3] = {0, 0, 0};         // clusters of 2, 4, 8 CTAs that run at once
+};
+TcDevice g_devices[64];
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+std::atomic<EncodeTiled> g_encode{nullptr};
+
+void launch_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, uint32_t cluster,
+                   uint32_t ctas, size_t smem, cudaStream_t s) {
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  *cfg = cudaLaunchConfig_t{};
+  cfg->gridDim = dim3(ctas);
+  cfg->blockDim = dim3(kTcThreads);
+  cfg->dynamicSmemBytes = smem;
+  cfg->stream = s;
+  cfg->attrs = attr;
+  cfg->numAttrs = 1;
+}
+
+const TcDevice* tc_device(cudaError_t* err) {
+  int dev = 0;
+  *err = cudaGetDevice(&dev);
+  if (*err != cudaSuccess || dev >= 64) return nullptr;
+  TcDevice& d = g_devices[dev];
+  if (d.state.load(std::memory_order_acquire) == 1) return &d;
+  // several threads may get here at once: each finds the same values
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  *err = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                          &found);
+  if (*err != cudaSuccess) return nullptr;
+  if (fn == nullptr || found != cudaDriverEntryPointSuccess) {
+    *err = cudaErrorNotSupported;
+    return nullptr;
+  }
+  g_encode.store(reinterpret_cast<EncodeTiled>(fn));
+  *err = cudaFuncSetAttribute(reinterpret_cast<const void*>(&matmul_tc_kernel),
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(kSmemMost));
+  cudaFuncAttributes attrs{};
+  if (*err == cudaSuccess)
+    *err = cudaFuncGetAttributes(&attrs, reinterpret_cast<const void*>(&matmul_tc_kernel));
+  if (*err == cudaSuccess && attrs.numRegs != kLaunchRegs) *err = cudaErrorInvalidConfiguration;
+  for (int i = 0; i < 3 && *err == cudaSuccess; ++i) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[1];
+    launch_config(&cfg, attr, 2u << i, (2u << i) * 64, kSmemMost, nullptr);
+    int most = 0;
+    *err = cudaOccupancyMaxActiveClusters(&most, reinterpret_cast<const void*>(&matmul_tc_kernel),
+                                          &cfg);
+    d.clusters[i] = most;
+  }
+  if (*err != cudaSuccess) return nullptr;
+  if (d.clusters[0] < 1) {
+    *err = cudaErrorInvalidConfiguration;
+    return nullptr;
+  }
+  d.state.store(1, std::memory_order_release);
+  return &d;
+}
+
+bool encode_map(CUtensorMap* map, const uint8_t* base, uint64_t k, uint64_t rows, uint64_t ld,
+                uint32_t box_rows) {
+  const cuuint64_t dims[2] = {k, rows};
+  const cuuint64_t strides[1] = {rows == 1 ? (k + 15) / 16 * 16 : ld};
+  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t elem[2] = {1, 1};
+  return g_encode.load()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims,
+                         strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Columns of a tile and pairs that share one, by the time that the busiest pair needs in
+// clocks: a group takes the tensor cores 2 clocks a column and each SM the bytes that it
+// stages (48 a clock from L2); sharing a tile adds one exchange.
+void choose_tile(const TcDevice& d, uint32_t m, uint32_t n, uint32_t groups, uint32_t* bn,
+                 uint32_t* splits) {
+  const uint64_t tiles_m = (m + 255) / 256;
+  const uint64_t a_bytes = m >= 128 ? kTileA : (m + 7) / 8 * 8 * 128;
+  uint64_t best = ~0ull;
+  for (uint32_t i = 0; i < 3; ++i) {
+    const uint32_t s = 1u << i;
+    if (s > 1 && groups < 4 * s) break;
+    for (uint32_t b = 256; b >= 32; b -= 32) {
+      const uint64_t tiles = tiles_m * ((n + b - 1) / b);
+      const uint64_t at_once = static_cast<uint64_t>(d.clusters[i]);
+      if (at_once == 0 || (s > 1 && tiles > at_once)) continue;
+      const uint64_t turns = (tiles + at_once - 1) / at_once;
+      const uint64_t bytes = (a_bytes + b * 64) / 48;
+      const uint64_t per_group = 2ull * b > bytes ? 2ull * b : bytes;
+      const uint64_t cost = turns * ((groups + s - 1) / s * (per_group + 32) + 2 * b) +
+                            (s > 1 ? 3000 : 0);
+      if (cost < best) {
+        best = cost;
+        *bn = b;
+        *splits = s;
+      }
+    }
+  }
+}
+
+cp_status launch_tc(const MatmulParams& q, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  const TcDevice* d = tc_device(&e);
+  if (d == nullptr) return cpx::cuda_fail(e, "fp8 matmul device query");
+  uint32_t bn = 32, splits = 1;
+  choose_tile(*d, q.m, q.n, q.groups, &bn, &splits);
+  TcParams p{};
+  p.sa = q.sa;
+  p.sw = q.sw;
+  p.out = q.out;
+  p.ldo = q.ldo;
+  p.m = q.m;
+  p.n = q.n;
+  p.groups = q.groups;
+  p.out_dtype = q.out_dtype;
+  p.bn = bn;
+  p.splits = splits;
+  p.tiles_m = (q.m + 255) / 256;
+  p.a_rows = q.m >= 128 ? 128 : (q.m + 7) / 8 * 8;
+  const uint64_t tiles = static_cast<uint64_t>(p.tiles_m) * ((q.n + bn - 1) / bn);
+  if (tiles >= (1ull << 31)) {
+    cpx::set_error("m and n make more than 2^31 tiles");
+    return CP_ERR_INVALID_ARG;
+  }
+  p.tiles = static_cast<uint32_t>(tiles);
+  const uint32_t stage = kTileA + bn * 64;
+  p.stages = (kSmemMost - 1024) / stage;
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  p.tmem_columns = 64;
+  while (p.tmem_columns < 2 * bn) p.tmem_columns *= 2;
+  const uint64_t elt = dtype_size(q.out_dtype);
+  p.vec = cpx::aligned(q.out, 16) && q.ldo * elt % 16 == 0;
+  CUtensorMap map_a, map_w;
+  if (!encode_map(&map_a, q.a, q.k, q.m, q.lda, p.a_rows) ||
+      !encode_map(&map_w, q.w, q.k, q.n, q.ldw, bn / 2)) {
+    cpx::set_error("tensor map refused");
+    return CP_ERR_CUDA;
+  }
+  const uint32_t at_once = static_cast<uint32_t>(d->clusters[splits == 1 ? 0 : splits == 2 ? 1 : 2]);
+  const uint32_t clusters = splits > 1 || p.tiles < at_once ? p.tiles : at_once;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[1];
+  launch_config(&cfg, attr, 2 * splits, 2 * splits * clusters, kSmemMost, s);
+  e = cudaLaunchKernelEx(&cfg, matmul_tc_kernel, map_a, map_w, p);
+  if (e != cudaSuccess) return cpx::cuda_fail(e, "fp8 matmul launch");
+  return CP_OK;
+}
+
 }  // namespace
+
+extern "C" cp_status cp_matmul_fp8_status(void* stream) {
+  cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cpx::cuda_fail(e, "fp8 matmul");
+  uint32_t word = 0;
+  e = cudaMemcpyFromSymbol(&word, g_matmul_gave_up, sizeof(word));
+  if (e != cudaSuccess) return cpx::cuda_fail(e, "fp8 matmul status");
+  if (word == 0) return CP_OK;
+  const uint32_t zero = 0;
+  e = cudaMemcpyToSymbol(g_matmul_gave_up, &zero, sizeof(zero));
+  if (e != cudaSuccess) return cpx::cuda_fail(e, "fp8 matmul status");
+  cpx::set_error("a wait inside cp_matmul_fp8 ran out of time; its output is not valid");
+  return CP_ERR_CUDA;
+}
 
 extern "C" cp_status cp_matmul_fp8(const uint8_t* a, uint64_t a_stride, const float* a_scales,
                                    const uint8_t* w, uint64_t w_stride, const float* w_scales,
@@ -192,6 +672,11 @@ extern "C" cp_status cp_matmul_fp8(const uint8_t* a, uint64_t a_stride, const fl
                  static_cast<uint32_t>((k + 127) / 128),
                  out_dtype};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // Tensor maps want 16-byte boundaries (and a row stride of their own: not one row for all).
+  if (k != 0 && cpx::aligned(a, 16) && cpx::aligned(w, 16) &&
+      (m == 1 || (a_stride % 16 == 0 && a_stride != 0)) &&
+      (n == 1 || (w_stride % 16 == 0 && w_stride != 0)))
+    return launch_tc(p, s);
   const uint64_t tiles = ((m + kTile - 1) / kTile) * ((n + kTile - 1) / kTile);
   if (tiles >= kMost) {
     cpx::set_error("m and n make more than 2^31 tiles");

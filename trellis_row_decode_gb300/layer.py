@@ -23,7 +23,7 @@ from . import CP_ERR_INVALID_ARG, CPError, _check, lib
 
 __all__ = ["CP_F32", "CP_F16", "CP_BF16", "embed", "embed_grad", "embed_grad_workspace",
            "rms_norm", "rms_norm_fp8", "rms_norm_grad", "rms_norm_grad_workspace",
-           "quantize_fp8", "matmul_fp8"]
+           "quantize_fp8", "matmul_fp8", "matmul_fp8_status"]
 
 CP_F32, CP_F16, CP_BF16 = 0, 1, 2
 _CODE = {torch.float32: CP_F32, torch.float16: CP_F16, torch.bfloat16: CP_BF16}
@@ -51,6 +51,8 @@ def _lib():
                                        vp, vp, u64, vp]
         L.cp_quantize_fp8.argtypes = [vp, u64, i32, u64, u32, u32, vp, vp, vp]
         L.cp_matmul_fp8.argtypes = [vp, u64, vp, vp, u64, vp, u64, u64, u64, vp, i32, u64, vp]
+        L.cp_matmul_fp8_status.argtypes = [vp]
+        L.cp_matmul_fp8_status.restype = i32
         for f in (L.cp_embed, L.cp_embed_grad, L.cp_rms_norm, L.cp_rms_norm_fp8,
                   L.cp_rms_norm_grad, L.cp_quantize_fp8, L.cp_matmul_fp8):
             f.restype = i32
@@ -359,3 +361,10 @@ def matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scale
                                 w_scales.data_ptr(), m, n, k, out.data_ptr(), code, ldo,
                                 _stream(stream, a.device)), "cp_matmul_fp8")
     return out
+
+
+def matmul_fp8_status(stream=None) -> int:
+    """Synchronise the stream; CP_ERR_CUDA if a wait inside a matmul_fp8 since the last call
+    ran out of time (its output is then not valid), else CP_OK."""
+    stream = torch.cuda.current_stream() if stream is None else stream
+    return int(_lib().cp_matmul_fp8_status(stream.cuda_stream))
