@@ -7,6 +7,7 @@
 // scaled and added to the running fp32 sum before the next group begins.
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -177,9 +178,9 @@ __global__ void __launch_bounds__(kAnyThreads) matmul_any_kernel(MatmulParams p)
 
 constexpr int kSumWarps = 8;
 constexpr int kTcThreads = (kSumWarps + 4) * 32;       // + the TMA warp, the MMA warp and two idle
-// Registers: launched with 168 a thread (65,536 over 12 warps); the eight summing warps (128
-// sums and 32 values in flight a thread) take what the other four give up.
-constexpr int kLaunchRegs = 168, kSumRegs = 224, kOtherRegs = 56;
+// Registers: launched with 168 a thread (65,536 over 12 warps); the summing warps (128 sums and 64
+// values in flight a thread) take what the other four give up.
+constexpr int kLaunchRegs = 168, kSumRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSumRegs + kOtherRegs <= 3 * kLaunchRegs, "a warpgroup's share of the launch");
 constexpr uint32_t kMaxStages = 8;
 constexpr uint32_t kTileA = 128 * 128;                 // bytes of a's rows per stage and CTA
@@ -195,49 +196,73 @@ struct TcParams {
   uint64_t ldo;
   uint32_t m, n, groups;
   int out_dtype;
-  uint32_t bn, tiles_m, tiles, stages, splits, tmem_columns;
+  uint32_t tiles_m, tiles, stages, splits, tmem_columns;
   uint32_t a_rows;          // rows of a's TMA box
   bool vec;                 // out rows on 16-byte boundaries
 };
 
-// Sixteen consecutive outputs of a row.
-__device__ __forceinline__ void store16(const TcParams& p, uint32_t row, uint32_t col,
-                                        const float (&v)[16]) {
+// Eight consecutive outputs of a row.
+__device__ __forceinline__ void store8(const TcParams& p, uint32_t row, uint32_t col,
+                                       const float (&v)[8]) {
   const uint64_t at = static_cast<uint64_t>(row) * p.ldo + col;
-  if (p.vec && col + 16 <= p.n) {
+  if (p.vec && col + 8 <= p.n) {
     if (p.out_dtype == CP_F32) {
       float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      o[0] = make_float4(v[0], v[1], v[2], v[3]);
+      o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else if (p.out_dtype == CP_F16) {
+      store_octet(static_cast<__half*>(p.out) + at, pack<__half>(v));
     } else {
-      uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float u[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] = v[8 * i + e];
-        uint4 w;
-        if (p.out_dtype == CP_F16) {
-          const Packed<__half> r = pack<__half>(u);
-          w = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
-        } else {
-          const Packed<__nv_bfloat16> r = pack<__nv_bfloat16>(u);
-          w = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
-        }
-        o[i] = w;
-      }
+      store_octet(static_cast<__nv_bfloat16*>(p.out) + at, pack<__nv_bfloat16>(v));
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
+    for (int e = 0; e < 8; ++e)
       if (col + e < p.n) store_from_f32(p.out, at + e, p.out_dtype, v[e]);
   }
 }
 
+// f(std::integral_constant) for 0 .. kCount - 1.
+template <uint32_t kCount, typename F, uint32_t kFrom = 0>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (kFrom < kCount) {
+    f(std::integral_constant<uint32_t, kFrom>{});
+    static_for<kCount, F, kFrom + 1>(static_cast<F&&>(f));
+  }
+}
+
+// Up to 32 columns of a warp's share of 8 * kEights, from column 32 * kChunk on.
+template <uint32_t kEights, uint32_t kChunk>
+__device__ __forceinline__ void load_chunk(float (&x)[32], uint32_t at) {
+  constexpr uint32_t kLeft = kEights - 4 * kChunk;
+  if constexpr (kLeft >= 4) {
+    cpt::tmem_load32<0>(x, at + 32 * kChunk);
+  } else {
+    if constexpr ((kLeft & 2) != 0) cpt::tmem_load16<0>(x, at + 32 * kChunk);
+    if constexpr ((kLeft & 1) != 0)
+      cpt::tmem_load8<(kLeft & 2) * 8>(x, at + 32 * kChunk + (kLeft & 2) * 8);
+  }
+}
+
+// acc += x * scale over those columns; those from `turn` eights on have the second scale.
+template <uint32_t kEights, uint32_t kChunk>
+__device__ __forceinline__ void add_chunk(float (&acc)[kEights * 8], const float (&x)[32],
+                                          uint32_t turn, float scale0, float scale1) {
+  constexpr uint32_t kLeft = kEights - 4 * kChunk, kHere = kLeft < 4 ? kLeft : 4;
+#pragma unroll
+  for (uint32_t c = 0; c < kHere; ++c) {
+    const float f = 4 * kChunk + c < turn ? scale0 : scale1;
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i)
+      acc[32 * kChunk + 8 * c + i] = fmaf(x[8 * c + i], f, acc[32 * kChunk + 8 * c + i]);
+  }
+}
+
+template <uint32_t kEights>            // columns of a warp's share / 8 = kBn / 16
 __global__ void __launch_bounds__(kTcThreads, 1)
     matmul_tc_kernel(const __grid_constant__ CUtensorMap map_a,
                      const __grid_constant__ CUtensorMap map_w, const TcParams p) {
+  constexpr uint32_t kBn = kEights * 16, kShare = kEights * 8;
   extern __shared__ uint8_t dyn[];
   __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 4];
   __shared__ uint32_t tmem_base;
@@ -247,7 +272,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cpt::cluster_rank();
   const uint32_t half = rank & 1, split = rank >> 1, first = rank & ~1u;
-  const uint32_t stage_bytes = kTileA + p.bn * 64;
+  const uint32_t stage_bytes = kTileA + kBn * 64;
   const uint32_t full = cpt::smem_addr(bars), empty = full + 8 * kMaxStages;
   const uint32_t acc_full = empty + 8 * kMaxStages, acc_empty = acc_full + 16;
   // the first CTA's barriers hold the pair's loads and reads
@@ -279,158 +304,174 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp >= kSumWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kSumWarps && lane == 0) {
+    // Both warps run their loops whole and elect a thread to issue.
+    if (warp == kSumWarps) {
       // -------------------------------------------------------------- loads
-      cpt::tma_prefetch_map(&map_a);
-      cpt::tma_prefetch_map(&map_w);
-      const uint32_t w_bytes = p.bn * 64;
-      uint32_t it = 0;
+      if (cpt::elect_one()) {
+        cpt::tma_prefetch_map(&map_a);
+        cpt::tma_prefetch_map(&map_w);
+      }
+      __syncwarp();
+      const uint32_t w_bytes = kBn * 64;
+      uint32_t s = 0, round = 0;
       bool ok = true;
       for (uint32_t tile = tile0; tile < p.tiles && ok; tile += step) {
-        const uint32_t row0 = tile % p.tiles_m * 256, col0 = tile / p.tiles_m * p.bn;
-        const bool a0 = row0 < p.m, a1 = row0 + 128 < p.m;      // a's halves with any row
-        const bool mine = half ? a1 : a0;
-        const uint32_t bytes =
-            2 * w_bytes + ((a0 ? 1 : 0) + (a1 ? 1 : 0)) * p.a_rows * 128;
-        for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
-          const uint32_t s = it % p.stages, round = it / p.stages;
-          if (round > 0 && !cpt::mbar_wait(empty + 8 * s, (round - 1) & 1, &gave_up)) {
-            ok = false;
-            break;
+        const uint32_t tile_n = tile / p.tiles_m;
+        const uint32_t row0 = (tile - tile_n * p.tiles_m) * 256, col0 = tile_n * kBn;
+        const bool a1 = row0 + 128 < p.m;               // the second CTA has rows of a
+        const bool mine = half == 0 || a1;
+        const uint32_t bytes = 2 * w_bytes + (a1 ? 2 : 1) * p.a_rows * 128;
+        for (uint32_t kb = kb0; kb < kb1; ++kb) {
+          if (round > 0) {
+            ok = cpt::mbar_wait(empty + 8 * s, (round - 1) & 1, &gave_up);
+            if (!ok) break;
           }
-          const uint32_t dst = cpt::smem_addr(tiles + s * stage_bytes);
-          if (half == 0) cpt::mbar_expect(full + 8 * s, bytes);
-          if (mine)
-            cpt::tma_load_pair(dst, &map_a, kb * 128, row0 + half * 128, pair_full + 8 * s);
-          cpt::tma_load_pair(dst + kTileA, &map_w, kb * 128, col0 + half * (p.bn / 2),
-                             pair_full + 8 * s);
+          const uint32_t dst = cpt::smem_addr(tiles) + s * stage_bytes;
+          if (cpt::elect_one()) {
+            if (half == 0) cpt::mbar_expect(full + 8 * s, bytes);
+            if (mine)
+              cpt::tma_load_pair(dst, &map_a, kb * 128, row0 + half * 128, pair_full + 8 * s);
+            cpt::tma_load_pair(dst + kTileA, &map_w, kb * 128, col0 + half * (kBn / 2),
+                               pair_full + 8 * s);
+          }
+          __syncwarp();
+          if (++s == p.stages) {
+            s = 0;
+            ++round;
+          }
         }
       }
-      if (!ok) {      // the loads in flight land before the CTA leaves
+      // Given up: the loads in flight land before the CTA leaves (stages s.. of the round
+      // before, stages ..s of this one).
+      if (!ok && half == 0) {
         int unused = 0;
-        for (uint32_t k = it > p.stages ? it - p.stages : 0; half == 0 && k < it; ++k)
-          cpt::mbar_wait(full + 8 * (k % p.stages), (k / p.stages) & 1, &unused);
+        for (uint32_t k = 0; k < p.stages; ++k) {
+          const uint32_t r = k < s ? round : round - 1;
+          if (k < s || round > 0) cpt::mbar_wait(full + 8 * k, r & 1, &unused);
+        }
       }
-    }
-    if (warp == kSumWarps + 1 && half == 0 && lane == 0) {
+    } else if (warp == kSumWarps + 1 && half == 0) {
       // ----------------------------------------------------------- products
-      const uint32_t instr = cpt::e4m3_instr_desc(256, p.bn);
+      const uint32_t instr = cpt::e4m3_instr_desc(256, kBn);
       const uint16_t pair = static_cast<uint16_t>(3u << first);
-      uint32_t it = 0;
+      uint32_t it = 0, s = 0, round = 0;
       bool ok = true;
       for (uint32_t tile = tile0; tile < p.tiles && ok; tile += step) {
         for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
-          const uint32_t s = it % p.stages, round = it / p.stages, b = it & 1;
-          if ((it >= 2 && !cpt::mbar_wait(acc_empty + 8 * b, ((it >> 1) - 1) & 1, &gave_up)) ||
-              !cpt::mbar_wait(full + 8 * s, round & 1, &gave_up)) {
-            ok = false;
-            break;
-          }
+          const uint32_t b = it & 1;
+          ok = (it < 2 || cpt::mbar_wait(acc_empty + 8 * b, ((it >> 1) - 1) & 1, &gave_up)) &&
+               cpt::mbar_wait(full + 8 * s, round & 1, &gave_up);
+          if (!ok) break;
           cpt::tc_fence_after();
-          const uint32_t at = cpt::smem_addr(tiles + s * stage_bytes);
+          const uint32_t at = cpt::smem_addr(tiles) + s * stage_bytes;
           const uint64_t da = cpt::operand_desc(at), dw = cpt::operand_desc(at + kTileA);
+          if (cpt::elect_one()) {
 #pragma unroll
-          for (uint32_t k = 0; k < 4; ++k)
-            cpt::mma_pair(tmem + b * p.bn, da + 2 * k, dw + 2 * k, instr, k != 0);
-          cpt::mma_commit_pair(empty + 8 * s, pair);
-          cpt::mma_commit_pair(acc_full + 8 * b, pair);
+            for (uint32_t k = 0; k < 4; ++k)
+              cpt::mma_pair(tmem + b * kBn, da + 2 * k, dw + 2 * k, instr, k != 0);
+            cpt::mma_commit_pair(empty + 8 * s, pair);
+            cpt::mma_commit_pair(acc_full + 8 * b, pair);
+          }
+          __syncwarp();
+          if (++s == p.stages) {
+            s = 0;
+            ++round;
+          }
         }
       }
     }
   } else {
     // ----------------------------------------------------------------- sums
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
-    const uint32_t side = warp >> 2;                     // which half of the columns
-    const uint32_t chunks = p.bn / 32;                   // of 16 columns
     const uint32_t lanes = (warp & 3) * 32;              // tensor-memory lanes of this warp
+    const uint32_t share = (warp >> 2) * kShare;         // its first column of the tile
+    const uint32_t tmem_warp = tmem + (lanes << 16) + share;
     uint32_t it = 0;
     bool ok = true;
     for (uint32_t tile = tile0; tile < p.tiles && ok; tile += step) {
-      const uint32_t row0 = tile % p.tiles_m * 256 + half * 128 + lanes;
+      const uint32_t tile_n = tile / p.tiles_m;
+      const uint32_t row0 = (tile - tile_n * p.tiles_m) * 256 + half * 128 + lanes;
       const uint32_t row = row0 + lane;
-      const uint32_t col = tile / p.tiles_m * p.bn + side * (p.bn / 2);
+      const uint32_t col = tile_n * kBn + share;
       const bool any = row0 < p.m && col < p.n;          // the warp has outputs
-      const uint32_t blocks = (p.n + 127) / 128;
-      const uint32_t block0 = min(col / 128, blocks - 1), block1 = min(col / 128 + 1, blocks - 1);
-      const uint32_t turn = (128 - col % 128) / 16;      // chunks from here on are in block1
-      const float* sa = p.sa + static_cast<uint64_t>(min(row, p.m - 1)) * p.groups;
-      const float* sw0 = p.sw + static_cast<uint64_t>(block0) * p.groups;
-      const float* sw1 = p.sw + static_cast<uint64_t>(block1) * p.groups;
-      uint64_t acc[64];
+      const uint32_t turn = (128 - col % 128) / 8;       // eights from here on are in the next block
+      constexpr uint32_t kChunks = (kEights + 3) / 4;    // of 32 columns, the last may be shorter
+      float acc[kShare];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0;
-      float fa = 0.0f, f0 = 0.0f, f1 = 0.0f;
-      if (any && kb0 < kb1) {
-        fa = __ldg(sa + kb0);
-        f0 = __ldg(sw0 + kb0);
-        f1 = __ldg(sw1 + kb0);
-      }
-      for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
-        const uint32_t b = it & 1;
-        const uint32_t s0 = __float_as_uint(fa * f0), s1 = __float_as_uint(fa * f1);
-        const uint64_t scale0 = cpt::pair_of(s0, s0), scale1 = cpt::pair_of(s1, s1);
-        if (any && kb + 1 < kb1) {
-          fa = __ldg(sa + kb + 1);
-          f0 = __ldg(sw0 + kb + 1);
-          f1 = __ldg(sw1 + kb + 1);
+      for (uint32_t i = 0; i < kShare; ++i) acc[i] = 0.0f;
+      if (!any) {
+        for (uint32_t kb = kb0; kb < kb1 && ok; ++kb, ++it) {
+          ok = cpt::mbar_wait(acc_full + 8 * (it & 1), (it >> 1) & 1, &gave_up);
+          if (ok && lane == 0) cpt::mbar_arrive_cluster(pair_acc_empty + 8 * (it & 1));
         }
-        if (!__all_sync(0xFFFFFFFFu, cpt::mbar_wait(acc_full + 8 * b, (it >> 1) & 1, &gave_up))) {
-          ok = false;
-          break;
-        }
-        cpt::tc_fence_after();
-        if (any) {
-          const uint32_t at = tmem + (lanes << 16) + b * p.bn + side * (p.bn / 2);
-          uint32_t v[2][16];
-          cpt::tmem_load16(v[0], at);
+      } else {
+        // scales are loaded two groups ahead, each into the registers of its parity
+        const float* sa = p.sa + static_cast<uint64_t>(min(row, p.m - 1)) * p.groups;
+        const uint32_t last = (p.n + 127) / 128 - 1;
+        const float* sw0 = p.sw + static_cast<uint64_t>(col / 128) * p.groups;
+        const float* sw1 = p.sw + static_cast<uint64_t>(min(col / 128 + 1, last)) * p.groups;
+        float fa[2] = {}, f0[2] = {}, f1[2] = {};
+        auto load_scales = [&](uint32_t k, uint32_t kb) {
+          if (kb < kb1) {
+            fa[k] = __ldg(sa + kb);
+            f0[k] = __ldg(sw0 + kb);
+            f1[k] = __ldg(sw1 + kb);
+          }
+        };
+        load_scales(0, kb0);
+        load_scales(1, kb0 + 1);
+        float v[2][32];
+        for (uint32_t kb = kb0; kb < kb1 && ok; kb += 2) {
 #pragma unroll
-          for (uint32_t c = 0; c < 8; ++c) {
-            if (c < chunks) {
-              cpt::tmem_load_wait(v[c & 1]);
-              if (c + 1 < chunks) cpt::tmem_load16(v[(c + 1) & 1], at + 16 * (c + 1));
-              const uint64_t f = c < turn ? scale0 : scale1;
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                cpt::fma2(acc[8 * c + i], cpt::pair_of(v[c & 1][2 * i], v[c & 1][2 * i + 1]), f);
+          for (uint32_t k = 0; k < 2; ++k) {
+            if (kb + k < kb1 && ok) {
+              const uint32_t b = it & 1;
+              const uint32_t at = tmem_warp + b * kBn;
+              ok = cpt::mbar_wait(acc_full + 8 * b, (it >> 1) & 1, &gave_up);
+              if (ok) {
+                cpt::tc_fence_after();
+                load_chunk<kEights, 0>(v[0], at);
+                const float scale0 = fa[k] * f0[k], scale1 = fa[k] * f1[k];
+                load_scales(k, kb + k + 2);
+                static_for<kChunks>([&](auto chunk) {
+                  constexpr uint32_t c = decltype(chunk)::value;
+                  float(&x)[32] = v[c & 1];
+                  cpt::tmem_load_wait(x);
+                  if constexpr (c + 1 < kChunks) {
+                    load_chunk<kEights, c + 1>(v[(c + 1) & 1], at);
+                  } else {                // the buffer is read: the tensor core may have it back
+                    cpt::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) cpt::mbar_arrive_cluster(pair_acc_empty + 8 * b);
+                  }
+                  add_chunk<kEights, c>(acc, x, turn, scale0, scale1);
+                });
+                ++it;
+              }
             }
           }
         }
-        cpt::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) cpt::mbar_arrive_cluster(pair_acc_empty + 8 * b);
       }
       if (!ok) break;
       if (p.splits == 1) {
         if (any && row < p.m) {
 #pragma unroll
-          for (uint32_t c = 0; c < 8; ++c) {
-            if (c < chunks && col + 16 * c < p.n) {
-              float v[16];
+          for (uint32_t c = 0; c < kEights; ++c) {
+            if (col + 8 * c < p.n) {
+              float v[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                v[2 * i] = __uint_as_float(static_cast<uint32_t>(acc[8 * c + i]));
-                v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(acc[8 * c + i] >> 32));
-              }
-              store16(p, row, col + 16 * c, v);
+              for (int i = 0; i < 8; ++i) v[i] = acc[8 * c + i];
+              store8(p, row, col + 8 * c, v);
             }
           }
         }
       } else if (any) {
-        // this pair's sums, [row][bn + 4] floats over the stages (all loads are used up)
-        float* part = reinterpret_cast<float*>(tiles) + (lanes + lane) * (p.bn + 4) +
-                      side * (p.bn / 2);
+        // this pair's sums, [row][kBn + 4] floats over the stages (all loads are used up)
+        float* part = reinterpret_cast<float*>(tiles) + (lanes + lane) * (kBn + 4) + share;
 #pragma unroll
-        for (uint32_t c = 0; c < 8; ++c) {
-          if (c < chunks) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint64_t x = acc[8 * c + 2 * i], y = acc[8 * c + 2 * i + 1];
-              *reinterpret_cast<uint4*>(part + 16 * c + 4 * i) =
-                  make_uint4(static_cast<uint32_t>(x), static_cast<uint32_t>(x >> 32),
-                             static_cast<uint32_t>(y), static_cast<uint32_t>(y >> 32));
-            }
-          }
-        }
+        for (uint32_t i = 0; i < kEights * 2; ++i)
+          *reinterpret_cast<float4*>(part + 4 * i) =
+              make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
       }
     }
     if (!ok && lane == 0) atomicOr(&g_matmul_gave_up, 1u);
@@ -441,14 +482,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   cpt::cluster_sync();
   if (p.splits > 1 && gave_up == 0 && warp < kSumWarps) {
     // the pairs' sums, added in order: each pair takes a share of the tile's columns
-    const uint32_t row0 = tile0 % p.tiles_m * 256 + half * 128, col0 = tile0 / p.tiles_m * p.bn;
+    const uint32_t row0 = tile0 % p.tiles_m * 256 + half * 128, col0 = tile0 / p.tiles_m * kBn;
     const uint32_t rows = row0 < p.m ? min(128u, p.m - row0) : 0;
-    const uint32_t c0 = p.bn * split / p.splits, c1 = p.bn * (split + 1) / p.splits;
+    const uint32_t c0 = kBn * split / p.splits, c1 = kBn * (split + 1) / p.splits;
     const uint32_t wide = c1 - c0, base = cpt::smem_addr(tiles);
     for (uint32_t i = threadIdx.x; i < rows * wide; i += kSumWarps * 32) {
       const uint32_t r = i / wide, c = c0 + i - r * wide;
       if (col0 + c < p.n) {
-        const uint32_t off = base + (r * (p.bn + 4) + c) * 4;
+        const uint32_t off = base + (r * (kBn + 4) + c) * 4;
         float sum = 0.0f;
         for (uint32_t q = 0; q < p.splits; ++q) {
           float v;
@@ -467,6 +508,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // What a launch needs to know of the device, found once.
+using TcKernel = void (*)(CUtensorMap, CUtensorMap, TcParams);
+constexpr TcKernel kTcKernels[8] = {      // tiles of 32, 64, .. 256 columns
+    &matmul_tc_kernel<2>,  &matmul_tc_kernel<4>,  &matmul_tc_kernel<6>,  &matmul_tc_kernel<8>,
+    &matmul_tc_kernel<10>, &matmul_tc_kernel<12>, &matmul_tc_kernel<14>, &matmul_tc_kernel<16>};
+
 struct TcDevice {
   std::atomic<int> state{0};           // 0: not asked, 1: usable, 2: not
   int clusters[3] = {0, 0, 0};         // clusters of 2, 4, 8 CTAs that run at once
@@ -511,19 +557,21 @@ const TcDevice* tc_device(cudaError_t* err) {
     return nullptr;
   }
   g_encode.store(reinterpret_cast<EncodeTiled>(fn));
-  *err = cudaFuncSetAttribute(reinterpret_cast<const void*>(&matmul_tc_kernel),
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(kSmemMost));
-  cudaFuncAttributes attrs{};
-  if (*err == cudaSuccess)
-    *err = cudaFuncGetAttributes(&attrs, reinterpret_cast<const void*>(&matmul_tc_kernel));
-  if (*err == cudaSuccess && attrs.numRegs != kLaunchRegs) *err = cudaErrorInvalidConfiguration;
+  for (TcKernel kernel : kTcKernels) {
+    const void* k = reinterpret_cast<const void*>(kernel);
+    cudaFuncAttributes attrs{};
+    *err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(kSmemMost));
+    if (*err == cudaSuccess) *err = cudaFuncGetAttributes(&attrs, k);
+    if (*err == cudaSuccess && attrs.numRegs != kLaunchRegs) *err = cudaErrorInvalidConfiguration;
+    if (*err != cudaSuccess) return nullptr;
+  }
   for (int i = 0; i < 3 && *err == cudaSuccess; ++i) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
     launch_config(&cfg, attr, 2u << i, (2u << i) * 64, kSmemMost, nullptr);
     int most = 0;
-    *err = cudaOccupancyMaxActiveClusters(&most, reinterpret_cast<const void*>(&matmul_tc_kernel),
+    *err = cudaOccupancyMaxActiveClusters(&most, reinterpret_cast<const void*>(kTcKernels[7]),
                                           &cfg);
     d.clusters[i] = most;
   }
@@ -592,7 +640,6 @@ cp_status launch_tc(const MatmulParams& q, cudaStream_t s) {
   p.n = q.n;
   p.groups = q.groups;
   p.out_dtype = q.out_dtype;
-  p.bn = bn;
   p.splits = splits;
   p.tiles_m = (q.m + 255) / 256;
   p.a_rows = q.m >= 128 ? 128 : (q.m + 7) / 8 * 8;
@@ -620,7 +667,7 @@ cp_status launch_tc(const MatmulParams& q, cudaStream_t s) {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
   launch_config(&cfg, attr, 2 * splits, 2 * splits * clusters, kSmemMost, s);
-  e = cudaLaunchKernelEx(&cfg, matmul_tc_kernel, map_a, map_w, p);
+  e = cudaLaunchKernelEx(&cfg, kTcKernels[bn / 32 - 1], map_a, map_w, p);
   if (e != cudaSuccess) return cpx::cuda_fail(e, "fp8 matmul launch");
   return CP_OK;
 }

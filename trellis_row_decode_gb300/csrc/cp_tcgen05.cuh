@@ -26,6 +26,20 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
+// True for one lane of a converged warp.  A branch on it is known to be taken by one thread,
+// so what the tcgen05 and TMA instructions in it take stays in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "elect.sync _|p, 0xFFFFFFFF;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(ok));
+  return ok != 0;
+}
+
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -71,17 +85,18 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Waits for the phase; gives up after two seconds, or when another wait of the CTA has
-// (`gave_up`, shared memory), and says so by returning false.
+// The whole warp waits for the phase; it gives up after two seconds, or when another wait of
+// the CTA has (`gave_up`, shared memory), and says so by returning false, the same to
+// every lane.
 constexpr uint64_t kWaitNs = 2000000000ull;
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
   uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
-    if (mbar_try(bar, parity)) return true;
+    if (__all_sync(0xFFFFFFFFu, mbar_try(bar, parity))) return true;
     if ((i & 1023) == 0) {             // the timer is slow to read: a wait of ordinary length never does
       const uint64_t t = global_ns();
       if (t0 == 0) t0 = t;
-      if (*gave_up != 0 || t - t0 > kWaitNs) {
+      if (__any_sync(0xFFFFFFFFu, *gave_up != 0 || t - t0 > kWaitNs)) {
         *gave_up = 1;
         return false;
       }
@@ -122,23 +137,61 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// 16 consecutive columns of the warp's 32 lanes: lane t gets row t's values.
-__device__ __forceinline__ void tmem_load16(uint32_t (&v)[16], uint32_t addr) {
+// 8, 16 or 32 consecutive columns of the warp's 32 lanes into v[kAt..]: lane t gets row t's
+// values.
+template <int kAt, int kLen>
+__device__ __forceinline__ void tmem_load8(float (&v)[kLen], uint32_t addr) {
+  static_assert(kAt + 8 <= kLen, "inside the array");
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-        "=r"(v[14]), "=r"(v[15])
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7"
+      "}, [%8];"
+      : "=f"(v[kAt + 0]), "=f"(v[kAt + 1]), "=f"(v[kAt + 2]), "=f"(v[kAt + 3]),
+        "=f"(v[kAt + 4]), "=f"(v[kAt + 5]), "=f"(v[kAt + 6]), "=f"(v[kAt + 7])
+      : "r"(addr));
+}
+template <int kAt, int kLen>
+__device__ __forceinline__ void tmem_load16(float (&v)[kLen], uint32_t addr) {
+  static_assert(kAt + 16 <= kLen, "inside the array");
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
+      "}, [%16];"
+      : "=f"(v[kAt + 0]), "=f"(v[kAt + 1]), "=f"(v[kAt + 2]), "=f"(v[kAt + 3]),
+        "=f"(v[kAt + 4]), "=f"(v[kAt + 5]), "=f"(v[kAt + 6]), "=f"(v[kAt + 7]),
+        "=f"(v[kAt + 8]), "=f"(v[kAt + 9]), "=f"(v[kAt + 10]), "=f"(v[kAt + 11]),
+        "=f"(v[kAt + 12]), "=f"(v[kAt + 13]), "=f"(v[kAt + 14]), "=f"(v[kAt + 15])
+      : "r"(addr));
+}
+template <int kAt, int kLen>
+__device__ __forceinline__ void tmem_load32(float (&v)[kLen], uint32_t addr) {
+  static_assert(kAt + 32 <= kLen, "inside the array");
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31"
+      "}, [%32];"
+      : "=f"(v[kAt + 0]), "=f"(v[kAt + 1]), "=f"(v[kAt + 2]), "=f"(v[kAt + 3]),
+        "=f"(v[kAt + 4]), "=f"(v[kAt + 5]), "=f"(v[kAt + 6]), "=f"(v[kAt + 7]),
+        "=f"(v[kAt + 8]), "=f"(v[kAt + 9]), "=f"(v[kAt + 10]), "=f"(v[kAt + 11]),
+        "=f"(v[kAt + 12]), "=f"(v[kAt + 13]), "=f"(v[kAt + 14]), "=f"(v[kAt + 15]),
+        "=f"(v[kAt + 16]), "=f"(v[kAt + 17]), "=f"(v[kAt + 18]), "=f"(v[kAt + 19]),
+        "=f"(v[kAt + 20]), "=f"(v[kAt + 21]), "=f"(v[kAt + 22]), "=f"(v[kAt + 23]),
+        "=f"(v[kAt + 24]), "=f"(v[kAt + 25]), "=f"(v[kAt + 26]), "=f"(v[kAt + 27]),
+        "=f"(v[kAt + 28]), "=f"(v[kAt + 29]), "=f"(v[kAt + 30]), "=f"(v[kAt + 31])
       : "r"(addr));
 }
 // All loads issued so far have arrived.  The values pass through, so that no use of
 // them is moved in front of the wait.
-__device__ __forceinline__ void tmem_load_wait(uint32_t (&v)[16]) {
+__device__ __forceinline__ void tmem_load_wait(float (&v)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
-                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
-                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                 "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
+                 "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]),
+                 "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+                 "+f"(v[30]), "+f"(v[31])::"memory");
 }
 
 // ------------------------------------------------------------------ tcgen05.mma
@@ -176,16 +229,6 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t mask) {
       "[%0], %1;" ::"r"(bar),
       "h"(mask)
       : "memory");
-}
-
-// Two independent fp32 fused multiply-adds, each rounded once.
-__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
-}
-__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
 }
 
 }  // namespace cpt
