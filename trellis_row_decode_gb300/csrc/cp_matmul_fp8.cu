@@ -163,6 +163,196 @@ __global__ void __launch_bounds__(kAnyThreads) matmul_any_kernel(MatmulParams p)
       }
 }
 
+// ------------------------------------------------------------------- few rows of a
+//
+// Up to 64 rows of a: the product reads w once and little else, so it is bound by memory.
+// A warp has 16 rows of w (the tensor core's 16 x 32 operand) and every 8th group of 128 of
+// the CTA's share of k; its lanes load whole 16-byte pieces straight into fragments (the same
+// order of k on both operands, whatever it is, gives the same sums), several groups ahead.
+// The eight warps' sums are added in order through shared memory, and those of the
+// `splits` CTAs of a cluster, which share the rows when w has few, through theirs.
+
+constexpr uint32_t kFewRows = 16;
+constexpr uint64_t kFewBytes = 8 << 20;
+constexpr int kFewThreads = 256;
+constexpr uint32_t kFewWarps = kFewThreads / 32;
+
+struct FewGroup {
+  uint4 w[2][2];           // rows g and g + 8; bytes 16 t.. and 64 + 16 t..
+};
+
+template <int kTokens>
+struct FewRows {
+  uint4 b[kTokens][2];
+  float scale[kTokens][2];
+  float scale_w;
+};
+
+// Sixteen bytes of a row from column `col` on, zeros behind the row's k bytes.
+__device__ __forceinline__ uint4 load_piece(const uint8_t* row, uint32_t col, uint32_t k) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (col + 16 <= k) {
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(row + col));
+  } else if (col < k) {
+    uint32_t u[4] = {};
+    for (uint32_t b = 0; col + b < k; ++b)
+      u[b / 4] |= static_cast<uint32_t>(row[col + b]) << (8 * (b & 3));
+    v = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  return v;
+}
+__device__ __forceinline__ uint4 load_piece_cached(const uint8_t* row, uint32_t col, uint32_t k) {
+  if (col + 16 <= k) return __ldg(reinterpret_cast<const uint4*>(row + col));
+  return load_piece(row, col, k);
+}
+
+// kTokens: rows of a / 8.  kAhead: groups of w in flight per warp.
+template <int kTokens, int kAhead>
+__global__ void __launch_bounds__(kFewThreads, 2) matmul_few_kernel(MatmulParams p, uint32_t splits) {
+  __shared__ float part[kFewWarps][16][kTokens * 8];
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t g = lane >> 2, t = lane & 3;
+  const uint32_t rank = splits == 1 ? 0 : cpt::cluster_rank();
+  const uint32_t row0 = blockIdx.x / splits * 16;
+  const uint32_t first = rank * kFewWarps + warp, step = splits * kFewWarps;
+  const bool live[2] = {row0 + g < p.n, row0 + g + 8 < p.n};
+  const uint8_t* wrow[2] = {p.w + static_cast<uint64_t>(live[0] ? row0 + g : 0) * p.ldw,
+                            p.w + static_cast<uint64_t>(live[1] ? row0 + g + 8 : 0) * p.ldw};
+  const float* sw = p.sw + static_cast<uint64_t>(row0 / 128) * p.groups;
+  FewGroup ring[kAhead];
+  auto fetch = [&](FewGroup& f, uint32_t kb) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        f.w[r][h] = kb < p.groups && live[r] ? load_piece(wrow[r], kb * 128 + 64 * h + 16 * t, p.k)
+                                             : make_uint4(0, 0, 0, 0);
+  };
+  // The rows of a and the scales of a group, one group ahead of their use.
+  FewRows<kTokens> rows;
+  auto fetch_rows = [&](uint32_t kb) {
+    const bool in = kb < p.groups;
+    rows.scale_w = in ? __ldg(sw + kb) : 0.0f;
+#pragma unroll
+    for (int n = 0; n < kTokens; ++n) {
+      const uint32_t row = 8 * n + g, c0 = 8 * n + 2 * t;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        rows.b[n][h] = in && row < p.m
+                           ? load_piece_cached(p.a + static_cast<uint64_t>(row) * p.lda,
+                                               kb * 128 + 64 * h + 16 * t, p.k)
+                           : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        rows.scale[n][e] =
+            in && c0 + e < p.m ? __ldg(p.sa + static_cast<uint64_t>(c0 + e) * p.groups + kb) : 0.0f;
+    }
+  };
+  float acc[kTokens][4];
+#pragma unroll
+  for (int n = 0; n < kTokens; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch(ring[i], first + i * step);
+  fetch_rows(first);
+  for (uint32_t kb0 = first; kb0 < p.groups; kb0 += kAhead * step) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const uint32_t kb = kb0 + i * step;
+      if (kb < p.groups) {
+        const FewRows<kTokens> now = rows;
+        fetch_rows(kb + step);
+#pragma unroll
+        for (int n = 0; n < kTokens; ++n) {
+          float c[4] = {};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 &x = ring[i].w[0][h], &y = ring[i].w[1][h];
+            mma_e4m3(c, {x.x, y.x, x.y, y.y}, now.b[n][h].x, now.b[n][h].y);
+            mma_e4m3(c, {x.z, y.z, x.w, y.w}, now.b[n][h].z, now.b[n][h].w);
+          }
+          const float f0 = now.scale[n][0] * now.scale_w, f1 = now.scale[n][1] * now.scale_w;
+          acc[n][0] = fmaf(f0, c[0], acc[n][0]);
+          acc[n][1] = fmaf(f1, c[1], acc[n][1]);
+          acc[n][2] = fmaf(f0, c[2], acc[n][2]);
+          acc[n][3] = fmaf(f1, c[3], acc[n][3]);
+        }
+        fetch(ring[i], kb + kAhead * step);
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < kTokens; ++n) {
+    *reinterpret_cast<float2*>(&part[warp][g][8 * n + 2 * t]) = make_float2(acc[n][0], acc[n][1]);
+    *reinterpret_cast<float2*>(&part[warp][g + 8][8 * n + 2 * t]) =
+        make_float2(acc[n][2], acc[n][3]);
+  }
+  __syncthreads();
+  // output (token, row): consecutive threads take consecutive rows of w
+  for (uint32_t i = threadIdx.x; i < kTokens * 8 * 16; i += kFewThreads) {
+    const uint32_t r = i % 16, token = i / 16;
+    float s = part[0][r][token];
+#pragma unroll
+    for (uint32_t w = 1; w < kFewWarps; ++w) s += part[w][r][token];
+    if (splits == 1) {
+      if (token < p.m && row0 + r < p.n)
+        store_from_f32(p.out, token * p.ldo + row0 + r, p.out_dtype, s);
+    } else {
+      part[0][r][token] = s;         // read by this thread alone before
+    }
+  }
+  if (splits == 1) return;
+  cpt::cluster_sync();
+  if (rank == 0) {
+    for (uint32_t i = threadIdx.x; i < kTokens * 8 * 16; i += kFewThreads) {
+      const uint32_t r = i % 16, token = i / 16;
+      const uint32_t at = cpt::smem_addr(&part[0][r][token]);
+      float s = part[0][r][token];
+      for (uint32_t q = 1; q < splits; ++q) {
+        float v;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cpt::map_rank(at, q)));
+        s += v;
+      }
+      if (token < p.m && row0 + r < p.n)
+        store_from_f32(p.out, token * p.ldo + row0 + r, p.out_dtype, s);
+    }
+  }
+  cpt::cluster_sync();               // no CTA leaves while another may read its shared memory
+}
+
+template <int kTokens, int kAhead>
+cudaError_t launch_few(const MatmulParams& p, uint32_t splits, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((p.n + 15) / 16 * splits);
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = splits == 1 ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, &matmul_few_kernel<kTokens, kAhead>, p, splits);
+}
+
+cp_status launch_few(const MatmulParams& p, cudaStream_t s) {
+  // Share rows among CTAs until there are about two per SM, as long as each warp keeps two
+  // groups or more.
+  uint32_t splits = 1;
+  while (splits < 8 && static_cast<uint64_t>((p.n + 15) / 16) * splits < 256 &&
+         p.groups >= 2 * kFewWarps * 2 * splits)
+    splits *= 2;
+  cudaError_t e;
+  if (p.m <= 8) e = launch_few<1, 4>(p, splits, s);
+  else e = launch_few<2, 3>(p, splits, s);
+  if (e != cudaSuccess) return cpx::cuda_fail(e, "fp8 matmul launch");
+  return CP_OK;
+}
+
 // ------------------------------------------------- rows on 16-byte boundaries: tcgen05
 //
 // A pair of CTAs (two SMs) makes 256 x bn outputs, bn a multiple of 32 up to 256.  Each
@@ -198,27 +388,51 @@ struct TcParams {
   int out_dtype;
   uint32_t tiles_m, tiles, stages, splits, tmem_columns;
   uint32_t a_rows;          // rows of a's TMA box
-  bool vec;                 // out rows on 16-byte boundaries
+  bool vec;                 // out rows on 32-byte boundaries
 };
 
 // Eight consecutive outputs of a row.
 __device__ __forceinline__ void store8(const TcParams& p, uint32_t row, uint32_t col,
-                                       const float (&v)[8]) {
+                                       const float* v) {
   const uint64_t at = static_cast<uint64_t>(row) * p.ldo + col;
-  if (p.vec && col + 8 <= p.n) {
-    if (p.out_dtype == CP_F32) {
-      float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
-      o[0] = make_float4(v[0], v[1], v[2], v[3]);
-      o[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else if (p.out_dtype == CP_F16) {
-      store_octet(static_cast<__half*>(p.out) + at, pack<__half>(v));
-    } else {
-      store_octet(static_cast<__nv_bfloat16*>(p.out) + at, pack<__nv_bfloat16>(v));
-    }
+  if (p.out_dtype == CP_F32 && p.vec && col + 8 <= p.n) {
+    Packed<float> r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r.w[e] = __float_as_uint(v[e]);
+    store_octet(static_cast<float*>(p.out) + at, r);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (col + e < p.n) store_from_f32(p.out, at + e, p.out_dtype, v[e]);
+  }
+}
+
+// Sixteen, whole 32-byte sectors of L2 where the rows allow it: a lane's outputs are its own
+// row's, so only whole sectors keep the writes from being merged in L2.
+__device__ __forceinline__ void store16(const TcParams& p, uint32_t row, uint32_t col,
+                                        const float* v) {
+  if (p.out_dtype != CP_F32 && p.vec && col + 16 <= p.n) {
+    Packed<float> r;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float u[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] = v[8 * h + e];
+      if (p.out_dtype == CP_F16) {
+        const Packed<__half> x = pack<__half>(u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r.w[4 * h + e] = x.w[e];
+      } else {
+        const Packed<__nv_bfloat16> x = pack<__nv_bfloat16>(u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r.w[4 * h + e] = x.w[e];
+      }
+    }
+    store_octet(reinterpret_cast<float*>(static_cast<uint16_t*>(p.out) +
+                                         static_cast<uint64_t>(row) * p.ldo + col), r);
+  } else {
+    store8(p, row, col, v);
+    store8(p, row, col + 8, v + 8);
   }
 }
 
@@ -456,14 +670,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (p.splits == 1) {
         if (any && row < p.m) {
 #pragma unroll
-          for (uint32_t c = 0; c < kEights; ++c) {
-            if (col + 8 * c < p.n) {
-              float v[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = acc[8 * c + i];
-              store8(p, row, col + 8 * c, v);
-            }
-          }
+          for (uint32_t c = 0; c < kEights; c += 2)
+            if (col + 8 * c < p.n) store16(p, row, col + 8 * c, acc + 8 * c);
         }
       } else if (any) {
         // this pair's sums, [row][kBn + 4] floats over the stages (all loads are used up)
@@ -486,25 +694,271 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t rows = row0 < p.m ? min(128u, p.m - row0) : 0;
     const uint32_t c0 = kBn * split / p.splits, c1 = kBn * (split + 1) / p.splits;
     const uint32_t wide = c1 - c0, base = cpt::smem_addr(tiles);
-    for (uint32_t i = threadIdx.x; i < rows * wide; i += kSumWarps * 32) {
-      const uint32_t r = i / wide, c = c0 + i - r * wide;
+    for (uint32_t i = threadIdx.x; i < rows * wide / 4; i += kSumWarps * 32) {
+      const uint32_t r = i / (wide / 4), c = c0 + (i - r * (wide / 4)) * 4;
       if (col0 + c < p.n) {
         const uint32_t off = base + (r * (kBn + 4) + c) * 4;
-        float sum = 0.0f;
-        for (uint32_t q = 0; q < p.splits; ++q) {
-          float v;
-          asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                       : "=f"(v)
-                       : "r"(cpt::map_rank(off, 2 * q + half)));
-          sum = q == 0 ? v : sum + v;
+        float4 v[4];
+#pragma unroll
+        for (uint32_t q = 0; q < 4; ++q)
+          if (q < p.splits) v[q] = cpt::load_cluster4(cpt::map_rank(off, 2 * q + half));
+        float4 sum = v[0];
+#pragma unroll
+        for (uint32_t q = 1; q < 4; ++q) {
+          if (q < p.splits) {
+            sum.x += v[q].x;
+            sum.y += v[q].y;
+            sum.z += v[q].z;
+            sum.w += v[q].w;
+          }
         }
-        store_from_f32(p.out, static_cast<uint64_t>(row0 + r) * p.ldo + col0 + c, p.out_dtype, sum);
+        const uint64_t at = static_cast<uint64_t>(row0 + r) * p.ldo + col0 + c;
+        const float out[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e)
+          if (col0 + c + e < p.n) store_from_f32(p.out, at + e, p.out_dtype, out[e]);
       }
     }
   }
   __syncwarp();
   cpt::cluster_sync();                 // no CTA leaves while another may read its shared memory
   if (warp == kSumWarps + 1) cpt::tmem_free_pair(tmem, p.tmem_columns);
+}
+
+// ----------------------------------------------- few rows of a, many bytes of w: tcgen05
+//
+// With at most 64 rows of a the operands change places: 128 rows of w are the tensor core's
+// 128 x 32 operand, the rows of a its N (16, 32 or 64) columns, and the kernel is bound by
+// the stream of w.  A unit is 128 columns of tensor memory, 128 / kN groups side by side, so
+// the sums (a lane has a row of w) wait once a unit; two units alternate.  Two CTAs share an
+// SM; `splits` CTAs of a cluster share a tile's groups and add their sums in order through
+// distributed shared memory.
+
+constexpr int kThinThreads = 256;      // four summing warps, TMA, MMA, scales, one idle
+constexpr uint32_t kThinUnit = 128;    // columns of tensor memory
+constexpr uint32_t kThinMaxStages = 6;
+constexpr uint32_t kThinSmem = 111616;  // dynamic shared memory of a CTA, two to an SM
+
+struct ThinParams {
+  const float* sa;
+  const float* sw;
+  void* out;
+  uint64_t ldo;
+  uint32_t m, n, groups, splits, stages;
+  int out_dtype;
+};
+
+template <uint32_t kN>
+__global__ void __launch_bounds__(kThinThreads, 2)
+    matmul_thin_kernel(const __grid_constant__ CUtensorMap map_a,
+                       const __grid_constant__ CUtensorMap map_w, const ThinParams p) {
+  constexpr uint32_t kPer = kThinUnit / kN;            // groups of a unit
+  constexpr uint32_t kStage = kTileA + kN * 128;
+  extern __shared__ uint8_t dyn[];
+  __shared__ __align__(8) uint64_t bars[2 * kThinMaxStages + 6];
+  __shared__ __align__(16) float scales[2][kThinUnit];
+  __shared__ uint32_t tmem_base;
+  __shared__ int gave_up;
+  uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = p.splits == 1 ? 0 : cpt::cluster_rank();
+  const uint32_t row0 = blockIdx.x / p.splits * 128;
+  const uint32_t full = cpt::smem_addr(bars), empty = full + 8 * kThinMaxStages;
+  const uint32_t acc_full = empty + 8 * kThinMaxStages, acc_empty = acc_full + 16;
+  const uint32_t scale_full = acc_empty + 16;
+  if (threadIdx.x == 0) {
+    for (uint32_t s = 0; s < p.stages; ++s) {
+      cpt::mbar_init(full + 8 * s, 1);
+      cpt::mbar_init(empty + 8 * s, 1);
+    }
+    for (uint32_t b = 0; b < 2; ++b) {
+      cpt::mbar_init(acc_full + 8 * b, 1);
+      cpt::mbar_init(acc_empty + 8 * b, 4);
+      cpt::mbar_init(scale_full + 8 * b, 32);
+    }
+    cpt::mbar_init_fence();
+    gave_up = 0;
+  }
+  if (warp == 5) cpt::tmem_alloc(cpt::smem_addr(&tmem_base), 2 * kThinUnit);
+  cpt::tc_fence_before();
+  __syncthreads();
+  cpt::tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  // whole units go to each CTA of the cluster
+  const uint32_t units = (p.groups + kPer - 1) / kPer;
+  const uint32_t u0 = units * rank / p.splits, u1 = units * (rank + 1) / p.splits;
+  const uint32_t kb0 = u0 * kPer, kb1 = min(u1 * kPer, p.groups);
+  float acc[kN];
+#pragma unroll
+  for (uint32_t i = 0; i < kN; ++i) acc[i] = 0.0f;
+  bool ok = true;
+
+  if (warp == 4) {
+    // ------------------------------------------------------------------ loads
+    if (cpt::elect_one()) {
+      cpt::tma_prefetch_map(&map_a);
+      cpt::tma_prefetch_map(&map_w);
+    }
+    __syncwarp();
+    uint32_t s = 0, round = 0;
+    for (uint32_t kb = kb0; kb < kb1; ++kb) {
+      if (round > 0) {
+        ok = cpt::mbar_wait(empty + 8 * s, (round - 1) & 1, &gave_up);
+        if (!ok) break;
+      }
+      const uint32_t dst = cpt::smem_addr(tiles) + s * kStage;
+      if (cpt::elect_one()) {
+        cpt::mbar_expect(full + 8 * s, kStage);
+        cpt::tma_load(dst, &map_w, kb * 128, row0, full + 8 * s);
+        cpt::tma_load(dst + kTileA, &map_a, kb * 128, 0, full + 8 * s);
+      }
+      __syncwarp();
+      if (++s == p.stages) {
+        s = 0;
+        ++round;
+      }
+    }
+    if (!ok) {          // given up: the loads in flight land before the CTA leaves
+      int unused = 0;
+      for (uint32_t k = 0; k < p.stages; ++k) {
+        const uint32_t r = k < s ? round : round - 1;
+        if (k < s || round > 0) cpt::mbar_wait(full + 8 * k, r & 1, &unused);
+      }
+    }
+  } else if (warp == 5) {
+    // --------------------------------------------------------------- products
+    constexpr uint32_t instr = cpt::e4m3_instr_desc(128, kN);
+    uint32_t s = 0, round = 0, kb = kb0;
+    for (uint32_t u = 0; kb < kb1; ++u) {
+      const uint32_t b = u & 1;
+      ok = u < 2 || cpt::mbar_wait(acc_empty + 8 * b, ((u >> 1) - 1) & 1, &gave_up);
+      for (uint32_t g = 0; g < kPer && kb < kb1 && ok; ++g, ++kb) {
+        ok = cpt::mbar_wait(full + 8 * s, round & 1, &gave_up);
+        if (!ok) break;
+        cpt::tc_fence_after();
+        const uint32_t at = cpt::smem_addr(tiles) + s * kStage;
+        const uint64_t dw = cpt::operand_desc(at), da = cpt::operand_desc(at + kTileA);
+        if (cpt::elect_one()) {
+#pragma unroll
+          for (uint32_t k = 0; k < 4; ++k)
+            cpt::mma_one(tmem + b * kThinUnit + g * kN, dw + 2 * k, da + 2 * k, instr, k != 0);
+          cpt::mma_commit(empty + 8 * s);
+          if (g + 1 == kPer || kb + 1 == kb1) cpt::mma_commit(acc_full + 8 * b);
+        }
+        __syncwarp();
+        if (++s == p.stages) {
+          s = 0;
+          ++round;
+        }
+      }
+      if (!ok) break;
+    }
+  } else if (warp == 6) {
+    // ----------------------------------------------------------------- scales
+    const float* sw = p.sw + static_cast<uint64_t>(row0 / 128) * p.groups;
+    uint32_t u = 0;
+    for (uint32_t kb = kb0; kb < kb1; kb += kPer, ++u) {
+      const uint32_t b = u & 1;
+      float f[4];
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) {
+        const uint32_t e = lane + 32 * i, group = kb + e / kN, token = e % kN;
+        f[i] = group < kb1 && token < p.m
+                   ? __ldg(p.sa + static_cast<uint64_t>(token) * p.groups + group) *
+                         __ldg(sw + group)
+                   : 0.0f;
+      }
+      if (u >= 2) {
+        ok = cpt::mbar_wait(acc_empty + 8 * b, ((u >> 1) - 1) & 1, &gave_up);
+        if (!ok) break;
+      }
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) scales[b][lane + 32 * i] = f[i];
+      cpt::mbar_arrive(scale_full + 8 * b);
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------------- sums
+    const uint32_t tmem_warp = tmem + ((warp * 32) << 16);
+    uint32_t u = 0;
+    for (uint32_t kb = kb0; kb < kb1; kb += kPer, ++u) {
+      const uint32_t b = u & 1;
+      ok = cpt::mbar_wait(scale_full + 8 * b, (u >> 1) & 1, &gave_up) &&
+           cpt::mbar_wait(acc_full + 8 * b, (u >> 1) & 1, &gave_up);
+      if (!ok) break;
+      cpt::tc_fence_after();
+      const uint32_t columns = min(kPer, kb1 - kb) * kN;     // of the unit that are filled
+#pragma unroll
+      for (uint32_t c = 0; c < 4; ++c) {
+        if (32 * c < columns) {          // (a last unit of 16-column groups may fill half of it)
+          float x[32];
+          cpt::tmem_load32<0>(x, tmem_warp + b * kThinUnit + 32 * c);
+          float f[32];
+#pragma unroll
+          for (uint32_t i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(&f[4 * i]) =
+                *reinterpret_cast<const float4*>(&scales[b][32 * c + 4 * i]);
+          cpt::tmem_load_wait(x);
+          const uint32_t here = min(32u, columns - 32 * c);
+#pragma unroll
+          for (uint32_t i = 0; i < 32; ++i)
+            if (kN >= 32 || i < 16 || here == 32)
+              acc[(32 * c + i) % kN] = fmaf(x[i], f[i], acc[(32 * c + i) % kN]);
+        }
+      }
+      cpt::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) cpt::mbar_arrive(acc_empty + 8 * b);
+    }
+  }
+  if (!ok && lane == 0) atomicOr(&g_matmul_gave_up, 1u);
+  __syncwarp();
+  cpt::tc_fence_before();
+  __syncthreads();
+  const uint32_t row = row0 + threadIdx.x;       // (of the summing warps)
+  if (p.splits == 1) {
+    if (warp < 4 && row < p.n) {
+#pragma unroll
+      for (uint32_t i = 0; i < kN; ++i)
+        if (i < p.m) store_from_f32(p.out, i * p.ldo + row, p.out_dtype, acc[i]);
+    }
+  } else {
+    // sums as [token][row] over the stages (all loads are used up); each CTA of the cluster
+    // then adds a share of the tokens
+    float* part = reinterpret_cast<float*>(tiles);
+    if (warp < 4) {
+#pragma unroll
+      for (uint32_t i = 0; i < kN; ++i) part[i * 128 + threadIdx.x] = acc[i];
+    }
+    __syncthreads();
+    cpt::cluster_sync();
+    const uint32_t i0 = p.m * 32 * rank / p.splits, i1 = p.m * 32 * (rank + 1) / p.splits;
+    for (uint32_t i = i0 + threadIdx.x; i < i1; i += kThinThreads) {
+      const uint32_t at = cpt::smem_addr(part + 4 * i);
+      float4 v[8];
+#pragma unroll
+      for (uint32_t q = 0; q < 8; ++q)
+        if (q < p.splits) v[q] = cpt::load_cluster4(cpt::map_rank(at, q));
+      float4 sum = v[0];
+#pragma unroll
+      for (uint32_t q = 1; q < 8; ++q) {
+        if (q < p.splits) {
+          sum.x += v[q].x;
+          sum.y += v[q].y;
+          sum.z += v[q].z;
+          sum.w += v[q].w;
+        }
+      }
+      const uint32_t token = i / 32, r = row0 + i % 32 * 4;
+      const float out[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+      for (uint32_t e = 0; e < 4; ++e)
+        if (r + e < p.n) store_from_f32(p.out, token * p.ldo + r + e, p.out_dtype, out[e]);
+    }
+    __syncwarp();
+    cpt::cluster_sync();             // no CTA leaves while another may read its shared memory
+  }
+  if (warp == 5) cpt::tmem_free(tmem, 2 * kThinUnit);
 }
 
 // What a launch needs to know of the device, found once.
@@ -566,6 +1020,13 @@ const TcDevice* tc_device(cudaError_t* err) {
     if (*err == cudaSuccess && attrs.numRegs != kLaunchRegs) *err = cudaErrorInvalidConfiguration;
     if (*err != cudaSuccess) return nullptr;
   }
+  for (const void* k : {reinterpret_cast<const void*>(&matmul_thin_kernel<16>),
+                        reinterpret_cast<const void*>(&matmul_thin_kernel<32>),
+                        reinterpret_cast<const void*>(&matmul_thin_kernel<64>)}) {
+    *err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(kThinSmem));
+    if (*err != cudaSuccess) return nullptr;
+  }
   for (int i = 0; i < 3 && *err == cudaSuccess; ++i) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
@@ -596,26 +1057,23 @@ bool encode_map(CUtensorMap* map, const uint8_t* base, uint64_t k, uint64_t rows
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Columns of a tile and pairs that share one, by the time that the busiest pair needs in
-// clocks: a group takes the tensor cores 2 clocks a column and each SM the bytes that it
-// stages (48 a clock from L2); sharing a tile adds one exchange.
+// Columns of a tile and pairs that share one, by the time that the busiest pair needs.  In
+// nanoseconds, measured on tiles of one turn (k = 4096 and 24576, 64 to 256 columns): a group
+// takes 250 + 0.85 a column, a tile's outputs 14 a column, and sharing a tile 4000.
 void choose_tile(const TcDevice& d, uint32_t m, uint32_t n, uint32_t groups, uint32_t* bn,
                  uint32_t* splits) {
-  const uint64_t tiles_m = (m + 255) / 256;
-  const uint64_t a_bytes = m >= 128 ? kTileA : (m + 7) / 8 * 8 * 128;
-  uint64_t best = ~0ull;
+  const uint64_t tiles_m = (static_cast<uint64_t>(m) + 255) / 256;
+  double best = 1e300;
   for (uint32_t i = 0; i < 3; ++i) {
     const uint32_t s = 1u << i;
     if (s > 1 && groups < 4 * s) break;
     for (uint32_t b = 256; b >= 32; b -= 32) {
-      const uint64_t tiles = tiles_m * ((n + b - 1) / b);
+      const uint64_t tiles = tiles_m * ((static_cast<uint64_t>(n) + b - 1) / b);
       const uint64_t at_once = static_cast<uint64_t>(d.clusters[i]);
       if (at_once == 0 || (s > 1 && tiles > at_once)) continue;
-      const uint64_t turns = (tiles + at_once - 1) / at_once;
-      const uint64_t bytes = (a_bytes + b * 64) / 48;
-      const uint64_t per_group = 2ull * b > bytes ? 2ull * b : bytes;
-      const uint64_t cost = turns * ((groups + s - 1) / s * (per_group + 32) + 2 * b) +
-                            (s > 1 ? 3000 : 0);
+      const double turns = static_cast<double>((tiles + at_once - 1) / at_once);
+      const double cost =
+          turns * ((groups + s - 1) / s * (250.0 + 0.85 * b) + 14.0 * b) + (s > 1 ? 4000.0 : 0.0);
       if (cost < best) {
         best = cost;
         *bn = b;
@@ -655,7 +1113,7 @@ cp_status launch_tc(const MatmulParams& q, cudaStream_t s) {
   p.tmem_columns = 64;
   while (p.tmem_columns < 2 * bn) p.tmem_columns *= 2;
   const uint64_t elt = dtype_size(q.out_dtype);
-  p.vec = cpx::aligned(q.out, 16) && q.ldo * elt % 16 == 0;
+  p.vec = cpx::aligned(q.out, 32) && q.ldo * elt % 32 == 0;
   CUtensorMap map_a, map_w;
   if (!encode_map(&map_a, q.a, q.k, q.m, q.lda, p.a_rows) ||
       !encode_map(&map_w, q.w, q.k, q.n, q.ldw, bn / 2)) {
@@ -668,6 +1126,37 @@ cp_status launch_tc(const MatmulParams& q, cudaStream_t s) {
   cudaLaunchAttribute attr[1];
   launch_config(&cfg, attr, 2 * splits, 2 * splits * clusters, kSmemMost, s);
   e = cudaLaunchKernelEx(&cfg, kTcKernels[bn / 32 - 1], map_a, map_w, p);
+  if (e != cudaSuccess) return cpx::cuda_fail(e, "fp8 matmul launch");
+  return CP_OK;
+}
+
+cp_status launch_thin(const MatmulParams& q, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if (tc_device(&e) == nullptr) return cpx::cuda_fail(e, "fp8 matmul device query");
+  const uint32_t kn = q.m <= 16 ? 16 : q.m <= 32 ? 32 : 64;
+  const uint32_t units = (q.groups + kThinUnit / kn - 1) / (kThinUnit / kn);
+  const uint32_t tiles = (q.n + 127) / 128;
+  // CTAs share a tile until there are enough to keep every SM's loads in flight.
+  uint32_t splits = 1;
+  while (splits < 8 && static_cast<uint64_t>(tiles) * splits * 2 <= 304 && units >= 2 * splits)
+    splits *= 2;
+  ThinParams p{q.sa, q.sw, q.out, q.ldo, q.m, q.n, q.groups, splits, 0, q.out_dtype};
+  const uint32_t stage = kTileA + kn * 128;
+  p.stages = (kThinSmem - 1024) / stage;
+  if (p.stages > kThinMaxStages) p.stages = kThinMaxStages;
+  CUtensorMap map_a, map_w;
+  if (!encode_map(&map_a, q.a, q.k, q.m, q.lda, kn) ||
+      !encode_map(&map_w, q.w, q.k, q.n, q.ldw, 128)) {
+    cpx::set_error("tensor map refused");
+    return CP_ERR_CUDA;
+  }
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[1];
+  launch_config(&cfg, attr, splits, splits * tiles, kThinSmem, s);
+  cfg.blockDim = dim3(kThinThreads);
+  auto* fn = kn == 16 ? &matmul_thin_kernel<16> : kn == 32 ? &matmul_thin_kernel<32>
+                                                            : &matmul_thin_kernel<64>;
+  e = cudaLaunchKernelEx(&cfg, fn, map_a, map_w, p);
   if (e != cudaSuccess) return cpx::cuda_fail(e, "fp8 matmul launch");
   return CP_OK;
 }
@@ -723,7 +1212,8 @@ extern "C" cp_status cp_matmul_fp8(const uint8_t* a, uint64_t a_stride, const fl
   if (k != 0 && cpx::aligned(a, 16) && cpx::aligned(w, 16) &&
       (m == 1 || (a_stride % 16 == 0 && a_stride != 0)) &&
       (n == 1 || (w_stride % 16 == 0 && w_stride != 0)))
-    return launch_tc(p, s);
+    return m > 64 ? launch_tc(p, s)
+           : m <= kFewRows && n * k <= kFewBytes ? launch_few(p, s) : launch_thin(p, s);
   const uint64_t tiles = ((m + kTile - 1) / kTile) * ((n + kTile - 1) / kTile);
   if (tiles >= kMost) {
     cpx::set_error("m and n make more than 2^31 tiles");

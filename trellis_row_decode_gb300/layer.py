@@ -60,94 +60,112 @@ def _lib():
     return _declared
 
 
-def _stream(stream, device) -> int:
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _device(t: torch.Tensor, name: str) -> int:
+    """The index of t's device, which has to be the current one."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    return dev
+
+
+def _on(t: torch.Tensor, dev: int, name: str) -> int:
+    """t's address; t has to lie on device `dev`."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the same CUDA device as the others")
+    return t.data_ptr()
+
+
+def _stream(stream, dev: int) -> int:
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    if stream.device != device:
+        return _raw_stream(dev)
+    if stream.device_index != dev:
         raise ValueError("stream and tensors must be on the same device")
     return stream.cuda_stream
 
 
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
+def _empty(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     """An allocation that belongs to the stream the kernels run on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _float(t: torch.Tensor, name: str) -> int:
-    code = _CODE.get(t.dtype)
+def _float(dtype: torch.dtype, name: str) -> int:
+    code = _CODE.get(dtype)
     if code is None:
         raise ValueError(f"{name} must be float32, float16 or bfloat16")
     return code
 
 
-def _here(t: torch.Tensor, name: str) -> torch.Tensor:
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current CUDA device")
-    return t
-
-
-def _rows(t: torch.Tensor, name: str) -> tuple[torch.Tensor, int]:
-    """t as [rows, d] and its row stride (leading dimensions are flattened, as a view)."""
-    _here(t, name)
-    if t.dim() != 2:
-        if t.dim() == 0:
+def _rows(t: torch.Tensor, name: str) -> tuple[int, int, int]:
+    """(rows, d, row stride) of t with its leading dimensions merged (as a view)."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2:
+        if len(shape) == 0:
             raise ValueError(f"{name} must have at least one dimension")
+        if len(shape) == 1:
+            if shape[0] > 1 and strides[0] != 1:
+                raise ValueError(f"{name} must have unit stride in its last dimension")
+            return 1, shape[0], shape[0]
         try:
-            t = t.view(-1, t.shape[-1]) if t.shape[-1] else t.view(0, 0)
+            t = t.view(-1, shape[-1]) if shape[-1] else t.view(0, 0)
         except RuntimeError:
             raise ValueError(f"{name}: leading dimensions must be mergeable without a copy"
                              ) from None
-    d = t.shape[1]
-    if d > 1 and t.stride(1) != 1:
+        shape, strides = t.shape, t.stride()
+    rows, d = shape
+    if d > 1 and strides[1] != 1:
         raise ValueError(f"{name} must have unit stride in its last dimension")
-    return t, (t.stride(0) if t.shape[0] > 1 else d)
+    return rows, d, (strides[0] if rows > 1 else d)
 
 
 def _ids(ids: torch.Tensor) -> int:
     if ids.dtype != torch.int64 or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous int64 CUDA tensor")
-    _here(ids, "ids")
     return ids.numel()
 
 
-def _status_ptr(status):
+def _status_ptr(status, dev: int):
     if status is None:
         return None
     if status.dtype != torch.int32 or status.numel() < 1:
         raise ValueError("status must be an int32 CUDA tensor")
-    return _here(status, "status").data_ptr()
+    return _on(status, dev, "status")
 
 
-def _out(out, shape, dtype, device, stream, name) -> tuple[torch.Tensor, int]:
-    """The caller's output, checked, or a new one; and its row stride."""
-    shape = tuple(shape)
-    if out is None:
-        return _empty(shape, dtype, device, stream), shape[-1]
-    if out.dtype != dtype or tuple(out.shape) != shape:
-        raise ValueError(f"{name} must be {dtype} of shape {shape}")
-    t, stride = _rows(out, name)
-    if t.shape[0] > 1 and stride < t.shape[1]:
+def _check_out(out: torch.Tensor, shape, dtype, dev: int, name: str) -> int:
+    """The row stride of the caller's output, whose rows may lie apart."""
+    if out.dtype != dtype or tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}")
+    rows, d, stride = _rows(out, name)
+    if rows > 1 and stride < d:
         raise ValueError(f"{name}'s rows must not overlap")
-    return out, stride
+    _on(out, dev, name)
+    return stride
 
 
-def _whole(out, shape, dtype, device, stream, name) -> torch.Tensor:
-    """The same for outputs that have to be contiguous."""
-    if out is not None and not out.is_contiguous():
+def _whole(out, shape, dtype, like: torch.Tensor, dev: int, stream, name: str) -> torch.Tensor:
+    """The caller's output, which has to be contiguous, or a new one."""
+    if out is None:
+        return _empty(shape, dtype, like, stream)
+    if not out.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return _out(out, shape, dtype, device, stream, name)[0]
+    _check_out(out, shape, dtype, dev, name)
+    return out
 
 
-def _workspace(workspace, nbytes: int, device, stream) -> torch.Tensor:
+def _workspace(workspace, nbytes: int, like: torch.Tensor, dev: int, stream) -> torch.Tensor:
     if workspace is None:
-        return _empty(nbytes, torch.uint8, device, stream)
+        return _empty(nbytes, torch.uint8, like, stream)
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous() \
             or workspace.numel() < nbytes:
         raise ValueError(f"workspace must be a contiguous uint8 CUDA tensor of {nbytes} bytes")
-    return _here(workspace, "workspace")
+    _on(workspace, dev, "workspace")
+    return workspace
 
 
 def embed(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0,
@@ -157,16 +175,20 @@ def embed(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0,
 
     An id outside the table gives a row of zeros and, where `status` (one int32 on the
     device) is given, sets its bit 0."""
-    code = _float(weight, "weight")
+    code = _float(weight.dtype, "weight")
     if weight.dim() != 2:
         raise ValueError("weight must be [n_rows, d]")
-    w, stride = _rows(weight, "weight")
+    dev = _device(weight, "weight")
+    n_rows, d, stride = _rows(weight, "weight")
     n = _ids(ids)
-    d = w.shape[1]
-    out, out_stride = _out(out, ids.shape + (d,), w.dtype, w.device, stream, "out")
-    _check(_lib().cp_embed(w.data_ptr(), code, w.shape[0], d, stride, ids.data_ptr(), n, scale,
-                           out.data_ptr(), out_stride, _status_ptr(status),
-                           _stream(stream, w.device)), "cp_embed")
+    shape = ids.shape + (d,)
+    if out is None:
+        out, out_stride = _empty(shape, weight.dtype, weight, stream), d
+    else:
+        out_stride = _check_out(out, shape, weight.dtype, dev, "out")
+    _check(_lib().cp_embed(weight.data_ptr(), code, n_rows, d, stride, _on(ids, dev, "ids"), n,
+                           scale, out.data_ptr(), out_stride, _status_ptr(status, dev),
+                           _stream(stream, dev)), "cp_embed")
     return out
 
 
@@ -187,50 +209,54 @@ def embed_grad(dy: torch.Tensor, ids: torch.Tensor, n_rows: int, scale: float = 
 
     accumulate=True adds to `out` instead of overwriting it and touches only the rows that
     ids name (with scale = -rate: a step of gradient descent on the table `out`)."""
-    code = _float(dy, "dy")
+    code = _float(dy.dtype, "dy")
+    dev = _device(dy, "dy")
     n = _ids(ids)
-    g, dy_stride = _rows(dy, "dy")
-    d = g.shape[1]
-    if tuple(dy.shape) != tuple(ids.shape) + (d,):
+    _, d, dy_stride = _rows(dy, "dy")
+    if dy.shape != ids.shape + (d,):
         raise ValueError("dy must be ids.shape + (d,)")
-    if accumulate and out is None:
-        raise ValueError("accumulate needs out")
-    if out is not None and dtype is not None and out.dtype != dtype:
-        raise ValueError("out and dtype differ")
-    out, out_stride = _out(out, (n_rows, d), out.dtype if out is not None else dtype or dy.dtype,
-                           g.device, stream, "out")
-    out_code = _float(out, "out")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        dtype = dtype or dy.dtype
+        out_code = _float(dtype, "the gradient")
+        out, out_stride = _empty((n_rows, d), dtype, dy, stream), d
+    else:
+        if dtype is not None and out.dtype != dtype:
+            raise ValueError("out and dtype differ")
+        out_code = _float(out.dtype, "out")
+        out_stride = _check_out(out, (n_rows, d), out.dtype, dev, "out")
     L = _lib()
     nbytes = L.cp_embed_grad_workspace_bytes(n, n_rows, d)
-    ws = _workspace(workspace, nbytes, g.device, stream)
-    _check(L.cp_embed_grad(g.data_ptr(), code, dy_stride, ids.data_ptr(), n, n_rows, d, scale,
-                           1 if accumulate else 0, out.data_ptr(), out_code, out_stride,
-                           _status_ptr(status), ws.data_ptr(), ws.numel(),
-                           _stream(stream, g.device)), "cp_embed_grad")
+    ws = _workspace(workspace, nbytes, dy, dev, stream)
+    _check(L.cp_embed_grad(dy.data_ptr(), code, dy_stride, _on(ids, dev, "ids"), n, n_rows, d,
+                           scale, 1 if accumulate else 0, out.data_ptr(), out_code, out_stride,
+                           _status_ptr(status, dev), ws.data_ptr(), ws.numel(),
+                           _stream(stream, dev)), "cp_embed_grad")
     return out
 
 
 def _weight(weight: torch.Tensor, d: int) -> int:
-    code = _float(weight, "weight")
     if weight.dim() != 1 or weight.shape[0] != d or not weight.is_contiguous():
         raise ValueError("weight must be contiguous, one value per column")
-    _here(weight, "weight")
-    return code
+    return _float(weight.dtype, "weight")
 
 
 def _norm_inputs(x, weight, residual, residual_out, stream):
-    code = _float(x, "x")
-    x2, x_stride = _rows(x, "x")
-    wcode = _weight(weight, x2.shape[1])
+    code = _float(x.dtype, "x")
+    dev = _device(x, "x")
+    rows, d, xs = _rows(x, "x")
+    wcode = _weight(weight, d)
+    args = [x.data_ptr(), xs, None, 0, code, _on(weight, dev, "weight"), wcode, rows, d]
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out needs a residual")
-        return code, wcode, x2, x_stride, None, 0, None
+        return dev, args, None
     if residual.dtype != x.dtype or residual.shape != x.shape:
         raise ValueError("residual must have x's type and shape")
-    r2, r_stride = _rows(residual, "residual")
-    h = _whole(residual_out, x.shape, x.dtype, x.device, stream, "residual_out")
-    return code, wcode, x2, x_stride, r2.data_ptr(), r_stride, h
+    args[3] = _rows(residual, "residual")[2]
+    args[2] = _on(residual, dev, "residual")
+    return dev, args, _whole(residual_out, x.shape, x.dtype, x, dev, stream, "residual_out")
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
@@ -240,12 +266,10 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
 
     Returns y, and with a residual (y, h), h = s rounded to x's type (`residual_out` may be
     the residual itself: the stream is then updated in place)."""
-    code, wcode, x2, xs, rp, rs, h = _norm_inputs(x, weight, residual, residual_out, stream)
-    y = _whole(out, x.shape, x.dtype, x.device, stream, "out")
-    _check(_lib().cp_rms_norm(x2.data_ptr(), xs, rp, rs, code, weight.data_ptr(), wcode,
-                              x2.shape[0], x2.shape[1], eps, y.data_ptr(),
-                              None if h is None else h.data_ptr(), _stream(stream, x.device)),
-           "cp_rms_norm")
+    dev, args, h = _norm_inputs(x, weight, residual, residual_out, stream)
+    y = _whole(out, x.shape, x.dtype, x, dev, stream, "out")
+    _check(_lib().cp_rms_norm(*args, eps, y.data_ptr(), None if h is None else h.data_ptr(),
+                              _stream(stream, dev)), "cp_rms_norm")
     return y if h is None else (y, h)
 
 
@@ -257,15 +281,13 @@ def rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
 
     q is float8_e4m3fn of x's shape; scales fp32, one for each 128 columns of a row
     (x.shape[:-1] + (ceil(d / 128),)): y is about q * scales."""
-    code, wcode, x2, xs, rp, rs, h = _norm_inputs(x, weight, residual, residual_out, stream)
-    rows, d = x2.shape
-    q = _whole(out, x.shape, _E4M3, x.device, stream, "out")
-    sc = _whole(scales, x.shape[:-1] + ((d + 127) // 128,), torch.float32, x.device, stream,
+    dev, args, h = _norm_inputs(x, weight, residual, residual_out, stream)
+    q = _whole(out, x.shape, _E4M3, x, dev, stream, "out")
+    sc = _whole(scales, x.shape[:-1] + ((args[8] + 127) // 128,), torch.float32, x, dev, stream,
                 "scales")
-    _check(_lib().cp_rms_norm_fp8(x2.data_ptr(), xs, rp, rs, code, weight.data_ptr(), wcode, rows,
-                                  d, eps, q.data_ptr(), sc.data_ptr(),
-                                  None if h is None else h.data_ptr(),
-                                  _stream(stream, x.device)), "cp_rms_norm_fp8")
+    _check(_lib().cp_rms_norm_fp8(*args, eps, q.data_ptr(), sc.data_ptr(),
+                                  None if h is None else h.data_ptr(), _stream(stream, dev)),
+           "cp_rms_norm_fp8")
     return (q, sc) if h is None else (q, sc, h)
 
 
@@ -284,27 +306,27 @@ def rms_norm_grad(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, eps: 
     """(dx, dw) of y = rms_norm at its summed input h: dx is the gradient by x and by the
     residual alike (`dres`, the gradient that reaches h past the norm, is added), dw the
     gradient by weight in weight's type.  `dx` may be `dres` or `dy` itself."""
-    code = _float(h, "h")
-    h2, hs = _rows(h, "h")
-    rows, d = h2.shape
+    code = _float(h.dtype, "h")
+    dev = _device(h, "h")
+    rows, d, hs = _rows(h, "h")
     wcode = _weight(weight, d)
     if dy.dtype != h.dtype or dy.shape != h.shape:
         raise ValueError("dy must have h's type and shape")
-    g2, gs = _rows(dy, "dy")
+    gs = _rows(dy, "dy")[2]
     rp, rs = None, 0
     if dres is not None:
         if dres.dtype != h.dtype or dres.shape != h.shape:
             raise ValueError("dres must have h's type and shape")
-        r2, rs = _rows(dres, "dres")
-        rp = r2.data_ptr()
-    dx = _whole(dx, h.shape, h.dtype, h.device, stream, "dx")
-    dw = _whole(dw, (d,), weight.dtype, h.device, stream, "dw")
+        rs = _rows(dres, "dres")[2]
+        rp = _on(dres, dev, "dres")
+    dx = _whole(dx, h.shape, h.dtype, h, dev, stream, "dx")
+    dw = _whole(dw, (d,), weight.dtype, h, dev, stream, "dw")
     L = _lib()
-    ws = _workspace(workspace, L.cp_rms_norm_grad_workspace_bytes(rows, d), h.device, stream)
-    _check(L.cp_rms_norm_grad(g2.data_ptr(), gs, h2.data_ptr(), hs, rp, rs, code,
-                              weight.data_ptr(), wcode, rows, d, eps, dx.data_ptr(),
-                              dw.data_ptr(), ws.data_ptr(), ws.numel(),
-                              _stream(stream, h.device)), "cp_rms_norm_grad")
+    ws = _workspace(workspace, L.cp_rms_norm_grad_workspace_bytes(rows, d), h, dev, stream)
+    _check(L.cp_rms_norm_grad(_on(dy, dev, "dy"), gs, h.data_ptr(), hs, rp, rs, code,
+                              _on(weight, dev, "weight"), wcode, rows, d, eps, dx.data_ptr(),
+                              dw.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream, dev)),
+           "cp_rms_norm_grad")
     return dx, dw
 
 
@@ -312,31 +334,30 @@ def quantize_fp8(x: torch.Tensor, block_rows: int = 1, out: torch.Tensor | None 
                  scales: torch.Tensor | None = None, stream=None):
     """(q, scales) of x [rows, d]: float8_e4m3fn, and one fp32 scale for each block of
     block_rows x 128 (1: activations, 128: weights), amax / 448."""
-    code = _float(x, "x")
+    code = _float(x.dtype, "x")
     if x.dim() != 2:
         raise ValueError("x must be [rows, d]")
     if block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128")
-    x2, xs = _rows(x, "x")
-    rows, d = x2.shape
-    q = _whole(out, (rows, d), _E4M3, x.device, stream, "out")
-    sc = _whole(scales, (-(-rows // block_rows), -(-d // 128)), torch.float32, x.device, stream,
+    dev = _device(x, "x")
+    rows, d, xs = _rows(x, "x")
+    q = _whole(out, (rows, d), _E4M3, x, dev, stream, "out")
+    sc = _whole(scales, (-(-rows // block_rows), -(-d // 128)), torch.float32, x, dev, stream,
                 "scales")
-    _check(_lib().cp_quantize_fp8(x2.data_ptr(), xs, code, rows, d, block_rows, q.data_ptr(),
-                                  sc.data_ptr(), _stream(stream, x.device)), "cp_quantize_fp8")
+    _check(_lib().cp_quantize_fp8(x.data_ptr(), xs, code, rows, d, block_rows, q.data_ptr(),
+                                  sc.data_ptr(), _stream(stream, dev)), "cp_quantize_fp8")
     return q, sc
 
 
-def _scaled(t, scales, rows, name):
+def _scaled(t: torch.Tensor, scales: torch.Tensor, block: int, dev: int, name: str):
+    """(rows, k, row stride) of an e4m3 matrix whose scales fit it."""
     if t.dtype != _E4M3 or t.dim() != 2:
         raise ValueError(f"{name} must be float8_e4m3fn, [rows, k]")
-    t2, stride = _rows(t, name)
-    want = (rows(t.shape[0]), -(-t.shape[1] // 128))
-    if scales.dtype != torch.float32 or tuple(scales.shape) != want \
-            or not scales.is_contiguous():
+    rows, k, stride = _rows(t, name)
+    want = (-(-rows // block), -(-k // 128))
+    if scales.dtype != torch.float32 or scales.shape != want or not scales.is_contiguous():
         raise ValueError(f"{name}_scales must be contiguous float32 of shape {want}")
-    _here(scales, f"{name}_scales")
-    return t2, stride
+    return rows, k, stride
 
 
 def matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
@@ -345,21 +366,21 @@ def matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scale
     """a @ w.T for a [m, k] and w [n, k] in float8_e4m3fn with scales for each block of 128
     along k (a_scales [m, ceil(k/128)], w_scales [ceil(n/128), ceil(k/128)], fp32), summed in
     fp32 and rounded once to `dtype`."""
-    a2, lda = _scaled(a, a_scales, lambda m: m, "a")
-    w2, ldw = _scaled(w, w_scales, lambda n: -(-n // 128), "w")
-    m, k = a2.shape
-    n = w2.shape[0]
-    if w2.shape[1] != k:
+    dev = _device(a, "a")
+    m, k, lda = _scaled(a, a_scales, 1, dev, "a")
+    n, kw, ldw = _scaled(w, w_scales, 128, dev, "w")
+    if kw != k:
         raise ValueError("a and w must have the same number of columns")
-    if out is not None:
-        dtype = out.dtype
-    code = _CODE.get(dtype)
-    if code is None:
-        raise ValueError("the output must be float32, float16 or bfloat16")
-    out, ldo = _out(out, (m, n), dtype, a.device, stream, "out")
-    _check(_lib().cp_matmul_fp8(a2.data_ptr(), lda, a_scales.data_ptr(), w2.data_ptr(), ldw,
-                                w_scales.data_ptr(), m, n, k, out.data_ptr(), code, ldo,
-                                _stream(stream, a.device)), "cp_matmul_fp8")
+    if out is None:
+        code = _float(dtype, "the output")
+        out, ldo = _empty((m, n), dtype, a, stream), n
+    else:
+        code = _float(out.dtype, "the output")
+        ldo = _check_out(out, (m, n), out.dtype, dev, "out")
+    _check(_lib().cp_matmul_fp8(a.data_ptr(), lda, _on(a_scales, dev, "a_scales"),
+                                _on(w, dev, "w"), ldw, _on(w_scales, dev, "w_scales"), m, n, k,
+                                out.data_ptr(), code, ldo, _stream(stream, dev)),
+           "cp_matmul_fp8")
     return out
 
 
