@@ -388,18 +388,25 @@ struct TcParams {
   int out_dtype;
   uint32_t tiles_m, tiles, stages, splits, tmem_columns;
   uint32_t a_rows;          // rows of a's TMA box
-  bool vec;                 // out rows on 32-byte boundaries
+  uint32_t out_align;       // 32, 16 or 0: bytes on whose boundaries out's rows lie
 };
 
 // Eight consecutive outputs of a row.
 __device__ __forceinline__ void store8(const TcParams& p, uint32_t row, uint32_t col,
                                        const float* v) {
   const uint64_t at = static_cast<uint64_t>(row) * p.ldo + col;
-  if (p.out_dtype == CP_F32 && p.vec && col + 8 <= p.n) {
-    Packed<float> r;
+  if (p.out_align >= 16 && col + 8 <= p.n) {
+    if (p.out_dtype == CP_F32) {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+      o[0] = make_float4(v[0], v[1], v[2], v[3]);
+      o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      float u[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) r.w[e] = __float_as_uint(v[e]);
-    store_octet(static_cast<float*>(p.out) + at, r);
+      for (int e = 0; e < 8; ++e) u[e] = v[e];
+      if (p.out_dtype == CP_F16) store_octet(static_cast<__half*>(p.out) + at, pack<__half>(u));
+      else store_octet(static_cast<__nv_bfloat16*>(p.out) + at, pack<__nv_bfloat16>(u));
+    }
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -411,7 +418,7 @@ __device__ __forceinline__ void store8(const TcParams& p, uint32_t row, uint32_t
 // row's, so only whole sectors keep the writes from being merged in L2.
 __device__ __forceinline__ void store16(const TcParams& p, uint32_t row, uint32_t col,
                                         const float* v) {
-  if (p.out_dtype != CP_F32 && p.vec && col + 16 <= p.n) {
+  if (p.out_dtype != CP_F32 && p.out_align >= 32 && col + 16 <= p.n) {
     Packed<float> r;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -727,15 +734,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 // ----------------------------------------------- few rows of a, many bytes of w: tcgen05
 //
-// With at most 64 rows of a the operands change places: 128 rows of w are the tensor core's
-// 128 x 32 operand, the rows of a its N (16, 32 or 64) columns, and the kernel is bound by
-// the stream of w.  A unit is 128 columns of tensor memory, 128 / kN groups side by side, so
+// With at most 128 rows of a the operands change places: 128 rows of w are the tensor core's
+// 128 x 32 operand, up to 64 rows of a its N (16, 32 or 64) columns, and the kernel is bound by
+// the stream of w (a second tile of rows of a finds it in L2).  A unit is 128 columns of tensor memory, 128 / kN groups side by side, so
 // the sums (a lane has a row of w) wait once a unit; two units alternate.  Two CTAs share an
 // SM; `splits` CTAs of a cluster share a tile's groups and add their sums in order through
 // distributed shared memory.
 
 constexpr int kThinThreads = 256;      // four summing warps, TMA, MMA, scales, one idle
 constexpr uint32_t kThinUnit = 128;    // columns of tensor memory
+constexpr uint32_t kThinRows = 128;
 constexpr uint32_t kThinMaxStages = 6;
 constexpr uint32_t kThinSmem = 111616;  // dynamic shared memory of a CTA, two to an SM
 
@@ -744,7 +752,7 @@ struct ThinParams {
   const float* sw;
   void* out;
   uint64_t ldo;
-  uint32_t m, n, groups, splits, stages;
+  uint32_t m, n, groups, splits, stages, tiles_m;
   int out_dtype;
 };
 
@@ -763,7 +771,9 @@ __global__ void __launch_bounds__(kThinThreads, 2)
                                               ~static_cast<uintptr_t>(1023));
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = p.splits == 1 ? 0 : cpt::cluster_rank();
-  const uint32_t row0 = blockIdx.x / p.splits * 128;
+  const uint32_t tile = blockIdx.x / p.splits;       // those of one part of w come together
+  const uint32_t row0 = tile / p.tiles_m * 128;
+  const uint32_t token0 = tile % p.tiles_m * kN, tokens = min(p.m - token0, kN);
   const uint32_t full = cpt::smem_addr(bars), empty = full + 8 * kThinMaxStages;
   const uint32_t acc_full = empty + 8 * kThinMaxStages, acc_empty = acc_full + 16;
   const uint32_t scale_full = acc_empty + 16;
@@ -811,7 +821,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
       if (cpt::elect_one()) {
         cpt::mbar_expect(full + 8 * s, kStage);
         cpt::tma_load(dst, &map_w, kb * 128, row0, full + 8 * s);
-        cpt::tma_load(dst + kTileA, &map_a, kb * 128, 0, full + 8 * s);
+        cpt::tma_load(dst + kTileA, &map_a, kb * 128, token0, full + 8 * s);
       }
       __syncwarp();
       if (++s == p.stages) {
@@ -864,8 +874,8 @@ __global__ void __launch_bounds__(kThinThreads, 2)
 #pragma unroll
       for (uint32_t i = 0; i < 4; ++i) {
         const uint32_t e = lane + 32 * i, group = kb + e / kN, token = e % kN;
-        f[i] = group < kb1 && token < p.m
-                   ? __ldg(p.sa + static_cast<uint64_t>(token) * p.groups + group) *
+        f[i] = group < kb1 && token < tokens
+                   ? __ldg(p.sa + static_cast<uint64_t>(token0 + token) * p.groups + group) *
                          __ldg(sw + group)
                    : 0.0f;
       }
@@ -920,10 +930,12 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     if (warp < 4 && row < p.n) {
 #pragma unroll
       for (uint32_t i = 0; i < kN; ++i)
-        if (i < p.m) store_from_f32(p.out, i * p.ldo + row, p.out_dtype, acc[i]);
+        if (i < tokens)
+          store_from_f32(p.out, static_cast<uint64_t>(token0 + i) * p.ldo + row, p.out_dtype,
+                         acc[i]);
     }
   } else {
-    // sums as [token][row] over the stages (all loads are used up); each CTA of the cluster
+    // sums as [row of a][row of w] over the stages (all loads are used up); each CTA of the cluster
     // then adds a share of the tokens
     float* part = reinterpret_cast<float*>(tiles);
     if (warp < 4) {
@@ -932,7 +944,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     }
     __syncthreads();
     cpt::cluster_sync();
-    const uint32_t i0 = p.m * 32 * rank / p.splits, i1 = p.m * 32 * (rank + 1) / p.splits;
+    const uint32_t i0 = tokens * 32 * rank / p.splits, i1 = tokens * 32 * (rank + 1) / p.splits;
     for (uint32_t i = i0 + threadIdx.x; i < i1; i += kThinThreads) {
       const uint32_t at = cpt::smem_addr(part + 4 * i);
       float4 v[8];
@@ -949,11 +961,12 @@ __global__ void __launch_bounds__(kThinThreads, 2)
           sum.w += v[q].w;
         }
       }
-      const uint32_t token = i / 32, r = row0 + i % 32 * 4;
+      const uint32_t token = token0 + i / 32, r = row0 + i % 32 * 4;
       const float out[4] = {sum.x, sum.y, sum.z, sum.w};
 #pragma unroll
       for (uint32_t e = 0; e < 4; ++e)
-        if (r + e < p.n) store_from_f32(p.out, token * p.ldo + r + e, p.out_dtype, out[e]);
+        if (r + e < p.n)
+          store_from_f32(p.out, static_cast<uint64_t>(token) * p.ldo + r + e, p.out_dtype, out[e]);
     }
     __syncwarp();
     cpt::cluster_sync();             // no CTA leaves while another may read its shared memory
@@ -1113,7 +1126,9 @@ cp_status launch_tc(const MatmulParams& q, cudaStream_t s) {
   p.tmem_columns = 64;
   while (p.tmem_columns < 2 * bn) p.tmem_columns *= 2;
   const uint64_t elt = dtype_size(q.out_dtype);
-  p.vec = cpx::aligned(q.out, 32) && q.ldo * elt % 32 == 0;
+  p.out_align = cpx::aligned(q.out, 32) && q.ldo * elt % 32 == 0   ? 32
+                : cpx::aligned(q.out, 16) && q.ldo * elt % 16 == 0 ? 16
+                                                                   : 0;
   CUtensorMap map_a, map_w;
   if (!encode_map(&map_a, q.a, q.k, q.m, q.lda, p.a_rows) ||
       !encode_map(&map_w, q.w, q.k, q.n, q.ldw, bn / 2)) {
@@ -1135,12 +1150,13 @@ cp_status launch_thin(const MatmulParams& q, cudaStream_t s) {
   if (tc_device(&e) == nullptr) return cpx::cuda_fail(e, "fp8 matmul device query");
   const uint32_t kn = q.m <= 16 ? 16 : q.m <= 32 ? 32 : 64;
   const uint32_t units = (q.groups + kThinUnit / kn - 1) / (kThinUnit / kn);
-  const uint32_t tiles = (q.n + 127) / 128;
+  const uint32_t tiles_m = (q.m + kn - 1) / kn;
+  const uint32_t tiles = (q.n + 127) / 128 * tiles_m;
   // CTAs share a tile until there are enough to keep every SM's loads in flight.
   uint32_t splits = 1;
   while (splits < 8 && static_cast<uint64_t>(tiles) * splits * 2 <= 304 && units >= 2 * splits)
     splits *= 2;
-  ThinParams p{q.sa, q.sw, q.out, q.ldo, q.m, q.n, q.groups, splits, 0, q.out_dtype};
+  ThinParams p{q.sa, q.sw, q.out, q.ldo, q.m, q.n, q.groups, splits, 0, tiles_m, q.out_dtype};
   const uint32_t stage = kTileA + kn * 128;
   p.stages = (kThinSmem - 1024) / stage;
   if (p.stages > kThinMaxStages) p.stages = kThinMaxStages;
@@ -1212,7 +1228,7 @@ extern "C" cp_status cp_matmul_fp8(const uint8_t* a, uint64_t a_stride, const fl
   if (k != 0 && cpx::aligned(a, 16) && cpx::aligned(w, 16) &&
       (m == 1 || (a_stride % 16 == 0 && a_stride != 0)) &&
       (n == 1 || (w_stride % 16 == 0 && w_stride != 0)))
-    return m > 64 ? launch_tc(p, s)
+    return m > kThinRows ? launch_tc(p, s)
            : m <= kFewRows && n * k <= kFewBytes ? launch_few(p, s) : launch_thin(p, s);
   const uint64_t tiles = ((m + kTile - 1) / kTile) * ((n + kTile - 1) / kTile);
   if (tiles >= kMost) {

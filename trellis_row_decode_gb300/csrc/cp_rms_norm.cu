@@ -7,10 +7,12 @@
 //
 // One pass: a row's octets stay in registers between the sum of squares and the
 // scaling, so every array is read and written once and the kernels are bound by
-// memory.  A team of threads holds a row (kOct octets a thread); 16 neighbouring lanes
-// hold one group of 128 columns, whose largest magnitude takes four shuffles.  Rows too
-// wide for the registers of one team (d > 16384) are read twice, the second time from
-// the cache.
+// memory.  A team of 4 to 1024 threads (a few lanes of a warp, or a whole CTA) holds a
+// row, up to kOct octets a thread; 16 neighbouring lanes hold one group of 128 columns,
+// whose largest magnitude takes four shuffles.  A team walks over the rows: its part of
+// the weight is loaded once, and a row's loads are issued before the row in front of it
+// is summed, so the memory system is busy through the reductions.  Rows too wide for
+// registers are read twice, the second time from the cache.
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -39,15 +41,18 @@ struct NormParams {
   float eps;
 };
 
-// Sums `a` and `b` over the CTA's threads, in the same order on every thread.
-// (One barrier each way: `red` is written again only behind the next call's.)
+// Sums `a` and `b` over the team's threads, in the same order on every thread.  Teams of more
+// than a warp are whole CTAs; `red` alternates between two halves from row to row, so one
+// barrier a row is enough.
 template <int THREADS>
 __device__ __forceinline__ void team_sum(float& a, float& b, float2* red) {
-  a = warp_sum(a);
-  b = warp_sum(b);
+#pragma unroll
+  for (int m = THREADS < 32 ? THREADS / 2 : 16; m > 0; m >>= 1) {
+    a += __shfl_xor_sync(0xFFFFFFFFu, a, m);
+    b += __shfl_xor_sync(0xFFFFFFFFu, b, m);
+  }
   if constexpr (THREADS > 32) {
     constexpr int W = THREADS / 32;
-    __syncthreads();
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
     __syncthreads();
     a = b = 0.0f;
@@ -90,31 +95,27 @@ __device__ __forceinline__ void load_sum(const NormParams& p, const T* x, const 
   }
 }
 
-// The octet's part of the output.  All lanes of the warp take part (the group's
-// largest magnitude is shuffled); `live`: the octet lies in the row.
-template <typename T, bool VEC, bool Q>
+// The octet's part of the output.  All lanes of the warp take part (the group's largest
+// magnitude is shuffled among kGroup lanes: 16, or all of a team of fewer); `live`: the octet
+// lies in a row.
+template <typename T, bool VEC, bool Q, int kGroup = 16>
 __device__ __forceinline__ void emit(const NormParams& p, uint64_t row, uint32_t o, bool live,
-                                     float r, const float (&s)[8]) {
+                                     float r, const float (&s)[8], const float (&w)[8]) {
   float y[8];
-  if (live) {
-    if (p.residual != nullptr)
-      store_row_octet<T, VEC>(static_cast<T*>(p.h) + row * p.d, o, p.d, pack<T>(s));
-    load_weight<VEC>(p.weight, p.weight_dtype, o, p.d, y);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = s[e] * r * y[e];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = 0.0f;
-  }
+  for (int e = 0; e < 8; ++e) y[e] = s[e] * r * w[e];
+  if (live && p.residual != nullptr)
+    store_row_octet<T, VEC>(static_cast<T*>(p.h) + row * p.d, o, p.d, pack<T>(s));
   if constexpr (!Q) {
     if (live) store_row_octet<T, VEC>(static_cast<T*>(p.y) + row * p.d, o, p.d, pack<T>(y));
   } else {
     uint32_t amax = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (VEC || 8 * o + e < p.d) amax = max(amax, mag_bits(y[e]));
+      if (live && (VEC || 8 * o + e < p.d)) amax = max(amax, mag_bits(y[e]));
 #pragma unroll
-    for (int m = 8; m > 0; m >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, m));
+    for (int m = kGroup / 2; m > 0; m >>= 1)
+      amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, m));
     const float scale = scale_of(amax);
     if (live) {
       store_q_octet<VEC>(p.q + row * p.d, o, p.d, quantize_octet(y, __frcp_rn(scale)));
@@ -123,41 +124,71 @@ __device__ __forceinline__ void emit(const NormParams& p, uint64_t row, uint32_t
   }
 }
 
-// A row per team of THREADS threads; one warp: several rows per CTA.
+// Threads of a CTA of teams of `threads`, and CTAs that share an SM.
+constexpr int cta_threads(int threads) { return threads <= 32 ? 256 : threads; }
+constexpr int norm_ctas(int threads) { return 768 / cta_threads(threads) > 1 ? 768 / cta_threads(threads) : 1; }
+
 template <typename T, bool VEC, bool Q, int THREADS, int kOct>
-__global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS) norm_kernel(NormParams p) {
-  constexpr int kTeams = THREADS == 32 ? 4 : 1;
-  __shared__ float2 red[THREADS / 32];
+__global__ void __launch_bounds__(cta_threads(THREADS), norm_ctas(THREADS)) norm_kernel(NormParams p) {
+  constexpr int kTeams = cta_threads(THREADS) / THREADS;
+  __shared__ float2 red[2][THREADS <= 32 ? 1 : THREADS / 32];
   const uint32_t tid = threadIdx.x % THREADS;
-  const uint64_t row = static_cast<uint64_t>(blockIdx.x) * kTeams + threadIdx.x / THREADS;
-  if (row >= p.rows) return;
   const uint32_t octets = (p.d + 7) / 8;
-  const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
-  const T* res = p.residual != nullptr
-                     ? static_cast<const T*>(p.residual) + row * p.residual_stride
-                     : nullptr;
-  float s[kOct][8];
-  float sq = 0.0f, unused = 0.0f;
+  float w[kOct][8];
 #pragma unroll
   for (int i = 0; i < kOct; ++i) {
     const uint32_t o = tid + i * THREADS;
     if (o < octets) {
-      load_sum<T, VEC>(p, x, res, o, s[i]);
+      load_weight<VEC>(p.weight, p.weight_dtype, o, p.d, w[i]);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[i][e] = 0.0f;
+      for (int e = 0; e < 8; ++e) w[i][e] = 0.0f;
     }
   }
+  Packed<T> xn[kOct], rn[kOct];        // the next row
+  auto fetch = [&](uint64_t row) {
+    const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
+    const T* res = static_cast<const T*>(p.residual) + row * p.residual_stride;
 #pragma unroll
-  for (int i = 0; i < kOct; ++i)
+    for (int i = 0; i < kOct; ++i) {
+      const uint32_t o = tid + i * THREADS;
+      const bool in = row < p.rows && o < octets;
+      xn[i] = in ? load_row_octet<T, VEC>(x, o, p.d) : zero_octet<T>();
+      rn[i] = in && p.residual != nullptr ? load_row_octet<T, VEC>(res, o, p.d) : zero_octet<T>();
+    }
+  };
+  // (teams within a warp take their turns together: the shuffles are the warp's)
+  const uint64_t lead = static_cast<uint64_t>(blockIdx.x) * kTeams +
+                        (THREADS < 32 ? threadIdx.x / 32 * (32 / THREADS) : threadIdx.x / THREADS);
+  const uint64_t mine = THREADS < 32 ? (threadIdx.x & 31) / THREADS : 0;
+  const uint64_t step = static_cast<uint64_t>(gridDim.x) * kTeams;
+  fetch(lead + mine);
+  int turn = 0;
+  for (uint64_t at = lead; at < p.rows; at += step, turn ^= 1) {
+    const uint64_t row = at + mine;
+    float s[kOct][8];
+    float sq = 0.0f, unused = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sq = fmaf(s[i][e], s[i][e], sq);
-  team_sum<THREADS>(sq, unused, red);
-  const float r = 1.0f / sqrtf(sq / static_cast<float>(p.d) + p.eps);
+    for (int i = 0; i < kOct; ++i) {
+      unpack<T>(xn[i], s[i]);
+      if (p.residual != nullptr) {
+        float u[8];
+        unpack<T>(rn[i], u);
 #pragma unroll
-  for (int i = 0; i < kOct; ++i) {
-    const uint32_t o = tid + i * THREADS;
-    emit<T, VEC, Q>(p, row, o, o < octets, r, s[i]);
+        for (int e = 0; e < 8; ++e) s[i][e] += u[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sq = fmaf(s[i][e], s[i][e], sq);
+    }
+    fetch(row + step);
+    team_sum<THREADS>(sq, unused, red[turn]);
+    const float r = 1.0f / sqrtf(sq / static_cast<float>(p.d) + p.eps);
+#pragma unroll
+    for (int i = 0; i < kOct; ++i) {
+      const uint32_t o = tid + i * THREADS;
+      emit<T, VEC, Q, THREADS < 16 ? THREADS : 16>(p, row, o, row < p.rows && o < octets, r, s[i],
+                                                   w[i]);
+    }
   }
 }
 
@@ -182,9 +213,12 @@ __global__ void __launch_bounds__(1024) norm_wide_kernel(NormParams p) {
   const float r = 1.0f / sqrtf(sq / static_cast<float>(p.d) + p.eps);
   for (uint32_t o0 = 0; o0 < octets; o0 += 1024) {
     const uint32_t o = o0 + threadIdx.x;
-    float s[8] = {};
-    if (o < octets) load_sum<T, VEC>(p, x, res, o, s);
-    emit<T, VEC, Q>(p, row, o, o < octets, r, s);
+    float s[8] = {}, w[8] = {};
+    if (o < octets) {
+      load_sum<T, VEC>(p, x, res, o, s);
+      load_weight<VEC>(p.weight, p.weight_dtype, o, p.d, w);
+    }
+    emit<T, VEC, Q>(p, row, o, o < octets, r, s, w);
   }
 }
 
@@ -204,88 +238,130 @@ struct GradParams {
   float eps;
 };
 
-// dx = dres + r t - h r^3 mean(t h), the formula with n = h r written out.
+// dx = dres + r (t - h c), c = r^2 mean(t h): the formula with n = h r written out.
 template <typename T, bool VEC>
 __device__ __forceinline__ void emit_dx(const GradParams& p, uint64_t row, uint32_t o, float r,
-                                        float c, const float (&t)[8], const float (&h)[8]) {
+                                        float c, const float (&t)[8], const float (&h)[8],
+                                        const Packed<T>& res) {
   float dx[8];
-  if (p.dres != nullptr) {
-    unpack<T>(load_row_octet<T, VEC>(static_cast<const T*>(p.dres) + row * p.dres_stride, o, p.d),
-              dx);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) dx[e] = 0.0f;
-  }
+  unpack<T>(res, dx);
 #pragma unroll
   for (int e = 0; e < 8; ++e) dx[e] += r * (t[e] - h[e] * c);
   store_row_octet<T, VEC>(static_cast<T*>(p.dx) + row * p.d, o, p.d, pack<T>(dx));
 }
 
-// CTAs walk over the rows; a thread's columns are the same in every row, so it sums
-// its part of dw in registers and leaves it behind the last row.
+constexpr int grad_ctas_per_sm(int threads) {
+  return 512 / cta_threads(threads) > 1 ? 512 / cta_threads(threads) : 1;
+}
+
+// Teams walk over the rows; a thread's columns are the same in every row, so it sums its part
+// of dw in registers, and the CTA's teams add theirs in order behind the last row.
 template <typename T, bool VEC, int THREADS, int kOct>
-__global__ void __launch_bounds__(THREADS) norm_grad_kernel(GradParams p) {
-  __shared__ float2 red[THREADS / 32];
+__global__ void __launch_bounds__(cta_threads(THREADS), grad_ctas_per_sm(THREADS))
+    norm_grad_kernel(GradParams p) {
+  constexpr int kTeams = cta_threads(THREADS) / THREADS;
+  __shared__ float2 red[2][THREADS <= 32 ? 1 : THREADS / 32];
+  __shared__ float sums[kTeams == 1 ? 1 : THREADS * kOct * 8];
+  const uint32_t tid = threadIdx.x % THREADS;
   const uint32_t octets = (p.d + 7) / 8;
-  float dw[kOct][8];
+  float w[kOct][8], dw[kOct][8];
 #pragma unroll
-  for (int i = 0; i < kOct; ++i)
+  for (int i = 0; i < kOct; ++i) {
+    const uint32_t o = tid + i * THREADS;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
-  for (uint64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const T* dyr = static_cast<const T*>(p.dy) + row * p.dy_stride;
-    const T* hr = static_cast<const T*>(p.h) + row * p.h_stride;
-    Packed<T> g[kOct], hp[kOct];
+    for (int e = 0; e < 8; ++e) w[i][e] = dw[i][e] = 0.0f;
+    if (o < octets) load_weight<VEC>(p.weight, p.weight_dtype, o, p.d, w[i]);
+  }
+  Packed<T> hn[kOct], gn[kOct], rn[kOct];          // the next row
+  auto fetch = [&](uint64_t row) {
+    const T* h = static_cast<const T*>(p.h) + row * p.h_stride;
+    const T* dy = static_cast<const T*>(p.dy) + row * p.dy_stride;
 #pragma unroll
     for (int i = 0; i < kOct; ++i) {
-      const uint32_t o = threadIdx.x + i * THREADS;
-      hp[i] = o < octets ? load_row_octet<T, VEC>(hr, o, p.d) : zero_octet<T>();
-      g[i] = o < octets ? load_row_octet<T, VEC>(dyr, o, p.d) : zero_octet<T>();
+      const uint32_t o = tid + i * THREADS;
+      const bool in = row < p.rows && o < octets;
+      hn[i] = in ? load_row_octet<T, VEC>(h, o, p.d) : zero_octet<T>();
+      gn[i] = in ? load_row_octet<T, VEC>(dy, o, p.d) : zero_octet<T>();
     }
+  };
+  auto fetch_res = [&](uint64_t row) {
+    const T* res = static_cast<const T*>(p.dres) + row * p.dres_stride;
+#pragma unroll
+    for (int i = 0; i < kOct; ++i) {
+      const uint32_t o = tid + i * THREADS;
+      rn[i] = row < p.rows && o < octets && p.dres != nullptr ? load_row_octet<T, VEC>(res, o, p.d)
+                                                               : zero_octet<T>();
+    }
+  };
+  const uint64_t lead = static_cast<uint64_t>(blockIdx.x) * kTeams +
+                        (THREADS < 32 ? threadIdx.x / 32 * (32 / THREADS) : threadIdx.x / THREADS);
+  const uint64_t mine = THREADS < 32 ? (threadIdx.x & 31) / THREADS : 0;
+  const uint64_t step = static_cast<uint64_t>(gridDim.x) * kTeams;
+  fetch(lead + mine);
+  fetch_res(lead + mine);
+  int turn = 0;
+  for (uint64_t at = lead; at < p.rows; at += step, turn ^= 1) {
+    const uint64_t row = at + mine;
+    float h[kOct][8], t[kOct][8];
     float sq = 0.0f, th = 0.0f;
 #pragma unroll
     for (int i = 0; i < kOct; ++i) {
-      const uint32_t o = threadIdx.x + i * THREADS;
-      float h[8], t[8], w[8];
-      unpack<T>(hp[i], h);
-      unpack<T>(g[i], t);
-      if (o < octets) {
-        load_weight<VEC>(p.weight, p.weight_dtype, o, p.d, w);
+      unpack<T>(hn[i], h[i]);
+      unpack<T>(gn[i], t[i]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          sq = fmaf(h[e], h[e], sq);
-          th = fmaf(t[e] * w[e], h[e], th);
-        }
+      for (int e = 0; e < 8; ++e) {
+        sq = fmaf(h[i][e], h[i][e], sq);
+        th = fmaf(t[i][e] * w[i][e], h[i][e], th);
       }
     }
-    team_sum<THREADS>(sq, th, red);
+    fetch(row + step);
+    team_sum<THREADS>(sq, th, red[turn]);
     const float inv_d = 1.0f / static_cast<float>(p.d);
     const float r = 1.0f / sqrtf(sq * inv_d + p.eps);
     const float c = r * r * (th * inv_d);
+    if (row < p.rows) {
 #pragma unroll
-    for (int i = 0; i < kOct; ++i) {
-      const uint32_t o = threadIdx.x + i * THREADS;
-      if (o < octets) {
-        float h[8], t[8], w[8];
-        unpack<T>(hp[i], h);
-        unpack<T>(g[i], t);
-        load_weight<VEC>(p.weight, p.weight_dtype, o, p.d, w);
+      for (int i = 0; i < kOct; ++i) {
+        const uint32_t o = tid + i * THREADS;
+        if (o < octets) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          dw[i][e] = fmaf(t[e], h[e] * r, dw[i][e]);
-          t[e] *= w[e];
+          for (int e = 0; e < 8; ++e) {
+            dw[i][e] = fmaf(t[i][e], h[i][e] * r, dw[i][e]);
+            t[i][e] *= w[i][e];
+          }
+          emit_dx<T, VEC>(p, row, o, r, c, t[i], h[i], rn[i]);
         }
-        emit_dx<T, VEC>(p, row, o, r, c, t, h);
       }
     }
+    fetch_res(row + step);
   }
   float* part = p.parts + static_cast<uint64_t>(blockIdx.x) * p.d;
+  if constexpr (kTeams == 1) {
 #pragma unroll
-  for (int i = 0; i < kOct; ++i) {
-    const uint32_t o = threadIdx.x + i * THREADS;
+    for (int i = 0; i < kOct; ++i) {
+      const uint32_t o = tid + i * THREADS;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (8 * o + e < p.d) part[8 * o + e] = dw[i][e];
+      for (int e = 0; e < 8; ++e)
+        if (8 * o + e < p.d) part[8 * o + e] = dw[i][e];
+    }
+  } else {
+    // columns lie by element first, so that neighbouring lanes have neighbouring words
+    for (uint32_t team = 0; team < kTeams; ++team) {
+      if (threadIdx.x / THREADS == team) {
+#pragma unroll
+        for (int i = 0; i < kOct; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float& s = sums[(i * 8 + e) * THREADS + tid];
+            s = team == 0 ? dw[i][e] : s + dw[i][e];
+          }
+      }
+      __syncthreads();
+    }
+    for (uint32_t c = threadIdx.x; c < p.d; c += cta_threads(THREADS)) {
+      const uint32_t o = c / 8;
+      part[c] = sums[(o / THREADS * 8 + c % 8) * THREADS + o % THREADS];
+    }
   }
 }
 
@@ -293,13 +369,14 @@ __global__ void __launch_bounds__(THREADS) norm_grad_kernel(GradParams p) {
 // its own columns).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(1024) norm_grad_wide_kernel(GradParams p) {
-  __shared__ float2 red[32];
+  __shared__ float2 red[2][32];
   extern __shared__ float dw[];
   const uint32_t octets = (p.d + 7) / 8;
   for (uint32_t o = threadIdx.x; o < octets; o += 1024)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[e * octets + o] = 0.0f;
-  for (uint64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+  int turn = 0;
+  for (uint64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
     const T* dyr = static_cast<const T*>(p.dy) + row * p.dy_stride;
     const T* hr = static_cast<const T*>(p.h) + row * p.h_stride;
     float sq = 0.0f, th = 0.0f;
@@ -314,7 +391,7 @@ __global__ void __launch_bounds__(1024) norm_grad_wide_kernel(GradParams p) {
         th = fmaf(t[e] * w[e], h[e], th);
       }
     }
-    team_sum<1024>(sq, th, red);
+    team_sum<1024>(sq, th, red[turn]);
     const float inv_d = 1.0f / static_cast<float>(p.d);
     const float r = 1.0f / sqrtf(sq * inv_d + p.eps);
     const float c = r * r * (th * inv_d);
@@ -328,7 +405,11 @@ __global__ void __launch_bounds__(1024) norm_grad_wide_kernel(GradParams p) {
         dw[e * octets + o] = fmaf(t[e], h[e] * r, dw[e * octets + o]);
         t[e] *= w[e];
       }
-      emit_dx<T, VEC>(p, row, o, r, c, t, h);
+      emit_dx<T, VEC>(p, row, o, r, c, t, h,
+                      p.dres != nullptr
+                          ? load_row_octet<T, VEC>(
+                                static_cast<const T*>(p.dres) + row * p.dres_stride, o, p.d)
+                          : zero_octet<T>());
     }
   }
   float* part = p.parts + static_cast<uint64_t>(blockIdx.x) * p.d;
@@ -363,22 +444,31 @@ __global__ void __launch_bounds__(kDwThreads) norm_dw_kernel(GradParams p) {
 
 // -------------------------------------------------------------------------- host
 
+constexpr uint64_t kSms = 152;
+
+template <typename T, bool VEC, bool Q, int THREADS, int kOct>
+void launch_teams(const NormParams& p, cudaStream_t s) {
+  constexpr int kTeams = cta_threads(THREADS) / THREADS;
+  const uint64_t ctas = (static_cast<uint64_t>(p.rows) + kTeams - 1) / kTeams;
+  const uint64_t most = kSms * norm_ctas(THREADS);
+  norm_kernel<T, VEC, Q, THREADS, kOct>
+      <<<static_cast<unsigned>(ctas < most ? ctas : most), cta_threads(THREADS), 0, s>>>(p);
+}
+
 template <typename T, bool VEC, bool Q>
 cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
   const uint32_t octets = (p.d + 7) / 8;
-  if (octets <= 128) {
-    norm_kernel<T, VEC, Q, 32, 4><<<(p.rows + 3) / 4, 128, 0, s>>>(p);
-  } else if (octets <= 256) {
-    norm_kernel<T, VEC, Q, 128, 2><<<p.rows, 128, 0, s>>>(p);
-  } else if (octets <= 512) {
-    norm_kernel<T, VEC, Q, 256, 2><<<p.rows, 256, 0, s>>>(p);
-  } else if (octets <= 1024) {
-    norm_kernel<T, VEC, Q, 512, 2><<<p.rows, 512, 0, s>>>(p);
-  } else if (octets <= 2048) {
-    norm_kernel<T, VEC, Q, 1024, 2><<<p.rows, 1024, 0, s>>>(p);
-  } else {
-    norm_wide_kernel<T, VEC, Q><<<p.rows, 1024, 0, s>>>(p);
-  }
+  if (octets <= 4) launch_teams<T, VEC, Q, 4, 1>(p, s);
+  else if (octets <= 8) launch_teams<T, VEC, Q, 8, 1>(p, s);
+  else if (octets <= 16) launch_teams<T, VEC, Q, 16, 1>(p, s);
+  else if (octets <= 32) launch_teams<T, VEC, Q, 32, 1>(p, s);
+  else if (octets <= 64) launch_teams<T, VEC, Q, 32, 2>(p, s);
+  else if (octets <= 128) launch_teams<T, VEC, Q, 64, 2>(p, s);
+  else if (octets <= 256) launch_teams<T, VEC, Q, 128, 2>(p, s);
+  else if (octets <= 512) launch_teams<T, VEC, Q, 256, 2>(p, s);
+  else if (octets <= 1024) launch_teams<T, VEC, Q, 512, 2>(p, s);
+  else if (octets <= 2048) launch_teams<T, VEC, Q, 1024, 2>(p, s);
+  else norm_wide_kernel<T, VEC, Q><<<p.rows, 1024, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -389,18 +479,24 @@ cudaError_t launch_norm(const NormParams& p, bool vec, cudaStream_t s) {
   return vec ? launch_norm<T, true, false>(p, s) : launch_norm<T, false, false>(p, s);
 }
 
+template <typename T, bool VEC, int THREADS, int kOct>
+void launch_grad_teams(const GradParams& p, cudaStream_t s) {
+  norm_grad_kernel<T, VEC, THREADS, kOct><<<p.ctas, cta_threads(THREADS), 0, s>>>(p);
+}
+
 template <typename T, bool VEC>
 cudaError_t launch_grad(const GradParams& p, cudaStream_t s) {
   const uint32_t octets = (p.d + 7) / 8;
-  if (octets <= 128) {
-    norm_grad_kernel<T, VEC, 128, 1><<<p.ctas, 128, 0, s>>>(p);
-  } else if (octets <= 256) {
-    norm_grad_kernel<T, VEC, 128, 2><<<p.ctas, 128, 0, s>>>(p);
-  } else if (octets <= 512) {
-    norm_grad_kernel<T, VEC, 256, 2><<<p.ctas, 256, 0, s>>>(p);
-  } else if (octets <= 1024) {
-    norm_grad_kernel<T, VEC, 512, 2><<<p.ctas, 512, 0, s>>>(p);
-  } else {
+  if (octets <= 4) launch_grad_teams<T, VEC, 4, 1>(p, s);
+  else if (octets <= 8) launch_grad_teams<T, VEC, 8, 1>(p, s);
+  else if (octets <= 16) launch_grad_teams<T, VEC, 16, 1>(p, s);
+  else if (octets <= 32) launch_grad_teams<T, VEC, 32, 1>(p, s);
+  else if (octets <= 64) launch_grad_teams<T, VEC, 32, 2>(p, s);
+  else if (octets <= 128) launch_grad_teams<T, VEC, 64, 2>(p, s);
+  else if (octets <= 256) launch_grad_teams<T, VEC, 128, 2>(p, s);
+  else if (octets <= 512) launch_grad_teams<T, VEC, 256, 2>(p, s);
+  else if (octets <= 1024) launch_grad_teams<T, VEC, 512, 2>(p, s);
+  else {
     const int smem = static_cast<int>(octets * 32);
     auto* fn = &norm_grad_wide_kernel<T, VEC>;
     cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
@@ -414,12 +510,16 @@ cudaError_t launch_grad(const GradParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// CTAs of a gradient call: enough to fill the card, each with its own sums for dw.
+// CTAs of a gradient call, each with its own sums for dw: those that fit on the card at once.
 uint32_t grad_ctas(uint64_t rows, uint32_t d) {
   const uint32_t octets = (d + 7) / 8;
-  const uint64_t per_sm = octets <= 256 ? 8 : octets <= 512 ? 4 : octets <= 1024 ? 2 : 1;
-  const uint64_t most = per_sm * 152;
-  return static_cast<uint32_t>(rows < most ? rows : most);
+  uint32_t team = 4;
+  while (team < 32 && team < octets) team *= 2;
+  if (octets > 64) team = octets <= 128 ? 64 : octets <= 256 ? 128 : octets <= 512 ? 256 : octets <= 1024 ? 512 : 1024;
+  const int threads = static_cast<int>(team);
+  const uint64_t teams = cta_threads(threads) / threads;
+  const uint64_t ctas = (rows + teams - 1) / teams, most = kSms * grad_ctas_per_sm(threads);
+  return static_cast<uint32_t>(ctas < most ? ctas : most);
 }
 
 // Checks shared by the norms; writes whether whole octets can be moved.
