@@ -32,14 +32,23 @@ using namespace cpl;
 
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
+// Kernels of one call run in order; each is launched while the one before it still runs
+// (programmatic dependent launch) and waits, in hardware, for its results here.
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ------------------------------------------------------------------------ sort
 
-constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kRounds = 4;                                   // keys per thread and sub-tile
-constexpr uint32_t kSub = kSortThreads * kRounds;            // 4096 keys per sub-tile
+constexpr int kSmallThreads = 1024;
+constexpr uint32_t kSmallMax = kSmallThreads * kRounds;      // ids that one CTA sorts
+constexpr int kSortThreads = 512;
+constexpr uint32_t kSub = kSortThreads * kRounds;            // 2048 keys per sub-tile
 constexpr uint32_t kMaxTiles = 512;
-constexpr uint32_t kSmallMax = kSub;                         // one CTA's keys
 constexpr int kMaxBits = 9;                                  // digit width
 constexpr int kSmallBits = 8;                                // in one CTA (48 KB of shared memory)
 constexpr uint32_t kMaxBins = 1u << kMaxBits;
@@ -48,40 +57,76 @@ __device__ __forceinline__ uint32_t key_of(int64_t id, uint32_t n_rows) {
   return static_cast<uint64_t>(id) < n_rows ? static_cast<uint32_t>(id) : n_rows;
 }
 
+// Lanes whose digit (of `bits` bits) is the same as this lane's, among those with a key.
+__device__ __forceinline__ uint32_t same_digit(uint32_t digit, int bits, bool have) {
+  uint32_t peers = __ballot_sync(kFull, have);
+  for (int b = 0; b < bits; ++b) {
+    const uint32_t set = __ballot_sync(kFull, (digit >> b) & 1);
+    peers &= (digit >> b) & 1 ? set : ~set;
+  }
+  return peers;
+}
+
+// Exclusive prefix sums of v[0..bins), bins <= 512, over the CTA (512 threads or more).
+__device__ __forceinline__ void exclusive_scan(uint32_t* v, uint32_t bins, uint32_t* warp_sums) {
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t own = 0, x = 0;
+  if (threadIdx.x < kMaxBins) {
+    own = x = threadIdx.x < bins ? v[threadIdx.x] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(kFull, x, o);
+      if (lane >= static_cast<uint32_t>(o)) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+  }
+  __syncthreads();
+  if (threadIdx.x < bins) {
+    uint32_t before = 0;
+    for (uint32_t w = 0; w < warp; ++w) before += warp_sums[w];
+    v[threadIdx.x] = before + x - own;
+  }
+  __syncthreads();
+}
+
 // Ranks of a sub-tile's keys among the keys of the same digit, in order.  Warp w owns
 // keys [w * 128, w * 128 + 128), 32 a round; `hist` [warp][bin] ends as the count of the
-// bin in earlier warps, `total` as the sub-tile's counts.
+// bin in earlier warps, `total` as the sub-tile's counts.  digit == bins: no key.
 struct Ranks {
   uint32_t r[kRounds];
 };
 
-__device__ __forceinline__ Ranks rank_digits(const uint32_t (&digit)[kRounds], uint32_t bins,
+template <int kThreads>
+__device__ __forceinline__ Ranks rank_digits(const uint32_t (&digit)[kRounds], int bits,
                                              uint16_t* hist, uint32_t* total) {
-  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kWarps = kThreads / 32;
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bins = 1u << bits;
   uint16_t* mine = hist + warp * bins;
   for (uint32_t b = lane; b < bins; b += 32) mine[b] = 0;
   __syncwarp();
   Ranks out;
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) {
-    const uint32_t d = digit[r];                 // bins: no key here
-    const uint32_t peers = __match_any_sync(kFull, d);
+    const uint32_t d = digit[r];
+    const bool have = d < bins;
+    const uint32_t peers = same_digit(d, bits, have);
     const uint32_t before = __popc(peers & ((1u << lane) - 1));
     uint32_t prior = 0;
-    if (d < bins) prior = mine[d];
+    if (have) prior = mine[d];
     __syncwarp();
-    if (d < bins && before == 0) mine[d] = static_cast<uint16_t>(prior + __popc(peers));
+    if (have && before == 0) mine[d] = static_cast<uint16_t>(prior + __popc(peers));
     __syncwarp();
     out.r[r] = prior + before;
   }
   __syncthreads();
-  for (uint32_t b = threadIdx.x; b < bins; b += kSortThreads) {
-    uint32_t sum = 0;
-#pragma unroll 8
-    for (int w = 0; w < kSortWarps; ++w) {
-      const uint32_t c = hist[w * bins + b];
+  for (uint32_t b = threadIdx.x; b < bins; b += kThreads) {
+    uint32_t c[kWarps], sum = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) c[w] = hist[w * bins + b];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
       hist[w * bins + b] = static_cast<uint16_t>(sum);
-      sum += c;
+      sum += c[w];
     }
     total[b] = sum;
   }
@@ -89,35 +134,16 @@ __device__ __forceinline__ Ranks rank_digits(const uint32_t (&digit)[kRounds], u
   return out;
 }
 
-// Exclusive prefix sums of v[0..bins), bins <= 512, by warp 0; all threads sync.
-__device__ __forceinline__ void exclusive_scan(uint32_t* v, uint32_t bins) {
-  if (threadIdx.x < 32) {
-    const uint32_t lane = threadIdx.x;
-    uint32_t carry = 0;
-    for (uint32_t b = 0; b < bins; b += 32) {
-      uint32_t x = b + lane < bins ? v[b + lane] : 0;
-      const uint32_t own = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(kFull, x, o);
-        if (lane >= static_cast<uint32_t>(o)) x += y;
-      }
-      if (b + lane < bins) v[b + lane] = carry + x - own;
-      carry += __shfl_sync(kFull, x, 31);
-    }
-  }
-  __syncthreads();
-}
-
 // Up to kSmallMax ids in one CTA: all passes in shared memory.
-__global__ void __launch_bounds__(kSortThreads)
+__global__ void __launch_bounds__(kSmallThreads)
     sort_small_kernel(const int64_t* __restrict__ ids, uint32_t n, uint32_t n_rows, int passes,
                       int bits, uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out,
                       uint32_t* status) {
-  __shared__ uint32_t key_s[kSub];
-  __shared__ uint16_t pos_s[kSub];
+  __shared__ uint32_t key_s[kSmallMax];
+  __shared__ uint16_t pos_s[kSmallMax];
   extern __shared__ uint16_t hist[];             // [warps][bins]
-  __shared__ uint32_t total[kMaxBins];
+  __shared__ uint32_t total[kMaxBins], warp_sums[32];
+  let_next_start();
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t key[kRounds], pos[kRounds];
   bool bad = false;
@@ -138,8 +164,8 @@ __global__ void __launch_bounds__(kSortThreads)
 #pragma unroll
     for (int r = 0; r < kRounds; ++r)
       digit[r] = pos[r] < n ? (key[r] >> (p * bits)) & (bins - 1) : bins;
-    const Ranks rk = rank_digits(digit, bins, hist, total);
-    exclusive_scan(total, bins);
+    const Ranks rk = rank_digits<kSmallThreads>(digit, bits, hist, total);
+    exclusive_scan(total, bins, warp_sums);
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
       if (digit[r] < bins) {
@@ -178,7 +204,8 @@ struct SortPass {
   uint32_t* pos_out;
   uint32_t* counts;              // [tiles][bins]
   uint32_t n, n_rows, per_tile;  // per_tile: a multiple of kSub
-  uint32_t shift, bits;
+  uint32_t shift;
+  int bits;
   uint32_t* status;
 };
 
@@ -187,6 +214,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortPass p) {
   const uint32_t bins = 1u << p.bits;
   for (uint32_t b = threadIdx.x; b < bins; b += kSortThreads) hist[b] = 0;
   __syncthreads();
+  wait_for_previous();
+  let_next_start();
   const uint64_t lo = static_cast<uint64_t>(blockIdx.x) * p.per_tile;
   const uint64_t hi = lo + p.per_tile < p.n ? lo + p.per_tile : p.n;
   bool bad = false;
@@ -202,13 +231,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortPass p) {
       }
     }
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-      const bool have = key[r] != kFull;
-      const uint32_t d = have ? (key[r] >> p.shift) & (bins - 1) : bins;
-      const uint32_t peers = __match_any_sync(kFull, d);
-      if (have && (peers & ((1u << (threadIdx.x & 31)) - 1)) == 0)
-        atomicAdd(&hist[d], static_cast<uint32_t>(__popc(peers)));
-    }
+    for (int r = 0; r < kRounds; ++r)
+      if (key[r] != kFull) atomicAdd(&hist[(key[r] >> p.shift) & (bins - 1)], 1u);
   }
   if (p.ids != nullptr && p.status != nullptr && bad) atomicOr(p.status, 1u);
   __syncthreads();
@@ -218,57 +242,76 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortPass p) {
 
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortPass p) {
   extern __shared__ uint16_t hist[];             // [warps][bins]
-  __shared__ uint32_t total[kMaxBins];
+  __shared__ uint32_t total[kMaxBins], warp_sums[32];
   __shared__ uint32_t base[kMaxBins];            // where this tile's next key of a digit goes
-  __shared__ uint32_t part[kSortThreads], part_all[kSortThreads];
+  __shared__ uint4 part[kSortThreads], part_all[kSortThreads];
   const uint32_t bins = 1u << p.bits, tiles = gridDim.x, tile = blockIdx.x;
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // counts of each digit before this tile and in all tiles: thread groups of `bins`
-  // threads share the tiles, reading whole rows of counts
+  wait_for_previous();
+  let_next_start();
+  const uint64_t lo = static_cast<uint64_t>(tile) * p.per_tile;
+  const uint64_t hi = lo + p.per_tile < p.n ? lo + p.per_tile : p.n;
+  uint32_t key[kRounds], pos[kRounds];
+  auto load_keys = [&](uint64_t i0) {
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      const uint64_t i = i0 + warp * (32 * kRounds) + r * 32 + lane;
+      key[r] = pos[r] = kFull;
+      if (i < hi) {
+        key[r] = p.ids != nullptr ? key_of(p.ids[i], p.n_rows) : p.keys[i];
+        pos[r] = p.ids != nullptr ? static_cast<uint32_t>(i) : p.pos[i];
+      }
+    }
+  };
+  load_keys(lo);
+  // Counts of each digit before this tile and in all tiles: bins / 4 threads read a tile's
+  // counts four at a time, and the thread groups share the tiles.
   {
-    const uint32_t groups = kSortThreads / bins;           // bins <= 512: at least 2
-    const uint32_t g = threadIdx.x / bins, b = threadIdx.x - g * bins;
-    uint32_t before = 0, all = 0;
+    const uint32_t per = bins / 4, groups = kSortThreads / per;       // bins >= 4
+    const uint32_t g = threadIdx.x / per, q = threadIdx.x - g * per;
+    uint4 before = make_uint4(0, 0, 0, 0), all = before;
     if (g < groups) {
 #pragma unroll 8
       for (uint32_t t = g; t < tiles; t += groups) {
-        const uint32_t c = p.counts[t * bins + b];
-        all += c;
-        before += t < tile ? c : 0;
+        const uint4 c = *reinterpret_cast<const uint4*>(p.counts + t * bins + 4 * q);
+        all.x += c.x;
+        all.y += c.y;
+        all.z += c.z;
+        all.w += c.w;
+        if (t < tile) {
+          before.x += c.x;
+          before.y += c.y;
+          before.z += c.z;
+          before.w += c.w;
+        }
       }
     }
     part[threadIdx.x] = before;
     part_all[threadIdx.x] = all;
     __syncthreads();
+    const uint32_t* parts = reinterpret_cast<const uint32_t*>(part);
+    const uint32_t* parts_all = reinterpret_cast<const uint32_t*>(part_all);
     for (uint32_t i = threadIdx.x; i < bins; i += kSortThreads) {
       uint32_t x = 0, y = 0;
       for (uint32_t k = 0; k < groups; ++k) {
-        x += part[k * bins + i];
-        y += part_all[k * bins + i];
+        x += parts[k * bins + i];
+        y += parts_all[k * bins + i];
       }
       base[i] = x;
       total[i] = y;
     }
     __syncthreads();
-    exclusive_scan(total, bins);
+    exclusive_scan(total, bins, warp_sums);
     for (uint32_t i = threadIdx.x; i < bins; i += kSortThreads) base[i] += total[i];
     __syncthreads();
   }
-  const uint64_t lo = static_cast<uint64_t>(tile) * p.per_tile;
-  const uint64_t hi = lo + p.per_tile < p.n ? lo + p.per_tile : p.n;
   for (uint64_t i0 = lo; i0 < hi; i0 += kSub) {
-    uint32_t key[kRounds], pos[kRounds], digit[kRounds];
+    if (i0 != lo) load_keys(i0);
+    uint32_t digit[kRounds];
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-      const uint64_t i = i0 + warp * (32 * kRounds) + r * 32 + lane;
-      digit[r] = bins;
-      if (i < hi) {
-        key[r] = p.ids != nullptr ? key_of(p.ids[i], p.n_rows) : p.keys[i];
-        pos[r] = p.ids != nullptr ? static_cast<uint32_t>(i) : p.pos[i];
-        digit[r] = (key[r] >> p.shift) & (bins - 1);
-      }
-    }
-    const Ranks rk = rank_digits(digit, bins, hist, total);
+    for (int r = 0; r < kRounds; ++r)
+      digit[r] = pos[r] != kFull ? (key[r] >> p.shift) & (bins - 1) : bins;
+    const Ranks rk = rank_digits<kSortThreads>(digit, p.bits, hist, total);
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
       if (digit[r] < bins) {
@@ -288,6 +331,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortPass p) {
 constexpr int kSumThreads = 256;
 constexpr uint32_t kSlab = 256;                  // columns of a warp: an octet per lane
 constexpr uint32_t kAhead = 8;                   // dy rows in flight per warp
+constexpr uint32_t kBatch = 128;                 // lookups whose ids a warp stages at a time
+constexpr uint32_t kWarps = kSumThreads / 32;
 
 struct SumParams {
   const uint32_t* keys;          // sorted; n_rows for ids outside the table
@@ -298,8 +343,9 @@ struct SumParams {
   float scale;
   void* grad;
   uint64_t grad_stride;
-  float* head;                   // [chunks][d]: a row's last part, where it began earlier
-  float* tail;                   // [chunks][d]: a row's part, where it goes on
+  uint64_t pitch;                // d rounded up to whole octets
+  float* head;                   // [chunks][pitch]: a row's last part, where it began earlier
+  float* tail;                   // [chunks][pitch]: a row's part, where it goes on
   uint32_t* head_row;            // [chunks]: that row, or kFull
   uint32_t* end_key;             // [chunks]: 2 * (row in progress at the end) + (1: a part is left)
 };
@@ -378,26 +424,35 @@ __device__ __forceinline__ void write_row(const SumParams& p, uint32_t row, uint
   store_row_octet<TG, VEC>(g, o, p.d, pack<TG>(v));
 }
 
-__device__ __forceinline__ void store_part(float* part, uint32_t o, uint32_t d,
-                                           const float (&acc)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (8 * o + e < d) part[8 * o + e] = acc[e];
+__device__ __forceinline__ void store_part(float* part, uint32_t o, const float (&acc)[8]) {
+  float4* to = reinterpret_cast<float4*>(part + 8 * o);
+  to[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+  to[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
 }
 
 template <typename TD, typename TG, bool VD, bool VG, bool ACC>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(SumParams p) {
-  const uint32_t lane = threadIdx.x & 31;
-  const uint64_t unit = (static_cast<uint64_t>(blockIdx.x) * kSumThreads + threadIdx.x) >> 5;
+  __shared__ Cut cuts[kWarps + 1];
+  __shared__ uint32_t key_s[kWarps][kBatch + kAhead], pos_s[kWarps][kBatch + kAhead];
+  extern __shared__ __align__(16) uint8_t ring[];  // [warp][kAhead][lane] octets
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  wait_for_previous();
+  // The CTA's warps find its chunks' cuts side by side: chunk0, chunk0 + 1, ..
+  const uint64_t unit0 = static_cast<uint64_t>(blockIdx.x) * kWarps, unit = unit0 + warp;
+  const uint32_t chunk0 = static_cast<uint32_t>(unit0 / p.slabs);
   const uint32_t chunk = static_cast<uint32_t>(unit / p.slabs);
+  const uint32_t last = static_cast<uint32_t>((unit0 + kWarps - 1) / p.slabs);
+  for (uint32_t k = warp; k <= last - chunk0 + 1; k += kWarps) {
+    const uint64_t c = static_cast<uint64_t>(chunk0) + k;
+    const Cut cut = c >= p.chunks ? Cut{p.n, p.n_rows, false} : find_cut<ACC>(p, c * p.per_chunk);
+    if (lane == 0) cuts[k] = cut;
+  }
+  __syncthreads();
   if (chunk >= p.chunks) return;
   const uint32_t slab = static_cast<uint32_t>(unit - static_cast<uint64_t>(chunk) * p.slabs);
   const uint32_t o = slab * 32 + lane;
   const bool live = 8 * o < p.d;
-  const Cut from = find_cut<ACC>(p, static_cast<uint64_t>(chunk) * p.per_chunk);
-  const Cut to = chunk + 1 == p.chunks
-                     ? Cut{p.n, p.n_rows, false}
-                     : find_cut<ACC>(p, static_cast<uint64_t>(chunk + 1) * p.per_chunk);
+  const Cut from = cuts[chunk - chunk0], to = cuts[chunk - chunk0 + 1];
   uint32_t cur = from.r;          // the row in progress
   bool begun = from.mid;          // whether it has parts in front of this chunk
   bool any = false;               // whether it has lookups in this chunk
@@ -411,7 +466,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(SumParams p) {
   auto advance = [&](uint32_t next) {
     if (begun) {
       head_row = cur;
-      if (live) store_part(p.head + static_cast<uint64_t>(chunk) * p.d, o, p.d, acc);
+      if (live) store_part(p.head + chunk * p.pitch, o, acc);
     } else if (any) {
       if (live) write_row<TG, VG, ACC>(p, cur, o, acc);
     } else if (!ACC) {
@@ -427,45 +482,78 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(SumParams p) {
     for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
   };
 
-  uint32_t i = from.i;
+  // Lookups [i, i + batch) at a time: their ids and places go to shared memory, their dy rows
+  // through a ring of copies to shared memory, kAhead - 1 in flight (copies complete in order,
+  // group by group; register loads would share too few scoreboards to be waited for one by one).  A key of n_rows ends the list.
+  constexpr uint32_t kOctet = 8 * sizeof(TD);
+  const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) +
+                        warp * (kAhead * 32 * kOctet) + lane * kOctet;
+  uint32_t* keys = key_s[warp];
+  uint32_t* places = pos_s[warp];
   bool done = false;
-  while (i < to.i && !done) {
-    const uint32_t batch = to.i - i < 32 ? to.i - i : 32;
-    uint32_t kk = p.n_rows, pp = 0;
-    if (lane < batch) {
-      kk = p.keys[i + lane];
-      pp = p.pos[i + lane];
+  for (uint32_t i = from.i; i < to.i && !done; i += kBatch) {
+    __syncwarp();
+    for (uint32_t k = lane; k < kBatch + kAhead; k += 32) {
+      const bool in = k < kBatch && i + k < to.i;
+      keys[k] = in ? p.keys[i + k] : kFull;
+      places[k] = in ? p.pos[i + k] : 0;
     }
-    for (uint32_t t = 0; t < batch && !done; t += kAhead) {
-      Packed<TD> r[kAhead];
+    __syncwarp();
+    auto fetch = [&](uint32_t k) {
+      if constexpr (VD) {
+        if (live && keys[k] < p.n_rows) {
+          const TD* from = dy + static_cast<uint64_t>(places[k]) * p.dy_stride + 8 * o;
+          const uint32_t slot = mine + k % kAhead * (32 * kOctet);
 #pragma unroll
-      for (uint32_t u = 0; u < kAhead; ++u) {
-        const uint32_t k = __shfl_sync(kFull, kk, t + u);
-        const uint32_t j = __shfl_sync(kFull, pp, t + u);
-        r[u] = live && k < p.n_rows
-                   ? load_row_octet<TD, VD>(dy + static_cast<uint64_t>(j) * p.dy_stride, o, p.d)
-                   : zero_octet<TD>();
-      }
-#pragma unroll
-      for (uint32_t u = 0; u < kAhead; ++u) {
-        const uint32_t k = __shfl_sync(kFull, kk, t + u);
-        if (k >= p.n_rows) {      // past the batch, or an id outside the table: all that follow too
-          if (t + u < batch) done = true;
-        } else {
-          if (k != cur) advance(k);
-          any = true;
-          float v[8];
-          unpack<TD>(r[u], v);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] += v[e];
+          for (uint32_t b = 0; b < kOctet; b += 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + b),
+                         "l"(reinterpret_cast<const uint8_t*>(from) + b)
+                         : "memory");
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
       }
+    };
+#pragma unroll
+    for (uint32_t u = 0; u < kAhead - 1; ++u) fetch(u);
+    for (uint32_t k0 = 0; k0 < kBatch; ++k0) {
+      fetch(k0 + kAhead - 1);
+      const uint32_t k = keys[k0];
+      if (k >= p.n_rows) {              // the chunk's end, or an id outside: all that follow too
+        done = true;
+        break;
+      }
+      if (k != cur) advance(k);
+      any = true;
+      Packed<TD> r;
+      if constexpr (VD) {
+        // the oldest copy has landed; a lane reads what it copied itself
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        const uint4* at = reinterpret_cast<const uint4*>(
+            ring + warp * (kAhead * 32 * kOctet) + k0 % kAhead * (32 * kOctet) + lane * kOctet);
+#pragma unroll
+        for (uint32_t b = 0; b < kOctet / 16; ++b) {
+          const uint4 x = at[b];
+          r.w[4 * b] = x.x;
+          r.w[4 * b + 1] = x.y;
+          r.w[4 * b + 2] = x.z;
+          r.w[4 * b + 3] = x.w;
+        }
+      } else {
+        r = live ? load_row_octet<TD, VD>(
+                       dy + static_cast<uint64_t>(places[k0]) * p.dy_stride, o, p.d)
+                 : zero_octet<TD>();
+      }
+      float v[8];
+      unpack<TD>(r, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += v[e];
     }
-    i += batch;
+    if constexpr (VD) asm volatile("cp.async.wait_all;" ::: "memory");
   }
+  let_next_start();        // (early, the next kernel's waiting CTAs would take this one's place)
   if (to.r > cur) advance(to.r);
   const bool left = any || begun;                 // a part of row `cur` that goes on
-  if (left && to.mid && live) store_part(p.tail + static_cast<uint64_t>(chunk) * p.d, o, p.d, acc);
+  if (left && to.mid && live) store_part(p.tail + chunk * p.pitch, o, acc);
   if (slab == 0 && lane == 0) {
     p.head_row[chunk] = head_row;
     p.end_key[chunk] = 2 * to.r + (left && to.mid ? 1u : 0u);
@@ -483,6 +571,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(SumParams p) {
   __shared__ float part[kJoinThreads / 32][kSlab];
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t o = blockIdx.y * 32 + lane;
+  const bool live = 8 * o < p.d;
+  wait_for_previous();
+  let_next_start();
   for (uint32_t k = 0; k < kJoinChunks; k += 32) {
     const uint32_t c0 = blockIdx.x * kJoinChunks + k;
     const uint32_t mine = c0 + lane < p.chunks ? p.head_row[c0 + lane] : kFull;
@@ -513,23 +604,28 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(SumParams p) {
       float acc[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-#pragma unroll 4
-      for (uint32_t q = q0; q < q1; ++q) {
-        const float* t = p.tail + static_cast<uint64_t>(q) * p.d;
+      if (live) {
+#pragma unroll 8
+        for (uint32_t q = q0; q < q1; ++q) {
+          const float4* from = reinterpret_cast<const float4*>(p.tail + q * p.pitch + 8 * o);
+          const float4 x = from[0], y = from[1];
+          const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (8 * o + e < p.d) acc[e] += t[8 * o + e];
+          for (int e = 0; e < 8; ++e) acc[e] += v[e];
+        }
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) part[warp][lane * 8 + e] = acc[e];
+      *reinterpret_cast<float4*>(&part[warp][lane * 8]) =
+          make_float4(acc[0], acc[1], acc[2], acc[3]);
+      *reinterpret_cast<float4*>(&part[warp][lane * 8 + 4]) =
+          make_float4(acc[4], acc[5], acc[6], acc[7]);
       __syncthreads();
-      if (warp == 0 && 8 * o < p.d) {
+      if (warp == 0 && live) {
+        const float* last = p.head + c * p.pitch + 8 * o;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float s = acc[e];
           for (int w = 1; w < kJoinThreads / 32; ++w) s += part[w][lane * 8 + e];
-          if (8 * o + e < p.d) s += p.head[static_cast<uint64_t>(c) * p.d + 8 * o + e];
-          acc[e] = s;
+          acc[e] = s + last[e];
         }
         write_row<TG, VEC, ACC>(p, row, o, acc);
       }
@@ -557,6 +653,7 @@ Plan plan(uint64_t n, uint64_t n_rows, uint32_t d, bool accumulate) {
   const int widest = n <= kSmallMax ? kSmallBits : kMaxBits;
   w.passes = (nbits + widest - 1) / widest;
   w.bits = (nbits + w.passes - 1) / w.passes;
+  if (w.bits < 2) w.bits = 2;                              // (counts are read four at a time)
   const uint64_t subs = (n + kSub - 1) / kSub;
   const uint64_t per = (subs + kMaxTiles - 1) / kMaxTiles;
   w.per_tile = static_cast<uint32_t>((per == 0 ? 1 : per) * kSub);
@@ -583,12 +680,30 @@ Plan plan(uint64_t n, uint64_t n_rows, uint32_t d, bool accumulate) {
     w.pos[k] = take(4 * n);
   }
   w.counts = take(4ull * w.tiles * kMaxBins);
-  w.head = take(4ull * chunks * d);
-  w.tail = take(4ull * chunks * d);
+  const uint64_t pitch = up(d, 8);
+  w.head = take(4 * chunks * pitch);
+  w.tail = take(4 * chunks * pitch);
   w.head_row = take(4 * chunks);
   w.end_key = take(4 * chunks);
   w.total = at;
   return w;
+}
+
+// Launches a kernel that may start while the one before it on the stream still runs.
+template <typename P>
+cudaError_t launch_after(void (*fn)(P), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                         const P& p) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
 template <typename TD, typename TG, bool ACC>
@@ -599,12 +714,18 @@ cudaError_t launch_sums(const SumParams& p, bool vd, bool vg, cudaStream_t s) {
   auto* fn = vd ? (vg ? &sum_kernel<TD, TG, true, true, ACC> : &sum_kernel<TD, TG, true, false, ACC>)
                 : (vg ? &sum_kernel<TD, TG, false, true, ACC>
                       : &sum_kernel<TD, TG, false, false, ACC>);
-  fn<<<static_cast<unsigned>(blocks), kSumThreads, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  constexpr int kRing = static_cast<int>(kWarps * kAhead * 32 * 8 * sizeof(TD));
+  const size_t smem = vd ? kRing : 0;
+  cudaError_t e = cudaSuccess;
+  if (smem > 32768)
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+  if (e == cudaSuccess)
+    e = launch_after(fn, dim3(static_cast<unsigned>(blocks)), kSumThreads, smem, s, p);
   if (e != cudaSuccess) return e;
   auto* jn = vg ? &join_kernel<TG, true, ACC> : &join_kernel<TG, false, ACC>;
-  jn<<<dim3((p.chunks + kJoinChunks - 1) / kJoinChunks, p.slabs), kJoinThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(jn, dim3((p.chunks + kJoinChunks - 1) / kJoinChunks, p.slabs), kJoinThreads, 0,
+                      s, p);
 }
 
 template <typename TD, typename TG>
@@ -661,9 +782,8 @@ extern "C" cp_status cp_embed_grad(const void* dy, int dy_dtype, uint64_t dy_str
   auto words = [&](uint64_t off) { return reinterpret_cast<uint32_t*>(ws + off); };
   int last = 0;
   cudaError_t e = cudaSuccess;
-  const size_t hist_bytes = (static_cast<size_t>(kSortWarps) << w.bits) * 2;
   if (n != 0 && n <= kSmallMax) {
-    sort_small_kernel<<<1, kSortThreads, hist_bytes, s>>>(
+    sort_small_kernel<<<1, kSmallThreads, (kSmallThreads / 32 << w.bits) * 2, s>>>(
         ids, static_cast<uint32_t>(n), static_cast<uint32_t>(n_rows), w.passes, w.bits,
         words(w.keys[0]), words(w.pos[0]), status);
     e = cudaGetLastError();
@@ -680,11 +800,17 @@ extern "C" cp_status cp_embed_grad(const void* dy, int dy_dtype, uint64_t dy_str
       p.n_rows = static_cast<uint32_t>(n_rows);
       p.per_tile = w.per_tile;
       p.shift = static_cast<uint32_t>(pass * w.bits);
-      p.bits = static_cast<uint32_t>(w.bits);
+      p.bits = w.bits;
       p.status = status;
-      sort_count_kernel<<<w.tiles, kSortThreads, 0, s>>>(p);
-      sort_place_kernel<<<w.tiles, kSortThreads, hist_bytes, s>>>(p);
-      e = cudaGetLastError();
+      if (pass == 0) {
+        sort_count_kernel<<<w.tiles, kSortThreads, 0, s>>>(p);
+        e = cudaGetLastError();
+      } else {
+        e = launch_after(&sort_count_kernel, dim3(w.tiles), kSortThreads, 0, s, p);
+      }
+      if (e == cudaSuccess)
+        e = launch_after(&sort_place_kernel, dim3(w.tiles), kSortThreads,
+                         (kSortThreads / 32 << w.bits) * 2, s, p);
       last = pass & 1;
     }
   }
@@ -704,6 +830,7 @@ extern "C" cp_status cp_embed_grad(const void* dy, int dy_dtype, uint64_t dy_str
   q.scale = scale;
   q.grad = grad;
   q.grad_stride = grad_stride;
+  q.pitch = up(d, 8);
   q.head = reinterpret_cast<float*>(ws + w.head);
   q.tail = reinterpret_cast<float*>(ws + w.tail);
   q.head_row = words(w.head_row);
