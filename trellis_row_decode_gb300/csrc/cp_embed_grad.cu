@@ -25,6 +25,7 @@
 #include "cp.h"
 #include "cp_internal.h"
 #include "cp_layer.cuh"
+#include "cp_tcgen05.cuh"
 
 namespace {
 
@@ -81,10 +82,9 @@ __device__ __forceinline__ void exclusive_scan(uint32_t* v, uint32_t bins, uint3
     if (lane == 31) warp_sums[warp] = x;
   }
   __syncthreads();
-  if (threadIdx.x < bins) {
-    uint32_t before = 0;
-    for (uint32_t w = 0; w < warp; ++w) before += warp_sums[w];
-    v[threadIdx.x] = before + x - own;
+  if (threadIdx.x < kMaxBins) {
+    const uint32_t before = __reduce_add_sync(kFull, lane < warp ? warp_sums[lane] : 0);
+    if (threadIdx.x < bins) v[threadIdx.x] = before + x - own;
   }
   __syncthreads();
 }
@@ -137,8 +137,7 @@ __device__ __forceinline__ Ranks rank_digits(const uint32_t (&digit)[kRounds], i
 // Up to kSmallMax ids in one CTA: all passes in shared memory.
 __global__ void __launch_bounds__(kSmallThreads)
     sort_small_kernel(const int64_t* __restrict__ ids, uint32_t n, uint32_t n_rows, int passes,
-                      int bits, uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out,
-                      uint32_t* status) {
+                      int bits, uint2* __restrict__ pairs_out, uint32_t* status) {
   __shared__ uint32_t key_s[kSmallMax];
   __shared__ uint16_t pos_s[kSmallMax];
   extern __shared__ uint16_t hist[];             // [warps][bins]
@@ -170,39 +169,40 @@ __global__ void __launch_bounds__(kSmallThreads)
     for (int r = 0; r < kRounds; ++r) {
       if (digit[r] < bins) {
         const uint32_t to = total[digit[r]] + hist[warp * bins + digit[r]] + rk.r[r];
-        if (p + 1 == passes) {
-          keys_out[to] = key[r];
-          pos_out[to] = pos[r];
-        } else {
-          key_s[to] = key[r];
-          pos_s[to] = static_cast<uint16_t>(pos[r]);
-        }
+        key_s[to] = key[r];
+        pos_s[to] = static_cast<uint16_t>(pos[r]);
       }
     }
     __syncthreads();
-    if (p + 1 < passes) {
 #pragma unroll
-      for (int r = 0; r < kRounds; ++r) {
-        const uint32_t i = warp * (32 * kRounds) + r * 32 + lane;
-        if (i < n) {
-          key[r] = key_s[i];
-          pos[r] = pos_s[i];
-        } else {
-          pos[r] = kFull;                        // no key: stays out of every digit
-        }
+    for (int r = 0; r < kRounds; ++r) {
+      const uint32_t i = warp * (32 * kRounds) + r * 32 + lane;
+      if (i < n) {
+        key[r] = key_s[i];
+        pos[r] = pos_s[i];
+      } else {
+        pos[r] = kFull;                          // no key: stays out of every digit
       }
     }
     __syncthreads();
   }
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const uint32_t i = warp * (32 * kRounds) + r * 32 + lane;
+    if (i < n) pairs_out[i] = make_uint2(key[r], pos[r]);
+  }
 }
+
+// Counts are kept at two levels, so that placing a tile reads few of them: a cluster of
+// kTileCluster tiles adds up its tiles' counts through distributed shared memory.
+constexpr uint32_t kTileCluster = 8;
 
 struct SortPass {
   const int64_t* ids;            // first pass: the ids; else null
-  const uint32_t* keys;          // later passes: pairs of the pass before
-  const uint32_t* pos;
-  uint32_t* keys_out;
-  uint32_t* pos_out;
-  uint32_t* counts;              // [tiles][bins]
+  const uint2* pairs;            // later passes: (key, position) of the pass before
+  uint2* pairs_out;
+  uint32_t* counts;              // [tiles][bins]: keys in the earlier tiles of the tile's cluster
+  uint32_t* totals;              // [clusters][bins]: keys of a cluster
   uint32_t n, n_rows, per_tile;  // per_tile: a multiple of kSub
   uint32_t shift;
   int bits;
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortPass p) {
       const uint64_t i = i0 + r * kSortThreads + threadIdx.x;
       key[r] = kFull;
       if (i < hi) {
-        key[r] = p.ids != nullptr ? key_of(p.ids[i], p.n_rows) : p.keys[i];
+        key[r] = p.ids != nullptr ? key_of(p.ids[i], p.n_rows) : p.pairs[i].x;
         bad |= key[r] == p.n_rows;
       }
     }
@@ -235,9 +235,23 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortPass p) {
       if (key[r] != kFull) atomicAdd(&hist[(key[r] >> p.shift) & (bins - 1)], 1u);
   }
   if (p.ids != nullptr && p.status != nullptr && bad) atomicOr(p.status, 1u);
-  __syncthreads();
-  for (uint32_t b = threadIdx.x; b < bins; b += kSortThreads)
-    p.counts[blockIdx.x * bins + b] = hist[b];
+  cpt::cluster_sync();
+  const uint32_t rank = blockIdx.x % kTileCluster;
+  for (uint32_t b = threadIdx.x; b < bins; b += kSortThreads) {
+    const uint32_t at = cpt::smem_addr(hist + b);
+    uint32_t c[kTileCluster], before = 0, all = 0;
+#pragma unroll
+    for (uint32_t q = 0; q < kTileCluster; ++q)
+      asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(c[q]) : "r"(cpt::map_rank(at, q)));
+#pragma unroll
+    for (uint32_t q = 0; q < kTileCluster; ++q) {
+      before += q < rank ? c[q] : 0;
+      all += c[q];
+    }
+    p.counts[blockIdx.x * bins + b] = before;
+    if (rank == 0) p.totals[blockIdx.x / kTileCluster * bins + b] = all;
+  }
+  cpt::cluster_sync();               // no CTA leaves while another may read its counts
 }
 
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortPass p) {
@@ -245,40 +259,41 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortPass p) {
   __shared__ uint32_t total[kMaxBins], warp_sums[32];
   __shared__ uint32_t base[kMaxBins];            // where this tile's next key of a digit goes
   __shared__ uint4 part[kSortThreads], part_all[kSortThreads];
-  const uint32_t bins = 1u << p.bits, tiles = gridDim.x, tile = blockIdx.x;
+  const uint32_t bins = 1u << p.bits, tile = blockIdx.x;
+  const uint32_t clusters = gridDim.x / kTileCluster, cluster = tile / kTileCluster;
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   wait_for_previous();
   let_next_start();
   const uint64_t lo = static_cast<uint64_t>(tile) * p.per_tile;
   const uint64_t hi = lo + p.per_tile < p.n ? lo + p.per_tile : p.n;
-  uint32_t key[kRounds], pos[kRounds];
-  auto load_keys = [&](uint64_t i0) {
+  uint2 pair[kRounds];
+  auto load_pairs = [&](uint64_t i0) {
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
       const uint64_t i = i0 + warp * (32 * kRounds) + r * 32 + lane;
-      key[r] = pos[r] = kFull;
-      if (i < hi) {
-        key[r] = p.ids != nullptr ? key_of(p.ids[i], p.n_rows) : p.keys[i];
-        pos[r] = p.ids != nullptr ? static_cast<uint32_t>(i) : p.pos[i];
-      }
+      pair[r] = make_uint2(kFull, kFull);
+      if (i < hi)
+        pair[r] = p.ids != nullptr
+                      ? make_uint2(key_of(p.ids[i], p.n_rows), static_cast<uint32_t>(i))
+                      : p.pairs[i];
     }
   };
-  load_keys(lo);
-  // Counts of each digit before this tile and in all tiles: bins / 4 threads read a tile's
-  // counts four at a time, and the thread groups share the tiles.
+  load_pairs(lo);
+  // Counts of each digit in the clusters before this one and in all: bins / 4 threads read a
+  // cluster's counts four at a time, and the thread groups share the clusters.
   {
     const uint32_t per = bins / 4, groups = kSortThreads / per;       // bins >= 4
     const uint32_t g = threadIdx.x / per, q = threadIdx.x - g * per;
     uint4 before = make_uint4(0, 0, 0, 0), all = before;
     if (g < groups) {
-#pragma unroll 8
-      for (uint32_t t = g; t < tiles; t += groups) {
-        const uint4 c = *reinterpret_cast<const uint4*>(p.counts + t * bins + 4 * q);
+#pragma unroll 4
+      for (uint32_t t = g; t < clusters; t += groups) {
+        const uint4 c = *reinterpret_cast<const uint4*>(p.totals + t * bins + 4 * q);
         all.x += c.x;
         all.y += c.y;
         all.z += c.z;
         all.w += c.w;
-        if (t < tile) {
+        if (t < cluster) {
           before.x += c.x;
           before.y += c.y;
           before.z += c.z;
@@ -288,38 +303,36 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortPass p) {
     }
     part[threadIdx.x] = before;
     part_all[threadIdx.x] = all;
+    uint32_t own = 0;
+    if (threadIdx.x < bins) own = p.counts[tile * bins + threadIdx.x];
     __syncthreads();
     const uint32_t* parts = reinterpret_cast<const uint32_t*>(part);
     const uint32_t* parts_all = reinterpret_cast<const uint32_t*>(part_all);
-    for (uint32_t i = threadIdx.x; i < bins; i += kSortThreads) {
-      uint32_t x = 0, y = 0;
+    static_assert(kMaxBins <= kSortThreads, "a thread per bin");
+    if (threadIdx.x < bins) {
+      uint32_t y = 0;
       for (uint32_t k = 0; k < groups; ++k) {
-        x += parts[k * bins + i];
-        y += parts_all[k * bins + i];
+        own += parts[k * bins + threadIdx.x];
+        y += parts_all[k * bins + threadIdx.x];
       }
-      base[i] = x;
-      total[i] = y;
+      total[threadIdx.x] = y;
     }
     __syncthreads();
     exclusive_scan(total, bins, warp_sums);
-    for (uint32_t i = threadIdx.x; i < bins; i += kSortThreads) base[i] += total[i];
+    if (threadIdx.x < bins) base[threadIdx.x] = own + total[threadIdx.x];
     __syncthreads();
   }
   for (uint64_t i0 = lo; i0 < hi; i0 += kSub) {
-    if (i0 != lo) load_keys(i0);
+    if (i0 != lo) load_pairs(i0);
     uint32_t digit[kRounds];
 #pragma unroll
     for (int r = 0; r < kRounds; ++r)
-      digit[r] = pos[r] != kFull ? (key[r] >> p.shift) & (bins - 1) : bins;
+      digit[r] = pair[r].y != kFull ? (pair[r].x >> p.shift) & (bins - 1) : bins;
     const Ranks rk = rank_digits<kSortThreads>(digit, p.bits, hist, total);
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-      if (digit[r] < bins) {
-        const uint32_t to = base[digit[r]] + hist[warp * bins + digit[r]] + rk.r[r];
-        p.keys_out[to] = key[r];
-        p.pos_out[to] = pos[r];
-      }
-    }
+    for (int r = 0; r < kRounds; ++r)
+      if (digit[r] < bins)
+        p.pairs_out[base[digit[r]] + hist[warp * bins + digit[r]] + rk.r[r]] = pair[r];
     __syncthreads();
     for (uint32_t b = threadIdx.x; b < bins; b += kSortThreads) base[b] += total[b];
     __syncthreads();
@@ -335,8 +348,7 @@ constexpr uint32_t kBatch = 128;                 // lookups whose ids a warp sta
 constexpr uint32_t kWarps = kSumThreads / 32;
 
 struct SumParams {
-  const uint32_t* keys;          // sorted; n_rows for ids outside the table
-  const uint32_t* pos;
+  const uint2* pairs;            // (id, position), sorted; id n_rows for those outside the table
   uint32_t n, n_rows, d, slabs, chunks, per_chunk;
   const void* dy;
   uint64_t dy_stride;
@@ -374,7 +386,7 @@ __device__ __forceinline__ Cut find_cut(const SumParams& p, uint64_t diag) {
     while (lo < hi) {
       const uint64_t step = (hi - lo + 32) / 33;
       const uint64_t at = lo + step * (lane + 1) - 1;        // probes lo+step-1, lo+2step-1, ..
-      const bool past = at >= hi || p.keys[at] >= diag - at;
+      const bool past = at >= hi || p.pairs[at].x >= diag - at;
       const uint32_t first = __ffs(__ballot_sync(kFull, past));
       if (first == 0) {
         lo = lo + step * 32;
@@ -386,17 +398,19 @@ __device__ __forceinline__ Cut find_cut(const SumParams& p, uint64_t diag) {
     }
     c.i = static_cast<uint32_t>(lo);
   }
-  c.r = ACC ? (c.i < p.n ? p.keys[c.i] : p.n_rows) : static_cast<uint32_t>(diag - c.i);
+  c.r = ACC ? (c.i < p.n ? p.pairs[c.i].x : p.n_rows) : static_cast<uint32_t>(diag - c.i);
   c.mid = false;
-  if (c.r < p.n_rows && c.i > 0 && p.keys[c.i - 1] == c.r) {
-    const uint32_t at = c.i + lane;
-    const bool other = at >= p.n || p.keys[at] != c.r;
+  const uint32_t at = c.i + lane;                // (both loads at once: they only depend on c.i)
+  const uint32_t in_front = c.i > 0 ? p.pairs[c.i - 1].x : kFull;
+  const uint32_t behind = at < p.n ? p.pairs[at].x : kFull;
+  if (c.r < p.n_rows && in_front == c.r) {
+    const bool other = behind != c.r;
     const uint32_t first = __ffs(__ballot_sync(kFull, other));
     if (first == 0) {
       c.mid = true;
     } else {
       c.i += first - 1;
-      c.r = ACC ? (c.i < p.n ? p.keys[c.i] : p.n_rows) : c.r + 1;
+      c.r = ACC ? (c.i < p.n ? p.pairs[c.i].x : p.n_rows) : c.r + 1;
     }
   }
   return c;
@@ -495,8 +509,9 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(SumParams p) {
     __syncwarp();
     for (uint32_t k = lane; k < kBatch + kAhead; k += 32) {
       const bool in = k < kBatch && i + k < to.i;
-      keys[k] = in ? p.keys[i + k] : kFull;
-      places[k] = in ? p.pos[i + k] : 0;
+      const uint2 pair = in ? p.pairs[i + k] : make_uint2(kFull, 0);
+      keys[k] = pair.x;
+      places[k] = pair.y;
     }
     __syncwarp();
     auto fetch = [&](uint32_t k) {
@@ -561,7 +576,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(SumParams p) {
 }
 
 constexpr int kJoinThreads = 256;
-constexpr uint32_t kJoinChunks = 64;             // chunks that a CTA looks through
+constexpr uint32_t kJoinChunks = 8;              // chunks that a CTA looks through
 
 // Rows that span chunks: chunk c holds the last part, the chunks in front of it the
 // earlier ones, from the one where the row began.  Eight warps take a contiguous share
@@ -573,10 +588,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(SumParams p) {
   const uint32_t o = blockIdx.y * 32 + lane;
   const bool live = 8 * o < p.d;
   wait_for_previous();
-  let_next_start();
-  for (uint32_t k = 0; k < kJoinChunks; k += 32) {
-    const uint32_t c0 = blockIdx.x * kJoinChunks + k;
-    const uint32_t mine = c0 + lane < p.chunks ? p.head_row[c0 + lane] : kFull;
+  {
+    const uint32_t c0 = blockIdx.x * kJoinChunks;
+    const uint32_t mine =
+        lane < kJoinChunks && c0 + lane < p.chunks ? p.head_row[c0 + lane] : kFull;
     uint32_t todo = __ballot_sync(kFull, mine != kFull);
     while (todo != 0) {
       const uint32_t b = __ffs(todo) - 1;
@@ -636,13 +651,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(SumParams p) {
 
 // ------------------------------------------------------------------------- host
 
-uint64_t up(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
+constexpr uint64_t up(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
 
 struct Plan {
   int passes, bits;
   uint32_t tiles, per_tile;
   uint32_t chunks, per_chunk;
-  uint64_t keys[2], pos[2], counts, head, tail, head_row, end_key, total;
+  uint64_t pairs[2], counts, totals, head, tail, head_row, end_key, total;
 };
 
 // Workspace of a call; accumulate or not, the larger list's chunks are planned for.
@@ -657,7 +672,7 @@ Plan plan(uint64_t n, uint64_t n_rows, uint32_t d, bool accumulate) {
   const uint64_t subs = (n + kSub - 1) / kSub;
   const uint64_t per = (subs + kMaxTiles - 1) / kMaxTiles;
   w.per_tile = static_cast<uint32_t>((per == 0 ? 1 : per) * kSub);
-  w.tiles = static_cast<uint32_t>((n + w.per_tile - 1) / w.per_tile);
+  w.tiles = static_cast<uint32_t>(up((n + w.per_tile - 1) / w.per_tile, kTileCluster));
   const uint64_t items = accumulate ? n : n + n_rows;
   // A chunk of 64 items when there are enough of them to fill the warps, down to 16
   // when there are few (their latency counts); more when there are so many that the
@@ -675,11 +690,9 @@ Plan plan(uint64_t n, uint64_t n_rows, uint32_t d, bool accumulate) {
     at += up(bytes, 256);
     return here;
   };
-  for (int k = 0; k < 2; ++k) {
-    w.keys[k] = take(4 * n);
-    w.pos[k] = take(4 * n);
-  }
+  for (int k = 0; k < 2; ++k) w.pairs[k] = take(8 * n);
   w.counts = take(4ull * w.tiles * kMaxBins);
+  w.totals = take(4ull * w.tiles / kTileCluster * kMaxBins);
   const uint64_t pitch = up(d, 8);
   w.head = take(4 * chunks * pitch);
   w.tail = take(4 * chunks * pitch);
@@ -689,20 +702,30 @@ Plan plan(uint64_t n, uint64_t n_rows, uint32_t d, bool accumulate) {
   return w;
 }
 
-// Launches a kernel that may start while the one before it on the stream still runs.
+// Launches a kernel that may start while the one before it on the stream still runs (`overlap`),
+// its CTAs in clusters of `cluster`.
 template <typename P>
 cudaError_t launch_after(void (*fn)(P), dim3 grid, int threads, size_t smem, cudaStream_t s,
-                         const P& p) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+                         const P& p, uint32_t cluster = 1, bool overlap = true) {
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (overlap) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
@@ -723,6 +746,7 @@ cudaError_t launch_sums(const SumParams& p, bool vd, bool vg, cudaStream_t s) {
   if (e == cudaSuccess)
     e = launch_after(fn, dim3(static_cast<unsigned>(blocks)), kSumThreads, smem, s, p);
   if (e != cudaSuccess) return e;
+  if (p.n <= 32) return e;       // a row spans chunks only with a lookup in front of a cut and 32 behind it
   auto* jn = vg ? &join_kernel<TG, true, ACC> : &join_kernel<TG, false, ACC>;
   return launch_after(jn, dim3((p.chunks + kJoinChunks - 1) / kJoinChunks, p.slabs), kJoinThreads, 0,
                       s, p);
@@ -779,35 +803,31 @@ extern "C" cp_status cp_embed_grad(const void* dy, int dy_dtype, uint64_t dy_str
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  auto pairs = [&](uint64_t off) { return reinterpret_cast<uint2*>(ws + off); };
   auto words = [&](uint64_t off) { return reinterpret_cast<uint32_t*>(ws + off); };
   int last = 0;
   cudaError_t e = cudaSuccess;
   if (n != 0 && n <= kSmallMax) {
     sort_small_kernel<<<1, kSmallThreads, (kSmallThreads / 32 << w.bits) * 2, s>>>(
         ids, static_cast<uint32_t>(n), static_cast<uint32_t>(n_rows), w.passes, w.bits,
-        words(w.keys[0]), words(w.pos[0]), status);
+        pairs(w.pairs[0]), status);
     e = cudaGetLastError();
   } else if (n != 0) {
     for (int pass = 0; pass < w.passes && e == cudaSuccess; ++pass) {
       SortPass p;
       p.ids = pass == 0 ? ids : nullptr;
-      p.keys = words(w.keys[(pass + 1) & 1]);
-      p.pos = words(w.pos[(pass + 1) & 1]);
-      p.keys_out = words(w.keys[pass & 1]);
-      p.pos_out = words(w.pos[pass & 1]);
+      p.pairs = pairs(w.pairs[(pass + 1) & 1]);
+      p.pairs_out = pairs(w.pairs[pass & 1]);
       p.counts = words(w.counts);
+      p.totals = words(w.totals);
       p.n = static_cast<uint32_t>(n);
       p.n_rows = static_cast<uint32_t>(n_rows);
       p.per_tile = w.per_tile;
       p.shift = static_cast<uint32_t>(pass * w.bits);
       p.bits = w.bits;
       p.status = status;
-      if (pass == 0) {
-        sort_count_kernel<<<w.tiles, kSortThreads, 0, s>>>(p);
-        e = cudaGetLastError();
-      } else {
-        e = launch_after(&sort_count_kernel, dim3(w.tiles), kSortThreads, 0, s, p);
-      }
+      e = launch_after(&sort_count_kernel, dim3(w.tiles), kSortThreads, 0, s, p, kTileCluster,
+                       pass != 0);
       if (e == cudaSuccess)
         e = launch_after(&sort_place_kernel, dim3(w.tiles), kSortThreads,
                          (kSortThreads / 32 << w.bits) * 2, s, p);
@@ -817,8 +837,7 @@ extern "C" cp_status cp_embed_grad(const void* dy, int dy_dtype, uint64_t dy_str
   if (e != cudaSuccess) return cpx::cuda_fail(e, "embed gradient sort");
   if (n_rows == 0) return CP_OK;
   SumParams q{};
-  q.keys = words(w.keys[last]);
-  q.pos = words(w.pos[last]);
+  q.pairs = pairs(w.pairs[last]);
   q.n = static_cast<uint32_t>(n);
   q.n_rows = static_cast<uint32_t>(n_rows);
   q.d = d;

@@ -6,7 +6,9 @@
 // Read once, written once: a block's values stay in registers between its largest
 // magnitude and the conversion.  Blocks of one row: 16 lanes hold a group of 128
 // columns, a half warp takes four groups at a time so that four loads are in flight.
-// Blocks of 128 rows: one CTA holds the 128 x 128 block, eight octets a thread.
+// Blocks of 128 rows: one CTA holds the 128 x 128 block, eight octets a thread.  Four such CTAs
+// an SM for 16-bit inputs (64 registers): 4096 x 24576 bf16 takes 47 us (6.4 TB/s), against 60 us
+// with three; with five the registers spill (56 us).
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -58,7 +60,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
     quantize_block_kernel(const T* __restrict__ x, uint64_t stride, uint64_t rows, uint32_t d,
                           uint32_t per_row, uint8_t* __restrict__ q, float* __restrict__ scales) {
   __shared__ uint32_t red[kThreads / 32];
