@@ -390,7 +390,7 @@ cp_status cp_embed(const void* weight, int dtype, uint64_t n_rows, uint32_t d,
 
 /*
  * cp_embed_grad -- the gradient of cp_embed by its table:
- *   sum[r][q] = sum of dy[j][q] over the j with ids[j] = r       (fp32)
+ *   sum[r][q] = sum of dy[j / group][q] over the j with ids[j] = r       (fp32)
  *   accumulate = 0: grad[r] = rn(scale * sum[r]) for every row, zeros for the
  *                   rows that no id names;
  *   accumulate = 1: grad[r] = rn(grad[r] + scale * sum[r]) for the rows that ids
@@ -399,7 +399,10 @@ cp_status cp_embed(const void* weight, int dtype, uint64_t n_rows, uint32_t d,
  * The ids are sorted (stably, so each row sums its lookups in an order fixed by
  * the ids), and rows and lookups are dealt evenly to the warps, so neither a hot
  * row nor a table of untouched rows holds one of them up.
- *   dy       [n][d] of dy_dtype, row stride dy_stride >= d.
+ *   group    lookups that share a row of dy (1: one each; a sum over groups of
+ *            lookups, as cp_lookup_decode_reduce makes, has one gradient row per
+ *            group); n is a multiple of it.
+ *   dy       [n / group][d] of dy_dtype, row stride dy_stride >= d.
  *   ids      n int64; ids outside [0, n_rows) are left out (bit 0 of status).
  *   grad     [n_rows][d] of grad_dtype, row stride grad_stride >= d.
  *   workspace  cp_embed_grad_workspace_bytes(n, n_rows, d) bytes, 16-byte aligned.
@@ -407,9 +410,10 @@ cp_status cp_embed(const void* weight, int dtype, uint64_t n_rows, uint32_t d,
  */
 uint64_t cp_embed_grad_workspace_bytes(uint64_t n, uint64_t n_rows, uint32_t d);
 cp_status cp_embed_grad(const void* dy, int dy_dtype, uint64_t dy_stride, const int64_t* ids,
-                        uint64_t n, uint64_t n_rows, uint32_t d, float scale, int accumulate,
-                        void* grad, int grad_dtype, uint64_t grad_stride, uint32_t* status,
-                        void* workspace, uint64_t workspace_bytes, void* stream);
+                        uint64_t n, uint32_t group, uint64_t n_rows, uint32_t d, float scale,
+                        int accumulate, void* grad, int grad_dtype, uint64_t grad_stride,
+                        uint32_t* status, void* workspace, uint64_t workspace_bytes,
+                        void* stream);
 
 /*
  * cp_rms_norm -- root-mean-square norm with the residual's addition:

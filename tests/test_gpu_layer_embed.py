@@ -172,6 +172,21 @@ def test_embed_grad_accumulate(n_rows, d, n, kind, dtype):
     assert torch.equal(out.cpu()[same], base[same])
 
 
+@pytest.mark.parametrize("group,d", [(2, 64), (24, 256), (7, 33)])
+def test_embed_grad_of_groups(group, d):
+    """The gradient of sums over groups of lookups: one row of dy per group, as if repeated."""
+    g = gen(group)
+    t, n_rows = 300, 500
+    ids = _ids(g, t * group, n_rows, "holes").view(t, group)
+    dy = randn(g, t, d, dtype=torch.bfloat16)
+    got = cp.embed_grad(dy.cuda(), ids.cuda(), n_rows, 0.5, dtype=torch.float32, group=group)
+    whole = dy.repeat_interleave(group, 0)
+    same = cp.embed_grad(whole.cuda(), ids.view(-1).cuda(), n_rows, 0.5, dtype=torch.float32)
+    assert torch.equal(got, same)
+    ref, mags, count = embed_grad64(whole, ids.view(-1), n_rows, 0.5)
+    assert_within(got, ref, (count[:, None] + 2) * U32 * mags + rounded(ref, torch.float32))
+
+
 def test_embed_grad_empty_and_status():
     out = torch.full((5, 8), 2.0, device="cuda")
     none = torch.empty(0, dtype=torch.int64, device="cuda")
@@ -262,6 +277,8 @@ def test_embed_refusals():
         lambda: cp.embed(w, ids, out=torch.zeros(1, 16, device="cuda").expand(4, 16)),
         lambda: cp.embed(w, ids, status=torch.zeros(1, device="cuda")),
         lambda: cp.embed_grad(dy[:3], ids, 10),
+        lambda: cp.embed_grad(dy, ids, 10, group=2),
+        lambda: cp.embed_grad(dy, ids, 10, group=0),
         lambda: cp.embed_grad(dy, ids, 10, accumulate=True),
         lambda: cp.embed_grad(dy, ids, 10, dtype=torch.float64),
         lambda: cp.embed_grad(dy, ids, 10, out=torch.zeros(9, 16, device="cuda")),

@@ -40,15 +40,15 @@ def test_embed_arguments(L, p):
 
 def test_embed_grad_arguments(L, p):
     big = 1 << 30
-    ok = dict(dy=p, t=0, ds=8, ids=p, n=2, rows=4, d=8, acc=0, g=p, gt=0, gs=8, st=None, ws=p,
+    ok = dict(dy=p, t=0, ds=8, ids=p, n=2, grp=1, rows=4, d=8, acc=0, g=p, gt=0, gs=8, st=None, ws=p,
               wb=big)
 
     def call(**kw):
         a = {**ok, **kw}
-        return L.cp_embed_grad(a["dy"], a["t"], a["ds"], a["ids"], a["n"], a["rows"], a["d"], 1.0,
-                               a["acc"], a["g"], a["gt"], a["gs"], a["st"], a["ws"], a["wb"], None)
+        return L.cp_embed_grad(a["dy"], a["t"], a["ds"], a["ids"], a["n"], a["grp"], a["rows"], a["d"],
+                               1.0, a["acc"], a["g"], a["gt"], a["gs"], a["st"], a["ws"], a["wb"], None)
     for kw in [dict(t=5), dict(gt=9), dict(d=0), dict(ds=7), dict(gs=7), dict(gs=0),
-               dict(n=1 << 31), dict(rows=1 << 31), dict(acc=2), dict(dy=None), dict(ids=None),
+               dict(n=1 << 31), dict(rows=1 << 31), dict(acc=2), dict(grp=0), dict(grp=3), dict(dy=None), dict(ids=None),
                dict(g=None), dict(dy=p + 2), dict(g=p + 1), dict(ids=p + 4), dict(ws=None),
                dict(ws=p + 8), dict(wb=16)]:
         assert call(**kw) == BAD, kw

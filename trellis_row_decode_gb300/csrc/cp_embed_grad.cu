@@ -1,7 +1,7 @@
 // cp_embed_grad.cu -- gradient of a table lookup by sorted ids (include/cp.h,
 // cp_embed_grad).
 //
-//   grad[r] = scale * sum of dy[j] over the j with ids[j] = r
+//   grad[r] = scale * sum of dy[j / group] over the j with ids[j] = r
 //
 // 1. Sort.  (id, position) pairs are sorted stably by id with a radix sort: a
 //    kernel counts digits per tile, the next places every pair (its digit's base,
@@ -350,6 +350,7 @@ constexpr uint32_t kWarps = kSumThreads / 32;
 struct SumParams {
   const uint2* pairs;            // (id, position), sorted; id n_rows for those outside the table
   uint32_t n, n_rows, d, slabs, chunks, per_chunk;
+  uint32_t group;                // lookups that share a row of dy
   const void* dy;
   uint64_t dy_stride;
   float scale;
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(SumParams p) {
       const bool in = k < kBatch && i + k < to.i;
       const uint2 pair = in ? p.pairs[i + k] : make_uint2(kFull, 0);
       keys[k] = pair.x;
-      places[k] = pair.y;
+      places[k] = p.group == 1 ? pair.y : pair.y / p.group;
     }
     __syncwarp();
     auto fetch = [&](uint32_t k) {
@@ -778,13 +779,14 @@ extern "C" uint64_t cp_embed_grad_workspace_bytes(uint64_t n, uint64_t n_rows, u
 }
 
 extern "C" cp_status cp_embed_grad(const void* dy, int dy_dtype, uint64_t dy_stride,
-                                   const int64_t* ids, uint64_t n, uint64_t n_rows, uint32_t d,
-                                   float scale, int accumulate, void* grad, int grad_dtype,
+                                   const int64_t* ids, uint64_t n, uint32_t group, uint64_t n_rows,
+                                   uint32_t d, float scale, int accumulate, void* grad, int grad_dtype,
                                    uint64_t grad_stride, uint32_t* status, void* workspace,
                                    uint64_t workspace_bytes, void* stream) {
   if (!dtype_ok(dy_dtype) || !dtype_ok(grad_dtype) || !sizes_ok(n, n_rows, d) ||
-      (dy_stride < d && dy_stride != 0) || grad_stride < d || (accumulate != 0 && accumulate != 1)) {
-    cpx::set_error("bad dtype, n, n_rows, d, row stride or accumulate");
+      (dy_stride < d && dy_stride != 0) || grad_stride < d || (accumulate != 0 && accumulate != 1) ||
+      group == 0 || n % group != 0) {
+    cpx::set_error("bad dtype, n, group, n_rows, d, row stride or accumulate");
     return CP_ERR_INVALID_ARG;
   }
   if (n_rows == 0 && n == 0) return CP_OK;
@@ -844,6 +846,7 @@ extern "C" cp_status cp_embed_grad(const void* dy, int dy_dtype, uint64_t dy_str
   q.slabs = (d + kSlab - 1) / kSlab;
   q.chunks = w.chunks;
   q.per_chunk = w.per_chunk;
+  q.group = group;
   q.dy = dy;
   q.dy_stride = dy_stride;
   q.scale = scale;

@@ -40,8 +40,8 @@ def _lib():
         L.cp_embed.argtypes = [vp, i32, u64, u32, u64, vp, u64, f32, vp, u64, vp, vp]
         L.cp_embed_grad_workspace_bytes.argtypes = [u64, u64, u32]
         L.cp_embed_grad_workspace_bytes.restype = u64
-        L.cp_embed_grad.argtypes = [vp, i32, u64, vp, u64, u64, u32, f32, i32, vp, i32, u64, vp,
-                                    vp, u64, vp]
+        L.cp_embed_grad.argtypes = [vp, i32, u64, vp, u64, u32, u64, u32, f32, i32, vp, i32, u64,
+                                    vp, vp, u64, vp]
         L.cp_rms_norm.argtypes = [vp, u64, vp, u64, i32, vp, i32, u64, u32, f32, vp, vp, vp]
         L.cp_rms_norm_fp8.argtypes = [vp, u64, vp, u64, i32, vp, i32, u64, u32, f32, vp, vp, vp,
                                       vp]
@@ -202,19 +202,22 @@ def embed_grad_workspace(n: int, n_rows: int, d: int) -> torch.Tensor:
 
 def embed_grad(dy: torch.Tensor, ids: torch.Tensor, n_rows: int, scale: float = 1.0,
                dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
-               accumulate: bool = False, status: torch.Tensor | None = None,
+               accumulate: bool = False, group: int = 1, status: torch.Tensor | None = None,
                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The gradient of embed by its table: [n_rows, d], row r = scale * the sum of dy over
     the lookups of r (fp32, in an order fixed by the ids), in `dtype` (default: dy's).
+
+    dy has a row per lookup, or, with `group`, one for each `group` consecutive lookups (the
+    gradient of their sum).
 
     accumulate=True adds to `out` instead of overwriting it and touches only the rows that
     ids name (with scale = -rate: a step of gradient descent on the table `out`)."""
     code = _float(dy.dtype, "dy")
     dev = _device(dy, "dy")
     n = _ids(ids)
-    _, d, dy_stride = _rows(dy, "dy")
-    if dy.shape != ids.shape + (d,):
-        raise ValueError("dy must be ids.shape + (d,)")
+    rows, d, dy_stride = _rows(dy, "dy")
+    if group < 1 or rows * group != n:
+        raise ValueError("dy must have one row for each `group` ids")
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
@@ -229,8 +232,8 @@ def embed_grad(dy: torch.Tensor, ids: torch.Tensor, n_rows: int, scale: float = 
     L = _lib()
     nbytes = L.cp_embed_grad_workspace_bytes(n, n_rows, d)
     ws = _workspace(workspace, nbytes, dy, dev, stream)
-    _check(L.cp_embed_grad(dy.data_ptr(), code, dy_stride, _on(ids, dev, "ids"), n, n_rows, d,
-                           scale, 1 if accumulate else 0, out.data_ptr(), out_code, out_stride,
+    _check(L.cp_embed_grad(dy.data_ptr(), code, dy_stride, _on(ids, dev, "ids"), n, group, n_rows,
+                           d, scale, 1 if accumulate else 0, out.data_ptr(), out_code, out_stride,
                            _status_ptr(status, dev), ws.data_ptr(), ws.numel(),
                            _stream(stream, dev)), "cp_embed_grad")
     return out
