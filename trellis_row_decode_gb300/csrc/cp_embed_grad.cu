@@ -33,15 +33,6 @@ using namespace cpl;
 
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
-// Kernels of one call run in order; each is launched while the one before it still runs
-// (programmatic dependent launch) and waits, in hardware, for its results here.
-__device__ __forceinline__ void wait_for_previous() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-__device__ __forceinline__ void let_next_start() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // ------------------------------------------------------------------------ sort
 
 constexpr int kRounds = 4;                                   // keys per thread and sub-tile
@@ -701,33 +692,6 @@ Plan plan(uint64_t n, uint64_t n_rows, uint32_t d, bool accumulate) {
   w.end_key = take(4 * chunks);
   w.total = at;
   return w;
-}
-
-// Launches a kernel that may start while the one before it on the stream still runs (`overlap`),
-// its CTAs in clusters of `cluster`.
-template <typename P>
-cudaError_t launch_after(void (*fn)(P), dim3 grid, int threads, size_t smem, cudaStream_t s,
-                         const P& p, uint32_t cluster = 1, bool overlap = true) {
-  cudaLaunchAttribute attr[2];
-  int n = 0;
-  if (overlap) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  if (cluster > 1) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = cluster;
-    attr[n].val.clusterDim.y = 1;
-    attr[n++].val.clusterDim.z = 1;
-  }
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
 template <typename TD, typename TG, bool ACC>

@@ -335,6 +335,7 @@ __global__ void __launch_bounds__(cta_threads(THREADS), grad_ctas_per_sm(THREADS
     }
     fetch_res(row + step);
   }
+  let_next_start();
   float* part = p.parts + static_cast<uint64_t>(blockIdx.x) * p.d;
   if constexpr (kTeams == 1) {
 #pragma unroll
@@ -412,6 +413,7 @@ __global__ void __launch_bounds__(1024) norm_grad_wide_kernel(GradParams p) {
                           : zero_octet<T>());
     }
   }
+  let_next_start();
   float* part = p.parts + static_cast<uint64_t>(blockIdx.x) * p.d;
   for (uint32_t o = threadIdx.x; o < octets; o += 1024)
 #pragma unroll
@@ -430,6 +432,7 @@ __global__ void __launch_bounds__(kDwThreads) norm_dw_kernel(GradParams p) {
   const uint32_t share = (p.ctas + 31) / 32;
   const uint32_t lo = warp * share, hi = min(lo + share, p.ctas);
   float s = 0.0f;
+  wait_for_previous();
   if (col < p.d) {
 #pragma unroll 8
     for (uint32_t k = lo; k < hi; ++k) s += p.parts[static_cast<uint64_t>(k) * p.d + col];
@@ -504,10 +507,9 @@ cudaError_t launch_grad(const GradParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     fn<<<p.ctas, 1024, smem, s>>>(p);
   }
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  norm_dw_kernel<<<(p.d + 31) / 32, kDwThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(&norm_dw_kernel, dim3((p.d + 31) / 32), kDwThreads, 0, s, p);
 }
 
 // CTAs of a gradient call, each with its own sums for dw: those that fit on the card at once.
