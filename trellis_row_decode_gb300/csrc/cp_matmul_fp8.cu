@@ -21,11 +21,18 @@ using namespace cpl;
 using cpm::MatmulParams;
 
 // ---------------------------------------------------- rows on any byte boundary
+//
+// 128 x 64 outputs per CTA, eight warps of 32 x 32.  A group's bytes are loaded as aligned words
+// and shifted into place, widened to fp16 (exact) once on their way to shared memory, and
+// multiplied by the warp-level fp16 product with fp32 sums: widening in front of every e4m3
+// product instead, as the warp-level e4m3 instruction does, took 46 us on 3000 x 700 x 900.
+// The next group's words are in flight while the tensor core works on this one's.
 
-constexpr int kTile = 64;              // rows of a and of w per CTA
-constexpr int kPitch = 144;            // shared row pitch: fragment reads without conflicts
-constexpr int kAnyThreads = 128;
-constexpr int kWords = kTile * 32 / kAnyThreads;   // 4-byte words a thread stages per operand
+constexpr int kTileRows = 128, kTileCols = 64;           // rows of a and of w per CTA
+constexpr int kAnyThreads = 256;
+constexpr int kPitch = 128 * 2 + 16;                     // shared row pitch: no bank conflicts
+constexpr int kPieces = (kTileRows + kTileCols) * 8 / kAnyThreads;   // 16-byte pieces of a thread
+constexpr int kAnySmem = (kTileRows + kTileCols) * kPitch;
 
 // d = a (16 x 32) * b (32 x 8) + d on the tensor core, e4m3 operands.
 __device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -37,49 +44,74 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// This thread's words of rows [row0, row0 + 64), columns [k0, k0 + 128); zeros outside
-// the matrix.  ALIGNED: rows on 4-byte boundaries.
-template <bool ALIGNED>
-__device__ __forceinline__ void stage_load(uint32_t (&v)[kWords], const uint8_t* base, uint64_t ld,
-                                           uint32_t row0, uint32_t rows, uint32_t k0, uint32_t k) {
-#pragma unroll
-  for (int i = 0; i < kWords; ++i) {
-    const uint32_t idx = threadIdx.x + i * kAnyThreads;
-    const uint32_t row = row0 + idx / 32, col = k0 + (idx % 32) * 4;
-    uint32_t x = 0;
-    if (row < rows && col < k) {
-      const uint8_t* p = base + row * ld + col;
-      if (ALIGNED && col + 4 <= k) {
-        x = *reinterpret_cast<const uint32_t*>(p);
-      } else {
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          if (col + b < k) x |= static_cast<uint32_t>(p[b]) << (8 * b);
-      }
-    }
-    v[i] = x;
-  }
+// d = a (16 x 16) * b (16 x 8) + d, fp16 operands.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void stage_store(uint8_t* tile, const uint32_t (&v)[kWords]) {
-#pragma unroll
-  for (int i = 0; i < kWords; ++i) {
-    const uint32_t idx = threadIdx.x + i * kAnyThreads;
-    *reinterpret_cast<uint32_t*>(tile + (idx / 32) * kPitch + (idx % 32) * 4) = v[i];
-  }
+__device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
 }
 
-// 64 x 64 outputs per CTA, four warps of 32 x 32; the next group's words are loaded
-// into registers while the tensor core works on this one's.
-template <bool ALIGNED>
-__global__ void __launch_bounds__(kAnyThreads) matmul_any_kernel(MatmulParams p) {
-  __shared__ __align__(16) uint8_t ta[kTile * kPitch];
-  __shared__ __align__(16) uint8_t tw[kTile * kPitch];
-  const uint32_t tiles_n = (p.n + kTile - 1) / kTile;
-  const uint32_t row0 = blockIdx.x / tiles_n * kTile, col0 = blockIdx.x % tiles_n * kTile;
+// Sixteen bytes from row + col on, zeros behind the row's k bytes.  Words that reach outside
+// the row are read byte by byte.
+__device__ __forceinline__ uint4 load_any_piece(const uint8_t* row, uint32_t col, uint32_t k) {
+  uint32_t w[4] = {};
+  const uint8_t* p = row + col;
+  const uint32_t skew = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3);
+  if (col >= skew && static_cast<uint64_t>(col) + (skew != 0 ? 20 - skew : 16) <= k) {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(p - skew);
+    uint32_t x[5];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __ldg(q + i);
+    x[4] = skew != 0 ? __ldg(q + 4) : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(x[i], x[i + 1], 8 * skew);
+  } else {
+#pragma unroll
+    for (int b = 0; b < 16; ++b)
+      if (static_cast<uint64_t>(col) + b < k) w[b / 4] |= static_cast<uint32_t>(p[b]) << (8 * (b & 3));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Four e4m3 bytes as fp16.
+__device__ __forceinline__ uint2 widen4(uint32_t w) {
+  const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3);
+  const __half2_raw hi =
+      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
+  return make_uint2(lo.x | static_cast<uint32_t>(lo.y) << 16,
+                    hi.x | static_cast<uint32_t>(hi.y) << 16);
+}
+
+__global__ void __launch_bounds__(kAnyThreads, 2) matmul_any_kernel(MatmulParams p) {
+  extern __shared__ __align__(16) uint8_t tile[];        // rows of a, then rows of w
+  const uint32_t tiles_n = (p.n + kTileCols - 1) / kTileCols;
+  const uint32_t row0 = blockIdx.x / tiles_n * kTileRows, col0 = blockIdx.x % tiles_n * kTileCols;
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t wr = (warp >> 1) * 32, wc = (warp & 1) * 32;
   const uint32_t g = lane >> 2, t = lane & 3;
+  const uint32_t base = cpt::smem_addr(tile);
+  uint4 v[kPieces];
+  auto fetch = [&](uint32_t k0) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const uint32_t piece = threadIdx.x + i * kAnyThreads, r = piece / 8;
+      const bool of_a = r < kTileRows;
+      const uint32_t row = of_a ? row0 + r : col0 + r - kTileRows;
+      const uint32_t col = k0 + piece % 8 * 16;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (row < (of_a ? p.m : p.n) && col < p.k)
+        v[i] = load_any_piece(of_a ? p.a + row * p.lda : p.w + row * p.ldw, col, p.k);
+    }
+  };
   float acc[2][4][4];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -87,41 +119,38 @@ __global__ void __launch_bounds__(kAnyThreads) matmul_any_kernel(MatmulParams p)
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
-  uint32_t va[kWords], vw[kWords];
-  stage_load<ALIGNED>(va, p.a, p.lda, row0, p.m, 0, p.k);
-  stage_load<ALIGNED>(vw, p.w, p.ldw, col0, p.n, 0, p.k);
   const float* sw = p.sw + static_cast<uint64_t>(col0 / 128) * p.groups;
+  // this lane's row and half of k in the 16 x 16 (a) and 8 x 16 pairs (w) that ldmatrix loads
+  const uint32_t at_a = base + (wr + (lane & 15)) * kPitch + (lane >> 4) * 16;
+  const uint32_t at_w =
+      base + (kTileRows + wc + (lane & 7) + (lane >> 4) * 8) * kPitch + (lane >> 3 & 1) * 16;
+  if (p.groups != 0) fetch(0);
   for (uint32_t kb = 0; kb < p.groups; ++kb) {
     __syncthreads();
-    stage_store(ta, va);
-    stage_store(tw, vw);
-    __syncthreads();
-    if (kb + 1 < p.groups) {
-      stage_load<ALIGNED>(va, p.a, p.lda, row0, p.m, (kb + 1) * 128, p.k);
-      stage_load<ALIGNED>(vw, p.w, p.ldw, col0, p.n, (kb + 1) * 128, p.k);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const uint32_t piece = threadIdx.x + i * kAnyThreads;
+      const uint2 a = widen4(v[i].x), b = widen4(v[i].y), c = widen4(v[i].z), d = widen4(v[i].w);
+      uint4* to = reinterpret_cast<uint4*>(tile + piece / 8 * kPitch + piece % 8 * 32);
+      to[0] = make_uint4(a.x, a.y, b.x, b.y);
+      to[1] = make_uint4(c.x, c.y, d.x, d.y);
     }
+    __syncthreads();
+    if (kb + 1 < p.groups) fetch((kb + 1) * 128);
     float c[2][4][4] = {};
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      uint32_t fa[2][4], fb[4][2];
+    for (int ks = 0; ks < 8; ++ks) {
+      uint32_t fa[2][4], fb[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint8_t* q = ta + (wr + 16 * i + g) * kPitch + ks * 32 + t * 4;
-        fa[i][0] = *reinterpret_cast<const uint32_t*>(q);
-        fa[i][1] = *reinterpret_cast<const uint32_t*>(q + 8 * kPitch);
-        fa[i][2] = *reinterpret_cast<const uint32_t*>(q + 16);
-        fa[i][3] = *reinterpret_cast<const uint32_t*>(q + 8 * kPitch + 16);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint8_t* q = tw + (wc + 8 * j + g) * kPitch + ks * 32 + t * 4;
-        fb[j][0] = *reinterpret_cast<const uint32_t*>(q);
-        fb[j][1] = *reinterpret_cast<const uint32_t*>(q + 16);
+        load_matrices(fa[i], at_a + i * 16 * kPitch + ks * 32);
+        load_matrices(fb[i], at_w + i * 16 * kPitch + ks * 32);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma_e4m3(c[i][j], fa[i], fb[j][0], fb[j][1]);
+        for (int j = 0; j < 4; ++j)
+          mma_f16(c[i][j], fa[i], fb[j / 2][j % 2 * 2], fb[j / 2][j % 2 * 2 + 1]);
     }
     const float scale_w = __ldg(sw + kb);
 #pragma unroll
@@ -165,7 +194,8 @@ __global__ void __launch_bounds__(kAnyThreads) matmul_any_kernel(MatmulParams p)
 // 17 MB of w they are even, 6.3 us, and with 101 MB the thin one leads, 20 us against 28: the
 // warp-level e4m3 product costs about 70 clocks each).  Up to 128 rows of a: the thin kernel
 // (128 x 4096 x 24576: 31 us against the pairs' 42; 128 x 4096 x 4096: 10.8 against 13.7; at 256 rows
-// 54 against 43 and 14.9 against 14.1).  More: the pairs.
+// 54 against 43 and 14.9 against 14.1).  More: the pairs.  Rows on other boundaries: this one for
+// few rows of a whatever the size of w, matmul_any_kernel for more.
 constexpr uint32_t kFewRows = 16;
 constexpr uint64_t kFewBytes = 8 << 20;
 constexpr uint32_t kThinRows = 128;
@@ -183,28 +213,28 @@ struct FewRows {
   float scale_w;
 };
 
-// Sixteen bytes of a row from column `col` on, zeros behind the row's k bytes.
+// Sixteen bytes of a row of w (read once: not kept in L1) or of a.
+template <bool kAligned>
 __device__ __forceinline__ uint4 load_piece(const uint8_t* row, uint32_t col, uint32_t k) {
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (col + 16 <= k) {
+  if (kAligned && static_cast<uint64_t>(col) + 16 <= k) {
+    uint4 v;
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(row + col));
-  } else if (col < k) {
-    uint32_t u[4] = {};
-    for (uint32_t b = 0; col + b < k; ++b)
-      u[b / 4] |= static_cast<uint32_t>(row[col + b]) << (8 * (b & 3));
-    v = make_uint4(u[0], u[1], u[2], u[3]);
+    return v;
   }
-  return v;
+  return load_any_piece(row, col, k);
 }
+template <bool kAligned>
 __device__ __forceinline__ uint4 load_piece_cached(const uint8_t* row, uint32_t col, uint32_t k) {
-  if (col + 16 <= k) return __ldg(reinterpret_cast<const uint4*>(row + col));
-  return load_piece(row, col, k);
+  if (kAligned && static_cast<uint64_t>(col) + 16 <= k)
+    return __ldg(reinterpret_cast<const uint4*>(row + col));
+  return load_any_piece(row, col, k);
 }
 
-// kTokens: rows of a / 8.  kAhead: groups of w in flight per warp.
-template <int kTokens, int kAhead>
+// kTokens: rows of a / 8.  kAhead: groups of w in flight per warp.  kAligned: rows on 16-byte
+// boundaries.
+template <int kTokens, int kAhead, bool kAligned>
 __global__ void __launch_bounds__(kFewThreads, 2) matmul_few_kernel(MatmulParams p, uint32_t splits) {
   __shared__ float part[kFewWarps][16][kTokens * 8];
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -222,8 +252,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) matmul_few_kernel(MatmulParams
     for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        f.w[r][h] = kb < p.groups && live[r] ? load_piece(wrow[r], kb * 128 + 64 * h + 16 * t, p.k)
-                                             : make_uint4(0, 0, 0, 0);
+        f.w[r][h] = kb < p.groups && live[r]
+                        ? load_piece<kAligned>(wrow[r], kb * 128 + 64 * h + 16 * t, p.k)
+                        : make_uint4(0, 0, 0, 0);
   };
   // The rows of a and the scales of a group, one group ahead of their use.
   FewRows<kTokens> rows;
@@ -236,7 +267,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) matmul_few_kernel(MatmulParams
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         rows.b[n][h] = in && row < p.m
-                           ? load_piece_cached(p.a + static_cast<uint64_t>(row) * p.lda,
+                           ? load_piece_cached<kAligned>(p.a + static_cast<uint64_t>(row) * p.lda,
                                                kb * 128 + 64 * h + 16 * t, p.k)
                            : make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -318,7 +349,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) matmul_few_kernel(MatmulParams
   cpt::cluster_sync();               // no CTA leaves while another may read its shared memory
 }
 
-template <int kTokens, int kAhead>
+template <int kTokens, int kAhead, bool kAligned>
 cudaError_t launch_few(const MatmulParams& p, uint32_t splits, cudaStream_t s) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -331,10 +362,10 @@ cudaError_t launch_few(const MatmulParams& p, uint32_t splits, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = splits == 1 ? 0 : 1;
-  return cudaLaunchKernelEx(&cfg, &matmul_few_kernel<kTokens, kAhead>, p, splits);
+  return cudaLaunchKernelEx(&cfg, &matmul_few_kernel<kTokens, kAhead, kAligned>, p, splits);
 }
 
-cp_status launch_few(const MatmulParams& p, cudaStream_t s) {
+cp_status launch_few(const MatmulParams& p, bool aligned, cudaStream_t s) {
   // Share rows among CTAs until there are about two per SM, as long as each warp keeps two
   // groups or more.
   uint32_t splits = 1;
@@ -342,8 +373,10 @@ cp_status launch_few(const MatmulParams& p, cudaStream_t s) {
          p.groups >= 2 * kFewWarps * 2 * splits)
     splits *= 2;
   cudaError_t e;
-  if (p.m <= 8) e = launch_few<1, 4>(p, splits, s);
-  else e = launch_few<2, 3>(p, splits, s);
+  if (p.m <= 8)
+    e = aligned ? launch_few<1, 4, true>(p, splits, s) : launch_few<1, 2, false>(p, splits, s);
+  else
+    e = aligned ? launch_few<2, 3, true>(p, splits, s) : launch_few<2, 2, false>(p, splits, s);
   if (e != cudaSuccess) return cpx::cuda_fail(e, "fp8 matmul launch");
   return CP_OK;
 }
@@ -386,18 +419,21 @@ extern "C" cp_status cp_matmul_fp8(const uint8_t* a, uint64_t a_stride, const fl
       (m == 1 || (a_stride % 16 == 0 && a_stride != 0)) &&
       (n == 1 || (w_stride % 16 == 0 && w_stride != 0)))
     return m > kThinRows                          ? cpm::launch_pairs(p, s)
-           : m <= kFewRows && n * k <= kFewBytes ? launch_few(p, s)
+           : m <= kFewRows && n * k <= kFewBytes ? launch_few(p, true, s)
                                                  : cpm::launch_thin(p, s);
-  const uint64_t tiles = ((m + kTile - 1) / kTile) * ((n + kTile - 1) / kTile);
+  if (m <= kFewRows) return launch_few(p, false, s);
+  const uint64_t tiles =
+      ((m + kTileRows - 1) / kTileRows) * ((n + kTileCols - 1) / kTileCols);
   if (tiles >= kMost) {
     cpx::set_error("m and n make more than 2^31 tiles");
     return CP_ERR_INVALID_ARG;
   }
-  const bool words = cpx::aligned(a, 4) && cpx::aligned(w, 4) && a_stride % 4 == 0 &&
-                     w_stride % 4 == 0;
-  auto* fn = words ? &matmul_any_kernel<true> : &matmul_any_kernel<false>;
-  fn<<<static_cast<unsigned>(tiles), kAnyThreads, 0, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&matmul_any_kernel),
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kAnySmem);
+  if (e == cudaSuccess) {
+    matmul_any_kernel<<<static_cast<unsigned>(tiles), kAnyThreads, kAnySmem, s>>>(p);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return cpx::cuda_fail(e, "fp8 matmul launch");
   return CP_OK;
 }
