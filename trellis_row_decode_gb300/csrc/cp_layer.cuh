@@ -133,15 +133,44 @@ __device__ __forceinline__ Packed<T> zero_octet() {
   return r;
 }
 
-// Octet `o` of a row of d elements at p.  VEC: rows whose every octet is whole and
-// aligned to its own size; otherwise single elements, and the last octet may be
-// part full (the rest reads as zero and is not written).
-template <typename T, bool VEC>
-__device__ __forceinline__ Packed<T> load_row_octet(const T* row, uint32_t o, uint32_t d) {
-  if constexpr (VEC) {
-    return load_octet(row + 8ull * o);
+// Octet `o` of a row of d elements at p.  VEC: rows whose every octet is whole and aligned to its
+// own size.  Otherwise rows start anywhere and the last octet may be part full (the rest reads
+// as zero and is not written): an octet is shifted out of the aligned 16-byte words that hold
+// it, where they lie within the row, and read by single elements at the row's ends; it is
+// written in the widest pieces that its address allows.
+template <typename T>
+__device__ __forceinline__ Packed<T> load_skewed_octet(const T* row, uint32_t o, uint32_t d) {
+  constexpr int kQuads = Packed<T>::kWords / 4;
+  const uintptr_t first = reinterpret_cast<uintptr_t>(row), at = first + 8ull * sizeof(T) * o;
+  const uint32_t skew = static_cast<uint32_t>(at & 15);
+  const uintptr_t from = at - skew, to = from + 16 * kQuads + (skew != 0 ? 16 : 0);
+  Packed<T> r = zero_octet<T>();
+  if (from >= first && to <= first + static_cast<uint64_t>(d) * sizeof(T)) {
+    uint32_t x[4 * kQuads + 4];
+#pragma unroll
+    for (int q = 0; q < kQuads + 1; ++q) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (q < kQuads || skew != 0)
+        asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(from + 16 * q));
+      x[4 * q] = v.x;
+      x[4 * q + 1] = v.y;
+      x[4 * q + 2] = v.z;
+      x[4 * q + 3] = v.w;
+    }
+    if (skew & 8) {
+#pragma unroll
+      for (int i = 0; i < 4 * kQuads + 2; ++i) x[i] = x[i + 2];
+    }
+    if (skew & 4) {
+#pragma unroll
+      for (int i = 0; i < 4 * kQuads + 1; ++i) x[i] = x[i + 1];
+    }
+#pragma unroll
+    for (int i = 0; i < Packed<T>::kWords; ++i)
+      r.w[i] = sizeof(T) == 4 ? x[i] : __funnelshift_r(x[i], x[i + 1], 8 * (skew & 2));
   } else {
-    Packed<T> r = zero_octet<T>();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t c = 8 * o + i;
@@ -154,8 +183,14 @@ __device__ __forceinline__ Packed<T> load_row_octet(const T* row, uint32_t o, ui
         }
       }
     }
-    return r;
   }
+  return r;
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ Packed<T> load_row_octet(const T* row, uint32_t o, uint32_t d) {
+  if constexpr (VEC) return load_octet(row + 8ull * o);
+  else return load_skewed_octet(row, o, d);
 }
 
 template <typename T, bool VEC>
@@ -163,18 +198,37 @@ __device__ __forceinline__ void store_row_octet(T* row, uint32_t o, uint32_t d,
                                                 const Packed<T>& r) {
   if constexpr (VEC) {
     store_octet(row + 8ull * o, r);
-  } else {
+    return;
+  }
+  T* to = row + 8ull * o;
+  const uint32_t skew = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(to) & 15);
+  if (8 * o + 8 > d) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t c = 8 * o + i;
-      if (c < d) {
-        if constexpr (sizeof(T) == 4) {
-          reinterpret_cast<uint32_t*>(row)[c] = r.w[i];
-        } else {
-          reinterpret_cast<uint16_t*>(row)[c] = static_cast<uint16_t>(r.w[i / 2] >> (16 * (i & 1)));
-        }
+      if (8 * o + i < d) {
+        if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(to)[i] = r.w[i];
+        else reinterpret_cast<uint16_t*>(to)[i] = static_cast<uint16_t>(r.w[i / 2] >> (16 * (i & 1)));
       }
     }
+  } else if (skew == 0) {
+#pragma unroll
+    for (int q = 0; q < Packed<T>::kWords / 4; ++q)
+      reinterpret_cast<uint4*>(to)[q] =
+          make_uint4(r.w[4 * q], r.w[4 * q + 1], r.w[4 * q + 2], r.w[4 * q + 3]);
+  } else if (skew == 8) {
+#pragma unroll
+    for (int q = 0; q < Packed<T>::kWords / 2; ++q)
+      reinterpret_cast<uint2*>(to)[q] = make_uint2(r.w[2 * q], r.w[2 * q + 1]);
+  } else if ((skew & 3) == 0) {
+#pragma unroll
+    for (int q = 0; q < Packed<T>::kWords; ++q) reinterpret_cast<uint32_t*>(to)[q] = r.w[q];
+  } else if constexpr (sizeof(T) == 2) {
+    uint16_t* h = reinterpret_cast<uint16_t*>(to);
+    h[0] = static_cast<uint16_t>(r.w[0]);
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      reinterpret_cast<uint32_t*>(h + 1)[q] = __funnelshift_r(r.w[q], r.w[q + 1], 16);
+    h[7] = static_cast<uint16_t>(r.w[3] >> 16);
   }
 }
 
@@ -228,14 +282,32 @@ __device__ __forceinline__ uint2 quantize_octet(const float (&v)[8], float inv) 
 // VEC: q rows 8-byte aligned with whole octets.
 template <bool VEC>
 __device__ __forceinline__ void store_q_octet(uint8_t* row, uint32_t o, uint32_t d, uint2 q) {
+  uint8_t* to = row + 8ull * o;
   if constexpr (VEC) {
-    *reinterpret_cast<uint2*>(row + 8ull * o) = q;
-  } else {
+    *reinterpret_cast<uint2*>(to) = q;
+    return;
+  }
+  if (8 * o + 8 > d) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t c = 8 * o + i;
-      if (c < d) row[c] = static_cast<uint8_t>((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
-    }
+    for (int i = 0; i < 8; ++i)
+      if (8 * o + i < d) to[i] = static_cast<uint8_t>((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+    return;
+  }
+  // bytes up to the first 4-byte boundary, the word there, the bytes behind it
+  const uint32_t head = static_cast<uint32_t>(-reinterpret_cast<uintptr_t>(to)) & 3;
+  if (head == 0) {
+    reinterpret_cast<uint32_t*>(to)[0] = q.x;
+    reinterpret_cast<uint32_t*>(to)[1] = q.y;
+  } else {
+    if (head & 1) to[0] = static_cast<uint8_t>(q.x);
+    if (head & 2)
+      *reinterpret_cast<uint16_t*>(to + (head & 1)) =
+          static_cast<uint16_t>(q.x >> (8 * (head & 1)));
+    *reinterpret_cast<uint32_t*>(to + head) = __funnelshift_r(q.x, q.y, 8 * head);
+    // 4 - head bytes are left behind the word: 3, 2 or 1
+    if (head != 3)
+      *reinterpret_cast<uint16_t*>(to + head + 4) = static_cast<uint16_t>(q.y >> (8 * head));
+    if (head & 1) to[7] = static_cast<uint8_t>(q.y >> 24);
   }
 }
 
