@@ -126,7 +126,49 @@ __device__ __forceinline__ void emit(const NormParams& p, uint64_t row, uint32_t
 
 // Threads of a CTA of teams of `threads`, and CTAs that share an SM.
 constexpr int cta_threads(int threads) { return threads <= 32 ? 256 : threads; }
-constexpr int norm_ctas(int threads) { return 768 / cta_threads(threads) > 1 ? 768 / cta_threads(threads) : 1; }
+constexpr int ctas_of(int sm_threads, int threads) {
+  return sm_threads / cta_threads(threads) > 1 ? sm_threads / cta_threads(threads) : 1;
+}
+constexpr int norm_ctas(int threads) { return ctas_of(768, threads); }
+constexpr int grad_ctas_per_sm(int threads) { return ctas_of(512, threads); }
+constexpr bool norm_ring(int threads) { return threads == 1024 || threads <= 16; }
+
+// Rows on octet boundaries travel through shared memory: a thread copies its own octets of the
+// coming rows there (asynchronously, 192 KB an SM in all) and reads them back itself, so it
+// waits for nobody and no registers hold what is under way.  Bytes of one row's octets of
+// `arrays` arrays, and the rows that fit; one row or less: they wait in registers instead.
+// Measured, 4096 x 4096 bf16: the gradient takes 28.4 us with three rows under way, 29.8 with
+// four, 32.0 from registers; the forward, with fewer values to hold, 20.6 us from registers and
+// 22.6 through shared memory, except in teams of 1024 (64 registers a thread; 1024 x 16384: 25.1
+// against 28.4) and of a few lanes (100000 x 128: 17.0 against 18.3).
+constexpr int stage_bytes(int arrays, int oct, int threads, int elt) {
+  return arrays * oct * cta_threads(threads) * 8 * elt;
+}
+constexpr int stages_of(int ctas, int stage) {
+  return 196608 / (ctas * stage) >= 3 ? 3 : 196608 / (ctas * stage);
+}
+
+template <typename T>
+__device__ __forceinline__ void copy_octet(uint32_t to, const T* from) {
+#pragma unroll
+  for (uint32_t b = 0; b < 8 * sizeof(T); b += 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + b),
+                 "l"(reinterpret_cast<const uint8_t*>(from) + b)
+                 : "memory");
+}
+template <typename T>
+__device__ __forceinline__ Packed<T> copied_octet(const uint8_t* at) {
+  Packed<T> r;
+#pragma unroll
+  for (int q = 0; q < Packed<T>::kWords / 4; ++q) {
+    const uint4 x = reinterpret_cast<const uint4*>(at)[q];
+    r.w[4 * q] = x.x;
+    r.w[4 * q + 1] = x.y;
+    r.w[4 * q + 2] = x.z;
+    r.w[4 * q + 3] = x.w;
+  }
+  return r;
+}
 
 template <typename T, bool VEC, bool Q, int THREADS, int kOct>
 __global__ void __launch_bounds__(cta_threads(THREADS), norm_ctas(THREADS)) norm_kernel(NormParams p) {
@@ -145,27 +187,56 @@ __global__ void __launch_bounds__(cta_threads(THREADS), norm_ctas(THREADS)) norm
       for (int e = 0; e < 8; ++e) w[i][e] = 0.0f;
     }
   }
-  Packed<T> xn[kOct], rn[kOct];        // the next row
-  auto fetch = [&](uint64_t row) {
+  constexpr int kStage = stage_bytes(2, kOct, THREADS, sizeof(T));
+  constexpr int kStages = VEC && norm_ring(THREADS) ? stages_of(norm_ctas(THREADS), kStage) : 1;
+  constexpr bool kRing = kStages >= 2;
+  constexpr uint32_t kOctet = 8 * sizeof(T);
+  extern __shared__ __align__(16) uint8_t ring[];
+  uint8_t* mine_ring = ring + threadIdx.x * kOctet;
+  const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(mine_ring));
+  Packed<T> xn[kOct], rn[kOct];        // the next row (or, with the ring, this one)
+  auto fetch = [&](uint64_t row, int stage) {
     const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
     const T* res = static_cast<const T*>(p.residual) + row * p.residual_stride;
 #pragma unroll
     for (int i = 0; i < kOct; ++i) {
       const uint32_t o = tid + i * THREADS;
       const bool in = row < p.rows && o < octets;
-      xn[i] = in ? load_row_octet<T, VEC>(x, o, p.d) : zero_octet<T>();
-      rn[i] = in && p.residual != nullptr ? load_row_octet<T, VEC>(res, o, p.d) : zero_octet<T>();
+      if constexpr (kRing) {
+        const uint32_t at = ring_at + stage * kStage + 2 * i * cta_threads(THREADS) * kOctet;
+        if (in) copy_octet(at, x + 8ull * o);
+        if (in && p.residual != nullptr)
+          copy_octet(at + cta_threads(THREADS) * kOctet, res + 8ull * o);
+      } else {
+        xn[i] = in ? load_row_octet<T, VEC>(x, o, p.d) : zero_octet<T>();
+        rn[i] = in && p.residual != nullptr ? load_row_octet<T, VEC>(res, o, p.d) : zero_octet<T>();
+      }
     }
+    if constexpr (kRing) asm volatile("cp.async.commit_group;" ::: "memory");
   };
   // (teams within a warp take their turns together: the shuffles are the warp's)
   const uint64_t lead = static_cast<uint64_t>(blockIdx.x) * kTeams +
                         (THREADS < 32 ? threadIdx.x / 32 * (32 / THREADS) : threadIdx.x / THREADS);
   const uint64_t mine = THREADS < 32 ? (threadIdx.x & 31) / THREADS : 0;
   const uint64_t step = static_cast<uint64_t>(gridDim.x) * kTeams;
-  fetch(lead + mine);
-  int turn = 0;
+#pragma unroll
+  for (int k = 0; k < (kRing ? kStages - 1 : 1); ++k) fetch(lead + mine + k * step, k);
+  int turn = 0, stage = 0;
   for (uint64_t at = lead; at < p.rows; at += step, turn ^= 1) {
     const uint64_t row = at + mine;
+    if constexpr (kRing) {
+      fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+#pragma unroll
+      for (int i = 0; i < kOct; ++i) {
+        const bool in = row < p.rows && tid + i * THREADS < octets;
+        const uint8_t* from = mine_ring + stage * kStage + 2 * i * cta_threads(THREADS) * kOctet;
+        xn[i] = in ? copied_octet<T>(from) : zero_octet<T>();
+        rn[i] = in && p.residual != nullptr ? copied_octet<T>(from + cta_threads(THREADS) * kOctet)
+                                            : zero_octet<T>();
+      }
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
     float s[kOct][8];
     float sq = 0.0f, unused = 0.0f;
 #pragma unroll
@@ -180,7 +251,7 @@ __global__ void __launch_bounds__(cta_threads(THREADS), norm_ctas(THREADS)) norm
 #pragma unroll
       for (int e = 0; e < 8; ++e) sq = fmaf(s[i][e], s[i][e], sq);
     }
-    fetch(row + step);
+    if constexpr (!kRing) fetch(row + step, 0);
     team_sum<THREADS>(sq, unused, red[turn]);
     const float r = 1.0f / sqrtf(sq / static_cast<float>(p.d) + p.eps);
 #pragma unroll
@@ -250,10 +321,6 @@ __device__ __forceinline__ void emit_dx(const GradParams& p, uint64_t row, uint3
   store_row_octet<T, VEC>(static_cast<T*>(p.dx) + row * p.d, o, p.d, pack<T>(dx));
 }
 
-constexpr int grad_ctas_per_sm(int threads) {
-  return 512 / cta_threads(threads) > 1 ? 512 / cta_threads(threads) : 1;
-}
-
 // Teams walk over the rows; a thread's columns are the same in every row, so it sums its part
 // of dw in registers, and the CTA's teams add theirs in order behind the last row.
 template <typename T, bool VEC, int THREADS, int kOct>
@@ -272,17 +339,35 @@ __global__ void __launch_bounds__(cta_threads(THREADS), grad_ctas_per_sm(THREADS
     for (int e = 0; e < 8; ++e) w[i][e] = dw[i][e] = 0.0f;
     if (o < octets) load_weight<VEC>(p.weight, p.weight_dtype, o, p.d, w[i]);
   }
-  Packed<T> hn[kOct], gn[kOct], rn[kOct];          // the next row
-  auto fetch = [&](uint64_t row) {
+  constexpr int kStage = stage_bytes(3, kOct, THREADS, sizeof(T));
+  constexpr int kStages = VEC ? stages_of(grad_ctas_per_sm(THREADS), kStage) : 1;
+  constexpr bool kRing = kStages >= 2;
+  constexpr uint32_t kOctet = 8 * sizeof(T), kArray = cta_threads(THREADS) * kOctet;
+  extern __shared__ __align__(16) uint8_t ring[];
+  uint8_t* mine_ring = ring + threadIdx.x * kOctet;
+  const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(mine_ring));
+  Packed<T> hn[kOct], gn[kOct], rn[kOct];          // the next row (or, with the ring, this one)
+  auto fetch = [&](uint64_t row, int stage) {
     const T* h = static_cast<const T*>(p.h) + row * p.h_stride;
     const T* dy = static_cast<const T*>(p.dy) + row * p.dy_stride;
+    const T* res = static_cast<const T*>(p.dres) + row * p.dres_stride;
 #pragma unroll
     for (int i = 0; i < kOct; ++i) {
       const uint32_t o = tid + i * THREADS;
       const bool in = row < p.rows && o < octets;
-      hn[i] = in ? load_row_octet<T, VEC>(h, o, p.d) : zero_octet<T>();
-      gn[i] = in ? load_row_octet<T, VEC>(dy, o, p.d) : zero_octet<T>();
+      if constexpr (kRing) {
+        const uint32_t at = ring_at + stage * kStage + 3 * i * kArray;
+        if (in) {
+          copy_octet(at, h + 8ull * o);
+          copy_octet(at + kArray, dy + 8ull * o);
+          if (p.dres != nullptr) copy_octet(at + 2 * kArray, res + 8ull * o);
+        }
+      } else {
+        hn[i] = in ? load_row_octet<T, VEC>(h, o, p.d) : zero_octet<T>();
+        gn[i] = in ? load_row_octet<T, VEC>(dy, o, p.d) : zero_octet<T>();
+      }
     }
+    if constexpr (kRing) asm volatile("cp.async.commit_group;" ::: "memory");
   };
   auto fetch_res = [&](uint64_t row) {
     const T* res = static_cast<const T*>(p.dres) + row * p.dres_stride;
@@ -297,11 +382,25 @@ __global__ void __launch_bounds__(cta_threads(THREADS), grad_ctas_per_sm(THREADS
                         (THREADS < 32 ? threadIdx.x / 32 * (32 / THREADS) : threadIdx.x / THREADS);
   const uint64_t mine = THREADS < 32 ? (threadIdx.x & 31) / THREADS : 0;
   const uint64_t step = static_cast<uint64_t>(gridDim.x) * kTeams;
-  fetch(lead + mine);
-  fetch_res(lead + mine);
-  int turn = 0;
+#pragma unroll
+  for (int k = 0; k < (kRing ? kStages - 1 : 1); ++k) fetch(lead + mine + k * step, k);
+  if constexpr (!kRing) fetch_res(lead + mine);
+  int turn = 0, stage = 0;
   for (uint64_t at = lead; at < p.rows; at += step, turn ^= 1) {
     const uint64_t row = at + mine;
+    if constexpr (kRing) {
+      fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+#pragma unroll
+      for (int i = 0; i < kOct; ++i) {
+        const bool in = row < p.rows && tid + i * THREADS < octets;
+        const uint8_t* from = mine_ring + stage * kStage + 3 * i * kArray;
+        hn[i] = in ? copied_octet<T>(from) : zero_octet<T>();
+        gn[i] = in ? copied_octet<T>(from + kArray) : zero_octet<T>();
+        rn[i] = in && p.dres != nullptr ? copied_octet<T>(from + 2 * kArray) : zero_octet<T>();
+      }
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
     float h[kOct][8], t[kOct][8];
     float sq = 0.0f, th = 0.0f;
 #pragma unroll
@@ -314,7 +413,7 @@ __global__ void __launch_bounds__(cta_threads(THREADS), grad_ctas_per_sm(THREADS
         th = fmaf(t[i][e] * w[i][e], h[i][e], th);
       }
     }
-    fetch(row + step);
+    if constexpr (!kRing) fetch(row + step, 0);
     team_sum<THREADS>(sq, th, red[turn]);
     const float inv_d = 1.0f / static_cast<float>(p.d);
     const float r = 1.0f / sqrtf(sq * inv_d + p.eps);
@@ -333,7 +432,7 @@ __global__ void __launch_bounds__(cta_threads(THREADS), grad_ctas_per_sm(THREADS
         }
       }
     }
-    fetch_res(row + step);
+    if constexpr (!kRing) fetch_res(row + step);
   }
   let_next_start();
   float* part = p.parts + static_cast<uint64_t>(blockIdx.x) * p.d;
@@ -449,29 +548,43 @@ __global__ void __launch_bounds__(kDwThreads) norm_dw_kernel(GradParams p) {
 
 constexpr uint64_t kSms = 152;
 
+// Dynamic shared memory of the ring, allowed for the kernel where it needs to be.
+template <typename K>
+cudaError_t allow_ring(K* kernel, int bytes) {
+  return bytes <= 32768 ? cudaSuccess
+                        : cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 template <typename T, bool VEC, bool Q, int THREADS, int kOct>
-void launch_teams(const NormParams& p, cudaStream_t s) {
+cudaError_t launch_teams(const NormParams& p, cudaStream_t s) {
   constexpr int kTeams = cta_threads(THREADS) / THREADS;
+  constexpr int kStage = stage_bytes(2, kOct, THREADS, sizeof(T));
+  constexpr int kStages = VEC && norm_ring(THREADS) ? stages_of(norm_ctas(THREADS), kStage) : 1;
+  constexpr int kBytes = kStages >= 2 ? kStages * kStage : 0;
+  auto* kernel = &norm_kernel<T, VEC, Q, THREADS, kOct>;
+  const cudaError_t e = allow_ring(kernel, kBytes);
+  if (e != cudaSuccess) return e;
   const uint64_t ctas = (static_cast<uint64_t>(p.rows) + kTeams - 1) / kTeams;
   const uint64_t most = kSms * norm_ctas(THREADS);
-  norm_kernel<T, VEC, Q, THREADS, kOct>
-      <<<static_cast<unsigned>(ctas < most ? ctas : most), cta_threads(THREADS), 0, s>>>(p);
+  kernel<<<static_cast<unsigned>(ctas < most ? ctas : most), cta_threads(THREADS), kBytes, s>>>(p);
+  return cudaGetLastError();
 }
 
 template <typename T, bool VEC, bool Q>
 cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
   const uint32_t octets = (p.d + 7) / 8;
-  if (octets <= 4) launch_teams<T, VEC, Q, 4, 1>(p, s);
-  else if (octets <= 8) launch_teams<T, VEC, Q, 8, 1>(p, s);
-  else if (octets <= 16) launch_teams<T, VEC, Q, 16, 1>(p, s);
-  else if (octets <= 32) launch_teams<T, VEC, Q, 32, 1>(p, s);
-  else if (octets <= 64) launch_teams<T, VEC, Q, 32, 2>(p, s);
-  else if (octets <= 128) launch_teams<T, VEC, Q, 64, 2>(p, s);
-  else if (octets <= 256) launch_teams<T, VEC, Q, 128, 2>(p, s);
-  else if (octets <= 512) launch_teams<T, VEC, Q, 256, 2>(p, s);
-  else if (octets <= 1024) launch_teams<T, VEC, Q, 512, 2>(p, s);
-  else if (octets <= 2048) launch_teams<T, VEC, Q, 1024, 2>(p, s);
-  else norm_wide_kernel<T, VEC, Q><<<p.rows, 1024, 0, s>>>(p);
+  if (octets <= 4) return launch_teams<T, VEC, Q, 4, 1>(p, s);
+  if (octets <= 8) return launch_teams<T, VEC, Q, 8, 1>(p, s);
+  if (octets <= 16) return launch_teams<T, VEC, Q, 16, 1>(p, s);
+  if (octets <= 32) return launch_teams<T, VEC, Q, 32, 1>(p, s);
+  if (octets <= 64) return launch_teams<T, VEC, Q, 32, 2>(p, s);
+  if (octets <= 128) return launch_teams<T, VEC, Q, 64, 2>(p, s);
+  if (octets <= 256) return launch_teams<T, VEC, Q, 128, 2>(p, s);
+  if (octets <= 512) return launch_teams<T, VEC, Q, 256, 2>(p, s);
+  if (octets <= 1024) return launch_teams<T, VEC, Q, 512, 2>(p, s);
+  if (octets <= 2048) return launch_teams<T, VEC, Q, 1024, 2>(p, s);
+  norm_wide_kernel<T, VEC, Q><<<p.rows, 1024, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -483,31 +596,40 @@ cudaError_t launch_norm(const NormParams& p, bool vec, cudaStream_t s) {
 }
 
 template <typename T, bool VEC, int THREADS, int kOct>
-void launch_grad_teams(const GradParams& p, cudaStream_t s) {
-  norm_grad_kernel<T, VEC, THREADS, kOct><<<p.ctas, cta_threads(THREADS), 0, s>>>(p);
+cudaError_t launch_grad_teams(const GradParams& p, cudaStream_t s) {
+  constexpr int kStage = stage_bytes(3, kOct, THREADS, sizeof(T));
+  constexpr int kStages = VEC ? stages_of(grad_ctas_per_sm(THREADS), kStage) : 1;
+  constexpr int kBytes = kStages >= 2 ? kStages * kStage : 0;
+  auto* kernel = &norm_grad_kernel<T, VEC, THREADS, kOct>;
+  const cudaError_t e = allow_ring(kernel, kBytes);
+  if (e != cudaSuccess) return e;
+  kernel<<<p.ctas, cta_threads(THREADS), kBytes, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T, bool VEC>
+cudaError_t launch_rows(const GradParams& p, cudaStream_t s) {
+  const uint32_t octets = (p.d + 7) / 8;
+  if (octets <= 4) return launch_grad_teams<T, VEC, 4, 1>(p, s);
+  if (octets <= 8) return launch_grad_teams<T, VEC, 8, 1>(p, s);
+  if (octets <= 16) return launch_grad_teams<T, VEC, 16, 1>(p, s);
+  if (octets <= 32) return launch_grad_teams<T, VEC, 32, 1>(p, s);
+  if (octets <= 64) return launch_grad_teams<T, VEC, 32, 2>(p, s);
+  if (octets <= 128) return launch_grad_teams<T, VEC, 64, 2>(p, s);
+  if (octets <= 256) return launch_grad_teams<T, VEC, 128, 2>(p, s);
+  if (octets <= 512) return launch_grad_teams<T, VEC, 256, 2>(p, s);
+  if (octets <= 1024) return launch_grad_teams<T, VEC, 512, 2>(p, s);
+  const int smem = static_cast<int>(octets * 32);
+  auto* fn = &norm_grad_wide_kernel<T, VEC>;
+  const cudaError_t e = allow_ring(fn, smem);
+  if (e != cudaSuccess) return e;
+  fn<<<p.ctas, 1024, smem, s>>>(p);
+  return cudaGetLastError();
 }
 
 template <typename T, bool VEC>
 cudaError_t launch_grad(const GradParams& p, cudaStream_t s) {
-  const uint32_t octets = (p.d + 7) / 8;
-  if (octets <= 4) launch_grad_teams<T, VEC, 4, 1>(p, s);
-  else if (octets <= 8) launch_grad_teams<T, VEC, 8, 1>(p, s);
-  else if (octets <= 16) launch_grad_teams<T, VEC, 16, 1>(p, s);
-  else if (octets <= 32) launch_grad_teams<T, VEC, 32, 1>(p, s);
-  else if (octets <= 64) launch_grad_teams<T, VEC, 32, 2>(p, s);
-  else if (octets <= 128) launch_grad_teams<T, VEC, 64, 2>(p, s);
-  else if (octets <= 256) launch_grad_teams<T, VEC, 128, 2>(p, s);
-  else if (octets <= 512) launch_grad_teams<T, VEC, 256, 2>(p, s);
-  else if (octets <= 1024) launch_grad_teams<T, VEC, 512, 2>(p, s);
-  else {
-    const int smem = static_cast<int>(octets * 32);
-    auto* fn = &norm_grad_wide_kernel<T, VEC>;
-    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    fn<<<p.ctas, 1024, smem, s>>>(p);
-  }
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_rows<T, VEC>(p, s);
   if (e != cudaSuccess) return e;
   return launch_after(&norm_dw_kernel, dim3((p.d + 31) / 32), kDwThreads, 0, s, p);
 }
