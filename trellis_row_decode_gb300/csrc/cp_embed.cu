@@ -33,6 +33,7 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t slab = slabs == 1 ? 0 : static_cast<uint32_t>(team - j * slabs);
   const uint32_t octets = (d + 7) / 8;
   const uint32_t o0 = slab * lanes * kOctets + (threadIdx.x & (lanes - 1));
+  wait_for_previous();
   const int64_t id = __ldg(ids + j);
   const bool valid = static_cast<uint64_t>(id) < n_rows;
   const T* src = weight + (valid ? static_cast<uint64_t>(id) : 0) * weight_stride;
@@ -58,7 +59,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 template <typename T>
-cudaError_t launch(const void* weight, uint64_t n_rows, uint32_t d, uint64_t weight_stride,
+cudaError_t launch_embed(const void* weight, uint64_t n_rows, uint32_t d, uint64_t weight_stride,
                    const int64_t* ids, uint64_t n, float scale, void* out, uint64_t out_stride,
                    uint32_t* status, cudaStream_t s) {
   const uint32_t octets = (d + 7) / 8;
@@ -71,10 +72,9 @@ cudaError_t launch(const void* weight, uint64_t n_rows, uint32_t d, uint64_t wei
   const bool vec = octets_ok(weight, weight_stride, d, sizeof(T)) &&
                    octets_ok(out, out_stride, d, sizeof(T));
   auto* fn = vec ? &embed_kernel<T, true> : &embed_kernel<T, false>;
-  fn<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(
-      static_cast<const T*>(weight), n_rows, d, weight_stride, ids, n, scale,
-      static_cast<T*>(out), out_stride, status, lanes_log2, slabs);
-  return cudaGetLastError();
+  return launch(Launch{dim3(static_cast<unsigned>(blocks)), kThreads, 0, s}, fn,
+                static_cast<const T*>(weight), n_rows, d, weight_stride, ids, n, scale,
+                static_cast<T*>(out), out_stride, status, lanes_log2, slabs);
 }
 
 }  // namespace
@@ -98,11 +98,11 @@ extern "C" cp_status cp_embed(const void* weight, int dtype, uint64_t n_rows, ui
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (dtype == CP_F32)
-    e = launch<float>(weight, n_rows, d, weight_stride, ids, n, scale, out, out_stride, status, s);
+    e = launch_embed<float>(weight, n_rows, d, weight_stride, ids, n, scale, out, out_stride, status, s);
   else if (dtype == CP_F16)
-    e = launch<__half>(weight, n_rows, d, weight_stride, ids, n, scale, out, out_stride, status, s);
+    e = launch_embed<__half>(weight, n_rows, d, weight_stride, ids, n, scale, out, out_stride, status, s);
   else
-    e = launch<__nv_bfloat16>(weight, n_rows, d, weight_stride, ids, n, scale, out, out_stride,
+    e = launch_embed<__nv_bfloat16>(weight, n_rows, d, weight_stride, ids, n, scale, out, out_stride,
                               status, s);
   if (e != cudaSuccess) return cpx::cuda_fail(e, "embed launch");
   return CP_OK;

@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(kSmallThreads)
   __shared__ uint16_t pos_s[kSmallMax];
   extern __shared__ uint16_t hist[];             // [warps][bins]
   __shared__ uint32_t total[kMaxBins], warp_sums[32];
+  wait_for_previous();
   let_next_start();
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t key[kRounds], pos[kRounds];
@@ -774,10 +775,9 @@ extern "C" cp_status cp_embed_grad(const void* dy, int dy_dtype, uint64_t dy_str
   int last = 0;
   cudaError_t e = cudaSuccess;
   if (n != 0 && n <= kSmallMax) {
-    sort_small_kernel<<<1, kSmallThreads, (kSmallThreads / 32 << w.bits) * 2, s>>>(
-        ids, static_cast<uint32_t>(n), static_cast<uint32_t>(n_rows), w.passes, w.bits,
-        pairs(w.pairs[0]), status);
-    e = cudaGetLastError();
+    e = launch(Launch{dim3(1), kSmallThreads, static_cast<size_t>(kSmallThreads / 32 << w.bits) * 2, s},
+               &sort_small_kernel, ids, static_cast<uint32_t>(n), static_cast<uint32_t>(n_rows),
+               w.passes, w.bits, pairs(w.pairs[0]), status);
   } else if (n != 0) {
     for (int pass = 0; pass < w.passes && e == cudaSuccess; ++pass) {
       SortPass p;
@@ -792,8 +792,7 @@ extern "C" cp_status cp_embed_grad(const void* dy, int dy_dtype, uint64_t dy_str
       p.shift = static_cast<uint32_t>(pass * w.bits);
       p.bits = w.bits;
       p.status = status;
-      e = launch_after(&sort_count_kernel, dim3(w.tiles), kSortThreads, 0, s, p, kTileCluster,
-                       pass != 0);
+      e = launch_after(&sort_count_kernel, dim3(w.tiles), kSortThreads, 0, s, p, kTileCluster);
       if (e == cudaSuccess)
         e = launch_after(&sort_place_kernel, dim3(w.tiles), kSortThreads,
                          (kSortThreads / 32 << w.bits) * 2, s, p);

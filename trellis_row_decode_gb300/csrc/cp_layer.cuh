@@ -322,31 +322,41 @@ __device__ __forceinline__ void let_next_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Launches a kernel that may start while the one before it on the stream still runs (`overlap`),
-// its CTAs in clusters of `cluster`.
-template <typename P>
-inline cudaError_t launch_after(void (*fn)(P), dim3 grid, int threads, size_t smem, cudaStream_t s,
-                         const P& p, uint32_t cluster = 1, bool overlap = true) {
+// Launches a kernel that may start while the one before it on the stream still runs, its CTAs in
+// clusters of `cluster`.  The kernel waits (wait_for_previous) before it touches memory.
+struct Launch {
+  dim3 grid;
+  int threads;
+  size_t smem = 0;
+  cudaStream_t stream = nullptr;
+  uint32_t cluster = 1;
+};
+
+template <typename... P>
+inline cudaError_t launch(const Launch& l, void (*fn)(P...), P... args) {
   cudaLaunchAttribute attr[2];
   int n = 0;
-  if (overlap) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  if (cluster > 1) {
+  attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  if (l.cluster > 1) {
     attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.x = l.cluster;
     attr[n].val.clusterDim.y = 1;
     attr[n++].val.clusterDim.z = 1;
   }
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
+  cfg.gridDim = l.grid;
+  cfg.blockDim = dim3(l.threads);
+  cfg.dynamicSmemBytes = l.smem;
+  cfg.stream = l.stream;
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, fn, p);
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+template <typename P>
+inline cudaError_t launch_after(void (*fn)(P), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                                const P& p, uint32_t cluster = 1) {
+  return launch(Launch{grid, threads, smem, s, cluster}, fn, P(p));
 }
 
 }  // namespace cpl

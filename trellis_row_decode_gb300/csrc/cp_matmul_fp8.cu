@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(kAnyThreads, 2) matmul_any_kernel(MatmulParams
   const uint32_t wr = (warp >> 1) * 32, wc = (warp & 1) * 32;
   const uint32_t g = lane >> 2, t = lane & 3;
   const uint32_t base = cpt::smem_addr(tile);
+  wait_for_previous();
   uint4 v[kPieces];
   auto fetch = [&](uint32_t k0) {
 #pragma unroll
@@ -247,6 +248,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) matmul_few_kernel(MatmulParams
                             p.w + static_cast<uint64_t>(live[1] ? row0 + g + 8 : 0) * p.ldw};
   const float* sw = p.sw + static_cast<uint64_t>(row0 / 128) * p.groups;
   FewGroup ring[kAhead];
+  wait_for_previous();
   auto fetch = [&](FewGroup& f, uint32_t kb) {
 #pragma unroll
     for (int r = 0; r < 2; ++r)
@@ -351,17 +353,19 @@ __global__ void __launch_bounds__(kFewThreads, 2) matmul_few_kernel(MatmulParams
 
 template <int kTokens, int kAhead, bool kAligned>
 cudaError_t launch_few(const MatmulParams& p, uint32_t splits, cudaStream_t s) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = splits;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = splits;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((p.n + 15) / 16 * splits);
   cfg.blockDim = dim3(kFewThreads);
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = splits == 1 ? 0 : 1;
+  cfg.numAttrs = splits == 1 ? 1 : 2;
   return cudaLaunchKernelEx(&cfg, &matmul_few_kernel<kTokens, kAhead, kAligned>, p, splits);
 }
 
@@ -431,8 +435,8 @@ extern "C" cp_status cp_matmul_fp8(const uint8_t* a, uint64_t a_stride, const fl
   cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&matmul_any_kernel),
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kAnySmem);
   if (e == cudaSuccess) {
-    matmul_any_kernel<<<static_cast<unsigned>(tiles), kAnyThreads, kAnySmem, s>>>(p);
-    e = cudaGetLastError();
+    e = launch_after(&matmul_any_kernel, dim3(static_cast<unsigned>(tiles)), kAnyThreads, kAnySmem, s,
+                     p);
   }
   if (e != cudaSuccess) return cpx::cuda_fail(e, "fp8 matmul launch");
   return CP_OK;

@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   cpt::cluster_sync();
   cpt::tc_fence_after();
+  wait_for_previous();          // (the set-up above runs while the kernel before this one ends)
   const uint32_t tmem = tmem_base;
   const uint32_t kb0 = static_cast<uint32_t>(static_cast<uint64_t>(p.groups) * split / p.splits);
   const uint32_t kb1 =
@@ -460,6 +461,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
   cpt::tc_fence_before();
   __syncthreads();
   cpt::tc_fence_after();
+  wait_for_previous();
   const uint32_t tmem = tmem_base;
   // whole units go to each CTA of the cluster
   const uint32_t units = (p.groups + kPer - 1) / kPer;
@@ -669,8 +671,10 @@ void launch_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, uint32_t 
   cfg->blockDim = dim3(kTcThreads);
   cfg->dynamicSmemBytes = smem;
   cfg->stream = s;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg->attrs = attr;
-  cfg->numAttrs = 1;
+  cfg->numAttrs = 2;
 }
 
 const TcDevice* tc_device(cudaError_t* err) {
@@ -708,7 +712,7 @@ const TcDevice* tc_device(cudaError_t* err) {
   }
   for (int i = 0; i < 3 && *err == cudaSuccess; ++i) {
     cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     launch_config(&cfg, attr, 2u << i, (2u << i) * 64, kSmemMost, nullptr);
     int most = 0;
     *err = cudaOccupancyMaxActiveClusters(&most, reinterpret_cast<const void*>(kTcKernels[7]),
@@ -808,7 +812,7 @@ cp_status launch_pairs(const MatmulParams& q, cudaStream_t s) {
   const uint32_t at_once = static_cast<uint32_t>(d->clusters[splits == 1 ? 0 : splits == 2 ? 1 : 2]);
   const uint32_t clusters = splits > 1 || p.tiles < at_once ? p.tiles : at_once;
   cudaLaunchConfig_t cfg;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   launch_config(&cfg, attr, 2 * splits, 2 * splits * clusters, kSmemMost, s);
   e = cudaLaunchKernelEx(&cfg, kTcKernels[bn / 32 - 1], map_a, map_w, p);
   if (e != cudaSuccess) return cpx::cuda_fail(e, "fp8 matmul launch");
@@ -837,7 +841,7 @@ cp_status launch_thin(const MatmulParams& q, cudaStream_t s) {
     return CP_ERR_CUDA;
   }
   cudaLaunchConfig_t cfg;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   launch_config(&cfg, attr, splits, splits * tiles, kThinSmem, s);
   cfg.blockDim = dim3(kThinThreads);
   auto* fn = kn == 16 ? &matmul_thin_kernel<16> : kn == 32 ? &matmul_thin_kernel<32>

@@ -30,6 +30,7 @@ __global__ void __launch_bounds__(kThreads)
                          uint32_t groups, uint8_t* __restrict__ q, float* __restrict__ scales) {
   const uint32_t sub = threadIdx.x & 15;
   const uint32_t half = (blockIdx.x * kThreads + threadIdx.x) >> 4;
+  wait_for_previous();
   Packed<T> r[kGroups];
 #pragma unroll
   for (int i = 0; i < kGroups; ++i) {
@@ -67,6 +68,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
   const uint32_t bi = blockIdx.x / per_row, bj = blockIdx.x - bi * per_row;
   const uint32_t o = bj * 16 + (threadIdx.x & 15);
   const uint64_t row0 = 128ull * bi + (threadIdx.x >> 4);
+  wait_for_previous();
   Packed<T> r[8];
   uint32_t amax = 0;
 #pragma unroll
@@ -101,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
 }
 
 template <typename T>
-cudaError_t launch(const void* x, uint64_t stride, uint64_t rows, uint32_t d, uint32_t block_rows,
+cudaError_t launch_quantize(const void* x, uint64_t stride, uint64_t rows, uint32_t d, uint32_t block_rows,
                    uint8_t* q, float* scales, cudaStream_t s) {
   const uint32_t per_row = (d + 127) / 128;
   const uint32_t blocks = static_cast<uint32_t>((rows + block_rows - 1) / block_rows) * per_row;
@@ -110,12 +112,11 @@ cudaError_t launch(const void* x, uint64_t stride, uint64_t rows, uint32_t d, ui
   if (block_rows == 1) {
     const uint32_t per_cta = kThreads / 16 * kGroups;
     auto* fn = vec ? &quantize_rows_kernel<T, true> : &quantize_rows_kernel<T, false>;
-    fn<<<(blocks - 1) / per_cta + 1, kThreads, 0, s>>>(p, stride, d, per_row, blocks, q, scales);
-  } else {
-    auto* fn = vec ? &quantize_block_kernel<T, true> : &quantize_block_kernel<T, false>;
-    fn<<<blocks, kThreads, 0, s>>>(p, stride, rows, d, per_row, q, scales);
+    return launch(Launch{dim3((blocks - 1) / per_cta + 1), kThreads, 0, s}, fn, p, stride, d,
+                  per_row, blocks, q, scales);
   }
-  return cudaGetLastError();
+  auto* fn = vec ? &quantize_block_kernel<T, true> : &quantize_block_kernel<T, false>;
+  return launch(Launch{dim3(blocks), kThreads, 0, s}, fn, p, stride, rows, d, per_row, q, scales);
 }
 
 }  // namespace
@@ -138,9 +139,9 @@ extern "C" cp_status cp_quantize_fp8(const void* x, uint64_t x_stride, int dtype
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (dtype == CP_F32) e = launch<float>(x, x_stride, rows, d, block_rows, q, scales, s);
-  else if (dtype == CP_F16) e = launch<__half>(x, x_stride, rows, d, block_rows, q, scales, s);
-  else e = launch<__nv_bfloat16>(x, x_stride, rows, d, block_rows, q, scales, s);
+  if (dtype == CP_F32) e = launch_quantize<float>(x, x_stride, rows, d, block_rows, q, scales, s);
+  else if (dtype == CP_F16) e = launch_quantize<__half>(x, x_stride, rows, d, block_rows, q, scales, s);
+  else e = launch_quantize<__nv_bfloat16>(x, x_stride, rows, d, block_rows, q, scales, s);
   if (e != cudaSuccess) return cpx::cuda_fail(e, "quantize launch");
   return CP_OK;
 }

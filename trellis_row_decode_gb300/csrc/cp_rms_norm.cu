@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(cta_threads(THREADS), norm_ctas(THREADS)) norm
   __shared__ float2 red[2][THREADS <= 32 ? 1 : THREADS / 32];
   const uint32_t tid = threadIdx.x % THREADS;
   const uint32_t octets = (p.d + 7) / 8;
+  wait_for_previous();
   float w[kOct][8];
 #pragma unroll
   for (int i = 0; i < kOct; ++i) {
@@ -331,6 +332,7 @@ __global__ void __launch_bounds__(cta_threads(THREADS), grad_ctas_per_sm(THREADS
   __shared__ float sums[kTeams == 1 ? 1 : THREADS * kOct * 8];
   const uint32_t tid = threadIdx.x % THREADS;
   const uint32_t octets = (p.d + 7) / 8;
+  wait_for_previous();
   float w[kOct][8], dw[kOct][8];
 #pragma unroll
   for (int i = 0; i < kOct; ++i) {
@@ -567,8 +569,8 @@ cudaError_t launch_teams(const NormParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const uint64_t ctas = (static_cast<uint64_t>(p.rows) + kTeams - 1) / kTeams;
   const uint64_t most = kSms * norm_ctas(THREADS);
-  kernel<<<static_cast<unsigned>(ctas < most ? ctas : most), cta_threads(THREADS), kBytes, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(kernel, dim3(static_cast<unsigned>(ctas < most ? ctas : most)),
+                      cta_threads(THREADS), kBytes, s, p);
 }
 
 template <typename T, bool VEC, bool Q>
@@ -603,8 +605,7 @@ cudaError_t launch_grad_teams(const GradParams& p, cudaStream_t s) {
   auto* kernel = &norm_grad_kernel<T, VEC, THREADS, kOct>;
   const cudaError_t e = allow_ring(kernel, kBytes);
   if (e != cudaSuccess) return e;
-  kernel<<<p.ctas, cta_threads(THREADS), kBytes, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(kernel, dim3(p.ctas), cta_threads(THREADS), kBytes, s, p);
 }
 
 template <typename T, bool VEC>
