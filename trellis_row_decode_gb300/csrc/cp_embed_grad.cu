@@ -667,12 +667,14 @@ Plan plan(uint64_t n, uint64_t n_rows, uint32_t d, bool accumulate) {
   w.per_tile = static_cast<uint32_t>((per == 0 ? 1 : per) * kSub);
   w.tiles = static_cast<uint32_t>(up((n + w.per_tile - 1) / w.per_tile, kTileCluster));
   const uint64_t items = accumulate ? n : n + n_rows;
-  // A chunk of 64 items when there are enough of them to fill the warps, down to 16
-  // when there are few (their latency counts); more when there are so many that the
-  // chunks' parts would pass 268 MB of workspace.
+  // A chunk of 64 items when there are enough of them to fill the warps, down to 4 when
+  // there are few and their latency counts (64 lookups of 64 rows: 8.5 us against 10.1 with
+  // 16; 4,096 of 4,096 x 256: 15.3 against 16.5; halving further at 196,608 lookups costs,
+  // 77 us against 58 at d = 8); more when there are so many that the chunks' parts would
+  // pass 268 MB of workspace.
   const uint64_t slabs = (d + kSlab - 1) / kSlab;
   uint64_t per_chunk = 64;
-  while (per_chunk > 16 && items / per_chunk * slabs < 4096) per_chunk /= 2;
+  while (per_chunk > 4 && items / per_chunk * slabs < 4096) per_chunk /= 2;
   while (items / per_chunk * slabs > (1u << 17)) per_chunk *= 2;
   const uint64_t chunks = items == 0 ? 1 : (items + per_chunk - 1) / per_chunk;
   w.per_chunk = static_cast<uint32_t>(per_chunk);
