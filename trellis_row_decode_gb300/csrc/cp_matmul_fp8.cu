@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(kAnyThreads, 2) matmul_any_kernel(MatmulParams
 // order of k on both operands, whatever it is, gives the same sums), several groups ahead.
 // The eight warps' sums are added in order through shared memory, and those of the
 // `splits` CTAs of a cluster, which share the rows when w has few, through theirs.
+// 1 x 1024 x 1024: 2.9 us; bound by latency there, by the warp-level product beyond 10 MB of w.
 
 // Which kernel takes operands on 16-byte boundaries.  Few rows of a and little of w: this one
 // (1 x 1024 x 1024: 3.0 us against the thin kernel's 4.9; 16 x 1024 x 1024: 3.8 against 4.9; with

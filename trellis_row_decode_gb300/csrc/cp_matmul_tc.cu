@@ -32,6 +32,12 @@ using cpm::MatmulParams;
 // running sum cannot stay in tensor memory; the two buffers let the tensor core work on
 // the next group meanwhile.  With few tiles, `splits` pairs of one cluster share a tile's
 // groups and add their sums, in the order of the pairs, through distributed shared memory.
+//
+// 4096 x 4096 x 24576: 348 us in bursts (2.37 PFLOP/s), 374 sustained.  Bound by the summing warps:
+// the tensor core alone takes 225 us (263 sustained, at the power limit), with the loads of
+// tensor memory 250, with the fused multiply-adds 334 (224 of them an SM partition and group,
+// issued at 0.8 a clock), with the loads of the scales 348.  2048^3: 14.0 us, 64 tiles of 16 groups
+// in one turn, of which about 6 us are the start, the first loads and the outputs.
 
 constexpr int kSumWarps = 8;
 constexpr int kTcThreads = (kSumWarps + 4) * 32;       // + the TMA warp, the MMA warp and two idle
@@ -404,10 +410,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 //
 // With at most 128 rows of a the operands change places: 128 rows of w are the tensor core's
 // 128 x 32 operand, up to 64 rows of a its N (16, 32 or 64) columns, and the kernel is bound by
-// the stream of w (a second tile of rows of a finds it in L2).  A unit is 128 columns of tensor memory, 128 / kN groups side by side, so
-// the sums (a lane has a row of w) wait once a unit; two units alternate.  Two CTAs share an
-// SM; `splits` CTAs of a cluster share a tile's groups and add their sums in order through
-// distributed shared memory.
+// the stream of w (a second tile of rows of a finds it in L2).  A unit is 128 columns of tensor
+// memory, 128 / kN groups side by side, so the sums (a lane has a row of w) wait once a unit; two
+// units alternate.  Two CTAs share an SM; `splits` CTAs of a cluster share a tile's groups and
+// add their sums in order through distributed shared memory.
+//
+// 1 x 4096 x 24576: 20.3 us, 101 MB at 5.0 TB/s; 48 rows of a: 23.4 us; 1 x 4096 x 4096: 6.1 us.  The
+// fixed part is about 4 us (launch, tensor maps, the first loads, the exchange); the stream
+// itself runs at the copy rate.
 
 constexpr int kThinThreads = 256;      // four summing warps, TMA, MMA, scales, one idle
 constexpr uint32_t kThinUnit = 128;    // columns of tensor memory
