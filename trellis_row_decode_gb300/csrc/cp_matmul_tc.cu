@@ -4,6 +4,7 @@
 //   out[i][j] = sum over g of sa[i][g] sw[j / 128][g] * (a[i] . w[j] over group g)
 #include <atomic>
 #include <cstdint>
+#include <mutex>
 #include <type_traits>
 
 #include <cuda.h>
@@ -659,10 +660,11 @@ constexpr TcKernel kTcKernels[8] = {      // tiles of 32, 64, .. 256 columns
     &matmul_tc_kernel<10>, &matmul_tc_kernel<12>, &matmul_tc_kernel<14>, &matmul_tc_kernel<16>};
 
 struct TcDevice {
-  std::atomic<int> state{0};           // 0: not asked, 1: usable, 2: not
+  std::atomic<int> state{0};           // 1: found
   int clusters[3] = {0, 0, 0};         // clusters of 2, 4, 8 CTAs that run at once
 };
 TcDevice g_devices[64];
+std::mutex g_device_lock;
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -690,10 +692,12 @@ void launch_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, uint32_t 
 const TcDevice* tc_device(cudaError_t* err) {
   int dev = 0;
   *err = cudaGetDevice(&dev);
-  if (*err != cudaSuccess || dev >= 64) return nullptr;
+  if (*err == cudaSuccess && dev >= 64) *err = cudaErrorInvalidDevice;
+  if (*err != cudaSuccess) return nullptr;
   TcDevice& d = g_devices[dev];
   if (d.state.load(std::memory_order_acquire) == 1) return &d;
-  // several threads may get here at once: each finds the same values
+  const std::lock_guard<std::mutex> one(g_device_lock);
+  if (d.state.load(std::memory_order_acquire) == 1) return &d;
   void* fn = nullptr;
   cudaDriverEntryPointQueryResult found;
   *err = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,

@@ -60,9 +60,6 @@ def _lib():
     return _declared
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
 def _device(t: torch.Tensor, name: str) -> int:
     """The index of t's device, which has to be the current one."""
     dev = t.get_device()
@@ -80,7 +77,7 @@ def _on(t: torch.Tensor, dev: int, name: str) -> int:
 
 def _stream(stream, dev: int) -> int:
     if stream is None:
-        return _raw_stream(dev)
+        return torch._C._cuda_getCurrentRawStream(dev)
     if stream.device_index != dev:
         raise ValueError("stream and tensors must be on the same device")
     return stream.cuda_stream
