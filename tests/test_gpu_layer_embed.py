@@ -63,6 +63,33 @@ def test_embed_strided_views_and_shapes():
         assert bool((buf[:, :8] == 5).all()) and bool((buf[:, 8 + hi - lo:] == 5).all())
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [9, 40, 129])
+def test_rows_that_start_on_any_element(d, dtype):
+    """Every offset of a row's start from a 16-byte boundary, and NaN all around the rows: in
+    embed, and as the rows of dy and of the gradient."""
+    g = gen(d)
+    n_rows, n, pitch = 24, 50, d + 37
+    ids = torch.randint(0, n_rows, (n,), generator=g).cuda()
+    for offset in range(17):
+        def rows(count, seed):
+            buf = torch.full((count * pitch + 32,), float("nan"), dtype=dtype, device="cuda")
+            view = torch.as_strided(buf, (count, d), (pitch, 1), offset)
+            view.copy_(randn(gen(seed), count, d, dtype=dtype))
+            return buf, view
+        _, w = rows(n_rows, offset)
+        buf, out = rows(n, 100)
+        cp.embed(w, ids, out=out)
+        assert torch.equal(out, w[ids])
+        assert int(torch.isnan(buf).sum()) == buf.numel() - n * d      # nothing else written
+        _, dy = rows(n, 200 + offset)
+        gbuf, grad = rows(n_rows, 300)
+        cp.embed_grad(dy, ids, n_rows, out=grad)
+        ref, mags, count = embed_grad64(dy.cpu(), ids.cpu(), n_rows, 1.0)
+        assert_within(grad, ref, (count[:, None] + 2) * U32 * mags + rounded(ref, dtype))
+        assert int(torch.isnan(gbuf).sum()) == gbuf.numel() - n_rows * d
+
+
 def test_embed_special_values_and_empty():
     w = torch.tensor([[float("inf"), float("nan"), -0.0, 1e38]], device="cuda")
     out = cp.embed(w, torch.zeros(2, dtype=torch.int64, device="cuda"), 10.0)

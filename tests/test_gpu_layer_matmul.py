@@ -72,6 +72,19 @@ def test_matmul_strides_and_boundaries(m, lda, ldw, offset):
     assert bool((buf[:, :3] == 7).all()) and bool((buf[:, 3 + n:] == 7).all())
 
 
+@pytest.mark.parametrize("m", [1, 9, 40, 140, 300])
+@pytest.mark.parametrize("k", [1, 250, 385, 500])
+def test_matmul_ignores_what_lies_behind_the_rows(m, k):
+    """Padded rows: the bytes between a row's end and the next row are NaN and stay out."""
+    g = gen(m + k)
+    n, ld = 300, -(-k // 16) * 16 + 32
+    a, sa, w, sw = _operands(g, m, n, k, ld, ld)
+    for t, rows in ((a, m), (w, n)):
+        whole = torch.as_strided(t.view(torch.uint8), (rows, ld), (ld, 1))
+        whole[:, k:] = 0x7F
+    _check(a, sa, w, sw, torch.float32, cp.matmul_fp8(a, sa, w, sw, dtype=torch.float32))
+
+
 @pytest.mark.parametrize("m", [1, 40, 300])
 def test_matmul_broadcast_rows(m):
     """One activation row for all (stride 0)."""

@@ -204,6 +204,24 @@ def test_quantize_matches(m, k, block, dtype):
     _check_q(q, sc, x.double(), block, rel=0)
 
 
+@pytest.mark.parametrize("d", [7, 130, 265])
+def test_e4m3_rows_that_start_on_any_byte(d):
+    """Rows of odd length put the 8-bit output on every byte boundary; an output buffer of the
+    caller's is written to its last byte and no further."""
+    g = gen(d)
+    m = 41
+    x = randn(g, m, d)
+    for offset in range(9):
+        buf = torch.full((m * d + 16,), 0x7F, dtype=torch.uint8, device="cuda")
+        out = buf[offset:offset + m * d].view(m, d).view(E4M3)
+        q, sc = cp.quantize_fp8(x.cuda(), 1, out=out)
+        _check_q(q, sc, x.double(), rel=0)
+        assert bool((buf[:offset] == 0x7F).all()) and bool((buf[offset + m * d:] == 0x7F).all())
+        q, sc = cp.quantize_fp8(x.cuda(), 128, out=out)
+        _check_q(q, sc, x.double(), 128, rel=0)
+        assert bool((buf[:offset] == 0x7F).all()) and bool((buf[offset + m * d:] == 0x7F).all())
+
+
 def test_quantize_extremes_and_views():
     x = torch.zeros(4, 256)
     x[0, :128] = 1e-38                                  # below the smallest amax: zeros
