@@ -486,13 +486,19 @@ cp_status cp_quantize_fp8(const void* x, uint64_t x_stride, int dtype, uint64_t 
  *   w        [n][k] e4m3 bytes, row stride w_stride (a projection's weights).
  *   w_scales [ceil(n / 128)][ceil(k / 128)] fp32, contiguous.
  *   out      [m][n] of out_dtype, row stride out_stride.
- * k = 0 gives zeros.  m, n, k < 2^31.  Rows on 16-byte boundaries (k of any
- * length, pointers and strides multiples of 16) take the tensor-memory kernels.
+ * k = 0 gives zeros.  m, n, k < 2^31.  The tensor-memory kernels want rows on 16-byte
+ * boundaries (k of any length, pointers and strides multiples of 16).  An operand whose
+ * rows lie elsewhere is copied to such rows first, unless a has 16 rows at most and w
+ * 8 MB at most:
+ *   workspace  cp_matmul_fp8_workspace_bytes bytes, 16-byte aligned (0 bytes and NULL
+ *              where nothing is copied).
  */
+uint64_t cp_matmul_fp8_workspace_bytes(const uint8_t* a, uint64_t a_stride, const uint8_t* w,
+                                       uint64_t w_stride, uint64_t m, uint64_t n, uint64_t k);
 cp_status cp_matmul_fp8(const uint8_t* a, uint64_t a_stride, const float* a_scales,
                         const uint8_t* w, uint64_t w_stride, const float* w_scales, uint64_t m,
                         uint64_t n, uint64_t k, void* out, int out_dtype, uint64_t out_stride,
-                        void* stream);
+                        void* workspace, uint64_t workspace_bytes, void* stream);
 
 /*
  * cp_matmul_fp8_status -- synchronise `stream`, then report and clear the current

@@ -85,6 +85,66 @@ def test_matmul_ignores_what_lies_behind_the_rows(m, k):
     _check(a, sa, w, sw, torch.float32, cp.matmul_fp8(a, sa, w, sw, dtype=torch.float32))
 
 
+@pytest.mark.parametrize("m", [17, 130])
+@pytest.mark.parametrize("k", [15, 33, 600, 2049, 4100])
+def test_matmul_rows_on_any_byte(m, k):
+    """Every offset of the rows from a 16-byte boundary, for either operand, NaN around them."""
+    g = gen(m + k)
+    n, kb = 70, -(-k // 128)
+    sa, sw = torch.exp(randn(g, m, kb)).cuda() * 0.01, torch.exp(randn(g, 1, kb)).cuda() * 0.01
+
+    def rows(count, ld, offset):
+        buf = torch.full((count * ld + 32,), 0x7F, dtype=torch.uint8, device="cuda").view(E4M3)
+        view = torch.as_strided(buf, (count, k), (ld, 1), offset)
+        view.copy_((randn(g, count, k) * 60).clamp(-448, 448).to(E4M3))
+        return view
+    even = -(-k // 16) * 16
+    for offset in range(16):
+        pitch = k + 3 * offset + 1
+        for a, w in ((rows(m, pitch, offset), rows(n, even, 0)),
+                     (rows(m, even, 0), rows(n, pitch, offset)),
+                     (rows(m, even + 16, offset), rows(n, pitch, 15 - offset))):
+            ws = cp.matmul_fp8_workspace(a, w)
+            got = cp.matmul_fp8(a, sa, w, sw, dtype=torch.float32, workspace=ws)
+            _check(a, sa, w, sw, torch.float32, got)
+            assert torch.equal(got, cp.matmul_fp8(a, sa, w, sw, dtype=torch.float32))
+
+
+def test_matmul_rows_on_any_byte_in_a_graph_and_refusals():
+    g = gen(5)
+    a, sa, w, sw = _operands(g, 50, 300, 1001)
+    need = (50 + 300) * 1008
+    ws = cp.matmul_fp8_workspace(a, w)
+    assert ws.numel() == need
+    assert cp.matmul_fp8_workspace(a[:, :1], w[:, :1]).numel() == 350 * 16
+    ref = cp.matmul_fp8(a, sa, w, sw)
+    for bad in (ws[1:], ws.view(torch.int8), ws.cpu()):
+        with pytest.raises(ValueError):
+            cp.matmul_fp8(a, sa, w, sw, workspace=bad)
+    with pytest.raises(cp.CPError):                      # not on a 16-byte boundary
+        cp.matmul_fp8(a, sa, w, sw, workspace=torch.empty(need + 8, dtype=torch.uint8,
+                                                          device="cuda")[8:])
+    with pytest.raises(ValueError):
+        cp.matmul_fp8_workspace(a, w[:, :7])
+    out = torch.zeros_like(ref)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cp.matmul_fp8(a, sa, w, sw, out=out)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(ref, out)
+
+
+@pytest.mark.parametrize("m", [1, 20, 300])
+def test_matmul_of_no_columns(m):
+    """k = 0: zeros, and only where the output's rows are."""
+    buf = torch.full((m, 12), 7.0, device="cuda")
+    a, w = torch.empty(m, 0, device="cuda").to(E4M3), torch.empty(5, 0, device="cuda").to(E4M3)
+    cp.matmul_fp8(a, torch.empty(m, 0, device="cuda"), w, torch.empty(1, 0, device="cuda"),
+                  out=buf[:, 3:8])
+    assert not buf[:, 3:8].any() and bool((buf[:, :3] == 7).all()) and bool((buf[:, 8:] == 7).all())
+
+
 @pytest.mark.parametrize("m", [1, 40, 300])
 def test_matmul_broadcast_rows(m):
     """One activation row for all (stride 0)."""

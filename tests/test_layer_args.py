@@ -118,14 +118,31 @@ def test_quantize_arguments(L, p):
 
 
 def test_matmul_arguments(L, p):
-    ok = dict(a=p, la=8, sa=p, w=p, lw=8, sw=p, m=2, n=3, k=8, o=p, t=0, lo=3)
+    ok = dict(a=p, la=8, sa=p, w=p, lw=8, sw=p, m=2, n=3, k=8, o=p, t=0, lo=3, ws=None, wb=0)
 
     def call(**kw):
         a = {**ok, **kw}
         return L.cp_matmul_fp8(a["a"], a["la"], a["sa"], a["w"], a["lw"], a["sw"], a["m"], a["n"],
-                               a["k"], a["o"], a["t"], a["lo"], None)
+                               a["k"], a["o"], a["t"], a["lo"], a["ws"], a["wb"], None)
     for kw in [dict(t=3), dict(la=7), dict(lw=7), dict(lo=2), dict(m=1 << 31), dict(n=1 << 31),
                dict(k=1 << 31), dict(a=None), dict(w=None), dict(sa=None), dict(sw=None),
-               dict(o=None), dict(o=p + 2), dict(sa=p + 2), dict(sw=p + 1)]:
+               dict(o=None), dict(o=p + 2), dict(sa=p + 2), dict(sw=p + 1), dict(m=17),
+               dict(m=17, ws=p, wb=16 * 20 - 1), dict(m=17, ws=p + 8, wb=1 << 20)]:
         assert call(**kw) == BAD, kw
     assert call(m=0) == 0 and call(n=0) == 0
+
+
+def test_matmul_workspace_sizes(L, p):
+    """One 16-byte-aligned copy of each operand whose rows need it, but for few rows of a and
+    little of w."""
+    need = L.cp_matmul_fp8_workspace_bytes
+    assert need(p, 512, p, 512, 300, 200, 500) == 0
+    assert need(p, 500, p, 512, 300, 200, 500) == 300 * 512
+    assert need(p, 512, p + 1, 512, 300, 200, 500) == 200 * 512
+    assert need(p, 0, p, 513, 300, 200, 512) == 500 * 512
+    assert need(p + 8, 500, p, 500, 16, 200, 500) == 0
+    assert need(p, 500, p, 77, 17, 1, 500) == 17 * 512
+    assert need(p, 4096, p, 4097, 16, 4096, 4096) == 4096 * 4096
+    assert need(p, 1, p, 1, 1 << 31, 4, 1) == 0 and need(p, 0, p, 0, 40, 4, 0) == 0
+    assert need(p, (1 << 31) + 1, p, 1, (1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 200) == \
+        2 * ((1 << 31) - 1) * (((1 << 31) - 200 + 15) // 16 * 16)

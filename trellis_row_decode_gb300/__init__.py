@@ -27,7 +27,7 @@ __all__ = [
     "CP_LAYOUT_AOS", "CP_LAYOUT_SOA", "CP_RESIDENT_DEVICE", "CP_RESIDENT_HOST",
     "CP_F32", "CP_F16", "CP_BF16", "embed", "embed_grad", "embed_grad_workspace", "rms_norm",
     "rms_norm_fp8", "rms_norm_grad", "rms_norm_grad_workspace", "quantize_fp8", "matmul_fp8",
-    "matmul_fp8_status",
+    "matmul_fp8_workspace", "matmul_fp8_status",
 ]
 
 _PKG = Path(__file__).resolve().parent
@@ -389,4 +389,5 @@ def lookup_decode_host_noalloc(records: torch.Tensor, n_rows: int, d: int, k: in
 # The memory layer's operators around the lookup-decode (their module uses the names above).
 from .layer import (  # noqa: E402
     CP_BF16, CP_F16, CP_F32, embed, embed_grad, embed_grad_workspace, matmul_fp8, matmul_fp8_status,
-    quantize_fp8, rms_norm, rms_norm_fp8, rms_norm_grad, rms_norm_grad_workspace)
+    matmul_fp8_workspace, quantize_fp8, rms_norm, rms_norm_fp8, rms_norm_grad,
+    rms_norm_grad_workspace)

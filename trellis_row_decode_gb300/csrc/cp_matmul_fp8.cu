@@ -5,6 +5,7 @@
 //
 // The products of a group are exact in the tensor core's fp32 sums; a group's sum is
 // scaled and added to the running fp32 sum before the next group begins.
+#include <algorithm>
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -20,20 +21,6 @@ namespace {
 using namespace cpl;
 using cpm::MatmulParams;
 
-// ---------------------------------------------------- rows on any byte boundary
-//
-// 128 x 64 outputs per CTA, eight warps of 32 x 32.  A group's bytes are loaded as aligned words
-// and shifted into place, widened to fp16 (exact) once on their way to shared memory, and
-// multiplied by the warp-level fp16 product with fp32 sums: widening in front of every e4m3
-// product instead, as the warp-level e4m3 instruction does, took 46 us on 3000 x 700 x 900.
-// The next group's words are in flight while the tensor core works on this one's.
-
-constexpr int kTileRows = 128, kTileCols = 64;           // rows of a and of w per CTA
-constexpr int kAnyThreads = 256;
-constexpr int kPitch = 128 * 2 + 16;                     // shared row pitch: no bank conflicts
-constexpr int kPieces = (kTileRows + kTileCols) * 8 / kAnyThreads;   // 16-byte pieces of a thread
-constexpr int kAnySmem = (kTileRows + kTileCols) * kPitch;
-
 // d = a (16 x 32) * b (32 x 8) + d on the tensor core, e4m3 operands.
 __device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
@@ -44,142 +31,91 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// d = a (16 x 16) * b (16 x 8) + d, fp16 operands.
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                        uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-
-// Sixteen bytes from row + col on, zeros behind the row's k bytes.  Words that reach outside
-// the row are read byte by byte.
+// Sixteen bytes from row + col on, zeros behind the row's k bytes: shifted out of two aligned
+// pieces, or byte by byte where those reach outside the row.
 __device__ __forceinline__ uint4 load_any_piece(const uint8_t* row, uint32_t col, uint32_t k) {
-  uint32_t w[4] = {};
   const uint8_t* p = row + col;
-  const uint32_t skew = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3);
-  if (col >= skew && static_cast<uint64_t>(col) + (skew != 0 ? 20 - skew : 16) <= k) {
-    const uint32_t* q = reinterpret_cast<const uint32_t*>(p - skew);
-    uint32_t x[5];
+  const uint32_t skew = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15);
+  if (col >= skew && static_cast<uint64_t>(col) + (skew != 0 ? 32 - skew : 16) <= k) {
+    const uint4* q = reinterpret_cast<const uint4*>(p - skew);
+    const uint4 lo = __ldg(q), hi = skew != 0 ? __ldg(q + 1) : make_uint4(0, 0, 0, 0);
+    uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (skew & 8) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = __ldg(q + i);
-    x[4] = skew != 0 ? __ldg(q + 4) : 0;
+      for (int i = 0; i < 6; ++i) x[i] = x[i + 2];
+    }
+    if (skew & 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(x[i], x[i + 1], 8 * skew);
-  } else {
-#pragma unroll
-    for (int b = 0; b < 16; ++b)
-      if (static_cast<uint64_t>(col) + b < k) w[b / 4] |= static_cast<uint32_t>(p[b]) << (8 * (b & 3));
+      for (int i = 0; i < 5; ++i) x[i] = x[i + 1];
+    }
+    const uint32_t bits = 8 * (skew & 3);
+    return make_uint4(__funnelshift_r(x[0], x[1], bits), __funnelshift_r(x[1], x[2], bits),
+                      __funnelshift_r(x[2], x[3], bits), __funnelshift_r(x[3], x[4], bits));
   }
+  uint32_t w[4] = {};
+#pragma unroll
+  for (int b = 0; b < 16; ++b)
+    if (static_cast<uint64_t>(col) + b < k) w[b / 4] |= static_cast<uint32_t>(p[b]) << (8 * (b & 3));
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Four e4m3 bytes as fp16.
-__device__ __forceinline__ uint2 widen4(uint32_t w) {
-  const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3);
-  const __half2_raw hi =
-      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
-  return make_uint2(lo.x | static_cast<uint32_t>(lo.y) << 16,
-                    hi.x | static_cast<uint32_t>(hi.y) << 16);
+// ---------------------------------------------------- rows on any byte boundary
+//
+// Tensor maps want rows on 16-byte boundaries.  Operands that lie elsewhere are copied to such
+// rows, zeros behind their ends, in the caller's workspace, in one launch for both; the product
+// starts while the copy ends.  A warp moves 2 KB of a row at a time, four pieces a lane in flight.
+// Bound by memory; the product then costs what it costs on such rows from the start.
+// 101 MB of w: 35 us at 5.8 TB/s read and written; 466 x 827 x 22133: 31.6 us in all, 2048 x 2048 x 2047
+// 17.4 (14.1 for the product of rows on 16-byte boundaries).  A warp-level fp16 product of the shifted
+// bytes, without a copy, ran at 125 TFLOP/s and took 738 and 137.
+
+constexpr int kAlignThreads = 256;
+constexpr uint64_t kAlignCtas = 152 * 6;                  // as many as run at once
+constexpr uint32_t kAlignPieces = 4;                      // 16-byte pieces of a lane
+constexpr uint32_t kAlignBytes = 32 * 16 * kAlignPieces;  // of a row, by one warp at a time
+
+struct AlignOperand {
+  const uint8_t* from;
+  uint8_t* to;
+  uint64_t ld, rows;       // rows: 0 for an operand that stays where it is
+};
+struct AlignParams {
+  AlignOperand of[2];
+  uint32_t k, chunks;      // chunks of kAlignBytes in a row
+  uint64_t pitch;
+};
+
+__global__ void __launch_bounds__(kAlignThreads) align_rows_kernel(AlignParams p) {
+  wait_for_previous();
+  let_next_start();
+  const uint32_t lane = threadIdx.x & 31;
+  const uint64_t warps = static_cast<uint64_t>(gridDim.x) * (kAlignThreads / 32);
+  const uint64_t units = (p.of[0].rows + p.of[1].rows) * p.chunks;
+  for (uint64_t u = static_cast<uint64_t>(blockIdx.x) * (kAlignThreads / 32) + threadIdx.x / 32;
+       u < units; u += warps) {
+    uint64_t row = u / p.chunks;
+    const uint32_t col = static_cast<uint32_t>(u - row * p.chunks) * kAlignBytes + lane * 16;
+    const bool second = row >= p.of[0].rows;
+    if (second) row -= p.of[0].rows;
+    const uint8_t* from = (second ? p.of[1].from : p.of[0].from) +
+                          row * (second ? p.of[1].ld : p.of[0].ld);
+    uint8_t* to = (second ? p.of[1].to : p.of[0].to) + row * p.pitch;
+    uint4 v[kAlignPieces];
+#pragma unroll
+    for (uint32_t i = 0; i < kAlignPieces; ++i)
+      if (col + i * 512 < p.k) v[i] = load_any_piece(from, col + i * 512, p.k);
+#pragma unroll
+    for (uint32_t i = 0; i < kAlignPieces; ++i)
+      if (col + i * 512 < p.k) *reinterpret_cast<uint4*>(to + col + i * 512) = v[i];
+  }
 }
 
-__global__ void __launch_bounds__(kAnyThreads, 2) matmul_any_kernel(MatmulParams p) {
-  extern __shared__ __align__(16) uint8_t tile[];        // rows of a, then rows of w
-  const uint32_t tiles_n = (p.n + kTileCols - 1) / kTileCols;
-  const uint32_t row0 = blockIdx.x / tiles_n * kTileRows, col0 = blockIdx.x % tiles_n * kTileCols;
-  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t wr = (warp >> 1) * 32, wc = (warp & 1) * 32;
-  const uint32_t g = lane >> 2, t = lane & 3;
-  const uint32_t base = cpt::smem_addr(tile);
-  wait_for_previous();
-  uint4 v[kPieces];
-  auto fetch = [&](uint32_t k0) {
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const uint32_t piece = threadIdx.x + i * kAnyThreads, r = piece / 8;
-      const bool of_a = r < kTileRows;
-      const uint32_t row = of_a ? row0 + r : col0 + r - kTileRows;
-      const uint32_t col = k0 + piece % 8 * 16;
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (row < (of_a ? p.m : p.n) && col < p.k)
-        v[i] = load_any_piece(of_a ? p.a + row * p.lda : p.w + row * p.ldw, col, p.k);
-    }
-  };
-  float acc[2][4][4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
-  const float* sw = p.sw + static_cast<uint64_t>(col0 / 128) * p.groups;
-  // this lane's row and half of k in the 16 x 16 (a) and 8 x 16 pairs (w) that ldmatrix loads
-  const uint32_t at_a = base + (wr + (lane & 15)) * kPitch + (lane >> 4) * 16;
-  const uint32_t at_w =
-      base + (kTileRows + wc + (lane & 7) + (lane >> 4) * 8) * kPitch + (lane >> 3 & 1) * 16;
-  if (p.groups != 0) fetch(0);
-  for (uint32_t kb = 0; kb < p.groups; ++kb) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const uint32_t piece = threadIdx.x + i * kAnyThreads;
-      const uint2 a = widen4(v[i].x), b = widen4(v[i].y), c = widen4(v[i].z), d = widen4(v[i].w);
-      uint4* to = reinterpret_cast<uint4*>(tile + piece / 8 * kPitch + piece % 8 * 32);
-      to[0] = make_uint4(a.x, a.y, b.x, b.y);
-      to[1] = make_uint4(c.x, c.y, d.x, d.y);
-    }
-    __syncthreads();
-    if (kb + 1 < p.groups) fetch((kb + 1) * 128);
-    float c[2][4][4] = {};
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
-      uint32_t fa[2][4], fb[2][4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        load_matrices(fa[i], at_a + i * 16 * kPitch + ks * 32);
-        load_matrices(fb[i], at_w + i * 16 * kPitch + ks * 32);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          mma_f16(c[i][j], fa[i], fb[j / 2][j % 2 * 2], fb[j / 2][j % 2 * 2 + 1]);
-    }
-    const float scale_w = __ldg(sw + kb);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t row = row0 + wr + 16 * i + 8 * half + g;
-        const float f =
-            row < p.m ? __ldg(p.sa + static_cast<uint64_t>(row) * p.groups + kb) * scale_w : 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            acc[i][j][2 * half + e] = fmaf(f, c[i][j][2 * half + e], acc[i][j][2 * half + e]);
-      }
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t row = row0 + wr + 16 * i + 8 * (e >> 1) + g;
-        const uint32_t col = col0 + wc + 8 * j + 2 * t + (e & 1);
-        if (row < p.m && col < p.n)
-          store_from_f32(p.out, row * p.ldo + col, p.out_dtype, acc[i][j][e]);
-      }
+// Rows that a tensor map takes (and a row stride of their own: not one row for all).
+bool rows_ok(const void* p, uint64_t stride, uint64_t rows) {
+  return cpx::aligned(p, 16) && (rows == 1 || (stride % 16 == 0 && stride != 0));
 }
+
+uint64_t aligned_pitch(uint64_t k) { return (k + 15) / 16 * 16; }
 
 // ------------------------------------------------------------------- few rows of a
 //
@@ -196,11 +132,13 @@ __global__ void __launch_bounds__(kAnyThreads, 2) matmul_any_kernel(MatmulParams
 // 17 MB of w they are even, 6.3 us, and with 101 MB the thin one leads, 20 us against 28: the
 // warp-level e4m3 product costs about 70 clocks each).  Up to 128 rows of a: the thin kernel
 // (128 x 4096 x 24576: 31 us against the pairs' 42; 128 x 4096 x 4096: 10.8 against 13.7; at 256 rows
-// 54 against 43 and 14.9 against 14.1).  More: the pairs.  Rows on other boundaries: this one for
-// few rows of a whatever the size of w, matmul_any_kernel for more.
+// 54 against 43 and 14.9 against 14.1).  More: the pairs.  Rows on other boundaries: the same rule, with
+// align_rows_kernel in front of the thin kernel and the pairs (1 x 4096 x 4097: 12.2 us against 11.0
+// here; 16 x 4096 x 24577: 55 against 103).
 constexpr uint32_t kFewRows = 16;
 constexpr uint64_t kFewBytes = 8 << 20;
 constexpr uint32_t kThinRows = 128;
+constexpr uint64_t kMost = 1ull << 31;                   // m, n and k stay below
 constexpr int kFewThreads = 256;
 constexpr uint32_t kFewWarps = kFewThreads / 32;
 
@@ -388,11 +326,25 @@ cp_status launch_few(const MatmulParams& p, bool aligned, cudaStream_t s) {
 
 }  // namespace
 
+namespace {
+bool few_rows(uint64_t m, uint64_t n, uint64_t k) { return m <= kFewRows && n * k <= kFewBytes; }
+}  // namespace
+
+extern "C" uint64_t cp_matmul_fp8_workspace_bytes(const uint8_t* a, uint64_t a_stride,
+                                                  const uint8_t* w, uint64_t w_stride, uint64_t m,
+                                                  uint64_t n, uint64_t k) {
+  if (m >= kMost || n >= kMost || k >= kMost - 128 || m == 0 || n == 0 || k == 0 ||
+      few_rows(m, n, k))
+    return 0;
+  return ((rows_ok(a, a_stride, m) ? 0 : m) + (rows_ok(w, w_stride, n) ? 0 : n)) *
+         aligned_pitch(k);
+}
+
 extern "C" cp_status cp_matmul_fp8(const uint8_t* a, uint64_t a_stride, const float* a_scales,
                                    const uint8_t* w, uint64_t w_stride, const float* w_scales,
                                    uint64_t m, uint64_t n, uint64_t k, void* out, int out_dtype,
-                                   uint64_t out_stride, void* stream) {
-  constexpr uint64_t kMost = 1ull << 31;
+                                   uint64_t out_stride, void* workspace, uint64_t workspace_bytes,
+                                   void* stream) {
   if (!dtype_ok(out_dtype) || m >= kMost || n >= kMost || k >= kMost - 128 || out_stride < n ||
       (a_stride < k && a_stride != 0) || (w_stride < k && w_stride != 0)) {
     cpx::set_error("bad out_dtype, m, n, k or row stride");
@@ -419,26 +371,42 @@ extern "C" cp_status cp_matmul_fp8(const uint8_t* a, uint64_t a_stride, const fl
                  static_cast<uint32_t>((k + 127) / 128),
                  out_dtype};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // Tensor maps want 16-byte boundaries (and a row stride of their own: not one row for all).
-  if (k != 0 && cpx::aligned(a, 16) && cpx::aligned(w, 16) &&
-      (m == 1 || (a_stride % 16 == 0 && a_stride != 0)) &&
-      (n == 1 || (w_stride % 16 == 0 && w_stride != 0)))
-    return m > kThinRows                          ? cpm::launch_pairs(p, s)
-           : m <= kFewRows && n * k <= kFewBytes ? launch_few(p, true, s)
-                                                 : cpm::launch_thin(p, s);
-  if (m <= kFewRows) return launch_few(p, false, s);
-  const uint64_t tiles =
-      ((m + kTileRows - 1) / kTileRows) * ((n + kTileCols - 1) / kTileCols);
-  if (tiles >= kMost) {
-    cpx::set_error("m and n make more than 2^31 tiles");
-    return CP_ERR_INVALID_ARG;
+  if (k == 0) {                      // sums over nothing; zero is all zero bits in each type
+    const uint64_t size = dtype_size(out_dtype);
+    const cudaError_t e = cudaMemset2DAsync(out, out_stride * size, 0, n * size, m, s);
+    return e == cudaSuccess ? CP_OK : cpx::cuda_fail(e, "fp8 matmul, k = 0");
   }
-  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&matmul_any_kernel),
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kAnySmem);
-  if (e == cudaSuccess) {
-    e = launch_after(&matmul_any_kernel, dim3(static_cast<unsigned>(tiles)), kAnyThreads, kAnySmem, s,
-                     p);
+  const bool a_ok = rows_ok(a, a_stride, m), w_ok = rows_ok(w, w_stride, n);
+  if (few_rows(m, n, k))
+    return launch_few(p, a_ok && w_ok, s);
+  const uint64_t need = cp_matmul_fp8_workspace_bytes(a, a_stride, w, w_stride, m, n, k);
+  if (need != 0) {
+    if (workspace == nullptr || !cpx::aligned(workspace, 16) || workspace_bytes < need) {
+      cpx::set_error("workspace must be 16-byte aligned and hold cp_matmul_fp8_workspace_bytes bytes");
+      return CP_ERR_INVALID_ARG;
+    }
+    AlignParams c{};
+    c.k = p.k;
+    c.pitch = aligned_pitch(k);
+    c.chunks = (p.k + kAlignBytes - 1) / kAlignBytes;
+    uint8_t* to = static_cast<uint8_t*>(workspace);
+    if (!a_ok) {
+      c.of[0] = AlignOperand{a, to, a_stride, m};
+      p.a = to;
+      p.lda = c.pitch;
+      to += m * c.pitch;
+    }
+    if (!w_ok) {
+      c.of[1] = AlignOperand{w, to, w_stride, n};
+      p.w = to;
+      p.ldw = c.pitch;
+    }
+    const uint64_t units = (c.of[0].rows + c.of[1].rows) * c.chunks;
+    const uint64_t ctas = (units + kAlignThreads / 32 - 1) / (kAlignThreads / 32);
+    const cudaError_t e =
+        launch_after(&align_rows_kernel, dim3(static_cast<unsigned>(std::min(ctas, kAlignCtas))),
+                     kAlignThreads, 0, s, c);
+    if (e != cudaSuccess) return cpx::cuda_fail(e, "fp8 matmul launch");
   }
-  if (e != cudaSuccess) return cpx::cuda_fail(e, "fp8 matmul launch");
-  return CP_OK;
+  return m > kThinRows ? cpm::launch_pairs(p, s) : cpm::launch_thin(p, s);
 }

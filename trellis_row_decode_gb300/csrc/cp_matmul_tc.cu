@@ -117,6 +117,33 @@ __device__ __forceinline__ void store16(const TcParams& p, uint32_t row, uint32_
   }
 }
 
+// Columns col to end, 32 at most, of the warp's 32 rows, where out's rows lie on no useful boundary: transposed by
+// five exchanges between lanes, so that each store writes 32 consecutive outputs of one row
+// (3000 x 700 x 900: 15.8 us, by each lane's single outputs of its own row 31.1; 3393 x 3777 x 384
+// in fp32: 40 against 83).
+__device__ __forceinline__ void store_transposed(const TcParams& p, uint32_t row0, uint32_t col,
+                                                 uint32_t end, uint32_t lane, float (&x)[32]) {
+#pragma unroll
+  for (uint32_t s = 16; s > 0; s /= 2) {
+    const bool high = (lane & s) != 0;
+#pragma unroll
+    for (uint32_t i = 0; i < 32; ++i) {
+      if ((i & s) == 0) {
+        const float got = __shfl_xor_sync(0xFFFFFFFFu, high ? x[i] : x[i + s], s);
+        x[i] = high ? got : x[i];
+        x[i + s] = high ? x[i + s] : got;
+      }
+    }
+  }
+  if (col + lane < end) {
+    const uint32_t rows = min(p.m - row0, 32u);
+    const uint64_t at = static_cast<uint64_t>(row0) * p.ldo + col + lane;
+#pragma unroll
+    for (uint32_t r = 0; r < 32; ++r)
+      if (r < rows) store_from_f32(p.out, at + r * p.ldo, p.out_dtype, x[r]);
+  }
+}
+
 // f(std::integral_constant) for 0 .. kCount - 1.
 template <uint32_t kCount, typename F, uint32_t kFrom = 0>
 __device__ __forceinline__ void static_for(F&& f) {
@@ -350,7 +377,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (!ok) break;
       if (p.splits == 1) {
-        if (any && row < p.m) {
+        if (any && p.out_align == 0) {
+          static_for<kChunks>([&](auto chunk) {
+            constexpr uint32_t c = decltype(chunk)::value;
+            constexpr uint32_t kHere = kShare - 32 * c < 32 ? kShare - 32 * c : 32;
+            float x[32];
+#pragma unroll
+            for (uint32_t i = 0; i < 32; ++i)
+              x[i] = i < kHere ? acc[32 * c + (i < kHere ? i : 0)] : 0.0f;
+            const uint32_t from = col + 32 * c;
+            if (from < p.n) store_transposed(p, row0, from, min(p.n, from + kHere), lane, x);
+          });
+        } else if (any && row < p.m) {
 #pragma unroll
           for (uint32_t c = 0; c < kEights; c += 2)
             if (col + 8 * c < p.n) store16(p, row, col + 8 * c, acc + 8 * c);

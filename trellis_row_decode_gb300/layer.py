@@ -23,7 +23,7 @@ from . import CP_ERR_INVALID_ARG, CPError, _check, lib
 
 __all__ = ["CP_F32", "CP_F16", "CP_BF16", "embed", "embed_grad", "embed_grad_workspace",
            "rms_norm", "rms_norm_fp8", "rms_norm_grad", "rms_norm_grad_workspace",
-           "quantize_fp8", "matmul_fp8", "matmul_fp8_status"]
+           "quantize_fp8", "matmul_fp8", "matmul_fp8_workspace", "matmul_fp8_status"]
 
 CP_F32, CP_F16, CP_BF16 = 0, 1, 2
 _CODE = {torch.float32: CP_F32, torch.float16: CP_F16, torch.bfloat16: CP_BF16}
@@ -50,7 +50,10 @@ def _lib():
         L.cp_rms_norm_grad.argtypes = [vp, u64, vp, u64, vp, u64, i32, vp, i32, u64, u32, f32, vp,
                                        vp, vp, u64, vp]
         L.cp_quantize_fp8.argtypes = [vp, u64, i32, u64, u32, u32, vp, vp, vp]
-        L.cp_matmul_fp8.argtypes = [vp, u64, vp, vp, u64, vp, u64, u64, u64, vp, i32, u64, vp]
+        L.cp_matmul_fp8_workspace_bytes.argtypes = [vp, u64, vp, u64, u64, u64, u64]
+        L.cp_matmul_fp8_workspace_bytes.restype = u64
+        L.cp_matmul_fp8.argtypes = [vp, u64, vp, vp, u64, vp, u64, u64, u64, vp, i32, u64, vp, u64,
+                                    vp]
         L.cp_matmul_fp8_status.argtypes = [vp]
         L.cp_matmul_fp8_status.restype = i32
         for f in (L.cp_embed, L.cp_embed_grad, L.cp_rms_norm, L.cp_rms_norm_fp8,
@@ -362,10 +365,13 @@ def _scaled(t: torch.Tensor, scales: torch.Tensor, block: int, dev: int, name: s
 
 def matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
                dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
-               stream=None) -> torch.Tensor:
+               workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """a @ w.T for a [m, k] and w [n, k] in float8_e4m3fn with scales for each block of 128
     along k (a_scales [m, ceil(k/128)], w_scales [ceil(n/128), ceil(k/128)], fp32), summed in
-    fp32 and rounded once to `dtype`."""
+    fp32 and rounded once to `dtype`.
+
+    Rows that do not start on 16-byte boundaries are copied to such rows in `workspace`
+    (matmul_fp8_workspace; allocated where it is not given), but for the smallest products."""
     dev = _device(a, "a")
     m, k, lda = _scaled(a, a_scales, 1, dev, "a")
     n, kw, ldw = _scaled(w, w_scales, 128, dev, "w")
@@ -377,11 +383,29 @@ def matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scale
     else:
         code = _float(out.dtype, "the output")
         ldo = _check_out(out, (m, n), out.dtype, dev, "out")
-    _check(_lib().cp_matmul_fp8(a.data_ptr(), lda, _on(a_scales, dev, "a_scales"),
-                                _on(w, dev, "w"), ldw, _on(w_scales, dev, "w_scales"), m, n, k,
-                                out.data_ptr(), code, ldo, _stream(stream, dev)),
+    pa, pw, ws = a.data_ptr(), _on(w, dev, "w"), None
+    if (pa | pw | lda | ldw) & 15 or lda == 0 or ldw == 0:
+        nbytes = _lib().cp_matmul_fp8_workspace_bytes(pa, lda, pw, ldw, m, n, k)
+        if nbytes:
+            ws = _workspace(workspace, nbytes, a, dev, stream)
+    _check(_lib().cp_matmul_fp8(pa, lda, _on(a_scales, dev, "a_scales"), pw, ldw,
+                                _on(w_scales, dev, "w_scales"), m, n, k, out.data_ptr(), code, ldo,
+                                None if ws is None else ws.data_ptr(),
+                                0 if ws is None else ws.numel(), _stream(stream, dev)),
            "cp_matmul_fp8")
     return out
+
+
+def matmul_fp8_workspace(a: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
+    """A workspace for matmul_fp8 calls on these operands (uint8; empty where nothing has to be
+    copied)."""
+    dev = _device(a, "a")
+    m, k, lda = _rows(a, "a")
+    n, kw, ldw = _rows(w, "w")
+    if kw != k:
+        raise ValueError("a and w must have the same number of columns")
+    nbytes = _lib().cp_matmul_fp8_workspace_bytes(a.data_ptr(), lda, _on(w, dev, "w"), ldw, m, n, k)
+    return torch.empty(int(nbytes), dtype=torch.uint8, device=a.device)
 
 
 def matmul_fp8_status(stream=None) -> int:
