@@ -133,6 +133,24 @@ __device__ __forceinline__ Packed<T> zero_octet() {
   return r;
 }
 
+// The octet that starts `skew` bytes into the words x.
+template <typename T>
+__device__ __forceinline__ Packed<T> shift_octet(uint32_t (&x)[Packed<T>::kWords + 4], uint32_t skew) {
+  if (skew & 8) {
+#pragma unroll
+    for (int i = 0; i < Packed<T>::kWords + 2; ++i) x[i] = x[i + 2];
+  }
+  if (skew & 4) {
+#pragma unroll
+    for (int i = 0; i < Packed<T>::kWords + 1; ++i) x[i] = x[i + 1];
+  }
+  Packed<T> r;
+#pragma unroll
+  for (int i = 0; i < Packed<T>::kWords; ++i)
+    r.w[i] = sizeof(T) == 4 ? x[i] : __funnelshift_r(x[i], x[i + 1], 8 * (skew & 2));
+  return r;
+}
+
 // Octet `o` of a row of d elements at p.  VEC: rows whose every octet is whole and aligned to its
 // own size.  Otherwise rows start anywhere and the last octet may be part full (the rest reads
 // as zero and is not written): an octet is shifted out of the aligned 16-byte words that hold
@@ -159,17 +177,7 @@ __device__ __forceinline__ Packed<T> load_skewed_octet(const T* row, uint32_t o,
       x[4 * q + 2] = v.z;
       x[4 * q + 3] = v.w;
     }
-    if (skew & 8) {
-#pragma unroll
-      for (int i = 0; i < 4 * kQuads + 2; ++i) x[i] = x[i + 2];
-    }
-    if (skew & 4) {
-#pragma unroll
-      for (int i = 0; i < 4 * kQuads + 1; ++i) x[i] = x[i + 1];
-    }
-#pragma unroll
-    for (int i = 0; i < Packed<T>::kWords; ++i)
-      r.w[i] = sizeof(T) == 4 ? x[i] : __funnelshift_r(x[i], x[i + 1], 8 * (skew & 2));
+    r = shift_octet<T>(x, skew);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

@@ -145,32 +145,63 @@ constexpr bool norm_ring(int threads) { return threads == 1024 || threads <= 16;
 // four, 32.0 from registers; the forward, with fewer values to hold, 20.6 us from registers and
 // 22.6 through shared memory, except in teams of 1024 (64 registers a thread; 1024 x 16384: 25.1
 // against 28.4) and of a few lanes (100000 x 128: 17.0 against 18.3).
-constexpr int stage_bytes(int arrays, int oct, int threads, int elt) {
-  return arrays * oct * cta_threads(threads) * 8 * elt;
+// Rows on other boundaries travel as the aligned 16-byte words that hold their bytes, one more an
+// octet, and are shifted into place on the way back (the gradient of 1707 x 4626 bf16: 33.5 us, 64.8
+// with loads to registers; forward, 19011 x 812: 38.4 against 51.9).
+template <typename T, bool VEC>
+constexpr int slot_bytes() {
+  return 8 * static_cast<int>(sizeof(T)) + (VEC ? 0 : 16);
+}
+constexpr int stage_bytes(int arrays, int oct, int threads, int slot) {
+  return arrays * oct * cta_threads(threads) * slot;
 }
 constexpr int stages_of(int ctas, int stage) {
   return 196608 / (ctas * stage) >= 3 ? 3 : 196608 / (ctas * stage);
 }
 
-template <typename T>
-__device__ __forceinline__ void copy_octet(uint32_t to, const T* from) {
+// Octet `o` of a row of d elements.  A row that starts off a 16-byte boundary: the first word
+// reaches up to 14 bytes in front of it, which are dropped (they lie in the row's allocation:
+// allocations start on 256-byte boundaries); behind the row's end nothing is read, zeros stand there.
+template <typename T, bool VEC>
+__device__ __forceinline__ void copy_octet(uint32_t to, const T* row, uint32_t o, uint32_t d) {
+  if constexpr (VEC) {
+    const uint8_t* from = reinterpret_cast<const uint8_t*>(row + 8ull * o);
 #pragma unroll
-  for (uint32_t b = 0; b < 8 * sizeof(T); b += 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + b),
-                 "l"(reinterpret_cast<const uint8_t*>(from) + b)
-                 : "memory");
+    for (uint32_t b = 0; b < 8 * sizeof(T); b += 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + b), "l"(from + b)
+                   : "memory");
+  } else {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + 8ull * o);
+    const uint32_t skew = static_cast<uint32_t>(at & 15);
+    const uint32_t left = skew + (d - 8 * o) * static_cast<uint32_t>(sizeof(T));
+#pragma unroll
+    for (uint32_t b = 0; b < 8 * sizeof(T) + 16; b += 16) {
+      const uint32_t bytes = left <= b ? 0 : min(left - b, 16u);
+      // (a word without a byte of the row is not read: its address is the row's own)
+      const uintptr_t from = at - skew + (bytes == 0 ? 0 : b);
+      if (b < 8 * sizeof(T) || skew != 0)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(to + b), "l"(from),
+                     "r"(bytes)
+                     : "memory");
+    }
+  }
 }
-template <typename T>
-__device__ __forceinline__ Packed<T> copied_octet(const uint8_t* at) {
+template <typename T, bool VEC>
+__device__ __forceinline__ Packed<T> copied_octet(const uint8_t* at, const T* row) {
+  uint32_t x[Packed<T>::kWords + 4];
+#pragma unroll
+  for (int q = 0; q < Packed<T>::kWords / 4 + (VEC ? 0 : 1); ++q) {
+    const uint4 v = reinterpret_cast<const uint4*>(at)[q];
+    x[4 * q] = v.x;
+    x[4 * q + 1] = v.y;
+    x[4 * q + 2] = v.z;
+    x[4 * q + 3] = v.w;
+  }
+  if constexpr (!VEC)
+    return shift_octet<T>(x, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 15));
   Packed<T> r;
 #pragma unroll
-  for (int q = 0; q < Packed<T>::kWords / 4; ++q) {
-    const uint4 x = reinterpret_cast<const uint4*>(at)[q];
-    r.w[4 * q] = x.x;
-    r.w[4 * q + 1] = x.y;
-    r.w[4 * q + 2] = x.z;
-    r.w[4 * q + 3] = x.w;
-  }
+  for (int i = 0; i < Packed<T>::kWords; ++i) r.w[i] = x[i];
   return r;
 }
 
@@ -192,12 +223,13 @@ __global__ void __launch_bounds__(cta_threads(THREADS), norm_ctas(THREADS)) norm
       for (int e = 0; e < 8; ++e) w[i][e] = 0.0f;
     }
   }
-  constexpr int kStage = stage_bytes(2, kOct, THREADS, sizeof(T));
-  constexpr int kStages = VEC && norm_ring(THREADS) ? stages_of(norm_ctas(THREADS), kStage) : 1;
+  constexpr int kStage = stage_bytes(2, kOct, THREADS, slot_bytes<T, VEC>());
+  constexpr int kStages =
+      !VEC || norm_ring(THREADS) ? stages_of(norm_ctas(THREADS), kStage) : 1;
   constexpr bool kRing = kStages >= 2;
-  constexpr uint32_t kOctet = 8 * sizeof(T);
+  constexpr uint32_t kSlot = slot_bytes<T, VEC>(), kArray = cta_threads(THREADS) * kSlot;
   extern __shared__ __align__(16) uint8_t ring[];
-  uint8_t* mine_ring = ring + threadIdx.x * kOctet;
+  uint8_t* mine_ring = ring + threadIdx.x * kSlot;
   const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(mine_ring));
   Packed<T> xn[kOct], rn[kOct];        // the next row (or, with the ring, this one)
   auto fetch = [&](uint64_t row, int stage) {
@@ -208,10 +240,9 @@ __global__ void __launch_bounds__(cta_threads(THREADS), norm_ctas(THREADS)) norm
       const uint32_t o = tid + i * THREADS;
       const bool in = row < p.rows && o < octets;
       if constexpr (kRing) {
-        const uint32_t at = ring_at + stage * kStage + 2 * i * cta_threads(THREADS) * kOctet;
-        if (in) copy_octet(at, x + 8ull * o);
-        if (in && p.residual != nullptr)
-          copy_octet(at + cta_threads(THREADS) * kOctet, res + 8ull * o);
+        const uint32_t at = ring_at + stage * kStage + 2 * i * kArray;
+        if (in) copy_octet<T, VEC>(at, x, o, p.d);
+        if (in && p.residual != nullptr) copy_octet<T, VEC>(at + kArray, res, o, p.d);
       } else {
         xn[i] = in ? load_row_octet<T, VEC>(x, o, p.d) : zero_octet<T>();
         rn[i] = in && p.residual != nullptr ? load_row_octet<T, VEC>(res, o, p.d) : zero_octet<T>();
@@ -232,12 +263,14 @@ __global__ void __launch_bounds__(cta_threads(THREADS), norm_ctas(THREADS)) norm
     if constexpr (kRing) {
       fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
+      const T* res = static_cast<const T*>(p.residual) + row * p.residual_stride;
 #pragma unroll
       for (int i = 0; i < kOct; ++i) {
         const bool in = row < p.rows && tid + i * THREADS < octets;
-        const uint8_t* from = mine_ring + stage * kStage + 2 * i * cta_threads(THREADS) * kOctet;
-        xn[i] = in ? copied_octet<T>(from) : zero_octet<T>();
-        rn[i] = in && p.residual != nullptr ? copied_octet<T>(from + cta_threads(THREADS) * kOctet)
+        const uint8_t* from = mine_ring + stage * kStage + 2 * i * kArray;
+        xn[i] = in ? copied_octet<T, VEC>(from, x) : zero_octet<T>();
+        rn[i] = in && p.residual != nullptr ? copied_octet<T, VEC>(from + kArray, res)
                                             : zero_octet<T>();
       }
       stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -345,12 +378,12 @@ __global__ void __launch_bounds__(cta_threads(THREADS), grad_ctas_per_sm(THREADS
     for (int e = 0; e < 8; ++e) w[i][e] = dw[i][e] = 0.0f;
     if (o < octets) load_weight<VEC>(p.weight, p.weight_dtype, o, p.d, w[i]);
   }
-  constexpr int kStage = stage_bytes(3, kOct, THREADS, sizeof(T));
-  constexpr int kStages = VEC ? stages_of(grad_ctas_per_sm(THREADS), kStage) : 1;
+  constexpr int kStage = stage_bytes(3, kOct, THREADS, slot_bytes<T, VEC>());
+  constexpr int kStages = stages_of(grad_ctas_per_sm(THREADS), kStage);
   constexpr bool kRing = kStages >= 2;
-  constexpr uint32_t kOctet = 8 * sizeof(T), kArray = cta_threads(THREADS) * kOctet;
+  constexpr uint32_t kSlot = slot_bytes<T, VEC>(), kArray = cta_threads(THREADS) * kSlot;
   extern __shared__ __align__(16) uint8_t ring[];
-  uint8_t* mine_ring = ring + threadIdx.x * kOctet;
+  uint8_t* mine_ring = ring + threadIdx.x * kSlot;
   const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(mine_ring));
   Packed<T> hn[kOct], gn[kOct], rn[kOct];          // the next row (or, with the ring, this one)
   auto fetch = [&](uint64_t row, int stage) {
@@ -364,9 +397,9 @@ __global__ void __launch_bounds__(cta_threads(THREADS), grad_ctas_per_sm(THREADS
       if constexpr (kRing) {
         const uint32_t at = ring_at + stage * kStage + 3 * i * kArray;
         if (in) {
-          copy_octet(at, h + 8ull * o);
-          copy_octet(at + kArray, dy + 8ull * o);
-          if (p.dres != nullptr) copy_octet(at + 2 * kArray, res + 8ull * o);
+          copy_octet<T, VEC>(at, h, o, p.d);
+          copy_octet<T, VEC>(at + kArray, dy, o, p.d);
+          if (p.dres != nullptr) copy_octet<T, VEC>(at + 2 * kArray, res, o, p.d);
         }
       } else {
         hn[i] = in ? load_row_octet<T, VEC>(h, o, p.d) : zero_octet<T>();
@@ -397,13 +430,17 @@ __global__ void __launch_bounds__(cta_threads(THREADS), grad_ctas_per_sm(THREADS
     if constexpr (kRing) {
       fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      const T* hr = static_cast<const T*>(p.h) + row * p.h_stride;
+      const T* dyr = static_cast<const T*>(p.dy) + row * p.dy_stride;
+      const T* res = static_cast<const T*>(p.dres) + row * p.dres_stride;
 #pragma unroll
       for (int i = 0; i < kOct; ++i) {
         const bool in = row < p.rows && tid + i * THREADS < octets;
         const uint8_t* from = mine_ring + stage * kStage + 3 * i * kArray;
-        hn[i] = in ? copied_octet<T>(from) : zero_octet<T>();
-        gn[i] = in ? copied_octet<T>(from + kArray) : zero_octet<T>();
-        rn[i] = in && p.dres != nullptr ? copied_octet<T>(from + 2 * kArray) : zero_octet<T>();
+        hn[i] = in ? copied_octet<T, VEC>(from, hr) : zero_octet<T>();
+        gn[i] = in ? copied_octet<T, VEC>(from + kArray, dyr) : zero_octet<T>();
+        rn[i] = in && p.dres != nullptr ? copied_octet<T, VEC>(from + 2 * kArray, res)
+                                        : zero_octet<T>();
       }
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
@@ -565,8 +602,9 @@ cudaError_t allow_ring(K* kernel, int bytes) {
 template <typename T, bool VEC, bool Q, int THREADS, int kOct>
 cudaError_t launch_teams(const NormParams& p, cudaStream_t s) {
   constexpr int kTeams = cta_threads(THREADS) / THREADS;
-  constexpr int kStage = stage_bytes(2, kOct, THREADS, sizeof(T));
-  constexpr int kStages = VEC && norm_ring(THREADS) ? stages_of(norm_ctas(THREADS), kStage) : 1;
+  constexpr int kStage = stage_bytes(2, kOct, THREADS, slot_bytes<T, VEC>());
+  constexpr int kStages =
+      !VEC || norm_ring(THREADS) ? stages_of(norm_ctas(THREADS), kStage) : 1;
   constexpr int kBytes = kStages >= 2 ? kStages * kStage : 0;
   auto* kernel = &norm_kernel<T, VEC, Q, THREADS, kOct>;
   const cudaError_t e = allow_ring(kernel, kBytes);
@@ -603,8 +641,8 @@ cudaError_t launch_norm(const NormParams& p, bool vec, cudaStream_t s) {
 
 template <typename T, bool VEC, int THREADS, int kOct>
 cudaError_t launch_grad_teams(const GradParams& p, cudaStream_t s) {
-  constexpr int kStage = stage_bytes(3, kOct, THREADS, sizeof(T));
-  constexpr int kStages = VEC ? stages_of(grad_ctas_per_sm(THREADS), kStage) : 1;
+  constexpr int kStage = stage_bytes(3, kOct, THREADS, slot_bytes<T, VEC>());
+  constexpr int kStages = stages_of(grad_ctas_per_sm(THREADS), kStage);
   constexpr int kBytes = kStages >= 2 ? kStages * kStage : 0;
   auto* kernel = &norm_grad_kernel<T, VEC, THREADS, kOct>;
   const cudaError_t e = allow_ring(kernel, kBytes);
