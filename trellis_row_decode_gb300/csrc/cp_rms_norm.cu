@@ -138,32 +138,40 @@ constexpr int grad_ctas_per_sm(int threads) { return ctas_of(512, threads); }
 constexpr bool norm_ring(int threads) { return threads == 1024 || threads <= 16; }
 
 // Rows on octet boundaries travel through shared memory: a thread copies its own octets of the
-// coming rows there (asynchronously, 192 KB an SM in all) and reads them back itself, so it
+// coming rows there (asynchronously, up to 216 KB an SM in all) and reads them back itself, so it
 // waits for nobody and no registers hold what is under way.  Bytes of one row's octets of
 // `arrays` arrays, and the rows that fit; one row or less: they wait in registers instead.
 // Measured, 4096 x 4096 bf16: the gradient takes 28.4 us with three rows under way, 29.8 with
 // four, 32.0 from registers; the forward, with fewer values to hold, 20.6 us from registers and
 // 22.6 through shared memory, except in teams of 1024 (64 registers a thread; 1024 x 16384: 25.1
 // against 28.4) and of a few lanes (100000 x 128: 17.0 against 18.3).
-// Rows on other boundaries travel as the aligned 16-byte words that hold their bytes, one more an
-// octet, and are shifted into place on the way back (the gradient of 1707 x 4626 bf16: 33.5 us, 64.8
-// with loads to registers; forward, 19011 x 812: 38.4 against 51.9).
-template <typename T, bool VEC>
-constexpr int slot_bytes() {
-  return 8 * static_cast<int>(sizeof(T)) + (VEC ? 0 : 16);
+// Rows on other boundaries travel as the aligned 16-byte words that hold their bytes, one word more
+// for each team or warp, and are shifted into place on the way back.  1707 x 4626 bf16: the
+// gradient takes 31.2 us (64.8 with loads to registers), the forward 21.7; 19011 x 812: forward 37.0
+// (51.9), gradient 39.5; 4096 x 4095 fp32: gradient 81 (116).
+constexpr int lanes_of(int threads) { return threads < 32 ? threads : 32; }
+template <typename T, bool VEC, int THREADS>
+constexpr int array_bytes() {          // one array's octets, one of each thread of the CTA
+  return cta_threads(THREADS) * 8 * static_cast<int>(sizeof(T)) +
+         (VEC ? 0 : cta_threads(THREADS) / lanes_of(THREADS) * 16);
 }
-constexpr int stage_bytes(int arrays, int oct, int threads, int slot) {
-  return arrays * oct * cta_threads(threads) * slot;
+template <typename T, bool VEC, int THREADS>
+constexpr int stage_bytes(int arrays, int oct) {
+  return arrays * oct * array_bytes<T, VEC, THREADS>();
 }
+constexpr int kRingBytes = 216 << 10;    // of an SM
 constexpr int stages_of(int ctas, int stage) {
-  return 196608 / (ctas * stage) >= 3 ? 3 : 196608 / (ctas * stage);
+  return kRingBytes / (ctas * stage) >= 3 ? 3 : kRingBytes / (ctas * stage);
 }
 
 // Octet `o` of a row of d elements.  A row that starts off a 16-byte boundary: the first word
 // reaches up to 14 bytes in front of it, which are dropped (they lie in the row's allocation:
-// allocations start on 256-byte boundaries); behind the row's end nothing is read, zeros stand there.
+// allocations start on 256-byte boundaries); behind the row's end nothing is read, zeros stand
+// there.  `last`: the lane that also copies the word behind its octet, the others find it at
+// their neighbour's.
 template <typename T, bool VEC>
-__device__ __forceinline__ void copy_octet(uint32_t to, const T* row, uint32_t o, uint32_t d) {
+__device__ __forceinline__ void copy_octet(uint32_t to, const T* row, uint32_t o, uint32_t d,
+                                           bool last) {
   if constexpr (VEC) {
     const uint8_t* from = reinterpret_cast<const uint8_t*>(row + 8ull * o);
 #pragma unroll
@@ -171,17 +179,17 @@ __device__ __forceinline__ void copy_octet(uint32_t to, const T* row, uint32_t o
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + b), "l"(from + b)
                    : "memory");
   } else {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(row + 8ull * o);
-    const uint32_t skew = static_cast<uint32_t>(at & 15);
-    const uint32_t left = skew + (d - 8 * o) * static_cast<uint32_t>(sizeof(T));
+    const uint32_t skew = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 15);
+    const uintptr_t first = reinterpret_cast<uintptr_t>(row) - skew;
+    const uint32_t end = skew + d * static_cast<uint32_t>(sizeof(T));     // of the row, from `first`
 #pragma unroll
     for (uint32_t b = 0; b < 8 * sizeof(T) + 16; b += 16) {
-      const uint32_t bytes = left <= b ? 0 : min(left - b, 16u);
+      const uint32_t at = 8 * static_cast<uint32_t>(sizeof(T)) * o + b;
+      const uint32_t bytes = end <= at ? 0 : min(end - at, 16u);
       // (a word without a byte of the row is not read: its address is the row's own)
-      const uintptr_t from = at - skew + (bytes == 0 ? 0 : b);
-      if (b < 8 * sizeof(T) || skew != 0)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(to + b), "l"(from),
-                     "r"(bytes)
+      if (b < 8 * sizeof(T) || last)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + b),
+                     "l"(first + (bytes == 0 ? 0 : at)), "r"(bytes)
                      : "memory");
     }
   }
@@ -204,6 +212,12 @@ __device__ __forceinline__ Packed<T> copied_octet(const uint8_t* at, const T* ro
   for (int i = 0; i < Packed<T>::kWords; ++i) r.w[i] = x[i];
   return r;
 }
+// Where a thread's octets lie in an array of a stage.
+template <typename T, bool VEC, int THREADS>
+__device__ __forceinline__ uint32_t slot_of() {
+  constexpr uint32_t kLanes = lanes_of(THREADS);
+  return threadIdx.x * 8 * static_cast<uint32_t>(sizeof(T)) + (VEC ? 0 : threadIdx.x / kLanes * 16);
+}
 
 template <typename T, bool VEC, bool Q, int THREADS, int kOct>
 __global__ void __launch_bounds__(cta_threads(THREADS), norm_ctas(THREADS)) norm_kernel(NormParams p) {
@@ -223,13 +237,14 @@ __global__ void __launch_bounds__(cta_threads(THREADS), norm_ctas(THREADS)) norm
       for (int e = 0; e < 8; ++e) w[i][e] = 0.0f;
     }
   }
-  constexpr int kStage = stage_bytes(2, kOct, THREADS, slot_bytes<T, VEC>());
+  constexpr int kStage = stage_bytes<T, VEC, THREADS>(2, kOct);
   constexpr int kStages =
       !VEC || norm_ring(THREADS) ? stages_of(norm_ctas(THREADS), kStage) : 1;
   constexpr bool kRing = kStages >= 2;
-  constexpr uint32_t kSlot = slot_bytes<T, VEC>(), kArray = cta_threads(THREADS) * kSlot;
+  constexpr uint32_t kArray = array_bytes<T, VEC, THREADS>();
+  const bool last = threadIdx.x % lanes_of(THREADS) == lanes_of(THREADS) - 1;
   extern __shared__ __align__(16) uint8_t ring[];
-  uint8_t* mine_ring = ring + threadIdx.x * kSlot;
+  uint8_t* mine_ring = ring + slot_of<T, VEC, THREADS>();
   const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(mine_ring));
   Packed<T> xn[kOct], rn[kOct];        // the next row (or, with the ring, this one)
   auto fetch = [&](uint64_t row, int stage) {
@@ -241,8 +256,10 @@ __global__ void __launch_bounds__(cta_threads(THREADS), norm_ctas(THREADS)) norm
       const bool in = row < p.rows && o < octets;
       if constexpr (kRing) {
         const uint32_t at = ring_at + stage * kStage + 2 * i * kArray;
-        if (in) copy_octet<T, VEC>(at, x, o, p.d);
-        if (in && p.residual != nullptr) copy_octet<T, VEC>(at + kArray, res, o, p.d);
+        if (in || (!VEC && row < p.rows && o == octets)) {
+          copy_octet<T, VEC>(at, x, o, p.d, last);
+          if (p.residual != nullptr) copy_octet<T, VEC>(at + kArray, res, o, p.d, last);
+        }
       } else {
         xn[i] = in ? load_row_octet<T, VEC>(x, o, p.d) : zero_octet<T>();
         rn[i] = in && p.residual != nullptr ? load_row_octet<T, VEC>(res, o, p.d) : zero_octet<T>();
@@ -261,8 +278,10 @@ __global__ void __launch_bounds__(cta_threads(THREADS), norm_ctas(THREADS)) norm
   for (uint64_t at = lead; at < p.rows; at += step, turn ^= 1) {
     const uint64_t row = at + mine;
     if constexpr (kRing) {
+      if constexpr (!VEC) __syncwarp();        // the neighbour has read what is overwritten now
       fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      if constexpr (!VEC) __syncwarp();        // (a word behind an octet is the neighbour's copy)
       const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
       const T* res = static_cast<const T*>(p.residual) + row * p.residual_stride;
 #pragma unroll
@@ -378,12 +397,13 @@ __global__ void __launch_bounds__(cta_threads(THREADS), grad_ctas_per_sm(THREADS
     for (int e = 0; e < 8; ++e) w[i][e] = dw[i][e] = 0.0f;
     if (o < octets) load_weight<VEC>(p.weight, p.weight_dtype, o, p.d, w[i]);
   }
-  constexpr int kStage = stage_bytes(3, kOct, THREADS, slot_bytes<T, VEC>());
+  constexpr int kStage = stage_bytes<T, VEC, THREADS>(3, kOct);
   constexpr int kStages = stages_of(grad_ctas_per_sm(THREADS), kStage);
   constexpr bool kRing = kStages >= 2;
-  constexpr uint32_t kSlot = slot_bytes<T, VEC>(), kArray = cta_threads(THREADS) * kSlot;
+  constexpr uint32_t kArray = array_bytes<T, VEC, THREADS>();
+  const bool last = threadIdx.x % lanes_of(THREADS) == lanes_of(THREADS) - 1;
   extern __shared__ __align__(16) uint8_t ring[];
-  uint8_t* mine_ring = ring + threadIdx.x * kSlot;
+  uint8_t* mine_ring = ring + slot_of<T, VEC, THREADS>();
   const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(mine_ring));
   Packed<T> hn[kOct], gn[kOct], rn[kOct];          // the next row (or, with the ring, this one)
   auto fetch = [&](uint64_t row, int stage) {
@@ -396,10 +416,10 @@ __global__ void __launch_bounds__(cta_threads(THREADS), grad_ctas_per_sm(THREADS
       const bool in = row < p.rows && o < octets;
       if constexpr (kRing) {
         const uint32_t at = ring_at + stage * kStage + 3 * i * kArray;
-        if (in) {
-          copy_octet<T, VEC>(at, h, o, p.d);
-          copy_octet<T, VEC>(at + kArray, dy, o, p.d);
-          if (p.dres != nullptr) copy_octet<T, VEC>(at + 2 * kArray, res, o, p.d);
+        if (in || (!VEC && row < p.rows && o == octets)) {
+          copy_octet<T, VEC>(at, h, o, p.d, last);
+          copy_octet<T, VEC>(at + kArray, dy, o, p.d, last);
+          if (p.dres != nullptr) copy_octet<T, VEC>(at + 2 * kArray, res, o, p.d, last);
         }
       } else {
         hn[i] = in ? load_row_octet<T, VEC>(h, o, p.d) : zero_octet<T>();
@@ -428,8 +448,10 @@ __global__ void __launch_bounds__(cta_threads(THREADS), grad_ctas_per_sm(THREADS
   for (uint64_t at = lead; at < p.rows; at += step, turn ^= 1) {
     const uint64_t row = at + mine;
     if constexpr (kRing) {
+      if constexpr (!VEC) __syncwarp();        // the neighbour has read what is overwritten now
       fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      if constexpr (!VEC) __syncwarp();        // (a word behind an octet is the neighbour's copy)
       const T* hr = static_cast<const T*>(p.h) + row * p.h_stride;
       const T* dyr = static_cast<const T*>(p.dy) + row * p.dy_stride;
       const T* res = static_cast<const T*>(p.dres) + row * p.dres_stride;
@@ -602,7 +624,7 @@ cudaError_t allow_ring(K* kernel, int bytes) {
 template <typename T, bool VEC, bool Q, int THREADS, int kOct>
 cudaError_t launch_teams(const NormParams& p, cudaStream_t s) {
   constexpr int kTeams = cta_threads(THREADS) / THREADS;
-  constexpr int kStage = stage_bytes(2, kOct, THREADS, slot_bytes<T, VEC>());
+  constexpr int kStage = stage_bytes<T, VEC, THREADS>(2, kOct);
   constexpr int kStages =
       !VEC || norm_ring(THREADS) ? stages_of(norm_ctas(THREADS), kStage) : 1;
   constexpr int kBytes = kStages >= 2 ? kStages * kStage : 0;
@@ -615,6 +637,9 @@ cudaError_t launch_teams(const NormParams& p, cudaStream_t s) {
                       cta_threads(THREADS), kBytes, s, p);
 }
 
+// Teams just wide enough: 96, 192 and 384 threads between the powers of two keep more rows under
+// way (bf16, 10900 x 1536: 19.8 us against 21.7; 6500 x 2560: 20.8 against 24.4; 2700 x 6144: 20.2
+// against 25.5).
 template <typename T, bool VEC, bool Q>
 cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
   const uint32_t octets = (p.d + 7) / 8;
@@ -624,8 +649,11 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
   if (octets <= 32) return launch_teams<T, VEC, Q, 32, 1>(p, s);
   if (octets <= 64) return launch_teams<T, VEC, Q, 32, 2>(p, s);
   if (octets <= 128) return launch_teams<T, VEC, Q, 64, 2>(p, s);
+  if (octets <= 192) return launch_teams<T, VEC, Q, 96, 2>(p, s);
   if (octets <= 256) return launch_teams<T, VEC, Q, 128, 2>(p, s);
+  if (octets <= 384) return launch_teams<T, VEC, Q, 192, 2>(p, s);
   if (octets <= 512) return launch_teams<T, VEC, Q, 256, 2>(p, s);
+  if (octets <= 768) return launch_teams<T, VEC, Q, 384, 2>(p, s);
   if (octets <= 1024) return launch_teams<T, VEC, Q, 512, 2>(p, s);
   if (octets <= 2048) return launch_teams<T, VEC, Q, 1024, 2>(p, s);
   norm_wide_kernel<T, VEC, Q><<<p.rows, 1024, 0, s>>>(p);
@@ -641,7 +669,7 @@ cudaError_t launch_norm(const NormParams& p, bool vec, cudaStream_t s) {
 
 template <typename T, bool VEC, int THREADS, int kOct>
 cudaError_t launch_grad_teams(const GradParams& p, cudaStream_t s) {
-  constexpr int kStage = stage_bytes(3, kOct, THREADS, slot_bytes<T, VEC>());
+  constexpr int kStage = stage_bytes<T, VEC, THREADS>(3, kOct);
   constexpr int kStages = stages_of(grad_ctas_per_sm(THREADS), kStage);
   constexpr int kBytes = kStages >= 2 ? kStages * kStage : 0;
   auto* kernel = &norm_grad_kernel<T, VEC, THREADS, kOct>;
