@@ -143,6 +143,24 @@ def test_embed_grad_types(din, dout, d):
     _check_grad(randn(g, 700, d, dtype=din, std=0.1), ids, 90, 2.0, dout)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d,gap", [(1, 0), (25, 0), (25, 3), (200, 8), (255, 0), (256, 0),
+                                   (257, 0), (601, 0), (601, 5), (520, 1)])
+def test_embed_grad_clears_the_rows_that_no_id_names(d, gap, dtype):
+    """Narrow and wide rows, with and without a gap, on any boundary; nothing around them."""
+    g = gen(d + gap)
+    n_rows, ids = 700, torch.tensor([5, 698, 5, 300, 301, -1])
+    dy = randn(g, 6, d, dtype=dtype)
+    ref, mags, count = embed_grad64(dy, ids, n_rows, 1.0)
+    bound = (count[:, None] + 2) * U32 * mags + rounded(ref, dtype)
+    for offset in (0, 1, 8, 15):
+        buf = torch.full((n_rows * (d + gap) + 32,), float("nan"), dtype=dtype, device="cuda")
+        out = torch.as_strided(buf, (n_rows, d), (d + gap, 1), offset)
+        cp.embed_grad(dy.cuda(), ids.cuda(), n_rows, out=out)
+        assert_within(out, ref, bound)
+        assert int(torch.isnan(buf).sum()) == buf.numel() - n_rows * d
+
+
 def test_embed_grad_many_tiles():
     """More ids than one sub-tile per sort tile (2.2e6), and keys of four digits."""
     g = gen(5)

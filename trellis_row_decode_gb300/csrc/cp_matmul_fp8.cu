@@ -65,9 +65,9 @@ __device__ __forceinline__ uint4 load_any_piece(const uint8_t* row, uint32_t col
 // rows, zeros behind their ends, in the caller's workspace, in one launch for both; the product
 // starts while the copy ends.  A warp moves 2 KB of a row at a time, four pieces a lane in flight.
 // Bound by memory; the product then costs what it costs on such rows from the start.
-// 101 MB of w: 35 us at 5.8 TB/s read and written; 466 x 827 x 22133: 31.6 us in all, 2048 x 2048 x 2047
-// 17.4 (14.1 for the product of rows on 16-byte boundaries).  A warp-level fp16 product of the shifted
-// bytes, without a copy, ran at 125 TFLOP/s and took 738 and 137.
+// 101 MB of w: 35 us at 5.8 TB/s read and written; 466 x 827 x 22133: 31.6 us in all,
+// 2048 x 2048 x 2047 17.4 (14.1 for the product of rows on 16-byte boundaries).  A warp-level fp16
+// product of the shifted bytes, without a copy, ran at 125 TFLOP/s and took 738 and 137.
 
 constexpr int kAlignThreads = 256;
 constexpr uint64_t kAlignCtas = 152 * 6;                  // as many as run at once
@@ -132,9 +132,9 @@ uint64_t aligned_pitch(uint64_t k) { return (k + 15) / 16 * 16; }
 // 17 MB of w they are even, 6.3 us, and with 101 MB the thin one leads, 20 us against 28: the
 // warp-level e4m3 product costs about 70 clocks each).  Up to 128 rows of a: the thin kernel
 // (128 x 4096 x 24576: 31 us against the pairs' 42; 128 x 4096 x 4096: 10.8 against 13.7; at 256 rows
-// 54 against 43 and 14.9 against 14.1).  More: the pairs.  Rows on other boundaries: the same rule, with
-// align_rows_kernel in front of the thin kernel and the pairs (1 x 4096 x 4097: 12.2 us against 11.0
-// here; 16 x 4096 x 24577: 55 against 103).
+// 54 against 43 and 14.9 against 14.1).  More: the pairs.  Rows on other boundaries: the
+// same rule, with align_rows_kernel in front of the thin kernel and the pairs (1 x 4096 x 4097:
+// 12.2 us against 11.0 here; 16 x 4096 x 24577: 55 against 103).
 constexpr uint32_t kFewRows = 16;
 constexpr uint64_t kFewBytes = 8 << 20;
 constexpr uint32_t kThinRows = 128;

@@ -117,8 +117,8 @@ __device__ __forceinline__ void store16(const TcParams& p, uint32_t row, uint32_
   }
 }
 
-// Columns col to end, 32 at most, of the warp's 32 rows, where out's rows lie on no useful boundary: transposed by
-// five exchanges between lanes, so that each store writes 32 consecutive outputs of one row
+// Columns col to end, 32 at most, of the warp's 32 rows, where out's rows lie on no useful
+// boundary: transposed by five exchanges between lanes, so that each store writes 32 consecutive outputs of one row
 // (3000 x 700 x 900: 15.8 us, by each lane's single outputs of its own row 31.1; 3393 x 3777 x 384
 // in fp32: 40 against 83).
 __device__ __forceinline__ void store_transposed(const TcParams& p, uint32_t row0, uint32_t col,

@@ -164,54 +164,6 @@ constexpr int stages_of(int ctas, int stage) {
   return kRingBytes / (ctas * stage) >= 3 ? 3 : kRingBytes / (ctas * stage);
 }
 
-// Octet `o` of a row of d elements.  A row that starts off a 16-byte boundary: the first word
-// reaches up to 14 bytes in front of it, which are dropped (they lie in the row's allocation:
-// allocations start on 256-byte boundaries); behind the row's end nothing is read, zeros stand
-// there.  `last`: the lane that also copies the word behind its octet, the others find it at
-// their neighbour's.
-template <typename T, bool VEC>
-__device__ __forceinline__ void copy_octet(uint32_t to, const T* row, uint32_t o, uint32_t d,
-                                           bool last) {
-  if constexpr (VEC) {
-    const uint8_t* from = reinterpret_cast<const uint8_t*>(row + 8ull * o);
-#pragma unroll
-    for (uint32_t b = 0; b < 8 * sizeof(T); b += 16)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + b), "l"(from + b)
-                   : "memory");
-  } else {
-    const uint32_t skew = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 15);
-    const uintptr_t first = reinterpret_cast<uintptr_t>(row) - skew;
-    const uint32_t end = skew + d * static_cast<uint32_t>(sizeof(T));     // of the row, from `first`
-#pragma unroll
-    for (uint32_t b = 0; b < 8 * sizeof(T) + 16; b += 16) {
-      const uint32_t at = 8 * static_cast<uint32_t>(sizeof(T)) * o + b;
-      const uint32_t bytes = end <= at ? 0 : min(end - at, 16u);
-      // (a word without a byte of the row is not read: its address is the row's own)
-      if (b < 8 * sizeof(T) || last)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + b),
-                     "l"(first + (bytes == 0 ? 0 : at)), "r"(bytes)
-                     : "memory");
-    }
-  }
-}
-template <typename T, bool VEC>
-__device__ __forceinline__ Packed<T> copied_octet(const uint8_t* at, const T* row) {
-  uint32_t x[Packed<T>::kWords + 4];
-#pragma unroll
-  for (int q = 0; q < Packed<T>::kWords / 4 + (VEC ? 0 : 1); ++q) {
-    const uint4 v = reinterpret_cast<const uint4*>(at)[q];
-    x[4 * q] = v.x;
-    x[4 * q + 1] = v.y;
-    x[4 * q + 2] = v.z;
-    x[4 * q + 3] = v.w;
-  }
-  if constexpr (!VEC)
-    return shift_octet<T>(x, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 15));
-  Packed<T> r;
-#pragma unroll
-  for (int i = 0; i < Packed<T>::kWords; ++i) r.w[i] = x[i];
-  return r;
-}
 // Where a thread's octets lie in an array of a stage.
 template <typename T, bool VEC, int THREADS>
 __device__ __forceinline__ uint32_t slot_of() {
