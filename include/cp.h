@@ -366,6 +366,8 @@ cp_status cp_measure_record_read(const void* table, uint64_t table_bytes, uint32
  *     view into a wider array).  Outputs do not overlap inputs, except where a
  *     call says so.  Any length is accepted; whole octets (rows whose every
  *     eight elements lie on a boundary of eight elements) run on wide loads.
+ *     Of a row that starts elsewhere, the bytes between the 16-byte boundary in
+ *     front of it and its start may be read too (never used).
  *   - Sums and statistics are fp32, in an order fixed by the shapes (and, for
  *     cp_embed_grad, the ids): the same call gives the same bits.
  * ---------------------------------------------------------------------- */
