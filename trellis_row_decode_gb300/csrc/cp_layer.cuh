@@ -337,7 +337,7 @@ __device__ __forceinline__ uint2 quantize_octet(const float (&v)[8], float inv) 
   return make_uint2(w[0], w[1]);
 }
 
-// VEC: q rows 8-byte aligned with whole octets.
+// VEC: q rows 8-byte aligned with whole octets.  8 o < d < 2^32.
 template <bool VEC>
 __device__ __forceinline__ void store_q_octet(uint8_t* row, uint32_t o, uint32_t d, uint2 q) {
   uint8_t* to = row + 8ull * o;
@@ -345,7 +345,7 @@ __device__ __forceinline__ void store_q_octet(uint8_t* row, uint32_t o, uint32_t
     *reinterpret_cast<uint2*>(to) = q;
     return;
   }
-  if (8 * o + 8 > d) {
+  if (d - 8 * o < 8) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (8 * o + i < d) to[i] = static_cast<uint8_t>((i < 4 ? q.x : q.y) >> (8 * (i & 3)));

@@ -29,7 +29,8 @@ __global__ void __launch_bounds__(kThreads)
     quantize_rows_kernel(const T* __restrict__ x, uint64_t stride, uint32_t d, uint32_t per_row,
                          uint32_t groups, uint8_t* __restrict__ q, float* __restrict__ scales) {
   const uint32_t sub = threadIdx.x & 15;
-  const uint32_t half = (blockIdx.x * kThreads + threadIdx.x) >> 4;
+  // (below 2^29: at most 2^31 groups; the thread's own index would pass 32 bits)
+  const uint32_t half = blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);
   wait_for_previous();
   Packed<T> r[kGroups];
 #pragma unroll
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
 template <typename T>
 cudaError_t launch_quantize(const void* x, uint64_t stride, uint64_t rows, uint32_t d, uint32_t block_rows,
                    uint8_t* q, float* scales, cudaStream_t s) {
-  const uint32_t per_row = (d + 127) / 128;
+  const uint32_t per_row = static_cast<uint32_t>((static_cast<uint64_t>(d) + 127) / 128);
   const uint32_t blocks = static_cast<uint32_t>((rows + block_rows - 1) / block_rows) * per_row;
   const bool vec = octets_ok(x, stride, d, sizeof(T)) && cpx::aligned(q, 8);
   const T* p = static_cast<const T*>(x);
