@@ -54,3 +54,18 @@ def test_quantize_a_row_of_almost_2_32_columns(block):
         got = q[:, lo:hi].cpu().float().double() * spread
         step = torch.maximum(ref.abs() * 2.0 ** -4, spread * 2.0 ** -10)
         assert_within(got, ref, step * (1 + 1e-5) + ref.abs() * 8 * U32, "values")
+
+
+def test_rows_of_2_32_columns_are_refused():
+    """The library takes a row's length in 32 bits; a longer row is no row of length mod 2^32."""
+    d = (1 << 32) + 128
+    x = torch.empty(1, d, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(128, device="cuda")
+    ids = torch.zeros(1, dtype=torch.int64, device="cuda")
+    for call in [lambda: cp.quantize_fp8(x), lambda: cp.quantize_fp8(x, 128),
+                 lambda: cp.rms_norm(x, w), lambda: cp.rms_norm(x[0], w),
+                 lambda: cp.rms_norm_fp8(x, w), lambda: cp.rms_norm_fp8(x.view(1, 1, d), w),
+                 lambda: cp.rms_norm_grad(x, x, w), lambda: cp.embed(x, ids),
+                 lambda: cp.embed_grad(x, ids, 1)]:
+        with pytest.raises(ValueError):
+            call()

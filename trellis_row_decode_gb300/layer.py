@@ -101,12 +101,21 @@ def _float(dtype: torch.dtype, name: str) -> int:
     return code
 
 
+def _u32(value: int, name: str) -> int:
+    """A size that the library takes in 32 bits: ctypes would cut a larger one without a word."""
+    if not 0 <= value < 1 << 32:
+        raise ValueError(f"{name} must be at least 0 and below 2^32")
+    return value
+
+
 def _rows(t: torch.Tensor, name: str) -> tuple[int, int, int]:
     """(rows, d, row stride) of t with its leading dimensions merged (as a view)."""
     shape, strides = t.shape, t.stride()
+    if len(shape) == 0:
+        raise ValueError(f"{name} must have at least one dimension")
+    if shape[-1] >> 32:
+        raise ValueError(f"{name}'s rows must be shorter than 2^32")
     if len(shape) != 2:
-        if len(shape) == 0:
-            raise ValueError(f"{name} must have at least one dimension")
         if len(shape) == 1:
             if shape[0] > 1 and strides[0] != 1:
                 raise ValueError(f"{name} must have unit stride in its last dimension")
@@ -194,7 +203,7 @@ def embed(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0,
 
 def embed_grad_workspace(n: int, n_rows: int, d: int) -> torch.Tensor:
     """A workspace for embed_grad calls of these sizes (uint8, on the current device)."""
-    nbytes = int(_lib().cp_embed_grad_workspace_bytes(n, n_rows, d))
+    nbytes = int(_lib().cp_embed_grad_workspace_bytes(n, n_rows, _u32(d, "d")))
     if nbytes == 0 and (n or n_rows):
         raise CPError(CP_ERR_INVALID_ARG, "cp_embed_grad_workspace_bytes")
     return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
@@ -216,7 +225,7 @@ def embed_grad(dy: torch.Tensor, ids: torch.Tensor, n_rows: int, scale: float = 
     dev = _device(dy, "dy")
     n = _ids(ids)
     rows, d, dy_stride = _rows(dy, "dy")
-    if group < 1 or rows * group != n:
+    if _u32(group, "group") < 1 or rows * group != n:
         raise ValueError("dy must have one row for each `group` ids")
     if out is None:
         if accumulate:
@@ -296,7 +305,7 @@ def rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
 
 def rms_norm_grad_workspace(rows: int, d: int) -> torch.Tensor:
     """A workspace for rms_norm_grad calls of these sizes (uint8, on the current device)."""
-    nbytes = int(_lib().cp_rms_norm_grad_workspace_bytes(rows, d))
+    nbytes = int(_lib().cp_rms_norm_grad_workspace_bytes(rows, _u32(d, "d")))
     if nbytes == 0:
         raise CPError(CP_ERR_INVALID_ARG, "cp_rms_norm_grad_workspace_bytes")
     return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
