@@ -232,6 +232,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) matmul_few_kernel(MatmulParams
       if (kb < p.groups) {
         const FewRows<kTokens> now = rows;
         fetch_rows(kb + step);
+        __syncwarp();                // (a lane's pieces at a row's end take a branch of their own)
 #pragma unroll
         for (int n = 0; n < kTokens; ++n) {
           float c[4] = {};

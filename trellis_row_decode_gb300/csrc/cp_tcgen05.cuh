@@ -40,7 +40,10 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
+// All threads of the cluster.  The aligned form wants each warp converged: lanes may come from
+// branches of their own (guarded stores, a flag that some of them set), so the warp joins first.
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
