@@ -14,6 +14,7 @@
 #include "cp_internal.h"
 #include "cp_layer.cuh"
 #include "cp_matmul_fp8.h"
+#include "cp_ring.h"
 #include "cp_tcgen05.cuh"
 
 namespace {
@@ -186,8 +187,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                      const __grid_constant__ CUtensorMap map_w, const TcParams p) {
   constexpr uint32_t kBn = kEights * 16, kShare = kEights * 8;
   extern __shared__ uint8_t dyn[];
-  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 4];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5];
   __shared__ uint32_t tmem_base;
+  __shared__ uint32_t issued;              // this CTA's fills of stages
   __shared__ int gave_up;
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -197,6 +199,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t stage_bytes = kTileA + kBn * 64;
   const uint32_t full = cpt::smem_addr(bars), empty = full + 8 * kMaxStages;
   const uint32_t acc_full = empty + 8 * kMaxStages, acc_empty = acc_full + 16;
+  const uint32_t drained = acc_empty + 16;
   // the first CTA's barriers hold the pair's loads and reads
   const uint32_t pair_full = cpt::map_rank(full, first);
   const uint32_t pair_acc_empty = cpt::map_rank(acc_empty, first);
@@ -210,6 +213,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       cpt::mbar_init(acc_full + 8 * b, 1);
       cpt::mbar_init(acc_empty + 8 * b, 2 * kSumWarps);
     }
+    cpt::mbar_init(drained, 1);
     cpt::mbar_init_fence();
     gave_up = 0;
   }
@@ -224,6 +228,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t kb1 =
       static_cast<uint32_t>(static_cast<uint64_t>(p.groups) * (split + 1) / p.splits);
   const uint32_t step = gridDim.x / (2 * p.splits), tile0 = blockIdx.x / (2 * p.splits);
+  // Every warp of the cluster comes here when its role ends.  If a wait of the pair's first CTA ran
+  // out, whichever warp's, what the pair has in flight then ends before either CTA leaves its shared
+  // and tensor memory (the second waits at the cluster's last barrier): loads up to the last fill
+  // that either CTA began, all of which count on the first CTA's barriers, and every product
+  // issued.  These waits have a limit too, one for each of the two warps that see to them; a fill
+  // that only one CTA began runs it out, and has landed by then.  Where the first CTA has not given
+  // up, its summing warps have seen every product done, so nothing is in flight.
+  auto end_role = [&] {
+    __syncwarp();
+    cpt::tc_fence_before();
+    asm volatile("barrier.sync 1, %0;" ::"n"(kTcThreads) : "memory");
+    cpt::cluster_sync();
+  };
 
   if (warp >= kSumWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -236,7 +253,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       __syncwarp();
       const uint32_t w_bytes = kBn * 64;
-      uint32_t s = 0, round = 0;
+      uint32_t s = 0, round = 0, fills = 0;
       bool ok = true;
       for (uint32_t tile = tile0; tile < p.tiles && ok; tile += step) {
         const uint32_t tile_n = tile / p.tiles_m;
@@ -258,19 +275,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                pair_full + 8 * s);
           }
           __syncwarp();
+          ++fills;
           if (++s == p.stages) {
             s = 0;
             ++round;
           }
         }
       }
-      // Given up: the loads in flight land before the CTA leaves (stages s.. of the round
-      // before, stages ..s of this one).
-      if (!ok && half == 0) {
-        int unused = 0;
+      if (lane == 0) issued = fills;
+      end_role();
+      if (gave_up != 0 && half == 0) {
+        const uint32_t other = cpt::load_cluster1(cpt::map_rank(cpt::smem_addr(&issued), rank + 1));
+        int late = 0;
         for (uint32_t k = 0; k < p.stages; ++k) {
-          const uint32_t r = k < s ? round : round - 1;
-          if (k < s || round > 0) cpt::mbar_wait(full + 8 * k, r & 1, &unused);
+          const LastFill last = last_fill(fills, other, p.stages, k);
+          if (last.any) cpt::mbar_wait(full + 8 * k, last.parity, &late);
         }
       }
     } else if (warp == kSumWarps + 1 && half == 0) {
@@ -302,6 +321,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
       }
+      end_role();
+      if (gave_up != 0) {
+        int late = 0;
+        if (cpt::elect_one()) cpt::mma_commit_pair(drained, static_cast<uint16_t>(1u << first));
+        __syncwarp();
+        cpt::mbar_wait(drained, 0, &late);
+      }
+    } else {
+      end_role();
     }
   } else {
     // ----------------------------------------------------------------- sums
@@ -403,11 +431,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
     if (!ok && lane == 0) atomicOr(&g_matmul_gave_up, 1u);
+    end_role();
   }
-  __syncwarp();
-  cpt::tc_fence_before();
-  __syncthreads();
-  cpt::cluster_sync();
   if (p.splits > 1 && gave_up == 0 && warp < kSumWarps) {
     // the pairs' sums, added in order: each pair takes a share of the tile's columns
     const uint32_t row0 = tile0 % p.tiles_m * 256 + half * 128, col0 = tile0 / p.tiles_m * kBn;
@@ -479,7 +504,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
   constexpr uint32_t kPer = kThinUnit / kN;            // groups of a unit
   constexpr uint32_t kStage = kTileA + kN * 128;
   extern __shared__ uint8_t dyn[];
-  __shared__ __align__(8) uint64_t bars[2 * kThinMaxStages + 6];
+  __shared__ __align__(8) uint64_t bars[2 * kThinMaxStages + 7];
   __shared__ __align__(16) float scales[2][kThinUnit];
   __shared__ uint32_t tmem_base;
   __shared__ int gave_up;
@@ -492,7 +517,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
   const uint32_t token0 = tile % p.tiles_m * kN, tokens = min(p.m - token0, kN);
   const uint32_t full = cpt::smem_addr(bars), empty = full + 8 * kThinMaxStages;
   const uint32_t acc_full = empty + 8 * kThinMaxStages, acc_empty = acc_full + 16;
-  const uint32_t scale_full = acc_empty + 16;
+  const uint32_t scale_full = acc_empty + 16, drained = scale_full + 16;
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < p.stages; ++s) {
       cpt::mbar_init(full + 8 * s, 1);
@@ -503,6 +528,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
       cpt::mbar_init(acc_empty + 8 * b, 4);
       cpt::mbar_init(scale_full + 8 * b, 32);
     }
+    cpt::mbar_init(drained, 1);
     cpt::mbar_init_fence();
     gave_up = 0;
   }
@@ -520,6 +546,16 @@ __global__ void __launch_bounds__(kThinThreads, 2)
 #pragma unroll
   for (uint32_t i = 0; i < kN; ++i) acc[i] = 0.0f;
   bool ok = true;
+  // Every warp comes here when its role ends.  If a wait ran out, whichever warp's, the loads and
+  // products in flight then end (their waits have a limit too) before the stages and tensor memory are
+  // used for anything else: the warps that issued them see to it within their own branches, where
+  // the sums are not held.
+  auto end_role = [&] {
+    if (!ok && lane == 0) atomicOr(&g_matmul_gave_up, 1u);
+    __syncwarp();
+    cpt::tc_fence_before();
+    asm volatile("barrier.sync 1, %0;" ::"n"(kThinThreads) : "memory");
+  };
 
   if (warp == 4) {
     // ------------------------------------------------------------------ loads
@@ -528,7 +564,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
       cpt::tma_prefetch_map(&map_w);
     }
     __syncwarp();
-    uint32_t s = 0, round = 0;
+    uint32_t s = 0, round = 0, fills = 0;
     for (uint32_t kb = kb0; kb < kb1; ++kb) {
       if (round > 0) {
         ok = cpt::mbar_wait(empty + 8 * s, (round - 1) & 1, &gave_up);
@@ -541,16 +577,18 @@ __global__ void __launch_bounds__(kThinThreads, 2)
         cpt::tma_load(dst + kTileA, &map_a, kb * 128, token0, full + 8 * s);
       }
       __syncwarp();
+      ++fills;
       if (++s == p.stages) {
         s = 0;
         ++round;
       }
     }
-    if (!ok) {          // given up: the loads in flight land before the CTA leaves
-      int unused = 0;
+    end_role();
+    if (gave_up != 0) {
+      int late = 0;
       for (uint32_t k = 0; k < p.stages; ++k) {
-        const uint32_t r = k < s ? round : round - 1;
-        if (k < s || round > 0) cpt::mbar_wait(full + 8 * k, r & 1, &unused);
+        const LastFill last = last_fill(fills, fills, p.stages, k);
+        if (last.any) cpt::mbar_wait(full + 8 * k, last.parity, &late);
       }
     }
   } else if (warp == 5) {
@@ -581,6 +619,13 @@ __global__ void __launch_bounds__(kThinThreads, 2)
       }
       if (!ok) break;
     }
+    end_role();
+    if (gave_up != 0) {
+      int late = 0;
+      if (cpt::elect_one()) cpt::mma_commit(drained);
+      __syncwarp();
+      cpt::mbar_wait(drained, 0, &late);
+    }
   } else if (warp == 6) {
     // ----------------------------------------------------------------- scales
     const float* sw = p.sw + static_cast<uint64_t>(row0 / 128) * p.groups;
@@ -604,6 +649,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
       for (uint32_t i = 0; i < 4; ++i) scales[b][lane + 32 * i] = f[i];
       cpt::mbar_arrive(scale_full + 8 * b);
     }
+    end_role();
   } else if (warp < 4) {
     // ------------------------------------------------------------------- sums
     const uint32_t tmem_warp = tmem + ((warp * 32) << 16);
@@ -637,11 +683,11 @@ __global__ void __launch_bounds__(kThinThreads, 2)
       __syncwarp();
       if (lane == 0) cpt::mbar_arrive(acc_empty + 8 * b);
     }
+    end_role();
+  } else {
+    end_role();
   }
-  if (!ok && lane == 0) atomicOr(&g_matmul_gave_up, 1u);
-  __syncwarp();
-  cpt::tc_fence_before();
-  __syncthreads();
+  if (gave_up != 0) __syncthreads();
   const uint32_t row = row0 + threadIdx.x;       // (of the summing warps)
   if (p.splits == 1) {
     if (warp < 4 && row < p.n) {
