@@ -318,15 +318,16 @@ struct GradParams {
   float eps;
 };
 
-// dx = dres + r (t - h c), c = r^2 mean(t h): the formula with n = h r written out.
+// dx = dres + r (t - n c), c = mean(t n).  (n = h r stays near one where r^2 would overflow: rows
+// of a mean square below 2.9e-39, with eps as small.)
 template <typename T, bool VEC>
 __device__ __forceinline__ void emit_dx(const GradParams& p, uint64_t row, uint32_t o, float r,
-                                        float c, const float (&t)[8], const float (&h)[8],
+                                        float c, const float (&t)[8], const float (&n)[8],
                                         const Packed<T>& res) {
   float dx[8];
   unpack<T>(res, dx);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) dx[e] += r * (t[e] - h[e] * c);
+  for (int e = 0; e < 8; ++e) dx[e] += r * (t[e] - n[e] * c);
   store_row_octet<T, VEC>(static_cast<T*>(p.dx) + row * p.d, o, p.d, pack<T>(dx));
 }
 
@@ -434,7 +435,7 @@ __global__ void __launch_bounds__(cta_threads(THREADS), grad_ctas_per_sm(THREADS
     team_sum<THREADS>(sq, th, red[turn]);
     const float inv_d = 1.0f / static_cast<float>(p.d);
     const float r = 1.0f / sqrtf(sq * inv_d + p.eps);
-    const float c = r * r * (th * inv_d);
+    const float c = r * (th * inv_d);              // mean(t n) = r mean(t h)
     if (row < p.rows) {
 #pragma unroll
       for (int i = 0; i < kOct; ++i) {
@@ -442,7 +443,8 @@ __global__ void __launch_bounds__(cta_threads(THREADS), grad_ctas_per_sm(THREADS
         if (o < octets) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            dw[i][e] = fmaf(t[i][e], h[i][e] * r, dw[i][e]);
+            h[i][e] *= r;                          // n
+            dw[i][e] = fmaf(t[i][e], h[i][e], dw[i][e]);
             t[i][e] *= w[i][e];
           }
           emit_dx<T, VEC>(p, row, o, r, c, t[i], h[i], rn[i]);
@@ -511,7 +513,7 @@ __global__ void __launch_bounds__(1024) norm_grad_wide_kernel(GradParams p) {
     team_sum<1024>(sq, th, red[turn]);
     const float inv_d = 1.0f / static_cast<float>(p.d);
     const float r = 1.0f / sqrtf(sq * inv_d + p.eps);
-    const float c = r * r * (th * inv_d);
+    const float c = r * (th * inv_d);              // mean(t n) = r mean(t h)
     for (uint32_t o = threadIdx.x; o < octets; o += 1024) {
       float h[8], t[8], w[8];
       unpack<T>(load_row_octet<T, VEC>(hr, o, p.d), h);
@@ -519,7 +521,8 @@ __global__ void __launch_bounds__(1024) norm_grad_wide_kernel(GradParams p) {
       load_weight<VEC>(p.weight, p.weight_dtype, o, p.d, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        dw[e * octets + o] = fmaf(t[e], h[e] * r, dw[e * octets + o]);
+        h[e] *= r;                                 // n
+        dw[e * octets + o] = fmaf(t[e], h[e], dw[e * octets + o]);
         t[e] *= w[e];
       }
       emit_dx<T, VEC>(p, row, o, r, c, t, h,
