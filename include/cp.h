@@ -380,7 +380,7 @@ enum { CP_F32 = 0, CP_F16 = 1, CP_BF16 = 2 };
  * training, or a token embedding):
  *   out[j][q] = rn(scale * weight[ids[j]][q]),  one fp32 product rounded once.
  *   weight   [n_rows][d] of dtype (CP_F32, CP_F16, CP_BF16), row stride
- *            weight_stride >= d.
+ *            weight_stride >= d, or 0 (one row for all ids).
  *   ids      n int64.  An id outside [0, n_rows) gives a row of zeros.
  *   out      [n][d] of the same type, row stride out_stride >= d.
  *   status   device uint32 or NULL: bit 0 is OR-ed in for an id out of range.

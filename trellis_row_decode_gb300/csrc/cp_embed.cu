@@ -84,8 +84,8 @@ cudaError_t launch_embed(const void* weight, uint64_t n_rows, uint32_t d, uint64
 extern "C" cp_status cp_embed(const void* weight, int dtype, uint64_t n_rows, uint32_t d,
                               uint64_t weight_stride, const int64_t* ids, uint64_t n, float scale,
                               void* out, uint64_t out_stride, uint32_t* status, void* stream) {
-  if (!dtype_ok(dtype) || d == 0 || d > (1u << 20) || n >= (1ull << 31) || weight_stride < d ||
-      out_stride < d) {
+  if (!dtype_ok(dtype) || d == 0 || d > (1u << 20) || n >= (1ull << 31) ||
+      (weight_stride < d && weight_stride != 0) || out_stride < d) {
     cpx::set_error("bad dtype, d, n or row stride");
     return CP_ERR_INVALID_ARG;
   }
