@@ -344,29 +344,31 @@ def rms_norm_grad(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, eps: 
 
 def quantize_fp8(x: torch.Tensor, block_rows: int = 1, out: torch.Tensor | None = None,
                  scales: torch.Tensor | None = None, stream=None):
-    """(q, scales) of x [rows, d]: float8_e4m3fn, and one fp32 scale for each block of
-    block_rows x 128 (1: activations, 128: weights), amax / 448."""
+    """(q, scales) of x: float8_e4m3fn of x's shape, and one fp32 scale for each block of
+    block_rows x 128, amax / 448.  block_rows 1 (activations): x [..., d], scales
+    [..., ceil(d / 128)]; 128 (weights): x [rows, d], scales [ceil(rows / 128), ceil(d / 128)]."""
     code = _float(x.dtype, "x")
-    if x.dim() != 2:
-        raise ValueError("x must be [rows, d]")
     if block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128")
+    if x.dim() != 2 and (x.dim() < 2 or block_rows != 1):
+        raise ValueError("x must be [rows, d], or [..., d] for blocks of one row")
     dev = _device(x, "x")
     rows, d, xs = _rows(x, "x")
-    q = _whole(out, (rows, d), _E4M3, x, dev, stream, "out")
-    sc = _whole(scales, (-(-rows // block_rows), -(-d // 128)), torch.float32, x, dev, stream,
-                "scales")
+    q = _whole(out, x.shape, _E4M3, x, dev, stream, "out")
+    lead = x.shape[:-1] if block_rows == 1 else (-(-rows // 128),)
+    sc = _whole(scales, lead + (-(-d // 128),), torch.float32, x, dev, stream, "scales")
     _check(_lib().cp_quantize_fp8(x.data_ptr(), xs, code, rows, d, block_rows, q.data_ptr(),
                                   sc.data_ptr(), _stream(stream, dev)), "cp_quantize_fp8")
     return q, sc
 
 
 def _scaled(t: torch.Tensor, scales: torch.Tensor, block: int, dev: int, name: str):
-    """(rows, k, row stride) of an e4m3 matrix whose scales fit it."""
-    if t.dtype != _E4M3 or t.dim() != 2:
-        raise ValueError(f"{name} must be float8_e4m3fn, [rows, k]")
+    """(rows, k, row stride) of an e4m3 operand whose scales fit it: [..., k] with blocks of one
+    row, [rows, k] with larger ones."""
+    if t.dtype != _E4M3 or (t.dim() != 2 and (t.dim() < 2 or block != 1)):
+        raise ValueError(f"{name} must be float8_e4m3fn, {'[..., k]' if block == 1 else '[n, k]'}")
     rows, k, stride = _rows(t, name)
-    want = (-(-rows // block), -(-k // 128))
+    want = (t.shape[:-1] if block == 1 else (-(-rows // block),)) + (-(-k // 128),)
     if scales.dtype != torch.float32 or scales.shape != want or not scales.is_contiguous():
         raise ValueError(f"{name}_scales must be contiguous float32 of shape {want}")
     return rows, k, stride
@@ -375,9 +377,9 @@ def _scaled(t: torch.Tensor, scales: torch.Tensor, block: int, dev: int, name: s
 def matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
                dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """a @ w.T for a [m, k] and w [n, k] in float8_e4m3fn with scales for each block of 128
-    along k (a_scales [m, ceil(k/128)], w_scales [ceil(n/128), ceil(k/128)], fp32), summed in
-    fp32 and rounded once to `dtype`.
+    """a @ w.T, [..., n], for a [..., k] and w [n, k] in float8_e4m3fn with scales for each block
+    of 128 along k (a_scales [..., ceil(k/128)], w_scales [ceil(n/128), ceil(k/128)], fp32),
+    summed in fp32 and rounded once to `dtype` (to out's type where `out` is given).
 
     Rows that do not start on 16-byte boundaries are copied to such rows in `workspace`
     (matmul_fp8_workspace; allocated where it is not given), but for the smallest products."""
@@ -388,10 +390,10 @@ def matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scale
         raise ValueError("a and w must have the same number of columns")
     if out is None:
         code = _float(dtype, "the output")
-        out, ldo = _empty((m, n), dtype, a, stream), n
+        out, ldo = _empty(a.shape[:-1] + (n,), dtype, a, stream), n
     else:
         code = _float(out.dtype, "the output")
-        ldo = _check_out(out, (m, n), out.dtype, dev, "out")
+        ldo = _check_out(out, a.shape[:-1] + (n,), out.dtype, dev, "out")
     pa, pw, ws = a.data_ptr(), _on(w, dev, "w"), None
     if (pa | pw | lda | ldw) & 15 or lda == 0 or ldw == 0:
         nbytes = _lib().cp_matmul_fp8_workspace_bytes(pa, lda, pw, ldw, m, n, k)
