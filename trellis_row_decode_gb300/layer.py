@@ -10,7 +10,9 @@ of a wider tensor) and, for inputs, be zero (an expanded row).  ``stream`` is th
 ``torch.cuda.Stream`` to queue on (default: the current one): outputs that the call
 allocates, and its workspace, belong to that stream.  A caller that hands in tensors
 made on another stream, or uses the outputs on one, orders the streams as for any
-PyTorch operation.  Wrong types, shapes or strides raise ValueError before anything
+PyTorch operation.  No call records anything for torch.autograd: a result is cut off from
+inputs that require gradients, and the caller chains embed_grad and rms_norm_grad by hand, as
+examples/memory_layer.py does.  Wrong types, shapes or strides raise ValueError before anything
 is queued; what the library itself refuses raises CPError.
 """
 from __future__ import annotations
