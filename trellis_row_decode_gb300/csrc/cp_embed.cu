@@ -25,8 +25,8 @@ constexpr uint32_t kOctets = 4;   // octets of a row that a lane holds at once
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads)
-    embed_kernel(const T* __restrict__ weight, uint64_t n_rows, uint32_t d, uint64_t weight_stride,
-                 const int64_t* __restrict__ ids, uint64_t n, float scale, T* __restrict__ out,
+    embed_kernel(const T* weight, uint64_t n_rows, uint32_t d, uint64_t weight_stride,
+                 const int64_t* ids, uint64_t n, float scale, T* out,
                  uint64_t out_stride, uint32_t* status, uint32_t lanes_log2, uint32_t slabs) {
   const uint32_t lanes = 1u << lanes_log2;
   const uint64_t team = (static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x) >> lanes_log2;
@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t octets = (d + 7) / 8;
   const uint32_t o0 = slab * lanes * kOctets + (threadIdx.x & (lanes - 1));
   wait_for_previous();
-  const int64_t id = __ldg(ids + j);
+  const int64_t id = ids[j];
   const bool valid = static_cast<uint64_t>(id) < n_rows;
   const T* src = weight + (valid ? static_cast<uint64_t>(id) : 0) * weight_stride;
   T* dst = out + j * out_stride;

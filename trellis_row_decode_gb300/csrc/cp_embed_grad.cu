@@ -130,8 +130,8 @@ __device__ __forceinline__ Ranks rank_digits(const uint32_t (&digit)[kRounds], i
 
 // Up to kSmallMax ids in one CTA: all passes in shared memory.
 __global__ void __launch_bounds__(kSmallThreads)
-    sort_small_kernel(const int64_t* __restrict__ ids, uint32_t n, uint32_t n_rows, int passes,
-                      int bits, uint2* __restrict__ pairs_out, uint32_t* status) {
+    sort_small_kernel(const int64_t* ids, uint32_t n, uint32_t n_rows, int passes,
+                      int bits, uint2* pairs_out, uint32_t* status) {
   __shared__ uint32_t key_s[kSmallMax];
   __shared__ uint16_t pos_s[kSmallMax];
   extern __shared__ uint16_t hist[];             // [warps][bins]

@@ -34,7 +34,7 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
 // One value of an array whose type is known at run time (CP_F32, CP_F16, CP_BF16);
 // the branch is the same for every thread.
 __device__ __forceinline__ float load_as_f32(const void* p, uint64_t i, int dtype) {
-  if (dtype == CP_F32) return __ldg(static_cast<const float*>(p) + i);
+  if (dtype == CP_F32) return static_cast<const float*>(p)[i];
   if (dtype == CP_F16) return to_f32(static_cast<const __half*>(p)[i]);
   return to_f32(static_cast<const __nv_bfloat16*>(p)[i]);
 }
@@ -372,7 +372,9 @@ __device__ __forceinline__ void store_q_octet(uint8_t* row, uint32_t o, uint32_t
 // ------------------------------------------------------------ one kernel after another
 //
 // Kernels of one call run in order; each is launched while the one before it still runs
-// (programmatic dependent launch) and waits, in hardware, for its results here.
+// (programmatic dependent launch) and waits, in hardware, for its results here.  What the kernel
+// before may have written is therefore not constant for this kernel's life: no load of these
+// kernels takes the read-only path (__ldg, const __restrict__), which the wait does not order.
 __device__ __forceinline__ void wait_for_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

@@ -38,7 +38,7 @@ __device__ __forceinline__ uint4 load_any_piece(const uint8_t* row, uint32_t col
   const uint32_t skew = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15);
   if (col >= skew && static_cast<uint64_t>(col) + (skew != 0 ? 32 - skew : 16) <= k) {
     const uint4* q = reinterpret_cast<const uint4*>(p - skew);
-    const uint4 lo = __ldg(q), hi = skew != 0 ? __ldg(q + 1) : make_uint4(0, 0, 0, 0);
+    const uint4 lo = q[0], hi = skew != 0 ? q[1] : make_uint4(0, 0, 0, 0);
     uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
     if (skew & 8) {
 #pragma unroll
@@ -158,7 +158,7 @@ template <bool kAligned>
 __device__ __forceinline__ uint4 load_piece(const uint8_t* row, uint32_t col, uint32_t k) {
   if (kAligned && static_cast<uint64_t>(col) + 16 <= k) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(row + col));
     return v;
@@ -168,7 +168,7 @@ __device__ __forceinline__ uint4 load_piece(const uint8_t* row, uint32_t col, ui
 template <bool kAligned>
 __device__ __forceinline__ uint4 load_piece_cached(const uint8_t* row, uint32_t col, uint32_t k) {
   if (kAligned && static_cast<uint64_t>(col) + 16 <= k)
-    return __ldg(reinterpret_cast<const uint4*>(row + col));
+    return *reinterpret_cast<const uint4*>(row + col);
   return load_any_piece(row, col, k);
 }
 
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) matmul_few_kernel(MatmulParams
   FewRows<kTokens> rows;
   auto fetch_rows = [&](uint32_t kb) {
     const bool in = kb < p.groups;
-    rows.scale_w = in ? __ldg(sw + kb) : 0.0f;
+    rows.scale_w = in ? sw[kb] : 0.0f;
 #pragma unroll
     for (int n = 0; n < kTokens; ++n) {
       const uint32_t row = 8 * n + g, c0 = 8 * n + 2 * t;
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) matmul_few_kernel(MatmulParams
 #pragma unroll
       for (int e = 0; e < 2; ++e)
         rows.scale[n][e] =
-            in && c0 + e < p.m ? __ldg(p.sa + static_cast<uint64_t>(c0 + e) * p.groups + kb) : 0.0f;
+            in && c0 + e < p.m ? p.sa[static_cast<uint64_t>(c0 + e) * p.groups + kb] : 0.0f;
     }
   };
   float acc[kTokens][4];

@@ -364,9 +364,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         float fa[2] = {}, f0[2] = {}, f1[2] = {};
         auto load_scales = [&](uint32_t k, uint32_t kb) {
           if (kb < kb1) {
-            fa[k] = __ldg(sa + kb);
-            f0[k] = __ldg(sw0 + kb);
-            f1[k] = __ldg(sw1 + kb);
+            fa[k] = sa[kb];
+            f0[k] = sw0[kb];
+            f1[k] = sw1[kb];
           }
         };
         load_scales(0, kb0);
@@ -637,8 +637,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
       for (uint32_t i = 0; i < 4; ++i) {
         const uint32_t e = lane + 32 * i, group = kb + e / kN, token = e % kN;
         f[i] = group < kb1 && token < tokens
-                   ? __ldg(p.sa + static_cast<uint64_t>(token0 + token) * p.groups + group) *
-                         __ldg(sw + group)
+                   ? p.sa[static_cast<uint64_t>(token0 + token) * p.groups + group] * sw[group]
                    : 0.0f;
       }
       if (u >= 2) {

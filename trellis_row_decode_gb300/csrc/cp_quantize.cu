@@ -26,8 +26,8 @@ constexpr int kGroups = 4;         // groups of a half warp
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads)
-    quantize_rows_kernel(const T* __restrict__ x, uint64_t stride, uint32_t d, uint32_t per_row,
-                         uint32_t groups, uint8_t* __restrict__ q, float* __restrict__ scales) {
+    quantize_rows_kernel(const T* x, uint64_t stride, uint32_t d, uint32_t per_row,
+                         uint32_t groups, uint8_t* q, float* scales) {
   const uint32_t sub = threadIdx.x & 15;
   // (below 2^29: at most 2^31 groups; the thread's own index would pass 32 bits)
   const uint32_t half = blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);
@@ -63,8 +63,8 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
-    quantize_block_kernel(const T* __restrict__ x, uint64_t stride, uint64_t rows, uint32_t d,
-                          uint32_t per_row, uint8_t* __restrict__ q, float* __restrict__ scales) {
+    quantize_block_kernel(const T* x, uint64_t stride, uint64_t rows, uint32_t d,
+                          uint32_t per_row, uint8_t* q, float* scales) {
   __shared__ uint32_t red[kThreads / 32];
   const uint32_t bi = blockIdx.x / per_row, bj = blockIdx.x - bi * per_row;
   const uint32_t o = bj * 16 + (threadIdx.x & 15);
