@@ -119,16 +119,17 @@ uint64_t aligned_pitch(uint64_t k) { return (k + 15) / 16 * 16; }
 
 // ------------------------------------------------------------------- few rows of a
 //
-// Up to 64 rows of a: the product reads w once and little else, so it is bound by memory.
+// Up to 16 rows of a and 8 MB of w (kFewRows, kFewBytes): the product reads w once and little
+// else, and is over in a few microseconds, so what counts is how soon the loads are under way.
 // A warp has 16 rows of w (the tensor core's 16 x 32 operand) and every 8th group of 128 of
 // the CTA's share of k; its lanes load whole 16-byte pieces straight into fragments (the same
 // order of k on both operands, whatever it is, gives the same sums), several groups ahead.
 // The eight warps' sums are added in order through shared memory, and those of the
 // `splits` CTAs of a cluster, which share the rows when w has few, through theirs.
-// 1 x 1024 x 1024: 2.9 us; bound by latency there, by the warp-level product beyond 10 MB of w.
+// 1 x 1024 x 1024: 3.1 us; bound by latency there, by the warp-level product beyond 10 MB of w.
 
 // Which kernel takes operands on 16-byte boundaries.  Few rows of a and little of w: this one
-// (1 x 1024 x 1024: 3.0 us against the thin kernel's 4.9; 16 x 1024 x 1024: 3.8 against 4.9; with
+// (1 x 1024 x 1024: 3.1 us against the thin kernel's 4.9; 16 x 1024 x 1024: 3.8 against 4.9; with
 // 17 MB of w they are even, 6.3 us, and with 101 MB the thin one leads, 20 us against 28: the
 // warp-level e4m3 product costs about 70 clocks each).  Up to 128 rows of a: the thin kernel
 // (128 x 4096 x 24576: 31 us against the pairs' 42; 128 x 4096 x 4096: 10.8 against 13.7; at 256 rows

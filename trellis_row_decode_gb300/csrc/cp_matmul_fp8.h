@@ -22,9 +22,10 @@ struct MatmulParams {
 };
 
 // Operands whose rows lie on 16-byte boundaries (cp_matmul_tc.cu).
-// Tiles of 256 rows of a and 64 to 256 rows of w, a pair of SMs each.
+// More than 128 rows of a (kThinRows): tiles of 256 rows of a and 32 to 256 rows of w, a pair of
+// SMs each.
 cp_status launch_pairs(const MatmulParams& p, cudaStream_t s);
-// Up to a few hundred rows of a: tiles of 128 rows of w and up to 64 rows of a.
+// Up to 128 rows of a: tiles of 128 rows of w and up to 64 rows of a.
 cp_status launch_thin(const MatmulParams& p, cudaStream_t s);
 
 }  // namespace cpm

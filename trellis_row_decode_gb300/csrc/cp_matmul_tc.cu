@@ -62,7 +62,6 @@ struct TcParams {
   uint32_t m, n, groups;
   int out_dtype;
   uint32_t tiles_m, tiles, stages, splits, tmem_columns;
-  uint32_t a_rows;          // rows of a's TMA box
   uint32_t out_align;       // 32, 16 or 0: bytes on whose boundaries out's rows lie
 };
 
@@ -260,7 +259,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t row0 = (tile - tile_n * p.tiles_m) * 256, col0 = tile_n * kBn;
         const bool a1 = row0 + 128 < p.m;               // the second CTA has rows of a
         const bool mine = half == 0 || a1;
-        const uint32_t bytes = 2 * w_bytes + (a1 ? 2 : 1) * p.a_rows * 128;
+        const uint32_t bytes = 2 * w_bytes + (a1 ? 2 : 1) * kTileA;
         for (uint32_t kb = kb0; kb < kb1; ++kb) {
           if (round > 0) {
             ok = cpt::mbar_wait(empty + 8 * s, (round - 1) & 1, &gave_up);
@@ -472,7 +471,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 // ----------------------------------------------- few rows of a, many bytes of w: tcgen05
 //
-// With at most 128 rows of a the operands change places: 128 rows of w are the tensor core's
+// With at most 128 rows of a (launch_thin) the operands change places: 128 rows of w are the tensor core's
 // 128 x 32 operand, up to 64 rows of a its N (16, 32 or 64) columns, and the kernel is bound by
 // the stream of w (a second tile of rows of a finds it in L2).  A unit is 128 columns of tensor
 // memory, 128 / kN groups side by side, so the sums (a lane has a row of w) wait once a unit; two
@@ -884,7 +883,6 @@ cp_status launch_pairs(const MatmulParams& q, cudaStream_t s) {
   p.out_dtype = q.out_dtype;
   p.splits = splits;
   p.tiles_m = (q.m + 255) / 256;
-  p.a_rows = q.m >= 128 ? 128 : (q.m + 7) / 8 * 8;
   const uint64_t tiles = static_cast<uint64_t>(p.tiles_m) * ((q.n + bn - 1) / bn);
   if (tiles >= (1ull << 31)) {
     cpx::set_error("m and n make more than 2^31 tiles");
@@ -901,7 +899,7 @@ cp_status launch_pairs(const MatmulParams& q, cudaStream_t s) {
                 : cpx::aligned(q.out, 16) && q.ldo * elt % 16 == 0 ? 16
                                                                    : 0;
   CUtensorMap map_a, map_w;
-  if (!encode_map(&map_a, q.a, q.k, q.m, q.lda, p.a_rows) ||
+  if (!encode_map(&map_a, q.a, q.k, q.m, q.lda, 128) ||
       !encode_map(&map_w, q.w, q.k, q.n, q.ldw, bn / 2)) {
     cpx::set_error("tensor map refused");
     return CP_ERR_CUDA;
