@@ -18,9 +18,9 @@
 // Every sum's order follows from the ids alone: no floating-point atomics.
 //
 // Bound by memory: dy read once, grad written once.  196,608 Zipf ids, 1024 columns of bf16 into
-// 131,072 rows: the sums take 112 us of the call's 147 (671 MB at 6.0 TB/s), the sort's four
+// 131,072 rows: the sums take 112 us of the call's 145 (671 MB at 6.0 TB/s), the sort's four
 // kernels and the join of the hot rows the rest, which waits for latency, not bandwidth.  4,096
-// ids of 4,096 x 256 fp32: 15.3 us, three kernels whose chains of dependent loads are the bound.
+// ids of 4,096 x 256 fp32: 15.2 us, three kernels whose chains of dependent loads are the bound.
 #include <cstdint>
 
 #include <cuda_runtime.h>

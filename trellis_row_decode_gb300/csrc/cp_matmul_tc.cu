@@ -35,7 +35,8 @@ using cpm::MatmulParams;
 // the next group meanwhile.  With few tiles, `splits` pairs of one cluster share a tile's
 // groups and add their sums, in the order of the pairs, through distributed shared memory.
 //
-// 4096 x 4096 x 24576: 348 us in bursts (2.37 PFLOP/s), 374 sustained.  Bound by the summing warps:
+// 4096 x 4096 x 24576: 340-348 us in bursts of a dozen (2.4 PFLOP/s), 364-376 in calls that go on
+// (2.2, at the power limit).  Bound by the summing warps:
 // the tensor core alone takes 225 us (263 sustained, at the power limit), with the loads of
 // tensor memory 250, with the fused multiply-adds 334 (224 of them an SM partition and group,
 // issued at 0.8 a clock), with the loads of the scales 348.  2048^3: 14.0 us, 64 tiles of 16 groups
@@ -478,7 +479,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // units alternate.  Two CTAs share an SM; `splits` CTAs of a cluster share a tile's groups and
 // add their sums in order through distributed shared memory.
 //
-// 1 x 4096 x 24576: 20.3 us, 101 MB at 5.0 TB/s; 48 rows of a: 23.4 us; 1 x 4096 x 4096: 6.1 us.  The
+// 1 x 4096 x 24576: 19.9 us, 101 MB at 5.1 TB/s; 48 rows of a: 22.8 us; 1 x 4096 x 4096: 6.3 us.  The
 // fixed part is about 4 us (launch, tensor maps, the first loads, the exchange); the stream
 // itself runs at the copy rate.
 

@@ -147,8 +147,8 @@ constexpr bool norm_ring(int threads) { return threads == 1024 || threads <= 16;
 // against 28.4) and of a few lanes (100000 x 128: 17.0 against 18.3).
 // Rows on other boundaries travel as the aligned 16-byte words that hold their bytes, one word more
 // for each team or warp, and are shifted into place on the way back.  1707 x 4626 bf16: the
-// gradient takes 31.2 us (64.8 with loads to registers), the forward 21.7; 19011 x 812: forward 37.0
-// (51.9), gradient 39.5; 4096 x 4095 fp32: gradient 81 (116).
+// gradient takes 30.1 us (64.8 with loads to registers), the forward 21.3; 19011 x 812: forward 36.2
+// (51.9), gradient 38.8; 4096 x 4095 fp32: gradient 81 (116).
 constexpr int lanes_of(int threads) { return threads < 32 ? threads : 32; }
 template <typename T, bool VEC, int THREADS>
 constexpr int array_bytes() {          // one array's octets, one of each thread of the CTA
