@@ -509,6 +509,98 @@ cp_status cp_matmul_fp8(const uint8_t* a, uint64_t a_stride, const float* a_scal
  */
 cp_status cp_matmul_fp8_status(void* stream);
 
+/* ------------------------------------------------------------------------
+ * The projection in 16 bits, in which a memory layer is trained (cp_matmul_fp8 serves it in
+ * 8), with what surrounds the product, and dropout.  The conventions of the operators above hold.
+ *
+ * Dropout.  Element [i][j] of an array of rows is kept where word j mod 4 of the generator
+ * Philox4x32-10 (Salmon, Moraes, Dror and Shaw, 2011), counter (j / 4, i, offset mod 2^32,
+ * offset / 2^32), key (seed mod 2^32, seed / 2^32), is below floor((1 - p) 2^32 + 1/2):
+ *   D(v)[i][j] = v[i][j] * fp32(1 / (1 - p)) where it is kept, and 0 elsewhere, whatever v is.
+ * So the same p, seed and offset make the same mask in every call and on every layout of the
+ * same rows, nothing of it is stored, and D is its own gradient.  p = 0 keeps everything as it
+ * is, p = 1 nothing.  Each use of a mask wants an offset of its own.
+ *   p        0 to 1.
+ *   rng      device uint64[2] or NULL.  Where it is given, the kernels read the seed from rng[0]
+ *            and add rng[1] to `offset` as they run: a captured graph draws other masks when its
+ *            owner changes the two between replays.  `seed` is not used then.
+ * ---------------------------------------------------------------------- */
+
+/* Activations: z, max(z, 0), z sigmoid(z), z Phi(z), and
+ * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2. */
+enum { CP_ACT_NONE = 0, CP_ACT_RELU = 1, CP_ACT_SILU = 2, CP_ACT_GELU = 3, CP_ACT_GELU_TANH = 4 };
+
+/*
+ * cp_dropout -- out = rn(residual + D(x)), fp32 in between, rounded once; without a residual
+ * rn(D(x)).  The gradient by x is the same call on dy without a residual.
+ *   x, residual   [rows][d] of dtype with row strides >= d, or 0 (one row for all).  residual may
+ *            be NULL.
+ *   out      [rows][d] of dtype, row stride >= d; it may be x or residual (same stride).
+ * rows < 2^32, d < 2^32.
+ */
+cp_status cp_dropout(const void* x, uint64_t x_stride, const void* residual,
+                     uint64_t residual_stride, int dtype, uint64_t rows, uint32_t d, double p,
+                     uint64_t seed, uint64_t offset, const uint64_t* rng, void* out,
+                     uint64_t out_stride, void* stream);
+
+/*
+ * cp_linear -- a projection and what follows it:
+ *   z = x w^T + bias;   pre = rn(z);   out = rn(residual + D(act(z)))
+ * sums and everything behind them in fp32, each output rounded once.
+ *   x        [m][k] of dtype (CP_F16 or CP_BF16), row stride x_stride >= k or 0.
+ *   w        [n][k] of dtype, row stride w_stride >= k or 0.
+ *   bias     [n] of bias_dtype, or NULL.
+ *   residual [m][n] of out_dtype, row stride residual_stride >= n or 0, or NULL.
+ *   out      [m][n] of out_dtype (any type), row stride out_stride >= n.  It may be residual
+ *            (same stride): the stream is updated in place.
+ *   pre      [m][n] of dtype, row stride pre_stride >= n, or NULL: what cp_linear_grad needs of
+ *            a call with an activation.
+ *   workspace  cp_linear_workspace_bytes bytes, 16-byte aligned (NULL where that is 0): copies of
+ *            operands whose rows do not lie on 16-byte boundaries, and sums of a k that is split.
+ * k = 0 gives z = bias.  m, n < 2^31, k < 2^30.  m x n tiles of one call stay below 2^31.
+ */
+uint64_t cp_linear_workspace_bytes(const void* x, uint64_t x_stride, const void* w,
+                                   uint64_t w_stride, uint64_t m, uint64_t n, uint64_t k);
+cp_status cp_linear(const void* x, uint64_t x_stride, const void* w, uint64_t w_stride, int dtype,
+                    uint64_t m, uint64_t n, uint64_t k, const void* bias, int bias_dtype,
+                    int activation, double p, uint64_t seed, uint64_t offset, const uint64_t* rng,
+                    const void* residual, uint64_t residual_stride, void* out, int out_dtype,
+                    uint64_t out_stride, void* pre, uint64_t pre_stride, void* workspace,
+                    uint64_t workspace_bytes, void* stream);
+
+/*
+ * cp_linear_grad -- the gradients of cp_linear by x, w and bias (the residual's is dy):
+ *   dz = D(dy) act'(pre);   dx = rn(dz w);   dw = rn(dz^T x);   db = rn(sum of dz over the rows)
+ * dz is rounded to dtype where it is not dy itself (the tensor core's operands have 16 bits); db sums it
+ * before that rounding.  act' of CP_ACT_RELU at 0 is 0.
+ *   dy       [m][n] of dy_dtype: dtype, or CP_F32 (out's type); row stride >= n or 0.
+ *   x, w     as in cp_linear;  pre: what cp_linear left, row stride >= n or 0; NULL with
+ *            CP_ACT_NONE.
+ *   p, seed, offset, rng   those of the forward call.
+ *   accumulate  0: dw and db are overwritten;  1: the gradients are added to them (fp32 sum,
+ *            rounded once).
+ *   dx       [m][k] of dtype, row stride dx_stride >= k, or NULL.
+ *   dw       [n][k] of dw_dtype, row stride dw_stride >= k, or NULL.
+ *   db       [n] of db_dtype, or NULL.
+ *   workspace  cp_linear_grad_workspace_bytes bytes, 16-byte aligned.
+ * m = 0 gives zeros for dw and db, n = 0 for dx.  m, n < 2^30, k < 2^30.
+ */
+uint64_t cp_linear_grad_workspace_bytes(uint64_t m, uint64_t n, uint64_t k);
+cp_status cp_linear_grad(const void* dy, int dy_dtype, uint64_t dy_stride, const void* x,
+                         uint64_t x_stride, const void* w, uint64_t w_stride, int dtype,
+                         const void* pre, uint64_t pre_stride, uint64_t m, uint64_t n, uint64_t k,
+                         int activation, double p, uint64_t seed, uint64_t offset,
+                         const uint64_t* rng, int accumulate, void* dx, uint64_t dx_stride,
+                         void* dw, int dw_dtype, uint64_t dw_stride, void* db, int db_dtype,
+                         void* workspace, uint64_t workspace_bytes, void* stream);
+
+/*
+ * cp_linear_status -- synchronise `stream`, then report and clear the current device's record
+ * of waits that ran out inside cp_linear and cp_linear_grad (two seconds each; the kernel then
+ * returns and its output is not valid): CP_ERR_CUDA if there was one.
+ */
+cp_status cp_linear_status(void* stream);
+
 /* Release what the handle owns (LUT copy, status word, host registration made
  * by cp_table_load).  Borrowed buffers are untouched.  NULL is a no-op. */
 void cp_table_free(cp_table* t);

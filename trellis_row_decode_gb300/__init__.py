@@ -27,7 +27,8 @@ __all__ = [
     "CP_LAYOUT_AOS", "CP_LAYOUT_SOA", "CP_RESIDENT_DEVICE", "CP_RESIDENT_HOST",
     "CP_F32", "CP_F16", "CP_BF16", "embed", "embed_grad", "embed_grad_workspace", "rms_norm",
     "rms_norm_fp8", "rms_norm_grad", "rms_norm_grad_workspace", "quantize_fp8", "matmul_fp8",
-    "matmul_fp8_workspace", "matmul_fp8_status",
+    "matmul_fp8_workspace", "matmul_fp8_status", "ACTIVATIONS", "linear", "linear_workspace",
+    "linear_grad", "linear_grad_workspace", "linear_status", "dropout", "dropout_grad",
 ]
 
 _PKG = Path(__file__).resolve().parent
@@ -391,3 +392,6 @@ from .layer import (  # noqa: E402
     CP_BF16, CP_F16, CP_F32, embed, embed_grad, embed_grad_workspace, matmul_fp8, matmul_fp8_status,
     matmul_fp8_workspace, quantize_fp8, rms_norm, rms_norm_fp8, rms_norm_grad,
     rms_norm_grad_workspace)
+from .projection import (  # noqa: E402
+    ACTIVATIONS, dropout, dropout_grad, linear, linear_grad, linear_grad_workspace, linear_status,
+    linear_workspace)

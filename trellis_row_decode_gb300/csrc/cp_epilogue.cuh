@@ -1,0 +1,384 @@
+// cp_epilogue.cuh -- what follows a projection's sums (include/cp.h, cp_linear): bias,
+// activation, dropout, the residual's addition; and what its gradient undoes.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "cp.h"
+#include "cp_layer.cuh"
+
+namespace cpe {
+
+using namespace cpl;
+
+// --------------------------------------------------------------------- dropout
+//
+// Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as easy as 1, 2, 3",
+// 2011): ten rounds of two 32 x 32 -> 64 bit products on a counter, the key stepped between them.
+// Element [i][j] takes word j mod 4 of counter (j / 4, i, offset) under the key `seed`, so four
+// neighbouring columns share a call, any kernel can make any part of the mask, and nothing of
+// it is stored.
+
+struct DropParams {
+  const uint64_t* rng;   // seed and offset on the device, or null
+  uint64_t seed, offset; // offset is added to rng[1]
+  uint32_t last;         // the largest word that keeps its element
+  float scale;           // 1 / (1 - p)
+  int mode;              // 0: nothing is dropped, 1: by the words, 2: everything
+};
+
+struct DropKey {
+  uint32_t k0, k1, o0, o1;
+};
+
+__device__ __forceinline__ DropKey drop_key(const DropParams& p) {
+  uint64_t seed = p.seed, offset = p.offset;
+  if (p.mode == 1 && p.rng != nullptr) {
+    seed = p.rng[0];
+    offset += p.rng[1];
+  }
+  return DropKey{static_cast<uint32_t>(seed), static_cast<uint32_t>(seed >> 32),
+                 static_cast<uint32_t>(offset), static_cast<uint32_t>(offset >> 32)};
+}
+
+__device__ __forceinline__ uint4 philox(uint32_t quad, uint32_t row, const DropKey& key) {
+  uint32_t c0 = quad, c1 = row, c2 = key.o0, c3 = key.o1, k0 = key.k0, k1 = key.k1;
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t a = static_cast<uint64_t>(c0) * 0xD2511F53u;
+    const uint64_t b = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
+    c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
+    c1 = static_cast<uint32_t>(b);
+    c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
+    c3 = static_cast<uint32_t>(a);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return make_uint4(c0, c1, c2, c3);
+}
+
+// Four columns of a row, 4 * quad on.  A dropped element is zero whatever it was.
+__device__ __forceinline__ void drop_quad(const DropParams& p, const DropKey& key, uint32_t quad,
+                                          uint32_t row, float* v) {
+  if (p.mode == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = 0.0f;
+    return;
+  }
+  const uint4 w = philox(quad, row, key);
+  v[0] = w.x <= p.last ? v[0] * p.scale : 0.0f;
+  v[1] = w.y <= p.last ? v[1] * p.scale : 0.0f;
+  v[2] = w.z <= p.last ? v[2] * p.scale : 0.0f;
+  v[3] = w.w <= p.last ? v[3] * p.scale : 0.0f;
+}
+
+// What a call's p, seed and offset say; false where p is no probability.
+inline bool drop_params(DropParams* d, double p, uint64_t seed, uint64_t offset,
+                        const uint64_t* rng) {
+  if (!(p >= 0.0 && p <= 1.0)) return false;
+  const uint64_t kept = static_cast<uint64_t>((1.0 - p) * 4294967296.0 + 0.5);
+  d->rng = rng;
+  d->seed = seed;
+  d->offset = offset;
+  d->mode = p == 0.0 ? 0 : kept == 0 ? 2 : 1;
+  d->last = static_cast<uint32_t>(kept == 0 ? 0 : kept - 1);
+  d->scale = kept == 0 ? 0.0f : static_cast<float>(1.0 / (1.0 - p));
+  return true;
+}
+
+// ------------------------------------------------------------------ activations
+//
+// In fp32 from library functions.  sigmoid(t) = 1 / (1 + e^-t); the tanh form of gelu is
+// z sigmoid(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3), since (1 + tanh u) / 2 = sigmoid(2 u).
+
+constexpr float kTanhScale = 1.5957691216057308f;      // 2 sqrt(2 / pi)
+constexpr float kTanhCube = 0.044715f;
+
+// The quotient is exact to 2 units in the last place, and 0 where e^-t overflows.
+__device__ __forceinline__ float sigmoid(float t) { return __fdividef(1.0f, 1.0f + expf(-t)); }
+
+template <int kAct>
+__device__ __forceinline__ float act(float z) {
+  if constexpr (kAct == CP_ACT_RELU) return z < 0.0f ? 0.0f : z;
+  if constexpr (kAct == CP_ACT_SILU) return z * sigmoid(z);
+  if constexpr (kAct == CP_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+  if constexpr (kAct == CP_ACT_GELU_TANH)
+    return z * sigmoid(kTanhScale * (z + kTanhCube * z * z * z));
+  return z;
+}
+
+// Its derivative.
+template <int kAct>
+__device__ __forceinline__ float slope(float z) {
+  if constexpr (kAct == CP_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+  if constexpr (kAct == CP_ACT_SILU) {
+    const float s = sigmoid(z);
+    return s * (1.0f + z * (1.0f - s));
+  }
+  if constexpr (kAct == CP_ACT_GELU)
+    return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
+           z * 0.39894228040143268f * expf(-0.5f * z * z);
+  if constexpr (kAct == CP_ACT_GELU_TANH) {
+    const float s = sigmoid(kTanhScale * (z + kTanhCube * z * z * z));
+    const float bend = s * (1.0f - s);                 // 0 far out, where z^2 may overflow
+    return bend == 0.0f ? s : s + z * bend * kTanhScale * (1.0f + 3.0f * kTanhCube * z * z);
+  }
+  return 1.0f;
+}
+
+// f(std::integral_constant-like tag) for the call's activation: the choice is made once for a
+// set of values, the same for every thread.
+template <int kAct>
+struct ActTag {
+  static constexpr int value = kAct;
+};
+template <typename F>
+__device__ __forceinline__ void with_act(int which, F&& f) {
+  if (which == CP_ACT_RELU) f(ActTag<CP_ACT_RELU>{});
+  else if (which == CP_ACT_SILU) f(ActTag<CP_ACT_SILU>{});
+  else if (which == CP_ACT_GELU) f(ActTag<CP_ACT_GELU>{});
+  else if (which == CP_ACT_GELU_TANH) f(ActTag<CP_ACT_GELU_TANH>{});
+}
+
+inline bool act_ok(int a) { return a >= CP_ACT_NONE && a <= CP_ACT_GELU_TANH; }
+
+// --------------------------------------------------------------------- epilogue
+
+struct Epilogue {
+  const void* bias;        // [n], or null
+  const void* residual;    // [m][n] of out's type, or null
+  void* out;
+  void* pre;               // the sums in front of the activation, in the operands' type, or null
+  uint64_t ldr, ldo, ldp;
+  uint32_t m, n;
+  int bias_dtype, out_dtype, pre_dtype, act;
+  uint32_t aligned;        // rows of out, residual and pre all lie on 32-byte boundaries
+  DropParams drop;
+};
+
+// Four neighbouring elements of a row, those before n; whole where `vec` (rows on 16 bytes).
+__device__ __forceinline__ void load_quad(const void* p, uint64_t at, uint32_t left, int dtype,
+                                          bool vec, float (&v)[4]) {
+  if (vec && left >= 4) {
+    if (dtype == CP_F32) {
+      const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
+      const uint32_t w[2] = {x.x, x.y};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint16_t u = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+        v[i] = dtype == CP_F16 ? __half2float(__ushort_as_half(u))
+                               : __bfloat162float(__ushort_as_bfloat16(u));
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = static_cast<uint32_t>(i) < left ? load_as_f32(p, at + i, dtype) : 0.0f;
+}
+__device__ __forceinline__ void store_quad(void* p, uint64_t at, uint32_t left, int dtype, bool vec,
+                                           const float (&v)[4]) {
+  if (vec && left >= 4) {
+    if (dtype == CP_F32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = dtype == CP_F16 ? __half_as_ushort(__float2half_rn(v[i]))
+                               : __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + at) =
+          make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (static_cast<uint32_t>(i) < left) store_from_f32(p, at + i, dtype, v[i]);
+}
+
+// The whole epilogue of four neighbouring sums, col a multiple of 4.
+__device__ __forceinline__ void finish_quad(const Epilogue& e, const DropKey& key, uint32_t row,
+                                            uint32_t col, float (&v)[4]) {
+  const uint32_t left = e.n - col;
+  const bool vec = e.aligned != 0;
+  float r[4] = {};
+  if (e.residual != nullptr)
+    load_quad(e.residual, static_cast<uint64_t>(row) * e.ldr + col, left, e.out_dtype, vec, r);
+  if (e.bias != nullptr) {
+    float b[4];
+    load_quad(e.bias, col, left, e.bias_dtype, false, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += b[i];
+  }
+  if (e.pre != nullptr)
+    store_quad(e.pre, static_cast<uint64_t>(row) * e.ldp + col, left, e.pre_dtype, vec, v);
+  with_act(e.act, [&](auto tag) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = act<decltype(tag)::value>(v[i]);
+  });
+  if (e.drop.mode != 0) drop_quad(e.drop, key, col / 4, row, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] += r[i];
+  store_quad(e.out, static_cast<uint64_t>(row) * e.ldo + col, left, e.out_dtype, vec, v);
+}
+
+// Sixteen outputs of a row on a 32-byte boundary, whole sectors of L2.
+template <typename T>
+__device__ __forceinline__ void store16(T* to, const float* v) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      Packed<float> r;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r.w[i] = __float_as_uint(v[8 * h + i]);
+      store_octet(reinterpret_cast<float*>(to) + 8 * h, r);
+    }
+  } else {
+    Packed<float> r;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float u[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] = v[8 * h + i];
+      const Packed<T> x = pack<T>(u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.w[4 * h + i] = x.w[i];
+    }
+    store_octet(reinterpret_cast<float*>(to), r);
+  }
+}
+__device__ __forceinline__ void store32(void* p, uint64_t at, int dtype, const float (&v)[32]) {
+  if (dtype == CP_F32) {
+    store16(static_cast<float*>(p) + at, v);
+    store16(static_cast<float*>(p) + at + 16, v + 16);
+  } else if (dtype == CP_F16) {
+    store16(static_cast<__half*>(p) + at, v);
+    store16(static_cast<__half*>(p) + at + 16, v + 16);
+  } else {
+    store16(static_cast<__nv_bfloat16*>(p) + at, v);
+    store16(static_cast<__nv_bfloat16*>(p) + at + 16, v + 16);
+  }
+}
+// v += 32 elements on a 32-byte boundary.
+__device__ __forceinline__ void add32(float (&v)[32], const void* p, uint64_t at, int dtype) {
+  if (dtype == CP_F32) {
+    Packed<float> r[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) r[h] = load_octet(static_cast<const float*>(p) + at + 8 * h);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(r[i / 8].w[i % 8]);
+  } else {
+    Packed<float> r[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      r[h] = load_octet(reinterpret_cast<const float*>(static_cast<const uint16_t*>(p) + at + 16 * h));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t w = r[i / 8].w[i % 8];
+      if (dtype == CP_F16) {
+        v[2 * i] += __half2float(__ushort_as_half(static_cast<uint16_t>(w)));
+        v[2 * i + 1] += __half2float(__ushort_as_half(static_cast<uint16_t>(w >> 16)));
+      } else {
+        v[2 * i] += __uint_as_float(w << 16);
+        v[2 * i + 1] += __uint_as_float(w & 0xFFFF0000u);
+      }
+    }
+  }
+}
+
+// x[i] of lane t becomes x[t] of lane i: five exchanges between lanes.
+__device__ __forceinline__ void transpose32(float (&x)[32], uint32_t lane) {
+#pragma unroll
+  for (uint32_t s = 16; s > 0; s /= 2) {
+    const bool high = (lane & s) != 0;
+#pragma unroll
+    for (uint32_t i = 0; i < 32; ++i) {
+      if ((i & s) == 0) {
+        const float got = __shfl_xor_sync(0xFFFFFFFFu, high ? x[i] : x[i + s], s);
+        x[i] = high ? got : x[i];
+        x[i + s] = high ? x[i + s] : got;
+      }
+    }
+  }
+}
+
+// The epilogue of a warp's 32 rows (row0 on, one a lane) by 32 columns (col on, a multiple of
+// 32) of sums.  `bias`: the columns' bias in shared memory, zeros where there is none.  Rows on
+// 32-byte boundaries and columns all there: a lane reads and writes its own row, whole sectors.
+// Else the block is transposed, so that each access is of 32 neighbours of one row.
+template <bool kRich>
+__device__ __forceinline__ void finish_block(const Epilogue& e, const DropKey& key, uint32_t row0,
+                                             uint32_t col, uint32_t lane, const float* bias,
+                                             float (&v)[32]) {
+  const uint32_t row = row0 + lane;
+  const bool fast = e.aligned != 0 && col + 32 <= e.n;
+  if (e.bias != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 b = *reinterpret_cast<const float4*>(bias + 4 * i);
+      v[4 * i] += b.x;
+      v[4 * i + 1] += b.y;
+      v[4 * i + 2] += b.z;
+      v[4 * i + 3] += b.w;
+    }
+  }
+  const uint32_t rows = min(32u, e.m - row0);
+  if constexpr (kRich) {
+    if (e.pre != nullptr) {
+      if (fast) {
+        if (row < e.m) store32(e.pre, static_cast<uint64_t>(row) * e.ldp + col, e.pre_dtype, v);
+      } else {
+        float u[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) u[i] = v[i];
+        transpose32(u, lane);
+        if (col + lane < e.n) {
+          const uint64_t at = static_cast<uint64_t>(row0) * e.ldp + col + lane;
+#pragma unroll
+          for (uint32_t r = 0; r < 32; ++r)
+            if (r < rows) store_from_f32(e.pre, at + r * e.ldp, e.pre_dtype, u[r]);
+        }
+        __syncwarp();
+      }
+    }
+    with_act(e.act, [&](auto tag) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = act<decltype(tag)::value>(v[i]);
+    });
+    if (e.drop.mode != 0) {
+#pragma unroll
+      for (uint32_t q = 0; q < 8; ++q) drop_quad(e.drop, key, col / 4 + q, row, v + 4 * q);
+    }
+  }
+  if (fast) {
+    if (row < e.m) {
+      if (e.residual != nullptr)
+        add32(v, e.residual, static_cast<uint64_t>(row) * e.ldr + col, e.out_dtype);
+      store32(e.out, static_cast<uint64_t>(row) * e.ldo + col, e.out_dtype, v);
+    }
+    __syncwarp();
+    return;
+  }
+  transpose32(v, lane);
+  if (col + lane < e.n) {
+    if (e.residual != nullptr) {
+      const uint64_t at = static_cast<uint64_t>(row0) * e.ldr + col + lane;
+#pragma unroll
+      for (uint32_t r = 0; r < 32; ++r)
+        if (r < rows) v[r] += load_as_f32(e.residual, at + r * e.ldr, e.out_dtype);
+    }
+    const uint64_t at = static_cast<uint64_t>(row0) * e.ldo + col + lane;
+#pragma unroll
+    for (uint32_t r = 0; r < 32; ++r)
+      if (r < rows) store_from_f32(e.out, at + r * e.ldo, e.out_dtype, v[r]);
+  }
+  __syncwarp();
+}
+
+}  // namespace cpe

@@ -1,0 +1,368 @@
+// cp_linear.cu -- the projection in 16 bits with its epilogue, and its gradient (include/cp.h,
+// cp_linear, cp_linear_grad): the checked calls, and the gradient's pass over dy.
+#include <algorithm>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "cp.h"
+#include "cp_epilogue.cuh"
+#include "cp_internal.h"
+#include "cp_layer.cuh"
+#include "cp_linear.h"
+#include "cp_matmul_fp8.h"
+
+namespace {
+
+using namespace cpl;
+using cpe::DropKey;
+using cpe::DropParams;
+using cplin::ColumnSums;
+using cplin::Operand;
+using cplin::Product;
+
+// ------------------------------------------------------------------ dz and its column sums
+//
+// dz = D(dy) act'(pre), rounded to the products' type, and the sums of dz (before that rounding)
+// over blocks of rows.  A CTA has 256 columns (an octet a lane) and one of `count` shares of the
+// rows, eight at a time; its sums go to `parts`, which the products' kernel adds in order.  Bound by
+// memory: dy and pre read, dz written.
+
+constexpr int kGradThreads = 256;
+constexpr uint32_t kGradColumns = 256;
+constexpr uint32_t kMostParts = 64;
+constexpr uint32_t kGradAhead = 4;         // rows whose loads a thread has in flight
+
+struct GradParams {
+  const void* dy;
+  const void* pre;
+  void* dz;                // null: column sums alone
+  float* parts;            // [count][pitch], or null
+  uint64_t ldy, ldp, pitch;
+  uint32_t m, n, count;
+  int act;
+  DropParams drop;
+};
+
+template <typename T, typename D, bool VEC>
+__global__ void __launch_bounds__(kGradThreads) dz_kernel(const GradParams p) {
+  __shared__ float sums[8][kGradColumns];
+  wait_for_previous();
+  let_next_start();
+  const uint32_t lane = threadIdx.x & 31, line = threadIdx.x >> 5;
+  const uint32_t o = blockIdx.x * (kGradColumns / 8) + lane;
+  const uint32_t r0 = static_cast<uint32_t>(static_cast<uint64_t>(p.m) * blockIdx.y / p.count);
+  const uint32_t r1 =
+      static_cast<uint32_t>(static_cast<uint64_t>(p.m) * (blockIdx.y + 1) / p.count);
+  const DropKey key = cpe::drop_key(p.drop);
+  float acc[8] = {};
+  if (8ull * o < p.n) {
+    for (uint32_t r = r0 + line; r < r1; r += 8 * kGradAhead) {
+      Packed<D> dy[kGradAhead];
+      Packed<T> pre[kGradAhead];
+#pragma unroll
+      for (uint32_t i = 0; i < kGradAhead; ++i) {
+        const uint32_t row = r + 8 * i;
+        if (row < r1) {
+          dy[i] = load_row_octet<D, VEC>(static_cast<const D*>(p.dy) + row * p.ldy, o, p.n);
+          if (p.act != CP_ACT_NONE)
+            pre[i] = load_row_octet<T, VEC>(static_cast<const T*>(p.pre) + row * p.ldp, o, p.n);
+        }
+      }
+#pragma unroll
+      for (uint32_t i = 0; i < kGradAhead; ++i) {
+        const uint32_t row = r + 8 * i;
+        if (row < r1) {
+          float v[8];
+          unpack(dy[i], v);
+          if (p.drop.mode != 0) {
+            cpe::drop_quad(p.drop, key, 2 * o, row, v);
+            cpe::drop_quad(p.drop, key, 2 * o + 1, row, v + 4);
+          }
+          if (p.act != CP_ACT_NONE) {
+            float z[8];
+            unpack(pre[i], z);
+            cpe::with_act(p.act, [&](auto tag) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] *= cpe::slope<decltype(tag)::value>(z[e]);
+            });
+          }
+          if (p.dz != nullptr)       // (rows on 16-byte boundaries; what lies behind n is not read)
+            store_octet(static_cast<T*>(p.dz) + row * p.pitch + 8ull * o, pack<T>(v));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] += v[e];
+        }
+      }
+    }
+  }
+  if (p.parts == nullptr) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sums[line][8 * lane + e] = acc[e];
+  __syncthreads();
+  const uint32_t col = blockIdx.x * kGradColumns + threadIdx.x;
+  if (col < p.n) {
+    float s = sums[0][threadIdx.x];
+#pragma unroll
+    for (uint32_t i = 1; i < 8; ++i) s += sums[i][threadIdx.x];
+    p.parts[blockIdx.y * p.pitch + col] = s;
+  }
+}
+
+// Shares of the rows: about six CTAs an SM, and few enough parts for the products' kernel to add.
+uint32_t grad_parts(uint64_t m, uint64_t n) {
+  const uint64_t wide = (n + kGradColumns - 1) / kGradColumns;
+  const uint64_t want = std::max<uint64_t>(1, 152 * 6 / std::max<uint64_t>(wide, 1));
+  return static_cast<uint32_t>(std::min({want, (m + 7) / 8, static_cast<uint64_t>(kMostParts)}));
+}
+
+template <typename T, typename D>
+cudaError_t launch_dz(const GradParams& p, bool vec, cudaStream_t s) {
+  const Launch l{dim3((p.n + kGradColumns - 1) / kGradColumns, p.count), kGradThreads, 0, s};
+  return vec ? launch(l, &dz_kernel<T, D, true>, p) : launch(l, &dz_kernel<T, D, false>, p);
+}
+
+// ---------------------------------------------------------------------------- host
+
+constexpr uint64_t kMostRows = 1ull << 31, kMostK = 1ull << 30;
+
+uint64_t up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
+uint64_t row_pitch(uint64_t k) { return up(k, 8); }        // elements of a 16-bit row
+
+// Rows that a tensor map takes (and a row stride of their own: not one row for all).
+bool rows_ok(const void* p, uint64_t stride, uint64_t rows) {
+  return cpx::aligned(p, 16) && (rows == 1 || (stride % 8 == 0 && stride != 0));
+}
+
+cp_status refuse(const char* what) {
+  cpx::set_error(what);
+  return CP_ERR_INVALID_ARG;
+}
+
+bool row_ok(uint64_t stride, uint64_t d) { return stride >= d || stride == 0; }
+
+// Operands that lie on other boundaries, copied behind each other to `to` in one launch.
+cudaError_t align(Operand* (&op)[2], const uint64_t (&rows)[2], uint64_t k, uint8_t*& to,
+                  cudaStream_t s) {
+  cpm::AlignOperand of[2] = {};
+  const uint64_t pitch = 2 * row_pitch(k);
+  bool any = false;
+  for (int i = 0; i < 2; ++i) {
+    if (op[i] == nullptr || rows_ok(op[i]->p, op[i]->ld, rows[i])) continue;
+    of[i] = cpm::AlignOperand{static_cast<const uint8_t*>(op[i]->p), to, 2 * op[i]->ld, rows[i]};
+    op[i]->p = to;
+    op[i]->ld = pitch / 2;
+    to += rows[i] * pitch;
+    any = true;
+  }
+  return any ? cpm::align_rows(of, static_cast<uint32_t>(2 * k), s) : cudaSuccess;
+}
+
+// Bytes for the sums of products whose k is split; they begin on a 32-byte boundary, the workspace
+// on a 16-byte one.
+uint64_t part_bytes(const uint32_t (&m)[2], const uint32_t (&n)[2], const uint32_t (&k)[2],
+                    int count) {
+  const uint64_t floats = cplin::part_floats(m, n, k, count);
+  return floats == 0 ? 0 : 4 * floats + 16;
+}
+float* part_at(uint8_t* p) {
+  return reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(p) + 31) & ~static_cast<uintptr_t>(31));
+}
+
+}  // namespace
+
+extern "C" uint64_t cp_linear_workspace_bytes(const void* x, uint64_t x_stride, const void* w,
+                                              uint64_t w_stride, uint64_t m, uint64_t n,
+                                              uint64_t k) {
+  if (m >= kMostRows || n >= kMostRows || k >= kMostK || m == 0 || n == 0 || k == 0) return 0;
+  const uint32_t ms[2] = {static_cast<uint32_t>(m)}, ns[2] = {static_cast<uint32_t>(n)},
+                 ks[2] = {static_cast<uint32_t>(k)};
+  return ((rows_ok(x, x_stride, m) ? 0 : m) + (rows_ok(w, w_stride, n) ? 0 : n)) * 2 *
+             row_pitch(k) +
+         (m > cplin::kThinRows ? part_bytes(ms, ns, ks, 1) : 0);
+}
+
+extern "C" cp_status cp_linear(const void* x, uint64_t x_stride, const void* w, uint64_t w_stride,
+                               int dtype, uint64_t m, uint64_t n, uint64_t k, const void* bias,
+                               int bias_dtype, int activation, double p, uint64_t seed,
+                               uint64_t offset, const uint64_t* rng, const void* residual,
+                               uint64_t residual_stride, void* out, int out_dtype,
+                               uint64_t out_stride, void* pre, uint64_t pre_stride,
+                               void* workspace, uint64_t workspace_bytes, void* stream) {
+  if ((dtype != CP_F16 && dtype != CP_BF16) || !dtype_ok(out_dtype) ||
+      (bias != nullptr && !dtype_ok(bias_dtype)) || m >= kMostRows || n >= kMostRows ||
+      k >= kMostK || !row_ok(x_stride, k) || !row_ok(w_stride, k) || out_stride < n ||
+      (residual != nullptr && !row_ok(residual_stride, n)) ||
+      (pre != nullptr && pre_stride < n))
+    return refuse("bad dtype, m, n, k or row stride");
+  Product q{};
+  if (!cpe::act_ok(activation) || !cpe::drop_params(&q.e.drop, p, seed, offset, rng) ||
+      !cpx::aligned(rng, 8))
+    return refuse("bad activation, p or rng");
+  if (m == 0 || n == 0) return CP_OK;
+  const uint64_t elt = dtype_size(out_dtype);
+  if (out == nullptr || !cpx::aligned(out, elt) || !cpx::aligned(residual, elt) ||
+      !cpx::aligned(pre, 2) || (bias != nullptr && !cpx::aligned(bias, dtype_size(bias_dtype))) ||
+      (k != 0 && (x == nullptr || w == nullptr || !cpx::aligned(x, 2) || !cpx::aligned(w, 2))))
+    return refuse("null or misaligned x, w, bias, residual, out or pre");
+  const uint64_t need = cp_linear_workspace_bytes(x, x_stride, w, w_stride, m, n, k);
+  if (need != 0 &&
+      (workspace == nullptr || !cpx::aligned(workspace, 16) || workspace_bytes < need))
+    return refuse("workspace must be 16-byte aligned and hold cp_linear_workspace_bytes bytes");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  q.a = Operand{x, x_stride, false};
+  q.b = Operand{w, w_stride, false};
+  q.k = static_cast<uint32_t>(k);
+  q.dtype = dtype;
+  q.e.bias = bias;
+  q.e.residual = residual;
+  q.e.out = out;
+  q.e.pre = pre;
+  q.e.ldr = residual_stride;
+  q.e.ldo = out_stride;
+  q.e.ldp = pre_stride;
+  q.e.m = static_cast<uint32_t>(m);
+  q.e.n = static_cast<uint32_t>(n);
+  q.e.bias_dtype = bias_dtype;
+  q.e.out_dtype = out_dtype;
+  q.e.pre_dtype = dtype;
+  q.e.act = activation;
+  q.e.aligned = cpx::aligned(out, 32) && out_stride * elt % 32 == 0 &&
+                cpx::aligned(residual, 32) && residual_stride * elt % 32 == 0 &&
+                cpx::aligned(pre, 32) && pre_stride * 2 % 32 == 0;
+  if (k == 0) return cplin::launch_products(&q, 1, ColumnSums{}, nullptr, s);
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  Operand* op[2] = {&q.a, &q.b};
+  const cudaError_t e = align(op, {m, n}, k, at, s);
+  if (e != cudaSuccess) return cpx::cuda_fail(e, "linear launch");
+  if (m <= cplin::kThinRows) return cplin::launch_thin(q, s);
+  return cplin::launch_products(&q, 1, ColumnSums{}, part_at(at), s);
+}
+
+extern "C" uint64_t cp_linear_grad_workspace_bytes(uint64_t m, uint64_t n, uint64_t k) {
+  if (m >= kMostK || n >= kMostK || k >= kMostK) return 0;
+  // dz, copies of x and w, the parts of db, the sums of products whose k is split
+  const uint64_t dz = 2 * m * row_pitch(n), copies = 2 * (m + n) * row_pitch(k);
+  const uint64_t db = 4ull * grad_parts(m, n) * row_pitch(n);
+  uint64_t parts = 0;
+  if (m != 0 && n != 0 && k != 0) {
+    const uint32_t ms[2] = {static_cast<uint32_t>(m), static_cast<uint32_t>(n)};
+    const uint32_t ns[2] = {static_cast<uint32_t>(k), static_cast<uint32_t>(k)};
+    const uint32_t ks[2] = {static_cast<uint32_t>(n), static_cast<uint32_t>(m)};
+    parts = part_bytes(ms, ns, ks, 2);
+  }
+  return std::max<uint64_t>(16, dz + copies + db + parts);
+}
+
+extern "C" cp_status cp_linear_grad(const void* dy, int dy_dtype, uint64_t dy_stride,
+                                    const void* x, uint64_t x_stride, const void* w,
+                                    uint64_t w_stride, int dtype, const void* pre,
+                                    uint64_t pre_stride, uint64_t m, uint64_t n, uint64_t k,
+                                    int activation, double p, uint64_t seed, uint64_t offset,
+                                    const uint64_t* rng, int accumulate, void* dx,
+                                    uint64_t dx_stride, void* dw, int dw_dtype,
+                                    uint64_t dw_stride, void* db, int db_dtype, void* workspace,
+                                    uint64_t workspace_bytes, void* stream) {
+  if ((dtype != CP_F16 && dtype != CP_BF16) || (dy_dtype != dtype && dy_dtype != CP_F32) ||
+      (dw != nullptr && !dtype_ok(dw_dtype)) || (db != nullptr && !dtype_ok(db_dtype)) ||
+      m >= kMostK || n >= kMostK || k >= kMostK || !row_ok(dy_stride, n) || !row_ok(x_stride, k) ||
+      !row_ok(w_stride, k) || (pre != nullptr && !row_ok(pre_stride, n)) ||
+      (dx != nullptr && dx_stride < k) || (dw != nullptr && dw_stride < k) ||
+      (accumulate != 0 && accumulate != 1))
+    return refuse("bad dtype, m, n, k, row stride or accumulate");
+  GradParams g{};
+  if (!cpe::act_ok(activation) || (activation != CP_ACT_NONE) != (pre != nullptr) ||
+      !cpe::drop_params(&g.drop, p, seed, offset, rng) || !cpx::aligned(rng, 8))
+    return refuse("bad activation, pre, p or rng");
+  const bool want_dx = dx != nullptr && m != 0 && k != 0, want_dw = dw != nullptr && n != 0 && k != 0;
+  if (!cpx::aligned(dx, 2) || (dw != nullptr && !cpx::aligned(dw, dtype_size(dw_dtype))) ||
+      (db != nullptr && !cpx::aligned(db, dtype_size(db_dtype))) ||
+      (m != 0 && n != 0 && (dy == nullptr || !cpx::aligned(dy, dtype_size(dy_dtype)))) ||
+      !cpx::aligned(pre, 2) ||
+      (want_dx && n != 0 && (w == nullptr || !cpx::aligned(w, 2))) ||
+      (want_dw && m != 0 && (x == nullptr || !cpx::aligned(x, 2))))
+    return refuse("null or misaligned dy, x, w, pre, dx, dw or db");
+  if (workspace == nullptr || !cpx::aligned(workspace, 16) ||
+      workspace_bytes < cp_linear_grad_workspace_bytes(m, n, k))
+    return refuse("workspace must be 16-byte aligned and hold cp_linear_grad_workspace_bytes bytes");
+  if (!want_dx && !want_dw && (db == nullptr || n == 0)) return CP_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+
+  // dz, where it is not dy on 16-byte boundaries already, and the parts of db
+  Operand dz{dy, dy_stride, false};
+  const bool has_dy = m != 0 && n != 0;
+  const bool as_is = activation == CP_ACT_NONE && g.drop.mode == 0 && dy_dtype == dtype &&
+                     rows_ok(dy, dy_stride, m);
+  g.pitch = row_pitch(n);
+  if (!as_is) dz = Operand{at, g.pitch, false};
+  g.dz = as_is || (!want_dx && !want_dw) ? nullptr : at;
+  at += 2 * m * g.pitch;
+  ColumnSums sums{};
+  if (db != nullptr && n != 0) {
+    sums = ColumnSums{reinterpret_cast<float*>(at), db, g.pitch, has_dy ? grad_parts(m, n) : 0,
+                      static_cast<uint32_t>(n), db_dtype, accumulate};
+    g.parts = reinterpret_cast<float*>(at);
+  }
+  at += 4ull * grad_parts(m, n) * g.pitch;
+  cudaError_t e = cudaSuccess;
+  if (has_dy && (g.dz != nullptr || g.parts != nullptr)) {
+    g.dy = dy;
+    g.pre = pre;
+    g.ldy = dy_stride;
+    g.ldp = pre_stride;
+    g.m = static_cast<uint32_t>(m);
+    g.n = static_cast<uint32_t>(n);
+    g.count = grad_parts(m, n);
+    g.act = activation;
+    const bool vec = octets_ok(dy, dy_stride, g.n, dtype_size(dy_dtype)) &&
+                     (pre == nullptr || octets_ok(pre, pre_stride, g.n, 2));
+    if (dtype == CP_F16)
+      e = dy_dtype == CP_F32 ? launch_dz<__half, float>(g, vec, s)
+                             : launch_dz<__half, __half>(g, vec, s);
+    else
+      e = dy_dtype == CP_F32 ? launch_dz<__nv_bfloat16, float>(g, vec, s)
+                             : launch_dz<__nv_bfloat16, __nv_bfloat16>(g, vec, s);
+    if (e != cudaSuccess) return cpx::cuda_fail(e, "linear gradient launch");
+  }
+
+  // dx [m][k] = dz w: w is stored across n;  dw [n][k] = dz^T x: both are stored across m
+  Operand xo{x, x_stride, true}, wo{w, w_stride, true};
+  if (has_dy && k != 0) {
+    Operand* op[2] = {want_dw ? &xo : nullptr, want_dx ? &wo : nullptr};
+    e = align(op, {m, n}, k, at, s);
+    if (e != cudaSuccess) return cpx::cuda_fail(e, "linear gradient launch");
+  }
+  Product q[cplin::kMostProducts] = {};
+  int count = 0;
+  if (want_dx) {
+    Product& d = q[count++];
+    d.a = dz;
+    d.b = wo;
+    d.k = static_cast<uint32_t>(n);
+    d.e.out = dx;
+    d.e.ldo = dx_stride;
+    d.e.m = static_cast<uint32_t>(m);
+    d.e.out_dtype = dtype;
+  }
+  if (want_dw && !(m == 0 && accumulate != 0)) {
+    Product& d = q[count++];
+    d.a = Operand{dz.p, dz.ld, true};
+    d.b = xo;
+    d.k = static_cast<uint32_t>(m);
+    d.e.out = dw;
+    d.e.ldo = dw_stride;
+    d.e.m = static_cast<uint32_t>(n);
+    d.e.out_dtype = dw_dtype;
+    if (accumulate != 0) {
+      d.e.residual = dw;
+      d.e.ldr = dw_stride;
+    }
+  }
+  for (int i = 0; i < count; ++i) {
+    Product& d = q[i];
+    d.dtype = dtype;
+    d.e.n = static_cast<uint32_t>(k);
+    d.e.aligned = cpx::aligned(d.e.out, 32) && d.e.ldo * dtype_size(d.e.out_dtype) % 32 == 0;
+  }
+  return cplin::launch_products(q, count, sums, part_at(at), s);
+}

@@ -1,0 +1,49 @@
+// cp_linear.h -- host side of cp_linear and cp_linear_grad shared by their translation units.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "cp.h"
+#include "cp_epilogue.cuh"
+
+namespace cplin {
+
+// A 16-bit operand on 16-byte boundaries: `rows` of the product's rows (or columns) by k.
+struct Operand {
+  const void* p;
+  uint64_t ld;             // elements between the array's rows
+  bool across;             // stored [k][rows] instead of [rows][k]
+};
+
+// out[i][j] = epilogue(sum over k of a[i][k] b[j][k]), e.m rows by e.n columns.
+struct Product {
+  Operand a, b;
+  uint32_t k;
+  int dtype;               // CP_F16 or CP_BF16
+  cpe::Epilogue e;
+};
+
+// Sums over rows that another kernel left in parts: out[j] (+)= sum of parts[i][j].
+struct ColumnSums {
+  const float* parts;      // [count][pitch]
+  void* out;               // null: none
+  uint64_t pitch;
+  uint32_t count, n;
+  int dtype, accumulate;
+};
+
+// Products of one launch on CTA pairs (cp_linear_tc.cu), two at most; `part` holds
+// part_floats(products) floats where some are split along k.
+constexpr int kMostProducts = 2;
+uint64_t part_floats(const uint32_t (&m)[kMostProducts], const uint32_t (&n)[kMostProducts],
+                     const uint32_t (&k)[kMostProducts], int count);
+cp_status launch_products(const Product* q, int count, const ColumnSums& sums, float* part,
+                          cudaStream_t s);
+
+// Up to kThinRows rows of a: tiles of 128 rows of b, neither operand stored across.
+constexpr uint32_t kThinRows = 128;
+cp_status launch_thin(const Product& q, cudaStream_t s);
+
+}  // namespace cplin

@@ -1,0 +1,825 @@
+// cp_linear_tc.cu -- the 16-bit products of cp_linear and cp_linear_grad on tensor memory
+// (tcgen05), for operands whose rows lie on 16-byte boundaries (include/cp.h).
+//
+//   out[i][j] = epilogue(sum over k of a[i][k] b[j][k])
+#include <atomic>
+#include <cstdint>
+#include <mutex>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "cp.h"
+#include "cp_epilogue.cuh"
+#include "cp_internal.h"
+#include "cp_layer.cuh"
+#include "cp_linear.h"
+#include "cp_ring.h"
+#include "cp_tcgen05.cuh"
+
+namespace {
+
+using namespace cpl;
+using cpe::DropKey;
+using cpe::Epilogue;
+using cplin::ColumnSums;
+using cplin::kMostProducts;
+
+// A wait that ran out sets this word; cp_linear_status reads and clears it.
+__device__ uint32_t g_linear_gave_up;
+
+// --------------------------------------------------------------- pairs of SMs
+//
+// A pair of CTAs (two SMs) makes 256 x bn sums, bn a multiple of 32 up to 256.  Each CTA stages
+// its 128 rows of a and its half of the bn rows of b, 64 of k a stage.  An operand that is stored
+// along k comes as rows of 128 bytes; one that is stored across k (the gradient's: dz and x for dw,
+// w for dx) as blocks of 64 by 64 that the tensor core transposes as it reads them, so neither
+// is ever transposed in memory.  Roles: a warp issues the TMA loads, a warp of the first CTA
+// the tcgen05.mma, eight warps per CTA finish the sums of one of two tensor-memory buffers while
+// the tensor core fills the other (a lane has a row, the warps of a half every other block of
+// 32 columns), two add up the column sums that the kernel before left in parts.  A CTA pair
+// walks over its units: tiles of up to two products (dx and dw of one call), the k of each
+// shared by `splits` units where there are few; their sums go to a workspace, and finish_kernel adds
+// them in order.
+
+constexpr int kSumWarps = 8;
+constexpr int kThreads = (kSumWarps + 4) * 32;         // + the TMA warp, the MMA warp, two for columns
+constexpr uint32_t kStageK = 64;                       // of k in a stage: 128 bytes
+constexpr uint32_t kMaxStages = 8;
+constexpr uint32_t kTileA = 128 * 128;                 // bytes of a's rows per stage and CTA
+constexpr uint32_t kBlock = 64 * 128;                  // bytes of a 64 x 64 block stored across k
+constexpr uint32_t kSmemMost = 220 * 1024;             // dynamic shared memory of a CTA
+constexpr uint32_t kBuffer = 256;                      // columns of tensor memory of a buffer
+constexpr uint32_t kRasterRows = 16;                   // tiles along m that are walked together
+
+struct PairProduct {
+  Epilogue e;
+  float* part;               // sums of the splits, [splits][m][pitch]
+  uint64_t pitch;
+  uint32_t kblocks, bn, splits, tiles_m, tiles_n, tiles;
+  uint32_t b_bytes, b_boxes; // of b, a stage and CTA
+  uint32_t instr;
+  int a_across, b_across;
+};
+
+struct PairParams {
+  CUtensorMap map_a[kMostProducts], map_b[kMostProducts];
+  PairProduct q[kMostProducts];
+  ColumnSums sums;
+  uint32_t first_units, units, stages, stage_bytes;
+};
+
+struct Unit {
+  uint32_t which, split, row0, col0, kb0, kb1;
+};
+
+__device__ __forceinline__ Unit unit_of(const PairParams& p, uint32_t u) {
+  Unit r;
+  r.which = u < p.first_units ? 0 : 1;
+  if (r.which != 0) u -= p.first_units;
+  const PairProduct& q = p.q[r.which];
+  r.split = u / q.tiles;
+  const uint32_t tile = u - r.split * q.tiles;
+  const uint32_t wide = kRasterRows * q.tiles_n, g = tile / wide, at = tile - g * wide;
+  const uint32_t rows = min(kRasterRows, q.tiles_m - g * kRasterRows), tn = at / rows;
+  r.row0 = (g * kRasterRows + at - tn * rows) * 256;
+  r.col0 = tn * q.bn;
+  r.kb0 = static_cast<uint32_t>(static_cast<uint64_t>(q.kblocks) * r.split / q.splits);
+  r.kb1 = static_cast<uint32_t>(static_cast<uint64_t>(q.kblocks) * (r.split + 1) / q.splits);
+  return r;
+}
+
+// kRich: some product has an activation, dropout, or sums to keep.
+template <bool kRich>
+__global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constant__ PairParams p) {
+  extern __shared__ uint8_t dyn[];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5];
+  __shared__ __align__(16) float bias[kSumWarps][4][32];
+  __shared__ uint32_t tmem_base;
+  __shared__ uint32_t issued;              // this CTA's fills of stages
+  __shared__ int gave_up;
+  uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t half = cpt::cluster_rank();
+  const uint32_t full = cpt::smem_addr(bars), empty = full + 8 * kMaxStages;
+  const uint32_t acc_full = empty + 8 * kMaxStages, acc_empty = acc_full + 16;
+  const uint32_t drained = acc_empty + 16;
+  // the first CTA's barriers hold the pair's loads and reads
+  const uint32_t pair_full = cpt::map_rank(full, 0);
+  const uint32_t pair_acc_empty = cpt::map_rank(acc_empty, 0);
+
+  if (threadIdx.x == 0) {
+    for (uint32_t s = 0; s < p.stages; ++s) {
+      cpt::mbar_init(full + 8 * s, 1);
+      cpt::mbar_init(empty + 8 * s, 1);
+    }
+    for (uint32_t b = 0; b < 2; ++b) {
+      cpt::mbar_init(acc_full + 8 * b, 1);
+      cpt::mbar_init(acc_empty + 8 * b, 2 * kSumWarps);
+    }
+    cpt::mbar_init(drained, 1);
+    cpt::mbar_init_fence();
+    gave_up = 0;
+  }
+  if (warp == kSumWarps + 1) cpt::tmem_alloc_pair(cpt::smem_addr(&tmem_base), 2 * kBuffer);
+  cpt::tc_fence_before();
+  __syncthreads();
+  cpt::cluster_sync();
+  cpt::tc_fence_after();
+  wait_for_previous();          // (the set-up above runs while the kernel before this one ends)
+  let_next_start();
+  const uint32_t tmem = tmem_base;
+  const uint32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  // Every warp of the pair comes here when its role ends.  If a wait of the first CTA ran out,
+  // whichever warp's, what the pair has in flight then ends before either CTA leaves its shared and
+  // tensor memory (the second waits at the cluster's last barrier): loads up to the last fill that
+  // either CTA began, all of which count on the first CTA's barriers, and every product issued.
+  // These waits have a limit too.  Where the first CTA has not given up, its finishing warps have
+  // seen every product done, so nothing is in flight.
+  auto end_role = [&] {
+    __syncwarp();
+    cpt::tc_fence_before();
+    asm volatile("barrier.sync 1, %0;" ::"n"(kThreads) : "memory");
+    cpt::cluster_sync();
+  };
+
+  if (warp == kSumWarps) {
+    // ---------------------------------------------------------------- loads
+    if (cpt::elect_one()) {
+      for (int i = 0; i < kMostProducts; ++i) {
+        cpt::tma_prefetch_map(&p.map_a[i]);
+        cpt::tma_prefetch_map(&p.map_b[i]);
+      }
+    }
+    __syncwarp();
+    uint32_t s = 0, round = 0, fills = 0;
+    bool ok = true;
+    for (uint32_t u = pair; u < p.units && ok; u += pairs) {
+      const Unit t = unit_of(p, u);
+      const PairProduct& q = p.q[t.which];
+      const CUtensorMap *map_a = &p.map_a[t.which], *map_b = &p.map_b[t.which];
+      const bool a1 = t.row0 + 128 < q.e.m;             // the second CTA has rows of a
+      const bool mine = half == 0 || a1;
+      const uint32_t bytes = 2 * q.b_bytes + (a1 ? 2 : 1) * kTileA;
+      const uint32_t row = t.row0 + half * 128, col = t.col0 + half * (q.bn / 2);
+      for (uint32_t kb = t.kb0; kb < t.kb1; ++kb) {
+        if (round > 0) {
+          ok = cpt::mbar_wait(empty + 8 * s, (round - 1) & 1, &gave_up);
+          if (!ok) break;
+        }
+        const uint32_t dst = cpt::smem_addr(tiles) + s * p.stage_bytes, k0 = kb * kStageK;
+        if (cpt::elect_one()) {
+          const uint32_t bar = pair_full + 8 * s;
+          if (half == 0) cpt::mbar_expect(full + 8 * s, bytes);
+          if (mine) {
+            if (q.a_across) {
+              cpt::tma_load_pair(dst, map_a, row, k0, bar);
+              cpt::tma_load_pair(dst + kBlock, map_a, row + 64, k0, bar);
+            } else {
+              cpt::tma_load_pair(dst, map_a, k0, row, bar);
+            }
+          }
+          if (q.b_across) {
+            for (uint32_t i = 0; i < q.b_boxes; ++i)
+              cpt::tma_load_pair(dst + kTileA + i * kBlock, map_b, col + 64 * i, k0, bar);
+          } else {
+            cpt::tma_load_pair(dst + kTileA, map_b, k0, col, bar);
+          }
+        }
+        __syncwarp();
+        ++fills;
+        if (++s == p.stages) {
+          s = 0;
+          ++round;
+        }
+      }
+    }
+    if (lane == 0) issued = fills;
+    end_role();
+    if (gave_up != 0 && half == 0) {
+      const uint32_t other = cpt::load_cluster1(cpt::map_rank(cpt::smem_addr(&issued), 1));
+      int late = 0;
+      for (uint32_t k = 0; k < p.stages; ++k) {
+        const LastFill last = last_fill(fills, other, p.stages, k);
+        if (last.any) cpt::mbar_wait(full + 8 * k, last.parity, &late);
+      }
+    }
+  } else if (warp == kSumWarps + 1 && half == 0) {
+    // ------------------------------------------------------------- products
+    uint32_t it = 0, s = 0, round = 0;
+    bool ok = true;
+    for (uint32_t u = pair; u < p.units && ok; u += pairs, ++it) {
+      const Unit t = unit_of(p, u);
+      const PairProduct& q = p.q[t.which];
+      const uint32_t b = it & 1;
+      const uint32_t a_step = q.a_across ? 128 : 2, b_step = q.b_across ? 128 : 2;
+      ok = it < 2 || cpt::mbar_wait(acc_empty + 8 * b, ((it >> 1) - 1) & 1, &gave_up);
+      if (!ok) break;
+      cpt::tc_fence_after();
+      for (uint32_t kb = t.kb0; kb < t.kb1; ++kb) {
+        ok = cpt::mbar_wait(full + 8 * s, round & 1, &gave_up);
+        if (!ok) break;
+        cpt::tc_fence_after();
+        const uint32_t at = cpt::smem_addr(tiles) + s * p.stage_bytes;
+        const uint64_t da = q.a_across ? cpt::operand_desc_mn(at) : cpt::operand_desc(at);
+        const uint64_t db =
+            q.b_across ? cpt::operand_desc_mn(at + kTileA) : cpt::operand_desc(at + kTileA);
+        if (cpt::elect_one()) {
+#pragma unroll
+          for (uint32_t k = 0; k < 4; ++k)
+            cpt::mma_half_pair(tmem + b * kBuffer, da + k * a_step, db + k * b_step, q.instr,
+                               kb != t.kb0 || k != 0);
+          cpt::mma_commit_pair(empty + 8 * s, 3);
+          if (kb + 1 == t.kb1) cpt::mma_commit_pair(acc_full + 8 * b, 3);
+        }
+        __syncwarp();
+        if (++s == p.stages) {
+          s = 0;
+          ++round;
+        }
+      }
+    }
+    end_role();
+    if (gave_up != 0) {
+      int late = 0;
+      if (cpt::elect_one()) cpt::mma_commit_pair(drained, 1);
+      __syncwarp();
+      cpt::mbar_wait(drained, 0, &late);
+    }
+  } else if (warp >= kSumWarps + 2) {
+    // ---------------------------------------------------------- column sums
+    if (p.sums.out != nullptr) {
+      for (uint32_t c = (blockIdx.x * 2 + warp - kSumWarps - 2) * 32 + lane; c < p.sums.n;
+           c += gridDim.x * 64) {
+        float sum = 0.0f;
+#pragma unroll 8
+        for (uint32_t i = 0; i < p.sums.count; ++i)
+          sum += p.sums.parts[static_cast<uint64_t>(i) * p.sums.pitch + c];
+        if (p.sums.accumulate) sum += load_as_f32(p.sums.out, c, p.sums.dtype);
+        store_from_f32(p.sums.out, c, p.sums.dtype, sum);
+      }
+    }
+    end_role();
+  } else if (warp < kSumWarps) {
+    // --------------------------------------------------------------- finish
+    const uint32_t lanes = (warp & 3) * 32, group = warp >> 2;
+    const DropKey key = cpe::drop_key(p.q[0].e.drop);      // (dropout is in the first product alone)
+    uint32_t it = 0;
+    bool ok = true;
+    for (uint32_t u = pair; u < p.units && ok; u += pairs, ++it) {
+      const Unit t = unit_of(p, u);
+      const PairProduct& q = p.q[t.which];
+      const uint32_t b = it & 1, blocks = q.bn / 32;
+      const uint32_t row0 = t.row0 + half * 128 + lanes;
+      const bool raw = q.splits > 1;
+      if (q.e.bias != nullptr && !raw) {
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+          const uint32_t col = t.col0 + (2 * i + group) * 32 + lane;
+          if (2 * i + group < blocks)
+            bias[warp][i][lane] = col < q.e.n ? load_as_f32(q.e.bias, col, q.e.bias_dtype) : 0.0f;
+        }
+        __syncwarp();
+      }
+      ok = cpt::mbar_wait(acc_full + 8 * b, (it >> 1) & 1, &gave_up);
+      if (!ok) break;
+      cpt::tc_fence_after();
+      uint32_t left = 0;                       // blocks of this warp that have outputs
+      if (row0 < q.e.m)
+        for (uint32_t c = group; c < blocks && t.col0 + 32 * c < q.e.n; c += 2) ++left;
+      if (left == 0) {
+        cpt::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) cpt::mbar_arrive_cluster(pair_acc_empty + 8 * b);
+      }
+      for (uint32_t i = 0; i < left; ++i) {
+        const uint32_t c = 2 * i + group, col = t.col0 + 32 * c;
+        float v[32];
+        cpt::tmem_load32<0>(v, tmem + (lanes << 16) + b * kBuffer + 32 * c);
+        cpt::tmem_load_wait(v);
+        if (i + 1 == left) {                   // the buffer is read: the tensor core may have it back
+          cpt::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) cpt::mbar_arrive_cluster(pair_acc_empty + 8 * b);
+        }
+        if (raw) {
+          if (row0 + lane < q.e.m)
+            cpe::store32(q.part,
+                         (static_cast<uint64_t>(t.split) * q.e.m + row0 + lane) * q.pitch + col,
+                         CP_F32, v);
+          __syncwarp();
+        } else {
+          cpe::finish_block<kRich>(q.e, key, row0, col, lane, bias[warp][i], v);
+        }
+      }
+    }
+    if (!ok && lane == 0) atomicOr(&g_linear_gave_up, 1u);
+    end_role();
+  } else {
+    end_role();
+  }
+  __syncwarp();
+  cpt::cluster_sync();                 // no CTA leaves while the other may use its memory
+  if (warp == kSumWarps + 1) cpt::tmem_free_pair(tmem, 2 * kBuffer);
+}
+
+// ------------------------------------------------------------- sums of the splits
+//
+// Four neighbouring sums a thread: the splits' added in order, then the epilogue.  Also the whole
+// of a product whose k is 0 (no splits: sums of nothing).
+
+struct FinishProduct {
+  Epilogue e;
+  const float* part;
+  uint64_t pitch;
+  uint32_t splits, quads;              // quads of a row
+};
+struct FinishParams {
+  FinishProduct q[kMostProducts];
+  uint64_t first, total;               // quads of the first product, of both
+};
+
+constexpr int kFinishThreads = 256;
+
+__global__ void __launch_bounds__(kFinishThreads)
+    finish_kernel(const __grid_constant__ FinishParams p) {
+  wait_for_previous();
+  let_next_start();
+  const DropKey key = cpe::drop_key(p.q[0].e.drop);
+  const uint64_t step = static_cast<uint64_t>(gridDim.x) * kFinishThreads;
+  for (uint64_t u = static_cast<uint64_t>(blockIdx.x) * kFinishThreads + threadIdx.x; u < p.total;
+       u += step) {
+    const FinishProduct& q = p.q[u < p.first ? 0 : 1];
+    const uint64_t at = u < p.first ? u : u - p.first;
+    const uint32_t row = static_cast<uint32_t>(at / q.quads);
+    const uint32_t col = static_cast<uint32_t>(at - static_cast<uint64_t>(row) * q.quads) * 4;
+    float v[4] = {};
+#pragma unroll 4
+    for (uint32_t i = 0; i < q.splits; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(
+          q.part + (static_cast<uint64_t>(i) * q.e.m + row) * q.pitch + col);
+      v[0] += x.x;
+      v[1] += x.y;
+      v[2] += x.z;
+      v[3] += x.w;
+    }
+    cpe::finish_quad(q.e, key, row, col, v);
+  }
+}
+
+// ------------------------------------------- few rows of a, many bytes of b: one SM
+//
+// With at most 128 rows of a the operands change places: 128 rows of b are the tensor core's
+// 128 x 16 operand, up to 64 rows of a its N (16, 32 or 64) columns, and the kernel is bound by
+// the stream of b (a second tile of rows of a finds it in L2).  Two CTAs share an SM; `splits` CTAs
+// of a cluster share a tile's k and add their sums in order through distributed shared memory.
+
+constexpr int kThinThreads = 256;      // four finishing warps, TMA, MMA, two idle
+constexpr uint32_t kThinMaxStages = 6;
+constexpr uint32_t kThinSmem = 111616; // dynamic shared memory of a CTA, two to an SM
+
+struct ThinParams {
+  Epilogue e;
+  uint32_t kblocks, splits, stages, tiles_m, instr;
+};
+
+template <uint32_t kN>
+__global__ void __launch_bounds__(kThinThreads, 2)
+    thin_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                const __grid_constant__ ThinParams p) {
+  constexpr uint32_t kStage = kTileA + kN * 128;
+  constexpr uint32_t kColumns = kN < 32 ? 32 : kN;
+  extern __shared__ uint8_t dyn[];
+  __shared__ __align__(8) uint64_t bars[2 * kThinMaxStages + 2];
+  __shared__ uint32_t tmem_base;
+  __shared__ int gave_up;
+  uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = p.splits == 1 ? 0 : cpt::cluster_rank();
+  const uint32_t tile = blockIdx.x / p.splits;       // those of one part of b come together
+  const uint32_t row0 = tile / p.tiles_m * 128;
+  const uint32_t token0 = tile % p.tiles_m * kN, tokens = min(p.e.m - token0, kN);
+  const uint32_t full = cpt::smem_addr(bars), empty = full + 8 * kThinMaxStages;
+  const uint32_t acc_full = empty + 8 * kThinMaxStages, drained = acc_full + 8;
+  if (threadIdx.x == 0) {
+    for (uint32_t s = 0; s < p.stages; ++s) {
+      cpt::mbar_init(full + 8 * s, 1);
+      cpt::mbar_init(empty + 8 * s, 1);
+    }
+    cpt::mbar_init(acc_full, 1);
+    cpt::mbar_init(drained, 1);
+    cpt::mbar_init_fence();
+    gave_up = 0;
+  }
+  if (warp == 5) cpt::tmem_alloc(cpt::smem_addr(&tmem_base), kColumns);
+  cpt::tc_fence_before();
+  __syncthreads();
+  cpt::tc_fence_after();
+  wait_for_previous();
+  let_next_start();
+  const uint32_t tmem = tmem_base;
+  const uint32_t kb0 = static_cast<uint32_t>(static_cast<uint64_t>(p.kblocks) * rank / p.splits);
+  const uint32_t kb1 =
+      static_cast<uint32_t>(static_cast<uint64_t>(p.kblocks) * (rank + 1) / p.splits);
+  float* part = reinterpret_cast<float*>(tiles);     // [row of a][row of b], over the stages
+  bool ok = true;
+  // Every warp comes here when its role ends.  If a wait ran out, whichever warp's, the loads and
+  // products in flight then end (their waits have a limit too) before the stages and tensor memory
+  // are used for anything else.
+  auto end_role = [&] {
+    if (!ok && lane == 0) atomicOr(&g_linear_gave_up, 1u);
+    __syncwarp();
+    cpt::tc_fence_before();
+    asm volatile("barrier.sync 1, %0;" ::"n"(kThinThreads) : "memory");
+  };
+
+  if (warp == 4) {
+    // ------------------------------------------------------------------ loads
+    if (cpt::elect_one()) {
+      cpt::tma_prefetch_map(&map_a);
+      cpt::tma_prefetch_map(&map_b);
+    }
+    __syncwarp();
+    uint32_t s = 0, round = 0, fills = 0;
+    for (uint32_t kb = kb0; kb < kb1; ++kb) {
+      if (round > 0) {
+        ok = cpt::mbar_wait(empty + 8 * s, (round - 1) & 1, &gave_up);
+        if (!ok) break;
+      }
+      const uint32_t dst = cpt::smem_addr(tiles) + s * kStage;
+      if (cpt::elect_one()) {
+        cpt::mbar_expect(full + 8 * s, kStage);
+        cpt::tma_load(dst, &map_b, kb * kStageK, row0, full + 8 * s);
+        cpt::tma_load(dst + kTileA, &map_a, kb * kStageK, token0, full + 8 * s);
+      }
+      __syncwarp();
+      ++fills;
+      if (++s == p.stages) {
+        s = 0;
+        ++round;
+      }
+    }
+    end_role();
+    if (gave_up != 0) {
+      int late = 0;
+      for (uint32_t k = 0; k < p.stages; ++k) {
+        const LastFill last = last_fill(fills, fills, p.stages, k);
+        if (last.any) cpt::mbar_wait(full + 8 * k, last.parity, &late);
+      }
+    }
+  } else if (warp == 5) {
+    // --------------------------------------------------------------- products
+    uint32_t s = 0, round = 0;
+    for (uint32_t kb = kb0; kb < kb1; ++kb) {
+      ok = cpt::mbar_wait(full + 8 * s, round & 1, &gave_up);
+      if (!ok) break;
+      cpt::tc_fence_after();
+      const uint32_t at = cpt::smem_addr(tiles) + s * kStage;
+      const uint64_t db = cpt::operand_desc(at), da = cpt::operand_desc(at + kTileA);
+      if (cpt::elect_one()) {
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k)
+          cpt::mma_half_one(tmem, db + 2 * k, da + 2 * k, p.instr, kb != kb0 || k != 0);
+        cpt::mma_commit(empty + 8 * s);
+        if (kb + 1 == kb1) cpt::mma_commit(acc_full);
+      }
+      __syncwarp();
+      if (++s == p.stages) {
+        s = 0;
+        ++round;
+      }
+    }
+    end_role();
+    if (gave_up != 0) {
+      int late = 0;
+      if (cpt::elect_one()) cpt::mma_commit(drained);
+      __syncwarp();
+      cpt::mbar_wait(drained, 0, &late);
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------------- sums
+    ok = cpt::mbar_wait(acc_full, 0, &gave_up);
+    if (ok) {                            // (all products are done: the stages are free)
+      cpt::tc_fence_after();
+      const uint32_t at = tmem + ((warp * 32) << 16);
+#pragma unroll
+      for (uint32_t c = 0; c < (kN + 31) / 32; ++c) {
+        float x[32] = {};
+        if constexpr (kN == 16) cpt::tmem_load16<0>(x, at);
+        else cpt::tmem_load32<0>(x, at + 32 * c);
+        cpt::tmem_load_wait(x);
+#pragma unroll
+        for (uint32_t i = 0; i < (kN < 32 ? kN : 32); ++i)
+          part[(32 * c + i) * 128 + threadIdx.x] = x[i];
+      }
+    }
+    end_role();
+  } else {
+    end_role();
+  }
+  __syncthreads();
+  if (p.splits > 1) cpt::cluster_sync();
+  const DropKey key = cpe::drop_key(p.e.drop);
+  const uint32_t i0 = tokens * 32 * rank / p.splits, i1 = tokens * 32 * (rank + 1) / p.splits;
+  for (uint32_t i = i0 + threadIdx.x; i < i1; i += kThinThreads) {
+    const uint32_t at = cpt::smem_addr(part + 4 * i);
+    float v[4];
+    if (p.splits == 1) {
+      const float4 x = *reinterpret_cast<const float4*>(part + 4 * i);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else {
+      float4 x[8];
+#pragma unroll
+      for (uint32_t q = 0; q < 8; ++q)
+        if (q < p.splits) x[q] = cpt::load_cluster4(cpt::map_rank(at, q));
+      v[0] = x[0].x; v[1] = x[0].y; v[2] = x[0].z; v[3] = x[0].w;
+#pragma unroll
+      for (uint32_t q = 1; q < 8; ++q) {
+        if (q < p.splits) {
+          v[0] += x[q].x;
+          v[1] += x[q].y;
+          v[2] += x[q].z;
+          v[3] += x[q].w;
+        }
+      }
+    }
+    const uint32_t col = row0 + i % 32 * 4;
+    if (col < p.e.n) cpe::finish_quad(p.e, key, token0 + i / 32, col, v);
+  }
+  if (p.splits > 1) cpt::cluster_sync();  // no CTA leaves while another may read its shared memory
+  __syncwarp();
+  if (warp == 5) cpt::tmem_free(tmem, kColumns);
+}
+
+// ---------------------------------------------------------------------------- host
+
+// What a launch needs to know of the device, found once.
+struct Device {
+  std::atomic<int> state{0};           // 1: found
+  int pairs = 0;                       // clusters of two CTAs that run at once
+};
+Device g_devices[64];
+std::mutex g_device_lock;
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+std::atomic<EncodeTiled> g_encode{nullptr};
+
+const Device* device(cudaError_t* err) {
+  int dev = 0;
+  *err = cudaGetDevice(&dev);
+  if (*err == cudaSuccess && dev >= 64) *err = cudaErrorInvalidDevice;
+  if (*err != cudaSuccess) return nullptr;
+  Device& d = g_devices[dev];
+  if (d.state.load(std::memory_order_acquire) == 1) return &d;
+  const std::lock_guard<std::mutex> one(g_device_lock);
+  if (d.state.load(std::memory_order_acquire) == 1) return &d;
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  *err = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                          &found);
+  if (*err != cudaSuccess) return nullptr;
+  if (fn == nullptr || found != cudaDriverEntryPointSuccess) {
+    *err = cudaErrorNotSupported;
+    return nullptr;
+  }
+  g_encode.store(reinterpret_cast<EncodeTiled>(fn));
+  auto allow = [&](const void* kernel, uint32_t bytes) {
+    if (*err == cudaSuccess)
+      *err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  static_cast<int>(bytes));
+  };
+  allow(reinterpret_cast<const void*>(&pairs_kernel<false>), kSmemMost);
+  allow(reinterpret_cast<const void*>(&pairs_kernel<true>), kSmemMost);
+  allow(reinterpret_cast<const void*>(&thin_kernel<16>), kThinSmem);
+  allow(reinterpret_cast<const void*>(&thin_kernel<32>), kThinSmem);
+  allow(reinterpret_cast<const void*>(&thin_kernel<64>), kThinSmem);
+  if (*err != cudaSuccess) return nullptr;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(256);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemMost;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int most = 0;
+  *err = cudaOccupancyMaxActiveClusters(&most, reinterpret_cast<const void*>(&pairs_kernel<true>),
+                                        &cfg);
+  if (*err == cudaSuccess && most < 1) *err = cudaErrorInvalidConfiguration;
+  if (*err != cudaSuccess) return nullptr;
+  d.pairs = most;
+  d.state.store(1, std::memory_order_release);
+  return &d;
+}
+
+// Boxes of 64 elements of the array's rows by box_rows of them.
+bool encode_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t ld,
+                uint32_t box_rows) {
+  const cuuint64_t dims[2] = {inner, rows};
+  const cuuint64_t strides[1] = {rows == 1 ? (2 * inner + 15) / 16 * 16 : 2 * ld};
+  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint32_t elem[2] = {1, 1};
+  return g_encode.load()(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims,
+                         strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Columns of a tile and units that share its k.  By shapes alone, for the 76 pairs of a whole
+// card, so that a product's sums and its workspace are the same wherever it runs.
+constexpr uint32_t kPairs = 76;
+struct Tiling {
+  uint32_t bn, splits;
+};
+Tiling choose_tiling(uint32_t m, uint32_t n, uint32_t k) {
+  const uint32_t kblocks = (k + kStageK - 1) / kStageK;
+  const uint64_t tiles_m = (static_cast<uint64_t>(m) + 255) / 256;
+  Tiling best{32, 1};
+  double least = 1e300;
+  for (uint32_t s = 1; s <= 32 && s <= (kblocks + 3) / 4; ++s) {
+    for (uint32_t bn = 256; bn >= 32; bn -= 32) {
+      const uint64_t units = tiles_m * ((static_cast<uint64_t>(n) + bn - 1) / bn) * s;
+      if (s > 1 && units > 2 * kPairs) continue;
+      const double turns = static_cast<double>((units + kPairs - 1) / kPairs);
+      const double stage = bn <= 128 ? 190.0 : 1.5 * bn;
+      double cost = turns * ((kblocks + s - 1) / s * stage + 400.0) + 8.0 * bn;
+      if (s > 1) cost += 3000.0 + 8e-4 * s * m * static_cast<double>(n);
+      if (cost < least) {
+        least = cost;
+        best = Tiling{bn, s};
+      }
+    }
+  }
+  return best;
+}
+uint64_t part_pitch(uint32_t n) { return (static_cast<uint64_t>(n) + 31) / 32 * 32; }
+
+bool rich(const Epilogue& e) {
+  return e.act != CP_ACT_NONE || e.drop.mode != 0 || e.pre != nullptr;
+}
+
+cp_status too_many_tiles() {
+  cpx::set_error("m and n make more than 2^31 tiles");
+  return CP_ERR_INVALID_ARG;
+}
+
+}  // namespace
+
+namespace cplin {
+
+uint64_t part_floats(const uint32_t (&m)[kMostProducts], const uint32_t (&n)[kMostProducts],
+                     const uint32_t (&k)[kMostProducts], int count) {
+  uint64_t floats = 0;
+  for (int i = 0; i < count; ++i) {
+    const Tiling t = choose_tiling(m[i], n[i], k[i]);
+    if (t.splits > 1) floats += static_cast<uint64_t>(t.splits) * m[i] * part_pitch(n[i]);
+  }
+  return floats;
+}
+
+cp_status launch_products(const Product* q, int count, const ColumnSums& sums, float* part,
+                          cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  const Device* d = device(&e);
+  if (d == nullptr) return cpx::cuda_fail(e, "linear device query");
+  PairParams p{};
+  FinishParams f{};
+  bool is_rich = false, finish = false;
+  uint64_t units[kMostProducts] = {};
+  int used = 0;
+  for (int i = 0; i < count; ++i) {
+    const Epilogue& ep = q[i].e;
+    if (ep.m == 0 || ep.n == 0) continue;
+    const uint64_t quads = (static_cast<uint64_t>(ep.n) + 3) / 4;
+    FinishProduct& fp = f.q[i];
+    fp.e = ep;
+    fp.quads = static_cast<uint32_t>(quads);
+    if (q[i].k == 0) {                     // sums of nothing
+      finish = true;
+      (i == 0 ? f.first : f.total) += quads * ep.m;
+      continue;
+    }
+    PairProduct& x = p.q[used];
+    const Tiling t = choose_tiling(ep.m, ep.n, q[i].k);
+    x.e = ep;
+    x.kblocks = (q[i].k + kStageK - 1) / kStageK;
+    x.bn = t.bn;
+    x.splits = t.splits;
+    x.tiles_m = (ep.m + 255) / 256;
+    x.tiles_n = (ep.n + t.bn - 1) / t.bn;
+    const uint64_t tiles = static_cast<uint64_t>(x.tiles_m) * x.tiles_n;
+    units[used] = tiles * t.splits;
+    if (units[used] >= (1ull << 31)) return too_many_tiles();
+    x.tiles = static_cast<uint32_t>(tiles);
+    x.a_across = q[i].a.across;
+    x.b_across = q[i].b.across;
+    x.b_boxes = x.b_across ? (t.bn / 2 + 63) / 64 : 1;
+    x.b_bytes = x.b_across ? x.b_boxes * kBlock : t.bn / 2 * 128;
+    x.instr = cpt::half_instr_desc(256, t.bn, q[i].dtype == CP_BF16, x.a_across, x.b_across);
+    if (t.splits > 1) {
+      x.pitch = part_pitch(ep.n);
+      x.part = part;
+      part += static_cast<uint64_t>(t.splits) * ep.m * x.pitch;
+      fp.part = x.part;
+      fp.pitch = x.pitch;
+      fp.splits = t.splits;
+      finish = true;
+      (i == 0 ? f.first : f.total) += quads * ep.m;
+    } else {
+      is_rich |= rich(ep);
+    }
+    const Operand &a = q[i].a, &b = q[i].b;
+    const bool ok =
+        (a.across ? encode_map(&p.map_a[used], a.p, ep.m, q[i].k, a.ld, kStageK)
+                  : encode_map(&p.map_a[used], a.p, q[i].k, ep.m, a.ld, 128)) &&
+        (b.across ? encode_map(&p.map_b[used], b.p, ep.n, q[i].k, b.ld, kStageK)
+                  : encode_map(&p.map_b[used], b.p, q[i].k, ep.n, b.ld, t.bn / 2));
+    if (!ok) {
+      cpx::set_error("tensor map refused");
+      return CP_ERR_CUDA;
+    }
+    p.stage_bytes = max(p.stage_bytes, kTileA + x.b_bytes);
+    ++used;
+  }
+  if (units[0] + units[1] >= (1ull << 31)) return too_many_tiles();
+  if (used > 0 || (sums.out != nullptr && sums.n != 0)) {
+    p.sums = sums;
+    p.first_units = static_cast<uint32_t>(units[0]);
+    p.units = static_cast<uint32_t>(units[0] + units[1]);
+    if (used == 0) p.stage_bytes = kTileA;
+    if (used == 1) {                       // (prefetched, not used)
+      p.map_a[1] = p.map_a[0];
+      p.map_b[1] = p.map_b[0];
+    }
+    p.stages = min((kSmemMost - 1024) / p.stage_bytes, kMaxStages);
+    uint32_t pairs = p.units;
+    if (sums.out != nullptr) pairs = max(pairs, (sums.n + 127) / 128);
+    pairs = min(pairs, static_cast<uint32_t>(d->pairs));
+    const Launch l{dim3(2 * pairs), kThreads, kSmemMost, s, 2};
+    e = is_rich ? launch(l, &pairs_kernel<true>, p) : launch(l, &pairs_kernel<false>, p);
+    if (e != cudaSuccess) return cpx::cuda_fail(e, "linear launch");
+  }
+  if (finish) {
+    f.total += f.first;
+    const uint64_t ctas = (f.total + kFinishThreads - 1) / kFinishThreads;
+    e = launch(Launch{dim3(static_cast<unsigned>(ctas < 1216 ? ctas : 1216)), kFinishThreads, 0, s},
+               &finish_kernel, f);
+    if (e != cudaSuccess) return cpx::cuda_fail(e, "linear launch");
+  }
+  return CP_OK;
+}
+
+cp_status launch_thin(const Product& q, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if (device(&e) == nullptr) return cpx::cuda_fail(e, "linear device query");
+  const uint32_t m = q.e.m, n = q.e.n;
+  const uint32_t kn = m <= 16 ? 16 : m <= 32 ? 32 : 64;
+  ThinParams p{};
+  p.e = q.e;
+  p.kblocks = (q.k + kStageK - 1) / kStageK;
+  p.tiles_m = (m + kn - 1) / kn;
+  const uint64_t tiles = (static_cast<uint64_t>(n) + 127) / 128 * p.tiles_m;
+  // CTAs share a tile until there are enough to keep every SM's loads in flight.
+  p.splits = 1;
+  while (p.splits < 8 && tiles * p.splits * 2 <= 304 && p.kblocks >= 2 * p.splits) p.splits *= 2;
+  if (tiles * p.splits >= (1ull << 31)) return too_many_tiles();
+  p.instr = cpt::half_instr_desc(128, kn, q.dtype == CP_BF16, false, false);
+  p.stages = min((kThinSmem - 1024) / (kTileA + kn * 128), kThinMaxStages);
+  CUtensorMap map_a, map_b;
+  if (!encode_map(&map_a, q.a.p, q.k, m, q.a.ld, kn) ||
+      !encode_map(&map_b, q.b.p, q.k, n, q.b.ld, 128)) {
+    cpx::set_error("tensor map refused");
+    return CP_ERR_CUDA;
+  }
+  const Launch l{dim3(static_cast<unsigned>(tiles * p.splits)), kThinThreads, kThinSmem, s,
+                 p.splits};
+  e = kn == 16   ? launch(l, &thin_kernel<16>, map_a, map_b, p)
+      : kn == 32 ? launch(l, &thin_kernel<32>, map_a, map_b, p)
+                 : launch(l, &thin_kernel<64>, map_a, map_b, p);
+  if (e != cudaSuccess) return cpx::cuda_fail(e, "linear launch");
+  return CP_OK;
+}
+
+}  // namespace cplin
+
+extern "C" cp_status cp_linear_status(void* stream) {
+  cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cpx::cuda_fail(e, "linear");
+  uint32_t word = 0;
+  e = cudaMemcpyFromSymbol(&word, g_linear_gave_up, sizeof(word));
+  if (e != cudaSuccess) return cpx::cuda_fail(e, "linear status");
+  if (word == 0) return CP_OK;
+  const uint32_t zero = 0;
+  e = cudaMemcpyToSymbol(g_linear_gave_up, &zero, sizeof(zero));
+  if (e != cudaSuccess) return cpx::cuda_fail(e, "linear status");
+  cpx::set_error("a wait inside cp_linear or cp_linear_grad ran out of time; its output is not valid");
+  return CP_ERR_CUDA;
+}

@@ -74,13 +74,8 @@ constexpr uint64_t kAlignCtas = 152 * 6;                  // as many as run at o
 constexpr uint32_t kAlignPieces = 4;                      // 16-byte pieces of a lane
 constexpr uint32_t kAlignBytes = 32 * 16 * kAlignPieces;  // of a row, by one warp at a time
 
-struct AlignOperand {
-  const uint8_t* from;
-  uint8_t* to;
-  uint64_t ld, rows;       // rows: 0 for an operand that stays where it is
-};
 struct AlignParams {
-  AlignOperand of[2];
+  cpm::AlignOperand of[2];
   uint32_t k, chunks;      // chunks of kAlignBytes in a row
   uint64_t pitch;
 };
@@ -328,6 +323,23 @@ cp_status launch_few(const MatmulParams& p, bool aligned, cudaStream_t s) {
 
 }  // namespace
 
+namespace cpm {
+
+cudaError_t align_rows(const AlignOperand (&of)[2], uint32_t k, cudaStream_t s) {
+  AlignParams c{};
+  c.of[0] = of[0];
+  c.of[1] = of[1];
+  c.k = k;
+  c.pitch = aligned_pitch(k);
+  c.chunks = (k + kAlignBytes - 1) / kAlignBytes;
+  const uint64_t units = (c.of[0].rows + c.of[1].rows) * c.chunks;
+  const uint64_t ctas = (units + kAlignThreads / 32 - 1) / (kAlignThreads / 32);
+  return launch_after(&align_rows_kernel, dim3(static_cast<unsigned>(std::min(ctas, kAlignCtas))),
+                      kAlignThreads, 0, s, c);
+}
+
+}  // namespace cpm
+
 namespace {
 bool few_rows(uint64_t m, uint64_t n, uint64_t k) { return m <= kFewRows && n * k <= kFewBytes; }
 }  // namespace
@@ -387,27 +399,21 @@ extern "C" cp_status cp_matmul_fp8(const uint8_t* a, uint64_t a_stride, const fl
       cpx::set_error("workspace must be 16-byte aligned and hold cp_matmul_fp8_workspace_bytes bytes");
       return CP_ERR_INVALID_ARG;
     }
-    AlignParams c{};
-    c.k = p.k;
-    c.pitch = aligned_pitch(k);
-    c.chunks = (p.k + kAlignBytes - 1) / kAlignBytes;
+    cpm::AlignOperand of[2] = {};
+    const uint64_t pitch = aligned_pitch(k);
     uint8_t* to = static_cast<uint8_t*>(workspace);
     if (!a_ok) {
-      c.of[0] = AlignOperand{a, to, a_stride, m};
+      of[0] = cpm::AlignOperand{a, to, a_stride, m};
       p.a = to;
-      p.lda = c.pitch;
-      to += m * c.pitch;
+      p.lda = pitch;
+      to += m * pitch;
     }
     if (!w_ok) {
-      c.of[1] = AlignOperand{w, to, w_stride, n};
+      of[1] = cpm::AlignOperand{w, to, w_stride, n};
       p.w = to;
-      p.ldw = c.pitch;
+      p.ldw = pitch;
     }
-    const uint64_t units = (c.of[0].rows + c.of[1].rows) * c.chunks;
-    const uint64_t ctas = (units + kAlignThreads / 32 - 1) / (kAlignThreads / 32);
-    const cudaError_t e =
-        launch_after(&align_rows_kernel, dim3(static_cast<unsigned>(std::min(ctas, kAlignCtas))),
-                     kAlignThreads, 0, s, c);
+    const cudaError_t e = cpm::align_rows(of, p.k, s);
     if (e != cudaSuccess) return cpx::cuda_fail(e, "fp8 matmul launch");
   }
   return m > kThinRows ? cpm::launch_pairs(p, s) : cpm::launch_thin(p, s);

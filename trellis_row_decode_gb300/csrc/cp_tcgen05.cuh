@@ -1,4 +1,4 @@
-// cp_tcgen05.cuh -- the sm_103a instructions that the 8-bit product is made of, one
+// cp_tcgen05.cuh -- the sm_103a instructions that the 8-bit and 16-bit products are made of, one
 // function each: mbarriers with a limit on every wait, TMA tile loads, tensor memory,
 // tcgen05.mma for CTA pairs.
 #pragma once
@@ -244,6 +244,46 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
 // Instruction descriptor: fp32 accumulator, e4m3 operands, both K-major, M x N.
 __host__ __device__ constexpr uint32_t e4m3_instr_desc(uint32_t m, uint32_t n) {
   return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+// Shared-memory descriptor of a 16-bit operand stored along its rows or columns (M or N) instead
+// of k: blocks of 64 of them (128 bytes, 128-byte swizzle) by 64 of k, a block 8192 bytes behind
+// the one before, eight of k 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand_desc_mn(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (512ull << 16) | (64ull << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+
+// Instruction descriptor: fp32 accumulator, bf16 or fp16 operands, each along k or across it.
+__host__ __device__ constexpr uint32_t half_instr_desc(uint32_t m, uint32_t n, bool bf16, bool a_mn,
+                                                       bool b_mn) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) |
+         (b_mn ? 1u << 16 : 0u) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+// D[256 x N over the pair] (+)= A (256 x 16) * B (N x 16)^T, 16-bit operands.
+__device__ __forceinline__ void mma_half_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t instr,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "setp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+      "}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(instr), "r"(accumulate)
+      : "memory");
+}
+// The same within one CTA: D[128 x N] (+)= A (128 x 16) * B (N x 16)^T.
+__device__ __forceinline__ void mma_half_one(uint32_t d, uint64_t a, uint64_t b, uint32_t instr,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "setp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      "}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(instr), "r"(accumulate)
+      : "memory");
 }
 
 // D[256 x N over the pair] (+)= A (256 x 32) * B (N x 32)^T, issued by the pair's first CTA.
