@@ -50,6 +50,11 @@ constexpr uint32_t kTileA = 128 * 128;                 // bytes of a's rows per 
 constexpr uint32_t kBlock = 64 * 128;                  // bytes of a 64 x 64 block stored across k
 constexpr uint32_t kSmemMost = 220 * 1024;             // dynamic shared memory of a CTA
 constexpr uint32_t kBuffer = 256;                      // columns of tensor memory of a buffer
+constexpr uint32_t kSegment = 8;                       // stages that the tensor core adds up alone
+// Registers with segments: launched with 168 a thread (65,536 over 12 warps); the finishing warps
+// (128 sums a thread) take what the other four give up.
+constexpr int kLaunchRegs = 168, kFinishRegs = 208, kOtherRegs = 88;
+static_assert(2 * kFinishRegs + kOtherRegs <= 3 * kLaunchRegs, "a warpgroup's share of the launch");
 constexpr uint32_t kRasterRows = 16;                   // tiles along m that are walked together
 
 struct PairProduct {
@@ -90,7 +95,11 @@ __device__ __forceinline__ Unit unit_of(const PairParams& p, uint32_t u) {
 }
 
 // kRich: some product has an activation, dropout, or sums to keep.
-template <bool kRich>
+// kSegments: some product is wanted in 32 bits.  The tensor core cuts its running sum at every
+// addition instead of rounding it, an error that grows with k (measured, relative: 1.07e-9 k,
+// 4.4e-6 at k = 4096, where fp32 additions that round leave 6e-7); so the sum is read every kSegment
+// stages and added up in registers.
+template <bool kRich, bool kSegments>
 __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constant__ PairParams p) {
   extern __shared__ uint8_t dyn[];
   __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5];
@@ -144,133 +153,152 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
     cpt::cluster_sync();
   };
 
-  if (warp == kSumWarps) {
-    // ---------------------------------------------------------------- loads
-    if (cpt::elect_one()) {
-      for (int i = 0; i < kMostProducts; ++i) {
-        cpt::tma_prefetch_map(&p.map_a[i]);
-        cpt::tma_prefetch_map(&p.map_b[i]);
-      }
-    }
-    __syncwarp();
-    uint32_t s = 0, round = 0, fills = 0;
-    bool ok = true;
-    for (uint32_t u = pair; u < p.units && ok; u += pairs) {
-      const Unit t = unit_of(p, u);
-      const PairProduct& q = p.q[t.which];
-      const CUtensorMap *map_a = &p.map_a[t.which], *map_b = &p.map_b[t.which];
-      const bool a1 = t.row0 + 128 < q.e.m;             // the second CTA has rows of a
-      const bool mine = half == 0 || a1;
-      const uint32_t bytes = 2 * q.b_bytes + (a1 ? 2 : 1) * kTileA;
-      const uint32_t row = t.row0 + half * 128, col = t.col0 + half * (q.bn / 2);
-      for (uint32_t kb = t.kb0; kb < t.kb1; ++kb) {
-        if (round > 0) {
-          ok = cpt::mbar_wait(empty + 8 * s, (round - 1) & 1, &gave_up);
-          if (!ok) break;
+  if (warp >= kSumWarps) {
+    if constexpr (kSegments) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kSumWarps) {
+      // ---------------------------------------------------------------- loads
+      uint32_t fills = 0;
+      if (cpt::elect_one()) {
+        for (int i = 0; i < kMostProducts; ++i) {
+          cpt::tma_prefetch_map(&p.map_a[i]);
+          cpt::tma_prefetch_map(&p.map_b[i]);
         }
-        const uint32_t dst = cpt::smem_addr(tiles) + s * p.stage_bytes, k0 = kb * kStageK;
-        if (cpt::elect_one()) {
-          const uint32_t bar = pair_full + 8 * s;
-          if (half == 0) cpt::mbar_expect(full + 8 * s, bytes);
-          if (mine) {
-            if (q.a_across) {
-              cpt::tma_load_pair(dst, map_a, row, k0, bar);
-              cpt::tma_load_pair(dst + kBlock, map_a, row + 64, k0, bar);
-            } else {
-              cpt::tma_load_pair(dst, map_a, k0, row, bar);
+        const uint32_t stages = p.stages, stage_bytes = p.stage_bytes;
+        uint32_t s = 0, round = 0;
+        bool ok = true, ready = false;       // ready: the next stage is known to be free
+        for (uint32_t u = pair; u < p.units && ok; u += pairs) {
+          const Unit t = unit_of(p, u);
+          const PairProduct& q = p.q[t.which];
+          const CUtensorMap *map_a = &p.map_a[t.which], *map_b = &p.map_b[t.which];
+          const bool a_across = q.a_across != 0, b_across = q.b_across != 0;
+          const bool a1 = t.row0 + 128 < q.e.m;             // the second CTA has rows of a
+          const bool mine = half == 0 || a1;
+          const uint32_t b_boxes = q.b_boxes;
+          const uint32_t bytes = 2 * q.b_bytes + (a1 ? 2 : 1) * kTileA;
+          const uint32_t row = t.row0 + half * 128, col = t.col0 + half * (q.bn / 2);
+          for (uint32_t kb = t.kb0; kb < t.kb1; ++kb) {
+            if (!ready && round > 0) {
+              ok = cpt::mbar_wait_one(empty + 8 * s, (round - 1) & 1, &gave_up);
+              if (!ok) break;
             }
+            const uint32_t dst = cpt::smem_addr(tiles) + s * stage_bytes, k0 = kb * kStageK;
+            const uint32_t bar = pair_full + 8 * s, mine_full = full + 8 * s;
+            if (++s == stages) {
+              s = 0;
+              ++round;
+            }
+            ready = round > 0 && cpt::mbar_try(empty + 8 * s, (round - 1) & 1);
+            if (half == 0) cpt::mbar_expect(mine_full, bytes);
+            if (mine) {
+              if (a_across) {
+                cpt::tma_load_pair(dst, map_a, row, k0, bar);
+                cpt::tma_load_pair(dst + kBlock, map_a, row + 64, k0, bar);
+              } else {
+                cpt::tma_load_pair(dst, map_a, k0, row, bar);
+              }
+            }
+            if (b_across) {
+              for (uint32_t i = 0; i < b_boxes; ++i)
+                cpt::tma_load_pair(dst + kTileA + i * kBlock, map_b, col + 64 * i, k0, bar);
+            } else {
+              cpt::tma_load_pair(dst + kTileA, map_b, k0, col, bar);
+            }
+            ++fills;
           }
-          if (q.b_across) {
-            for (uint32_t i = 0; i < q.b_boxes; ++i)
-              cpt::tma_load_pair(dst + kTileA + i * kBlock, map_b, col + 64 * i, k0, bar);
-          } else {
-            cpt::tma_load_pair(dst + kTileA, map_b, k0, col, bar);
-          }
         }
-        __syncwarp();
-        ++fills;
-        if (++s == p.stages) {
-          s = 0;
-          ++round;
-        }
+        issued = fills;
       }
-    }
-    if (lane == 0) issued = fills;
-    end_role();
-    if (gave_up != 0 && half == 0) {
-      const uint32_t other = cpt::load_cluster1(cpt::map_rank(cpt::smem_addr(&issued), 1));
-      int late = 0;
-      for (uint32_t k = 0; k < p.stages; ++k) {
-        const LastFill last = last_fill(fills, other, p.stages, k);
-        if (last.any) cpt::mbar_wait(full + 8 * k, last.parity, &late);
-      }
-    }
-  } else if (warp == kSumWarps + 1 && half == 0) {
-    // ------------------------------------------------------------- products
-    uint32_t it = 0, s = 0, round = 0;
-    bool ok = true;
-    for (uint32_t u = pair; u < p.units && ok; u += pairs, ++it) {
-      const Unit t = unit_of(p, u);
-      const PairProduct& q = p.q[t.which];
-      const uint32_t b = it & 1;
-      const uint32_t a_step = q.a_across ? 128 : 2, b_step = q.b_across ? 128 : 2;
-      ok = it < 2 || cpt::mbar_wait(acc_empty + 8 * b, ((it >> 1) - 1) & 1, &gave_up);
-      if (!ok) break;
-      cpt::tc_fence_after();
-      for (uint32_t kb = t.kb0; kb < t.kb1; ++kb) {
-        ok = cpt::mbar_wait(full + 8 * s, round & 1, &gave_up);
-        if (!ok) break;
-        cpt::tc_fence_after();
-        const uint32_t at = cpt::smem_addr(tiles) + s * p.stage_bytes;
-        const uint64_t da = q.a_across ? cpt::operand_desc_mn(at) : cpt::operand_desc(at);
-        const uint64_t db =
-            q.b_across ? cpt::operand_desc_mn(at + kTileA) : cpt::operand_desc(at + kTileA);
-        if (cpt::elect_one()) {
-#pragma unroll
-          for (uint32_t k = 0; k < 4; ++k)
-            cpt::mma_half_pair(tmem + b * kBuffer, da + k * a_step, db + k * b_step, q.instr,
-                               kb != t.kb0 || k != 0);
-          cpt::mma_commit_pair(empty + 8 * s, 3);
-          if (kb + 1 == t.kb1) cpt::mma_commit_pair(acc_full + 8 * b, 3);
-        }
-        __syncwarp();
-        if (++s == p.stages) {
-          s = 0;
-          ++round;
-        }
-      }
-    }
-    end_role();
-    if (gave_up != 0) {
-      int late = 0;
-      if (cpt::elect_one()) cpt::mma_commit_pair(drained, 1);
       __syncwarp();
-      cpt::mbar_wait(drained, 0, &late);
-    }
-  } else if (warp >= kSumWarps + 2) {
-    // ---------------------------------------------------------- column sums
-    if (p.sums.out != nullptr) {
-      for (uint32_t c = (blockIdx.x * 2 + warp - kSumWarps - 2) * 32 + lane; c < p.sums.n;
-           c += gridDim.x * 64) {
-        float sum = 0.0f;
-#pragma unroll 8
-        for (uint32_t i = 0; i < p.sums.count; ++i)
-          sum += p.sums.parts[static_cast<uint64_t>(i) * p.sums.pitch + c];
-        if (p.sums.accumulate) sum += load_as_f32(p.sums.out, c, p.sums.dtype);
-        store_from_f32(p.sums.out, c, p.sums.dtype, sum);
+      fills = issued;
+      end_role();
+      if (gave_up != 0 && half == 0) {
+        const uint32_t other = cpt::load_cluster1(cpt::map_rank(cpt::smem_addr(&issued), 1));
+        int late = 0;
+        for (uint32_t k = 0; k < p.stages; ++k) {
+          const LastFill last = last_fill(fills, other, p.stages, k);
+          if (last.any) cpt::mbar_wait(full + 8 * k, last.parity, &late);
+        }
       }
+    } else if (warp == kSumWarps + 1 && half == 0) {
+      // ------------------------------------------------------------- products
+      if (cpt::elect_one()) {
+        const uint32_t stages = p.stages, stage_bytes = p.stage_bytes;
+        uint32_t it = 0, s = 0, round = 0;
+        bool ok = true, ready = false;       // ready: the next stage is known to be full
+        for (uint32_t u = pair; u < p.units && ok; u += pairs) {
+          const Unit t = unit_of(p, u);
+          const PairProduct& q = p.q[t.which];
+          const uint32_t instr = q.instr;
+          const uint64_t a_step = q.a_across ? 128 : 2, b_step = q.b_across ? 128 : 2;
+          const uint64_t a_base = q.a_across ? cpt::operand_desc_mn(0) : cpt::operand_desc(0);
+          const uint64_t b_base = q.b_across ? cpt::operand_desc_mn(0) : cpt::operand_desc(0);
+          for (uint32_t kb = t.kb0; kb < t.kb1 && ok; ++it) {
+            const uint32_t b = it & 1, to = tmem + b * kBuffer;
+            const uint32_t end = kSegments ? min(kb + kSegment, t.kb1) : t.kb1;
+            ok = it < 2 || cpt::mbar_wait_one(acc_empty + 8 * b, ((it >> 1) - 1) & 1, &gave_up);
+            if (!ok) break;
+            uint32_t more = 0;
+            for (; kb < end; ++kb) {
+              if (!ready) {
+                ok = cpt::mbar_wait_one(full + 8 * s, round & 1, &gave_up);
+                if (!ok) break;
+              }
+              cpt::tc_fence_after();
+              const uint32_t at = (cpt::smem_addr(tiles) + s * stage_bytes) >> 4;
+              const uint32_t free = empty + 8 * s;
+              if (++s == stages) {
+                s = 0;
+                ++round;
+              }
+              ready = cpt::mbar_try(full + 8 * s, round & 1);
+              const uint64_t da = a_base + at, db = b_base + (at + kTileA / 16);
+              cpt::mma_half_pair(to, da, db, instr, more);
+#pragma unroll
+              for (uint32_t k = 1; k < 4; ++k)
+                cpt::mma_half_pair(to, da + k * a_step, db + k * b_step, instr, 1);
+              more = 1;
+              cpt::mma_commit_pair(free, 3);
+            }
+            if (ok) cpt::mma_commit_pair(acc_full + 8 * b, 3);
+          }
+        }
+      }
+      __syncwarp();
+      end_role();
+      if (gave_up != 0) {
+        int late = 0;
+        if (cpt::elect_one()) cpt::mma_commit_pair(drained, 1);
+        __syncwarp();
+        cpt::mbar_wait(drained, 0, &late);
+      }
+    } else if (warp >= kSumWarps + 2) {
+      // ---------------------------------------------------------- column sums
+      if (p.sums.out != nullptr) {
+        for (uint32_t c = (blockIdx.x * 2 + warp - kSumWarps - 2) * 32 + lane; c < p.sums.n;
+             c += gridDim.x * 64) {
+          float sum = 0.0f;
+#pragma unroll 8
+          for (uint32_t i = 0; i < p.sums.count; ++i)
+            sum += p.sums.parts[static_cast<uint64_t>(i) * p.sums.pitch + c];
+          if (p.sums.accumulate) sum += load_as_f32(p.sums.out, c, p.sums.dtype);
+          store_from_f32(p.sums.out, c, p.sums.dtype, sum);
+        }
+      }
+      end_role();
+    } else {
+      end_role();
     }
-    end_role();
-  } else if (warp < kSumWarps) {
+  } else {
     // --------------------------------------------------------------- finish
+    if constexpr (kSegments) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFinishRegs));
     const uint32_t lanes = (warp & 3) * 32, group = warp >> 2;
     const DropKey key = cpe::drop_key(p.q[0].e.drop);      // (dropout is in the first product alone)
     uint32_t it = 0;
     bool ok = true;
-    for (uint32_t u = pair; u < p.units && ok; u += pairs, ++it) {
+    for (uint32_t u = pair; u < p.units && ok; u += pairs) {
       const Unit t = unit_of(p, u);
       const PairProduct& q = p.q[t.which];
-      const uint32_t b = it & 1, blocks = q.bn / 32;
+      const uint32_t blocks = q.bn / 32;
       const uint32_t row0 = t.row0 + half * 128 + lanes;
       const bool raw = q.splits > 1;
       if (q.e.bias != nullptr && !raw) {
@@ -282,27 +310,17 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
         }
         __syncwarp();
       }
-      ok = cpt::mbar_wait(acc_full + 8 * b, (it >> 1) & 1, &gave_up);
-      if (!ok) break;
-      cpt::tc_fence_after();
       uint32_t left = 0;                       // blocks of this warp that have outputs
       if (row0 < q.e.m)
         for (uint32_t c = group; c < blocks && t.col0 + 32 * c < q.e.n; c += 2) ++left;
-      if (left == 0) {
+      const uint32_t tmem_warp = tmem + (lanes << 16) + 32 * group;
+      auto give_back = [&](uint32_t b) {       // the tensor core may have the buffer again
         cpt::tc_fence_before();
         __syncwarp();
         if (lane == 0) cpt::mbar_arrive_cluster(pair_acc_empty + 8 * b);
-      }
-      for (uint32_t i = 0; i < left; ++i) {
-        const uint32_t c = 2 * i + group, col = t.col0 + 32 * c;
-        float v[32];
-        cpt::tmem_load32<0>(v, tmem + (lanes << 16) + b * kBuffer + 32 * c);
-        cpt::tmem_load_wait(v);
-        if (i + 1 == left) {                   // the buffer is read: the tensor core may have it back
-          cpt::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) cpt::mbar_arrive_cluster(pair_acc_empty + 8 * b);
-        }
+      };
+      auto finish = [&](uint32_t i, float(&v)[32]) {
+        const uint32_t col = t.col0 + 32 * (2 * i + group);
         if (raw) {
           if (row0 + lane < q.e.m)
             cpe::store32(q.part,
@@ -312,11 +330,54 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
         } else {
           cpe::finish_block<kRich>(q.e, key, row0, col, lane, bias[warp][i], v);
         }
+      };
+      if constexpr (kSegments) {
+        float acc[128];
+#pragma unroll
+        for (uint32_t i = 0; i < 128; ++i) acc[i] = 0.0f;
+        for (uint32_t kb = t.kb0; kb < t.kb1; kb += kSegment, ++it) {
+          const uint32_t b = it & 1;
+          ok = cpt::mbar_wait(acc_full + 8 * b, (it >> 1) & 1, &gave_up);
+          if (!ok) break;
+          cpt::tc_fence_after();
+#pragma unroll
+          for (uint32_t i = 0; i < 4; ++i) {
+            if (i < left) {
+              float v[32];
+              cpt::tmem_load32<0>(v, tmem_warp + b * kBuffer + 64 * i);
+              cpt::tmem_load_wait(v);
+#pragma unroll
+              for (uint32_t j = 0; j < 32; ++j) acc[32 * i + j] += v[j];
+            }
+          }
+          give_back(b);
+        }
+        if (!ok) break;
+        for (uint32_t i = 0; i < left; ++i) {
+          float v[32];
+#pragma unroll
+          for (uint32_t j = 0; j < 32; ++j) v[j] = acc[j];
+#pragma unroll
+          for (uint32_t j = 0; j < 96; ++j) acc[j] = acc[j + 32];
+          finish(i, v);
+        }
+      } else {
+        const uint32_t b = it & 1;
+        ok = cpt::mbar_wait(acc_full + 8 * b, (it >> 1) & 1, &gave_up);
+        if (!ok) break;
+        cpt::tc_fence_after();
+        ++it;
+        if (left == 0) give_back(b);
+        for (uint32_t i = 0; i < left; ++i) {
+          float v[32];
+          cpt::tmem_load32<0>(v, tmem_warp + b * kBuffer + 64 * i);
+          cpt::tmem_load_wait(v);
+          if (i + 1 == left) give_back(b);
+          finish(i, v);
+        }
       }
     }
     if (!ok && lane == 0) atomicOr(&g_linear_gave_up, 1u);
-    end_role();
-  } else {
     end_role();
   }
   __syncwarp();
@@ -389,9 +450,9 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     thin_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                 const __grid_constant__ ThinParams p) {
   constexpr uint32_t kStage = kTileA + kN * 128;
-  constexpr uint32_t kColumns = kN < 32 ? 32 : kN;
+  constexpr uint32_t kColumns = 2 * kN;              // of tensor memory: two buffers
   extern __shared__ uint8_t dyn[];
-  __shared__ __align__(8) uint64_t bars[2 * kThinMaxStages + 2];
+  __shared__ __align__(8) uint64_t bars[2 * kThinMaxStages + 5];
   __shared__ uint32_t tmem_base;
   __shared__ int gave_up;
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) &
@@ -402,13 +463,17 @@ __global__ void __launch_bounds__(kThinThreads, 2)
   const uint32_t row0 = tile / p.tiles_m * 128;
   const uint32_t token0 = tile % p.tiles_m * kN, tokens = min(p.e.m - token0, kN);
   const uint32_t full = cpt::smem_addr(bars), empty = full + 8 * kThinMaxStages;
-  const uint32_t acc_full = empty + 8 * kThinMaxStages, drained = acc_full + 8;
+  const uint32_t acc_full = empty + 8 * kThinMaxStages, acc_empty = acc_full + 16;
+  const uint32_t drained = acc_empty + 16;
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < p.stages; ++s) {
       cpt::mbar_init(full + 8 * s, 1);
       cpt::mbar_init(empty + 8 * s, 1);
     }
-    cpt::mbar_init(acc_full, 1);
+    for (uint32_t b = 0; b < 2; ++b) {
+      cpt::mbar_init(acc_full + 8 * b, 1);
+      cpt::mbar_init(acc_empty + 8 * b, 4);
+    }
     cpt::mbar_init(drained, 1);
     cpt::mbar_init_fence();
     gave_up = 0;
@@ -437,30 +502,31 @@ __global__ void __launch_bounds__(kThinThreads, 2)
 
   if (warp == 4) {
     // ------------------------------------------------------------------ loads
+    uint32_t fills = 0;
     if (cpt::elect_one()) {
       cpt::tma_prefetch_map(&map_a);
       cpt::tma_prefetch_map(&map_b);
-    }
-    __syncwarp();
-    uint32_t s = 0, round = 0, fills = 0;
-    for (uint32_t kb = kb0; kb < kb1; ++kb) {
-      if (round > 0) {
-        ok = cpt::mbar_wait(empty + 8 * s, (round - 1) & 1, &gave_up);
-        if (!ok) break;
-      }
-      const uint32_t dst = cpt::smem_addr(tiles) + s * kStage;
-      if (cpt::elect_one()) {
+      uint32_t s = 0, round = 0;
+      for (uint32_t kb = kb0; kb < kb1; ++kb) {
+        if (round > 0) {
+          ok = cpt::mbar_wait_one(empty + 8 * s, (round - 1) & 1, &gave_up);
+          if (!ok) break;
+        }
+        const uint32_t dst = cpt::smem_addr(tiles) + s * kStage;
         cpt::mbar_expect(full + 8 * s, kStage);
         cpt::tma_load(dst, &map_b, kb * kStageK, row0, full + 8 * s);
         cpt::tma_load(dst + kTileA, &map_a, kb * kStageK, token0, full + 8 * s);
+        ++fills;
+        if (++s == p.stages) {
+          s = 0;
+          ++round;
+        }
       }
-      __syncwarp();
-      ++fills;
-      if (++s == p.stages) {
-        s = 0;
-        ++round;
-      }
+      if (!ok) atomicOr(&g_linear_gave_up, 1u);
     }
+    __syncwarp();
+    fills = __reduce_max_sync(0xFFFFFFFFu, fills);       // the one issuer's
+    ok = true;
     end_role();
     if (gave_up != 0) {
       int late = 0;
@@ -471,26 +537,36 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     }
   } else if (warp == 5) {
     // --------------------------------------------------------------- products
-    uint32_t s = 0, round = 0;
-    for (uint32_t kb = kb0; kb < kb1; ++kb) {
-      ok = cpt::mbar_wait(full + 8 * s, round & 1, &gave_up);
-      if (!ok) break;
-      cpt::tc_fence_after();
-      const uint32_t at = cpt::smem_addr(tiles) + s * kStage;
-      const uint64_t db = cpt::operand_desc(at), da = cpt::operand_desc(at + kTileA);
-      if (cpt::elect_one()) {
+    if (cpt::elect_one()) {
+      uint32_t s = 0, round = 0, it = 0;
+      for (uint32_t kb = kb0; kb < kb1 && ok; ++it) {
+        const uint32_t b = it & 1, end = min(kb + kSegment, kb1);
+        ok = it < 2 || cpt::mbar_wait_one(acc_empty + 8 * b, ((it >> 1) - 1) & 1, &gave_up);
+        if (!ok) break;
+        uint32_t more = 0;
+        for (; kb < end; ++kb) {
+          ok = cpt::mbar_wait_one(full + 8 * s, round & 1, &gave_up);
+          if (!ok) break;
+          cpt::tc_fence_after();
+          const uint32_t at = cpt::smem_addr(tiles) + s * kStage;
+          const uint64_t db = cpt::operand_desc(at), da = cpt::operand_desc(at + kTileA);
+          cpt::mma_half_one(tmem + b * kN, db, da, p.instr, more);
 #pragma unroll
-        for (uint32_t k = 0; k < 4; ++k)
-          cpt::mma_half_one(tmem, db + 2 * k, da + 2 * k, p.instr, kb != kb0 || k != 0);
-        cpt::mma_commit(empty + 8 * s);
-        if (kb + 1 == kb1) cpt::mma_commit(acc_full);
+          for (uint32_t k = 1; k < 4; ++k)
+            cpt::mma_half_one(tmem + b * kN, db + 2 * k, da + 2 * k, p.instr, 1);
+          more = 1;
+          cpt::mma_commit(empty + 8 * s);
+          if (++s == p.stages) {
+            s = 0;
+            ++round;
+          }
+        }
+        if (ok) cpt::mma_commit(acc_full + 8 * b);
       }
-      __syncwarp();
-      if (++s == p.stages) {
-        s = 0;
-        ++round;
-      }
+      if (!ok) atomicOr(&g_linear_gave_up, 1u);
     }
+    __syncwarp();
+    ok = true;
     end_role();
     if (gave_up != 0) {
       int late = 0;
@@ -500,10 +576,16 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     }
   } else if (warp < 4) {
     // ------------------------------------------------------------------- sums
-    ok = cpt::mbar_wait(acc_full, 0, &gave_up);
-    if (ok) {                            // (all products are done: the stages are free)
+    float acc[kN];
+#pragma unroll
+    for (uint32_t i = 0; i < kN; ++i) acc[i] = 0.0f;
+    uint32_t it = 0;
+    for (uint32_t kb = kb0; kb < kb1; kb += kSegment, ++it) {
+      const uint32_t b = it & 1;
+      ok = cpt::mbar_wait(acc_full + 8 * b, (it >> 1) & 1, &gave_up);
+      if (!ok) break;
       cpt::tc_fence_after();
-      const uint32_t at = tmem + ((warp * 32) << 16);
+      const uint32_t at = tmem + ((warp * 32) << 16) + b * kN;
 #pragma unroll
       for (uint32_t c = 0; c < (kN + 31) / 32; ++c) {
         float x[32] = {};
@@ -511,9 +593,15 @@ __global__ void __launch_bounds__(kThinThreads, 2)
         else cpt::tmem_load32<0>(x, at + 32 * c);
         cpt::tmem_load_wait(x);
 #pragma unroll
-        for (uint32_t i = 0; i < (kN < 32 ? kN : 32); ++i)
-          part[(32 * c + i) * 128 + threadIdx.x] = x[i];
+        for (uint32_t i = 0; i < (kN < 32 ? kN : 32); ++i) acc[32 * c + i] += x[i];
       }
+      cpt::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) cpt::mbar_arrive(acc_empty + 8 * b);
+    }
+    if (ok) {                            // (all products are done: the stages are free)
+#pragma unroll
+      for (uint32_t i = 0; i < kN; ++i) part[i * 128 + threadIdx.x] = acc[i];
     }
     end_role();
   } else {
@@ -555,6 +643,11 @@ __global__ void __launch_bounds__(kThinThreads, 2)
 
 // ---------------------------------------------------------------------------- host
 
+using PairKernel = void (*)(PairParams);
+constexpr PairKernel kPairKernels[4] = {      // 1: rich, 2: segments
+    &pairs_kernel<false, false>, &pairs_kernel<true, false>, &pairs_kernel<false, true>,
+    &pairs_kernel<true, true>};
+
 // What a launch needs to know of the device, found once.
 struct Device {
   std::atomic<int> state{0};           // 1: found
@@ -593,8 +686,14 @@ const Device* device(cudaError_t* err) {
       *err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   static_cast<int>(bytes));
   };
-  allow(reinterpret_cast<const void*>(&pairs_kernel<false>), kSmemMost);
-  allow(reinterpret_cast<const void*>(&pairs_kernel<true>), kSmemMost);
+  for (int i = 0; i < 4; ++i) {
+    allow(reinterpret_cast<const void*>(kPairKernels[i]), kSmemMost);
+    cudaFuncAttributes attrs{};
+    if (*err == cudaSuccess)
+      *err = cudaFuncGetAttributes(&attrs, reinterpret_cast<const void*>(kPairKernels[i]));
+    if (*err == cudaSuccess && i >= 2 && attrs.numRegs != kLaunchRegs)
+      *err = cudaErrorInvalidConfiguration;
+  }
   allow(reinterpret_cast<const void*>(&thin_kernel<16>), kThinSmem);
   allow(reinterpret_cast<const void*>(&thin_kernel<32>), kThinSmem);
   allow(reinterpret_cast<const void*>(&thin_kernel<64>), kThinSmem);
@@ -611,7 +710,7 @@ const Device* device(cudaError_t* err) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int most = 0;
-  *err = cudaOccupancyMaxActiveClusters(&most, reinterpret_cast<const void*>(&pairs_kernel<true>),
+  *err = cudaOccupancyMaxActiveClusters(&most, reinterpret_cast<const void*>(kPairKernels[3]),
                                         &cfg);
   if (*err == cudaSuccess && most < 1) *err = cudaErrorInvalidConfiguration;
   if (*err != cudaSuccess) return nullptr;
@@ -692,7 +791,7 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
   if (d == nullptr) return cpx::cuda_fail(e, "linear device query");
   PairParams p{};
   FinishParams f{};
-  bool is_rich = false, finish = false;
+  bool is_rich = false, segments = false, finish = false;
   uint64_t units[kMostProducts] = {};
   int used = 0;
   for (int i = 0; i < count; ++i) {
@@ -724,6 +823,7 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
     x.b_boxes = x.b_across ? (t.bn / 2 + 63) / 64 : 1;
     x.b_bytes = x.b_across ? x.b_boxes * kBlock : t.bn / 2 * 128;
     x.instr = cpt::half_instr_desc(256, t.bn, q[i].dtype == CP_BF16, x.a_across, x.b_across);
+    segments |= ep.out_dtype == CP_F32 && (x.kblocks + t.splits - 1) / t.splits > kSegment;
     if (t.splits > 1) {
       x.pitch = part_pitch(ep.n);
       x.part = part;
@@ -764,7 +864,7 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
     if (sums.out != nullptr) pairs = max(pairs, (sums.n + 127) / 128);
     pairs = min(pairs, static_cast<uint32_t>(d->pairs));
     const Launch l{dim3(2 * pairs), kThreads, kSmemMost, s, 2};
-    e = is_rich ? launch(l, &pairs_kernel<true>, p) : launch(l, &pairs_kernel<false>, p);
+    e = launch(l, kPairKernels[(is_rich ? 1 : 0) + (segments ? 2 : 0)], p);
     if (e != cudaSuccess) return cpx::cuda_fail(e, "linear launch");
   }
   if (finish) {

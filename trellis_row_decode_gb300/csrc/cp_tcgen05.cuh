@@ -124,6 +124,22 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// The same for one thread of a warp that issues alone.
+__device__ __forceinline__ bool mbar_wait_one(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try(bar, parity)) return true;
+    if ((i & 1023) == 0) {
+      const uint64_t t = global_ns();
+      if (t0 == 0) t0 = t;
+      if (*gave_up != 0 || t - t0 > kWaitNs) {
+        *gave_up = 1;
+        return false;
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------------- TMA
 
 // A 2-D tile into shared memory; its bytes count on `bar`, which may be the barrier of
