@@ -30,60 +30,76 @@ struct DropoutParams {
   void* out;
   uint64_t ldx, ldr, ldo, rows;
   uint32_t d, octets;                      // octets of a row
+  uint32_t step_rows, step_octets;         // what one step of the grid comes to
   cpe::DropParams drop;
 };
 
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool kResidual>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p) {
   wait_for_previous();
   let_next_start();
   const DropKey key = cpe::drop_key(p.drop);
-  const uint64_t units = p.rows * p.octets, step = static_cast<uint64_t>(gridDim.x) * kThreads;
-  for (uint64_t u0 = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x; u0 < units;
-       u0 += kAhead * step) {
+  const cpe::RoundKeys keys = cpe::round_keys(key);
+  // (row, octet) moves on by the grid's step without a division
+  const uint64_t first = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  uint64_t row = first / p.octets;
+  uint32_t o = static_cast<uint32_t>(first - row * p.octets);
+  while (row < p.rows) {
     Packed<T> x[kAhead], r[kAhead];
-    uint64_t row[kAhead];
-    uint32_t o[kAhead];
+    uint64_t at[kAhead];
+    uint32_t col[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const uint64_t u = u0 + i * step;
-      row[i] = u / p.octets;
-      o[i] = static_cast<uint32_t>(u - row[i] * p.octets);
-      if (u < units) {
-        x[i] = load_row_octet<T, VEC>(static_cast<const T*>(p.x) + row[i] * p.ldx, o[i], p.d);
-        if (p.residual != nullptr)
-          r[i] = load_row_octet<T, VEC>(static_cast<const T*>(p.residual) + row[i] * p.ldr, o[i],
-                                        p.d);
+      at[i] = row;
+      col[i] = o;
+      if (row < p.rows) {
+        x[i] = load_row_octet<T, VEC>(static_cast<const T*>(p.x) + row * p.ldx, o, p.d);
+        if constexpr (kResidual)
+          r[i] = load_row_octet<T, VEC>(static_cast<const T*>(p.residual) + row * p.ldr, o, p.d);
+      }
+      o += p.step_octets;
+      row += p.step_rows;
+      if (o >= p.octets) {
+        o -= p.octets;
+        ++row;
       }
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      if (u0 + i * step < units) {
+      if (at[i] < p.rows) {
         float v[8];
         unpack(x[i], v);
         if (p.drop.mode != 0) {
-          const uint32_t line = static_cast<uint32_t>(row[i]);
-          cpe::drop_quad(p.drop, key, 2 * o[i], line, v);
-          cpe::drop_quad(p.drop, key, 2 * o[i] + 1, line, v + 4);
+          const uint32_t line = static_cast<uint32_t>(at[i]);
+          cpe::drop_quad(p.drop, key, keys, 2 * col[i], line, v);
+          cpe::drop_quad(p.drop, key, keys, 2 * col[i] + 1, line, v + 4);
         }
-        if (p.residual != nullptr) {
+        if constexpr (kResidual) {
           float w[8];
           unpack(r[i], w);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] += w[e];
         }
-        store_row_octet<T, VEC>(static_cast<T*>(p.out) + row[i] * p.ldo, o[i], p.d, pack<T>(v));
+        store_row_octet<T, VEC>(static_cast<T*>(p.out) + at[i] * p.ldo, col[i], p.d, pack<T>(v));
       }
     }
   }
 }
 
 template <typename T>
-cudaError_t launch_dropout(const DropoutParams& p, bool vec, cudaStream_t s) {
+cudaError_t launch_dropout(DropoutParams p, bool vec, cudaStream_t s) {
+  // (rows and octets of a row lie below 2^32 and 2^29: the product does not wrap)
   const uint64_t units = p.rows * p.octets;
   const uint64_t ctas = std::min((units + kThreads - 1) / kThreads, kMostCtas);
+  const uint64_t step = ctas * kThreads;
+  p.step_rows = static_cast<uint32_t>(step / p.octets);
+  p.step_octets = static_cast<uint32_t>(step % p.octets);
   const Launch l{dim3(static_cast<unsigned>(ctas)), kThreads, 0, s};
-  return vec ? launch(l, &dropout_kernel<T, true>, p) : launch(l, &dropout_kernel<T, false>, p);
+  if (p.residual != nullptr)
+    return vec ? launch(l, &dropout_kernel<T, true, true>, p)
+               : launch(l, &dropout_kernel<T, false, true>, p);
+  return vec ? launch(l, &dropout_kernel<T, true, false>, p)
+             : launch(l, &dropout_kernel<T, false, false>, p);
 }
 
 }  // namespace

@@ -43,35 +43,53 @@ __device__ __forceinline__ DropKey drop_key(const DropParams& p) {
                  static_cast<uint32_t>(offset), static_cast<uint32_t>(offset >> 32)};
 }
 
-__device__ __forceinline__ uint4 philox(uint32_t quad, uint32_t row, const DropKey& key) {
-  uint32_t c0 = quad, c1 = row, c2 = key.o0, c3 = key.o1, k0 = key.k0, k1 = key.k1;
+// The key of each round, for kernels that make many calls and have the registers.
+struct RoundKeys {
+  uint32_t k0[10], k1[10];
+};
+__device__ __forceinline__ RoundKeys round_keys(const DropKey& key) {
+  RoundKeys r;
+#pragma unroll
+  for (uint32_t i = 0; i < 10; ++i) {
+    r.k0[i] = key.k0 + i * 0x9E3779B9u;
+    r.k1[i] = key.k1 + i * 0xBB67AE85u;
+  }
+  return r;
+}
+
+__device__ __forceinline__ uint4 philox(uint32_t quad, uint32_t row, const DropKey& key,
+                                        const RoundKeys& k) {
+  uint32_t c0 = quad, c1 = row, c2 = key.o0, c3 = key.o1;
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t a = static_cast<uint64_t>(c0) * 0xD2511F53u;
     const uint64_t b = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
-    c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
+    c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k.k0[r];
     c1 = static_cast<uint32_t>(b);
-    c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
+    c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k.k1[r];
     c3 = static_cast<uint32_t>(a);
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
   }
   return make_uint4(c0, c1, c2, c3);
 }
 
 // Four columns of a row, 4 * quad on.  A dropped element is zero whatever it was.
-__device__ __forceinline__ void drop_quad(const DropParams& p, const DropKey& key, uint32_t quad,
-                                          uint32_t row, float* v) {
+__device__ __forceinline__ void drop_quad(const DropParams& p, const DropKey& key,
+                                          const RoundKeys& k, uint32_t quad, uint32_t row,
+                                          float* v) {
   if (p.mode == 2) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = 0.0f;
     return;
   }
-  const uint4 w = philox(quad, row, key);
+  const uint4 w = philox(quad, row, key, k);
   v[0] = w.x <= p.last ? v[0] * p.scale : 0.0f;
   v[1] = w.y <= p.last ? v[1] * p.scale : 0.0f;
   v[2] = w.z <= p.last ? v[2] * p.scale : 0.0f;
   v[3] = w.w <= p.last ? v[3] * p.scale : 0.0f;
+}
+__device__ __forceinline__ void drop_quad(const DropParams& p, const DropKey& key, uint32_t quad,
+                                          uint32_t row, float* v) {
+  drop_quad(p, key, round_keys(key), quad, row, v);
 }
 
 // What a call's p, seed and offset say; false where p is no probability.

@@ -413,7 +413,8 @@ __global__ void __launch_bounds__(kFinishThreads)
        u += step) {
     const FinishProduct& q = p.q[u < p.first ? 0 : 1];
     const uint64_t at = u < p.first ? u : u - p.first;
-    const uint32_t row = static_cast<uint32_t>(at / q.quads);
+    const uint32_t row = (at >> 32) == 0 ? static_cast<uint32_t>(at) / q.quads
+                                         : static_cast<uint32_t>(at / q.quads);
     const uint32_t col = static_cast<uint32_t>(at - static_cast<uint64_t>(row) * q.quads) * 4;
     float v[4] = {};
 #pragma unroll 4
