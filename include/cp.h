@@ -536,7 +536,7 @@ enum { CP_ACT_NONE = 0, CP_ACT_RELU = 1, CP_ACT_SILU = 2, CP_ACT_GELU = 3, CP_AC
  *   x, residual   [rows][d] of dtype with row strides >= d, or 0 (one row for all).  residual may
  *            be NULL.
  *   out      [rows][d] of dtype, row stride >= d; it may be x or residual (same stride).
- * rows < 2^32, d < 2^32.
+ * rows < 2^31.
  */
 cp_status cp_dropout(const void* x, uint64_t x_stride, const void* residual,
                      uint64_t residual_stride, int dtype, uint64_t rows, uint32_t d, double p,

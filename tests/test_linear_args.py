@@ -47,7 +47,7 @@ def test_dropout_arguments(L, p):
         return L.cp_dropout(a["x"], a["xs"], a["r"], a["rs"], a["t"], a["m"], a["d"], a["p"],
                             a["seed"], a["off"], a["rng"], a["o"], a["os"], None)
     for kw in [dict(t=3), dict(t=-1), dict(xs=7), dict(os=7), dict(os=0), dict(r=p, rs=7),
-               dict(m=1 << 32), dict(p=-0.1), dict(p=1.1), dict(p=float("nan")), dict(rng=p + 4),
+               dict(m=1 << 31), dict(p=-0.1), dict(p=1.1), dict(p=float("nan")), dict(rng=p + 4),
                dict(x=None), dict(o=None), dict(x=p + 2), dict(o=p + 2), dict(r=p + 1, rs=8),
                dict(t=2, x=p + 1)]:
         assert call(**kw) == BAD, kw

@@ -7,6 +7,7 @@
 // written).
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_runtime.h>
 
@@ -22,40 +23,81 @@ using cpe::DropKey;
 
 constexpr int kThreads = 256;
 constexpr int kAhead = 2;                  // octets whose loads a thread has in flight
-constexpr uint64_t kMostCtas = 152 * 8;
+constexpr uint32_t kPer = 8;               // octets of a thread: CTAs short enough to even out
+template <typename T, bool kResidual>      // CTAs of an SM, by registers
+constexpr int kCtas = sizeof(T) == 4 ? 4 : kResidual ? 5 : 6;
+
+// x * scale of two elements, by one instruction; and an octet's bits widened by byte moves: the
+// generator's products fill the pipe that multiplications and shifts by multiplication share.
+__device__ __forceinline__ void scale_pair(float& a, float& b, float scale) {
+  asm("{\n"
+      ".reg .b64 v, s;\n"
+      "mov.b64 v, {%0, %1};\n"
+      "mov.b64 s, {%2, %2};\n"
+      "mul.rn.f32x2 v, v, s;\n"
+      "mov.b64 {%0, %1}, v;\n"
+      "}\n"
+      : "+f"(a), "+f"(b)
+      : "f"(scale));
+}
+template <typename T>
+__device__ __forceinline__ void widen(const Packed<T>& r, float (&v)[8]) {
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(__byte_perm(r.w[i], 0, 0x1044));
+      v[2 * i + 1] = __uint_as_float(__byte_perm(r.w[i], 0, 0x3244));
+    }
+  } else {
+    unpack(r, v);
+  }
+}
 
 struct DropoutParams {
   const void* x;
   const void* residual;
   void* out;
-  uint64_t ldx, ldr, ldo, rows;
-  uint32_t d, octets;                      // octets of a row
-  uint32_t step_rows, step_octets;         // what one step of the grid comes to
+  uint64_t ldx, ldr, ldo;                  // flat: all d, d a multiple of 8
+  uint32_t rows, d, octets;                // octets of a row
+  uint32_t step_rows, step_octets;         // what kThreads octets come to
   cpe::DropParams drop;
 };
 
-template <typename T, bool VEC, bool kResidual>
-__global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p) {
+// How rows lie: one behind the other in whole octets; apart, in whole octets; anywhere.  The first
+// needs no position of a row (a product of 64 bits each, on the generator's pipe).
+enum { kFlat, kRows, kAny };
+
+template <typename T, int kLayout, bool kResidual>
+__global__ void __launch_bounds__(kThreads, (kCtas<T, kResidual>))
+    dropout_kernel(const __grid_constant__ DropoutParams p) {
+  constexpr bool VEC = kLayout != kAny;
   wait_for_previous();
   let_next_start();
   const DropKey key = cpe::drop_key(p.drop);
   const cpe::RoundKeys keys = cpe::round_keys(key);
-  // (row, octet) moves on by the grid's step without a division
-  const uint64_t first = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  uint64_t row = first / p.octets;
-  uint32_t o = static_cast<uint32_t>(first - row * p.octets);
-  while (row < p.rows) {
+  const uint64_t first = static_cast<uint64_t>(blockIdx.x) * (kThreads * kPer) + threadIdx.x;
+  uint32_t row = static_cast<uint32_t>(first / p.octets);
+  uint32_t o = static_cast<uint32_t>(first - static_cast<uint64_t>(row) * p.octets);
+  const T* px = static_cast<const T*>(p.x) + 8 * first;          // (of kFlat)
+  const T* pr = static_cast<const T*>(p.residual) + 8 * first;
+  T* po = static_cast<T*>(p.out) + 8 * first;
+#pragma unroll 1
+  for (uint32_t n = 0; n < kPer && row < p.rows; n += kAhead) {
     Packed<T> x[kAhead], r[kAhead];
-    uint64_t at[kAhead];
-    uint32_t col[kAhead];
+    uint32_t at[kAhead], col[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       at[i] = row;
       col[i] = o;
       if (row < p.rows) {
-        x[i] = load_row_octet<T, VEC>(static_cast<const T*>(p.x) + row * p.ldx, o, p.d);
-        if constexpr (kResidual)
-          r[i] = load_row_octet<T, VEC>(static_cast<const T*>(p.residual) + row * p.ldr, o, p.d);
+        if constexpr (kLayout == kFlat) {
+          x[i] = load_octet(px + 8 * kThreads * i);
+          if constexpr (kResidual) r[i] = load_octet(pr + 8 * kThreads * i);
+        } else {
+          x[i] = load_row_octet<T, VEC>(static_cast<const T*>(p.x) + row * p.ldx, o, p.d);
+          if constexpr (kResidual)
+            r[i] = load_row_octet<T, VEC>(static_cast<const T*>(p.residual) + row * p.ldr, o, p.d);
+        }
       }
       o += p.step_octets;
       row += p.step_rows;
@@ -68,38 +110,53 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p
     for (int i = 0; i < kAhead; ++i) {
       if (at[i] < p.rows) {
         float v[8];
-        unpack(x[i], v);
-        if (p.drop.mode != 0) {
-          const uint32_t line = static_cast<uint32_t>(at[i]);
-          cpe::drop_quad(p.drop, key, keys, 2 * col[i], line, v);
-          cpe::drop_quad(p.drop, key, keys, 2 * col[i] + 1, line, v + 4);
+        widen(x[i], v);
+        if (p.drop.mode == 1) {
+#pragma unroll
+          for (uint32_t h = 0; h < 2; ++h) {
+            const uint4 w = cpe::philox(2 * col[i] + h, at[i], key, keys);
+            float* u = v + 4 * h;
+            scale_pair(u[0], u[1], p.drop.scale);
+            scale_pair(u[2], u[3], p.drop.scale);
+            u[0] = w.x <= p.drop.last ? u[0] : 0.0f;
+            u[1] = w.y <= p.drop.last ? u[1] : 0.0f;
+            u[2] = w.z <= p.drop.last ? u[2] : 0.0f;
+            u[3] = w.w <= p.drop.last ? u[3] : 0.0f;
+          }
+        } else if (p.drop.mode == 2) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = 0.0f;
         }
         if constexpr (kResidual) {
           float w[8];
-          unpack(r[i], w);
+          widen(r[i], w);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] += w[e];
         }
-        store_row_octet<T, VEC>(static_cast<T*>(p.out) + at[i] * p.ldo, col[i], p.d, pack<T>(v));
+        if constexpr (kLayout == kFlat)
+          store_octet(po + 8 * kThreads * i, pack<T>(v));
+        else
+          store_row_octet<T, VEC>(static_cast<T*>(p.out) + at[i] * p.ldo, col[i], p.d, pack<T>(v));
       }
     }
+    px += 8 * kThreads * kAhead;
+    pr += 8 * kThreads * kAhead;
+    po += 8 * kThreads * kAhead;
   }
 }
 
-template <typename T>
-cudaError_t launch_dropout(DropoutParams p, bool vec, cudaStream_t s) {
-  // (rows and octets of a row lie below 2^32 and 2^29: the product does not wrap)
-  const uint64_t units = p.rows * p.octets;
-  const uint64_t ctas = std::min((units + kThreads - 1) / kThreads, kMostCtas);
-  const uint64_t step = ctas * kThreads;
-  p.step_rows = static_cast<uint32_t>(step / p.octets);
-  p.step_octets = static_cast<uint32_t>(step % p.octets);
+template <typename T, bool kResidual>
+cudaError_t launch_dropout(DropoutParams p, bool vec, uint64_t ctas, cudaStream_t s) {
   const Launch l{dim3(static_cast<unsigned>(ctas)), kThreads, 0, s};
-  if (p.residual != nullptr)
-    return vec ? launch(l, &dropout_kernel<T, true, true>, p)
-               : launch(l, &dropout_kernel<T, false, true>, p);
-  return vec ? launch(l, &dropout_kernel<T, true, false>, p)
-             : launch(l, &dropout_kernel<T, false, false>, p);
+  const bool flat = vec && p.ldx == p.d && p.ldo == p.d && (!kResidual || p.ldr == p.d);
+  return flat  ? launch(l, &dropout_kernel<T, kFlat, kResidual>, p)
+         : vec ? launch(l, &dropout_kernel<T, kRows, kResidual>, p)
+               : launch(l, &dropout_kernel<T, kAny, kResidual>, p);
+}
+template <typename T>
+cudaError_t launch_dropout(const DropoutParams& p, bool vec, uint64_t ctas, cudaStream_t s) {
+  return p.residual != nullptr ? launch_dropout<T, true>(p, vec, ctas, s)
+                               : launch_dropout<T, false>(p, vec, ctas, s);
 }
 
 }  // namespace
@@ -109,7 +166,7 @@ extern "C" cp_status cp_dropout(const void* x, uint64_t x_stride, const void* re
                                 double p, uint64_t seed, uint64_t offset, const uint64_t* rng,
                                 void* out, uint64_t out_stride, void* stream) {
   DropoutParams q{};
-  if (!dtype_ok(dtype) || rows >= (1ull << 32) || (x_stride < d && x_stride != 0) ||
+  if (!dtype_ok(dtype) || rows >= (1ull << 31) || (x_stride < d && x_stride != 0) ||
       (residual != nullptr && residual_stride < d && residual_stride != 0) || out_stride < d) {
     cpx::set_error("bad dtype, rows or row stride");
     return CP_ERR_INVALID_ARG;
@@ -131,15 +188,22 @@ extern "C" cp_status cp_dropout(const void* x, uint64_t x_stride, const void* re
   q.ldx = x_stride;
   q.ldr = residual_stride;
   q.ldo = out_stride;
-  q.rows = rows;
+  q.rows = static_cast<uint32_t>(rows);
   q.d = d;
   q.octets = static_cast<uint32_t>((static_cast<uint64_t>(d) + 7) / 8);
   const bool vec = octets_ok(x, x_stride, d, elt) && octets_ok(out, out_stride, d, elt) &&
                    (residual == nullptr || octets_ok(residual, residual_stride, d, elt));
+  q.step_rows = kThreads / q.octets;
+  q.step_octets = kThreads % q.octets;
+  const uint64_t units = rows * q.octets, ctas = (units + kThreads * kPer - 1) / (kThreads * kPer);
+  if (ctas >= (1ull << 31)) {
+    cpx::set_error("rows of d make more than 2^42 octets");
+    return CP_ERR_INVALID_ARG;
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == CP_F32   ? launch_dropout<float>(q, vec, s)
-                        : dtype == CP_F16 ? launch_dropout<__half>(q, vec, s)
-                                          : launch_dropout<__nv_bfloat16>(q, vec, s);
+  const cudaError_t e = dtype == CP_F32   ? launch_dropout<float>(q, vec, ctas, s)
+                        : dtype == CP_F16 ? launch_dropout<__half>(q, vec, ctas, s)
+                                          : launch_dropout<__nv_bfloat16>(q, vec, ctas, s);
   if (e != cudaSuccess) return cpx::cuda_fail(e, "dropout launch");
   return CP_OK;
 }
