@@ -34,16 +34,17 @@ __device__ uint32_t g_linear_gave_up;
 // its 128 rows of a and its half of the bn rows of b, 64 of k a stage.  An operand that is stored
 // along k comes as rows of 128 bytes; one that is stored across k (the gradient's: dz and x for dw,
 // w for dx) as blocks of 64 by 64 that the tensor core transposes as it reads them, so neither
-// is ever transposed in memory.  Roles: a warp issues the TMA loads, a warp of the first CTA
-// the tcgen05.mma, eight warps per CTA finish the sums of one of two tensor-memory buffers while
-// the tensor core fills the other (a lane has a row, the warps of a half every other block of
-// 32 columns), two add up the column sums that the kernel before left in parts.  A CTA pair
+// is ever transposed in memory.  Roles: a thread each issues the TMA loads of a and of b, one of the
+// first CTA the tcgen05.mma, sixteen warps per CTA finish the sums of one of two tensor-memory
+// buffers while the tensor core fills the other (a lane has a row, four warps every fourth block of
+// 32 columns), one adds up the column sums that the kernel before left in parts.  A CTA pair
 // walks over its units: tiles of up to two products (dx and dw of one call), the k of each
 // shared by `splits` units where there are few; their sums go to a workspace, and finish_kernel adds
 // them in order.
 
-constexpr int kSumWarps = 8;
-constexpr int kThreads = (kSumWarps + 4) * 32;         // + the TMA warp, the MMA warp, two for columns
+constexpr int kSumWarps = 16;
+constexpr uint32_t kGroups = kSumWarps / 4;            // of four warps, one for each 32 lanes
+constexpr int kThreads = (kSumWarps + 4) * 32;         // + loads of a, products, loads of b, column sums
 constexpr uint32_t kStageK = 64;                       // of k in a stage: 128 bytes
 constexpr uint32_t kMaxStages = 8;
 constexpr uint32_t kTileA = 128 * 128;                 // bytes of a's rows per stage and CTA
@@ -51,10 +52,10 @@ constexpr uint32_t kBlock = 64 * 128;                  // bytes of a 64 x 64 blo
 constexpr uint32_t kSmemMost = 220 * 1024;             // dynamic shared memory of a CTA
 constexpr uint32_t kBuffer = 256;                      // columns of tensor memory of a buffer
 constexpr uint32_t kSegment = 8;                       // stages that the tensor core adds up alone
-// Registers with segments: launched with 168 a thread (65,536 over 12 warps); the finishing warps
-// (128 sums a thread) take what the other four give up.
-constexpr int kLaunchRegs = 168, kFinishRegs = 208, kOtherRegs = 88;
-static_assert(2 * kFinishRegs + kOtherRegs <= 3 * kLaunchRegs, "a warpgroup's share of the launch");
+// Registers with segments: launched with 96 a thread (65,536 over 20 warps); the finishing warps
+// (64 sums a thread) take what the other four give up.
+constexpr int kLaunchRegs = 96, kFinishRegs = 104, kOtherRegs = 64;
+static_assert(4 * kFinishRegs + kOtherRegs <= 5 * kLaunchRegs, "a warpgroup's share of the launch");
 constexpr uint32_t kRasterRows = 16;                   // tiles along m that are walked together
 
 struct PairProduct {
@@ -103,13 +104,13 @@ template <bool kRich, bool kSegments>
 __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constant__ PairParams p) {
   extern __shared__ uint8_t dyn[];
   __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5];
-  __shared__ __align__(16) float bias[kSumWarps][4][32];
+  __shared__ __align__(16) float bias[kSumWarps][2][32];
   __shared__ uint32_t tmem_base;
-  __shared__ uint32_t issued;              // this CTA's fills of stages
+  __shared__ uint32_t issued[2];           // this CTA's fills of stages, by either issuer
   __shared__ int gave_up;
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t warp = cpt::warp_index(), lane = threadIdx.x & 31;
   const uint32_t half = cpt::cluster_rank();
   const uint32_t full = cpt::smem_addr(bars), empty = full + 8 * kMaxStages;
   const uint32_t acc_full = empty + 8 * kMaxStages, acc_empty = acc_full + 16;
@@ -155,115 +156,101 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
 
   if (warp >= kSumWarps) {
     if constexpr (kSegments) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kSumWarps) {
+    if (warp == kSumWarps || warp == kSumWarps + 2) {
       // ---------------------------------------------------------------- loads
-      uint32_t fills = 0;
+      // (a warp for a, one for b; each runs its loop whole and elects a thread to issue)
+      const bool is_a = warp == kSumWarps;
       if (cpt::elect_one()) {
-        for (int i = 0; i < kMostProducts; ++i) {
-          cpt::tma_prefetch_map(&p.map_a[i]);
-          cpt::tma_prefetch_map(&p.map_b[i]);
-        }
-        const uint32_t stages = p.stages, stage_bytes = p.stage_bytes;
-        uint32_t s = 0, round = 0;
-        bool ok = true, ready = false;       // ready: the next stage is known to be free
-        for (uint32_t u = pair; u < p.units && ok; u += pairs) {
-          const Unit t = unit_of(p, u);
-          const PairProduct& q = p.q[t.which];
-          const CUtensorMap *map_a = &p.map_a[t.which], *map_b = &p.map_b[t.which];
-          const bool a_across = q.a_across != 0, b_across = q.b_across != 0;
-          const bool a1 = t.row0 + 128 < q.e.m;             // the second CTA has rows of a
-          const bool mine = half == 0 || a1;
-          const uint32_t b_boxes = q.b_boxes;
-          const uint32_t bytes = 2 * q.b_bytes + (a1 ? 2 : 1) * kTileA;
-          const uint32_t row = t.row0 + half * 128, col = t.col0 + half * (q.bn / 2);
-          for (uint32_t kb = t.kb0; kb < t.kb1; ++kb) {
-            if (!ready && round > 0) {
-              ok = cpt::mbar_wait_one(empty + 8 * s, (round - 1) & 1, &gave_up);
-              if (!ok) break;
-            }
-            const uint32_t dst = cpt::smem_addr(tiles) + s * stage_bytes, k0 = kb * kStageK;
-            const uint32_t bar = pair_full + 8 * s, mine_full = full + 8 * s;
-            if (++s == stages) {
-              s = 0;
-              ++round;
-            }
-            ready = round > 0 && cpt::mbar_try(empty + 8 * s, (round - 1) & 1);
-            if (half == 0) cpt::mbar_expect(mine_full, bytes);
-            if (mine) {
-              if (a_across) {
-                cpt::tma_load_pair(dst, map_a, row, k0, bar);
-                cpt::tma_load_pair(dst + kBlock, map_a, row + 64, k0, bar);
-              } else {
-                cpt::tma_load_pair(dst, map_a, k0, row, bar);
-              }
-            }
-            if (b_across) {
-              for (uint32_t i = 0; i < b_boxes; ++i)
-                cpt::tma_load_pair(dst + kTileA + i * kBlock, map_b, col + 64 * i, k0, bar);
-            } else {
-              cpt::tma_load_pair(dst + kTileA, map_b, k0, col, bar);
-            }
-            ++fills;
-          }
-        }
-        issued = fills;
+        for (int i = 0; i < kMostProducts; ++i)
+          cpt::tma_prefetch_map(is_a ? &p.map_a[i] : &p.map_b[i]);
       }
       __syncwarp();
-      fills = issued;
+      const uint32_t base = cpt::smem_addr(tiles) + (is_a ? 0 : kTileA);
+      uint32_t s = 0, parity = 1, fills = 0;     // (parity 1: a stage that was never filled is free)
+      bool ok = true;
+      for (uint32_t u = pair; u < p.units && ok; u += pairs) {
+        const Unit t = unit_of(p, u);
+        const PairProduct& q = p.q[t.which];
+        const CUtensorMap* map = is_a ? &p.map_a[t.which] : &p.map_b[t.which];
+        const bool a1 = t.row0 + 128 < q.e.m;             // the second CTA has rows of a
+        const bool across = (is_a ? q.a_across : q.b_across) != 0;
+        const uint32_t boxes = is_a ? (half == 0 || a1 ? (across ? 2 : 1) : 0) : q.b_boxes;
+        const uint32_t bytes = 2 * q.b_bytes + (a1 ? 2 : 1) * kTileA;
+        const uint32_t at = is_a ? t.row0 + half * 128 : t.col0 + half * (q.bn / 2);
+        const bool expect = is_a && half == 0;
+        for (uint32_t kb = t.kb0; kb < t.kb1; ++kb) {
+          ok = cpt::mbar_wait(empty + 8 * s, parity, &gave_up);
+          if (!ok) break;
+          const uint32_t dst = base + s * p.stage_bytes, k0 = kb * kStageK;
+          if (cpt::elect_one()) {
+            if (expect) cpt::mbar_expect(full + 8 * s, bytes);
+            if (across) {
+              for (uint32_t i = 0; i < boxes; ++i)
+                cpt::tma_load_pair(dst + i * kBlock, map, at + 64 * i, k0, pair_full + 8 * s);
+            } else if (boxes != 0) {
+              cpt::tma_load_pair(dst, map, k0, at, pair_full + 8 * s);
+            }
+          }
+          __syncwarp();
+          ++fills;
+          if (++s == p.stages) {
+            s = 0;
+            parity ^= 1;
+          }
+        }
+      }
+      if (lane == 0) issued[is_a ? 0 : 1] = fills;
       end_role();
-      if (gave_up != 0 && half == 0) {
-        const uint32_t other = cpt::load_cluster1(cpt::map_rank(cpt::smem_addr(&issued), 1));
+      if (gave_up != 0 && half == 0 && is_a) {
+        const uint32_t other = cpt::map_rank(cpt::smem_addr(issued), 1);
+        const uint32_t mine = max(issued[0], issued[1]);
+        const uint32_t theirs = max(cpt::load_cluster1(other), cpt::load_cluster1(other + 4));
         int late = 0;
         for (uint32_t k = 0; k < p.stages; ++k) {
-          const LastFill last = last_fill(fills, other, p.stages, k);
+          const LastFill last = last_fill(mine, theirs, p.stages, k);
           if (last.any) cpt::mbar_wait(full + 8 * k, last.parity, &late);
         }
       }
     } else if (warp == kSumWarps + 1 && half == 0) {
       // ------------------------------------------------------------- products
-      if (cpt::elect_one()) {
-        const uint32_t stages = p.stages, stage_bytes = p.stage_bytes;
-        uint32_t it = 0, s = 0, round = 0;
-        bool ok = true, ready = false;       // ready: the next stage is known to be full
-        for (uint32_t u = pair; u < p.units && ok; u += pairs) {
-          const Unit t = unit_of(p, u);
-          const PairProduct& q = p.q[t.which];
-          const uint32_t instr = q.instr;
-          const uint64_t a_step = q.a_across ? 128 : 2, b_step = q.b_across ? 128 : 2;
-          const uint64_t a_base = q.a_across ? cpt::operand_desc_mn(0) : cpt::operand_desc(0);
-          const uint64_t b_base = q.b_across ? cpt::operand_desc_mn(0) : cpt::operand_desc(0);
-          for (uint32_t kb = t.kb0; kb < t.kb1 && ok; ++it) {
-            const uint32_t b = it & 1, to = tmem + b * kBuffer;
-            const uint32_t end = kSegments ? min(kb + kSegment, t.kb1) : t.kb1;
-            ok = it < 2 || cpt::mbar_wait_one(acc_empty + 8 * b, ((it >> 1) - 1) & 1, &gave_up);
+      uint32_t it = 0, s = 0, parity = 0;
+      bool ok = true;
+      for (uint32_t u = pair; u < p.units && ok; u += pairs) {
+        const Unit t = unit_of(p, u);
+        const PairProduct& q = p.q[t.which];
+        const uint32_t instr = q.instr;
+        const uint32_t a_step = q.a_across ? 128 : 2, b_step = q.b_across ? 128 : 2;
+        const uint32_t a_low = cpt::desc_low(cpt::smem_addr(tiles), q.a_across != 0);
+        const uint32_t b_low = cpt::desc_low(cpt::smem_addr(tiles) + kTileA, q.b_across != 0);
+        for (uint32_t kb = t.kb0; kb < t.kb1 && ok; ++it) {
+          const uint32_t b = it & 1, to = tmem + b * kBuffer;
+          const uint32_t end = kSegments ? min(kb + kSegment, t.kb1) : t.kb1;
+          ok = it < 2 || cpt::mbar_wait(acc_empty + 8 * b, ((it >> 1) - 1) & 1, &gave_up);
+          if (!ok) break;
+          uint32_t more = 0;
+          for (; kb < end; ++kb) {
+            ok = cpt::mbar_wait(full + 8 * s, parity, &gave_up);
             if (!ok) break;
-            uint32_t more = 0;
-            for (; kb < end; ++kb) {
-              if (!ready) {
-                ok = cpt::mbar_wait_one(full + 8 * s, round & 1, &gave_up);
-                if (!ok) break;
-              }
-              cpt::tc_fence_after();
-              const uint32_t at = (cpt::smem_addr(tiles) + s * stage_bytes) >> 4;
-              const uint32_t free = empty + 8 * s;
-              if (++s == stages) {
-                s = 0;
-                ++round;
-              }
-              ready = cpt::mbar_try(full + 8 * s, round & 1);
-              const uint64_t da = a_base + at, db = b_base + (at + kTileA / 16);
-              cpt::mma_half_pair(to, da, db, instr, more);
+            cpt::tc_fence_after();
+            const uint32_t at = s * (p.stage_bytes >> 4);
+            if (cpt::elect_one()) {
+              cpt::mma_half_pair(to, cpt::desc_of(a_low + at), cpt::desc_of(b_low + at), instr, more);
 #pragma unroll
               for (uint32_t k = 1; k < 4; ++k)
-                cpt::mma_half_pair(to, da + k * a_step, db + k * b_step, instr, 1);
-              more = 1;
-              cpt::mma_commit_pair(free, 3);
+                cpt::mma_half_pair(to, cpt::desc_of(a_low + at + k * a_step),
+                                   cpt::desc_of(b_low + at + k * b_step), instr, 1);
+              cpt::mma_commit_pair(empty + 8 * s, 3);
+              if (kb + 1 == end) cpt::mma_commit_pair(acc_full + 8 * b, 3);
             }
-            if (ok) cpt::mma_commit_pair(acc_full + 8 * b, 3);
+            __syncwarp();
+            more = 1;
+            if (++s == p.stages) {
+              s = 0;
+              parity ^= 1;
+            }
           }
         }
       }
-      __syncwarp();
       end_role();
       if (gave_up != 0) {
         int late = 0;
@@ -271,11 +258,10 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
         __syncwarp();
         cpt::mbar_wait(drained, 0, &late);
       }
-    } else if (warp >= kSumWarps + 2) {
+    } else if (warp == kSumWarps + 3) {
       // ---------------------------------------------------------- column sums
       if (p.sums.out != nullptr) {
-        for (uint32_t c = (blockIdx.x * 2 + warp - kSumWarps - 2) * 32 + lane; c < p.sums.n;
-             c += gridDim.x * 64) {
+        for (uint32_t c = blockIdx.x * 32 + lane; c < p.sums.n; c += gridDim.x * 32) {
           float sum = 0.0f;
 #pragma unroll 8
           for (uint32_t i = 0; i < p.sums.count; ++i)
@@ -303,16 +289,16 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
       const bool raw = q.splits > 1;
       if (q.e.bias != nullptr && !raw) {
 #pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) {
-          const uint32_t col = t.col0 + (2 * i + group) * 32 + lane;
-          if (2 * i + group < blocks)
+        for (uint32_t i = 0; i < 2; ++i) {
+          const uint32_t c = kGroups * i + group, col = t.col0 + c * 32 + lane;
+          if (c < blocks)
             bias[warp][i][lane] = col < q.e.n ? load_as_f32(q.e.bias, col, q.e.bias_dtype) : 0.0f;
         }
         __syncwarp();
       }
       uint32_t left = 0;                       // blocks of this warp that have outputs
       if (row0 < q.e.m)
-        for (uint32_t c = group; c < blocks && t.col0 + 32 * c < q.e.n; c += 2) ++left;
+        for (uint32_t c = group; c < blocks && t.col0 + 32 * c < q.e.n; c += kGroups) ++left;
       const uint32_t tmem_warp = tmem + (lanes << 16) + 32 * group;
       auto give_back = [&](uint32_t b) {       // the tensor core may have the buffer again
         cpt::tc_fence_before();
@@ -320,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
         if (lane == 0) cpt::mbar_arrive_cluster(pair_acc_empty + 8 * b);
       };
       auto finish = [&](uint32_t i, float(&v)[32]) {
-        const uint32_t col = t.col0 + 32 * (2 * i + group);
+        const uint32_t col = t.col0 + 32 * (kGroups * i + group);
         if (raw) {
           if (row0 + lane < q.e.m)
             cpe::store32(q.part,
@@ -332,19 +318,19 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
         }
       };
       if constexpr (kSegments) {
-        float acc[128];
+        float acc[64];
 #pragma unroll
-        for (uint32_t i = 0; i < 128; ++i) acc[i] = 0.0f;
+        for (uint32_t i = 0; i < 64; ++i) acc[i] = 0.0f;
         for (uint32_t kb = t.kb0; kb < t.kb1; kb += kSegment, ++it) {
           const uint32_t b = it & 1;
           ok = cpt::mbar_wait(acc_full + 8 * b, (it >> 1) & 1, &gave_up);
           if (!ok) break;
           cpt::tc_fence_after();
 #pragma unroll
-          for (uint32_t i = 0; i < 4; ++i) {
+          for (uint32_t i = 0; i < 2; ++i) {
             if (i < left) {
               float v[32];
-              cpt::tmem_load32<0>(v, tmem_warp + b * kBuffer + 64 * i);
+              cpt::tmem_load32<0>(v, tmem_warp + b * kBuffer + 32 * kGroups * i);
               cpt::tmem_load_wait(v);
 #pragma unroll
               for (uint32_t j = 0; j < 32; ++j) acc[32 * i + j] += v[j];
@@ -358,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
 #pragma unroll
           for (uint32_t j = 0; j < 32; ++j) v[j] = acc[j];
 #pragma unroll
-          for (uint32_t j = 0; j < 96; ++j) acc[j] = acc[j + 32];
+          for (uint32_t j = 0; j < 32; ++j) acc[j] = acc[j + 32];
           finish(i, v);
         }
       } else {
@@ -370,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
         if (left == 0) give_back(b);
         for (uint32_t i = 0; i < left; ++i) {
           float v[32];
-          cpt::tmem_load32<0>(v, tmem_warp + b * kBuffer + 64 * i);
+          cpt::tmem_load32<0>(v, tmem_warp + b * kBuffer + 32 * kGroups * i);
           cpt::tmem_load_wait(v);
           if (i + 1 == left) give_back(b);
           finish(i, v);
@@ -458,7 +444,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
   __shared__ int gave_up;
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t warp = cpt::warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = p.splits == 1 ? 0 : cpt::cluster_rank();
   const uint32_t tile = blockIdx.x / p.splits;       // those of one part of b come together
   const uint32_t row0 = tile / p.tiles_m * 128;
@@ -503,31 +489,30 @@ __global__ void __launch_bounds__(kThinThreads, 2)
 
   if (warp == 4) {
     // ------------------------------------------------------------------ loads
-    uint32_t fills = 0;
     if (cpt::elect_one()) {
       cpt::tma_prefetch_map(&map_a);
       cpt::tma_prefetch_map(&map_b);
-      uint32_t s = 0, round = 0;
-      for (uint32_t kb = kb0; kb < kb1; ++kb) {
-        if (round > 0) {
-          ok = cpt::mbar_wait_one(empty + 8 * s, (round - 1) & 1, &gave_up);
-          if (!ok) break;
-        }
-        const uint32_t dst = cpt::smem_addr(tiles) + s * kStage;
+    }
+    __syncwarp();
+    uint32_t s = 0, round = 0, fills = 0;
+    for (uint32_t kb = kb0; kb < kb1; ++kb) {
+      if (round > 0) {
+        ok = cpt::mbar_wait(empty + 8 * s, (round - 1) & 1, &gave_up);
+        if (!ok) break;
+      }
+      const uint32_t dst = cpt::smem_addr(tiles) + s * kStage;
+      if (cpt::elect_one()) {
         cpt::mbar_expect(full + 8 * s, kStage);
         cpt::tma_load(dst, &map_b, kb * kStageK, row0, full + 8 * s);
         cpt::tma_load(dst + kTileA, &map_a, kb * kStageK, token0, full + 8 * s);
-        ++fills;
-        if (++s == p.stages) {
-          s = 0;
-          ++round;
-        }
       }
-      if (!ok) atomicOr(&g_linear_gave_up, 1u);
+      __syncwarp();
+      ++fills;
+      if (++s == p.stages) {
+        s = 0;
+        ++round;
+      }
     }
-    __syncwarp();
-    fills = __reduce_max_sync(0xFFFFFFFFu, fills);       // the one issuer's
-    ok = true;
     end_role();
     if (gave_up != 0) {
       int late = 0;
@@ -538,36 +523,34 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     }
   } else if (warp == 5) {
     // --------------------------------------------------------------- products
-    if (cpt::elect_one()) {
-      uint32_t s = 0, round = 0, it = 0;
-      for (uint32_t kb = kb0; kb < kb1 && ok; ++it) {
-        const uint32_t b = it & 1, end = min(kb + kSegment, kb1);
-        ok = it < 2 || cpt::mbar_wait_one(acc_empty + 8 * b, ((it >> 1) - 1) & 1, &gave_up);
+    uint32_t s = 0, round = 0, it = 0;
+    for (uint32_t kb = kb0; kb < kb1 && ok; ++it) {
+      const uint32_t b = it & 1, end = min(kb + kSegment, kb1);
+      ok = it < 2 || cpt::mbar_wait(acc_empty + 8 * b, ((it >> 1) - 1) & 1, &gave_up);
+      if (!ok) break;
+      uint32_t more = 0;
+      for (; kb < end; ++kb) {
+        ok = cpt::mbar_wait(full + 8 * s, round & 1, &gave_up);
         if (!ok) break;
-        uint32_t more = 0;
-        for (; kb < end; ++kb) {
-          ok = cpt::mbar_wait_one(full + 8 * s, round & 1, &gave_up);
-          if (!ok) break;
-          cpt::tc_fence_after();
-          const uint32_t at = cpt::smem_addr(tiles) + s * kStage;
-          const uint64_t db = cpt::operand_desc(at), da = cpt::operand_desc(at + kTileA);
+        cpt::tc_fence_after();
+        const uint32_t at = cpt::smem_addr(tiles) + s * kStage;
+        const uint64_t db = cpt::operand_desc(at), da = cpt::operand_desc(at + kTileA);
+        if (cpt::elect_one()) {
           cpt::mma_half_one(tmem + b * kN, db, da, p.instr, more);
 #pragma unroll
           for (uint32_t k = 1; k < 4; ++k)
             cpt::mma_half_one(tmem + b * kN, db + 2 * k, da + 2 * k, p.instr, 1);
-          more = 1;
           cpt::mma_commit(empty + 8 * s);
-          if (++s == p.stages) {
-            s = 0;
-            ++round;
-          }
+          if (kb + 1 == end) cpt::mma_commit(acc_full + 8 * b);
         }
-        if (ok) cpt::mma_commit(acc_full + 8 * b);
+        __syncwarp();
+        more = 1;
+        if (++s == p.stages) {
+          s = 0;
+          ++round;
+        }
       }
-      if (!ok) atomicOr(&g_linear_gave_up, 1u);
     }
-    __syncwarp();
-    ok = true;
     end_role();
     if (gave_up != 0) {
       int late = 0;
@@ -862,7 +845,7 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
     }
     p.stages = min((kSmemMost - 1024) / p.stage_bytes, kMaxStages);
     uint32_t pairs = p.units;
-    if (sums.out != nullptr) pairs = max(pairs, (sums.n + 127) / 128);
+    if (sums.out != nullptr) pairs = max(pairs, (sums.n + 63) / 64);
     pairs = min(pairs, static_cast<uint32_t>(d->pairs));
     const Launch l{dim3(2 * pairs), kThreads, kSmemMost, s, 2};
     e = launch(l, kPairKernels[(is_rich ? 1 : 0) + (segments ? 2 : 0)], p);

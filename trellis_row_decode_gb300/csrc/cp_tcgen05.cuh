@@ -26,6 +26,13 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
+// The warp's number in its CTA, known to be the same for all of its lanes: a role's loop that
+// branches on it keeps its counters, addresses and descriptors in uniform registers, where the TMA
+// and tcgen05 instructions want them.
+__device__ __forceinline__ uint32_t warp_index() {
+  return __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
+}
+
 // True for one lane of a converged warp.  A branch on it is known to be taken by one thread,
 // so what the tcgen05 and TMA instructions in it take stays in uniform registers.
 __device__ __forceinline__ bool elect_one() {
@@ -124,20 +131,20 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
-// The same for one thread of a warp that issues alone.
-__device__ __forceinline__ bool mbar_wait_one(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try(bar, parity)) return true;
-    if ((i & 1023) == 0) {
-      const uint64_t t = global_ns();
-      if (t0 == 0) t0 = t;
-      if (*gave_up != 0 || t - t0 > kWaitNs) {
-        *gave_up = 1;
-        return false;
-      }
-    }
-  }
+// Whether the phase is over, without waiting (try_wait may hold the thread for microseconds), the
+// same to every lane.
+__device__ __forceinline__ bool mbar_ready(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return __all_sync(0xFFFFFFFFu, ok != 0);
 }
 
 // ------------------------------------------------------------------------- TMA
@@ -268,6 +275,16 @@ __host__ __device__ constexpr uint32_t e4m3_instr_desc(uint32_t m, uint32_t n) {
 __device__ __forceinline__ uint64_t operand_desc_mn(uint32_t addr) {
   return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (512ull << 16) | (64ull << 32) |
          (1ull << 46) | (2ull << 61);
+}
+
+// The two words of a descriptor, the upper one the same for both kinds: what steps along an operand
+// is added to the lower one.
+constexpr uint32_t kDescHigh = 64u | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, bool across) {
+  return ((addr & 0x3FFFFu) >> 4) | (across ? 512u << 16 : 1u << 16);
+}
+__device__ __forceinline__ uint64_t desc_of(uint32_t low) {
+  return static_cast<uint64_t>(kDescHigh) << 32 | low;
 }
 
 // Instruction descriptor: fp32 accumulator, bf16 or fp16 operands, each along k or across it.
