@@ -45,13 +45,14 @@ __device__ uint32_t g_linear_gave_up;
 constexpr int kSumWarps = 16;
 constexpr uint32_t kGroups = kSumWarps / 4;            // of four warps, one for each 32 lanes
 constexpr int kThreads = (kSumWarps + 4) * 32;         // + loads of a, products, loads of b, column sums
-constexpr uint32_t kStageK = 64;                       // of k in a stage: 128 bytes
+constexpr uint32_t kStageK = 64;                       // of k in a stage, or a part of it: 128 bytes
 constexpr uint32_t kMaxStages = 8;
 constexpr uint32_t kTileA = 128 * 128;                 // bytes of a's rows per stage and CTA
 constexpr uint32_t kBlock = 64 * 128;                  // bytes of a 64 x 64 block stored across k
 constexpr uint32_t kSmemMost = 220 * 1024;             // dynamic shared memory of a CTA
+constexpr uint32_t kTwoBytes = 24 * 1024;              // stages up to here hold two parts
 constexpr uint32_t kBuffer = 256;                      // columns of tensor memory of a buffer
-constexpr uint32_t kSegment = 8;                       // stages that the tensor core adds up alone
+constexpr uint32_t kSegment = 512;                     // of k that the tensor core adds up alone
 // Registers with segments: launched with 96 a thread (65,536 over 20 warps); the finishing warps
 // (64 sums a thread) take what the other four give up.
 constexpr int kLaunchRegs = 96, kFinishRegs = 104, kOtherRegs = 64;
@@ -73,6 +74,7 @@ struct PairParams {
   PairProduct q[kMostProducts];
   ColumnSums sums;
   uint32_t first_units, units, stages, stage_bytes;
+  uint32_t two;                // a stage holds 128 of k, in two parts
 };
 
 struct Unit {
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
           cpt::tma_prefetch_map(is_a ? &p.map_a[i] : &p.map_b[i]);
       }
       __syncwarp();
-      const uint32_t base = cpt::smem_addr(tiles) + (is_a ? 0 : kTileA);
+      const uint32_t base = cpt::smem_addr(tiles) + (is_a ? 0 : kTileA), k_shift = 6 + p.two;
       uint32_t s = 0, parity = 1, fills = 0;     // (parity 1: a stage that was never filled is free)
       bool ok = true;
       for (uint32_t u = pair; u < p.units && ok; u += pairs) {
@@ -175,20 +177,24 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
         const bool a1 = t.row0 + 128 < q.e.m;             // the second CTA has rows of a
         const bool across = (is_a ? q.a_across : q.b_across) != 0;
         const uint32_t boxes = is_a ? (half == 0 || a1 ? (across ? 2 : 1) : 0) : q.b_boxes;
-        const uint32_t bytes = 2 * q.b_bytes + (a1 ? 2 : 1) * kTileA;
+        const uint32_t bytes = (2 * q.b_bytes + (a1 ? 2 : 1) * kTileA) << p.two;
         const uint32_t at = is_a ? t.row0 + half * 128 : t.col0 + half * (q.bn / 2);
         const bool expect = is_a && half == 0;
         for (uint32_t kb = t.kb0; kb < t.kb1; ++kb) {
           ok = cpt::mbar_wait(empty + 8 * s, parity, &gave_up);
           if (!ok) break;
-          const uint32_t dst = base + s * p.stage_bytes, k0 = kb * kStageK;
+          const uint32_t dst = base + s * p.stage_bytes, k0 = kb << k_shift;
+          const uint32_t dst2 = dst + p.stage_bytes / 2, bar = pair_full + 8 * s;
           if (cpt::elect_one()) {
             if (expect) cpt::mbar_expect(full + 8 * s, bytes);
             if (across) {
-              for (uint32_t i = 0; i < boxes; ++i)
-                cpt::tma_load_pair(dst + i * kBlock, map, at + 64 * i, k0, pair_full + 8 * s);
+              for (uint32_t i = 0; i < boxes; ++i) {
+                cpt::tma_load_pair(dst + i * kBlock, map, at + 64 * i, k0, bar);
+                if (p.two) cpt::tma_load_pair(dst2 + i * kBlock, map, at + 64 * i, k0 + kStageK, bar);
+              }
             } else if (boxes != 0) {
-              cpt::tma_load_pair(dst, map, k0, at, pair_full + 8 * s);
+              cpt::tma_load_pair(dst, map, k0, at, bar);
+              if (p.two) cpt::tma_load_pair(dst2, map, k0 + kStageK, at, bar);
             }
           }
           __syncwarp();
@@ -213,6 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
       }
     } else if (warp == kSumWarps + 1 && half == 0) {
       // ------------------------------------------------------------- products
+      const uint32_t segment = kSegment / kStageK >> p.two;
       uint32_t it = 0, s = 0, parity = 0;
       bool ok = true;
       for (uint32_t u = pair; u < p.units && ok; u += pairs) {
@@ -224,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
         const uint32_t b_low = cpt::desc_low(cpt::smem_addr(tiles) + kTileA, q.b_across != 0);
         for (uint32_t kb = t.kb0; kb < t.kb1 && ok; ++it) {
           const uint32_t b = it & 1, to = tmem + b * kBuffer;
-          const uint32_t end = kSegments ? min(kb + kSegment, t.kb1) : t.kb1;
+          const uint32_t end = kSegments ? min(kb + segment, t.kb1) : t.kb1;
           ok = it < 2 || cpt::mbar_wait(acc_empty + 8 * b, ((it >> 1) - 1) & 1, &gave_up);
           if (!ok) break;
           uint32_t more = 0;
@@ -232,13 +239,19 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
             ok = cpt::mbar_wait(full + 8 * s, parity, &gave_up);
             if (!ok) break;
             cpt::tc_fence_after();
-            const uint32_t at = s * (p.stage_bytes >> 4);
+            const uint32_t at = s * (p.stage_bytes >> 4), at2 = at + (p.stage_bytes >> 5);
             if (cpt::elect_one()) {
               cpt::mma_half_pair(to, cpt::desc_of(a_low + at), cpt::desc_of(b_low + at), instr, more);
 #pragma unroll
               for (uint32_t k = 1; k < 4; ++k)
                 cpt::mma_half_pair(to, cpt::desc_of(a_low + at + k * a_step),
                                    cpt::desc_of(b_low + at + k * b_step), instr, 1);
+              if (p.two) {
+#pragma unroll
+                for (uint32_t k = 0; k < 4; ++k)
+                  cpt::mma_half_pair(to, cpt::desc_of(a_low + at2 + k * a_step),
+                                     cpt::desc_of(b_low + at2 + k * b_step), instr, 1);
+              }
               cpt::mma_commit_pair(empty + 8 * s, 3);
               if (kb + 1 == end) cpt::mma_commit_pair(acc_full + 8 * b, 3);
             }
@@ -321,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
         float acc[64];
 #pragma unroll
         for (uint32_t i = 0; i < 64; ++i) acc[i] = 0.0f;
-        for (uint32_t kb = t.kb0; kb < t.kb1; kb += kSegment, ++it) {
+        for (uint32_t kb = t.kb0; kb < t.kb1; kb += kSegment / kStageK >> p.two, ++it) {
           const uint32_t b = it & 1;
           ok = cpt::mbar_wait(acc_full + 8 * b, (it >> 1) & 1, &gave_up);
           if (!ok) break;
@@ -525,7 +538,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     // --------------------------------------------------------------- products
     uint32_t s = 0, round = 0, it = 0;
     for (uint32_t kb = kb0; kb < kb1 && ok; ++it) {
-      const uint32_t b = it & 1, end = min(kb + kSegment, kb1);
+      const uint32_t b = it & 1, end = min(kb + kSegment / kStageK, kb1);
       ok = it < 2 || cpt::mbar_wait(acc_empty + 8 * b, ((it >> 1) - 1) & 1, &gave_up);
       if (!ok) break;
       uint32_t more = 0;
@@ -564,7 +577,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
 #pragma unroll
     for (uint32_t i = 0; i < kN; ++i) acc[i] = 0.0f;
     uint32_t it = 0;
-    for (uint32_t kb = kb0; kb < kb1; kb += kSegment, ++it) {
+    for (uint32_t kb = kb0; kb < kb1; kb += kSegment / kStageK, ++it) {
       const uint32_t b = it & 1;
       ok = cpt::mbar_wait(acc_full + 8 * b, (it >> 1) & 1, &gave_up);
       if (!ok) break;
@@ -777,6 +790,7 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
   FinishParams f{};
   bool is_rich = false, segments = false, finish = false;
   uint64_t units[kMostProducts] = {};
+  uint32_t ks[kMostProducts] = {};
   int used = 0;
   for (int i = 0; i < count; ++i) {
     const Epilogue& ep = q[i].e;
@@ -793,7 +807,6 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
     PairProduct& x = p.q[used];
     const Tiling t = choose_tiling(ep.m, ep.n, q[i].k);
     x.e = ep;
-    x.kblocks = (q[i].k + kStageK - 1) / kStageK;
     x.bn = t.bn;
     x.splits = t.splits;
     x.tiles_m = (ep.m + 255) / 256;
@@ -807,7 +820,8 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
     x.b_boxes = x.b_across ? (t.bn / 2 + 63) / 64 : 1;
     x.b_bytes = x.b_across ? x.b_boxes * kBlock : t.bn / 2 * 128;
     x.instr = cpt::half_instr_desc(256, t.bn, q[i].dtype == CP_BF16, x.a_across, x.b_across);
-    segments |= ep.out_dtype == CP_F32 && (x.kblocks + t.splits - 1) / t.splits > kSegment;
+    segments |= ep.out_dtype == CP_F32 && q[i].k / t.splits > kSegment;
+    ks[used] = q[i].k;
     if (t.splits > 1) {
       x.pitch = part_pitch(ep.n);
       x.part = part;
@@ -843,7 +857,11 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
       p.map_a[1] = p.map_a[0];
       p.map_b[1] = p.map_b[0];
     }
+    p.two = p.stage_bytes <= kTwoBytes ? 1 : 0;
+    p.stage_bytes <<= p.two;
     p.stages = min((kSmemMost - 1024) / p.stage_bytes, kMaxStages);
+    for (int i = 0; i < used; ++i)
+      p.q[i].kblocks = (ks[i] + (kStageK << p.two) - 1) / (kStageK << p.two);
     uint32_t pairs = p.units;
     if (sums.out != nullptr) pairs = max(pairs, (sums.n + 63) / 64);
     pairs = min(pairs, static_cast<uint32_t>(d->pairs));
