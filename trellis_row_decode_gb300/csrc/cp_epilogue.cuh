@@ -92,6 +92,46 @@ __device__ __forceinline__ void drop_quad(const DropParams& p, const DropKey& ke
   drop_quad(p, key, round_keys(key), quad, row, v);
 }
 
+// Sixteen columns of a row, 4 * quad on: four calls of the generator side by side, so that its
+// chains of products overlap and a round's key is made once for all.
+__device__ __forceinline__ void drop16(const DropParams& p, const DropKey& key, uint32_t quad,
+                                       uint32_t row, float* v) {
+  if (p.mode == 2) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+    return;
+  }
+  uint32_t c0[4], c1[4], c2[4], c3[4], k0 = key.k0, k1 = key.k1;
+#pragma unroll
+  for (uint32_t q = 0; q < 4; ++q) {
+    c0[q] = quad + q;
+    c1[q] = row;
+    c2[q] = key.o0;
+    c3[q] = key.o1;
+  }
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+#pragma unroll
+    for (uint32_t q = 0; q < 4; ++q) {
+      const uint64_t a = static_cast<uint64_t>(c0[q]) * 0xD2511F53u;
+      const uint64_t b = static_cast<uint64_t>(c2[q]) * 0xCD9E8D57u;
+      c0[q] = static_cast<uint32_t>(b >> 32) ^ c1[q] ^ k0;
+      c1[q] = static_cast<uint32_t>(b);
+      c2[q] = static_cast<uint32_t>(a >> 32) ^ c3[q] ^ k1;
+      c3[q] = static_cast<uint32_t>(a);
+    }
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+#pragma unroll
+  for (uint32_t q = 0; q < 4; ++q) {
+    v[4 * q] = c0[q] <= p.last ? v[4 * q] * p.scale : 0.0f;
+    v[4 * q + 1] = c1[q] <= p.last ? v[4 * q + 1] * p.scale : 0.0f;
+    v[4 * q + 2] = c2[q] <= p.last ? v[4 * q + 2] * p.scale : 0.0f;
+    v[4 * q + 3] = c3[q] <= p.last ? v[4 * q + 3] * p.scale : 0.0f;
+  }
+}
+
 // What a call's p, seed and offset say; false where p is no probability.
 inline bool drop_params(DropParams* d, double p, uint64_t seed, uint64_t offset,
                         const uint64_t* rng) {
@@ -283,30 +323,37 @@ __device__ __forceinline__ void store32(void* p, uint64_t at, int dtype, const f
     store16(static_cast<__nv_bfloat16*>(p) + at + 16, v + 16);
   }
 }
-// v += 32 elements on a 32-byte boundary.
-__device__ __forceinline__ void add32(float (&v)[32], const void* p, uint64_t at, int dtype) {
-  if (dtype == CP_F32) {
-    Packed<float> r[4];
+// 32 elements on a 32-byte boundary: v += p, and for 16 bits the loads and the addition apart, so
+// that the loads are under way while the rest of the epilogue runs.
+struct Early {
+  Packed<float> r[2];
+};
+__device__ __forceinline__ Early load32(const void* p, uint64_t at) {
+  Early e;
 #pragma unroll
-    for (int h = 0; h < 4; ++h) r[h] = load_octet(static_cast<const float*>(p) + at + 8 * h);
+  for (int h = 0; h < 2; ++h)
+    e.r[h] = load_octet(reinterpret_cast<const float*>(static_cast<const uint16_t*>(p) + at + 16 * h));
+  return e;
+}
+__device__ __forceinline__ void add32(float (&v)[32], const Early& e, int dtype) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(r[i / 8].w[i % 8]);
-  } else {
-    Packed<float> r[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      r[h] = load_octet(reinterpret_cast<const float*>(static_cast<const uint16_t*>(p) + at + 16 * h));
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t w = r[i / 8].w[i % 8];
-      if (dtype == CP_F16) {
-        v[2 * i] += __half2float(__ushort_as_half(static_cast<uint16_t>(w)));
-        v[2 * i + 1] += __half2float(__ushort_as_half(static_cast<uint16_t>(w >> 16)));
-      } else {
-        v[2 * i] += __uint_as_float(w << 16);
-        v[2 * i + 1] += __uint_as_float(w & 0xFFFF0000u);
-      }
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t w = e.r[i / 8].w[i % 8];
+    if (dtype == CP_F16) {
+      v[2 * i] += __half2float(__ushort_as_half(static_cast<uint16_t>(w)));
+      v[2 * i + 1] += __half2float(__ushort_as_half(static_cast<uint16_t>(w >> 16)));
+    } else {
+      v[2 * i] += __uint_as_float(w << 16);
+      v[2 * i + 1] += __uint_as_float(w & 0xFFFF0000u);
     }
+  }
+}
+__device__ __forceinline__ void add32(float (&v)[32], const float* p) {
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const Packed<float> r = load_octet(p + 8 * h);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[8 * h + i] += __uint_as_float(r.w[i]);
   }
 }
 
@@ -336,6 +383,10 @@ __device__ __forceinline__ void finish_block(const Epilogue& e, const DropKey& k
                                              float (&v)[32]) {
   const uint32_t row = row0 + lane;
   const bool fast = e.aligned != 0 && col + 32 <= e.n;
+  const uint64_t res_at = static_cast<uint64_t>(row) * e.ldr + col;
+  const bool early = fast && row < e.m && e.residual != nullptr && e.out_dtype != CP_F32;
+  Early res = {};
+  if (early) res = load32(e.residual, res_at);
   if (e.bias != nullptr) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -370,14 +421,14 @@ __device__ __forceinline__ void finish_block(const Epilogue& e, const DropKey& k
       for (int i = 0; i < 32; ++i) v[i] = act<decltype(tag)::value>(v[i]);
     });
     if (e.drop.mode != 0) {
-#pragma unroll
-      for (uint32_t q = 0; q < 8; ++q) drop_quad(e.drop, key, col / 4 + q, row, v + 4 * q);
+      drop16(e.drop, key, col / 4, row, v);
+      drop16(e.drop, key, col / 4 + 4, row, v + 16);
     }
   }
   if (fast) {
     if (row < e.m) {
-      if (e.residual != nullptr)
-        add32(v, e.residual, static_cast<uint64_t>(row) * e.ldr + col, e.out_dtype);
+      if (early) add32(v, res, e.out_dtype);
+      else if (e.residual != nullptr) add32(v, static_cast<const float*>(e.residual) + res_at);
       store32(e.out, static_cast<uint64_t>(row) * e.ldo + col, e.out_dtype, v);
     }
     __syncwarp();
