@@ -323,37 +323,31 @@ __device__ __forceinline__ void store32(void* p, uint64_t at, int dtype, const f
     store16(static_cast<__nv_bfloat16*>(p) + at + 16, v + 16);
   }
 }
-// 32 elements on a 32-byte boundary: v += p, and for 16 bits the loads and the addition apart, so
-// that the loads are under way while the rest of the epilogue runs.
-struct Early {
-  Packed<float> r[2];
-};
-__device__ __forceinline__ Early load32(const void* p, uint64_t at) {
-  Early e;
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    e.r[h] = load_octet(reinterpret_cast<const float*>(static_cast<const uint16_t*>(p) + at + 16 * h));
-  return e;
-}
-__device__ __forceinline__ void add32(float (&v)[32], const Early& e, int dtype) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t w = e.r[i / 8].w[i % 8];
-    if (dtype == CP_F16) {
-      v[2 * i] += __half2float(__ushort_as_half(static_cast<uint16_t>(w)));
-      v[2 * i + 1] += __half2float(__ushort_as_half(static_cast<uint16_t>(w >> 16)));
-    } else {
-      v[2 * i] += __uint_as_float(w << 16);
-      v[2 * i + 1] += __uint_as_float(w & 0xFFFF0000u);
-    }
+// v += 32 elements on a 32-byte boundary.
+__device__ __forceinline__ void add_pair(float& lo, float& hi, uint32_t w, int dtype) {
+  if (dtype == CP_F16) {
+    lo += __half2float(__ushort_as_half(static_cast<uint16_t>(w)));
+    hi += __half2float(__ushort_as_half(static_cast<uint16_t>(w >> 16)));
+  } else {
+    lo += __uint_as_float(w << 16);
+    hi += __uint_as_float(w & 0xFFFF0000u);
   }
 }
-__device__ __forceinline__ void add32(float (&v)[32], const float* p) {
+__device__ __forceinline__ void add32(float (&v)[32], const void* p, uint64_t at, int dtype) {
+  if (dtype == CP_F32) {
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    const Packed<float> r = load_octet(p + 8 * h);
+    for (int h = 0; h < 4; ++h) {
+      const Packed<float> r = load_octet(static_cast<const float*>(p) + at + 8 * h);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[8 * h + i] += __uint_as_float(r.w[i]);
+      for (int i = 0; i < 8; ++i) v[8 * h + i] += __uint_as_float(r.w[i]);
+    }
+  } else {
+    Packed<float> r[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      r[h] = load_octet(reinterpret_cast<const float*>(static_cast<const uint16_t*>(p) + at + 16 * h));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) add_pair(v[2 * i], v[2 * i + 1], r[i / 8].w[i % 8], dtype);
   }
 }
 
@@ -373,20 +367,16 @@ __device__ __forceinline__ void transpose32(float (&x)[32], uint32_t lane) {
   }
 }
 
-// The epilogue of a warp's 32 rows (row0 on, one a lane) by 32 columns (col on, a multiple of
-// 32) of sums.  `bias`: the columns' bias in shared memory, zeros where there is none.  Rows on
-// 32-byte boundaries and columns all there: a lane reads and writes its own row, whole sectors.
-// Else the block is transposed, so that each access is of 32 neighbours of one row.
+// The epilogue of a warp's 32 rows (row0 on, one a lane) by 32 columns (col on, a multiple of 32)
+// of sums, in two steps.  The first: bias, kept sums, activation, dropout.  `bias`: the columns'
+// bias in shared memory.  fast: rows on 32-byte boundaries and columns all there, so a lane reads
+// and writes its own row, whole sectors; else the block is transposed, so that each access is of
+// 32 neighbours of one row.
 template <bool kRich>
-__device__ __forceinline__ void finish_block(const Epilogue& e, const DropKey& key, uint32_t row0,
-                                             uint32_t col, uint32_t lane, const float* bias,
-                                             float (&v)[32]) {
+__device__ __forceinline__ void shape_block(const Epilogue& e, const DropKey& key, uint32_t row0,
+                                            uint32_t col, uint32_t lane, const float* bias,
+                                            bool fast, float (&v)[32]) {
   const uint32_t row = row0 + lane;
-  const bool fast = e.aligned != 0 && col + 32 <= e.n;
-  const uint64_t res_at = static_cast<uint64_t>(row) * e.ldr + col;
-  const bool early = fast && row < e.m && e.residual != nullptr && e.out_dtype != CP_F32;
-  Early res = {};
-  if (early) res = load32(e.residual, res_at);
   if (e.bias != nullptr) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -397,7 +387,6 @@ __device__ __forceinline__ void finish_block(const Epilogue& e, const DropKey& k
       v[4 * i + 3] += b.w;
     }
   }
-  const uint32_t rows = min(32u, e.m - row0);
   if constexpr (kRich) {
     if (e.pre != nullptr) {
       if (fast) {
@@ -408,6 +397,7 @@ __device__ __forceinline__ void finish_block(const Epilogue& e, const DropKey& k
         for (int i = 0; i < 32; ++i) u[i] = v[i];
         transpose32(u, lane);
         if (col + lane < e.n) {
+          const uint32_t rows = min(32u, e.m - row0);
           const uint64_t at = static_cast<uint64_t>(row0) * e.ldp + col + lane;
 #pragma unroll
           for (uint32_t r = 0; r < 32; ++r)
@@ -425,15 +415,22 @@ __device__ __forceinline__ void finish_block(const Epilogue& e, const DropKey& k
       drop16(e.drop, key, col / 4 + 4, row, v + 16);
     }
   }
+}
+
+// The second: the residual's addition and the outputs.
+__device__ __forceinline__ void write_block(const Epilogue& e, uint32_t row0, uint32_t col,
+                                            uint32_t lane, bool fast, float (&v)[32]) {
+  const uint32_t row = row0 + lane;
   if (fast) {
     if (row < e.m) {
-      if (early) add32(v, res, e.out_dtype);
-      else if (e.residual != nullptr) add32(v, static_cast<const float*>(e.residual) + res_at);
+      if (e.residual != nullptr)
+        add32(v, e.residual, static_cast<uint64_t>(row) * e.ldr + col, e.out_dtype);
       store32(e.out, static_cast<uint64_t>(row) * e.ldo + col, e.out_dtype, v);
     }
     __syncwarp();
     return;
   }
+  const uint32_t rows = min(32u, e.m - row0);
   transpose32(v, lane);
   if (col + lane < e.n) {
     if (e.residual != nullptr) {

@@ -67,14 +67,17 @@ struct PairProduct {
   uint32_t b_bytes, b_boxes; // of b, a stage and CTA
   uint32_t instr;
   int a_across, b_across;
+  int tma_out, tma_residual; // outputs leave, the residual comes, through shared memory and TMA
 };
 
 struct PairParams {
-  CUtensorMap map_a[kMostProducts], map_b[kMostProducts];
+  CUtensorMap map_a[kMostProducts], map_b[kMostProducts], map_out[kMostProducts],
+      map_residual[kMostProducts];
   PairProduct q[kMostProducts];
   ColumnSums sums;
   uint32_t first_units, units, stages, stage_bytes;
   uint32_t two;                // a stage holds 128 of k, in two parts
+  uint32_t slots_at, slots;    // behind the stages: each finishing warp's bytes for its blocks
 };
 
 struct Unit {
@@ -97,6 +100,39 @@ __device__ __forceinline__ Unit unit_of(const PairParams& p, uint32_t u) {
   return r;
 }
 
+// A block of 32 x 32 outputs in its slot, as the tensor map of 32 columns lays it out: rows of 64
+// bytes with the 64-byte swizzle, or of 128 (fp32) with the 128-byte one; a lane has a row.  `add`:
+// the residual's block lies there already.
+constexpr uint32_t kSlot = 32 * 64, kSlotF32 = 32 * 128;
+__device__ __forceinline__ void write_slot(uint32_t slot, uint32_t lane, int dtype, bool add,
+                                           float (&v)[32]) {
+  if (dtype == CP_F32) {
+#pragma unroll
+    for (uint32_t c = 0; c < 8; ++c)
+      cpt::store_shared4(slot + lane * 128 + ((c ^ (lane & 7)) << 4), __float_as_uint(v[4 * c]),
+                         __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
+                         __float_as_uint(v[4 * c + 3]));
+    return;
+  }
+#pragma unroll
+  for (uint32_t c = 0; c < 4; ++c) {
+    const uint32_t at = slot + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4);
+    if (add) {
+      const uint4 r = cpt::load_shared4(at);
+      cpe::add_pair(v[8 * c], v[8 * c + 1], r.x, dtype);
+      cpe::add_pair(v[8 * c + 2], v[8 * c + 3], r.y, dtype);
+      cpe::add_pair(v[8 * c + 4], v[8 * c + 5], r.z, dtype);
+      cpe::add_pair(v[8 * c + 6], v[8 * c + 7], r.w, dtype);
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i)
+      w[i] = dtype == CP_F16 ? pack_pair<__half>(v[8 * c + 2 * i], v[8 * c + 2 * i + 1])
+                             : pack_pair<__nv_bfloat16>(v[8 * c + 2 * i], v[8 * c + 2 * i + 1]);
+    cpt::store_shared4(at, w[0], w[1], w[2], w[3]);
+  }
+}
+
 // kRich: some product has an activation, dropout, or sums to keep.
 // kSegments: some product is wanted in 32 bits.  The tensor core cuts its running sum at every
 // addition instead of rounding it, an error that grows with k (measured, relative: 1.07e-9 k,
@@ -107,6 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
   extern __shared__ uint8_t dyn[];
   __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5];
   __shared__ __align__(16) float bias[kSumWarps][2][32];
+  __shared__ __align__(8) uint64_t residual_bars[kSumWarps];
   __shared__ uint32_t tmem_base;
   __shared__ uint32_t issued[2];           // this CTA's fills of stages, by either issuer
   __shared__ int gave_up;
@@ -131,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
       cpt::mbar_init(acc_empty + 8 * b, 2 * kSumWarps);
     }
     cpt::mbar_init(drained, 1);
+    for (uint32_t w = 0; w < kSumWarps; ++w) cpt::mbar_init(cpt::smem_addr(&residual_bars[w]), 1);
     cpt::mbar_init_fence();
     gave_up = 0;
   }
@@ -292,8 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
     if constexpr (kSegments) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFinishRegs));
     const uint32_t lanes = (warp & 3) * 32, group = warp >> 2;
     const DropKey key = cpe::drop_key(p.q[0].e.drop);      // (dropout is in the first product alone)
-    uint32_t it = 0;
-    bool ok = true;
+    const uint32_t slots = cpt::smem_addr(tiles) + p.slots_at + warp * p.slots;
+    const uint32_t residual_bar = cpt::smem_addr(&residual_bars[warp]);
+    uint32_t it = 0, residual_parity = 0;
+    bool ok = true, coming = false;            // coming: loads of the residual are under way
     for (uint32_t u = pair; u < p.units && ok; u += pairs) {
       const Unit t = unit_of(p, u);
       const PairProduct& q = p.q[t.which];
@@ -312,6 +352,17 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
       uint32_t left = 0;                       // blocks of this warp that have outputs
       if (row0 < q.e.m)
         for (uint32_t c = group; c < blocks && t.col0 + 32 * c < q.e.n; c += kGroups) ++left;
+      if (q.tma_residual && left != 0) {       // a slot for each block, free since the tile before
+        if (lane == 0) {
+          cpt::stores_read();
+          cpt::mbar_expect(residual_bar, left * kSlot);
+          for (uint32_t i = 0; i < left; ++i)
+            cpt::tma_load(slots + i * kSlot, &p.map_residual[t.which],
+                          t.col0 + 32 * (kGroups * i + group), row0, residual_bar);
+        }
+        __syncwarp();
+        coming = true;
+      }
       const uint32_t tmem_warp = tmem + (lanes << 16) + 32 * group;
       auto give_back = [&](uint32_t b) {       // the tensor core may have the buffer again
         cpt::tc_fence_before();
@@ -326,9 +377,34 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
                          (static_cast<uint64_t>(t.split) * q.e.m + row0 + lane) * q.pitch + col,
                          CP_F32, v);
           __syncwarp();
-        } else {
-          cpe::finish_block<kRich>(q.e, key, row0, col, lane, bias[warp][i], v);
+          return;
         }
+        const bool fast = q.e.aligned != 0 && col + 32 <= q.e.n;
+        cpe::shape_block<kRich>(q.e, key, row0, col, lane, bias[warp][i], fast, v);
+        if (!q.tma_out) {
+          cpe::write_block(q.e, row0, col, lane, fast, v);
+          return;
+        }
+        uint32_t slot = slots;
+        if (q.tma_residual) {
+          slot += i * kSlot;
+          if (coming) {                        // (the first block of the tile)
+            ok = cpt::mbar_wait(residual_bar, residual_parity, &gave_up);
+            residual_parity ^= 1;
+            coming = !ok;
+          }
+        } else {
+          if (q.e.residual != nullptr && row0 + lane < q.e.m)
+            cpe::add32(v, q.e.residual, static_cast<uint64_t>(row0 + lane) * q.e.ldr + col,
+                       q.e.out_dtype);
+          if (lane == 0) cpt::stores_read();
+          __syncwarp();
+        }
+        write_slot(slot, lane, q.e.out_dtype, q.tma_residual != 0, v);
+        cpt::stores_fence();
+        __syncwarp();
+        if (lane == 0) cpt::tma_store(&p.map_out[t.which], col, row0, slot);
+        __syncwarp();
       };
       if constexpr (kSegments) {
         float acc[64];
@@ -352,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
           give_back(b);
         }
         if (!ok) break;
-        for (uint32_t i = 0; i < left; ++i) {
+        for (uint32_t i = 0; i < left && ok; ++i) {
           float v[32];
 #pragma unroll
           for (uint32_t j = 0; j < 32; ++j) v[j] = acc[j];
@@ -367,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
         cpt::tc_fence_after();
         ++it;
         if (left == 0) give_back(b);
-        for (uint32_t i = 0; i < left; ++i) {
+        for (uint32_t i = 0; i < left && ok; ++i) {
           float v[32];
           cpt::tmem_load32<0>(v, tmem_warp + b * kBuffer + 32 * kGroups * i);
           cpt::tmem_load_wait(v);
@@ -377,6 +453,12 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
       }
     }
     if (!ok && lane == 0) atomicOr(&g_linear_gave_up, 1u);
+    if (lane == 0) cpt::stores_done();         // before the slots are someone else's
+    __syncwarp();
+    if (coming) {
+      int late = 0;
+      cpt::mbar_wait(residual_bar, residual_parity, &late);
+    }
     end_role();
   }
   __syncwarp();
@@ -729,6 +811,24 @@ bool encode_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t row
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Blocks of 32 x 32 outputs (or of the residual) as write_slot lays them out.
+bool encode_block_map(CUtensorMap* map, const void* base, int dtype, uint64_t n, uint64_t m,
+                      uint64_t ld) {
+  const uint64_t size = dtype_size(dtype);
+  const cuuint64_t dims[2] = {n, m};
+  const cuuint64_t strides[1] = {m == 1 ? (size * n + 15) / 16 * 16 : size * ld};
+  const cuuint32_t box[2] = {32, 32};
+  const cuuint32_t elem[2] = {1, 1};
+  return g_encode.load()(
+             map, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+             const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             size == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool block_map_ok(const void* p, int dtype, uint64_t m, uint64_t ld) {
+  return cpx::aligned(p, 16) && (m == 1 || (ld != 0 && ld * dtype_size(dtype) % 16 == 0));
+}
+
 // Columns of a tile and units that share its k.  By shapes alone, for the 76 pairs of a whole
 // card, so that a product's sums and its workspace are the same wherever it runs.
 constexpr uint32_t kPairs = 76;
@@ -844,6 +944,23 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
       cpx::set_error("tensor map refused");
       return CP_ERR_CUDA;
     }
+    // Outputs through TMA, where their rows allow it and what else the epilogue touches is read and
+    // written by whole blocks (the residual through TMA too, unless it has 32 bits).
+    const bool whole = ep.aligned != 0 && ep.n % 32 == 0, f32 = ep.out_dtype == CP_F32;
+    const bool residual_ok =
+        ep.residual == nullptr ||
+        (f32 ? whole : block_map_ok(ep.residual, ep.out_dtype, ep.m, ep.ldr));
+    x.tma_out = t.splits == 1 && block_map_ok(ep.out, ep.out_dtype, ep.m, ep.ldo) && residual_ok &&
+                (ep.pre == nullptr || whole);
+    x.tma_residual = x.tma_out && ep.residual != nullptr && !f32;
+    if ((x.tma_out &&
+         !encode_block_map(&p.map_out[used], ep.out, ep.out_dtype, ep.n, ep.m, ep.ldo)) ||
+        (x.tma_residual &&
+         !encode_block_map(&p.map_residual[used], ep.residual, ep.out_dtype, ep.n, ep.m, ep.ldr))) {
+      cpx::set_error("tensor map refused");
+      return CP_ERR_CUDA;
+    }
+    if (x.tma_out) p.slots = max(p.slots, f32 ? kSlotF32 : x.tma_residual ? 2 * kSlot : kSlot);
     p.stage_bytes = max(p.stage_bytes, kTileA + x.b_bytes);
     ++used;
   }
@@ -859,7 +976,8 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
     }
     p.two = p.stage_bytes <= kTwoBytes ? 1 : 0;
     p.stage_bytes <<= p.two;
-    p.stages = min((kSmemMost - 1024) / p.stage_bytes, kMaxStages);
+    p.stages = min((kSmemMost - 1024 - kSumWarps * p.slots) / p.stage_bytes, kMaxStages);
+    p.slots_at = p.stages * p.stage_bytes;
     for (int i = 0; i < used; ++i)
       p.q[i].kblocks = (ks[i] + (kStageK << p.two) - 1) / (kStageK << p.two);
     uint32_t pairs = p.units;
