@@ -159,8 +159,7 @@ cudaError_t align(Operand* (&op)[2], const uint64_t (&rows)[2], uint64_t k, uint
 
 // Bytes for the sums of products whose k is split; they begin on a 32-byte boundary, the workspace
 // on a 16-byte one.
-uint64_t part_bytes(const uint32_t (&m)[2], const uint32_t (&n)[2], const uint32_t (&k)[2],
-                    int count) {
+uint64_t part_bytes(const uint32_t* m, const uint32_t* n, const uint32_t* k, int count) {
   const uint64_t floats = cplin::part_floats(m, n, k, count);
   return floats == 0 ? 0 : 4 * floats + 16;
 }
@@ -174,11 +173,11 @@ extern "C" uint64_t cp_linear_workspace_bytes(const void* x, uint64_t x_stride, 
                                               uint64_t w_stride, uint64_t m, uint64_t n,
                                               uint64_t k) {
   if (m >= kMostRows || n >= kMostRows || k >= kMostK || m == 0 || n == 0 || k == 0) return 0;
-  const uint32_t ms[2] = {static_cast<uint32_t>(m)}, ns[2] = {static_cast<uint32_t>(n)},
-                 ks[2] = {static_cast<uint32_t>(k)};
+  const uint32_t ms = static_cast<uint32_t>(m), ns = static_cast<uint32_t>(n),
+                 ks = static_cast<uint32_t>(k);
   return ((rows_ok(x, x_stride, m) ? 0 : m) + (rows_ok(w, w_stride, n) ? 0 : n)) * 2 *
              row_pitch(k) +
-         (m > cplin::kThinRows ? part_bytes(ms, ns, ks, 1) : 0);
+         (m > cplin::kThinRows ? part_bytes(&ms, &ns, &ks, 1) : 0);
 }
 
 extern "C" cp_status cp_linear(const void* x, uint64_t x_stride, const void* w, uint64_t w_stride,
@@ -248,7 +247,9 @@ extern "C" uint64_t cp_linear_grad_workspace_bytes(uint64_t m, uint64_t n, uint6
     const uint32_t ms[2] = {static_cast<uint32_t>(m), static_cast<uint32_t>(n)};
     const uint32_t ns[2] = {static_cast<uint32_t>(k), static_cast<uint32_t>(k)};
     const uint32_t ks[2] = {static_cast<uint32_t>(n), static_cast<uint32_t>(m)};
-    parts = part_bytes(ms, ns, ks, 2);
+    // (of both products together, or of either where the other is not wanted)
+    parts = std::max({part_bytes(ms, ns, ks, 2), part_bytes(ms, ns, ks, 1),
+                      part_bytes(ms + 1, ns + 1, ks + 1, 1)});
   }
   return std::max<uint64_t>(16, dz + copies + db + parts);
 }

@@ -37,8 +37,7 @@ struct ColumnSums {
 // Products of one launch on CTA pairs (cp_linear_tc.cu), two at most; `part` holds
 // part_floats(products) floats where some are split along k.
 constexpr int kMostProducts = 2;
-uint64_t part_floats(const uint32_t (&m)[kMostProducts], const uint32_t (&n)[kMostProducts],
-                     const uint32_t (&k)[kMostProducts], int count);
+uint64_t part_floats(const uint32_t* m, const uint32_t* n, const uint32_t* k, int count);
 cp_status launch_products(const Product* q, int count, const ColumnSums& sums, float* part,
                           cudaStream_t s);
 

@@ -44,7 +44,10 @@ __device__ uint32_t g_linear_gave_up;
 
 constexpr int kSumWarps = 16;
 constexpr uint32_t kGroups = kSumWarps / 4;            // of four warps, one for each 32 lanes
-constexpr int kThreads = (kSumWarps + 4) * 32;         // + loads of a, products, loads of b, column sums
+// The issuing warps come first: where a scheduler has several ready warps the older one goes, and
+// the tensor core waits for these (4096 x 4096 x 1024 with everything: FIGURE).
+constexpr uint32_t kLoadA = 0, kMmaWarp = 1, kLoadB = 2, kSumsWarp = 3, kFirstFinish = 4;
+constexpr int kThreads = (kFirstFinish + kSumWarps) * 32;
 constexpr uint32_t kStageK = 64;                       // of k in a stage, or a part of it: 128 bytes
 constexpr uint32_t kMaxStages = 8;
 constexpr uint32_t kTileA = 128 * 128;                 // bytes of a's rows per stage and CTA
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
     cpt::mbar_init_fence();
     gave_up = 0;
   }
-  if (warp == kSumWarps + 1) cpt::tmem_alloc_pair(cpt::smem_addr(&tmem_base), 2 * kBuffer);
+  if (warp == kMmaWarp) cpt::tmem_alloc_pair(cpt::smem_addr(&tmem_base), 2 * kBuffer);
   cpt::tc_fence_before();
   __syncthreads();
   cpt::cluster_sync();
@@ -194,12 +197,12 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
     cpt::cluster_sync();
   };
 
-  if (warp >= kSumWarps) {
+  if (warp < kFirstFinish) {
     if constexpr (kSegments) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kSumWarps || warp == kSumWarps + 2) {
+    if (warp == kLoadA || warp == kLoadB) {
       // ---------------------------------------------------------------- loads
       // (a warp for a, one for b; each runs its loop whole and elects a thread to issue)
-      const bool is_a = warp == kSumWarps;
+      const bool is_a = warp == kLoadA;
       if (cpt::elect_one()) {
         for (int i = 0; i < kMostProducts; ++i)
           cpt::tma_prefetch_map(is_a ? &p.map_a[i] : &p.map_b[i]);
@@ -255,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
           if (last.any) cpt::mbar_wait(full + 8 * k, last.parity, &late);
         }
       }
-    } else if (warp == kSumWarps + 1 && half == 0) {
+    } else if (warp == kMmaWarp && half == 0) {
       // ------------------------------------------------------------- products
       const uint32_t segment = kSegment / kStageK >> p.two;
       uint32_t it = 0, s = 0, parity = 0;
@@ -309,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
         __syncwarp();
         cpt::mbar_wait(drained, 0, &late);
       }
-    } else if (warp == kSumWarps + 3) {
+    } else if (warp == kSumsWarp) {
       // ---------------------------------------------------------- column sums
       if (p.sums.out != nullptr) {
         for (uint32_t c = blockIdx.x * 32 + lane; c < p.sums.n; c += gridDim.x * 32) {
@@ -328,10 +331,10 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
   } else {
     // --------------------------------------------------------------- finish
     if constexpr (kSegments) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFinishRegs));
-    const uint32_t lanes = (warp & 3) * 32, group = warp >> 2;
+    const uint32_t mine = warp - kFirstFinish, lanes = (warp & 3) * 32, group = mine >> 2;
     const DropKey key = cpe::drop_key(p.q[0].e.drop);      // (dropout is in the first product alone)
-    const uint32_t slots = cpt::smem_addr(tiles) + p.slots_at + warp * p.slots;
-    const uint32_t residual_bar = cpt::smem_addr(&residual_bars[warp]);
+    const uint32_t slots = cpt::smem_addr(tiles) + p.slots_at + mine * p.slots;
+    const uint32_t residual_bar = cpt::smem_addr(&residual_bars[mine]);
     uint32_t it = 0, residual_parity = 0;
     bool ok = true, coming = false;            // coming: loads of the residual are under way
     for (uint32_t u = pair; u < p.units && ok; u += pairs) {
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
         for (uint32_t i = 0; i < 2; ++i) {
           const uint32_t c = kGroups * i + group, col = t.col0 + c * 32 + lane;
           if (c < blocks)
-            bias[warp][i][lane] = col < q.e.n ? load_as_f32(q.e.bias, col, q.e.bias_dtype) : 0.0f;
+            bias[mine][i][lane] = col < q.e.n ? load_as_f32(q.e.bias, col, q.e.bias_dtype) : 0.0f;
         }
         __syncwarp();
       }
@@ -380,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
           return;
         }
         const bool fast = q.e.aligned != 0 && col + 32 <= q.e.n;
-        cpe::shape_block<kRich>(q.e, key, row0, col, lane, bias[warp][i], fast, v);
+        cpe::shape_block<kRich>(q.e, key, row0, col, lane, bias[mine][i], fast, v);
         if (!q.tma_out) {
           cpe::write_block(q.e, row0, col, lane, fast, v);
           return;
@@ -463,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
   }
   __syncwarp();
   cpt::cluster_sync();                 // no CTA leaves while the other may use its memory
-  if (warp == kSumWarps + 1) cpt::tmem_free_pair(tmem, 2 * kBuffer);
+  if (warp == kMmaWarp) cpt::tmem_free_pair(tmem, 2 * kBuffer);
 }
 
 // ------------------------------------------------------------- sums of the splits
@@ -829,32 +832,55 @@ bool block_map_ok(const void* p, int dtype, uint64_t m, uint64_t ld) {
   return cpx::aligned(p, 16) && (m == 1 || (ld != 0 && ld * dtype_size(dtype) % 16 == 0));
 }
 
-// Columns of a tile and units that share its k.  By shapes alone, for the 76 pairs of a whole
-// card, so that a product's sums and its workspace are the same wherever it runs.
+// Columns of a tile and units that share its k, of each product of a launch.  By shapes alone, for
+// the 76 pairs of a whole card, so that a product's sums and its workspace are the same wherever it
+// runs.  In nanoseconds, measured at 4096 x 4096 and on a turn of few tiles: 64 of k take 303 at
+// 256 columns, 273 at 224, 204 at 128, 144 at 64 and below; a tile besides them 300 + 6.5 a
+// column; sharing k 4500 and the sums' way to memory and back.  Units are dealt in turn, so the
+// first pair has the most.
 constexpr uint32_t kPairs = 76;
 struct Tiling {
   uint32_t bn, splits;
+  uint64_t units;
+  double each, extra;
 };
-Tiling choose_tiling(uint32_t m, uint32_t n, uint32_t k) {
+Tiling best_splits(uint32_t m, uint32_t n, uint32_t k, uint32_t bn) {
   const uint32_t kblocks = (k + kStageK - 1) / kStageK;
-  const uint64_t tiles_m = (static_cast<uint64_t>(m) + 255) / 256;
-  Tiling best{32, 1};
-  double least = 1e300;
-  for (uint32_t s = 1; s <= 32 && s <= (kblocks + 3) / 4; ++s) {
-    for (uint32_t bn = 256; bn >= 32; bn -= 32) {
-      const uint64_t units = tiles_m * ((static_cast<uint64_t>(n) + bn - 1) / bn) * s;
-      if (s > 1 && units > 2 * kPairs) continue;
-      const double turns = static_cast<double>((units + kPairs - 1) / kPairs);
-      const double stage = bn <= 128 ? 190.0 : 1.5 * bn;
-      double cost = turns * ((kblocks + s - 1) / s * stage + 400.0) + 8.0 * bn;
-      if (s > 1) cost += 3000.0 + 8e-4 * s * m * static_cast<double>(n);
-      if (cost < least) {
-        least = cost;
-        best = Tiling{bn, s};
-      }
+  const uint64_t tiles = (static_cast<uint64_t>(m) + 255) / 256 * ((static_cast<uint64_t>(n) + bn - 1) / bn);
+  const double stage = bn <= 80 ? 140.0 : 60.0 + 0.95 * bn;
+  Tiling best{};
+  double least = 0.0;
+  for (uint32_t s : {1u, 2u, 3u, 4u, 6u, 8u, 12u, 16u, 24u, 32u}) {
+    if (s > 1 && (tiles * s > 2 * kPairs || 4 * s > kblocks)) break;
+    Tiling t{bn, s, tiles * s, (kblocks + s - 1) / s * stage + 300.0 + 6.5 * bn, 0.0};
+    if (s > 1) t.extra = 4500.0 + (s + 1) * 4.0 * m * static_cast<double>(n) / 3000.0;
+    const double cost = static_cast<double>((t.units + kPairs - 1) / kPairs) * t.each + t.extra;
+    if (s == 1 || cost < least) {
+      least = cost;
+      best = t;
     }
   }
   return best;
+}
+void choose_tilings(const uint32_t* m, const uint32_t* n, const uint32_t* k, int count,
+                    Tiling* out) {
+  Tiling t[kMostProducts][8] = {};
+  for (int i = 0; i < count; ++i)
+    for (uint32_t b = 0; b < 8; ++b) t[i][b] = best_splits(m[i], n[i], k[i], 256 - 32 * b);
+  double least = 1e300;
+  for (uint32_t a = 0; a < 8; ++a) {
+    for (uint32_t b = 0; b < (count > 1 ? 8 : 1); ++b) {
+      const Tiling &x = t[0][a], &y = t[1][b];
+      const uint64_t first = (x.units + kPairs - 1) / kPairs;
+      const uint64_t all = (x.units + y.units + kPairs - 1) / kPairs;
+      const double cost = first * x.each + (all - first) * y.each + (x.extra > y.extra ? x.extra : y.extra);
+      if (cost < least) {
+        least = cost;
+        out[0] = x;
+        if (count > 1) out[1] = y;
+      }
+    }
+  }
 }
 uint64_t part_pitch(uint32_t n) { return (static_cast<uint64_t>(n) + 31) / 32 * 32; }
 
@@ -871,13 +897,12 @@ cp_status too_many_tiles() {
 
 namespace cplin {
 
-uint64_t part_floats(const uint32_t (&m)[kMostProducts], const uint32_t (&n)[kMostProducts],
-                     const uint32_t (&k)[kMostProducts], int count) {
+uint64_t part_floats(const uint32_t* m, const uint32_t* n, const uint32_t* k, int count) {
+  Tiling t[kMostProducts];
+  choose_tilings(m, n, k, count, t);
   uint64_t floats = 0;
-  for (int i = 0; i < count; ++i) {
-    const Tiling t = choose_tiling(m[i], n[i], k[i]);
-    if (t.splits > 1) floats += static_cast<uint64_t>(t.splits) * m[i] * part_pitch(n[i]);
-  }
+  for (int i = 0; i < count; ++i)
+    if (t[i].splits > 1) floats += static_cast<uint64_t>(t[i].splits) * m[i] * part_pitch(n[i]);
   return floats;
 }
 
@@ -890,8 +915,17 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
   FinishParams f{};
   bool is_rich = false, segments = false, finish = false;
   uint64_t units[kMostProducts] = {};
-  uint32_t ks[kMostProducts] = {};
+  uint32_t ms[kMostProducts] = {}, ns[kMostProducts] = {}, ks[kMostProducts] = {};
   int used = 0;
+  for (int i = 0; i < count; ++i) {
+    if (q[i].e.m == 0 || q[i].e.n == 0 || q[i].k == 0) continue;
+    ms[used] = q[i].e.m;
+    ns[used] = q[i].e.n;
+    ks[used++] = q[i].k;
+  }
+  Tiling tilings[kMostProducts] = {};
+  if (used > 0) choose_tilings(ms, ns, ks, used, tilings);
+  used = 0;
   for (int i = 0; i < count; ++i) {
     const Epilogue& ep = q[i].e;
     if (ep.m == 0 || ep.n == 0) continue;
@@ -905,7 +939,7 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
       continue;
     }
     PairProduct& x = p.q[used];
-    const Tiling t = choose_tiling(ep.m, ep.n, q[i].k);
+    const Tiling& t = tilings[used];
     x.e = ep;
     x.bn = t.bn;
     x.splits = t.splits;
@@ -921,7 +955,6 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
     x.b_bytes = x.b_across ? x.b_boxes * kBlock : t.bn / 2 * 128;
     x.instr = cpt::half_instr_desc(256, t.bn, q[i].dtype == CP_BF16, x.a_across, x.b_across);
     segments |= ep.out_dtype == CP_F32 && q[i].k / t.splits > kSegment;
-    ks[used] = q[i].k;
     if (t.splits > 1) {
       x.pitch = part_pitch(ep.n);
       x.part = part;
