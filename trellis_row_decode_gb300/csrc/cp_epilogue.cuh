@@ -92,18 +92,19 @@ __device__ __forceinline__ void drop_quad(const DropParams& p, const DropKey& ke
   drop_quad(p, key, round_keys(key), quad, row, v);
 }
 
-// Sixteen columns of a row, 4 * quad on: four calls of the generator side by side, so that its
-// chains of products overlap and a round's key is made once for all.
-__device__ __forceinline__ void drop16(const DropParams& p, const DropKey& key, uint32_t quad,
+// Columns of a row, 4 * quad on, kQuads calls of the generator side by side, so that its chains of
+// products overlap and a round's key is made once for all.
+template <uint32_t kQuads>
+__device__ __forceinline__ void drop_quads(const DropParams& p, const DropKey& key, uint32_t quad,
                                        uint32_t row, float* v) {
   if (p.mode == 2) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+    for (int i = 0; i < 4 * static_cast<int>(kQuads); ++i) v[i] = 0.0f;
     return;
   }
-  uint32_t c0[4], c1[4], c2[4], c3[4], k0 = key.k0, k1 = key.k1;
+  uint32_t c0[kQuads], c1[kQuads], c2[kQuads], c3[kQuads], k0 = key.k0, k1 = key.k1;
 #pragma unroll
-  for (uint32_t q = 0; q < 4; ++q) {
+  for (uint32_t q = 0; q < kQuads; ++q) {
     c0[q] = quad + q;
     c1[q] = row;
     c2[q] = key.o0;
@@ -112,7 +113,7 @@ __device__ __forceinline__ void drop16(const DropParams& p, const DropKey& key, 
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
 #pragma unroll
-    for (uint32_t q = 0; q < 4; ++q) {
+    for (uint32_t q = 0; q < kQuads; ++q) {
       const uint64_t a = static_cast<uint64_t>(c0[q]) * 0xD2511F53u;
       const uint64_t b = static_cast<uint64_t>(c2[q]) * 0xCD9E8D57u;
       c0[q] = static_cast<uint32_t>(b >> 32) ^ c1[q] ^ k0;
@@ -124,7 +125,7 @@ __device__ __forceinline__ void drop16(const DropParams& p, const DropKey& key, 
     k1 += 0xBB67AE85u;
   }
 #pragma unroll
-  for (uint32_t q = 0; q < 4; ++q) {
+  for (uint32_t q = 0; q < kQuads; ++q) {
     v[4 * q] = c0[q] <= p.last ? v[4 * q] * p.scale : 0.0f;
     v[4 * q + 1] = c1[q] <= p.last ? v[4 * q + 1] * p.scale : 0.0f;
     v[4 * q + 2] = c2[q] <= p.last ? v[4 * q + 2] * p.scale : 0.0f;
@@ -148,14 +149,26 @@ inline bool drop_params(DropParams* d, double p, uint64_t seed, uint64_t offset,
 
 // ------------------------------------------------------------------ activations
 //
-// In fp32 from library functions.  sigmoid(t) = 1 / (1 + e^-t); the tanh form of gelu is
-// z sigmoid(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3), since (1 + tanh u) / 2 = sigmoid(2 u).
+// In fp32.  sigmoid(t) = 1 / (1 + 2^(-t log2 e)), by the approximate exponential and reciprocal: an
+// error of the exponent's argument, |t| 2^-24 relative, reaches the sigmoid times 1 - sigmoid, and is
+// below 2^-25 for every t > -20 or so and relative to a value below 2^-28 beyond; with the two
+// instructions' own errors 2^-22.  The tanh form of gelu is z sigmoid(2 u),
+// u = sqrt(2 / pi) (z + 0.044715 z^3), since (1 + tanh u) / 2 = sigmoid(2 u).
 
 constexpr float kTanhScale = 1.5957691216057308f;      // 2 sqrt(2 / pi)
 constexpr float kTanhCube = 0.044715f;
+constexpr float kLog2E = 1.4426950408889634f;
 
-// The quotient is exact to 2 units in the last place, and 0 where e^-t overflows.
-__device__ __forceinline__ float sigmoid(float t) { return __fdividef(1.0f, 1.0f + expf(-t)); }
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float sigmoid(float t) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp2_approx(-kLog2E * t)));
+  return r;
+}
 
 template <int kAct>
 __device__ __forceinline__ float act(float z) {
@@ -177,7 +190,7 @@ __device__ __forceinline__ float slope(float z) {
   }
   if constexpr (kAct == CP_ACT_GELU)
     return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
-           z * 0.39894228040143268f * expf(-0.5f * z * z);
+           z * 0.39894228040143268f * exp2_approx(-0.5f * kLog2E * z * z);
   if constexpr (kAct == CP_ACT_GELU_TANH) {
     const float s = sigmoid(kTanhScale * (z + kTanhCube * z * z * z));
     const float bend = s * (1.0f - s);                 // 0 far out, where z^2 may overflow
@@ -411,8 +424,8 @@ __device__ __forceinline__ void shape_block(const Epilogue& e, const DropKey& ke
       for (int i = 0; i < 32; ++i) v[i] = act<decltype(tag)::value>(v[i]);
     });
     if (e.drop.mode != 0) {
-      drop16(e.drop, key, col / 4, row, v);
-      drop16(e.drop, key, col / 4 + 4, row, v + 16);
+      drop_quads<4>(e.drop, key, col / 4, row, v);
+      drop_quads<4>(e.drop, key, col / 4 + 4, row, v + 16);
     }
   }
 }

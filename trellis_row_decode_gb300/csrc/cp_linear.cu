@@ -31,7 +31,10 @@ using cplin::Product;
 constexpr int kGradThreads = 256;
 constexpr uint32_t kGradColumns = 256;
 constexpr uint32_t kMostParts = 64;
-constexpr uint32_t kGradAhead = 4;         // rows whose loads a thread has in flight
+// Rows whose loads a thread has in flight, CTAs of an SM (by registers: slopes and the generator
+// take more).
+constexpr uint32_t grad_ahead(bool shape) { return shape ? 2 : 4; }
+constexpr uint32_t grad_ctas(bool shape) { return shape ? 3 : 4; }
 
 struct GradParams {
   const void* dy;
@@ -44,8 +47,11 @@ struct GradParams {
   DropParams drop;
 };
 
-template <typename T, typename D, bool VEC>
-__global__ void __launch_bounds__(kGradThreads) dz_kernel(const GradParams p) {
+// kShape: there is an activation or dropout.
+template <typename T, typename D, bool VEC, bool kShape>
+__global__ void __launch_bounds__(kGradThreads, grad_ctas(kShape))
+    dz_kernel(const __grid_constant__ GradParams p) {
+  constexpr uint32_t kAhead = grad_ahead(kShape);
   __shared__ float sums[8][kGradColumns];
   wait_for_previous();
   let_next_start();
@@ -57,35 +63,34 @@ __global__ void __launch_bounds__(kGradThreads) dz_kernel(const GradParams p) {
   const DropKey key = cpe::drop_key(p.drop);
   float acc[8] = {};
   if (8ull * o < p.n) {
-    for (uint32_t r = r0 + line; r < r1; r += 8 * kGradAhead) {
-      Packed<D> dy[kGradAhead];
-      Packed<T> pre[kGradAhead];
+    for (uint32_t r = r0 + line; r < r1; r += 8 * kAhead) {
+      Packed<D> dy[kAhead];
+      Packed<T> pre[kAhead];
 #pragma unroll
-      for (uint32_t i = 0; i < kGradAhead; ++i) {
+      for (uint32_t i = 0; i < kAhead; ++i) {
         const uint32_t row = r + 8 * i;
         if (row < r1) {
           dy[i] = load_row_octet<D, VEC>(static_cast<const D*>(p.dy) + row * p.ldy, o, p.n);
-          if (p.act != CP_ACT_NONE)
+          if (kShape && p.act != CP_ACT_NONE)
             pre[i] = load_row_octet<T, VEC>(static_cast<const T*>(p.pre) + row * p.ldp, o, p.n);
         }
       }
 #pragma unroll
-      for (uint32_t i = 0; i < kGradAhead; ++i) {
+      for (uint32_t i = 0; i < kAhead; ++i) {
         const uint32_t row = r + 8 * i;
         if (row < r1) {
           float v[8];
           unpack(dy[i], v);
-          if (p.drop.mode != 0) {
-            cpe::drop_quad(p.drop, key, 2 * o, row, v);
-            cpe::drop_quad(p.drop, key, 2 * o + 1, row, v + 4);
-          }
-          if (p.act != CP_ACT_NONE) {
-            float z[8];
-            unpack(pre[i], z);
-            cpe::with_act(p.act, [&](auto tag) {
+          if constexpr (kShape) {
+            if (p.act != CP_ACT_NONE) {
+              float z[8];
+              unpack(pre[i], z);
+              cpe::with_act(p.act, [&](auto tag) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] *= cpe::slope<decltype(tag)::value>(z[e]);
-            });
+                for (int e = 0; e < 8; ++e) v[e] *= cpe::slope<decltype(tag)::value>(z[e]);
+              });
+            }
+            if (p.drop.mode != 0) cpe::drop_quads<2>(p.drop, key, 2 * o, row, v);
           }
           if (p.dz != nullptr)       // (rows on 16-byte boundaries; what lies behind n is not read)
             store_octet(static_cast<T*>(p.dz) + row * p.pitch + 8ull * o, pack<T>(v));
@@ -108,17 +113,22 @@ __global__ void __launch_bounds__(kGradThreads) dz_kernel(const GradParams p) {
   }
 }
 
-// Shares of the rows: about six CTAs an SM, and few enough parts for the products' kernel to add.
-uint32_t grad_parts(uint64_t m, uint64_t n) {
+// Shares of the rows: CTAs that all run at once, and few enough parts for the products' kernel to
+// add.
+uint32_t grad_parts(uint64_t m, uint64_t n, bool shape) {
   const uint64_t wide = (n + kGradColumns - 1) / kGradColumns;
-  const uint64_t want = std::max<uint64_t>(1, 152 * 6 / std::max<uint64_t>(wide, 1));
+  const uint64_t want = std::max<uint64_t>(1, 152 * grad_ctas(shape) / std::max<uint64_t>(wide, 1));
   return static_cast<uint32_t>(std::min({want, (m + 7) / 8, static_cast<uint64_t>(kMostParts)}));
 }
 
 template <typename T, typename D>
 cudaError_t launch_dz(const GradParams& p, bool vec, cudaStream_t s) {
   const Launch l{dim3((p.n + kGradColumns - 1) / kGradColumns, p.count), kGradThreads, 0, s};
-  return vec ? launch(l, &dz_kernel<T, D, true>, p) : launch(l, &dz_kernel<T, D, false>, p);
+  if (p.act != CP_ACT_NONE || p.drop.mode != 0)
+    return vec ? launch(l, &dz_kernel<T, D, true, true>, p)
+               : launch(l, &dz_kernel<T, D, false, true>, p);
+  return vec ? launch(l, &dz_kernel<T, D, true, false>, p)
+             : launch(l, &dz_kernel<T, D, false, false>, p);
 }
 
 // ---------------------------------------------------------------------------- host
@@ -241,7 +251,7 @@ extern "C" uint64_t cp_linear_grad_workspace_bytes(uint64_t m, uint64_t n, uint6
   if (m >= kMostK || n >= kMostK || k >= kMostK) return 0;
   // dz, copies of x and w, the parts of db, the sums of products whose k is split
   const uint64_t dz = 2 * m * row_pitch(n), copies = 2 * (m + n) * row_pitch(k);
-  const uint64_t db = 4ull * grad_parts(m, n) * row_pitch(n);
+  const uint64_t db = 4ull * grad_parts(m, n, false) * row_pitch(n);
   uint64_t parts = 0;
   if (m != 0 && n != 0 && k != 0) {
     const uint32_t ms[2] = {static_cast<uint32_t>(m), static_cast<uint32_t>(n)};
@@ -292,19 +302,19 @@ extern "C" cp_status cp_linear_grad(const void* dy, int dy_dtype, uint64_t dy_st
   // dz, where it is not dy on 16-byte boundaries already, and the parts of db
   Operand dz{dy, dy_stride, false};
   const bool has_dy = m != 0 && n != 0;
-  const bool as_is = activation == CP_ACT_NONE && g.drop.mode == 0 && dy_dtype == dtype &&
-                     rows_ok(dy, dy_stride, m);
+  const bool shape = activation != CP_ACT_NONE || g.drop.mode != 0;
+  const bool as_is = !shape && dy_dtype == dtype && rows_ok(dy, dy_stride, m);
   g.pitch = row_pitch(n);
   if (!as_is) dz = Operand{at, g.pitch, false};
   g.dz = as_is || (!want_dx && !want_dw) ? nullptr : at;
   at += 2 * m * g.pitch;
   ColumnSums sums{};
   if (db != nullptr && n != 0) {
-    sums = ColumnSums{reinterpret_cast<float*>(at), db, g.pitch, has_dy ? grad_parts(m, n) : 0,
+    sums = ColumnSums{reinterpret_cast<float*>(at), db, g.pitch, has_dy ? grad_parts(m, n, shape) : 0,
                       static_cast<uint32_t>(n), db_dtype, accumulate};
     g.parts = reinterpret_cast<float*>(at);
   }
-  at += 4ull * grad_parts(m, n) * g.pitch;
+  at += 4ull * grad_parts(m, n, false) * g.pitch;
   cudaError_t e = cudaSuccess;
   if (has_dy && (g.dz != nullptr || g.parts != nullptr)) {
     g.dy = dy;
@@ -313,7 +323,7 @@ extern "C" cp_status cp_linear_grad(const void* dy, int dy_dtype, uint64_t dy_st
     g.ldp = pre_stride;
     g.m = static_cast<uint32_t>(m);
     g.n = static_cast<uint32_t>(n);
-    g.count = grad_parts(m, n);
+    g.count = grad_parts(m, n, shape);
     g.act = activation;
     const bool vec = octets_ok(dy, dy_stride, g.n, dtype_size(dy_dtype)) &&
                      (pre == nullptr || octets_ok(pre, pre_stride, g.n, 2));

@@ -68,7 +68,7 @@ def _lib():
 def _device(t: torch.Tensor, name: str) -> int:
     """The index of t's device, which has to be the current one."""
     dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != torch._C._cuda_getDevice():     # (t lies on a GPU: CUDA is set up)
         raise ValueError(f"{name} must be on the current CUDA device")
     return dev
 
@@ -112,7 +112,10 @@ def _u32(value: int, name: str) -> int:
 
 def _rows(t: torch.Tensor, name: str) -> tuple[int, int, int]:
     """(rows, d, row stride) of t with its leading dimensions merged (as a view)."""
-    shape, strides = t.shape, t.stride()
+    shape = t.shape
+    if len(shape) == 2 and t.is_contiguous() and not shape[1] >> 32:       # the common case
+        return shape[0], shape[1], shape[1]
+    strides = t.stride()
     if len(shape) == 0:
         raise ValueError(f"{name} must have at least one dimension")
     if shape[-1] >> 32:

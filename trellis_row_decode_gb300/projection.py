@@ -17,7 +17,7 @@ import torch
 
 from . import CP_ERR_INVALID_ARG, CPError, _check
 from . import layer as _layer
-from .layer import (CP_BF16, CP_F16, _check_out, _device, _empty, _float, _on, _rows, _stream,
+from .layer import (CP_BF16, CP_F16, CP_F32, _check_out, _device, _empty, _float, _on, _rows, _stream,
                     _workspace)
 
 __all__ = ["ACTIVATIONS", "linear", "linear_workspace", "linear_grad", "linear_grad_workspace",
@@ -66,14 +66,10 @@ def _activation(name: str) -> int:
     return code
 
 
-def _u64(value: int, name: str) -> int:
-    """A whole number of 64 bits: ctypes would cut a larger one without a word."""
-    if not 0 <= value < 1 << 64:
-        raise ValueError(f"{name} must be at least 0 and below 2^64")
-    return value
-
-
-def _rng(rng, dev: int):
+def _rng(seed: int, offset: int, rng, dev: int):
+    """rng's address, and seed and offset checked: ctypes would cut larger ones without a word."""
+    if (seed | offset) >> 64:                     # (a negative one too: its sign stays)
+        raise ValueError("seed and offset must be at least 0 and below 2^64")
     if rng is None:
         return None
     if rng.dtype != torch.int64 or rng.numel() != 2 or not rng.is_contiguous():
@@ -101,13 +97,13 @@ def dropout(x: torch.Tensor, p: float, seed: int = 0, offset: int = 0,
             raise ValueError("residual must have x's type and shape")
         rs = _rows(residual, "residual")[2]
         rp = _on(residual, dev, "residual")
+    gp = _rng(seed, offset, rng, dev)
     if out is None:
         out, ldo = _empty(x.shape, x.dtype, x, stream), d
     else:
         ldo = _check_out(out, x.shape, x.dtype, dev, "out")
-    _check(_lib().cp_dropout(x.data_ptr(), xs, rp, rs, code, rows, d, p, _u64(seed, "seed"),
-                             _u64(offset, "offset"), _rng(rng, dev), out.data_ptr(), ldo,
-                             _stream(stream, dev)), "cp_dropout")
+    _check(_lib().cp_dropout(x.data_ptr(), xs, rp, rs, code, rows, d, p, seed, offset, gp,
+                             out.data_ptr(), ldo, _stream(stream, dev)), "cp_dropout")
     return out
 
 
@@ -177,15 +173,18 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
         else:
             ps = _check_out(pre, shape, x.dtype, dev, "pre")
         pp = pre.data_ptr()
+    gp = _rng(seed, offset, rng, dev)
     L = _lib()
-    xp, wp, ws = x.data_ptr(), _on(weight, dev, "weight"), None
-    nbytes = L.cp_linear_workspace_bytes(xp, ldx, wp, ldw, m, n, k)
-    if nbytes:
-        ws = _workspace(workspace, nbytes, x, dev, stream)
-    _check(L.cp_linear(xp, ldx, wp, ldw, code, m, n, k, bp, bcode, act, p, _u64(seed, "seed"),
-                       _u64(offset, "offset"), _rng(rng, dev), rp, rs, out.data_ptr(), ocode, ldo,
-                       pp, ps, None if ws is None else ws.data_ptr(),
-                       0 if ws is None else ws.numel(), _stream(stream, dev)), "cp_linear")
+    xp, wp, sp, nbytes = x.data_ptr(), _on(weight, dev, "weight"), None, 0
+    # (few rows on 16-byte boundaries, the form for single tokens, need none)
+    if m > 128 or (xp | wp | 2 * (ldx | ldw)) & 15 or not ldx or not ldw:
+        nbytes = L.cp_linear_workspace_bytes(xp, ldx, wp, ldw, m, n, k)
+        if nbytes:
+            workspace = _workspace(workspace, nbytes, x, dev, stream)
+            sp = workspace.data_ptr()
+    _check(L.cp_linear(xp, ldx, wp, ldw, code, m, n, k, bp, bcode, act, p, seed, offset, gp, rp, rs,
+                       out.data_ptr(), ocode, ldo, pp, ps, sp, nbytes, _stream(stream, dev)),
+           "cp_linear")
     return (out, pre) if keep else out
 
 
@@ -262,13 +261,15 @@ def linear_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, activat
         dbp, dbc = db.data_ptr(), _float(db.dtype, "db")
     elif db is not None:
         raise ValueError("db is given, but not needed")
+    gp = _rng(seed, offset, rng, dev)
     L = _lib()
-    ws = _workspace(workspace, L.cp_linear_grad_workspace_bytes(m, n, k), x, dev, stream)
-    _check(L.cp_linear_grad(_on(dy, dev, "dy"), _float(dy.dtype, "dy"), lddy, x.data_ptr(), ldx,
-                            _on(weight, dev, "weight"), ldw, code, pp, ps, m, n, k, act, p,
-                            _u64(seed, "seed"), _u64(offset, "offset"), _rng(rng, dev),
-                            1 if accumulate else 0, dxp, dxs, dwp, dwc, dws, dbp, dbc,
-                            ws.data_ptr(), ws.numel(), _stream(stream, dev)), "cp_linear_grad")
+    nbytes = L.cp_linear_grad_workspace_bytes(m, n, k)
+    ws = _workspace(workspace, nbytes, x, dev, stream)
+    _check(L.cp_linear_grad(_on(dy, dev, "dy"), code if dy.dtype == x.dtype else CP_F32, lddy,
+                            x.data_ptr(), ldx, _on(weight, dev, "weight"), ldw, code, pp, ps, m, n,
+                            k, act, p, seed, offset, gp, 1 if accumulate else 0, dxp, dxs, dwp, dwc,
+                            dws, dbp, dbc, ws.data_ptr(), nbytes, _stream(stream, dev)),
+           "cp_linear_grad")
     return dx, dw, db
 
 
