@@ -2,6 +2,7 @@
 // (tcgen05), for operands whose rows lie on 16-byte boundaries (include/cp.h).
 //
 //   out[i][j] = epilogue(sum over k of a[i][k] b[j][k])
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 #include <mutex>
@@ -870,14 +871,17 @@ void choose_tilings(const uint32_t* m, const uint32_t* n, const uint32_t* k, int
   double least = 1e300;
   for (uint32_t a = 0; a < 8; ++a) {
     for (uint32_t b = 0; b < (count > 1 ? 8 : 1); ++b) {
-      const Tiling &x = t[0][a], &y = t[1][b];
+      const bool swap = t[1][b].each > t[0][a].each;       // (the longer units go first)
+      const Tiling &x = swap ? t[1][b] : t[0][a], &y = swap ? t[0][a] : t[1][b];
       const uint64_t first = (x.units + kPairs - 1) / kPairs;
       const uint64_t all = (x.units + y.units + kPairs - 1) / kPairs;
-      const double cost = first * x.each + (all - first) * y.each + (x.extra > y.extra ? x.extra : y.extra);
+      const double even = (x.units * x.each + y.units * y.each) / kPairs;
+      const double cost = std::max(first * x.each + (all - first) * y.each, even) +
+                          std::max(x.extra, y.extra);
       if (cost < least) {
         least = cost;
-        out[0] = x;
-        if (count > 1) out[1] = y;
+        out[0] = t[0][a];
+        if (count > 1) out[1] = t[1][b];
       }
     }
   }
@@ -925,6 +929,8 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
   }
   Tiling tilings[kMostProducts] = {};
   if (used > 0) choose_tilings(ms, ns, ks, used, tilings);
+  // units are dealt in turn: the longer ones first
+  const bool swap = used == 2 && tilings[1].each > tilings[0].each;
   used = 0;
   for (int i = 0; i < count; ++i) {
     const Epilogue& ep = q[i].e;
@@ -938,7 +944,8 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
       (i == 0 ? f.first : f.total) += quads * ep.m;
       continue;
     }
-    PairProduct& x = p.q[used];
+    const int at = swap ? 1 - used : used;
+    PairProduct& x = p.q[at];
     const Tiling& t = tilings[used];
     x.e = ep;
     x.bn = t.bn;
@@ -946,8 +953,8 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
     x.tiles_m = (ep.m + 255) / 256;
     x.tiles_n = (ep.n + t.bn - 1) / t.bn;
     const uint64_t tiles = static_cast<uint64_t>(x.tiles_m) * x.tiles_n;
-    units[used] = tiles * t.splits;
-    if (units[used] >= (1ull << 31)) return too_many_tiles();
+    units[at] = tiles * t.splits;
+    if (units[at] >= (1ull << 31)) return too_many_tiles();
     x.tiles = static_cast<uint32_t>(tiles);
     x.a_across = q[i].a.across;
     x.b_across = q[i].b.across;
@@ -969,10 +976,10 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
     }
     const Operand &a = q[i].a, &b = q[i].b;
     const bool ok =
-        (a.across ? encode_map(&p.map_a[used], a.p, ep.m, q[i].k, a.ld, kStageK)
-                  : encode_map(&p.map_a[used], a.p, q[i].k, ep.m, a.ld, 128)) &&
-        (b.across ? encode_map(&p.map_b[used], b.p, ep.n, q[i].k, b.ld, kStageK)
-                  : encode_map(&p.map_b[used], b.p, q[i].k, ep.n, b.ld, t.bn / 2));
+        (a.across ? encode_map(&p.map_a[at], a.p, ep.m, q[i].k, a.ld, kStageK)
+                  : encode_map(&p.map_a[at], a.p, q[i].k, ep.m, a.ld, 128)) &&
+        (b.across ? encode_map(&p.map_b[at], b.p, ep.n, q[i].k, b.ld, kStageK)
+                  : encode_map(&p.map_b[at], b.p, q[i].k, ep.n, b.ld, t.bn / 2));
     if (!ok) {
       cpx::set_error("tensor map refused");
       return CP_ERR_CUDA;
@@ -987,9 +994,9 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
                 (ep.pre == nullptr || whole);
     x.tma_residual = x.tma_out && ep.residual != nullptr && !f32;
     if ((x.tma_out &&
-         !encode_block_map(&p.map_out[used], ep.out, ep.out_dtype, ep.n, ep.m, ep.ldo)) ||
+         !encode_block_map(&p.map_out[at], ep.out, ep.out_dtype, ep.n, ep.m, ep.ldo)) ||
         (x.tma_residual &&
-         !encode_block_map(&p.map_residual[used], ep.residual, ep.out_dtype, ep.n, ep.m, ep.ldr))) {
+         !encode_block_map(&p.map_residual[at], ep.residual, ep.out_dtype, ep.n, ep.m, ep.ldr))) {
       cpx::set_error("tensor map refused");
       return CP_ERR_CUDA;
     }
@@ -1012,7 +1019,7 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
     p.stages = min((kSmemMost - 1024 - kSumWarps * p.slots) / p.stage_bytes, kMaxStages);
     p.slots_at = p.stages * p.stage_bytes;
     for (int i = 0; i < used; ++i)
-      p.q[i].kblocks = (ks[i] + (kStageK << p.two) - 1) / (kStageK << p.two);
+      p.q[swap ? 1 - i : i].kblocks = (ks[i] + (kStageK << p.two) - 1) / (kStageK << p.two);
     uint32_t pairs = p.units;
     if (sums.out != nullptr) pairs = max(pairs, (sums.n + 63) / 64);
     pairs = min(pairs, static_cast<uint32_t>(d->pairs));
