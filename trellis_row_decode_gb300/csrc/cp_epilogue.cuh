@@ -381,24 +381,18 @@ __device__ __forceinline__ void transpose32(float (&x)[32], uint32_t lane) {
 }
 
 // The epilogue of a warp's 32 rows (row0 on, one a lane) by 32 columns (col on, a multiple of 32)
-// of sums, in two steps.  The first: bias, kept sums, activation, dropout.  `bias`: the columns'
-// bias in shared memory.  fast: rows on 32-byte boundaries and columns all there, so a lane reads
+// of sums, in two steps.  The first: bias, kept sums, activation, dropout.  `bias`: a lane has that
+// of column col + lane.  fast: rows on 32-byte boundaries and columns all there, so a lane reads
 // and writes its own row, whole sectors; else the block is transposed, so that each access is of
 // 32 neighbours of one row.
 template <bool kRich>
 __device__ __forceinline__ void shape_block(const Epilogue& e, const DropKey& key, uint32_t row0,
-                                            uint32_t col, uint32_t lane, const float* bias,
+                                            uint32_t col, uint32_t lane, float bias,
                                             bool fast, float (&v)[32]) {
   const uint32_t row = row0 + lane;
   if (e.bias != nullptr) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float4 b = *reinterpret_cast<const float4*>(bias + 4 * i);
-      v[4 * i] += b.x;
-      v[4 * i + 1] += b.y;
-      v[4 * i + 2] += b.z;
-      v[4 * i + 3] += b.w;
-    }
+    for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xFFFFFFFFu, bias, i);
   }
   if constexpr (kRich) {
     if (e.pre != nullptr) {

@@ -45,15 +45,15 @@ __device__ uint32_t g_linear_gave_up;
 
 constexpr int kSumWarps = 16;
 constexpr uint32_t kGroups = kSumWarps / 4;            // of four warps, one for each 32 lanes
-// The issuing warps come first: where a scheduler has several ready warps the older one goes, and
-// the tensor core waits for these (4096 x 4096 x 1024 with everything: FIGURE).
 constexpr uint32_t kLoadA = 0, kMmaWarp = 1, kLoadB = 2, kSumsWarp = 3, kFirstFinish = 4;
 constexpr int kThreads = (kFirstFinish + kSumWarps) * 32;
 constexpr uint32_t kStageK = 64;                       // of k in a stage, or a part of it: 128 bytes
 constexpr uint32_t kMaxStages = 8;
 constexpr uint32_t kTileA = 128 * 128;                 // bytes of a's rows per stage and CTA
 constexpr uint32_t kBlock = 64 * 128;                  // bytes of a 64 x 64 block stored across k
-constexpr uint32_t kSmemMost = 220 * 1024;             // dynamic shared memory of a CTA
+constexpr uint32_t kSmemUsed = 225 * 1024;             // dynamic shared memory of a CTA
+constexpr uint32_t kSmemMost = kSmemUsed + 1023;       // (and what it takes to start on 1024 bytes)
+constexpr uint32_t kQuickK = 512;                      // k up to here: two slots a warp for residuals
 constexpr uint32_t kTwoBytes = 24 * 1024;              // stages up to here hold two parts
 constexpr uint32_t kBuffer = 256;                      // columns of tensor memory of a buffer
 constexpr uint32_t kSegment = 512;                     // of k that the tensor core adds up alone
@@ -104,16 +104,16 @@ __device__ __forceinline__ Unit unit_of(const PairParams& p, uint32_t u) {
   return r;
 }
 
-// A block of 32 x 32 outputs in its slot, as the tensor map of 32 columns lays it out: rows of 64
-// bytes with the 64-byte swizzle, or of 128 (fp32) with the 128-byte one; a lane has a row.  `add`:
-// the residual's block lies there already.
-constexpr uint32_t kSlot = 32 * 64, kSlotF32 = 32 * 128;
+// 32 rows of 64 bytes of outputs (32 columns of 16 bits, the first 16 of v in 32 bits) in a slot, as
+// a tensor map with the 64-byte swizzle lays them out; a lane has a row.  `add`: the residual's
+// block lies there already.
+constexpr uint32_t kSlot = 32 * 64;
 __device__ __forceinline__ void write_slot(uint32_t slot, uint32_t lane, int dtype, bool add,
                                            float (&v)[32]) {
   if (dtype == CP_F32) {
 #pragma unroll
-    for (uint32_t c = 0; c < 8; ++c)
-      cpt::store_shared4(slot + lane * 128 + ((c ^ (lane & 7)) << 4), __float_as_uint(v[4 * c]),
+    for (uint32_t c = 0; c < 4; ++c)
+      cpt::store_shared4(slot + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), __float_as_uint(v[4 * c]),
                          __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
                          __float_as_uint(v[4 * c + 3]));
     return;
@@ -146,7 +146,6 @@ template <bool kRich, bool kSegments>
 __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constant__ PairParams p) {
   extern __shared__ uint8_t dyn[];
   __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5];
-  __shared__ __align__(16) float bias[kSumWarps][2][32];
   __shared__ __align__(8) uint64_t residual_bars[kSumWarps];
   __shared__ uint32_t tmem_base;
   __shared__ uint32_t issued[2];           // this CTA's fills of stages, by either issuer
@@ -344,29 +343,30 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
       const uint32_t blocks = q.bn / 32;
       const uint32_t row0 = t.row0 + half * 128 + lanes;
       const bool raw = q.splits > 1;
+      float bias[2] = {};                      // of this lane's columns
       if (q.e.bias != nullptr && !raw) {
 #pragma unroll
         for (uint32_t i = 0; i < 2; ++i) {
           const uint32_t c = kGroups * i + group, col = t.col0 + c * 32 + lane;
-          if (c < blocks)
-            bias[mine][i][lane] = col < q.e.n ? load_as_f32(q.e.bias, col, q.e.bias_dtype) : 0.0f;
+          if (c < blocks && col < q.e.n) bias[i] = load_as_f32(q.e.bias, col, q.e.bias_dtype);
         }
-        __syncwarp();
       }
       uint32_t left = 0;                       // blocks of this warp that have outputs
       if (row0 < q.e.m)
         for (uint32_t c = group; c < blocks && t.col0 + 32 * c < q.e.n; c += kGroups) ++left;
-      if (q.tma_residual && left != 0) {       // a slot for each block, free since the tile before
+      auto load_residual = [&](uint32_t i, uint32_t count) {   // of blocks i on, slots are free
         if (lane == 0) {
           cpt::stores_read();
-          cpt::mbar_expect(residual_bar, left * kSlot);
-          for (uint32_t i = 0; i < left; ++i)
-            cpt::tma_load(slots + i * kSlot, &p.map_residual[t.which],
-                          t.col0 + 32 * (kGroups * i + group), row0, residual_bar);
+          cpt::mbar_expect(residual_bar, count * kSlot);
+          for (uint32_t j = 0; j < count; ++j)
+            cpt::tma_load(slots + j * kSlot, &p.map_residual[t.which],
+                          t.col0 + 32 * (kGroups * (i + j) + group), row0, residual_bar);
         }
         __syncwarp();
         coming = true;
-      }
+      };
+      const bool two_slots = p.slots > kSlot;
+      if (q.tma_residual && left != 0) load_residual(0, two_slots ? left : 1);
       const uint32_t tmem_warp = tmem + (lanes << 16) + 32 * group;
       auto give_back = [&](uint32_t b) {       // the tensor core may have the buffer again
         cpt::tc_fence_before();
@@ -384,31 +384,44 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
           return;
         }
         const bool fast = q.e.aligned != 0 && col + 32 <= q.e.n;
-        cpe::shape_block<kRich>(q.e, key, row0, col, lane, bias[mine][i], fast, v);
+        cpe::shape_block<kRich>(q.e, key, row0, col, lane, i == 0 ? bias[0] : bias[1], fast, v);
         if (!q.tma_out) {
           cpe::write_block(q.e, row0, col, lane, fast, v);
           return;
         }
-        uint32_t slot = slots;
         if (q.tma_residual) {
-          slot += i * kSlot;
-          if (coming) {                        // (the first block of the tile)
+          if (i != 0 && !two_slots) load_residual(i, 1);
+          const uint32_t slot = slots + (two_slots ? i * kSlot : 0);
+          if (coming) {
             ok = cpt::mbar_wait(residual_bar, residual_parity, &gave_up);
             residual_parity ^= 1;
             coming = !ok;
           }
-        } else {
-          if (q.e.residual != nullptr && row0 + lane < q.e.m)
-            cpe::add32(v, q.e.residual, static_cast<uint64_t>(row0 + lane) * q.e.ldr + col,
-                       q.e.out_dtype);
+          write_slot(slot, lane, q.e.out_dtype, true, v);
+          cpt::stores_fence();
+          __syncwarp();
+          if (lane == 0) cpt::tma_store(&p.map_out[t.which], col, row0, slot);
+          __syncwarp();
+          return;
+        }
+        if (q.e.residual != nullptr && row0 + lane < q.e.m)
+          cpe::add32(v, q.e.residual, static_cast<uint64_t>(row0 + lane) * q.e.ldr + col,
+                     q.e.out_dtype);
+        // 32 columns of 16 bits at a time, or 16 of 32
+        const uint32_t halves = q.e.out_dtype == CP_F32 ? 2 : 1;
+        for (uint32_t h = 0; h < halves && col + 16 * h < q.e.n; ++h) {
           if (lane == 0) cpt::stores_read();
           __syncwarp();
+          write_slot(slots, lane, q.e.out_dtype, false, v);
+          cpt::stores_fence();
+          __syncwarp();
+          if (lane == 0) cpt::tma_store(&p.map_out[t.which], col + 16 * h, row0, slots);
+          __syncwarp();
+          if (halves == 2) {
+#pragma unroll
+            for (uint32_t j = 0; j < 16; ++j) v[j] = v[j + 16];
+          }
         }
-        write_slot(slot, lane, q.e.out_dtype, q.tma_residual != 0, v);
-        cpt::stores_fence();
-        __syncwarp();
-        if (lane == 0) cpt::tma_store(&p.map_out[t.which], col, row0, slot);
-        __syncwarp();
       };
       if constexpr (kSegments) {
         float acc[64];
@@ -815,18 +828,18 @@ bool encode_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t row
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Blocks of 32 x 32 outputs (or of the residual) as write_slot lays them out.
+// 32 rows by 64 bytes of the outputs (or of the residual) as write_slot lays them out.
 bool encode_block_map(CUtensorMap* map, const void* base, int dtype, uint64_t n, uint64_t m,
                       uint64_t ld) {
   const uint64_t size = dtype_size(dtype);
   const cuuint64_t dims[2] = {n, m};
   const cuuint64_t strides[1] = {m == 1 ? (size * n + 15) / 16 * 16 : size * ld};
-  const cuuint32_t box[2] = {32, 32};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(64 / size), 32};
   const cuuint32_t elem[2] = {1, 1};
   return g_encode.load()(
              map, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
              const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             size == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 bool block_map_ok(const void* p, int dtype, uint64_t m, uint64_t ld) {
@@ -1000,7 +1013,10 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
       cpx::set_error("tensor map refused");
       return CP_ERR_CUDA;
     }
-    if (x.tma_out) p.slots = max(p.slots, f32 ? kSlotF32 : x.tma_residual ? 2 * kSlot : kSlot);
+    // (both blocks' residuals ahead where tiles follow one another quickly: 4096 x 4096 x 256 16.7 us
+    // against 18.6; a deeper ring of stages where they do not: k = 24576 453 against 500)
+    if (x.tma_out)
+      p.slots = max(p.slots, x.tma_residual && q[i].k <= kQuickK ? 2 * kSlot : kSlot);
     p.stage_bytes = max(p.stage_bytes, kTileA + x.b_bytes);
     ++used;
   }
@@ -1016,7 +1032,7 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
     }
     p.two = p.stage_bytes <= kTwoBytes ? 1 : 0;
     p.stage_bytes <<= p.two;
-    p.stages = min((kSmemMost - 1024 - kSumWarps * p.slots) / p.stage_bytes, kMaxStages);
+    p.stages = min((kSmemUsed - kSumWarps * p.slots) / p.stage_bytes, kMaxStages);
     p.slots_at = p.stages * p.stage_bytes;
     for (int i = 0; i < used; ++i)
       p.q[swap ? 1 - i : i].kblocks = (ks[i] + (kStageK << p.two) - 1) / (kStageK << p.two);
