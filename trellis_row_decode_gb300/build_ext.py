@@ -1,13 +1,15 @@
 """Build libcp.so (the CUDA lookup-decode and its C ABI) in-tree for sm_103a.
 
 Each .cu file compiles in its own nvcc process (in parallel), then one link.
-Output: trellis_row_decode_gb300/_build/libcp.so.
+Output: trellis_row_decode_gb300/_build/libcp.so, and beside it _calls.so (cp_calls.cpp, host code
+for this Python, linked to libcp.so).
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -16,6 +18,7 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 BUILD = PKG / "_build"
 LIB = BUILD / "libcp.so"
+CALLS = BUILD / "_calls.so"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -62,6 +65,14 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> Path:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = CALLS.with_suffix(f".{os.getpid()}.tmp.so")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I",
+           sysconfig.get_paths()["include"], "-I", str(ROOT / "include"), "-o", str(tmp),
+           str(CSRC / "cp_calls.cpp"), "-L", str(BUILD), "-lcp", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for cp_calls.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
     return LIB
 
 

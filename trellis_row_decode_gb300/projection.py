@@ -12,10 +12,12 @@ or strides and CPError for what the library itself refuses.
 from __future__ import annotations
 
 import ctypes as C
+import importlib.machinery
+import importlib.util
 
 import torch
 
-from . import CP_ERR_INVALID_ARG, CPError, _check
+from . import CP_ERR_INVALID_ARG, LIB_PATH, CPError, _check, lib
 from . import layer as _layer
 from .layer import (CP_BF16, CP_F16, CP_F32, _check_out, _device, _empty, _float, _on, _rows, _stream,
                     _workspace)
@@ -27,6 +29,20 @@ ACTIVATIONS = ("none", "relu", "silu", "gelu", "gelu_tanh")
 _ACT = {name: i for i, name in enumerate(ACTIVATIONS)}
 _HALF = {torch.float16: CP_F16, torch.bfloat16: CP_BF16}
 _declared = None
+_calls = None
+
+
+def _common():
+    """The calls' common forms in compiled code (csrc/cp_calls.cpp), built beside libcp.so."""
+    global _calls
+    if _calls is None:
+        lib()                                     # (raises where nothing has been built)
+        path = str(LIB_PATH.with_name("_calls.so"))
+        loader = importlib.machinery.ExtensionFileLoader("_calls", path)
+        spec = importlib.util.spec_from_file_location("_calls", path, loader=loader)
+        _calls = importlib.util.module_from_spec(spec)
+        loader.exec_module(_calls)
+    return _calls
 
 
 def _lib():
@@ -88,6 +104,10 @@ def dropout(x: torch.Tensor, p: float, seed: int = 0, offset: int = 0,
     again (dropout_grad).  Each use of a mask wants an offset of its own.  `rng` (int64 [2] on the
     device: a seed, and what is added to `offset`) is read by the kernel as it runs, so that the
     replays of a captured graph draw masks of their own.  `out` may be x or the residual."""
+    if out is None and stream is None:
+        made = _common().dropout(x, residual, p, seed, offset, rng)
+        if made is not NotImplemented:
+            return made
     code = _float(x.dtype, "x")
     dev = _device(x, "x")
     rows, d, xs = _rows(x, "x")
@@ -142,9 +162,13 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
     fill) returns (out, pre): the sums in front of the activation in x's type, for linear_grad.
     Operands off 16-byte boundaries and sums of a split k need `workspace` (linear_workspace;
     allocated where it is not given)."""
+    act = _activation(activation)
+    if out is None and stream is None and workspace is None and (pre is False or pre is True):
+        made = _common().linear(x, weight, bias, act, residual, dtype, pre, p, seed, offset, rng)
+        if made is not NotImplemented:
+            return made
     dev, code, m, n, k, ldx, ldw = _operands(x, weight)
     shape = x.shape[:-1] + (n,)
-    act = _activation(activation)
     if out is None:
         dtype = dtype or x.dtype
         ocode = _float(dtype, "the output")
@@ -211,8 +235,14 @@ def linear_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, activat
     activation, p, seed, offset and rng are those of the forward call, `pre` what it left.  The
     products take dz rounded to x's type (dy itself without activation and dropout).
     accumulate=True adds to the `dw` and `db` that are given (gradients of several batches)."""
-    dev, code, m, n, k, ldx, ldw = _operands(x, weight)
     act = _activation(activation)
+    if (need_dx and need_dw and need_db and not accumulate and dx is None and dw is None
+            and db is None and workspace is None and stream is None):
+        made = _common().linear_grad(dy, x, weight, act, pre, dw_dtype, db_dtype, p, seed, offset,
+                                     rng)
+        if made is not NotImplemented:
+            return made
+    dev, code, m, n, k, ldx, ldw = _operands(x, weight)
     if dy.dtype != x.dtype and dy.dtype != torch.float32:
         raise ValueError("dy must have x's type or float32")
     if dy.shape != x.shape[:-1] + (n,):
