@@ -116,3 +116,26 @@ def test_linear_workspace_sizes(L, p):
     assert grad(1 << 30, 4, 4) == 0 and grad(4, 1 << 30, 4) == 0 and grad(4, 4, 1 << 30) == 0
     assert 6 * m * (m + 1) <= grad(m, m, m) < 1 << 63
     assert grad(0, 0, 0) == 16 and grad(0, 5, 7) >= 16
+
+
+def test_compiled_calls_leave_other_forms_alone():
+    """What is not of the common form is answered NotImplemented, with no error left behind: host
+    tensors, views, wrong objects, wrong counts of arguments."""
+    import torch
+    from trellis_row_decode_gb300 import build_ext, projection
+    if not build_ext.CALLS.exists():
+        build_ext.build()
+    calls = projection._common()
+    x = torch.zeros(4, 8, dtype=torch.bfloat16)
+    for args in [(), (x,), (x, None, 0.1, 1, 2, None), (x.T, None, 0.1, 1, 2, None),
+                 (None, None, 0.1, 1, 2, None), (3, x, 0.1, 1, 2, None),
+                 (x, None, "p", 1, 2, None), (x, None, 0.1, -1, 2, None),
+                 (x, None, 0.1, 1 << 70, 2, None)]:
+        assert calls.dropout(*args) is NotImplemented
+    for args in [(), (x, x, None, 0, None, None, False, 0.0, 0, 0, None),
+                 (x, None, None, 0, None, None, False, 0.0, 0, 0, None),
+                 (x, x, x, "silu", x, torch.float32, True, 0.0, 0, 0, x)]:
+        assert calls.linear(*args) is NotImplemented
+    for args in [(x,), (x, x, x, 0, None, None, None, 0.0, 0, 0, None),
+                 (None,) * 11, (x, x, x, 1 << 80, None, None, None, 0.0, 0, 0, None)]:
+        assert calls.linear_grad(*args) is NotImplemented
