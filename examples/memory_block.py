@@ -74,10 +74,10 @@ def main(tokens=512, steps=20, seed=0):
     residual = torch.randn(tokens, d, device="cuda", generator=g).to(BF16)
     target = torch.randn(tokens, d, device="cuda", generator=g)
     rng = torch.tensor([seed, 0], dtype=torch.int64, device="cuda")
-    first = block.step(residual, ids, target, 100.0, rng)            # (before the capture: warm-up)
+    first = block.step(residual, ids, target, 5.0, rng)            # (before the capture: warm-up)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        loss = block.step(residual, ids, target, 100.0, rng)
+        loss = block.step(residual, ids, target, 5.0, rng)
     for _ in range(steps):
         graph.replay()
     one, _ = block.forward(residual[:1], ids[:1])                    # a single token, served
