@@ -404,9 +404,16 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
           __syncwarp();
           return;
         }
-        if (q.e.residual != nullptr && row0 + lane < q.e.m)
-          cpe::add32(v, q.e.residual, static_cast<uint64_t>(row0 + lane) * q.e.ldr + col,
-                     q.e.out_dtype);
+        if (q.e.residual != nullptr && row0 + lane < q.e.m) {      // (of 32 bits)
+          const uint64_t at = static_cast<uint64_t>(row0 + lane) * q.e.ldr + col;
+          if (fast) {
+            cpe::add32(v, q.e.residual, at, CP_F32);
+          } else {
+#pragma unroll
+            for (uint32_t j = 0; j < 32; ++j)
+              if (col + j < q.e.n) v[j] += static_cast<const float*>(q.e.residual)[at + j];
+          }
+        }
         // 32 columns of 16 bits at a time, or 16 of 32
         const uint32_t halves = q.e.out_dtype == CP_F32 ? 2 : 1;
         for (uint32_t h = 0; h < halves && col + 16 * h < q.e.n; ++h) {
@@ -997,14 +1004,12 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
       cpx::set_error("tensor map refused");
       return CP_ERR_CUDA;
     }
-    // Outputs through TMA, where their rows allow it and what else the epilogue touches is read and
-    // written by whole blocks (the residual through TMA too, unless it has 32 bits).
-    const bool whole = ep.aligned != 0 && ep.n % 32 == 0, f32 = ep.out_dtype == CP_F32;
+    // Outputs through TMA, where their rows allow it, and the residual too, unless it has 32 bits.
+    const bool f32 = ep.out_dtype == CP_F32;
     const bool residual_ok =
         ep.residual == nullptr ||
-        (f32 ? whole : block_map_ok(ep.residual, ep.out_dtype, ep.m, ep.ldr));
-    x.tma_out = t.splits == 1 && block_map_ok(ep.out, ep.out_dtype, ep.m, ep.ldo) && residual_ok &&
-                (ep.pre == nullptr || whole);
+        (f32 ? ep.aligned != 0 : block_map_ok(ep.residual, ep.out_dtype, ep.m, ep.ldr));
+    x.tma_out = t.splits == 1 && block_map_ok(ep.out, ep.out_dtype, ep.m, ep.ldo) && residual_ok;
     x.tma_residual = x.tma_out && ep.residual != nullptr && !f32;
     if ((x.tma_out &&
          !encode_block_map(&p.map_out[at], ep.out, ep.out_dtype, ep.n, ep.m, ep.ldo)) ||
