@@ -92,28 +92,29 @@ __device__ __forceinline__ void drop_quad(const DropParams& p, const DropKey& ke
   drop_quad(p, key, round_keys(key), quad, row, v);
 }
 
-// Columns of a row, 4 * quad on, kQuads calls of the generator side by side, so that its chains of
-// products overlap and a round's key is made once for all.
-template <uint32_t kQuads>
-__device__ __forceinline__ void drop_quads(const DropParams& p, const DropKey& key, uint32_t quad,
-                                       uint32_t row, float* v) {
+// 4 * kQuads columns, 4 * quad on, of kRows rows, row_step apart: all calls of the generator side by
+// side, so that its chains of products overlap and a round's key is made once for all.
+template <uint32_t kQuads, uint32_t kRows>
+__device__ __forceinline__ void drop_block(const DropParams& p, const DropKey& key, uint32_t quad,
+                                           uint32_t row, uint32_t row_step, float* v) {
+  constexpr uint32_t kCalls = kQuads * kRows;
   if (p.mode == 2) {
 #pragma unroll
-    for (int i = 0; i < 4 * static_cast<int>(kQuads); ++i) v[i] = 0.0f;
+    for (uint32_t i = 0; i < 4 * kCalls; ++i) v[i] = 0.0f;
     return;
   }
-  uint32_t c0[kQuads], c1[kQuads], c2[kQuads], c3[kQuads], k0 = key.k0, k1 = key.k1;
+  uint32_t c0[kCalls], c1[kCalls], c2[kCalls], c3[kCalls], k0 = key.k0, k1 = key.k1;
 #pragma unroll
-  for (uint32_t q = 0; q < kQuads; ++q) {
-    c0[q] = quad + q;
-    c1[q] = row;
+  for (uint32_t q = 0; q < kCalls; ++q) {
+    c0[q] = quad + q % kQuads;
+    c1[q] = row + q / kQuads * row_step;
     c2[q] = key.o0;
     c3[q] = key.o1;
   }
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
 #pragma unroll
-    for (uint32_t q = 0; q < kQuads; ++q) {
+    for (uint32_t q = 0; q < kCalls; ++q) {
       const uint64_t a = static_cast<uint64_t>(c0[q]) * 0xD2511F53u;
       const uint64_t b = static_cast<uint64_t>(c2[q]) * 0xCD9E8D57u;
       c0[q] = static_cast<uint32_t>(b >> 32) ^ c1[q] ^ k0;
@@ -125,7 +126,7 @@ __device__ __forceinline__ void drop_quads(const DropParams& p, const DropKey& k
     k1 += 0xBB67AE85u;
   }
 #pragma unroll
-  for (uint32_t q = 0; q < kQuads; ++q) {
+  for (uint32_t q = 0; q < kCalls; ++q) {
     v[4 * q] = c0[q] <= p.last ? v[4 * q] * p.scale : 0.0f;
     v[4 * q + 1] = c1[q] <= p.last ? v[4 * q + 1] * p.scale : 0.0f;
     v[4 * q + 2] = c2[q] <= p.last ? v[4 * q + 2] * p.scale : 0.0f;
@@ -418,8 +419,8 @@ __device__ __forceinline__ void shape_block(const Epilogue& e, const DropKey& ke
       for (int i = 0; i < 32; ++i) v[i] = act<decltype(tag)::value>(v[i]);
     });
     if (e.drop.mode != 0) {
-      drop_quads<4>(e.drop, key, col / 4, row, v);
-      drop_quads<4>(e.drop, key, col / 4 + 4, row, v + 16);
+      drop_block<4, 1>(e.drop, key, col / 4, row, 0, v);
+      drop_block<4, 1>(e.drop, key, col / 4 + 4, row, 0, v + 16);
     }
   }
 }

@@ -47,6 +47,11 @@ struct GradParams {
   DropParams drop;
 };
 
+template <uint32_t kCount>
+struct Count {
+  static constexpr uint32_t value = kCount;
+};
+
 // kShape: there is an activation or dropout.
 template <typename T, typename D, bool VEC, bool kShape>
 __global__ void __launch_bounds__(kGradThreads, grad_ctas(kShape))
@@ -62,43 +67,58 @@ __global__ void __launch_bounds__(kGradThreads, grad_ctas(kShape))
       static_cast<uint32_t>(static_cast<uint64_t>(p.m) * (blockIdx.y + 1) / p.count);
   const DropKey key = cpe::drop_key(p.drop);
   float acc[8] = {};
-  if (8ull * o < p.n) {
-    for (uint32_t r = r0 + line; r < r1; r += 8 * kAhead) {
-      Packed<D> dy[kAhead];
-      Packed<T> pre[kAhead];
+  // kRows rows, eight apart, all of them there: their chains of arithmetic side by side
+  auto rows = [&](uint32_t r, auto count) {
+    constexpr uint32_t kRows = decltype(count)::value;
+    Packed<D> dy[kRows];
+    Packed<T> pre[kRows];
 #pragma unroll
-      for (uint32_t i = 0; i < kAhead; ++i) {
-        const uint32_t row = r + 8 * i;
-        if (row < r1) {
-          dy[i] = load_row_octet<D, VEC>(static_cast<const D*>(p.dy) + row * p.ldy, o, p.n);
-          if (kShape && p.act != CP_ACT_NONE)
-            pre[i] = load_row_octet<T, VEC>(static_cast<const T*>(p.pre) + row * p.ldp, o, p.n);
-        }
-      }
-#pragma unroll
-      for (uint32_t i = 0; i < kAhead; ++i) {
-        const uint32_t row = r + 8 * i;
-        if (row < r1) {
-          float v[8];
-          unpack(dy[i], v);
-          if constexpr (kShape) {
-            if (p.act != CP_ACT_NONE) {
-              float z[8];
-              unpack(pre[i], z);
-              cpe::with_act(p.act, [&](auto tag) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= cpe::slope<decltype(tag)::value>(z[e]);
-              });
-            }
-            if (p.drop.mode != 0) cpe::drop_quads<2>(p.drop, key, 2 * o, row, v);
-          }
-          if (p.dz != nullptr)       // (rows on 16-byte boundaries; what lies behind n is not read)
-            store_octet(static_cast<T*>(p.dz) + row * p.pitch + 8ull * o, pack<T>(v));
-#pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] += v[e];
-        }
-      }
+    for (uint32_t i = 0; i < kRows; ++i) {
+      dy[i] = load_row_octet<D, VEC>(static_cast<const D*>(p.dy) + (r + 8 * i) * p.ldy, o, p.n);
+      if (kShape && p.act != CP_ACT_NONE)
+        pre[i] = load_row_octet<T, VEC>(static_cast<const T*>(p.pre) + (r + 8 * i) * p.ldp, o, p.n);
     }
+    float v[8 * kRows];
+#pragma unroll
+    for (uint32_t i = 0; i < kRows; ++i) {
+      float u[8];
+      unpack(dy[i], u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[8 * i + e] = u[e];
+    }
+    if constexpr (kShape) {
+      if (p.act != CP_ACT_NONE) {
+        float z[8 * kRows];
+#pragma unroll
+        for (uint32_t i = 0; i < kRows; ++i) {
+          float u[8];
+          unpack(pre[i], u);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[8 * i + e] = u[e];
+        }
+        cpe::with_act(p.act, [&](auto tag) {
+#pragma unroll
+          for (uint32_t e = 0; e < 8 * kRows; ++e) v[e] *= cpe::slope<decltype(tag)::value>(z[e]);
+        });
+      }
+      if (p.drop.mode != 0) cpe::drop_block<2, kRows>(p.drop, key, 2 * o, r, 8, v);
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kRows; ++i) {
+      float u[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        u[e] = v[8 * i + e];
+        acc[e] += u[e];
+      }
+      if (p.dz != nullptr)           // (rows on 16-byte boundaries; what lies behind n is not read)
+        store_octet(static_cast<T*>(p.dz) + (r + 8 * i) * p.pitch + 8ull * o, pack<T>(u));
+    }
+  };
+  if (8ull * o < p.n) {
+    uint32_t r = r0 + line;
+    for (; r + 8 * (kAhead - 1) < r1; r += 8 * kAhead) rows(r, Count<kAhead>{});
+    for (; r < r1; r += 8) rows(r, Count<1>{});
   }
   if (p.parts == nullptr) return;
 #pragma unroll
