@@ -538,13 +538,13 @@ __global__ void __launch_bounds__(kFinishThreads)
 // ------------------------------------------- few rows of a, many bytes of b: one SM
 //
 // With at most 128 rows of a the operands change places: 128 rows of b are the tensor core's
-// 128 x 16 operand, up to 64 rows of a its N (16, 32 or 64) columns, and the kernel is bound by
+// 128 x 16 operand, up to 64 rows of a its N (16, 32, 48 or 64) columns, and the kernel is bound by
 // the stream of b (a second tile of rows of a finds it in L2).  Two CTAs share an SM; `splits` CTAs
 // of a cluster share a tile's k and add their sums in order through distributed shared memory.
 
 constexpr int kThinThreads = 256;      // four finishing warps, TMA, MMA, two idle
 constexpr uint32_t kThinMaxStages = 6;
-constexpr uint32_t kThinSmem = 111616; // dynamic shared memory of a CTA, two to an SM
+constexpr uint32_t kThinSmem = 115200; // dynamic shared memory of a CTA, two to an SM
 
 struct ThinParams {
   Epilogue e;
@@ -556,7 +556,8 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     thin_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                 const __grid_constant__ ThinParams p) {
   constexpr uint32_t kStage = kTileA + kN * 128;
-  constexpr uint32_t kColumns = 2 * kN;              // of tensor memory: two buffers
+  constexpr uint32_t kBufferN = kN == 48 ? 64 : kN;  // of tensor memory: two buffers, a power of two
+  constexpr uint32_t kColumns = 2 * kBufferN;
   extern __shared__ uint8_t dyn[];
   __shared__ __align__(8) uint64_t bars[2 * kThinMaxStages + 5];
   __shared__ uint32_t tmem_base;
@@ -655,10 +656,10 @@ __global__ void __launch_bounds__(kThinThreads, 2)
         const uint32_t at = cpt::smem_addr(tiles) + s * kStage;
         const uint64_t db = cpt::operand_desc(at), da = cpt::operand_desc(at + kTileA);
         if (cpt::elect_one()) {
-          cpt::mma_half_one(tmem + b * kN, db, da, p.instr, more);
+          cpt::mma_half_one(tmem + b * kBufferN, db, da, p.instr, more);
 #pragma unroll
           for (uint32_t k = 1; k < 4; ++k)
-            cpt::mma_half_one(tmem + b * kN, db + 2 * k, da + 2 * k, p.instr, 1);
+            cpt::mma_half_one(tmem + b * kBufferN, db + 2 * k, da + 2 * k, p.instr, 1);
           cpt::mma_commit(empty + 8 * s);
           if (kb + 1 == end) cpt::mma_commit(acc_full + 8 * b);
         }
@@ -688,15 +689,17 @@ __global__ void __launch_bounds__(kThinThreads, 2)
       ok = cpt::mbar_wait(acc_full + 8 * b, (it >> 1) & 1, &gave_up);
       if (!ok) break;
       cpt::tc_fence_after();
-      const uint32_t at = tmem + ((warp * 32) << 16) + b * kN;
+      const uint32_t at = tmem + ((warp * 32) << 16) + b * kBufferN;
 #pragma unroll
       for (uint32_t c = 0; c < (kN + 31) / 32; ++c) {
         float x[32] = {};
-        if constexpr (kN == 16) cpt::tmem_load16<0>(x, at);
+        const bool part = 32 * c + 32 > kN;
+        if (part) cpt::tmem_load16<0>(x, at + 32 * c);
         else cpt::tmem_load32<0>(x, at + 32 * c);
         cpt::tmem_load_wait(x);
 #pragma unroll
-        for (uint32_t i = 0; i < (kN < 32 ? kN : 32); ++i) acc[32 * c + i] += x[i];
+        for (uint32_t i = 0; i < 32; ++i)
+          if (32 * c + i < kN) acc[32 * c + i < kN ? 32 * c + i : 0] += x[i];
       }
       cpt::tc_fence_before();
       __syncwarp();
@@ -799,6 +802,7 @@ const Device* device(cudaError_t* err) {
   }
   allow(reinterpret_cast<const void*>(&thin_kernel<16>), kThinSmem);
   allow(reinterpret_cast<const void*>(&thin_kernel<32>), kThinSmem);
+  allow(reinterpret_cast<const void*>(&thin_kernel<48>), kThinSmem);
   allow(reinterpret_cast<const void*>(&thin_kernel<64>), kThinSmem);
   if (*err != cudaSuccess) return nullptr;
   cudaLaunchAttribute attr[1];
@@ -1062,7 +1066,7 @@ cp_status launch_thin(const Product& q, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (device(&e) == nullptr) return cpx::cuda_fail(e, "linear device query");
   const uint32_t m = q.e.m, n = q.e.n;
-  const uint32_t kn = m <= 16 ? 16 : m <= 32 ? 32 : 64;
+  const uint32_t kn = m <= 16 ? 16 : m <= 32 ? 32 : m <= 48 || (m > 64 && m <= 96) ? 48 : 64;
   ThinParams p{};
   p.e = q.e;
   p.kblocks = (q.k + kStageK - 1) / kStageK;
@@ -1084,6 +1088,7 @@ cp_status launch_thin(const Product& q, cudaStream_t s) {
                  p.splits};
   e = kn == 16   ? launch(l, &thin_kernel<16>, map_a, map_b, p)
       : kn == 32 ? launch(l, &thin_kernel<32>, map_a, map_b, p)
+      : kn == 48 ? launch(l, &thin_kernel<48>, map_a, map_b, p)
                  : launch(l, &thin_kernel<64>, map_a, map_b, p);
   if (e != cudaSuccess) return cpx::cuda_fail(e, "linear launch");
   return CP_OK;
