@@ -1,0 +1,81 @@
+"""The projection and dropout where offsets pass 32 bits: outputs, kept sums and gradients of more
+than 2^32 elements, rows far apart; rows at the ends and around 2^32 elements are checked."""
+import pytest
+import torch
+
+import trellis_row_decode_gb300 as cp
+
+from layer_util import U32, assert_within, gen, randn, rounded
+from linear_util import drop64, linear64, out_bound, philox, slope64, sum_bound
+
+pytestmark = pytest.mark.gpu
+M, N, K = 70001, 65536, 8
+ROWS = [0, 1, 65535, 65536, 65537, 70000]       # 65536 * 65536 = 2^32
+
+
+def _mask_rows(rows, d, p, seed):
+    import numpy as np
+    quad = np.arange(d // 4, dtype=np.uint64)[None, :]
+    row = np.array(rows, dtype=np.uint64)[:, None]
+    z = np.zeros((1, 1), dtype=np.uint64)
+    w = np.stack(np.broadcast_arrays(*philox(quad + z, row + z, z, z, seed, 0)), -1)
+    return torch.from_numpy(w.reshape(len(rows), d) < int((1 - p) * 2.0 ** 32 + 0.5))
+
+
+def test_dropout_past_32_bits():
+    x = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    x.view(-1)[:1 << 20].normal_()
+    for r in ROWS:
+        x[r].normal_()
+    out = cp.dropout(x, 0.25, 9, residual=x, out=x)
+    assert out is x
+    y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda").fill_(1.0)
+    out = cp.dropout(y, 0.25, 9)
+    keep = _mask_rows(ROWS, N, 0.25, 9)
+    got = out[ROWS].float().cpu()
+    want = keep.float() * torch.tensor(1 / 0.75).bfloat16().float()
+    assert torch.equal(got, want)
+
+
+def test_linear_and_its_gradient_past_32_bits():
+    g = gen(0)
+    x, w = randn(g, M, K, dtype=torch.bfloat16), randn(g, N, K, dtype=torch.bfloat16, std=0.3)
+    xc, wc = x.cuda(), w.cuda()
+    out, pre = cp.linear(xc, wc, None, "silu", pre=True)
+    ref, z, mag = linear64(x[ROWS], w, None, "silu")
+    assert_within(out[ROWS], ref, out_bound(ref, z, mag, K, torch.bfloat16))
+    assert_within(pre[ROWS], z, sum_bound(mag, K) + rounded(z, torch.bfloat16))
+    out.zero_()                                  # a gradient whose rows are mostly zeros
+    out[ROWS] = randn(g, len(ROWS), N, dtype=torch.bfloat16).cuda()
+    dy = out[ROWS].cpu().double()
+    dx, dw, db = cp.linear_grad(out, xc, wc, "silu", pre, db_dtype=torch.float32)
+    zs = pre[ROWS].cpu().double()
+    own = 16 * U32 * (zs.abs() + 1) * dy.abs()
+    dz = dy * slope64(zs, "silu")
+    cut = own * 1.01 + dz.abs() * (2.0 ** -8 + 4 * U32) + 2.0 ** -130
+    X, W = x[ROWS].double(), w.double()
+    assert_within(dx[ROWS], dz @ W, cut @ W.abs() + sum_bound((dz.abs() + cut) @ W.abs(), N)
+                  + rounded(dz @ W, torch.bfloat16))
+    assert_within(dw, dz.T @ X, cut.T @ X.abs() + sum_bound((dz.abs() + cut).T @ X.abs(), M)
+                  + rounded(dz.T @ X, torch.bfloat16))
+    assert_within(db, dz.sum(0), (own + 4 * U32 * dz.abs()).sum(0)
+                  + (M + 64) * U32 * (dz.abs() + own).sum(0) + rounded(dz.sum(0), torch.float32))
+    assert cp.linear_status() == cp.CP_OK
+
+
+@pytest.mark.parametrize("m", [12, 200])
+def test_linear_rows_far_apart(m):
+    """Row strides of 2^28 and more elements: 12 rows span 6 GB, 200 rows 4 GB a side."""
+    g = gen(m)
+    n, k = 48, 64
+    pitch = (1 << 28) + 8 if m == 12 else (1 << 23) + 8
+    x = torch.empty(m * pitch, dtype=torch.bfloat16, device="cuda").as_strided((m, k), (pitch, 1))
+    out = torch.empty(m * pitch, dtype=torch.bfloat16, device="cuda").as_strided((m, n), (pitch, 1))
+    xs, w = randn(g, m, k, dtype=torch.bfloat16), randn(g, n, k, dtype=torch.bfloat16, std=0.125)
+    x.copy_(xs)
+    cp.linear(x, w.cuda(), None, "relu", out=out)
+    ref, z, mag = linear64(xs, w, None, "relu")
+    assert_within(out, ref, out_bound(ref, z, mag, k, torch.bfloat16))
+    cp.dropout(x[:, :n], 0.5, 3, out=out)
+    want = drop64(xs[:, :n].double(), 0.5, 3, 0)
+    assert_within(out, want, 2 * U32 * want.abs() + rounded(want, torch.bfloat16))
