@@ -23,7 +23,6 @@ using cpe::DropKey;
 
 constexpr int kThreads = 256;
 constexpr int kAhead = 2;                  // octets whose loads a thread has in flight
-constexpr uint32_t kPer = 8;               // octets of a thread: CTAs short enough to even out
 template <typename T, bool kResidual>      // CTAs of an SM, by registers
 constexpr int kCtas = sizeof(T) == 4 ? 4 : kResidual ? 5 : 6;
 
@@ -60,6 +59,7 @@ struct DropoutParams {
   uint64_t ldx, ldr, ldo;                  // flat: all d, d a multiple of 8
   uint32_t rows, d, octets;                // octets of a row
   uint32_t step_rows, step_octets;         // what kThreads octets come to
+  uint32_t per;                            // octets of a thread
   cpe::DropParams drop;
 };
 
@@ -75,14 +75,14 @@ __global__ void __launch_bounds__(kThreads, (kCtas<T, kResidual>))
   let_next_start();
   const DropKey key = cpe::drop_key(p.drop);
   const cpe::RoundKeys keys = cpe::round_keys(key);
-  const uint64_t first = static_cast<uint64_t>(blockIdx.x) * (kThreads * kPer) + threadIdx.x;
+  const uint64_t first = static_cast<uint64_t>(blockIdx.x) * (kThreads * p.per) + threadIdx.x;
   uint32_t row = static_cast<uint32_t>(first / p.octets);
   uint32_t o = static_cast<uint32_t>(first - static_cast<uint64_t>(row) * p.octets);
   const T* px = static_cast<const T*>(p.x) + 8 * first;          // (of kFlat)
   const T* pr = static_cast<const T*>(p.residual) + 8 * first;
   T* po = static_cast<T*>(p.out) + 8 * first;
 #pragma unroll 1
-  for (uint32_t n = 0; n < kPer && row < p.rows; n += kAhead) {
+  for (uint32_t n = 0; n < p.per && row < p.rows; n += kAhead) {
     Packed<T> x[kAhead], r[kAhead];
     uint32_t at[kAhead], col[kAhead];
 #pragma unroll
@@ -158,11 +158,11 @@ __global__ void __launch_bounds__(kThreads, 5)
   const DropKey key = cpe::drop_key(p.drop);
   const cpe::RoundKeys keys = cpe::round_keys(key);
   const uint32_t lane = threadIdx.x & 31, e = lane & 7;
-  const uint64_t first = static_cast<uint64_t>(blockIdx.x) * (kThreads * kPer) + threadIdx.x;
+  const uint64_t first = static_cast<uint64_t>(blockIdx.x) * (kThreads * p.per) + threadIdx.x;
   uint32_t row = static_cast<uint32_t>(first / p.octets);
   uint32_t o = static_cast<uint32_t>(first - static_cast<uint64_t>(row) * p.octets);
 #pragma unroll 1
-  for (uint32_t n = 0; n < kPer; ++n) {
+  for (uint32_t n = 0; n < p.per; ++n) {
     const bool in = row < p.rows;
     if (!__any_sync(0xFFFFFFFFu, in)) break;
     // how many elements the octet has (bits 0 to 3), how far it lies from the warp's first
@@ -265,7 +265,12 @@ extern "C" cp_status cp_dropout(const void* x, uint64_t x_stride, const void* re
                    (residual == nullptr || octets_ok(residual, residual_stride, d, elt));
   q.step_rows = kThreads / q.octets;
   q.step_octets = kThreads % q.octets;
-  const uint64_t units = rows * q.octets, ctas = (units + kThreads * kPer - 1) / (kThreads * kPer);
+  const uint64_t units = rows * q.octets;
+  // CTAs short enough to even out, and as many as run at once where there is little (bf16, 48 x 1024:
+  // 2.1 us with two octets a thread, 4.5 with eight; 4096 x 4096: 16.6 with four, 18.4; 196,608 x 1024:
+  // 159 with eight, 165 with four).
+  q.per = units < (1u << 17) ? 2 : units < (1u << 22) ? 4 : 8;
+  const uint64_t ctas = (units + kThreads * q.per - 1) / (kThreads * q.per);
   if (ctas >= (1ull << 31)) {
     cpx::set_error("rows of d make more than 2^42 octets");
     return CP_ERR_INVALID_ARG;

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include "cp.h"
+#include "cp_align.cuh"
 #include "cp_epilogue.cuh"
 #include "cp_internal.h"
 #include "cp_layer.cuh"
@@ -31,6 +32,7 @@ using cplin::Product;
 constexpr int kGradThreads = 256;
 constexpr uint32_t kGradColumns = 256;
 constexpr uint32_t kMostParts = 64;
+static_assert(kGradThreads == cpm::kAlignThreads, "CTAs of the copies are those of dz");
 // Rows whose loads a thread has in flight, CTAs of an SM (by registers: slopes and the generator
 // take more).
 constexpr uint32_t grad_ahead(bool shape) { return shape ? 2 : 4; }
@@ -45,6 +47,8 @@ struct GradParams {
   uint32_t m, n, count;
   int act;
   DropParams drop;
+  uint32_t copy_rows;      // rows of CTAs (blockIdx.y) from `count` on that copy operands of the
+  cpm::AlignParams copy;   // products to 16-byte boundaries meanwhile
 };
 
 template <uint32_t kCount>
@@ -60,6 +64,11 @@ __global__ void __launch_bounds__(kGradThreads, grad_ctas(kShape))
   __shared__ float sums[8][kGradColumns];
   wait_for_previous();
   let_next_start();
+  if (blockIdx.y >= p.count) {
+    cpm::align_rows_of(p.copy, (blockIdx.y - p.count) * gridDim.x + blockIdx.x,
+                       p.copy_rows * gridDim.x);
+    return;
+  }
   const uint32_t lane = threadIdx.x & 31, line = threadIdx.x >> 5;
   const uint32_t o = blockIdx.x * (kGradColumns / 8) + lane;
   const uint32_t r0 = static_cast<uint32_t>(static_cast<uint64_t>(p.m) * blockIdx.y / p.count);
@@ -143,7 +152,8 @@ uint32_t grad_parts(uint64_t m, uint64_t n, bool shape) {
 
 template <typename T, typename D>
 cudaError_t launch_dz(const GradParams& p, bool vec, cudaStream_t s) {
-  const Launch l{dim3((p.n + kGradColumns - 1) / kGradColumns, p.count), kGradThreads, 0, s};
+  const Launch l{dim3((p.n + kGradColumns - 1) / kGradColumns, p.count + p.copy_rows),
+                 kGradThreads, 0, s};
   if (p.act != CP_ACT_NONE || p.drop.mode != 0)
     return vec ? launch(l, &dz_kernel<T, D, true, true>, p)
                : launch(l, &dz_kernel<T, D, false, true>, p);
@@ -170,13 +180,13 @@ cp_status refuse(const char* what) {
 
 bool row_ok(uint64_t stride, uint64_t d) { return stride >= d || stride == 0; }
 
-// Operands that lie on other boundaries, copied behind each other to `to` in one launch.
-cudaError_t align(Operand* (&op)[2], const uint64_t (&rows)[2], uint64_t k, uint8_t*& to,
-                  cudaStream_t s) {
-  cpm::AlignOperand of[2] = {};
+// Operands that lie on other boundaries, to be copied behind each other to `to`; false: none.
+bool to_align(Operand* (&op)[2], const uint64_t (&rows)[2], uint64_t k, uint8_t*& to,
+              cpm::AlignOperand (&of)[2]) {
   const uint64_t pitch = 2 * row_pitch(k);
   bool any = false;
   for (int i = 0; i < 2; ++i) {
+    of[i] = cpm::AlignOperand{};
     if (op[i] == nullptr || rows_ok(op[i]->p, op[i]->ld, rows[i])) continue;
     of[i] = cpm::AlignOperand{static_cast<const uint8_t*>(op[i]->p), to, 2 * op[i]->ld, rows[i]};
     op[i]->p = to;
@@ -184,7 +194,7 @@ cudaError_t align(Operand* (&op)[2], const uint64_t (&rows)[2], uint64_t k, uint
     to += rows[i] * pitch;
     any = true;
   }
-  return any ? cpm::align_rows(of, static_cast<uint32_t>(2 * k), s) : cudaSuccess;
+  return any;
 }
 
 // Bytes for the sums of products whose k is split; they begin on a 32-byte boundary, the workspace
@@ -261,8 +271,11 @@ extern "C" cp_status cp_linear(const void* x, uint64_t x_stride, const void* w, 
   if (k == 0) return cplin::launch_products(&q, 1, ColumnSums{}, nullptr, s);
   uint8_t* at = static_cast<uint8_t*>(workspace);
   Operand* op[2] = {&q.a, &q.b};
-  const cudaError_t e = align(op, {m, n}, k, at, s);
-  if (e != cudaSuccess) return cpx::cuda_fail(e, "linear launch");
+  cpm::AlignOperand of[2];
+  if (to_align(op, {m, n}, k, at, of)) {
+    const cudaError_t e = cpm::align_rows(of, static_cast<uint32_t>(2 * k), s);
+    if (e != cudaSuccess) return cpx::cuda_fail(e, "linear launch");
+  }
   if (m <= cplin::kThinRows) return cplin::launch_thin(q, s);
   return cplin::launch_products(&q, 1, ColumnSums{}, part_at(at), s);
 }
@@ -335,6 +348,14 @@ extern "C" cp_status cp_linear_grad(const void* dy, int dy_dtype, uint64_t dy_st
     g.parts = reinterpret_cast<float*>(at);
   }
   at += 4ull * grad_parts(m, n, false) * g.pitch;
+  // dx [m][k] = dz w: w is stored across n;  dw [n][k] = dz^T x: both are stored across m
+  Operand xo{x, x_stride, true}, wo{w, w_stride, true};
+  cpm::AlignOperand of[2];
+  bool copies = false;
+  if (has_dy && k != 0) {
+    Operand* op[2] = {want_dw ? &xo : nullptr, want_dx ? &wo : nullptr};
+    copies = to_align(op, {m, n}, k, at, of);
+  }
   cudaError_t e = cudaSuccess;
   if (has_dy && (g.dz != nullptr || g.parts != nullptr)) {
     g.dy = dy;
@@ -345,6 +366,11 @@ extern "C" cp_status cp_linear_grad(const void* dy, int dy_dtype, uint64_t dy_st
     g.n = static_cast<uint32_t>(n);
     g.count = grad_parts(m, n, shape);
     g.act = activation;
+    if (copies) {
+      const uint32_t wide = (g.n + kGradColumns - 1) / kGradColumns;
+      g.copy = cpm::align_params(of, static_cast<uint32_t>(2 * k));
+      g.copy_rows = (cpm::align_ctas(g.copy) + wide - 1) / wide;
+    }
     const bool vec = octets_ok(dy, dy_stride, g.n, dtype_size(dy_dtype)) &&
                      (pre == nullptr || octets_ok(pre, pre_stride, g.n, 2));
     if (dtype == CP_F16)
@@ -353,16 +379,11 @@ extern "C" cp_status cp_linear_grad(const void* dy, int dy_dtype, uint64_t dy_st
     else
       e = dy_dtype == CP_F32 ? launch_dz<__nv_bfloat16, float>(g, vec, s)
                              : launch_dz<__nv_bfloat16, __nv_bfloat16>(g, vec, s);
-    if (e != cudaSuccess) return cpx::cuda_fail(e, "linear gradient launch");
+  } else if (copies) {
+    e = cpm::align_rows(of, static_cast<uint32_t>(2 * k), s);
   }
+  if (e != cudaSuccess) return cpx::cuda_fail(e, "linear gradient launch");
 
-  // dx [m][k] = dz w: w is stored across n;  dw [n][k] = dz^T x: both are stored across m
-  Operand xo{x, x_stride, true}, wo{w, w_stride, true};
-  if (has_dy && k != 0) {
-    Operand* op[2] = {want_dw ? &xo : nullptr, want_dx ? &wo : nullptr};
-    e = align(op, {m, n}, k, at, s);
-    if (e != cudaSuccess) return cpx::cuda_fail(e, "linear gradient launch");
-  }
   Product q[cplin::kMostProducts] = {};
   int count = 0;
   if (want_dx) {

@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include "cp.h"
+#include "cp_align.cuh"
 #include "cp_internal.h"
 #include "cp_layer.cuh"
 #include "cp_matmul_fp8.h"
@@ -31,34 +32,6 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Sixteen bytes from row + col on, zeros behind the row's k bytes: shifted out of two aligned
-// pieces, or byte by byte where those reach outside the row.
-__device__ __forceinline__ uint4 load_any_piece(const uint8_t* row, uint32_t col, uint32_t k) {
-  const uint8_t* p = row + col;
-  const uint32_t skew = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15);
-  if (col >= skew && static_cast<uint64_t>(col) + (skew != 0 ? 32 - skew : 16) <= k) {
-    const uint4* q = reinterpret_cast<const uint4*>(p - skew);
-    const uint4 lo = q[0], hi = skew != 0 ? q[1] : make_uint4(0, 0, 0, 0);
-    uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    if (skew & 8) {
-#pragma unroll
-      for (int i = 0; i < 6; ++i) x[i] = x[i + 2];
-    }
-    if (skew & 4) {
-#pragma unroll
-      for (int i = 0; i < 5; ++i) x[i] = x[i + 1];
-    }
-    const uint32_t bits = 8 * (skew & 3);
-    return make_uint4(__funnelshift_r(x[0], x[1], bits), __funnelshift_r(x[1], x[2], bits),
-                      __funnelshift_r(x[2], x[3], bits), __funnelshift_r(x[3], x[4], bits));
-  }
-  uint32_t w[4] = {};
-#pragma unroll
-  for (int b = 0; b < 16; ++b)
-    if (static_cast<uint64_t>(col) + b < k) w[b / 4] |= static_cast<uint32_t>(p[b]) << (8 * (b & 3));
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // ---------------------------------------------------- rows on any byte boundary
 //
 // Tensor maps want rows on 16-byte boundaries.  Operands that lie elsewhere are copied to such
@@ -69,48 +42,16 @@ __device__ __forceinline__ uint4 load_any_piece(const uint8_t* row, uint32_t col
 // 2048 x 2048 x 2047 17.4 (14.1 for the product of rows on 16-byte boundaries).  A warp-level fp16
 // product of the shifted bytes, without a copy, ran at 125 TFLOP/s and took 738 and 137.
 
-constexpr int kAlignThreads = 256;
-constexpr uint64_t kAlignCtas = 152 * 6;                  // as many as run at once
-constexpr uint32_t kAlignPieces = 4;                      // 16-byte pieces of a lane
-constexpr uint32_t kAlignBytes = 32 * 16 * kAlignPieces;  // of a row, by one warp at a time
-
-struct AlignParams {
-  cpm::AlignOperand of[2];
-  uint32_t k, chunks;      // chunks of kAlignBytes in a row
-  uint64_t pitch;
-};
-
-__global__ void __launch_bounds__(kAlignThreads) align_rows_kernel(AlignParams p) {
+__global__ void __launch_bounds__(cpm::kAlignThreads) align_rows_kernel(cpm::AlignParams p) {
   wait_for_previous();
   let_next_start();
-  const uint32_t lane = threadIdx.x & 31;
-  const uint64_t warps = static_cast<uint64_t>(gridDim.x) * (kAlignThreads / 32);
-  const uint64_t units = (p.of[0].rows + p.of[1].rows) * p.chunks;
-  for (uint64_t u = static_cast<uint64_t>(blockIdx.x) * (kAlignThreads / 32) + threadIdx.x / 32;
-       u < units; u += warps) {
-    uint64_t row = u / p.chunks;
-    const uint32_t col = static_cast<uint32_t>(u - row * p.chunks) * kAlignBytes + lane * 16;
-    const bool second = row >= p.of[0].rows;
-    if (second) row -= p.of[0].rows;
-    const uint8_t* from = (second ? p.of[1].from : p.of[0].from) +
-                          row * (second ? p.of[1].ld : p.of[0].ld);
-    uint8_t* to = (second ? p.of[1].to : p.of[0].to) + row * p.pitch;
-    uint4 v[kAlignPieces];
-#pragma unroll
-    for (uint32_t i = 0; i < kAlignPieces; ++i)
-      if (col + i * 512 < p.k) v[i] = load_any_piece(from, col + i * 512, p.k);
-#pragma unroll
-    for (uint32_t i = 0; i < kAlignPieces; ++i)
-      if (col + i * 512 < p.k) *reinterpret_cast<uint4*>(to + col + i * 512) = v[i];
-  }
+  cpm::align_rows_of(p, blockIdx.x, gridDim.x);
 }
 
 // Rows that a tensor map takes (and a row stride of their own: not one row for all).
 bool rows_ok(const void* p, uint64_t stride, uint64_t rows) {
   return cpx::aligned(p, 16) && (rows == 1 || (stride % 16 == 0 && stride != 0));
 }
-
-uint64_t aligned_pitch(uint64_t k) { return (k + 15) / 16 * 16; }
 
 // ------------------------------------------------------------------- few rows of a
 //
@@ -159,13 +100,13 @@ __device__ __forceinline__ uint4 load_piece(const uint8_t* row, uint32_t col, ui
                  : "l"(row + col));
     return v;
   }
-  return load_any_piece(row, col, k);
+  return cpm::load_any_piece(row, col, k);
 }
 template <bool kAligned>
 __device__ __forceinline__ uint4 load_piece_cached(const uint8_t* row, uint32_t col, uint32_t k) {
   if (kAligned && static_cast<uint64_t>(col) + 16 <= k)
     return *reinterpret_cast<const uint4*>(row + col);
-  return load_any_piece(row, col, k);
+  return cpm::load_any_piece(row, col, k);
 }
 
 // kTokens: rows of a / 8.  kAhead: groups of w in flight per warp.  kAligned: rows on 16-byte
@@ -326,16 +267,8 @@ cp_status launch_few(const MatmulParams& p, bool aligned, cudaStream_t s) {
 namespace cpm {
 
 cudaError_t align_rows(const AlignOperand (&of)[2], uint32_t k, cudaStream_t s) {
-  AlignParams c{};
-  c.of[0] = of[0];
-  c.of[1] = of[1];
-  c.k = k;
-  c.pitch = aligned_pitch(k);
-  c.chunks = (k + kAlignBytes - 1) / kAlignBytes;
-  const uint64_t units = (c.of[0].rows + c.of[1].rows) * c.chunks;
-  const uint64_t ctas = (units + kAlignThreads / 32 - 1) / (kAlignThreads / 32);
-  return launch_after(&align_rows_kernel, dim3(static_cast<unsigned>(std::min(ctas, kAlignCtas))),
-                      kAlignThreads, 0, s, c);
+  const AlignParams p = align_params(of, k);
+  return launch_after(&align_rows_kernel, dim3(align_ctas(p)), kAlignThreads, 0, s, p);
 }
 
 }  // namespace cpm
@@ -351,7 +284,7 @@ extern "C" uint64_t cp_matmul_fp8_workspace_bytes(const uint8_t* a, uint64_t a_s
       few_rows(m, n, k))
     return 0;
   return ((rows_ok(a, a_stride, m) ? 0 : m) + (rows_ok(w, w_stride, n) ? 0 : n)) *
-         aligned_pitch(k);
+         cpm::aligned_pitch(k);
 }
 
 extern "C" cp_status cp_matmul_fp8(const uint8_t* a, uint64_t a_stride, const float* a_scales,
@@ -400,7 +333,7 @@ extern "C" cp_status cp_matmul_fp8(const uint8_t* a, uint64_t a_stride, const fl
       return CP_ERR_INVALID_ARG;
     }
     cpm::AlignOperand of[2] = {};
-    const uint64_t pitch = aligned_pitch(k);
+    const uint64_t pitch = cpm::aligned_pitch(k);
     uint8_t* to = static_cast<uint8_t*>(workspace);
     if (!a_ok) {
       of[0] = cpm::AlignOperand{a, to, a_stride, m};
