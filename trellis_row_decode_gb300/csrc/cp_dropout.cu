@@ -3,8 +3,11 @@
 //
 //   out[i][j] = rn(residual[i][j] + D(x)[i][j])
 //
-// An octet a thread: two calls of the generator.  Bound by memory (x and the residual read, out
-// written).
+// An octet a thread: two calls of the generator.  In fp32, and in 16 bits with a residual, bound by
+// memory (65,536 x 1024 fp32 80 us, 6.7 TB/s; 196,608 x 1024 bf16 with a residual 186, 6.5 TB/s); in 16 bits
+// without one by the generator's 32 x 32 -> 64 bit products (158 us at 76 % of their pipe, where the copy
+// takes 119): so nothing else is left on that pipe (scales two at a time, values widened by byte
+// moves, flat addresses by addition).
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>

@@ -26,8 +26,10 @@ using cplin::Product;
 //
 // dz = D(dy) act'(pre), rounded to the products' type, and the sums of dz (before that rounding)
 // over blocks of rows.  A CTA has 256 columns (an octet a lane) and one of `count` shares of the
-// rows, eight at a time; its sums go to `parts`, which the products' kernel adds in order.  Bound by
-// memory: dy and pre read, dz written.
+// rows, eight at a time; its sums go to `parts`, which the products' kernel adds in order.  Column
+// sums alone are bound by memory (4096 x 4096: 10 us), slopes and the generator by their instructions
+// (270 an octet for silu and dropout, half of them the generator's: 28 us, silu alone 20, where dy, pre
+// and dz would take 15).
 
 constexpr int kGradThreads = 256;
 constexpr uint32_t kGradColumns = 256;
