@@ -110,6 +110,46 @@ def test_linear_strides_and_boundaries(m):
     _check(got, x.expand(m, k), w.expand(n, k), torch.float16, residual=res.expand(m, n))
 
 
+@pytest.mark.parametrize("m", [3, 300])
+@pytest.mark.parametrize("n", [121, 124, 126, 128, 130, 132, 136, 200])
+def test_linear_writes_its_columns_alone(m, n):
+    """Rows on 16-byte boundaries whose ends are not: what lies behind them stays, in each type, with
+    the residual and the kept sums on such rows too."""
+    x, w, g = _case(m, n, 72, torch.bfloat16)
+    for dtype in DTYPES:
+        buf = torch.full((m + 1, 208), 7.0, dtype=dtype, device="cuda")
+        keep = torch.full((m + 1, 208), 7.0, dtype=torch.bfloat16, device="cuda")
+        wide = torch.full((m, 208), float("nan"), dtype=dtype, device="cuda")
+        res = wide[:, :n]
+        res.copy_(randn(g, m, n, dtype=dtype))
+        for r in (None, res):
+            cp.linear(x.cuda(), w.cuda(), None, "relu", residual=r, out=buf[:m, :n],
+                      pre=keep[:m, :n])
+            out, z, mag = linear64(x, w, None, "relu", None if r is None else r.cpu())
+            assert_within(buf[:m, :n], out, out_bound(out, z, mag, 72, dtype))
+            assert_within(keep[:m, :n], z, sum_bound(mag, 72) + rounded(z, torch.bfloat16))
+            for t in (buf, keep):
+                assert bool((t[:, n:] == 7).all()) and bool((t[m] == 7).all())
+
+
+@pytest.mark.parametrize("m", [3, 300])
+@pytest.mark.parametrize("k", [1, 63, 65, 130, 201, 204, 519])
+def test_linear_reads_its_columns_alone(m, k):
+    """Rows on 16-byte boundaries with NaN behind their ends, for either operand."""
+    g = gen(m + k)
+    n, ld = 140, -(-k // 8) * 8 + 16
+    x = torch.full((m, ld), float("nan"), dtype=torch.float16)
+    w = torch.full((n, ld), float("nan"), dtype=torch.float16)
+    x[:, :k], w[:, :k] = randn(g, m, k, dtype=torch.float16), randn(g, n, k, dtype=torch.float16)
+    got = cp.linear(x.cuda()[:, :k], w.cuda()[:, :k], dtype=torch.float32)
+    _check(got, x[:, :k], w[:, :k], torch.float32)
+    dy = randn(g, m, n, dtype=torch.float16)
+    dx, dw, _ = cp.linear_grad(dy.cuda(), x.cuda()[:, :k], w.cuda()[:, :k])
+    X, W, D = x[:, :k].double(), w[:, :k].double(), dy.double()
+    assert_within(dx, D @ W, sum_bound(D.abs() @ W.abs(), n) + rounded(D @ W, torch.float16))
+    assert_within(dw, D.T @ X, sum_bound(D.abs().T @ X.abs(), m) + rounded(D.T @ X, torch.float16))
+
+
 @pytest.mark.parametrize("m", [1, 128, 129, 1000])
 def test_linear_sums_of_nothing(m):
     bias = torch.randn(70)

@@ -870,6 +870,11 @@ bool encode_block_map(CUtensorMap* map, const void* base, int dtype, uint64_t n,
 bool block_map_ok(const void* p, int dtype, uint64_t m, uint64_t ld) {
   return cpx::aligned(p, 16) && (m == 1 || (ld != 0 && ld * dtype_size(dtype) % 16 == 0));
 }
+// A store writes whole 16-byte pieces: of a row that ends inside one, what lies behind it too
+// (measured).  Loads end with the row's last element.
+bool store_map_ok(const void* p, int dtype, uint64_t n, uint64_t m, uint64_t ld) {
+  return block_map_ok(p, dtype, m, ld) && n * dtype_size(dtype) % 16 == 0;
+}
 
 // Columns of a tile and units that share its k, of each product of a launch.  By shapes alone, for
 // the 76 pairs of a whole card, so that a product's sums and its workspace are the same wherever it
@@ -1027,7 +1032,8 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
     const bool residual_ok =
         ep.residual == nullptr ||
         (f32 ? ep.aligned != 0 : block_map_ok(ep.residual, ep.out_dtype, ep.m, ep.ldr));
-    x.tma_out = t.splits == 1 && block_map_ok(ep.out, ep.out_dtype, ep.m, ep.ldo) && residual_ok;
+    x.tma_out = t.splits == 1 && residual_ok &&
+                store_map_ok(ep.out, ep.out_dtype, ep.n, ep.m, ep.ldo);
     x.tma_residual = x.tma_out && ep.residual != nullptr && !f32;
     if ((x.tma_out &&
          !encode_block_map(&p.map_out[at], ep.out, ep.out_dtype, ep.n, ep.m, ep.ldo)) ||
