@@ -139,3 +139,24 @@ def test_dropout_refusals():
     for p in (-0.01, 1.01, float("nan"), float("inf")):
         with pytest.raises(cp.CPError):
             cp.dropout(x, p)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [1, 7, 13, 63, 96, 101, 250])
+def test_dropout_keeps_to_its_columns(d, dtype):
+    """NaN behind the rows of the input and the residual stays out, what lies behind those of the
+    output stays; rows one behind the other too, where the next row follows at once."""
+    g = gen(d)
+    x, r = randn(g, 300, d, dtype=dtype), randn(g, 300, d, dtype=dtype)
+    wide = [torch.full((300, 256), float("nan"), dtype=dtype, device="cuda") for _ in range(2)]
+    wide[0][:, :d], wide[1][:, :d] = x.cuda(), r.cuda()
+    for residual in (None, wide[1][:, :d]):
+        out = torch.full((301, 256), 7.0, dtype=dtype, device="cuda")
+        cp.dropout(wide[0][:, :d], 0.3, 5, out=out[:300, :d], residual=residual)
+        _check(out[:300, :d], x, 0.3, 5, 0, None if residual is None else r)
+        assert bool((out[:, d:] == 7).all()) and bool((out[300] == 7).all())
+        flat = torch.full((302 * d,), 7.0, dtype=dtype, device="cuda")
+        cp.dropout(x.cuda(), 0.3, 5, out=flat[d:301 * d].view(300, d),
+                   residual=None if residual is None else r.cuda())
+        _check(flat[d:301 * d].view(300, d), x, 0.3, 5, 0, None if residual is None else r)
+        assert bool((flat[:d] == 7).all()) and bool((flat[301 * d:] == 7).all())

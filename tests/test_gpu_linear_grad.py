@@ -245,3 +245,34 @@ def test_linear_grad_refusals():
         cp.linear_grad(dy, x, w, p=2.0)
     with pytest.raises(cp.CPError):
         cp.linear_grad_workspace(1 << 30, 4, 4)
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("m", [5, 300])
+@pytest.mark.parametrize("n,k", [(121, 126), (130, 124), (77, 136), (136, 201)])
+def test_linear_grad_keeps_to_its_columns(m, n, k, act):
+    """Every array on 16-byte boundaries with rows that end inside 16 bytes: NaN behind the rows of
+    inputs stay out, what lies behind those of outputs stays."""
+    g = gen(m + n + k)
+
+    def rows(count, width):
+        t = torch.full((count, 216), float("nan"), dtype=torch.bfloat16, device="cuda")
+        t[:, :width] = randn(g, count, width, dtype=torch.bfloat16).cuda()
+        return t[:, :width]
+    dy, x, w, pre = rows(m, n), rows(m, k), rows(n, k), rows(m, n)
+    kw = {} if act == "none" else {"activation": act, "pre": pre}
+    ref = _reference(dy.cpu(), x.cpu(), w.cpu(), act, pre.cpu())
+    for dtype in (torch.bfloat16, torch.float32):
+        dx = torch.full((m + 1, 216), 7.0, dtype=torch.bfloat16, device="cuda")
+        dw = torch.full((n + 1, 216), 7.0, dtype=dtype, device="cuda")
+        db = torch.full((n + 1,), 7.0, device="cuda")
+        cp.linear_grad(dy, x, w, **kw, dx=dx[:m, :k], dw=dw[:n, :k], db=db[:n])
+        _check((dx[:m, :k], dw[:n, :k], db[:n]), ref, (torch.bfloat16, dtype, torch.float32))
+        assert bool((dx[:, k:] == 7).all()) and bool((dx[m] == 7).all())
+        assert bool((dw[:, k:] == 7).all()) and bool((dw[n] == 7).all()) and float(db[n]) == 7
+        dw.fill_(7.0)
+        cp.linear_grad(dy, x, w, **kw, need_dx=False, need_db=False, dw=dw[:n, :k], accumulate=True)
+        want = ref[1][0] + 7.0
+        assert_within(dw[:n, :k], want, ref[1][1] + 2 * U32 * (ref[1][0].abs() + 7)
+                      + rounded(want, dtype))
+        assert bool((dw[:, k:] == 7).all()) and bool((dw[n] == 7).all())
