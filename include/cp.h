@@ -582,10 +582,14 @@ cp_status cp_linear(const void* x, uint64_t x_stride, const void* w, uint64_t w_
  *   dx       [m][k] of dtype, row stride dx_stride >= k, or NULL.
  *   dw       [n][k] of dw_dtype, row stride dw_stride >= k, or NULL.
  *   db       [n] of db_dtype, or NULL.
- *   workspace  cp_linear_grad_workspace_bytes bytes, 16-byte aligned.
+ *   workspace  cp_linear_grad_call_bytes bytes for these arguments (NULL where that is 0), or
+ *            cp_linear_grad_workspace_bytes for any call of these sizes; 16-byte aligned.
  * m = 0 gives zeros for dw and db, n = 0 for dx.  m, n < 2^30, k < 2^30.
  */
 uint64_t cp_linear_grad_workspace_bytes(uint64_t m, uint64_t n, uint64_t k);
+uint64_t cp_linear_grad_call_bytes(const void* dy, int dy_dtype, uint64_t dy_stride, const void* x,
+                                   uint64_t x_stride, const void* w, uint64_t w_stride, int dtype,
+                                   uint64_t m, uint64_t n, uint64_t k, int activation, double p);
 cp_status cp_linear_grad(const void* dy, int dy_dtype, uint64_t dy_stride, const void* x,
                          uint64_t x_stride, const void* w, uint64_t w_stride, int dtype,
                          const void* pre, uint64_t pre_stride, uint64_t m, uint64_t n, uint64_t k,

@@ -237,8 +237,8 @@ def test_linear_grad_refusals():
                  lambda: cp.linear_grad(dy, x, w, db=f, db_dtype=torch.bfloat16),
                  lambda: cp.linear_grad(dy, x, w, db=torch.zeros(48, device="cuda")[::2]),
                  lambda: cp.linear_grad(dy.cpu(), x, w), lambda: cp.linear_grad(dy, x, w.float()),
-                 lambda: cp.linear_grad(dy, x, w, workspace=torch.empty(9, dtype=torch.uint8,
-                                                                        device="cuda"))]:
+                 lambda: cp.linear_grad(dy, x, w, "silu", pre,
+                                        workspace=torch.empty(9, dtype=torch.uint8, device="cuda"))]:
         with pytest.raises(ValueError):
             call()
     with pytest.raises(cp.CPError):

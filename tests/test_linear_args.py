@@ -93,8 +93,13 @@ def test_linear_grad_arguments(L, p):
                dict(pre=p, ps=8), dict(act=2, pre=p, ps=7), dict(act=2, pre=p + 1, ps=8),
                dict(p=1.5), dict(rng=p + 1), dict(dy=None), dict(x=None), dict(w=None),
                dict(dy=p + 1), dict(x=p + 1), dict(w=p + 1), dict(dx=p + 1), dict(dw=p + 2),
-               dict(db=p + 2), dict(dt=0, dy=p + 2), dict(wk=None), dict(wk=p + 8), dict(wb=64)]:
+               dict(db=p + 2), dict(dt=0, dy=p + 2)]:
         assert call(**kw) == BAD, kw
+    # an activation, dropout, dy in 32 bits or off 16 bytes, x or w off them: each wants a workspace
+    for kw in [dict(act=2, pre=p, ps=8), dict(p=0.5), dict(dt=0), dict(ds=9), dict(xs=17),
+               dict(w=p + 2), dict(m=600, ds=8)]:
+        for ws in [dict(wk=None), dict(wk=p + 8), dict(wb=16)]:
+            assert call(**kw, **ws) == BAD, (kw, ws)
     assert call(dx=None, dw=None, db=None) == 0 and call(n=0, dx=None, db=None, k=0, dw=None) == 0
 
 
@@ -116,6 +121,13 @@ def test_linear_workspace_sizes(L, p):
     assert grad(1 << 30, 4, 4) == 0 and grad(4, 1 << 30, 4) == 0 and grad(4, 4, 1 << 30) == 0
     assert 6 * m * (m + 1) <= grad(m, m, m) < 1 << 63
     assert grad(0, 0, 0) == 16 and grad(0, 5, 7) >= 16
+    one = L.cp_linear_grad_call_bytes
+    assert one(p, 2, 504, p, 64, p, 64, 2, 100, 500, 64, 0, 0.0) == 0
+    assert one(p, 2, 504, p, 64, p, 64, 2, 100, 500, 64, 0, 0.1) >= 100 * 504 * 2
+    assert one(p, 2, 500, p, 65, p, 64, 2, 100, 500, 65, 0, 0.0) >= (504 + 72) * 200
+    for m, n, k in [(1, 1, 1), (100, 500, 65), (5000, 64, 3000), (300, 4000, 20000)]:
+        for dy, act in [(p, 0), (p + 2, 0), (p, 2)]:
+            assert one(dy, 2, n, p + 2, k, p + 2, k, 2, m, n, k, act, 0.0) <= grad(m, n, k)
 
 
 def test_compiled_calls_leave_other_forms_alone():

@@ -249,18 +249,21 @@ PyObject* linear_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (dw_code < 0 || db_code < 0) return other_way();
   const uint64_t m = static_cast<uint64_t>(x.rows()), wide = static_cast<uint64_t>(w.dims[0]),
                  k = static_cast<uint64_t>(x.last());
-  const uint64_t bytes = cp_linear_grad_workspace_bytes(m, wide, k);
+  const uint64_t bytes = cp_linear_grad_call_bytes(dy.data, dy_code, wide, x.data, k, w.data, k, code,
+                                                   m, wide, k, static_cast<int>(act), d.p);
   const long long size = static_cast<long long>(bytes);
-  Ref device(PyObject_GetAttr(a[1], s_device));
-  if (bytes == 0 || device.p == nullptr) return other_way();
+  Ref device(PyObject_GetAttr(a[1], s_device)), ws;
+  if (device.p == nullptr) return other_way();
   Ref dx(empty(x.dims, x.n_dims, x.dtype.p, device.p, &dx_data));
   if (dx.p == nullptr) return other_way();
   Ref dw(empty(w.dims, 2, dw_type, device.p, &dw_data));
   if (dw.p == nullptr) return other_way();
   Ref db(empty(w.dims, 1, db_type, device.p, &db_data));
   if (db.p == nullptr) return other_way();
-  Ref ws(empty(&size, 1, t_u8, device.p, &ws_data));
-  if (ws.p == nullptr) return other_way();
+  if (bytes != 0) {
+    ws.p = empty(&size, 1, t_u8, device.p, &ws_data);
+    if (ws.p == nullptr) return other_way();
+  }
   if (cp_linear_grad(dy.data, dy_code, wide, x.data, k, w.data, k, code, z.data, wide, m, wide, k,
                      static_cast<int>(act), d.p, d.seed, d.offset, d.rng, 0, dx_data, k, dw_data,
                      dw_code, k, db_data, db_code, ws_data, bytes, stream) != CP_OK)

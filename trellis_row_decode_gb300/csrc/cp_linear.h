@@ -25,13 +25,15 @@ struct Product {
   cpe::Epilogue e;
 };
 
-// Sums over rows that another kernel left in parts: out[j] (+)= sum of parts[i][j].
+// Sums over rows: out[j] (+)= sum of parts[i][j], which another kernel left, or of rows of 16 bits
+// themselves (few of them, on 16-byte boundaries).
 struct ColumnSums {
   const float* parts;      // [count][pitch]
+  const void* rows;        // [count][pitch] of rows_dtype, or null
   void* out;               // null: none
   uint64_t pitch;
   uint32_t count, n;
-  int dtype, accumulate;
+  int dtype, accumulate, rows_dtype;
 };
 
 // Products of one launch on CTA pairs (cp_linear_tc.cu), two at most; `part` holds

@@ -60,7 +60,10 @@ def _lib():
                                      i32, f64, u64, u64, vp, i32, vp, u64, vp, i32, u64, vp, i32,
                                      vp, u64, vp]
         L.cp_linear_status.argtypes = [vp]
-        for f in (L.cp_linear_workspace_bytes, L.cp_linear_grad_workspace_bytes):
+        L.cp_linear_grad_call_bytes.argtypes = [vp, i32, u64, vp, u64, vp, u64, i32, u64, u64, u64,
+                                                i32, f64]
+        for f in (L.cp_linear_workspace_bytes, L.cp_linear_grad_workspace_bytes,
+                  L.cp_linear_grad_call_bytes):
             f.restype = u64
         for f in (L.cp_dropout, L.cp_linear, L.cp_linear_grad, L.cp_linear_status):
             f.restype = i32
@@ -293,13 +296,15 @@ def linear_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, activat
         raise ValueError("db is given, but not needed")
     gp = _rng(seed, offset, rng, dev)
     L = _lib()
-    nbytes = L.cp_linear_grad_workspace_bytes(m, n, k)
-    ws = _workspace(workspace, nbytes, x, dev, stream)
-    _check(L.cp_linear_grad(_on(dy, dev, "dy"), code if dy.dtype == x.dtype else CP_F32, lddy,
-                            x.data_ptr(), ldx, _on(weight, dev, "weight"), ldw, code, pp, ps, m, n,
-                            k, act, p, seed, offset, gp, 1 if accumulate else 0, dxp, dxs, dwp, dwc,
-                            dws, dbp, dbc, ws.data_ptr(), nbytes, _stream(stream, dev)),
-           "cp_linear_grad")
+    gradient = (_on(dy, dev, "dy"), code if dy.dtype == x.dtype else CP_F32, lddy, x.data_ptr(),
+                ldx, _on(weight, dev, "weight"), ldw, code)
+    nbytes, sp = L.cp_linear_grad_call_bytes(*gradient, m, n, k, act, p), None
+    if nbytes:
+        workspace = _workspace(workspace, nbytes, x, dev, stream)
+        sp = workspace.data_ptr()
+    _check(L.cp_linear_grad(*gradient, pp, ps, m, n, k, act, p, seed, offset, gp,
+                            1 if accumulate else 0, dxp, dxs, dwp, dwc, dws, dbp, dbc, sp, nbytes,
+                            _stream(stream, dev)), "cp_linear_grad")
     return dx, dw, db
 
 
