@@ -171,11 +171,30 @@ __device__ __forceinline__ float sigmoid(float t) {
   return r;
 }
 
+// Phi(z), the normal distribution: erfc(|x|) = (a1 t + .. + a5 t^5) e^(-x^2), t = 1 / (1 + p |x|),
+// x = z / sqrt(2), to 1.5e-7 (Abramowitz and Stegun, "Handbook of Mathematical Functions", 7.1.26), a
+// third of the instructions of an error function to the last place.  Of the lower tail itself, so
+// nothing cancels there.  `bell`: e^(-z^2 / 2).
+__device__ __forceinline__ float normal_cdf(float z, float& bell) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  float t;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.3275911f, x, 1.0f)));
+  bell = exp2_approx(-kLog2E * x * x);
+  const float poly =
+      t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f),
+                       -0.284496736f), 0.254829592f);
+  const float tail = 0.5f * poly * bell;
+  return z < 0.0f ? tail : 1.0f - tail;
+}
+
 template <int kAct>
 __device__ __forceinline__ float act(float z) {
   if constexpr (kAct == CP_ACT_RELU) return z < 0.0f ? 0.0f : z;
   if constexpr (kAct == CP_ACT_SILU) return z * sigmoid(z);
-  if constexpr (kAct == CP_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+  if constexpr (kAct == CP_ACT_GELU) {
+    float bell;
+    return z * normal_cdf(z, bell);
+  }
   if constexpr (kAct == CP_ACT_GELU_TANH)
     return z * sigmoid(kTanhScale * (z + kTanhCube * z * z * z));
   return z;
@@ -189,9 +208,11 @@ __device__ __forceinline__ float slope(float z) {
     const float s = sigmoid(z);
     return s * (1.0f + z * (1.0f - s));
   }
-  if constexpr (kAct == CP_ACT_GELU)
-    return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
-           z * 0.39894228040143268f * exp2_approx(-0.5f * kLog2E * z * z);
+  if constexpr (kAct == CP_ACT_GELU) {
+    float bell;
+    const float cdf = normal_cdf(z, bell);
+    return cdf + z * 0.39894228040143268f * bell;
+  }
   if constexpr (kAct == CP_ACT_GELU_TANH) {
     const float s = sigmoid(kTanhScale * (z + kTanhCube * z * z * z));
     const float bend = s * (1.0f - s);                 // 0 far out, where z^2 may overflow
