@@ -151,6 +151,16 @@ bool read_drop(PyObject* const* a, const Tensor& x, Drop* d) {
 
 constexpr long long kMostRow = (1ll << 32) - 1;
 
+// The library's call, other threads running meanwhile: a launch waits where the stream's queue is
+// full, and what it waits for may itself want the interpreter.
+template <typename F>
+cp_status unlocked(F call) {
+  PyThreadState* state = PyEval_SaveThread();
+  const cp_status status = call();
+  PyEval_RestoreThread(state);
+  return status;
+}
+
 // dropout(x, residual, p, seed, offset, rng)
 PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor x, r;
@@ -168,9 +178,11 @@ PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Ref out(device.p == nullptr ? nullptr : empty(x.dims, x.n_dims, x.dtype.p, device.p, &data));
   if (out.p == nullptr) return other_way();
   const uint64_t width = static_cast<uint64_t>(x.last());
-  if (cp_dropout(x.data, width, r.data, width, code, static_cast<uint64_t>(x.rows()),
-                 static_cast<uint32_t>(width), d.p, d.seed, d.offset, d.rng, data, width,
-                 stream) != CP_OK)
+  const uint64_t rows = static_cast<uint64_t>(x.rows());
+  if (unlocked([&] {
+        return cp_dropout(x.data, width, r.data, width, code, rows, static_cast<uint32_t>(width), d.p,
+                          d.seed, d.offset, d.rng, data, width, stream);
+      }) != CP_OK)
     return other_way();
   return out.take();
 }
@@ -217,9 +229,11 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     ws.p = empty(&size, 1, t_u8, device.p, &ws_data);
     if (ws.p == nullptr) return other_way();
   }
-  if (cp_linear(x.data, k, w.data, k, code, m, wide, k, b.data, bias_code, static_cast<int>(act),
-                d.p, d.seed, d.offset, d.rng, r.data, wide, out_data, out_code, wide, pre_data, wide,
-                ws_data, bytes, stream) != CP_OK)
+  if (unlocked([&] {
+        return cp_linear(x.data, k, w.data, k, code, m, wide, k, b.data, bias_code,
+                         static_cast<int>(act), d.p, d.seed, d.offset, d.rng, r.data, wide, out_data,
+                         out_code, wide, pre_data, wide, ws_data, bytes, stream);
+      }) != CP_OK)
     return other_way();
   return pre.p == nullptr ? out.take() : PyTuple_Pack(2, out.p, pre.p);
 }
@@ -264,9 +278,12 @@ PyObject* linear_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     ws.p = empty(&size, 1, t_u8, device.p, &ws_data);
     if (ws.p == nullptr) return other_way();
   }
-  if (cp_linear_grad(dy.data, dy_code, wide, x.data, k, w.data, k, code, z.data, wide, m, wide, k,
-                     static_cast<int>(act), d.p, d.seed, d.offset, d.rng, 0, dx_data, k, dw_data,
-                     dw_code, k, db_data, db_code, ws_data, bytes, stream) != CP_OK)
+  if (unlocked([&] {
+        return cp_linear_grad(dy.data, dy_code, wide, x.data, k, w.data, k, code, z.data, wide, m,
+                              wide, k, static_cast<int>(act), d.p, d.seed, d.offset, d.rng, 0,
+                              dx_data, k, dw_data, dw_code, k, db_data, db_code, ws_data, bytes,
+                              stream);
+      }) != CP_OK)
     return other_way();
   return PyTuple_Pack(3, dx.p, dw.p, db.p);
 }
