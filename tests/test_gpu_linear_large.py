@@ -79,3 +79,21 @@ def test_linear_rows_far_apart(m):
     cp.dropout(x[:, :n], 0.5, 3, out=out)
     want = drop64(xs[:, :n].double(), 0.5, 3, 0)
     assert_within(out, want, 2 * U32 * want.abs() + rounded(want, torch.bfloat16))
+
+
+def test_linear_sums_a_long_k():
+    """131,072 positive products a sum: what the sums lose to one side shows in the outputs' mean
+    error, where their own roundings cancel."""
+    m, n, k = 2560, 2560, 1 << 17
+    at = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.rand(m, k, generator=at, device="cuda", dtype=torch.float16)
+    w = torch.rand(n, k, generator=at, device="cuda", dtype=torch.float16)
+    w *= (torch.rand(n, 1, generator=at, device="cuda") * 0.25 + 0.25).half()
+    out = cp.linear(x, w)
+    ref, z, mag = linear64(x[::20].cpu(), w[::20].cpu())
+    got = out[::20, ::20].cpu().double()
+    assert_within(got, ref, out_bound(ref, z, mag, k, torch.float16))
+    # 16,384 roundings of up to 2^-11 each have a mean of 2.2e-6 (one deviation); sums of 512 cut at
+    # each addition, joined by additions that round, lose up to 5.5e-7 + 256 U32
+    assert ((got - ref) / ref).mean().abs() < 5 * 2.2e-6 + 5.5e-7 + 256 * U32
+    assert cp.linear_status() == cp.CP_OK

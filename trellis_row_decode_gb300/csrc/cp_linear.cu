@@ -301,6 +301,10 @@ uint64_t grad_part_bytes(uint64_t m, uint64_t n, uint64_t k) {
 uint64_t dz_bytes(uint64_t m, uint64_t n) { return 2 * m * row_pitch(n); }
 uint64_t db_bytes(uint64_t m, uint64_t n) { return 4ull * grad_parts(m, n, false) * row_pitch(n); }
 
+// Whether the products' kernel makes the column sums from dy's rows.  (Not beside a dx whose k is so
+// long that its sums are read in segments: the warps in question have few registers there.)
+bool direct_sums(uint64_t m, uint64_t n) { return m <= kDirectRows && n <= cplin::kLongSum; }
+
 // Whether dz is dy itself.
 bool dy_as_is(const void* dy, int dy_dtype, uint64_t dy_stride, int dtype, uint64_t m,
               int activation, double p) {
@@ -322,7 +326,7 @@ extern "C" uint64_t cp_linear_grad_call_bytes(const void* dy, int dy_dtype, uint
                                               uint64_t k, int activation, double p) {
   if (m >= kMostK || n >= kMostK || k >= kMostK || m == 0 || n == 0) return 0;
   const bool as_is = dy_as_is(dy, dy_dtype, dy_stride, dtype, m, activation, p);
-  return (as_is ? 0 : dz_bytes(m, n)) + (as_is && m <= kDirectRows ? 0 : db_bytes(m, n)) +
+  return (as_is ? 0 : dz_bytes(m, n)) + (as_is && direct_sums(m, n) ? 0 : db_bytes(m, n)) +
          ((rows_ok(x, x_stride, m) ? 0 : m) + (rows_ok(w, w_stride, n) ? 0 : n)) * 2 *
              row_pitch(k) +
          grad_part_bytes(m, n, k);
@@ -382,7 +386,7 @@ extern "C" cp_status cp_linear_grad(const void* dy, int dy_dtype, uint64_t dy_st
     sums.n = static_cast<uint32_t>(n);
     sums.dtype = db_dtype;
     sums.accumulate = accumulate;
-    if (as_is && m <= kDirectRows) {
+    if (as_is && direct_sums(m, n)) {
       sums.rows = dy;
       sums.rows_dtype = dy_dtype;
       sums.pitch = dy_stride;

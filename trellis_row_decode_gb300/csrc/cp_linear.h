@@ -43,6 +43,10 @@ uint64_t part_floats(const uint32_t* m, const uint32_t* n, const uint32_t* k, in
 cp_status launch_products(const Product* q, int count, const ColumnSums& sums, float* part,
                           cudaStream_t s);
 
+// k of a unit above which sums are read in segments for 16-bit outputs too: the tensor core's own error
+// is 7e-5 there, where fp16's rounding is 4.9e-4.
+constexpr uint32_t kLongSum = 65536;
+
 // Up to kThinRows rows of a: tiles of 128 rows of b, neither operand stored across.
 constexpr uint32_t kThinRows = 128;
 cp_status launch_thin(const Product& q, cudaStream_t s);

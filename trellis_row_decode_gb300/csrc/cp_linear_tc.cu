@@ -201,10 +201,10 @@ __device__ __forceinline__ void sum_rows(const ColumnSums& p, uint32_t c, uint32
 }
 
 // kRich: some product has an activation, dropout, or sums to keep.
-// kSegments: some product is wanted in 32 bits.  The tensor core cuts its running sum at every
-// addition instead of rounding it, an error that grows with k (measured, relative: 1.07e-9 k,
-// 4.4e-6 at k = 4096, where fp32 additions that round leave 6e-7); so the sum is read every kSegment
-// stages and added up in registers.
+// kSegments: some product is wanted in 32 bits, or has more than kLongSum of k in a unit.  The tensor
+// core cuts its running sum at every addition instead of rounding it, an error that grows with k
+// (measured, relative: 1.07e-9 k, 4.4e-6 at k = 4096, where fp32 additions that round leave 6e-7);
+// so the sum is read every kSegment of k and added up in registers.
 template <bool kRich, bool kSegments>
 __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constant__ PairParams p) {
   extern __shared__ uint8_t dyn[];
@@ -1060,7 +1060,7 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
     x.b_boxes = x.b_across ? (t.bn / 2 + 63) / 64 : 1;
     x.b_bytes = x.b_across ? x.b_boxes * kBlock : t.bn / 2 * 128;
     x.instr = cpt::half_instr_desc(256, t.bn, q[i].dtype == CP_BF16, x.a_across, x.b_across);
-    segments |= ep.out_dtype == CP_F32 && q[i].k / t.splits > kSegment;
+    segments |= q[i].k / t.splits > (ep.out_dtype == CP_F32 ? kSegment : kLongSum);
     if (t.splits > 1) {
       x.pitch = part_pitch(ep.n);
       x.part = part;
