@@ -75,8 +75,8 @@ __device__ __forceinline__ void align_rows_of(const AlignParams& p, uint32_t cta
 
 inline uint64_t aligned_pitch(uint64_t k) { return (k + 15) / 16 * 16; }
 
-inline AlignParams align_params(const AlignOperand (&of)[2], uint32_t k) {
-  return AlignParams{{of[0], of[1]}, k, (k + kAlignBytes - 1) / kAlignBytes, aligned_pitch(k)};
+inline AlignParams align_params(const AlignOperand (&of)[2], uint32_t k, uint64_t pitch) {
+  return AlignParams{{of[0], of[1]}, k, (k + kAlignBytes - 1) / kAlignBytes, pitch};
 }
 inline uint32_t align_ctas(const AlignParams& p) {
   const uint64_t units = (p.of[0].rows + p.of[1].rows) * p.chunks;

@@ -402,6 +402,35 @@ __device__ __forceinline__ void transpose32(float (&x)[32], uint32_t lane) {
   }
 }
 
+// A column of up to 32 rows, ld elements apart: written, or added to v.  (One test of the type, not one
+// a row.)
+template <typename T>
+__device__ __forceinline__ void store_column_of(T* to, uint64_t ld, uint32_t rows,
+                                                const float (&v)[32]) {
+#pragma unroll
+  for (uint32_t r = 0; r < 32; ++r, to += ld)
+    if (r < rows) *to = from_f32<T>(v[r]);
+}
+__device__ __forceinline__ void store_column(void* p, uint64_t at, uint64_t ld, uint32_t rows,
+                                             int dtype, const float (&v)[32]) {
+  if (dtype == CP_F32) store_column_of(static_cast<float*>(p) + at, ld, rows, v);
+  else if (dtype == CP_F16) store_column_of(static_cast<__half*>(p) + at, ld, rows, v);
+  else store_column_of(static_cast<__nv_bfloat16*>(p) + at, ld, rows, v);
+}
+template <typename T>
+__device__ __forceinline__ void add_column_of(const T* from, uint64_t ld, uint32_t rows,
+                                              float (&v)[32]) {
+#pragma unroll
+  for (uint32_t r = 0; r < 32; ++r, from += ld)
+    if (r < rows) v[r] += to_f32(*from);
+}
+__device__ __forceinline__ void add_column(float (&v)[32], const void* p, uint64_t at, uint64_t ld,
+                                           uint32_t rows, int dtype) {
+  if (dtype == CP_F32) add_column_of(static_cast<const float*>(p) + at, ld, rows, v);
+  else if (dtype == CP_F16) add_column_of(static_cast<const __half*>(p) + at, ld, rows, v);
+  else add_column_of(static_cast<const __nv_bfloat16*>(p) + at, ld, rows, v);
+}
+
 // The epilogue of a warp's 32 rows (row0 on, one a lane) by 32 columns (col on, a multiple of 32)
 // of sums, in two steps.  The first: bias, kept sums, activation, dropout.  `bias`: a lane has that
 // of column col + lane.  fast: rows on 32-byte boundaries and columns all there, so a lane reads
@@ -425,13 +454,9 @@ __device__ __forceinline__ void shape_block(const Epilogue& e, const DropKey& ke
 #pragma unroll
         for (int i = 0; i < 32; ++i) u[i] = v[i];
         transpose32(u, lane);
-        if (col + lane < e.n) {
-          const uint32_t rows = min(32u, e.m - row0);
-          const uint64_t at = static_cast<uint64_t>(row0) * e.ldp + col + lane;
-#pragma unroll
-          for (uint32_t r = 0; r < 32; ++r)
-            if (r < rows) store_from_f32(e.pre, at + r * e.ldp, e.pre_dtype, u[r]);
-        }
+        if (col + lane < e.n)
+          store_column(e.pre, static_cast<uint64_t>(row0) * e.ldp + col + lane, e.ldp,
+                       min(32u, e.m - row0), e.pre_dtype, u);
         __syncwarp();
       }
     }
@@ -462,16 +487,11 @@ __device__ __forceinline__ void write_block(const Epilogue& e, uint32_t row0, ui
   const uint32_t rows = min(32u, e.m - row0);
   transpose32(v, lane);
   if (col + lane < e.n) {
-    if (e.residual != nullptr) {
-      const uint64_t at = static_cast<uint64_t>(row0) * e.ldr + col + lane;
-#pragma unroll
-      for (uint32_t r = 0; r < 32; ++r)
-        if (r < rows) v[r] += load_as_f32(e.residual, at + r * e.ldr, e.out_dtype);
-    }
-    const uint64_t at = static_cast<uint64_t>(row0) * e.ldo + col + lane;
-#pragma unroll
-    for (uint32_t r = 0; r < 32; ++r)
-      if (r < rows) store_from_f32(e.out, at + r * e.ldo, e.out_dtype, v[r]);
+    if (e.residual != nullptr)
+      add_column(v, e.residual, static_cast<uint64_t>(row0) * e.ldr + col + lane, e.ldr, rows,
+                 e.out_dtype);
+    store_column(e.out, static_cast<uint64_t>(row0) * e.ldo + col + lane, e.ldo, rows, e.out_dtype,
+                 v);
   }
   __syncwarp();
 }

@@ -266,8 +266,8 @@ cp_status launch_few(const MatmulParams& p, bool aligned, cudaStream_t s) {
 
 namespace cpm {
 
-cudaError_t align_rows(const AlignOperand (&of)[2], uint32_t k, cudaStream_t s) {
-  const AlignParams p = align_params(of, k);
+cudaError_t align_rows(const AlignOperand (&of)[2], uint32_t k, uint64_t pitch, cudaStream_t s) {
+  const AlignParams p = align_params(of, k, pitch);
   return launch_after(&align_rows_kernel, dim3(align_ctas(p)), kAlignThreads, 0, s, p);
 }
 
@@ -346,7 +346,7 @@ extern "C" cp_status cp_matmul_fp8(const uint8_t* a, uint64_t a_stride, const fl
       p.w = to;
       p.ldw = pitch;
     }
-    const cudaError_t e = cpm::align_rows(of, p.k, s);
+    const cudaError_t e = cpm::align_rows(of, p.k, cpm::aligned_pitch(p.k), s);
     if (e != cudaSuccess) return cpx::cuda_fail(e, "fp8 matmul launch");
   }
   return m > kThinRows ? cpm::launch_pairs(p, s) : cpm::launch_thin(p, s);

@@ -28,13 +28,13 @@ cp_status launch_pairs(const MatmulParams& p, cudaStream_t s);
 // Up to 128 rows of a: tiles of 128 rows of w and up to 64 rows of a.
 cp_status launch_thin(const MatmulParams& p, cudaStream_t s);
 
-// Rows of k bytes on any boundary copied to rows on 16-byte ones, `pitch` = k rounded up to 16
-// apart, zeros behind their ends; two operands in one launch (rows 0: one that stays).
+// Rows of k bytes on any boundary copied to rows on 16-byte ones, `pitch` apart (a multiple of 16, at
+// least k), zeros behind their ends to the next of those; two operands in one launch (rows 0: one that stays).
 struct AlignOperand {
   const uint8_t* from;
   uint8_t* to;
   uint64_t ld, rows;       // ld in bytes
 };
-cudaError_t align_rows(const AlignOperand (&of)[2], uint32_t k, cudaStream_t s);
+cudaError_t align_rows(const AlignOperand (&of)[2], uint32_t k, uint64_t pitch, cudaStream_t s);
 
 }  // namespace cpm
