@@ -21,6 +21,8 @@ using cpe::DropParams;
 using cplin::ColumnSums;
 using cplin::Operand;
 using cplin::Product;
+using cplin::Tiling;
+using cplin::Tilings;
 
 // ------------------------------------------------------------------ dz and its column sums
 //
@@ -208,9 +210,19 @@ bool to_align(Operand* (&op)[2], const uint64_t (&rows)[2], uint64_t k, uint8_t*
 
 // Bytes for the sums of products whose k is split; they begin on a 32-byte boundary, the workspace
 // on a 16-byte one.
-uint64_t part_bytes(const uint32_t* m, const uint32_t* n, const uint32_t* k, int count) {
-  const uint64_t floats = cplin::part_floats(m, n, k, count);
+uint64_t part_bytes(const Tilings& t, int first, int count) {
+  const uint64_t floats = cplin::part_floats(t, first, count);
   return floats == 0 ? 0 : 4 * floats + 16;
+}
+Tilings linear_tilings(uint64_t m, uint64_t n, uint64_t k) {
+  const uint32_t ms = static_cast<uint32_t>(m), ns = static_cast<uint32_t>(n),
+                 ks = static_cast<uint32_t>(k);
+  return cplin::tilings(&ms, &ns, &ks, 1);
+}
+// Bytes for the copies of operands that lie on other boundaries.
+uint64_t copy_bytes(const void* x, uint64_t x_stride, const void* w, uint64_t w_stride, uint64_t m,
+                    uint64_t n, uint64_t k) {
+  return ((rows_ok(x, x_stride, m) ? 0 : m) + (rows_ok(w, w_stride, n) ? 0 : n)) * 2 * row_pitch(k);
 }
 float* part_at(uint8_t* p) {
   return reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(p) + 31) & ~static_cast<uintptr_t>(31));
@@ -222,11 +234,8 @@ extern "C" uint64_t cp_linear_workspace_bytes(const void* x, uint64_t x_stride, 
                                               uint64_t w_stride, uint64_t m, uint64_t n,
                                               uint64_t k) {
   if (m >= kMostRows || n >= kMostRows || k >= kMostK || m == 0 || n == 0 || k == 0) return 0;
-  const uint32_t ms = static_cast<uint32_t>(m), ns = static_cast<uint32_t>(n),
-                 ks = static_cast<uint32_t>(k);
-  return ((rows_ok(x, x_stride, m) ? 0 : m) + (rows_ok(w, w_stride, n) ? 0 : n)) * 2 *
-             row_pitch(k) +
-         (m > cplin::kThinRows ? part_bytes(&ms, &ns, &ks, 1) : 0);
+  return copy_bytes(x, x_stride, w, w_stride, m, n, k) +
+         (m > cplin::kThinRows ? part_bytes(linear_tilings(m, n, k), 0, 1) : 0);
 }
 
 extern "C" cp_status cp_linear(const void* x, uint64_t x_stride, const void* w, uint64_t w_stride,
@@ -252,7 +261,18 @@ extern "C" cp_status cp_linear(const void* x, uint64_t x_stride, const void* w, 
       !cpx::aligned(pre, 2) || (bias != nullptr && !cpx::aligned(bias, dtype_size(bias_dtype))) ||
       (k != 0 && (x == nullptr || w == nullptr || !cpx::aligned(x, 2) || !cpx::aligned(w, 2))))
     return refuse("null or misaligned x, w, bias, residual, out or pre");
-  const uint64_t need = cp_linear_workspace_bytes(x, x_stride, w, w_stride, m, n, k);
+  const bool thin = m <= cplin::kThinRows;
+  Tilings ways{};
+  Tiling chosen{};
+  uint64_t need = 0;
+  if (k != 0) {
+    need = copy_bytes(x, x_stride, w, w_stride, m, n, k);
+    if (!thin) {
+      ways = linear_tilings(m, n, k);
+      cplin::choose(ways, 0, 1, &chosen);
+      need += part_bytes(ways, 0, 1);
+    }
+  }
   if (need != 0 &&
       (workspace == nullptr || !cpx::aligned(workspace, 16) || workspace_bytes < need))
     return refuse("workspace must be 16-byte aligned and hold cp_linear_workspace_bytes bytes");
@@ -277,7 +297,7 @@ extern "C" cp_status cp_linear(const void* x, uint64_t x_stride, const void* w, 
   q.e.aligned = cpx::aligned(out, 32) && out_stride * elt % 32 == 0 &&
                 cpx::aligned(residual, 32) && residual_stride * elt % 32 == 0 &&
                 cpx::aligned(pre, 32) && pre_stride * 2 % 32 == 0;
-  if (k == 0) return cplin::launch_products(&q, 1, ColumnSums{}, nullptr, s);
+  if (k == 0) return cplin::launch_products(&q, 1, &chosen, ColumnSums{}, nullptr, s);
   uint8_t* at = static_cast<uint8_t*>(workspace);
   Operand* op[2] = {&q.a, &q.b};
   cpm::AlignOperand of[2];
@@ -285,21 +305,24 @@ extern "C" cp_status cp_linear(const void* x, uint64_t x_stride, const void* w, 
     const cudaError_t e = cpm::align_rows(of, static_cast<uint32_t>(2 * k), 2 * row_pitch(k), s);
     if (e != cudaSuccess) return cpx::cuda_fail(e, "linear launch");
   }
-  if (m <= cplin::kThinRows) return cplin::launch_thin(q, s);
-  return cplin::launch_products(&q, 1, ColumnSums{}, part_at(at), s);
+  if (thin) return cplin::launch_thin(q, s);
+  return cplin::launch_products(&q, 1, &chosen, ColumnSums{}, part_at(at), s);
 }
 
 namespace {
 
-// Bytes for the sums of a gradient's products, of both together or of either where the other is not
-// wanted.
-uint64_t grad_part_bytes(uint64_t m, uint64_t n, uint64_t k) {
-  if (m == 0 || n == 0 || k == 0) return 0;
+// The ways of a gradient's products, dx and dw.
+Tilings grad_tilings(uint64_t m, uint64_t n, uint64_t k) {
+  if (m == 0 || n == 0 || k == 0) return Tilings{};
   const uint32_t ms[2] = {static_cast<uint32_t>(m), static_cast<uint32_t>(n)};
   const uint32_t ns[2] = {static_cast<uint32_t>(k), static_cast<uint32_t>(k)};
   const uint32_t ks[2] = {static_cast<uint32_t>(n), static_cast<uint32_t>(m)};
-  return std::max({part_bytes(ms, ns, ks, 2), part_bytes(ms, ns, ks, 1),
-                   part_bytes(ms + 1, ns + 1, ks + 1, 1)});
+  return cplin::tilings(ms, ns, ks, 2);
+}
+// Bytes for their sums, of both together or of either where the other is not wanted.
+uint64_t grad_part_bytes(const Tilings& t) {
+  if (t.m[0] == 0) return 0;
+  return std::max({part_bytes(t, 0, 2), part_bytes(t, 0, 1), part_bytes(t, 1, 1)});
 }
 uint64_t dz_bytes(uint64_t m, uint64_t n) { return 2 * m * row_pitch(n); }
 uint64_t db_bytes(uint64_t m, uint64_t n) { return 4ull * grad_parts(m, n, false) * row_pitch(n); }
@@ -314,13 +337,20 @@ bool dy_as_is(const void* dy, int dy_dtype, uint64_t dy_stride, int dtype, uint6
   return activation == CP_ACT_NONE && p == 0.0 && dy_dtype == dtype && rows_ok(dy, dy_stride, m);
 }
 
+// Bytes of a call with m and n above 0.
+uint64_t grad_bytes(const Tilings& t, bool as_is, const void* x, uint64_t x_stride, const void* w,
+                    uint64_t w_stride, uint64_t m, uint64_t n, uint64_t k) {
+  return (as_is ? 0 : dz_bytes(m, n)) + (as_is && direct_sums(m, n) ? 0 : db_bytes(m, n)) +
+         copy_bytes(x, x_stride, w, w_stride, m, n, k) + grad_part_bytes(t);
+}
+
 }  // namespace
 
 extern "C" uint64_t cp_linear_grad_workspace_bytes(uint64_t m, uint64_t n, uint64_t k) {
   if (m >= kMostK || n >= kMostK || k >= kMostK) return 0;
   // dz, copies of x and w, the parts of db, the sums of products whose k is split
   return std::max<uint64_t>(16, dz_bytes(m, n) + 2 * (m + n) * row_pitch(k) + db_bytes(m, n) +
-                                    grad_part_bytes(m, n, k));
+                                    grad_part_bytes(grad_tilings(m, n, k)));
 }
 
 extern "C" uint64_t cp_linear_grad_call_bytes(const void* dy, int dy_dtype, uint64_t dy_stride,
@@ -328,11 +358,9 @@ extern "C" uint64_t cp_linear_grad_call_bytes(const void* dy, int dy_dtype, uint
                                               uint64_t w_stride, int dtype, uint64_t m, uint64_t n,
                                               uint64_t k, int activation, double p) {
   if (m >= kMostK || n >= kMostK || k >= kMostK || m == 0 || n == 0) return 0;
-  const bool as_is = dy_as_is(dy, dy_dtype, dy_stride, dtype, m, activation, p);
-  return (as_is ? 0 : dz_bytes(m, n)) + (as_is && direct_sums(m, n) ? 0 : db_bytes(m, n)) +
-         ((rows_ok(x, x_stride, m) ? 0 : m) + (rows_ok(w, w_stride, n) ? 0 : n)) * 2 *
-             row_pitch(k) +
-         grad_part_bytes(m, n, k);
+  return grad_bytes(grad_tilings(m, n, k),
+                    dy_as_is(dy, dy_dtype, dy_stride, dtype, m, activation, p), x, x_stride, w,
+                    w_stride, m, n, k);
 }
 
 extern "C" cp_status cp_linear_grad(const void* dy, int dy_dtype, uint64_t dy_stride,
@@ -364,8 +392,10 @@ extern "C" cp_status cp_linear_grad(const void* dy, int dy_dtype, uint64_t dy_st
       (want_dw && m != 0 && (x == nullptr || !cpx::aligned(x, 2))))
     return refuse("null or misaligned dy, x, w, pre, dx, dw or db");
   if (!want_dx && !want_dw && (db == nullptr || n == 0)) return CP_OK;
-  const uint64_t need = cp_linear_grad_call_bytes(dy, dy_dtype, dy_stride, x, x_stride, w, w_stride,
-                                                  dtype, m, n, k, activation, p);
+  const bool as_is = dy_as_is(dy, dy_dtype, dy_stride, dtype, m, activation, p);
+  const Tilings ways = grad_tilings(m, n, k);
+  const uint64_t need =
+      m == 0 || n == 0 ? 0 : grad_bytes(ways, as_is, x, x_stride, w, w_stride, m, n, k);
   if (need != 0 &&
       (workspace == nullptr || !cpx::aligned(workspace, 16) || workspace_bytes < need))
     return refuse("workspace must be 16-byte aligned and hold cp_linear_grad_call_bytes bytes");
@@ -376,7 +406,6 @@ extern "C" cp_status cp_linear_grad(const void* dy, int dy_dtype, uint64_t dy_st
   Operand dz{dy, dy_stride, false};
   const bool has_dy = m != 0 && n != 0;
   const bool shape = activation != CP_ACT_NONE || g.drop.mode != 0;
-  const bool as_is = dy_as_is(dy, dy_dtype, dy_stride, dtype, m, activation, p);
   g.pitch = row_pitch(n);
   if (!as_is && has_dy) {
     dz = Operand{at, g.pitch, false};
@@ -469,5 +498,7 @@ extern "C" cp_status cp_linear_grad(const void* dy, int dy_dtype, uint64_t dy_st
     d.e.n = static_cast<uint32_t>(k);
     d.e.aligned = cpx::aligned(d.e.out, 32) && d.e.ldo * dtype_size(d.e.out_dtype) % 32 == 0;
   }
-  return cplin::launch_products(q, count, sums, part_at(at), s);
+  Tiling chosen[cplin::kMostProducts] = {};
+  if (count > 0) cplin::choose(ways, want_dx ? 0 : 1, count, chosen);
+  return cplin::launch_products(q, count, chosen, sums, part_at(at), s);
 }

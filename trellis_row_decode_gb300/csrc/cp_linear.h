@@ -36,12 +36,29 @@ struct ColumnSums {
   int dtype, accumulate, rows_dtype;
 };
 
-// Products of one launch on CTA pairs (cp_linear_tc.cu), two at most; `part` holds
-// part_floats(products) floats where some are split along k.
-constexpr int kMostProducts = 2;
-uint64_t part_floats(const uint32_t* m, const uint32_t* n, const uint32_t* k, int count);
-cp_status launch_products(const Product* q, int count, const ColumnSums& sums, float* part,
-                          cudaStream_t s);
+// Products of one launch on CTA pairs (cp_linear_tc.cu), two at most.
+constexpr int kMostProducts = 2, kWidths = 8;
+
+// How a product may be cut: columns of a tile, units that share a tile's k, and what that costs.
+struct Tiling {
+  uint32_t bn, splits;
+  uint64_t units;
+  double each, extra;      // ns of a unit, of sharing k
+};
+// The ways of up to two products, m x n x k each (none of them 0), by width of the tiles.
+struct Tilings {
+  uint32_t m[kMostProducts], n[kMostProducts];
+  Tiling way[kMostProducts][kWidths];
+};
+Tilings tilings(const uint32_t* m, const uint32_t* n, const uint32_t* k, int count);
+// Those of products `first` on that are launched together.
+void choose(const Tilings& t, int first, int count, Tiling* out);
+// Floats for the sums of products whose k is split, so chosen.
+uint64_t part_floats(const Tilings& t, int first, int count);
+
+// `chosen` is for the products that have outputs and sums, in their order; `part` holds part_floats.
+cp_status launch_products(const Product* q, int count, const Tiling* chosen, const ColumnSums& sums,
+                          float* part, cudaStream_t s);
 
 // k of a unit above which sums are read in segments for 16-bit outputs too: the tensor core's own error
 // is 7e-5 there, where fp16's rounding is 4.9e-4.

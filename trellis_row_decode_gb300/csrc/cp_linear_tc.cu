@@ -25,6 +25,7 @@ using cpe::DropKey;
 using cpe::Epilogue;
 using cplin::ColumnSums;
 using cplin::kMostProducts;
+using cplin::Tiling;
 
 // A wait that ran out sets this word; cp_linear_status reads and clears it.
 __device__ uint32_t g_linear_gave_up;
@@ -939,21 +940,17 @@ bool store_map_ok(const void* p, int dtype, uint64_t n, uint64_t m, uint64_t ld)
 // column; sharing k 4500 and the sums' way to memory and back.  Units are dealt in turn, so the
 // first pair has the most.
 constexpr uint32_t kPairs = 76;
-struct Tiling {
-  uint32_t bn, splits;
-  uint64_t units;
-  double each, extra;
-};
 Tiling best_splits(uint32_t m, uint32_t n, uint32_t k, uint32_t bn) {
   const uint32_t kblocks = (k + kStageK - 1) / kStageK;
   const uint64_t tiles = (static_cast<uint64_t>(m) + 255) / 256 * ((static_cast<uint64_t>(n) + bn - 1) / bn);
   const double stage = bn <= 80 ? 140.0 : 60.0 + 0.95 * bn;
+  const double traffic = 4.0 / 3000.0 * m * n;
   Tiling best{};
   double least = 0.0;
   for (uint32_t s : {1u, 2u, 3u, 4u, 6u, 8u, 12u, 16u, 24u, 32u}) {
     if (s > 1 && (tiles * s > 2 * kPairs || 4 * s > kblocks)) break;
     Tiling t{bn, s, tiles * s, (kblocks + s - 1) / s * stage + 300.0 + 6.5 * bn, 0.0};
-    if (s > 1) t.extra = 4500.0 + (s + 1) * 4.0 * m * static_cast<double>(n) / 3000.0;
+    if (s > 1) t.extra = 4500.0 + (s + 1) * traffic;
     const double cost = static_cast<double>((t.units + kPairs - 1) / kPairs) * t.each + t.extra;
     if (s == 1 || cost < least) {
       least = cost;
@@ -961,29 +958,6 @@ Tiling best_splits(uint32_t m, uint32_t n, uint32_t k, uint32_t bn) {
     }
   }
   return best;
-}
-void choose_tilings(const uint32_t* m, const uint32_t* n, const uint32_t* k, int count,
-                    Tiling* out) {
-  Tiling t[kMostProducts][8] = {};
-  for (int i = 0; i < count; ++i)
-    for (uint32_t b = 0; b < 8; ++b) t[i][b] = best_splits(m[i], n[i], k[i], 256 - 32 * b);
-  double least = 1e300;
-  for (uint32_t a = 0; a < 8; ++a) {
-    for (uint32_t b = 0; b < (count > 1 ? 8 : 1); ++b) {
-      const bool swap = t[1][b].each > t[0][a].each;       // (the longer units go first)
-      const Tiling &x = swap ? t[1][b] : t[0][a], &y = swap ? t[0][a] : t[1][b];
-      const uint64_t first = (x.units + kPairs - 1) / kPairs;
-      const uint64_t all = (x.units + y.units + kPairs - 1) / kPairs;
-      const double even = (x.units * x.each + y.units * y.each) / kPairs;
-      const double cost = std::max(first * x.each + (all - first) * y.each, even) +
-                          std::max(x.extra, y.extra);
-      if (cost < least) {
-        least = cost;
-        out[0] = t[0][a];
-        if (count > 1) out[1] = t[1][b];
-      }
-    }
-  }
 }
 uint64_t part_pitch(uint32_t n) { return (static_cast<uint64_t>(n) + 31) / 32 * 32; }
 
@@ -1000,17 +974,50 @@ cp_status too_many_tiles() {
 
 namespace cplin {
 
-uint64_t part_floats(const uint32_t* m, const uint32_t* n, const uint32_t* k, int count) {
-  Tiling t[kMostProducts];
-  choose_tilings(m, n, k, count, t);
+Tilings tilings(const uint32_t* m, const uint32_t* n, const uint32_t* k, int count) {
+  Tilings t{};
+  for (int i = 0; i < count; ++i) {
+    t.m[i] = m[i];
+    t.n[i] = n[i];
+    for (uint32_t b = 0; b < kWidths; ++b) t.way[i][b] = best_splits(m[i], n[i], k[i], 256 - 32 * b);
+  }
+  return t;
+}
+
+void choose(const Tilings& t, int first, int count, Tiling* out) {
+  const Tiling none{};
+  const Tiling *ways = t.way[first], *others = count > 1 ? t.way[first + 1] : &none;
+  double least = 1e300;
+  for (int a = 0; a < kWidths; ++a) {
+    for (int b = 0; b < (count > 1 ? kWidths : 1); ++b) {
+      const bool swap = others[b].each > ways[a].each;     // (the longer units go first)
+      const Tiling &x = swap ? others[b] : ways[a], &y = swap ? ways[a] : others[b];
+      const uint64_t turns = (x.units + kPairs - 1) / kPairs;
+      const uint64_t all = (x.units + y.units + kPairs - 1) / kPairs;
+      const double even = (x.units * x.each + y.units * y.each) * (1.0 / kPairs);
+      const double cost = std::max(turns * x.each + (all - turns) * y.each, even) +
+                          std::max(x.extra, y.extra);
+      if (cost < least) {
+        least = cost;
+        out[0] = ways[a];
+        if (count > 1) out[1] = others[b];
+      }
+    }
+  }
+}
+
+uint64_t part_floats(const Tilings& t, int first, int count) {
+  Tiling chosen[kMostProducts];
+  choose(t, first, count, chosen);
   uint64_t floats = 0;
   for (int i = 0; i < count; ++i)
-    if (t[i].splits > 1) floats += static_cast<uint64_t>(t[i].splits) * m[i] * part_pitch(n[i]);
+    if (chosen[i].splits > 1)
+      floats += static_cast<uint64_t>(chosen[i].splits) * t.m[first + i] * part_pitch(t.n[first + i]);
   return floats;
 }
 
-cp_status launch_products(const Product* q, int count, const ColumnSums& sums, float* part,
-                          cudaStream_t s) {
+cp_status launch_products(const Product* q, int count, const Tiling* chosen, const ColumnSums& sums,
+                          float* part, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   const Device* d = device(&e);
   if (d == nullptr) return cpx::cuda_fail(e, "linear device query");
@@ -1018,18 +1025,12 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
   FinishParams f{};
   bool is_rich = false, segments = false, finish = false;
   uint64_t units[kMostProducts] = {};
-  uint32_t ms[kMostProducts] = {}, ns[kMostProducts] = {}, ks[kMostProducts] = {};
+  uint32_t ks[kMostProducts] = {};
   int used = 0;
-  for (int i = 0; i < count; ++i) {
-    if (q[i].e.m == 0 || q[i].e.n == 0 || q[i].k == 0) continue;
-    ms[used] = q[i].e.m;
-    ns[used] = q[i].e.n;
-    ks[used++] = q[i].k;
-  }
-  Tiling tilings[kMostProducts] = {};
-  if (used > 0) choose_tilings(ms, ns, ks, used, tilings);
+  for (int i = 0; i < count; ++i)
+    if (q[i].e.m != 0 && q[i].e.n != 0 && q[i].k != 0) ks[used++] = q[i].k;
   // units are dealt in turn: the longer ones first
-  const bool swap = used == 2 && tilings[1].each > tilings[0].each;
+  const bool swap = used == 2 && chosen[1].each > chosen[0].each;
   used = 0;
   for (int i = 0; i < count; ++i) {
     const Epilogue& ep = q[i].e;
@@ -1045,7 +1046,7 @@ cp_status launch_products(const Product* q, int count, const ColumnSums& sums, f
     }
     const int at = swap ? 1 - used : used;
     PairProduct& x = p.q[at];
-    const Tiling& t = tilings[used];
+    const Tiling& t = chosen[used];
     x.e = ep;
     x.bn = t.bn;
     x.splits = t.splits;
