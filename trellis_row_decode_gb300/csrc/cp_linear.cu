@@ -270,6 +270,7 @@ extern "C" cp_status cp_linear(const void* x, uint64_t x_stride, const void* w, 
     if (!thin) {
       ways = linear_tilings(m, n, k);
       cplin::choose(ways, 0, 1, &chosen);
+      if (q.e.drop.mode == 1) cplin::choose_dropped(ways, &chosen);
       need += part_bytes(ways, 0, 1);
     }
   }

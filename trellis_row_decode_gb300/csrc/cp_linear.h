@@ -53,6 +53,8 @@ struct Tilings {
 Tilings tilings(const uint32_t* m, const uint32_t* n, const uint32_t* k, int count);
 // Those of products `first` on that are launched together.
 void choose(const Tilings& t, int first, int count, Tiling* out);
+// The first product's again where it has dropout: another width, never another split.
+void choose_dropped(const Tilings& t, Tiling* chosen);
 // Floats for the sums of products whose k is split, so chosen.
 uint64_t part_floats(const Tilings& t, int first, int count);
 

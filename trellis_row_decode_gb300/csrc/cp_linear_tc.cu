@@ -1006,6 +1006,21 @@ void choose(const Tilings& t, int first, int count, Tiling* out) {
   }
 }
 
+// With dropout a short k's products are done before the finishing warps are.  Up to 128 columns a warp
+// has one block of a tile, above two in a row: 128 columns where the last turn then loses clearly less.
+// Nanoseconds of a tile's finishing, measured at k = 1024.  Both widths measured at 84 sizes and epilogues
+// beyond L2: 0.86 to 1.02 of the time where this takes 128 (8192 x 2048 x 1024 with a residual 43.8 us to
+// 37.6, with silu and kept sums too 50.6 to 45.2), 0.96 to 1.05 where it does not.
+void choose_dropped(const Tilings& t, Tiling* chosen) {
+  const Tiling& narrow = t.way[0][4];                      // 128 columns
+  if (chosen->splits != 1 || narrow.splits != 1 || chosen->bn <= narrow.bn) return;
+  auto cost = [](const Tiling& x, double finish) {
+    return x.each + static_cast<double>((x.units + kPairs - 1) / kPairs) * std::max(x.each, finish);
+  };
+  if (cost(narrow, 1800.0 + 22.5 * 128) < 0.92 * cost(*chosen, 3800.0 + 19.5 * chosen->bn))
+    *chosen = narrow;
+}
+
 uint64_t part_floats(const Tilings& t, int first, int count) {
   Tiling chosen[kMostProducts];
   choose(t, first, count, chosen);
