@@ -25,9 +25,6 @@ using namespace cpl;
 using cpe::DropKey;
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 2;                  // octets whose loads a thread has in flight
-template <typename T, bool kResidual>      // CTAs of an SM, by registers
-constexpr int kCtas = sizeof(T) == 4 ? 4 : kResidual ? 5 : 6;
 
 // x * scale of two elements, by one instruction; and an octet's bits widened by byte moves: the
 // generator's products fill the pipe that multiplications and shifts by multiplication share.
@@ -70,10 +67,19 @@ struct DropoutParams {
 // needs no position of a row (a product of 64 bits each, on the generator's pipe).
 enum { kFlat, kRows, kAny };
 
+// Octets whose loads a thread has in flight, and CTAs of an SM, by registers.  Rows anywhere take more
+// warps instead, which hides their chains of shifts better (100,000 x 1023 bf16 with a residual 165 us
+// against 186 as the others, 9001 x 813 fp32 16.4 against 17.5).
+template <int kLayout>
+constexpr int kAhead = kLayout == kAny ? 1 : 2;
 template <typename T, int kLayout, bool kResidual>
-__global__ void __launch_bounds__(kThreads, (kCtas<T, kResidual>))
+constexpr int kCtas = kLayout == kAny ? (sizeof(T) == 4 ? 6 : 8) : sizeof(T) == 4 ? 4 : kResidual ? 5 : 6;
+
+template <typename T, int kLayout, bool kResidual>
+__global__ void __launch_bounds__(kThreads, (kCtas<T, kLayout, kResidual>))
     dropout_kernel(const __grid_constant__ DropoutParams p) {
   constexpr bool VEC = kLayout != kAny;
+  constexpr int kAt = kAhead<kLayout>;
   wait_for_previous();
   let_next_start();
   const DropKey key = cpe::drop_key(p.drop);
@@ -85,11 +91,11 @@ __global__ void __launch_bounds__(kThreads, (kCtas<T, kResidual>))
   const T* pr = static_cast<const T*>(p.residual) + 8 * first;
   T* po = static_cast<T*>(p.out) + 8 * first;
 #pragma unroll 1
-  for (uint32_t n = 0; n < p.per && row < p.rows; n += kAhead) {
-    Packed<T> x[kAhead], r[kAhead];
-    uint32_t at[kAhead], col[kAhead];
+  for (uint32_t n = 0; n < p.per && row < p.rows; n += kAt) {
+    Packed<T> x[kAt], r[kAt];
+    uint32_t at[kAt], col[kAt];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
+    for (int i = 0; i < kAt; ++i) {
       at[i] = row;
       col[i] = o;
       if (row < p.rows) {
@@ -110,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, (kCtas<T, kResidual>))
       }
     }
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
+    for (int i = 0; i < kAt; ++i) {
       if (at[i] < p.rows) {
         float v[8];
         widen(x[i], v);
@@ -142,9 +148,9 @@ __global__ void __launch_bounds__(kThreads, (kCtas<T, kResidual>))
           store_row_octet<T, VEC>(static_cast<T*>(p.out) + at[i] * p.ldo, col[i], p.d, pack<T>(v));
       }
     }
-    px += 8 * kThreads * kAhead;
-    pr += 8 * kThreads * kAhead;
-    po += 8 * kThreads * kAhead;
+    px += 8 * kThreads * kAt;
+    pr += 8 * kThreads * kAt;
+    po += 8 * kThreads * kAt;
   }
 }
 
@@ -152,8 +158,8 @@ __global__ void __launch_bounds__(kThreads, (kCtas<T, kResidual>))
 // elements go to the lanes one by one, 32 neighbours an access, and each takes its place and its bit
 // from the lane that has its octet.  For fp32 with a residual, where it is the stores of shifted
 // octets that take the time (90010 x 813: 146 us against 200).
-// Without a residual or in 16 bits the exchange costs more than it saves (119 us against 124; 100000 x
-// 1023 bf16 129 against 176).
+// Without a residual or in 16 bits the exchange costs more than it saves (116 us against 124; 100000 x
+// 1023 bf16 126 against 176).
 __global__ void __launch_bounds__(kThreads, 5)
     dropout_elements_kernel(const __grid_constant__ DropoutParams p) {
   wait_for_previous();
