@@ -97,3 +97,16 @@ def test_linear_sums_a_long_k():
     # each addition, joined by additions that round, lose up to 5.5e-7 + 256 U32
     assert ((got - ref) / ref).mean().abs() < 5 * 2.2e-6 + 5.5e-7 + 256 * U32
     assert cp.linear_status() == cp.CP_OK
+
+
+@pytest.mark.parametrize("m,n,k", [(8192, 2048, 200), (16384, 1024, 520), (4096, 1000, 1100)])
+def test_dropout_changes_no_sum(m, n, k):
+    """Dropout may choose another tile: what it keeps is what the product without it has, bit by bit."""
+    at = torch.Generator(device="cuda").manual_seed(m)
+    x = torch.randn(m, k, generator=at, device="cuda").half()
+    w = torch.randn(n, k, generator=at, device="cuda").half()
+    r = torch.randn(m, n, generator=at, device="cuda")
+    z = cp.linear(x, w, dtype=torch.float32)
+    out = cp.linear(x, w, residual=r, p=0.25, seed=3, offset=4, dtype=torch.float32)
+    assert torch.equal(out, cp.dropout(z, 0.25, 3, 4, residual=r))
+    assert cp.linear_status() == cp.CP_OK

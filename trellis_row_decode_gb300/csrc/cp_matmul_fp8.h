@@ -29,7 +29,8 @@ cp_status launch_pairs(const MatmulParams& p, cudaStream_t s);
 cp_status launch_thin(const MatmulParams& p, cudaStream_t s);
 
 // Rows of k bytes on any boundary copied to rows on 16-byte ones, `pitch` apart (a multiple of 16, at
-// least k), zeros behind their ends to the next of those; two operands in one launch (rows 0: one that stays).
+// least k), zeros behind their ends to the next of those; two operands in one launch (rows 0: one
+// that stays).
 struct AlignOperand {
   const uint8_t* from;
   uint8_t* to;
