@@ -18,6 +18,7 @@ is queued; what the library itself refuses raises CPError.
 from __future__ import annotations
 
 import ctypes as C
+import math
 
 import torch
 
@@ -125,8 +126,10 @@ def _rows(t: torch.Tensor, name: str) -> tuple[int, int, int]:
             if shape[0] > 1 and strides[0] != 1:
                 raise ValueError(f"{name} must have unit stride in its last dimension")
             return 1, shape[0], shape[0]
+        if not shape[-1]:                         # rows of no columns lie nowhere, but they count
+            return math.prod(shape[:-1]), 0, 0
         try:
-            t = t.view(-1, shape[-1]) if shape[-1] else t.view(0, 0)
+            t = t.view(-1, shape[-1])
         except RuntimeError:
             raise ValueError(f"{name}: leading dimensions must be mergeable without a copy"
                              ) from None
