@@ -402,8 +402,9 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
     const DropKey key = cpe::drop_key(p.q[0].e.drop);      // (dropout is in the first product alone)
     const uint32_t slots = cpt::smem_addr(tiles) + p.slots_at + mine * p.slots;
     const uint32_t residual_bar = cpt::smem_addr(&residual_bars[mine]);
-    uint32_t it = 0, residual_parity = 0;
-    bool ok = true, coming = false;            // coming: loads of the residual are under way
+    uint32_t it = 0;
+    Awaited coming;                            // loads of the residual
+    bool ok = true;
     for (uint32_t u = pair; u < p.units && ok; u += pairs) {
       const Unit t = unit_of(p, u);
       const PairProduct& q = p.q[t.which];
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
                           t.col0 + 32 * (kGroups * (i + j) + group), row0, residual_bar);
         }
         __syncwarp();
-        coming = true;
+        coming.begun();
       };
       const bool two_slots = p.slots > kSlot;
       if (q.tma_residual && left != 0) load_residual(0, two_slots ? left : 1);
@@ -459,10 +460,10 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
         if (q.tma_residual) {
           if (i != 0 && !two_slots) load_residual(i, 1);
           const uint32_t slot = slots + (two_slots ? i * kSlot : 0);
-          if (coming) {
-            ok = cpt::mbar_wait(residual_bar, residual_parity, &gave_up);
-            residual_parity ^= 1;
-            coming = !ok;
+          if (coming.under_way) {
+            ok = cpt::mbar_wait(residual_bar, coming.parity, &gave_up);
+            coming.waited(ok);
+            if (!ok) return;                   // (the slot is still the load's)
           }
           write_slot(slot, lane, q.e.out_dtype, true, v);
           cpt::stores_fence();
@@ -546,9 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
     if (!ok && lane == 0) atomicOr(&g_linear_gave_up, 1u);
     if (lane == 0) cpt::stores_done();         // before the slots are someone else's
     __syncwarp();
-    if (coming) {
+    if (coming.under_way) {
       int late = 0;
-      cpt::mbar_wait(residual_bar, residual_parity, &late);
+      cpt::mbar_wait(residual_bar, coming.parity, &late);
     }
     end_role();
   }

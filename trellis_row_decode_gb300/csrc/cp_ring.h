@@ -25,4 +25,18 @@ constexpr LastFill last_fill(uint32_t mine, uint32_t other, uint32_t stages, uin
   return LastFill{n != 0, (n - 1) & 1};
 }
 
+// Loads that a warp begins and waits for on a barrier of its own, one phase after the other: `parity` is
+// that of the phase which the loads under way complete, or the next ones will.  A wait that ran out
+// leaves both as they are, so the wait before the memory is someone else's asks for that phase again.
+struct Awaited {
+  uint32_t parity = 0;
+  bool under_way = false;
+  constexpr void begun() { under_way = true; }
+  constexpr void waited(bool arrived) {
+    if (!arrived) return;
+    parity ^= 1;
+    under_way = false;
+  }
+};
+
 }  // namespace cpl
