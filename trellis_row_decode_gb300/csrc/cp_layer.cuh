@@ -217,7 +217,7 @@ __device__ __forceinline__ void store_row_octet(T* row, uint32_t o, uint32_t d,
   }
   T* to = row + 8ull * o;
   const uint32_t skew = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(to) & 15);
-  if (8 * o + 8 > d) {
+  if (o >= d / 8) {                      // (8 o + 8 wraps in rows of almost 2^32 columns)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (8 * o + i < d) {
