@@ -109,10 +109,7 @@ __global__ void __launch_bounds__(kGradThreads, grad_ctas(kShape))
 #pragma unroll
           for (int e = 0; e < 8; ++e) z[8 * i + e] = u[e];
         }
-        cpe::with_act(p.act, [&](auto tag) {
-#pragma unroll
-          for (uint32_t e = 0; e < 8 * kRows; ++e) v[e] *= cpe::slope<decltype(tag)::value>(z[e]);
-        });
+        cpe::with_act(p.act, [&](auto tag) { cpe::slope_all<decltype(tag)::value>(z, v); });
       }
       if (p.drop.mode != 0) cpe::drop_block<2, kRows>(p.drop, key, 2 * o, r, 8, v);
     }
