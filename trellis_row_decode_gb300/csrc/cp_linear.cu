@@ -327,7 +327,9 @@ uint64_t db_bytes(uint64_t m, uint64_t n) { return 4ull * grad_parts(m, n, false
 
 // Whether the products' kernel makes the column sums from dy's rows.  (Not beside a dx whose k is so
 // long that its sums are read in segments: the warps in question have few registers there.)
-bool direct_sums(uint64_t m, uint64_t n) { return m <= kDirectRows && n <= cplin::kLongSum; }
+bool direct_sums(uint64_t m, uint64_t n, int dtype) {
+  return m <= kDirectRows && n <= cplin::long_sum(dtype);
+}
 
 // Whether dz is dy itself.
 bool dy_as_is(const void* dy, int dy_dtype, uint64_t dy_stride, int dtype, uint64_t m,
@@ -336,9 +338,9 @@ bool dy_as_is(const void* dy, int dy_dtype, uint64_t dy_stride, int dtype, uint6
 }
 
 // Bytes of a call with m and n above 0.
-uint64_t grad_bytes(const Tilings& t, bool as_is, const void* x, uint64_t x_stride, const void* w,
-                    uint64_t w_stride, uint64_t m, uint64_t n, uint64_t k) {
-  return (as_is ? 0 : dz_bytes(m, n)) + (as_is && direct_sums(m, n) ? 0 : db_bytes(m, n)) +
+uint64_t grad_bytes(const Tilings& t, bool as_is, int dtype, const void* x, uint64_t x_stride,
+                    const void* w, uint64_t w_stride, uint64_t m, uint64_t n, uint64_t k) {
+  return (as_is ? 0 : dz_bytes(m, n)) + (as_is && direct_sums(m, n, dtype) ? 0 : db_bytes(m, n)) +
          copy_bytes(x, x_stride, w, w_stride, m, n, k) + grad_part_bytes(t);
 }
 
@@ -357,8 +359,8 @@ extern "C" uint64_t cp_linear_grad_call_bytes(const void* dy, int dy_dtype, uint
                                               uint64_t k, int activation, double p) {
   if (m >= kMostK || n >= kMostK || k >= kMostK || m == 0 || n == 0) return 0;
   return grad_bytes(grad_tilings(m, n, k),
-                    dy_as_is(dy, dy_dtype, dy_stride, dtype, m, activation, p), x, x_stride, w,
-                    w_stride, m, n, k);
+                    dy_as_is(dy, dy_dtype, dy_stride, dtype, m, activation, p), dtype, x, x_stride,
+                    w, w_stride, m, n, k);
 }
 
 extern "C" cp_status cp_linear_grad(const void* dy, int dy_dtype, uint64_t dy_stride,
@@ -393,7 +395,7 @@ extern "C" cp_status cp_linear_grad(const void* dy, int dy_dtype, uint64_t dy_st
   const bool as_is = dy_as_is(dy, dy_dtype, dy_stride, dtype, m, activation, p);
   const Tilings ways = grad_tilings(m, n, k);
   const uint64_t need =
-      m == 0 || n == 0 ? 0 : grad_bytes(ways, as_is, x, x_stride, w, w_stride, m, n, k);
+      m == 0 || n == 0 ? 0 : grad_bytes(ways, as_is, dtype, x, x_stride, w, w_stride, m, n, k);
   if (need != 0 &&
       (workspace == nullptr || !cpx::aligned(workspace, 16) || workspace_bytes < need))
     return refuse("workspace must be 16-byte aligned and hold cp_linear_grad_call_bytes bytes");
@@ -416,7 +418,7 @@ extern "C" cp_status cp_linear_grad(const void* dy, int dy_dtype, uint64_t dy_st
     sums.n = static_cast<uint32_t>(n);
     sums.dtype = db_dtype;
     sums.accumulate = accumulate;
-    if (as_is && direct_sums(m, n)) {
+    if (as_is && direct_sums(m, n, dtype)) {
       sums.rows = dy;
       sums.rows_dtype = dy_dtype;
       sums.pitch = dy_stride;

@@ -62,9 +62,13 @@ uint64_t part_floats(const Tilings& t, int first, int count);
 cp_status launch_products(const Product* q, int count, const Tiling* chosen, const ColumnSums& sums,
                           float* part, cudaStream_t s);
 
-// k of a unit above which sums are read in segments for 16-bit outputs too: the tensor core's own error
-// is 7e-5 there, where fp16's rounding is 4.9e-4.
-constexpr uint32_t kLongSum = 65536;
+// k of a unit above which sums are read in segments, by the type they are rounded to.  The tensor core
+// cuts its running sum and each product that it adds: a sum of positive products loses 6.4e-9 k of itself
+// (fp16; bf16 5.9e-9), all to one side.  In 16 bits that may come to an eighth of the rounding's half
+// step (2^-11, 2^-8).  Segments cost 2 to 4 % (4096 x 4096 x 24576 fp16 468 us, 478 in segments).
+constexpr uint32_t long_sum(int dtype) {
+  return dtype == CP_F32 ? 512 : dtype == CP_F16 ? 8192 : 65536;
+}
 
 // Up to kThinRows rows of a: tiles of 128 rows of b, neither operand stored across.
 constexpr uint32_t kThinRows = 128;

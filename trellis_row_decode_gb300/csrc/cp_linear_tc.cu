@@ -67,7 +67,7 @@ constexpr uint32_t kSmemMost = kSmemUsed + 1023;       // (and what it takes to 
 constexpr uint32_t kQuickK = 512;                      // k up to here: two slots a warp for residuals
 constexpr uint32_t kTwoBytes = 24 * 1024;              // stages up to here hold two parts
 constexpr uint32_t kBuffer = 256;                      // columns of tensor memory of a buffer
-constexpr uint32_t kSegment = 512;                     // of k that the tensor core adds up alone
+constexpr uint32_t kSegment = cplin::long_sum(CP_F32); // of k that the tensor core adds up alone
 // Registers with segments: launched with 96 a thread (65,536 over 20 warps); the finishing warps
 // (64 sums a thread) take what the other four give up.
 constexpr int kLaunchRegs = 96, kFinishRegs = 104, kOtherRegs = 64;
@@ -202,10 +202,10 @@ __device__ __forceinline__ void sum_rows(const ColumnSums& p, uint32_t c, uint32
 }
 
 // kRich: some product has an activation, dropout, or sums to keep.
-// kSegments: some product is wanted in 32 bits, or has more than kLongSum of k in a unit.  The tensor
-// core cuts its running sum at every addition instead of rounding it, an error that grows with k
-// (measured, relative: 1.07e-9 k, 4.4e-6 at k = 4096, where fp32 additions that round leave 6e-7);
-// so the sum is read every kSegment of k and added up in registers.
+// kSegments: some product has more of k in a unit than its outputs' type allows (long_sum).  The tensor
+// core cuts what it adds instead of rounding it, an error that grows with k (relative, random bf16
+// operands: 1.07e-9 k, 4.4e-6 at k = 4096, where fp32 additions that round leave 6e-7; positive ones
+// 6e-9 k, all to one side); so the sum is read every kSegment of k and added up in registers.
 template <bool kRich, bool kSegments>
 __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constant__ PairParams p) {
   extern __shared__ uint8_t dyn[];
@@ -1077,7 +1077,8 @@ cp_status launch_products(const Product* q, int count, const Tiling* chosen, con
     x.b_boxes = x.b_across ? (t.bn / 2 + 63) / 64 : 1;
     x.b_bytes = x.b_across ? x.b_boxes * kBlock : t.bn / 2 * 128;
     x.instr = cpt::half_instr_desc(256, t.bn, q[i].dtype == CP_BF16, x.a_across, x.b_across);
-    segments |= q[i].k / t.splits > (ep.out_dtype == CP_F32 ? kSegment : kLongSum);
+    segments |= q[i].k / t.splits > min(long_sum(ep.out_dtype),
+                                        ep.pre != nullptr ? long_sum(ep.pre_dtype) : ~0u);
     if (t.splits > 1) {
       x.pitch = part_pitch(ep.n);
       x.part = part;
