@@ -31,6 +31,12 @@ inline bool aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) % a) == 0;
 }
 
+// Whether an array that a call may leave out has its rows of `elt`-byte elements, `stride` of them apart,
+// on 32-byte boundaries.  One that is not there stands in no other's way, whatever its stride.
+inline bool sectors_ok(const void* p, uint64_t stride, uint64_t elt) {
+  return p == nullptr || (aligned(p, 32) && stride * elt % 32 == 0);
+}
+
 // Row-range buckets of the host path's visiting order: bucket of row r is
 // r >> shift, nb buckets in all (nb <= 2^kBucketBitsHost).  n_rows >= 1.
 inline void bucket_params(uint64_t n_rows, uint32_t* shift, uint32_t* nb) {

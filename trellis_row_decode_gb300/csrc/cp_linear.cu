@@ -292,9 +292,9 @@ extern "C" cp_status cp_linear(const void* x, uint64_t x_stride, const void* w, 
   q.e.out_dtype = out_dtype;
   q.e.pre_dtype = dtype;
   q.e.act = activation;
-  q.e.aligned = cpx::aligned(out, 32) && out_stride * elt % 32 == 0 &&
-                cpx::aligned(residual, 32) && residual_stride * elt % 32 == 0 &&
-                cpx::aligned(pre, 32) && pre_stride * 2 % 32 == 0;
+  q.e.aligned = cpx::sectors_ok(out, out_stride, elt) &&
+                cpx::sectors_ok(residual, residual_stride, elt) &&
+                cpx::sectors_ok(pre, pre_stride, 2);
   if (k == 0) return cplin::launch_products(&q, 1, &chosen, ColumnSums{}, nullptr, s);
   uint8_t* at = static_cast<uint8_t*>(workspace);
   Operand* op[2] = {&q.a, &q.b};
@@ -496,7 +496,7 @@ extern "C" cp_status cp_linear_grad(const void* dy, int dy_dtype, uint64_t dy_st
     Product& d = q[i];
     d.dtype = dtype;
     d.e.n = static_cast<uint32_t>(k);
-    d.e.aligned = cpx::aligned(d.e.out, 32) && d.e.ldo * dtype_size(d.e.out_dtype) % 32 == 0;
+    d.e.aligned = cpx::sectors_ok(d.e.out, d.e.ldo, dtype_size(d.e.out_dtype));
   }
   Tiling chosen[cplin::kMostProducts] = {};
   if (count > 0) cplin::choose(ways, want_dx ? 0 : 1, count, chosen);
