@@ -1,8 +1,8 @@
 """Build libcp.so (the CUDA lookup-decode and its C ABI) in-tree for sm_103a.
 
 Each .cu file compiles in its own nvcc process (in parallel), then one link.
-Output: trellis_row_decode_gb300/_build/libcp.so, and beside it _calls.so (cp_calls.cpp, host code
-for this Python, linked to libcp.so).
+Output: trellis_row_decode_gb300/_build/libcp.so, and beside it _calls (cp_calls.cpp, host code for
+this Python, linked to libcp.so; its file's name says for which), where the Python's headers are there.
 """
 from __future__ import annotations
 
@@ -10,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -18,7 +19,7 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 BUILD = PKG / "_build"
 LIB = BUILD / "libcp.so"
-CALLS = BUILD / "_calls.so"
+CALLS = BUILD / ("_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -34,6 +35,26 @@ def nvcc() -> str:
 
 def sources() -> list[Path]:
     return sorted(CSRC.glob("*.cu"))
+
+
+def build_calls() -> Path | None:
+    """_calls, linked to the libcp.so that is there; None where this Python's headers or g++ are not:
+    the calls then go through ctypes alone."""
+    include = Path(sysconfig.get_paths()["include"])
+    if not (include / "Python.h").exists() or shutil.which("g++") is None:
+        warnings.warn("no Python.h or g++: small calls of linear, linear_grad and dropout will take "
+                      "longer on the host", RuntimeWarning, stacklevel=2)
+        CALLS.unlink(missing_ok=True)            # (one that is there may be of another libcp.so)
+        return None
+    tmp = CALLS.with_name(f"{CALLS.name}.{os.getpid()}.tmp")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I", str(include),
+           "-I", str(ROOT / "include"), "-o", str(tmp), str(CSRC / "cp_calls.cpp"),
+           "-L", str(BUILD), "-lcp", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for cp_calls.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
 
 
 def build(verbose: bool = False, ptxas_info: bool = False) -> Path:
@@ -65,14 +86,7 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> Path:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    tmp = CALLS.with_suffix(f".{os.getpid()}.tmp.so")
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I",
-           sysconfig.get_paths()["include"], "-I", str(ROOT / "include"), "-o", str(tmp),
-           str(CSRC / "cp_calls.cpp"), "-L", str(BUILD), "-lcp", "-Wl,-rpath,$ORIGIN"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"g++ failed for cp_calls.cpp:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS)
+    build_calls()
     return LIB
 
 

@@ -3,8 +3,9 @@
 // interpreted checks cost, 5 to 9 us a call, is as much as the smallest kernels take.
 //
 // Each function answers NotImplemented for every other form and for whatever the library refuses;
-// the caller (projection.py) then takes its own way, which checks, explains and raises.  Tensors are
-// read through their Python attributes: nothing here depends on PyTorch's C++ interface.
+// the caller (projection.py) then takes its own way, which checks, explains and raises, as it does for
+// every call where this file is not built.  Tensors are read through their Python attributes: nothing
+// here depends on PyTorch's C++ interface.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

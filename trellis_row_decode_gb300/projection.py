@@ -14,10 +14,11 @@ from __future__ import annotations
 import ctypes as C
 import importlib.machinery
 import importlib.util
+import warnings
 
 import torch
 
-from . import CP_ERR_INVALID_ARG, LIB_PATH, CPError, _check, lib
+from . import CP_ERR_INVALID_ARG, LIB_PATH, CPError, _check, build_ext, lib
 from . import layer as _layer
 from .layer import (CP_BF16, CP_F16, CP_F32, _check_out, _device, _empty, _float, _on, _rows, _stream,
                     _workspace)
@@ -28,20 +29,39 @@ __all__ = ["ACTIVATIONS", "linear", "linear_workspace", "linear_grad", "linear_g
 ACTIVATIONS = ("none", "relu", "silu", "gelu", "gelu_tanh")
 _ACT = {name: i for i, name in enumerate(ACTIVATIONS)}
 _HALF = {torch.float16: CP_F16, torch.bfloat16: CP_BF16}
+_CALLS_PATH = LIB_PATH.with_name(build_ext.CALLS.name)
 _declared = None
 _calls = None
 
 
+class _Checked:
+    """What stands for the calls' common forms where the compiled code is not there: every call takes
+    the checked way."""
+
+    @staticmethod
+    def dropout(*args):
+        return NotImplemented
+
+    linear = linear_grad = dropout
+
+
 def _common():
-    """The calls' common forms in compiled code (csrc/cp_calls.cpp), built beside libcp.so."""
+    """The calls' common forms in compiled code (csrc/cp_calls.cpp), built beside libcp.so for this
+    Python."""
     global _calls
     if _calls is None:
         lib()                                     # (raises where nothing has been built)
-        path = str(LIB_PATH.with_name("_calls.so"))
+        path = str(_CALLS_PATH)
         loader = importlib.machinery.ExtensionFileLoader("_calls", path)
-        spec = importlib.util.spec_from_file_location("_calls", path, loader=loader)
-        _calls = importlib.util.module_from_spec(spec)
-        loader.exec_module(_calls)
+        try:
+            calls = importlib.util.module_from_spec(
+                importlib.util.spec_from_file_location("_calls", path, loader=loader))
+            loader.exec_module(calls)
+        except (ImportError, AttributeError) as e:    # none, another Python's, or another PyTorch's
+            warnings.warn(f"calls of linear, linear_grad and dropout go through ctypes alone: {e}",
+                          RuntimeWarning, stacklevel=3)
+            calls = _Checked
+        _calls = calls
     return _calls
 
 
