@@ -131,22 +131,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
-// Whether the phase is over, without waiting (try_wait may hold the thread for microseconds), the
-// same to every lane.
-__device__ __forceinline__ bool mbar_ready(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n"
-      ".reg .pred p;\n"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      "selp.u32 %0, 1, 0, p;\n"
-      "}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return __all_sync(0xFFFFFFFFu, ok != 0);
-}
-
 // ------------------------------------------------------------------------- TMA
 
 // A 2-D tile into shared memory; its bytes count on `bar`, which may be the barrier of
@@ -301,16 +285,10 @@ __host__ __device__ constexpr uint32_t e4m3_instr_desc(uint32_t m, uint32_t n) {
   return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
-// Shared-memory descriptor of a 16-bit operand stored along its rows or columns (M or N) instead
-// of k: blocks of 64 of them (128 bytes, 128-byte swizzle) by 64 of k, a block 8192 bytes behind
-// the one before, eight of k 1024 bytes apart.
-__device__ __forceinline__ uint64_t operand_desc_mn(uint32_t addr) {
-  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (512ull << 16) | (64ull << 32) |
-         (1ull << 46) | (2ull << 61);
-}
-
-// The two words of a descriptor, the upper one the same for both kinds: what steps along an operand
-// is added to the lower one.
+// The two words of such a descriptor, or (across) of one of a 16-bit operand stored along its rows or
+// columns (M or N) instead of k: blocks of 64 of them (128 bytes, 128-byte swizzle) by 64 of k, a block
+// 8192 bytes behind the one before, eight of k 1024 bytes apart.  The upper word is the same for both:
+// what steps along an operand is added to the lower one.
 constexpr uint32_t kDescHigh = 64u | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_low(uint32_t addr, bool across) {
   return ((addr & 0x3FFFFu) >> 4) | (across ? 512u << 16 : 1u << 16);
