@@ -42,9 +42,9 @@ def build_calls() -> Path | None:
     the calls then go through ctypes alone."""
     include = Path(sysconfig.get_paths()["include"])
     if not (include / "Python.h").exists() or shutil.which("g++") is None:
+        CALLS.unlink(missing_ok=True)            # (one that is there may be of another libcp.so)
         warnings.warn("no Python.h or g++: small calls of linear, linear_grad and dropout will take "
                       "longer on the host", RuntimeWarning, stacklevel=2)
-        CALLS.unlink(missing_ok=True)            # (one that is there may be of another libcp.so)
         return None
     tmp = CALLS.with_name(f"{CALLS.name}.{os.getpid()}.tmp")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I", str(include),
