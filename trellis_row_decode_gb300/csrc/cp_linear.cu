@@ -166,9 +166,14 @@ cudaError_t launch_dz(const GradParams& p, bool vec, cudaStream_t s) {
 
 constexpr uint64_t kMostRows = 1ull << 31, kMostK = 1ull << 30;
 // Rows of dy, where it is dz itself, whose sums the products' kernel makes on the way: no launch and no
-// workspace for them (256 x 384 x 256: 5.4 us against 6.7, 512 x 384 x 256 7.6 against 7.0, but 16 us a
-// call against 21).
+// workspace for them.  With up to 1,024 columns the two ways cross between 384 and 640 rows on the
+// device (bf16, kernels here / in two launches: n x k of 384 x 256 with 256 rows 5.5 / 6.4 us, 512 7.5 / 6.8,
+// 1,024 11.7 / 8.5; 1024 x 1024 7.0 / 8.5, 8.8 / 8.9, 13.8 / 10.5), with 4,096 columns and so more
+// warps never up to 2,048 rows (512 rows 18.5 / 20.7); and a call is 2 to 7 us shorter on the host up to
+// 1,024.  No further than a segment either: beside a dw that is read in segments the warps in
+// question have few registers.
 constexpr uint64_t kDirectRows = 512;
+static_assert(kDirectRows <= cplin::long_sum(CP_F32), "no segments beside direct sums");
 
 uint64_t up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
 // Elements of a 16-bit row that is made here: whole lines of memory where it is long, so that 128 bytes
