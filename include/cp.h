@@ -535,7 +535,8 @@ enum { CP_ACT_NONE = 0, CP_ACT_RELU = 1, CP_ACT_SILU = 2, CP_ACT_GELU = 3, CP_AC
  * rn(D(x)).  The gradient by x is the same call on dy without a residual.
  *   x, residual   [rows][d] of dtype with row strides >= d, or 0 (one row for all).  residual may
  *            be NULL.
- *   out      [rows][d] of dtype, row stride >= d; it may be x or residual (same stride).
+ *   out      [rows][d] of dtype, row stride >= d; it may be x or residual (same stride), but not lie on
+ *            part of them.
  * rows < 2^31.
  */
 cp_status cp_dropout(const void* x, uint64_t x_stride, const void* residual,
@@ -552,7 +553,8 @@ cp_status cp_dropout(const void* x, uint64_t x_stride, const void* residual,
  *   bias     [n] of bias_dtype, or NULL.
  *   residual [m][n] of out_dtype, row stride residual_stride >= n or 0, or NULL.
  *   out      [m][n] of out_dtype (any type), row stride out_stride >= n.  It may be residual
- *            (same stride): the stream is updated in place.
+ *            (same stride): the stream is updated in place.  x and w are read while out and pre are
+ *            written: neither may lie on them, nor pre on out or the residual.
  *   pre      [m][n] of dtype, row stride pre_stride >= n, or NULL: what cp_linear_grad needs of
  *            a call with an activation.
  *   workspace  cp_linear_workspace_bytes bytes, 16-byte aligned (NULL where that is 0): copies of
@@ -584,6 +586,7 @@ cp_status cp_linear(const void* x, uint64_t x_stride, const void* w, uint64_t w_
  *   db       [n] of db_dtype, or NULL.
  *   workspace  cp_linear_grad_call_bytes bytes for these arguments (NULL where that is 0), or
  *            cp_linear_grad_workspace_bytes for any call of these sizes; 16-byte aligned.
+ * dx and dw may not lie on what is read while they are written: x, w, and dy where it is dz itself.
  * m = 0 gives zeros for dw and db, n = 0 for dx.  m, n < 2^30, k < 2^30.
  */
 uint64_t cp_linear_grad_workspace_bytes(uint64_t m, uint64_t n, uint64_t k);

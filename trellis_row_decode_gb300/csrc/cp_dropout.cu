@@ -261,6 +261,12 @@ extern "C" cp_status cp_dropout(const void* x, uint64_t x_stride, const void* re
     cpx::set_error("null or misaligned x, residual or out");
     return CP_ERR_INVALID_ARG;
   }
+  const cpx::RowBytes to{out, out_stride * elt, d * elt, rows};
+  if (cpx::rows_clash(to, {x, x_stride * elt, d * elt, rows}) ||
+      cpx::rows_clash(to, {residual, residual_stride * elt, d * elt, rows})) {
+    cpx::set_error("out lies on part of x or of the residual");
+    return CP_ERR_INVALID_ARG;
+  }
   q.x = x;
   q.residual = residual;
   q.out = out;

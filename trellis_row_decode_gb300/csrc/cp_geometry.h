@@ -37,6 +37,44 @@ inline bool sectors_ok(const void* p, uint64_t stride, uint64_t elt) {
   return p == nullptr || (aligned(p, 32) && stride * elt % 32 == 0);
 }
 
+// An array of rows, in bytes: `rows` of them, each `width` long, `stride` apart (0: one row for all).
+struct RowBytes {
+  const void* p;
+  uint64_t stride, width, rows;
+};
+// Whether two such arrays share a byte.  Rows of the same stride may lie between one another's, as columns
+// of one wider array do; of different strides, of which at most one can be that array's own, they count
+// as apart.
+inline bool rows_meet(RowBytes a, RowBytes b) {
+  if (a.p == nullptr || b.p == nullptr || a.rows == 0 || b.rows == 0 || a.width == 0 || b.width == 0)
+    return false;
+  if (a.stride == 0) a.rows = 1;
+  if (b.stride == 0) b.rows = 1;
+  uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  if (a0 + (a.rows - 1) * a.stride + a.width <= b0 || b0 + (b.rows - 1) * b.stride + b.width <= a0)
+    return false;
+  const uint64_t stride = a.rows == 1 ? b.stride : a.stride;
+  if (a.rows == 1 && b.rows == 1) return true;
+  if (b.rows != 1 && b.stride != stride) return false;
+  if (b0 < a0) {
+    const RowBytes c = a;
+    a = b;
+    b = c;
+    const uintptr_t t = a0;
+    a0 = b0;
+    b0 = t;
+  }
+  if (a.rows == 1) return true;            // (b begins inside the one row)
+  const uint64_t at = (b0 - a0) % stride;  // where b begins, from the row of a at or in front of it
+  return at < a.width || at + b.width > stride;
+}
+// Whether what is written to `out` could be read at another place of `in` afterwards: they meet, and are
+// not the same rows, each element of which is read before it is written.
+inline bool rows_clash(const RowBytes& out, const RowBytes& in) {
+  const bool same = out.p == in.p && (out.rows == 1 || out.stride == in.stride);
+  return !same && rows_meet(out, in);
+}
+
 // Row-range buckets of the host path's visiting order: bucket of row r is
 // r >> shift, nb buckets in all (nb <= 2^kBucketBitsHost).  n_rows >= 1.
 inline void bucket_params(uint64_t n_rows, uint32_t* shift, uint32_t* nb) {

@@ -193,6 +193,11 @@ cp_status refuse(const char* what) {
 
 bool row_ok(uint64_t stride, uint64_t d) { return stride >= d || stride == 0; }
 
+// Whether an operand of a product, read tile by tile where it lies, shares a byte with an output.
+bool reads(const Operand& op, uint64_t rows, uint64_t k, const cpx::RowBytes& out) {
+  return cpx::rows_meet({op.p, 2 * op.ld, 2 * k, rows}, out);
+}
+
 // Operands that lie on other boundaries, to be copied behind each other to `to`; false: none.
 bool to_align(Operand* (&op)[2], const uint64_t (&rows)[2], uint64_t k, uint8_t*& to,
               cpm::AlignOperand (&of)[2]) {
@@ -263,6 +268,10 @@ extern "C" cp_status cp_linear(const void* x, uint64_t x_stride, const void* w, 
       !cpx::aligned(pre, 2) || (bias != nullptr && !cpx::aligned(bias, dtype_size(bias_dtype))) ||
       (k != 0 && (x == nullptr || w == nullptr || !cpx::aligned(x, 2) || !cpx::aligned(w, 2))))
     return refuse("null or misaligned x, w, bias, residual, out or pre");
+  const cpx::RowBytes o{out, out_stride * elt, n * elt, m}, kept{pre, 2 * pre_stride, 2 * n, m},
+      stream_rows{residual, residual_stride * elt, n * elt, m};
+  if (cpx::rows_clash(o, stream_rows) || cpx::rows_meet(kept, o) || cpx::rows_meet(kept, stream_rows))
+    return refuse("out lies on part of the residual, or pre on out or the residual");
   const bool thin = m <= cplin::kThinRows;
   Tilings ways{};
   Tiling chosen{};
@@ -304,7 +313,10 @@ extern "C" cp_status cp_linear(const void* x, uint64_t x_stride, const void* w, 
   uint8_t* at = static_cast<uint8_t*>(workspace);
   Operand* op[2] = {&q.a, &q.b};
   cpm::AlignOperand of[2];
-  if (to_align(op, {m, n}, k, at, of)) {
+  const bool copies = to_align(op, {m, n}, k, at, of);
+  if (reads(q.a, m, k, o) || reads(q.b, n, k, o) || reads(q.a, m, k, kept) || reads(q.b, n, k, kept))
+    return refuse("out or pre lies on x or w, which are read while it is written");
+  if (copies) {
     const cudaError_t e = cpm::align_rows(of, static_cast<uint32_t>(2 * k), 2 * row_pitch(k), s);
     if (e != cudaSuccess) return cpx::cuda_fail(e, "linear launch");
   }
@@ -442,6 +454,13 @@ extern "C" cp_status cp_linear_grad(const void* dy, int dy_dtype, uint64_t dy_st
   if (has_dy && k != 0) {
     Operand* op[2] = {want_dw ? &xo : nullptr, want_dx ? &wo : nullptr};
     copies = to_align(op, {m, n}, k, at, of);
+    for (const cpx::RowBytes& out :
+         {cpx::RowBytes{dx, 2 * dx_stride, 2 * k, m},
+          cpx::RowBytes{dw, dw_stride * dtype_size(dw_dtype), k * dtype_size(dw_dtype), n}}) {
+      if (((want_dx || want_dw) && reads(dz, m, n, out)) || (want_dw && reads(xo, m, k, out)) ||
+          (want_dx && reads(wo, n, k, out)))
+        return refuse("dx or dw lies on dy, x or w, which are read while it is written");
+    }
   }
   cudaError_t e = cudaSuccess;
   if (has_dy && (g.dz != nullptr || g.parts != nullptr)) {

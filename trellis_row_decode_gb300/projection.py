@@ -181,10 +181,10 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
     `out` is given; the residual has it too).  D: dropout with probability p, as ``dropout`` makes
     it on the output's rows.
 
-    `out` may be the residual (the stream is updated in place).  With `pre` (True, or a tensor to
-    fill) returns (out, pre): the sums in front of the activation in x's type, for linear_grad.
-    Operands off 16-byte boundaries and sums of a split k need `workspace` (linear_workspace;
-    allocated where it is not given)."""
+    `out` may be the residual (the stream is updated in place); neither it nor `pre` may lie on x or
+    weight.  With `pre` (True, or a tensor to fill) returns (out, pre): the sums in front of the
+    activation in x's type, for linear_grad.  Operands off 16-byte boundaries and sums of a split k
+    need `workspace` (linear_workspace; allocated where it is not given)."""
     act = _activation(activation)
     if out is None and stream is None and workspace is None and (pre is False or pre is True):
         made = _common().linear(x, weight, bias, act, residual, dtype, pre, p, seed, offset, rng)
@@ -257,7 +257,8 @@ def linear_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, activat
     dy has x's type, or float32 (that of linear's output); the residual's gradient is dy itself.
     activation, p, seed, offset and rng are those of the forward call, `pre` what it left.  The
     products take dz rounded to x's type (dy itself without activation and dropout).
-    accumulate=True adds to the `dw` and `db` that are given (gradients of several batches)."""
+    accumulate=True adds to the `dw` and `db` that are given (gradients of several batches); `dx` and
+    `dw` may not lie on x, weight, or a dy that is taken as it is."""
     act = _activation(activation)
     if (need_dx and need_dw and need_db and not accumulate and dx is None and dw is None
             and db is None and workspace is None and stream is None):
