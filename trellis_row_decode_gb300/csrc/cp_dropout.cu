@@ -157,9 +157,10 @@ __global__ void __launch_bounds__(kThreads, (kCtas<T, kLayout, kResidual>))
 // Rows one behind the other on any boundary.  A lane makes the mask of an octet, eight bits; the
 // elements go to the lanes one by one, 32 neighbours an access, and each takes its place and its bit
 // from the lane that has its octet.  For fp32 with a residual, where it is the stores of shifted
-// octets that take the time (90010 x 813: 146 us against 200).
-// Without a residual or in 16 bits the exchange costs more than it saves (116 us against 124; 100000 x
-// 1023 bf16 126 against 176).
+// octets that take the time (an array of its own as the residual, here / by octets: 90010 x 813 144.6 /
+// 145.9 us, 100000 x 1023 200 / 206, 1000 x 4097 14.2 / 19.2, 40000 x 25 6.8 / 8.0, 48 x 1023 3.0 / 3.6).
+// Without a residual or in 16 bits the exchange costs more than it saves (90010 x 813 without one 124 us
+// against 115; 100000 x 1023 bf16 176 against 125).
 __global__ void __launch_bounds__(kThreads, 5)
     dropout_elements_kernel(const __grid_constant__ DropoutParams p) {
   wait_for_previous();

@@ -44,15 +44,16 @@ __device__ uint32_t g_linear_gave_up;
 // shared by `splits` units where there are few; their sums go to a workspace, and finish_kernel adds
 // them in order.
 //
-// 4096^3: 73.5-74.6 us (1.84-1.87 PFLOP/s), k = 24576: 445-456 in bursts, about 510 in calls that go on (at
-// the power limit); both gradients of 4096^3: 142 us (1.94).  Bound by the tensor core there (85-89 % of
+// bf16, plain outputs, in bursts: 4096^3 72-73 us (1.9 PFLOP/s), k = 24576 429-434 (with bias and residual
+// 432-438), in calls that go on, at the power limit, 83 and 503; fp16 76-77 and, read in segments,
+// 467-473; both gradients of 4096^3: 142 us (1.94).  Bound by the tensor core there (85-89 % of
 // its cycles): loads alone would take 216 ns for 64 of k at 256 columns, products alone 265, together
 // 300.  What each piece is for: the issuing warps run whole on a warp-uniform index, so their
 // operands are in uniform registers (64 of k at 64 columns: 230 -> 162 ns), narrow tiles stage 128 of
 // k (162 -> 144; at 256 columns nothing), sixteen finishing warps and not eight hide the epilogue's
 // chains, and the ring keeps what the slots leave (five stages and not six of 30 KB: 457 -> 497 us at
-// k = 24576).  Short k is bound by the epilogue: 4096 x 4096 x 1024 plain 24.6 us, with silu 27, dropout 35,
-// with everything 45 (the generator's products on their pipe, then the activations').
+// k = 24576).  Short k is bound by the epilogue: 4096 x 4096 x 1024 plain 24.6 us, with silu 24.8, gelu
+// 26.6, dropout 35, with everything 45 (the generator's products on their pipe, then the activations').
 
 constexpr int kSumWarps = 16;
 constexpr uint32_t kGroups = kSumWarps / 4;            // of four warps, one for each 32 lanes
