@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
       // ---------------------------------------------------------------- loads
       // (a warp for a, one for b; each runs its loop whole and elects a thread to issue)
       const bool is_a = warp == kLoadA;
-      if (cpt::elect_one()) {
+      if (p.units != 0 && cpt::elect_one()) {    // (column sums alone come without a map)
         for (int i = 0; i < kMostProducts; ++i)
           cpt::tma_prefetch_map(is_a ? &p.map_a[i] : &p.map_b[i]);
       }
