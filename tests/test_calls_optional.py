@@ -1,12 +1,17 @@
 """The calls' compiled form is optional: without this Python's headers the library builds all the same, and
 where the compiled code is missing or another machine's every call takes the checked way."""
+import subprocess
+import sys
 import sysconfig
+from pathlib import Path
 
 import pytest
 import torch
 
 import trellis_row_decode_gb300 as cp
 from trellis_row_decode_gb300 import build_ext, projection
+
+ROOT = Path(__file__).resolve().parent.parent
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -34,6 +39,14 @@ def test_building_with_headers_makes_them(tmp_path, monkeypatch):
 
 def test_the_calls_are_named_for_their_python():
     assert build_ext.CALLS.name == "_calls" + sysconfig.get_config_var("EXT_SUFFIX")
+    assert projection._CALLS_PATH == build_ext.CALLS
+
+
+def test_the_package_leaves_its_build_alone():
+    """`python -m trellis_row_decode_gb300.build_ext` runs a module that the package has not loaded."""
+    code = "import sys, trellis_row_decode_gb300 as cp; print(cp.__name__ + '.build_ext' in sys.modules)"
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
+    assert run.stdout.strip() == "False", run.stderr
 
 
 @pytest.mark.parametrize("content", [None, b"", b"\x7fELF of another machine"])

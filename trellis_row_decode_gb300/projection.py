@@ -18,7 +18,7 @@ import warnings
 
 import torch
 
-from . import CP_ERR_INVALID_ARG, LIB_PATH, CPError, _check, build_ext, lib
+from . import CP_ERR_INVALID_ARG, LIB_PATH, CPError, _check, lib
 from . import layer as _layer
 from .layer import (CP_BF16, CP_F16, CP_F32, _check_out, _device, _empty, _float, _on, _rows, _stream,
                     _workspace)
@@ -29,7 +29,7 @@ __all__ = ["ACTIVATIONS", "linear", "linear_workspace", "linear_grad", "linear_g
 ACTIVATIONS = ("none", "relu", "silu", "gelu", "gelu_tanh")
 _ACT = {name: i for i, name in enumerate(ACTIVATIONS)}
 _HALF = {torch.float16: CP_F16, torch.bfloat16: CP_BF16}
-_CALLS_PATH = LIB_PATH.with_name(build_ext.CALLS.name)
+_CALLS_PATH = LIB_PATH.with_name("_calls" + importlib.machinery.EXTENSION_SUFFIXES[0])
 _declared = None
 _calls = None
 
